@@ -22,7 +22,8 @@
  *     overlap on the device.
  *   - d_status: optional device int; kernels OR an error bit into it
  *     (1 = token id out of range, 2 = bounded wait timed out, 4 = target id
- *     out of range) and never trap.
+ *     out of range, 8 = sequence offsets out of order or out of range) and
+ *     never trap.
  *   - Return GPT2_OK or a negative gpt2_status (see gpt2.h) for bad
  *     arguments or a failed launch.
  */
@@ -223,6 +224,61 @@ int gpt2_op_attention_backward(int dtype, void* dqkv, const void* dout, const vo
                                const void* o, const float* lse, int B, int T, int C, int H,
                                void* scratch, size_t scratch_bytes, void* stream);
 
+/* Causal attention over packed sequences of different lengths, with grouped
+ * heads (an addition of this library: the attention of the step, which takes
+ * B sequences of one length, for a batch of documents laid end to end).
+ * Sequence s has the queries cu_q[s] .. cu_q[s+1]-1 and the keys
+ * cu_k[s] .. cu_k[s+1]-1 (cu_q, cu_k: n_seq + 1 ascending int32 offsets in
+ * device memory, read by the kernels, so a captured graph follows them; they
+ * may be one array). Its query i sees its keys 0 .. i + lk - lq (lq, lk the
+ * sequence's own lengths: the last query sees every key, so lq < lk continues
+ * a prompt whose first keys are cached, lq = 1 is one new token). Query head h
+ * reads key head h / (Hq / Hkv).
+ *   o[i,h,:] = softmax(q[i,h,:] . k / sqrt(hd)) v, lse[h,i] = log-sum-exp of
+ *   the scaled scores. A query that sees no key (lk < lq) gets o = 0 and
+ *   lse = -inf.
+ * q, o [total_q] rows of Hq * hd values, k, v [total_k] rows of Hkv * hd,
+ * head h at columns h*hd .. of a row; *_stride: elements from one row to the
+ * next (so q, k and v may be column blocks of one fused buffer). lse [Hq,
+ * total_q] fp32. Rows of o and lse that belong to no sequence (before
+ * cu_q[0], at or after cu_q[n_seq]) are left as they were, and no row's
+ * result depends on rows of another sequence, whatever they hold. Within a
+ * sequence, a NaN or infinity at a position may reach the results of earlier
+ * positions of the same 128-row tile.
+ *   - max_q, max_k: at least the longest sequence's queries and keys (they
+ *     choose the kernel; a longer sequence sets bit 8 of *d_status).
+ *   - Offsets that descend or leave [0, total] set bit 8 of *d_status; they
+ *     are clamped, so no memory outside the buffers is touched.
+ *   - hd == 64 for bf16; hd 8, 16, 32 or 64 for fp32. Hq a multiple of Hkv,
+ *     at most 128 query heads to a key head. Pointers 16-byte aligned, strides
+ *     multiples of 16 bytes and at least the row (total_q * Hq, total_k * Hkv
+ *     and n_seq + total / 16 times Hq below 2^31, else GPT2_ERR_ARG).
+ *   - n_seq = 0 or total_q = 0 launches nothing.
+ * Scratch: partial results of keys split over blocks (few queries). */
+size_t gpt2_op_attention_packed_forward_scratch(int dtype, int n_seq, int max_q, int max_k, int Hq, int Hkv, int hd);
+int gpt2_op_attention_packed_forward(int dtype, void* o, int64_t o_stride, float* lse, const void* q,
+                                     int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                     int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k, int n_seq,
+                                     int total_q, int total_k, int max_q, int max_k, int Hq, int Hkv, int hd,
+                                     void* scratch, size_t scratch_bytes, int* d_status, void* stream);
+
+/* Its backward, from the forward's o and lse: with D = rowsum(dO * O) and P
+ * recomputed from lse, dV = P^T dO, dS = P (dO V^T - D), dQ = dS K / sqrt(hd),
+ * dK = dS^T Q / sqrt(hd); dK and dV are summed over the query heads of their
+ * group. dq [total_q] rows, dk, dv [total_k] rows (dtype, their own strides,
+ * overwritten; rows of no sequence are left as they were, a key that no query
+ * sees gets 0). Deterministic (no atomics). dq, dk, dv must not overlap the
+ * inputs. Sequences, strides and limits as in the forward. Scratch: D. */
+size_t gpt2_op_attention_packed_backward_scratch(int dtype, int n_seq, int total_q, int total_k, int Hq, int Hkv,
+                                                 int hd);
+int gpt2_op_attention_packed_backward(int dtype, void* dq, int64_t dq_stride, void* dk, int64_t dk_stride, void* dv,
+                                      int64_t dv_stride, const void* dout, int64_t dout_stride, const void* q,
+                                      int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                      int64_t v_stride, const void* o, int64_t o_stride, const float* lse,
+                                      const int32_t* cu_q, const int32_t* cu_k, int n_seq, int total_q, int total_k,
+                                      int max_q, int max_k, int Hq, int Hkv, int hd, void* scratch,
+                                      size_t scratch_bytes, int* d_status, void* stream);
+
 /* GELU, tanh form ("gelu_forward"): g = 0.5 u (1 + tanh(sqrt(2/pi)(u + 0.044715 u^3))).
  * n % 8 == 0. In place (g == u) is allowed. */
 int gpt2_op_gelu_forward(int dtype, void* g, const void* u, int64_t n, void* stream);
@@ -280,6 +336,37 @@ int gpt2_op_bias_backward_noalloc(int dtype, float* dbias, const void* dy, int N
  * A target outside [0,V) sets bit 4 of *d_status and is treated as 0. */
 int gpt2_op_classifier(int dtype, void* logits, float* losses, const int32_t* targets, int N,
                        int V, int Vp, float dloss, int* d_status, void* stream);
+
+/* Log-probabilities of given tokens, with entropy and the top alternatives
+ * (an addition of this library: the classifier's softmax kept for scoring; the
+ * logits are read once and left as they are). Per row i of logits [N, Vp]
+ * (dtype), over columns j < V only (Vp % 8 == 0):
+ *   lse[i]  = log sum exp z_ij,  logp[i] = z_i,targets[i] - lse[i],
+ *   entropy[i] = -sum_j p_ij log p_ij with p = exp(z - lse) (0 log 0 = 0),
+ *   top_ids[i, 0..k-1] = the columns of the k largest logits, largest first,
+ *   equal logits by the lowest column, top_logp[i, r] their log-probability.
+ * All outputs fp32 (top_ids int32); 0 <= k <= 64, k <= V, top_logp and top_ids
+ * [N, k] (unused for k = 0); entropy may be null; logp and targets may both be
+ * null. A target outside [0,V) sets bit 4 of *d_status and is treated as 0. A
+ * row whose every logit is -inf has no distribution: lse = logp = top_logp =
+ * -inf, entropy = 0. A row with a NaN gets NaN in all of them; one with +inf
+ * (and no NaN) gets lse = inf, entropy = NaN, and log-probabilities of -inf
+ * (NaN for its infinite columns). top_ids stay in [0,V), unspecified for a
+ * row with a NaN. */
+int gpt2_op_token_logprobs(int dtype, float* logp, float* lse, float* entropy, float* top_logp, int32_t* top_ids,
+                           int k, const void* logits, const int32_t* targets, int N, int V, int Vp, int* d_status,
+                           void* stream);
+
+/* Its gradient: with g = dlogp[i], a = dlse[i], b = dentropy[i] (each array
+ * may be null: 0) and p, log p from the forward's lse,
+ *   dlogits_ij = g ([j == target_i] - p_ij) + a p_ij - b p_ij (log p_ij + entropy_i)
+ * for j < V (0 where p_ij = 0, and in a row that has no distribution), 0 for
+ * V <= j < Vp. dlogits [N, Vp] (dtype, overwritten) may be logits itself.
+ * entropy is needed with dentropy, targets with dlogp; targets out of range as
+ * above. Nothing is summed across rows: deterministic. */
+int gpt2_op_token_logprobs_backward(int dtype, void* dlogits, const void* logits, const int32_t* targets,
+                                    const float* lse, const float* entropy, const float* dlogp, const float* dlse,
+                                    const float* dentropy, int N, int V, int Vp, int* d_status, void* stream);
 
 /* Mean of losses [N] into *out (device fp32): fixed-order tree, deterministic.
  * The mean loss of the forward with targets (llm.c "State of the Union",

@@ -1,0 +1,195 @@
+// Causal attention over packed sequences with grouped heads: the fp32 path
+// and the launchers.
+#include "attention_packed.cuh"
+
+#include <cfloat>
+
+namespace {
+
+template <typename T, int HD> __device__ __forceinline__ void load_row(float (&x)[HD], const T* p) {
+#pragma unroll
+    for (int d = 0; d < HD; d += 8) {
+        float t[8];
+        load8(p + d, t);
+#pragma unroll
+        for (int e = 0; e < 8; e++) x[d + e] = t[e];
+    }
+}
+template <typename T, int HD> __device__ __forceinline__ void store_row(T* p, const float (&x)[HD], float s) {
+#pragma unroll
+    for (int d = 0; d < HD; d += 8) {
+        float t[8];
+#pragma unroll
+        for (int e = 0; e < 8; e++) t[e] = x[d + e] * s;
+        store8(p + d, t);
+    }
+}
+
+// One thread per (head, query).
+template <typename T, int HD> __global__ void __launch_bounds__(128) packed_fwd_kernel(PackedAttn a, float scale) {
+    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    packed_check(a, i, gridDim.x * blockDim.x);
+    if (i >= a.total_q * a.Hq) return;
+    const int h = i / a.total_q, row = i - h * a.total_q;
+    const int s = packed_find_row(a.cu_q, a.n_seq, row);
+    if (s < 0) return;
+    const PackedSeq p = packed_seq(a, s);
+    const int t = row - p.q0;
+    if (t < 0 || t >= p.lq) return;
+    const int hk = h / (a.Hq / a.Hkv);
+    float q[HD], acc[HD];
+    load_row<T, HD>(q, (const T*)a.q + row * a.q_stride + h * HD);
+#pragma unroll
+    for (int d = 0; d < HD; d++) acc[d] = 0.f;
+    float m = -INFINITY, l = 0.f;
+    const int n = min(t + p.lk - p.lq + 1, p.lk);
+    for (int j = 0; j < n; j++) {
+        float x[HD];
+        load_row<T, HD>(x, (const T*)a.k + (p.k0 + j) * a.k_stride + hk * HD);
+        float sc = 0.f;
+#pragma unroll
+        for (int d = 0; d < HD; d++) sc += q[d] * x[d];
+        sc *= scale;
+        if (sc > m) {
+            const float f = m == -INFINITY ? 0.f : expf(m - sc);
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < HD; d++) acc[d] *= f;
+            m = sc;
+        }
+        const float w = m == -INFINITY ? (sc == sc ? 0.f : sc) : expf(sc - m);
+        l += w;
+        load_row<T, HD>(x, (const T*)a.v + (p.k0 + j) * a.v_stride + hk * HD);
+#pragma unroll
+        for (int d = 0; d < HD; d++) acc[d] += w * x[d];
+    }
+    store_row<T, HD>((T*)a.o + row * a.o_stride + h * HD, acc, l == 0.f ? 0.f : 1.f / l);
+    a.lse[(int64_t)h * a.total_q + row] = l == 0.f ? -INFINITY : m + logf(l);
+}
+
+// One thread per (head, query): dQ, and D for the other kernel.
+template <typename T, int HD>
+__global__ void __launch_bounds__(128) packed_dq_kernel(PackedAttn a, PackedAttnGrad g, float scale) {
+    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    packed_check(a, i, gridDim.x * blockDim.x);
+    if (i >= a.total_q * a.Hq) return;
+    const int h = i / a.total_q, row = i - h * a.total_q;
+    const int s = packed_find_row(a.cu_q, a.n_seq, row);
+    if (s < 0) return;
+    const PackedSeq p = packed_seq(a, s);
+    const int t = row - p.q0;
+    if (t < 0 || t >= p.lq) return;
+    const int hk = h / (a.Hq / a.Hkv);
+    float q[HD], dy[HD], dq[HD];
+    float D = 0.f;
+    load_row<T, HD>(q, (const T*)a.o + row * a.o_stride + h * HD);
+    load_row<T, HD>(dy, (const T*)g.dout + row * g.dout_stride + h * HD);
+#pragma unroll
+    for (int d = 0; d < HD; d++) D += q[d] * dy[d];
+    g.D[(int64_t)h * a.total_q + row] = D;
+    load_row<T, HD>(q, (const T*)a.q + row * a.q_stride + h * HD);
+#pragma unroll
+    for (int d = 0; d < HD; d++) dq[d] = 0.f;
+    const float L = a.lse[(int64_t)h * a.total_q + row];
+    const int n = min(t + p.lk - p.lq + 1, p.lk);
+    for (int j = 0; j < n; j++) {
+        float k[HD], v[HD];
+        load_row<T, HD>(k, (const T*)a.k + (p.k0 + j) * a.k_stride + hk * HD);
+        load_row<T, HD>(v, (const T*)a.v + (p.k0 + j) * a.v_stride + hk * HD);
+        float sc = 0.f, dp = 0.f;
+#pragma unroll
+        for (int d = 0; d < HD; d++) {
+            sc += q[d] * k[d];
+            dp += dy[d] * v[d];
+        }
+        const float ds = expf(sc * scale - L) * (dp - D);
+#pragma unroll
+        for (int d = 0; d < HD; d++) dq[d] += ds * k[d];
+    }
+    store_row<T, HD>((T*)g.dq + row * g.dq_stride + h * HD, dq, scale);
+}
+
+// One thread per (key head, key).
+template <typename T, int HD>
+__global__ void __launch_bounds__(128) packed_dkdv_kernel(PackedAttn a, PackedAttnGrad g, float scale) {
+    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= a.total_k * a.Hkv) return;
+    const int hk = i / a.total_k, row = i - hk * a.total_k;
+    const int s = packed_find_row(a.cu_k, a.n_seq, row);
+    if (s < 0) return;
+    const PackedSeq p = packed_seq(a, s);
+    const int j = row - p.k0;
+    if (j < 0 || j >= p.lk) return;
+    const int group = a.Hq / a.Hkv;
+    float k[HD], v[HD], dk[HD], dv[HD];
+    load_row<T, HD>(k, (const T*)a.k + row * a.k_stride + hk * HD);
+    load_row<T, HD>(v, (const T*)a.v + row * a.v_stride + hk * HD);
+#pragma unroll
+    for (int d = 0; d < HD; d++) dk[d] = dv[d] = 0.f;
+    for (int h = hk * group; h < (hk + 1) * group; h++)
+        for (int t = max(0, j - (p.lk - p.lq)); t < p.lq; t++) {
+            float q[HD], dy[HD];
+            const int64_t r = p.q0 + t;
+            load_row<T, HD>(q, (const T*)a.q + r * a.q_stride + h * HD);
+            load_row<T, HD>(dy, (const T*)g.dout + r * g.dout_stride + h * HD);
+            float sc = 0.f, dp = 0.f;
+#pragma unroll
+            for (int d = 0; d < HD; d++) {
+                sc += q[d] * k[d];
+                dp += dy[d] * v[d];
+            }
+            const float w = expf(sc * scale - a.lse[h * (int64_t)a.total_q + r]);
+            const float ds = w * (dp - g.D[h * (int64_t)a.total_q + r]);
+#pragma unroll
+            for (int d = 0; d < HD; d++) {
+                dv[d] += w * dy[d];
+                dk[d] += ds * q[d];
+            }
+        }
+    store_row<T, HD>((T*)g.dk + row * g.dk_stride + hk * HD, dk, scale);
+    store_row<T, HD>((T*)g.dv + row * g.dv_stride + hk * HD, dv, 1.f);
+}
+
+template <typename T, int HD> int forward(const PackedAttn& a, cudaStream_t s) {
+    packed_fwd_kernel<T, HD><<<(a.total_q * a.Hq + 127) / 128, 128, 0, s>>>(a, 1.f / sqrtf((float)HD));
+    return 1;
+}
+template <typename T, int HD> int backward(const PackedAttn& a, const PackedAttnGrad& g, cudaStream_t s) {
+    const float scale = 1.f / sqrtf((float)HD);
+    if (a.total_q) packed_dq_kernel<T, HD><<<(a.total_q * a.Hq + 127) / 128, 128, 0, s>>>(a, g, scale);
+    if (a.total_k) packed_dkdv_kernel<T, HD><<<(a.total_k * a.Hkv + 127) / 128, 128, 0, s>>>(a, g, scale);
+    return (a.total_q > 0) + (a.total_k > 0);
+}
+
+}  // namespace
+
+size_t attention_packed_forward_scratch(int dtype, int n_seq, int max_q, int max_k, int Hq, int Hkv, int hd) {
+    return 0;
+}
+
+int launch_attention_packed_forward(int dtype, const PackedAttn& a, void* scratch, cudaStream_t s) {
+    if (dtype == GPT2_MODE_BF16) return forward<bf16, 64>(a, s);
+    switch (a.hd) {
+        case 8: return forward<float, 8>(a, s);
+        case 16: return forward<float, 16>(a, s);
+        case 32: return forward<float, 32>(a, s);
+        default: return forward<float, 64>(a, s);
+    }
+}
+
+size_t attention_packed_backward_scratch(int dtype, int n_seq, int total_q, int total_k, int Hq, int Hkv, int hd) {
+    return (size_t)Hq * total_q * 4;
+}
+
+int launch_attention_packed_backward(int dtype, const PackedAttn& a, const PackedAttnGrad& grad, void* scratch,
+                                     cudaStream_t s) {
+    PackedAttnGrad g = grad;
+    g.D = (float*)scratch;
+    if (dtype == GPT2_MODE_BF16) return backward<bf16, 64>(a, g, s);
+    switch (a.hd) {
+        case 8: return backward<float, 8>(a, g, s);
+        case 16: return backward<float, 16>(a, g, s);
+        case 32: return backward<float, 32>(a, g, s);
+        default: return backward<float, 64>(a, g, s);
+    }
+}

@@ -105,6 +105,37 @@ int launch_attention_backward(int dtype, void* dqkv, const void* dout, const voi
                               const float* lse, int B, int T, int C, int H, void* scratch, int* status,
                               cudaStream_t s);
 
+// Attention over packed sequences (gpt2_op_attention_packed_*): validated arguments.
+struct PackedAttn {
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;  // elements between rows
+    void* o;                               // forward: output; backward: the forward's output
+    int64_t o_stride;
+    float* lse;                            // [Hq, total_q]
+    const int32_t *cu_q, *cu_k;            // n_seq + 1 offsets each (device)
+    int n_seq, total_q, total_k, max_q, max_k, Hq, Hkv, hd;
+    int* status;
+};
+struct PackedAttnGrad {
+    const void* dout;
+    void *dq, *dk, *dv;
+    int64_t dout_stride, dq_stride, dk_stride, dv_stride;
+    float* D;  // [Hq, total_q]
+};
+size_t attention_packed_forward_scratch(int dtype, int n_seq, int max_q, int max_k, int Hq, int Hkv, int hd);
+int launch_attention_packed_forward(int dtype, const PackedAttn& a, void* scratch, cudaStream_t s);
+size_t attention_packed_backward_scratch(int dtype, int n_seq, int total_q, int total_k, int Hq, int Hkv, int hd);
+int launch_attention_packed_backward(int dtype, const PackedAttn& a, const PackedAttnGrad& g, void* scratch,
+                                     cudaStream_t s);
+
+// Log-probabilities of given tokens, entropy and top alternatives (gpt2_op_token_logprobs) and their gradient.
+int launch_token_logprobs(int dtype, float* logp, float* lse, float* entropy, float* top_logp, int32_t* top_ids,
+                          int k, const void* logits, const int32_t* targets, int N, int V, int Vp, int* status,
+                          cudaStream_t s);
+int launch_token_logprobs_backward(int dtype, void* dlogits, const void* logits, const int32_t* targets,
+                                   const float* lse, const float* entropy, const float* dlogp, const float* dlse,
+                                   const float* dentropy, int N, int V, int Vp, int* status, cudaStream_t s);
+
 // bf16 linear forward with the GELU fused into its epilogue: u = A W^T + bias
 // (A [M,K], W [N,K], both K-major) rounded to bf16, out = gelu(u), dgelu =
 // gelu'(u) (kept for the backward); see gpt2_op_matmul_gelu.

@@ -254,6 +254,76 @@ int gpt2_op_attention_backward(int dtype, void* dqkv, const void* dout, const vo
     return finish(launch_attention_backward(dtype, dqkv, dout, qkv, o, lse, B, T, C, H, scratch, nullptr, st(stream)));
 }
 
+static bool packed_ok(int dtype, int64_t total_q, int64_t total_k, int n_seq, int max_q, int max_k, int Hq, int Hkv,
+                      int hd) {
+    if (!dt_ok(dtype) || n_seq < 0 || total_q < 0 || total_k < 0 || max_q < 0 || max_k < 0) return false;
+    if (Hq < 1 || Hkv < 1 || Hq % Hkv || Hq / Hkv > 128) return false;
+    if (dtype == GPT2_MODE_BF16 ? hd != 64 : hd != 8 && hd != 16 && hd != 32 && hd != 64) return false;
+    // the kernels' work items and (head, row) pairs are counted in 32 bits
+    const int64_t most = (int64_t)1 << 31;
+    const int64_t items = n_seq + (total_q > total_k ? total_q : total_k) / 16 + 1;
+    return total_q * Hq < most && total_k * Hkv < most && items * Hq < most;
+}
+static bool rows_ok(const void* p, int64_t stride, int heads, int hd, int dtype) {
+    const int per16 = dtype == GPT2_MODE_BF16 ? 8 : 4;
+    return al16(p) && stride >= (int64_t)heads * hd && stride % per16 == 0 && stride < ((int64_t)1 << 31);
+}
+
+size_t gpt2_op_attention_packed_forward_scratch(int dtype, int n_seq, int max_q, int max_k, int Hq, int Hkv, int hd) {
+    if (!packed_ok(dtype, 0, 0, n_seq, max_q, max_k, Hq, Hkv, hd)) return 0;
+    return attention_packed_forward_scratch(dtype, n_seq, max_q, max_k, Hq, Hkv, hd);
+}
+
+int gpt2_op_attention_packed_forward(int dtype, void* o, int64_t o_stride, float* lse, const void* q,
+                                     int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                     int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k, int n_seq,
+                                     int total_q, int total_k, int max_q, int max_k, int Hq, int Hkv, int hd,
+                                     void* scratch, size_t scratch_bytes, int* d_status, void* stream) {
+    if (!packed_ok(dtype, total_q, total_k, n_seq, max_q, max_k, Hq, Hkv, hd)) return GPT2_ERR_ARG;
+    if (n_seq == 0 || total_q == 0) return GPT2_OK;
+    if (!o || !lse || !q || !cu_q || !cu_k || (total_k > 0 && (!k || !v))) return GPT2_ERR_ARG;
+    if (!rows_ok(o, o_stride, Hq, hd, dtype) || !rows_ok(q, q_stride, Hq, hd, dtype) ||
+        !rows_ok(k, k_stride, Hkv, hd, dtype) || !rows_ok(v, v_stride, Hkv, hd, dtype))
+        return GPT2_ERR_ARG;
+    const size_t need = attention_packed_forward_scratch(dtype, n_seq, max_q, max_k, Hq, Hkv, hd);
+    if (need && (!scratch || scratch_bytes < need)) return GPT2_ERR_WORKSPACE;
+    const PackedAttn a = {q,    k,     v,     q_stride, k_stride, v_stride, o,     o_stride, lse, cu_q,
+                          cu_k, n_seq, total_q, total_k,  max_q,    max_k,    Hq,    Hkv,      hd,  d_status};
+    return finish(launch_attention_packed_forward(dtype, a, scratch, st(stream)));
+}
+
+size_t gpt2_op_attention_packed_backward_scratch(int dtype, int n_seq, int total_q, int total_k, int Hq, int Hkv,
+                                                 int hd) {
+    if (!packed_ok(dtype, total_q, total_k, n_seq, 0, 0, Hq, Hkv, hd)) return 0;
+    return attention_packed_backward_scratch(dtype, n_seq, total_q, total_k, Hq, Hkv, hd);
+}
+
+int gpt2_op_attention_packed_backward(int dtype, void* dq, int64_t dq_stride, void* dk, int64_t dk_stride, void* dv,
+                                      int64_t dv_stride, const void* dout, int64_t dout_stride, const void* q,
+                                      int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                      int64_t v_stride, const void* o, int64_t o_stride, const float* lse,
+                                      const int32_t* cu_q, const int32_t* cu_k, int n_seq, int total_q, int total_k,
+                                      int max_q, int max_k, int Hq, int Hkv, int hd, void* scratch,
+                                      size_t scratch_bytes, int* d_status, void* stream) {
+    if (!packed_ok(dtype, total_q, total_k, n_seq, max_q, max_k, Hq, Hkv, hd)) return GPT2_ERR_ARG;
+    if (n_seq == 0 || (total_q == 0 && total_k == 0)) return GPT2_OK;
+    if (!cu_q || !cu_k || (total_q > 0 && (!dq || !dout || !q || !o || !lse)) ||
+        (total_k > 0 && (!dk || !dv || !k || !v)))
+        return GPT2_ERR_ARG;
+    if (!rows_ok(dq, dq_stride, Hq, hd, dtype) || !rows_ok(dk, dk_stride, Hkv, hd, dtype) ||
+        !rows_ok(dv, dv_stride, Hkv, hd, dtype) || !rows_ok(dout, dout_stride, Hq, hd, dtype) ||
+        !rows_ok(q, q_stride, Hq, hd, dtype) || !rows_ok(k, k_stride, Hkv, hd, dtype) ||
+        !rows_ok(v, v_stride, Hkv, hd, dtype) || !rows_ok(o, o_stride, Hq, hd, dtype))
+        return GPT2_ERR_ARG;
+    const size_t need = attention_packed_backward_scratch(dtype, n_seq, total_q, total_k, Hq, Hkv, hd);
+    if (!scratch || scratch_bytes < need) return GPT2_ERR_WORKSPACE;
+    const PackedAttn a = {q,    k,     v,     q_stride, k_stride, v_stride, const_cast<void*>(o),
+                          o_stride, const_cast<float*>(lse), cu_q, cu_k, n_seq, total_q, total_k, max_q,
+                          max_k,    Hq,    Hkv,   hd,       d_status};
+    const PackedAttnGrad g = {dout, dq, dk, dv, dout_stride, dq_stride, dk_stride, dv_stride, nullptr};
+    return finish(launch_attention_packed_backward(dtype, a, g, scratch, st(stream)));
+}
+
 int gpt2_op_gelu_forward(int dtype, void* g, const void* u, int64_t n, void* stream) {
     if (!dt_ok(dtype) || !g || !u || n < 0 || n % 8 || !al16(g) || !al16(u)) return GPT2_ERR_ARG;
     return finish(launch_gelu_forward(dtype, g, u, n, st(stream)));
@@ -294,6 +364,28 @@ int gpt2_op_classifier(int dtype, void* logits, float* losses, const int32_t* ta
     if (!dt_ok(dtype) || !logits || !losses || !targets || N < 0 || V < 1 || Vp < V || Vp % 8 || !al16(logits))
         return GPT2_ERR_ARG;
     return finish(launch_classifier(dtype, logits, losses, targets, N, V, Vp, dloss, d_status, st(stream)));
+}
+
+int gpt2_op_token_logprobs(int dtype, float* logp, float* lse, float* entropy, float* top_logp, int32_t* top_ids,
+                           int k, const void* logits, const int32_t* targets, int N, int V, int Vp, int* d_status,
+                           void* stream) {
+    if (!dt_ok(dtype) || N < 0 || V < 1 || Vp < V || Vp % 8 || k < 0 || k > 64 || k > V) return GPT2_ERR_ARG;
+    if (N == 0) return GPT2_OK;
+    if (!lse || !logits || (logp != nullptr) != (targets != nullptr) || !al16(logits)) return GPT2_ERR_ARG;
+    if (k && (!top_logp || !top_ids)) return GPT2_ERR_ARG;
+    return finish(launch_token_logprobs(dtype, logp, lse, entropy, top_logp, top_ids, k, logits, targets, N, V, Vp,
+                                        d_status, st(stream)));
+}
+
+int gpt2_op_token_logprobs_backward(int dtype, void* dlogits, const void* logits, const int32_t* targets,
+                                    const float* lse, const float* entropy, const float* dlogp, const float* dlse,
+                                    const float* dentropy, int N, int V, int Vp, int* d_status, void* stream) {
+    if (!dt_ok(dtype) || N < 0 || V < 1 || Vp < V || Vp % 8) return GPT2_ERR_ARG;
+    if (N == 0) return GPT2_OK;
+    if (!dlogits || !logits || !lse || !al16(dlogits) || !al16(logits)) return GPT2_ERR_ARG;
+    if ((dlogp && !targets) || (dentropy && !entropy)) return GPT2_ERR_ARG;
+    return finish(launch_token_logprobs_backward(dtype, dlogits, logits, targets, lse, entropy, dlogp, dlse, dentropy,
+                                                 N, V, Vp, d_status, st(stream)));
 }
 
 int gpt2_op_mean_loss(float* out, const float* losses, int N, void* stream) {

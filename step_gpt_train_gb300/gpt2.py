@@ -135,6 +135,21 @@ _SIGNATURES = {
     "gpt2_op_attention_backward_scratch": (c_size_t, [c_int, c_int, c_int]),
     "gpt2_op_attention_backward": (c_int, [c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int,
                                            c_int, c_int, c_void_p, c_size_t, c_void_p]),
+    "gpt2_op_attention_packed_forward_scratch": (c_size_t, [c_int, c_int, c_int, c_int, c_int, c_int, c_int]),
+    "gpt2_op_attention_packed_forward": (c_int, [c_int, c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_void_p,
+                                                 c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_int, c_int, c_int,
+                                                 c_int, c_int, c_int, c_int, c_int, c_void_p, c_size_t, c_void_p,
+                                                 c_void_p]),
+    "gpt2_op_attention_packed_backward_scratch": (c_size_t, [c_int, c_int, c_int, c_int, c_int, c_int, c_int]),
+    "gpt2_op_attention_packed_backward": (c_int, [c_int, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64,
+                                                  c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
+                                                  c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_int,
+                                                  c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_void_p, c_size_t,
+                                                  c_void_p, c_void_p]),
+    "gpt2_op_token_logprobs": (c_int, [c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_void_p,
+                                       c_void_p, c_int, c_int, c_int, c_void_p, c_void_p]),
+    "gpt2_op_token_logprobs_backward": (c_int, [c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                                c_void_p, c_void_p, c_int, c_int, c_int, c_void_p, c_void_p]),
     "gpt2_op_gelu_forward": (c_int, [c_int, c_void_p, c_void_p, c_int64, c_void_p]),
     "gpt2_op_gelu_backward": (c_int, [c_int, c_void_p, c_void_p, c_void_p, c_int64, c_void_p]),
     "gpt2_op_residual_forward": (c_int, [c_int, c_void_p, c_void_p, c_void_p, c_int64, c_void_p]),
@@ -576,6 +591,77 @@ def gpt2_op_attention_backward(dqkv, dout, qkv, o, lse, B, T, H, stream=None):
     check(lib.gpt2_op_attention_backward(_dtype_of(qkv), _p(dqkv), _p(dout), _p(qkv), _p(o), _p(lse), B, T, C, H,
                                          _p(sc), sc.numel(), _s(stream)), "gpt2_op_attention_backward")
     return sc
+
+
+def _rows(t, what):
+    """Row stride of a [rows, heads, hd] tensor whose heads are contiguous in a row."""
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{what}: a [rows, heads, hd] tensor with the heads of a row contiguous is needed")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def gpt2_op_attention_packed_forward(o, lse, q, k, v, cu_q, cu_k, max_q, max_k, status=None, stream=None):
+    """o [total_q, Hq, hd], lse [Hq, total_q] (float32): causal attention over packed sequences; q like o,
+    k and v [total_k, Hkv, hd] (each may be a column block of a wider buffer), cu_q and cu_k int32 [n_seq + 1]
+    CUDA offsets, max_q and max_k the longest sequence's queries and keys."""
+    lib = load_library()
+    dt = _dtype_of(q)
+    tq, hq, hd = q.shape
+    tk, hkv = k.shape[0], k.shape[1]
+    if cu_k.numel() != cu_q.numel():
+        raise ValueError("cu_q and cu_k need the same number of sequences")
+    n = cu_q.numel() - 1
+    nb = lib.gpt2_op_attention_packed_forward_scratch(dt, n, max_q, max_k, hq, hkv, hd)
+    sc = _scratch(nb) if nb else None
+    check(lib.gpt2_op_attention_packed_forward(dt, _p(o), _rows(o, "o"), _p(lse), _p(q), _rows(q, "q"), _p(k),
+                                               _rows(k, "k"), _p(v), _rows(v, "v"), _p(cu_q), _p(cu_k), n, tq, tk,
+                                               max_q, max_k, hq, hkv, hd, _p(sc), nb, _p(status), _s(stream)),
+          "gpt2_op_attention_packed_forward")
+    return sc
+
+
+def gpt2_op_attention_packed_backward(dq, dk, dv, dout, q, k, v, o, lse, cu_q, cu_k, max_q, max_k, status=None,
+                                      stream=None):
+    """dq, dk, dv of gpt2_op_attention_packed_forward from dout and the forward's o and lse."""
+    lib = load_library()
+    dt = _dtype_of(q)
+    tq, hq, hd = q.shape
+    tk, hkv = k.shape[0], k.shape[1]
+    if cu_k.numel() != cu_q.numel():
+        raise ValueError("cu_q and cu_k need the same number of sequences")
+    n = cu_q.numel() - 1
+    nb = lib.gpt2_op_attention_packed_backward_scratch(dt, n, tq, tk, hq, hkv, hd)
+    sc = _scratch(nb)
+    check(lib.gpt2_op_attention_packed_backward(dt, _p(dq), _rows(dq, "dq"), _p(dk), _rows(dk, "dk"), _p(dv),
+                                                _rows(dv, "dv"), _p(dout), _rows(dout, "dout"), _p(q), _rows(q, "q"),
+                                                _p(k), _rows(k, "k"), _p(v), _rows(v, "v"), _p(o), _rows(o, "o"),
+                                                _p(lse), _p(cu_q), _p(cu_k), n, tq, tk, max_q, max_k, hq, hkv, hd,
+                                                _p(sc), sc.numel(), _p(status), _s(stream)),
+          "gpt2_op_attention_packed_backward")
+    return sc
+
+
+def gpt2_op_token_logprobs(logp, lse, entropy, logits, targets, V, top_logp=None, top_ids=None, status=None,
+                           stream=None):
+    """logp, lse, entropy (float32 [N]) of the rows of logits [N, Vp] over their first V columns; top_logp and
+    top_ids ([N, k], both or none): the k largest."""
+    N, Vp = logits.shape
+    if (top_logp is None) != (top_ids is None) or (top_ids is not None and top_logp.shape != top_ids.shape):
+        raise ValueError("top_logp and top_ids come together, in one shape")
+    check(load_library().gpt2_op_token_logprobs(_dtype_of(logits), _p(logp), _p(lse), _p(entropy), _p(top_logp),
+                                                _p(top_ids), 0 if top_ids is None else top_ids.shape[1], _p(logits),
+                                                _p(targets), N, V, Vp, _p(status), _s(stream)),
+          "gpt2_op_token_logprobs")
+
+
+def gpt2_op_token_logprobs_backward(dlogits, logits, targets, lse, entropy, V, dlogp=None, dlse=None, dentropy=None,
+                                    status=None, stream=None):
+    """dlogits [N, Vp] (may be logits) from the gradients of gpt2_op_token_logprobs' logp, lse and entropy."""
+    N, Vp = logits.shape
+    check(load_library().gpt2_op_token_logprobs_backward(_dtype_of(logits), _p(dlogits), _p(logits), _p(targets),
+                                                         _p(lse), _p(entropy), _p(dlogp), _p(dlse), _p(dentropy), N,
+                                                         V, Vp, _p(status), _s(stream)),
+          "gpt2_op_token_logprobs_backward")
 
 
 def gpt2_op_gelu_forward(g, u, stream=None):
