@@ -251,8 +251,8 @@ int gpt2_op_attention_backward(int dtype, void* dqkv, const void* dout, const vo
  *     are clamped, so no memory outside the buffers is touched.
  *   - hd == 64 for bf16; hd 8, 16, 32 or 64 for fp32. Hq a multiple of Hkv,
  *     at most 128 query heads to a key head. Pointers 16-byte aligned, strides
- *     multiples of 16 bytes and at least the row (total_q * Hq, total_k * Hkv
- *     and n_seq + total / 16 times Hq below 2^31, else GPT2_ERR_ARG).
+ *     multiples of 16 bytes and at least the row. total_q * Hq, total_k * Hkv
+ *     and n_seq * Hq below 2^30 (else GPT2_ERR_ARG).
  *   - n_seq = 0 or total_q = 0 launches nothing.
  * Scratch: partial results of keys split over blocks (few queries). */
 size_t gpt2_op_attention_packed_forward_scratch(int dtype, int n_seq, int max_q, int max_k, int Hq, int Hkv, int hd);

@@ -168,7 +168,7 @@ size_t attention_packed_forward_scratch(int dtype, int n_seq, int max_q, int max
 }
 
 int launch_attention_packed_forward(int dtype, const PackedAttn& a, void* scratch, cudaStream_t s) {
-    if (dtype == GPT2_MODE_BF16) return forward<bf16, 64>(a, s);
+    if (dtype == GPT2_MODE_BF16) return launch_attention_packed_forward_tc(a, s);
     switch (a.hd) {
         case 8: return forward<float, 8>(a, s);
         case 16: return forward<float, 16>(a, s);

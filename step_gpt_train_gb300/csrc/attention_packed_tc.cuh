@@ -1,0 +1,83 @@
+// What the tcgen05 kernels of packed attention share: tensor maps, the search
+// for a work item's sequence, small arithmetic.
+#pragma once
+
+#include "attention_packed.cuh"
+#include "tc_common.cuh"
+
+namespace packed_tc {
+
+using namespace tc;
+
+constexpr int HD = 64;              // head size
+constexpr int TILE = 128 * HD * 2;  // 16 KB: 128 rows of 64 bf16
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+
+// Three-input maximum (one instruction on sm_100 and later).
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// (lo, hi) rounded to a packed bf16 pair, lo in the low half.
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// The work items of a packed batch are tiles of `per` rows of each sequence,
+// numbered without a table: sequence s owns the slots floor(cu[s] / per) + s
+// up to the next sequence's, which are at least its ceil(len / per) tiles
+// (floor(a + len) - floor(a) + 1 >= ceil(len) in units of per) and at most one
+// more, so total / per + n_seq slots hold every tile. The last sequence whose
+// first slot is at or before `slot`, found by a whole warp (32 probes a
+// round), or -1; any offsets give an answer in range.
+__device__ __forceinline__ int find_slot(const int32_t* cu, int n_seq, int total, int per, int slot, int& first) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = n_seq, f_lo = 0;
+    bool any = false;
+    while (true) {
+        const int step = (hi - lo + 31) / 32;
+        const int s = lo + lane * step;
+        const int f = s < hi ? min(max(cu[s], 0), total) / per + s : 0;
+        const uint32_t hit = __ballot_sync(0xffffffffu, s < hi && f <= slot);
+        const int c = __popc(hit);
+        if (c) {
+            any = true;
+            f_lo = __shfl_sync(0xffffffffu, f, c - 1);
+            lo += (c - 1) * step;
+        } else if (!any) {
+            return -1;
+        }
+        if (step == 1) break;
+        hi = min(hi, lo + step);
+    }
+    first = f_lo;
+    return lo;
+}
+
+// Rows of [heads][64] bf16 at `stride` elements, viewed as (64, heads, rows)
+// with boxes of (64, box_h, box_rows); rows past the end read as zero.
+inline bool rows_map(CUtensorMap* map, const void* p, int heads, int rows, int64_t stride, int box_h, int box_rows) {
+    auto fn = tensor_map_encoder();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)HD, (cuuint64_t)heads, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {(cuuint64_t)HD * 2, (cuuint64_t)stride * 2};
+    cuuint32_t box[3] = {HD, (cuuint32_t)box_h, (cuuint32_t)box_rows};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows [from, 128) of a swizzled tile := 0 by one warp, visible to the tensor
+// cores before the caller's arrive. (Rows keep their place under the swizzle,
+// which only permutes the 16-byte units of a row.)
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int lane) {
+    for (int i = from * 8 + lane; i < 128 * 8; i += 32) reinterpret_cast<uint4*>(tile)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
+}  // namespace packed_tc

@@ -259,10 +259,9 @@ static bool packed_ok(int dtype, int64_t total_q, int64_t total_k, int n_seq, in
     if (!dt_ok(dtype) || n_seq < 0 || total_q < 0 || total_k < 0 || max_q < 0 || max_k < 0) return false;
     if (Hq < 1 || Hkv < 1 || Hq % Hkv || Hq / Hkv > 128) return false;
     if (dtype == GPT2_MODE_BF16 ? hd != 64 : hd != 8 && hd != 16 && hd != 32 && hd != 64) return false;
-    // the kernels' work items and (head, row) pairs are counted in 32 bits
-    const int64_t most = (int64_t)1 << 31;
-    const int64_t items = n_seq + (total_q > total_k ? total_q : total_k) / 16 + 1;
-    return total_q * Hq < most && total_k * Hkv < most && items * Hq < most;
+    // the kernels count (head, row) pairs and work items in 32 bits
+    const int64_t most = (int64_t)1 << 30;
+    return total_q * Hq < most && total_k * Hkv < most && (int64_t)n_seq * Hq < most;
 }
 static bool rows_ok(const void* p, int64_t stride, int heads, int hd, int dtype) {
     const int per16 = dtype == GPT2_MODE_BF16 ? 8 : 4;
@@ -404,7 +403,8 @@ int gpt2_op_adamw(float* master, void* param_bf16, const float* grad, float* m, 
 
 int gpt2_debug_set_wait_limit(int64_t cycles) {
     const long long c = cycles > 0 ? (long long)cycles : 0;
-    if (gemm_tc_set_wait_limit(c) || attention_tc_set_wait_limit(c) || classifier_set_wait_limit(c))
+    if (gemm_tc_set_wait_limit(c) || attention_tc_set_wait_limit(c) || attention_packed_fwd_set_wait_limit(c) ||
+        classifier_set_wait_limit(c))
         return GPT2_ERR_CUDA;
     return GPT2_OK;
 }

@@ -157,6 +157,17 @@ def test_attention_many_sequences(torch_cuda, mode):
     c.check()
 
 
+@pytest.mark.parametrize("Hq,Hkv,lo,hi", [(12, 12, 1, 520), (8, 4, 20, 100), (25, 25, 100, 700)])
+def test_attention_more_items_than_ctas(torch_cuda, Hq, Hkv, lo, hi):
+    """Many short sequences: several work items for each CTA of the persistent kernels, runs of them with one tile."""
+    r = np.random.default_rng(6)
+    lk = [int(x) for x in r.integers(lo, hi, 40)]
+    c = Packed(torch_cuda, 20, lk, lk, Hq, Hkv, 64, 1, fused=True)
+    c.forward()
+    c.backward()
+    c.check()
+
+
 @pytest.mark.parametrize("mode", [1, 0], ids=["bf16", "fp32"])
 def test_attention_large_scores(torch_cuda, mode):
     """Scores up to about +-150: the running maximum moves far, most weights underflow."""
