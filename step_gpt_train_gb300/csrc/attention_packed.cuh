@@ -45,3 +45,32 @@ __device__ __forceinline__ int packed_find_row(const int32_t* cu, int n_seq, int
     }
     return lo;
 }
+
+// A work item of the query-tile kernels: `per` consecutive queries of one
+// sequence (less at its end).
+struct PackedTile {
+    int q0, nq;   // first row in the buffer, queries
+    int k0, lk;   // the sequence's keys
+    int vis;      // keys that the first query sees (may be negative)
+    int pad[3];
+};
+// The items of a call, the longest first, with a counter from which the CTAs
+// of the persistent kernels draw.
+struct PackedPlan {
+    int next, count, pad[6];
+    PackedTile tile[1];
+};
+inline size_t packed_plan_bytes(int slots) { return 32 + (size_t)slots * sizeof(PackedTile); }
+// Slots (at least as many as tiles) of `per` rows: see find_slot.
+inline int packed_slots(int total, int n_seq, int per) { return total / per + n_seq; }
+constexpr int PACKED_PLAN_MAX = 8192;  // slots that one block sorts in about the time of a launch
+int launch_packed_plan(const PackedAttn& a, PackedPlan* plan, int per, cudaStream_t s);
+
+__device__ __forceinline__ PackedTile packed_tile(const PackedSeq& p, int at, int per) {
+    PackedTile t = {p.q0 + at, min(per, p.lq - at), p.k0, p.lk, at + 1 + p.lk - p.lq, {0, 0, 0}};
+    return t;
+}
+// Key blocks of 128 that the first n queries of a tile see.
+__device__ __forceinline__ int packed_blocks(const PackedTile& t, int n) {
+    return n > 0 ? (max(0, t.vis + n - 1) + 127) / 128 : 0;
+}

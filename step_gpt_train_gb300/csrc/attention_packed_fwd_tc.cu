@@ -15,34 +15,38 @@
 //                      when the maximum grows by more than 8 (log2 units), in
 //                      fp32; back to TMEM as bf16 pairs (its one rounding);
 //   O += P V           tcgen05.mma with P from TMEM as the A operand.
-// Two threads share a row, 64 keys each: they exchange their maxima through
-// shared memory and keep their own sums. 16 softmax warps (two tiles of eight)
-// hide each other's latencies. O moves with m (rarely) in TMEM; at the end of
-// an item it is normalised and leaves through a swizzled staging buffer.
+// One thread per row, 128 scores in its registers: two threads per row with 64
+// each (16 softmax warps) exchanged their maxima and spent 470 instructions a
+// warp and step where this form spends about as many for twice the scores. O
+// moves with m (rarely) in TMEM; at the end of an item it is normalised and
+// leaves through a swizzled staging buffer.
 //
 // Warps: 0 TMA producer; 1, 2 MMA issue for tile 0, 1 (S of the next step
 // before PV of the current one); 3 finds the work items (a ring of four in
 // shared memory) and zeroes the rows of a V block behind the sequence's end
-// (0 * NaN from a neighbour would reach O); 4..19 softmax. Every wait is
-// bounded.
+// (0 * NaN from a neighbour would reach O); 4..7 output, so that the softmax
+// warps go on with the next item (short documents spent more on the way out
+// than on their blocks); 8..15 softmax. Registers: 184 a thread for the
+// softmax warps, 72 for the others. Every wait is bounded.
 #include "attention_packed_tc.cuh"
 
 namespace {
 
 using namespace packed_tc;
 
-constexpr int NST = 3;              // K and V stages
+constexpr int NST = 4;              // K and V stages
 constexpr int NIT = 4;              // work item ring
-constexpr int SOFT = 16;            // softmax warps
-constexpr int THREADS = 32 * (4 + SOFT);
+constexpr int SOFT = 8;             // softmax warps, four to a tile
+constexpr int THREADS = 32 * (8 + SOFT);
+constexpr int REGS_SOFT = 184, REGS_REST = 72;  // 256 * 184 + 256 * 72 = the 65536 of the launch (128 a thread)
 constexpr float RESCALE = 8.f;      // log2 of the largest P before the reference max moves
 // TMEM columns: S of tile 0, 1 | P of tile 0, 1 (bf16 pairs) | O of tile 0, 1
 constexpr uint32_t C_S = 0, C_P = 256, C_O = 384;
-// shared memory: Q [2 buffers][2 tiles] | K [NST] | V [NST] | staging per softmax warp | exchange | items | barriers
+// shared memory: Q [2 buffers][2 tiles] | K [NST] | V [NST] | staging per output warp | m, l | items | barriers
 constexpr int OFF_K = 4 * TILE, OFF_V = OFF_K + NST * TILE, OFF_STG = OFF_V + NST * TILE;
-constexpr int STG = 32 * 64;        // 32 half rows of O
-constexpr int OFF_X = OFF_STG + SOFT * STG;           // [2 steps][2 tiles][2 halves][128] floats
-constexpr int OFF_IT = OFF_X + 2 * 2 * 2 * 128 * 4;
+constexpr int STG = 32 * 128;       // 32 rows of O
+constexpr int OFF_ML = OFF_STG + 4 * STG;  // [2 tiles][m, l][128] floats
+constexpr int OFF_IT = OFF_ML + 2 * 2 * 128 * 4;
 constexpr int OFF_BAR = OFF_IT + NIT * 64;
 constexpr int SMEM = OFF_BAR + 512 + 1024;
 static_assert(SMEM <= 232448, "shared memory per CTA");
@@ -60,15 +64,8 @@ struct Args {
     int group, qt;        // query heads per key head, queries per tile (128 / group)
     int items;
     float scale_log2;     // log2(e) / sqrt(hd)
+    PackedPlan* plan;     // sorted items, or null: found from the offsets
 };
-
-// No use of these 16 values is scheduled before this point.
-__device__ __forceinline__ void hold16(uint32_t* r) {
-    asm volatile(""
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                   "+r"(r[15]));
-}
 
 __global__ void __launch_bounds__(THREADS, 1)
     packed_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -87,7 +84,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t it_full = bar(NIT), it_empty = bar(NIT), q_full = bar(2), q_empty = bar(2);
     const uint32_t k_full = bar(NST), k_empty = bar(NST), v_full = bar(NST), v_empty = bar(NST), v_raw = bar(NST);
     const uint32_t s_full = bar(2), s_free = bar(2), p_full = bar(2), p_free = bar(2), o_done = bar(2), o_free = bar(2);
-    const uint32_t xch = bar(8), drain = bar(2);
+    const uint32_t l_full = bar(2), l_empty = bar(2), drain = bar(2);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(gbase + OFF_BAR + 496);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + OFF_BAR + 500);
     Item* ring = reinterpret_cast<Item*>(gbase + OFF_IT);
@@ -98,7 +95,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < NIT; i++) {
             mbar_init(it_full + 8 * i, 1);
-            mbar_init(it_empty + 8 * i, 3 + SOFT);
+            mbar_init(it_empty + 8 * i, 3 + 4 + SOFT);
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(q_full + 8 * i, 1);
@@ -108,7 +105,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(p_full + 8 * i, SOFT / 2);
             mbar_init(p_free + 8 * i, 1);
             mbar_init(o_done + 8 * i, 1);
-            mbar_init(o_free + 8 * i, SOFT / 2);
+            mbar_init(o_free + 8 * i, 4);
+            mbar_init(l_full + 8 * i, SOFT / 2);
+            mbar_init(l_empty + 8 * i, 4);
             mbar_init(drain + 8 * i, 1);
         }
         for (int i = 0; i < NST; i++) {
@@ -118,7 +117,6 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(v_empty + 8 * i, 2);
             mbar_init(v_raw + 8 * i, 1);
         }
-        for (int i = 0; i < 8; i++) mbar_init(xch + 8 * i, 2);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -132,12 +130,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     // Item i of this CTA's list, by a whole warp; false when the CTA gave up.
     auto take = [&](int i, Item& it) -> bool {
         const int sl = i % NIT;
-        if (!warp_wait(it_full + 8 * sl, (i / NIT) & 1, abort_flag, status)) return false;
+        if (!wait(it_full + 8 * sl, (i / NIT) & 1, abort_flag, status)) return false;
         it = ring[sl];
         __syncwarp();
         if (lane == 0) mbar_arrive(it_empty + 8 * sl);
         return it.valid;
     };
+
+    if (warp < 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFT));
 
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer
@@ -217,11 +218,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             return Cur{false, i, 0, 0, 0};
         };
+        int k_seen = -1;  // the last key block waited for ahead of its step
         auto issue_s = [&](const Cur& c, int g) -> bool {
             const int b = c.base + c.j, st = b % NST;
-            if (c.j == 0 && !warp_wait(q_full + 8 * (c.i & 1), (c.i >> 1) & 1, abort_flag, status)) return false;
-            if (!warp_wait(k_full + 8 * st, (b / NST) & 1, abort_flag, status)) return false;
-            if (!warp_wait(s_free + 8 * t, (g & 1) ^ 1u, abort_flag, status)) return false;
+            if (c.j == 0 && !wait(q_full + 8 * (c.i & 1), (c.i >> 1) & 1, abort_flag, status)) return false;
+            if (k_seen != b && !wait(k_full + 8 * st, (b / NST) & 1, abort_flag, status)) return false;
+            if (!wait(s_free + 8 * t, (g & 1) ^ 1u, abort_flag, status)) return false;
             tc_fence_after();
             const uint64_t da = sw128_desc(sQ(c.i & 1, t), 16, 1024), db = sw128_desc(sK(st), 16, 1024);
             if (leader) {
@@ -242,12 +244,18 @@ __global__ void __launch_bounds__(THREADS, 1)
             Cur nx = c;
             if (++nx.j == nx.n) nx = first_of(c.i + 1, 1);
             if (nx.valid && !(ok = issue_s(nx, g + 1))) break;
+            // P last: the others have long arrived, and each wait passed after P would delay PV
             const int b = c.base + c.j, st = b % NST;
-            if (!(ok = warp_wait(p_full + 8 * t, g & 1, abort_flag, status))) break;
-            if (!(ok = warp_wait(v_full + 8 * st, (b / NST) & 1, abort_flag, status))) break;
-            if (c.j == 0 && !(ok = warp_wait(o_free + 8 * t, (done & 1) ^ 1u, abort_flag, status))) break;
-            tc_fence_after();
             const uint64_t dv = sw128_desc(sV(st), 8192, 1024);
+            if (!(ok = wait(v_full + 8 * st, (b / NST) & 1, abort_flag, status))) break;
+            if (c.j == 0 && !(ok = wait(o_free + 8 * t, (done & 1) ^ 1u, abort_flag, status))) break;
+            if (nx.valid && nx.j < nx.n - 1) {  // the K block after the next one, for the S that follows this PV
+                const int b2 = nx.base + nx.j + 1, st2 = b2 % NST;
+                if (!(ok = wait(k_full + 8 * st2, (b2 / NST) & 1, abort_flag, status))) break;
+                k_seen = b2;
+            }
+            if (!(ok = wait(p_full + 8 * t, g & 1, abort_flag, status))) break;
+            tc_fence_after();
             if (leader) {
 #pragma unroll
                 for (int kk = 0; kk < 8; kk++)
@@ -272,34 +280,49 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int per = 2 * A.qt;
         const int slots = A.items / a.Hkv;
         int x = blockIdx.x, blocks = 0;
-        if (blockIdx.x == 0) packed_check(a, lane, 32);
-        auto put = [&](int i, Item& it) -> bool {  // the next item with queries, or the end, into ring slot i
-            it.valid = 0;
+        if (blockIdx.x == 0 && !A.plan) packed_check(a, lane, 32);
+        auto next_tile = [&](PackedTile& p, int& kh) -> bool {
+            if (A.plan) {
+                int n = 0;
+                if (lane == 0) n = atomicAdd(&A.plan->next, 1);
+                n = __shfl_sync(0xffffffffu, n, 0);
+                if (n >= A.plan->count * a.Hkv) return false;
+                p = A.plan->tile[n / a.Hkv];
+                kh = n % a.Hkv;
+                return true;
+            }
             for (; x < A.items; x += gridDim.x) {
                 int f;
                 const int slot = slots - 1 - x / a.Hkv;  // the later tiles of a sequence, which see more keys, first
                 const int s = find_slot(a.cu_q, a.n_seq, a.total_q, per, slot, f);
                 if (s < 0) continue;
-                const PackedSeq p = packed_seq(a, s);
+                const PackedSeq q = packed_seq(a, s);
                 const int at = (slot - f) * per;
-                if (at < 0 || at >= p.lq) continue;
-                it.valid = 1;
-                it.kh = x % a.Hkv;
-                it.q0 = p.q0 + at;
-                it.nq0 = min(A.qt, p.lq - at);
-                it.nq1 = min(A.qt, max(0, p.lq - at - A.qt));
+                if (at < 0 || at >= q.lq) continue;
+                p = packed_tile(q, at, per);
+                kh = x % a.Hkv;
+                x += gridDim.x;
+                return true;
+            }
+            return false;
+        };
+        auto put = [&](int i, Item& it) -> bool {  // the next item, or the end, into ring slot i
+            PackedTile p;
+            it.valid = next_tile(p, it.kh);
+            if (it.valid) {
+                it.q0 = p.q0;
+                it.nq0 = min(A.qt, p.nq);
+                it.nq1 = p.nq - it.nq0;
                 it.k0 = p.k0;
                 it.lk = p.lk;
-                it.vis = at + 1 + p.lk - p.lq;
-                it.n0 = (max(0, it.vis + it.nq0 - 1) + 127) / 128;
-                it.n1 = it.nq1 > 0 ? (max(0, it.vis + A.qt + it.nq1 - 1) + 127) / 128 : 0;
+                it.vis = p.vis;
+                it.n0 = packed_blocks(p, it.nq0);
+                it.n1 = it.nq1 > 0 ? packed_blocks(p, p.nq) : 0;
                 it.base = blocks;
                 blocks += max(it.n0, it.n1);
-                x += gridDim.x;
-                break;
             }
             const int sl = i % NIT;
-            if (!warp_wait(it_empty + 8 * sl, ((i / NIT) & 1) ^ 1u, abort_flag, status)) return false;
+            if (!wait(it_empty + 8 * sl, ((i / NIT) & 1) ^ 1u, abort_flag, status)) return false;
             if (lane == 0) {
                 ring[sl] = it;
                 mbar_arrive(it_full + 8 * sl);
@@ -320,41 +343,103 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int e = 0; e < NST; e++)
                     if (e == st) u = uses[e]++;
-                if (!(ok = warp_wait(v_raw + 8 * st, u & 1, abort_flag, status))) break;
+                if (!(ok = wait(v_raw + 8 * st, u & 1, abort_flag, status))) break;
                 zero_rows(gbase + OFF_V + st * TILE, cur.lk - (n - 1) * 128, lane);
                 if (lane == 0) mbar_arrive(v_full + 8 * st);
             }
             cur = nxt;
         }
+    } else if (warp < 8) {
+        // ------------------------------------------------------ output
+        const int quad = warp & 3, r = quad * 32 + lane;  // row of a tile = TMEM lane
+        const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16) + C_O;
+        const float* ml = reinterpret_cast<const float*>(gbase + OFF_ML);
+        uint8_t* st = gbase + OFF_STG + quad * STG;
+        bf16* o = reinterpret_cast<bf16*>(a.o);
+        const int qi = r / A.group, hg = r - qi * A.group;  // this row's query in the tile, head in the group
+        int done[2] = {0, 0};
+        Item it;
+        bool ok = true;
+#pragma unroll 1
+        for (int i = 0; ok && take(i, it); i++) {
+#pragma unroll 1
+            for (int t = 0; t < 2; t++) {
+                const int n = t ? it.n1 : it.n0, nq = t ? it.nq1 : it.nq0;
+                if (nq <= 0) continue;
+                const int row = it.q0 + (t ? A.qt : 0) + qi;
+                const bool mine = qi < nq;  // (and qi < qt: a tile's unused last rows lie behind its nq queries)
+                // out through this warp's staging buffer (chunk c of row s at (c ^ (s & 7)) * 16: conflict-free
+                // both ways), so that each store covers four whole 128-byte rows
+                const int64_t off = mine ? (int64_t)row * a.o_stride + (it.kh * A.group + hg) * HD : -1;
+                uint8_t* my = st + lane * 128;
+                float L = -INFINITY;
+                if (n) {
+                    const int d = t ? done[1]++ : done[0]++;
+                    if (!(ok = wait(l_full + 8 * t, d & 1, abort_flag, status))) break;
+                    const float m = ml[t * 256 + r], l = ml[t * 256 + 128 + r];
+                    if (!(ok = wait(o_done + 8 * t, d & 1, abort_flag, status))) break;
+                    tc_fence_after();
+                    const bool some = it.vis + (t ? A.qt : 0) + qi > 0;  // the query sees a key
+                    const float inv = 1.f / l;
+#pragma unroll
+                    for (int hh = 0; hh < 2; hh++) {
+                        uint32_t ov[32];
+                        tc_ld32_issue(trow + 64 * t + 32 * hh, ov);
+                        tc_ld_wait(ov);
+                        if (hh) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) {
+                                mbar_arrive(o_free + 8 * t);
+                                mbar_arrive(l_empty + 8 * t);
+                            }
+                        }
+#pragma unroll
+                        for (int c = 0; c < 4; c++) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int u = 0; u < 4; u++)
+                                w[u] = some ? cvt_bf16x2(__uint_as_float(ov[c * 8 + 2 * u]) * inv,
+                                                         __uint_as_float(ov[c * 8 + 2 * u + 1]) * inv)
+                                            : 0u;
+                            *reinterpret_cast<uint4*>(my + (((hh * 4 + c) ^ (lane & 7)) << 4)) =
+                                make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                    if (some) L = (m + log2f(l)) * LN2;
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 8; c++)
+                        *reinterpret_cast<uint4*>(my + (c << 4)) = make_uint4(0, 0, 0, 0);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    const int sr = e * 4 + (lane >> 3), c = lane & 7;
+                    const int64_t at = __shfl_sync(0xffffffffu, off, sr);
+                    const uint4 w = *reinterpret_cast<const uint4*>(st + sr * 128 + ((c ^ (sr & 7)) << 4));
+                    if (at >= 0) *reinterpret_cast<uint4*>(o + at + c * 8) = w;
+                }
+                __syncwarp();  // the staged rows have been read
+                if (mine) a.lse[(int64_t)(it.kh * A.group + hg) * a.total_q + row] = L;
+            }
+        }
     } else {
         // ------------------------------------------------------ softmax
-        const int sw = warp - 4, t = sw >> 3, half = (sw >> 2) & 1, quad = warp & 3;
+        const int t = (warp >> 2) & 1, quad = warp & 3;
         const int r = quad * 32 + lane;  // row of the tile = TMEM lane
         const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
-        const uint32_t tS = trow + C_S + 128 * t + 64 * half, tP = trow + C_P + 64 * t + 32 * half;
-        const uint32_t tO = trow + C_O + 64 * t + 32 * half;
-        const uint32_t xbar = xch + 8 * (t * 4 + quad);
-        float* xs = reinterpret_cast<float*>(gbase + OFF_X) + t * 256;  // [step & 1][..][half][row]
-        const int qi = r / A.group, hg = r - qi * A.group;              // this row's query in the tile, head in the group
+        const uint32_t tS = trow + C_S + 128 * t, tP = trow + C_P + 64 * t, tO = trow + C_O + 64 * t;
+        const int qi = r / A.group;      // this row's query in the tile
+        float* ml = reinterpret_cast<float*>(gbase + OFF_ML) + t * 256;
         const uint64_t scale2 = f2_pack(A.scale_log2, A.scale_log2);
-        int g = 0, xc = 0, done = 0;  // steps, exchanges, finished items with blocks
-        // this row's value of the other half's thread
-        auto exchange = [&](float mine, float& theirs) -> bool {
-            float* at = xs + (xc & 1) * 512;
-            at[half * 128 + r] = mine;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(xbar);
-            if (!warp_wait(xbar, xc & 1, abort_flag, status)) return false;
-            theirs = at[(half ^ 1) * 128 + r];
-            xc++;
-            return true;
-        };
+        int g = 0, done = 0;             // steps, finished items with blocks
         bool ok = true;
 #pragma unroll 1
         for (int i = 0;; i++) {
             // the item stays in the ring until its end, so that its fields take no registers meanwhile
             const int sl = i % NIT;
-            if (!warp_wait(it_full + 8 * sl, (i / NIT) & 1, abort_flag, status)) break;
+            if (!wait(it_full + 8 * sl, (i / NIT) & 1, abort_flag, status)) break;
             const volatile Item& it = ring[sl];
             if (!it.valid) break;
             const int n = t ? it.n1 : it.n0;
@@ -362,122 +447,87 @@ __global__ void __launch_bounds__(THREADS, 1)
             float m = -INFINITY, l = 0.f;
 #pragma unroll 1
             for (int j = 0; j < n; j++, g++) {
-                uint32_t v[2][32];
-                if (!(ok = warp_wait(s_full + 8 * t, g & 1, abort_flag, status))) break;
+                uint32_t v[4][32];
+                if (!(ok = wait(s_full + 8 * t, g & 1, abort_flag, status))) break;
                 tc_fence_after();
-                tc_ld32_issue(tS, v[0]);
-                tc_ld32_issue(tS + 32, v[1]);
-                tc_ld_wait(v[0]);
-                tc_ld_wait(v[1]);
+#pragma unroll
+                for (int c = 0; c < 4; c++) tc_ld32_issue(tS + 32 * c, v[c]);
+#pragma unroll
+                for (int c = 0; c < 4; c++) tc_ld_wait(v[c]);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_free + 8 * t);  // the MMA may write the next S
-                const int hi = vis - j * 128 - half * 64;    // columns [0, hi) are seen
-                if (__any_sync(0xffffffffu, hi < 64)) {
+                const int hi = vis - j * 128;  // columns [0, hi) are seen
+                if (__any_sync(0xffffffffu, hi < 128)) {
+                    // chunks that some row of the warp does not see whole
+                    const int least = __reduce_min_sync(0xffffffffu, hi);
 #pragma unroll
-                    for (int e = 0; e < 64; e++)
-                        if (e >= hi) v[e >> 5][e & 31] = 0xff800000u;
+                    for (int c = 0; c < 4; c++)
+                        if (least < c * 32 + 32) {
+#pragma unroll
+                            for (int e = 0; e < 32; e++)
+                                if (c * 32 + e >= hi) v[c][e] = 0xff800000u;
+                        }
                 }
+                // From here to the stores one straight block: branches in it cost more than the work they saved
+                // (chunks that no row sees left out: 113 -> 133 us on the ragged prompts)
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int e = 0; e < 64; e += 2)
-                    m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], __uint_as_float(v[e >> 5][e & 31]),
-                                             __uint_as_float(v[e >> 5][(e & 31) + 1]));
-                float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), other;
-                if (!(ok = exchange(mx, other))) break;
-                mx = fmaxf(mx, other) * A.scale_log2;
-                float factor = 1.f;
+                for (int c = 0; c < 4; c++)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2)
+                        m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
+                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * A.scale_log2;
                 const bool move = mx > m + RESCALE;
-                if (move) {
-                    factor = ex2_approx(m - mx);  // 0 from -inf
-                    m = mx;
-                    l *= factor;
-                }
-                const uint64_t nm2 = f2_pack(-m, -m);
-                uint64_t l2[2] = {0, 0};
+                const float factor = move ? ex2_approx(m - mx) : 1.f;  // 0 from -inf
+                m = move ? mx : m;
+                l *= factor;
+                const float nm = m == -INFINITY ? 0.f : -m;  // no finite score yet: every weight is 0
+                const uint64_t nm2 = f2_pack(nm, nm);
+                uint64_t l2[4] = {0, 0, 0, 0};
+                uint32_t pk[2][32];
 #pragma unroll
-                for (int e = 0; e < 64; e += 2) {
-                    if (e % 16 == 0) hold16(&v[e >> 5][e & 31]);  // 16 scores at a time: the registers do not suffice for more
-                    float x0, x1;
-                    f2_unpack(f2_fma(f2_pack(v[e >> 5][e & 31], v[e >> 5][(e & 31) + 1]), scale2, nm2), x0, x1);
-                    const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-                    l2[(e >> 1) & 1] = f2_add(l2[(e >> 1) & 1], f2_pack(p0, p1));
-                    v[0][e / 2] = cvt_bf16x2(p0, p1);
-                }
-                float s0, s1, s2, s3;
-                f2_unpack(l2[0], s0, s1);
-                f2_unpack(l2[1], s2, s3);
-                l += (s0 + s1) + (s2 + s3);
+                for (int c = 0; c < 4; c++)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float x0, x1;
+                        f2_unpack(f2_fma(f2_pack(v[c][e], v[c][e + 1]), scale2, nm2), x0, x1);
+                        const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+                        l2[(e >> 1) & 3] = f2_add(l2[(e >> 1) & 3], f2_pack(p0, p1));
+                        pk[c >> 1][(c & 1) * 16 + e / 2] = cvt_bf16x2(p0, p1);
+                    }
                 // PV of the previous step has finished with P and O
-                if (!(ok = warp_wait(p_free + 8 * t, (g & 1) ^ 1u, abort_flag, status))) break;
+                if (!(ok = wait(p_free + 8 * t, (g & 1) ^ 1u, abort_flag, status))) break;
                 tc_fence_after();
+                tc_st32(tP, pk[0]);
+                tc_st32(tP + 32, pk[1]);
+                l += f2_total(f2_add(f2_add(l2[0], l2[1]), f2_add(l2[2], l2[3])));
                 if (j > 0 && __any_sync(0xffffffffu, move)) {
-                    uint32_t ov[32];
-                    tc_ld32_issue(tO, ov);
-                    tc_ld_wait(ov);
 #pragma unroll
-                    for (int e = 0; e < 32; e++) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * factor);
-                    tc_st32(tO, ov);
+                    for (int c = 0; c < 2; c++) {
+                        uint32_t ov[32];
+                        tc_ld32_issue(tO + 32 * c, ov);
+                        tc_ld_wait(ov);
+#pragma unroll
+                        for (int e = 0; e < 32; e++) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * factor);
+                        tc_st32(tO + 32 * c, ov);
+                    }
                 }
-                tc_st32(tP, v[0]);
                 tc_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full + 8 * t);
             }
             if (!ok) break;
-            uint32_t ov[32];
-            float other = 0.f;
-            if (n) {
-                if (!(ok = exchange(l, other))) break;
-                if (!(ok = warp_wait(o_done + 8 * t, done & 1, abort_flag, status))) break;
-                done++;
-                tc_fence_after();
-                tc_ld32_issue(tO, ov);
-                tc_ld_wait(ov);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(o_free + 8 * t);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 32; e++) ov[e] = 0;
-            }
-            const int nq = t ? it.nq1 : it.nq0, row0 = it.q0 + (t ? A.qt : 0), head0 = it.kh * A.group;
             __syncwarp();
             if (lane == 0) mbar_arrive(it_empty + 8 * sl);
-            if (nq > 0) {
-                // O / l through this warp's staging buffer (half rows of 64 bytes), so that
-                // each store covers whole 64-byte pieces of 8 rows
-                const bool some = n && vis > 0;
-                l += other;
-                const float inv = 1.f / l;
-                uint8_t* st = gbase + OFF_STG + sw * STG;
+            if (n) {  // m and l to the output warps
+                if (!wait(l_empty + 8 * t, (done & 1) ^ 1u, abort_flag, status)) break;
+                done++;
+                ml[r] = m;
+                ml[128 + r] = l;
                 __syncwarp();
-#pragma unroll
-                for (int q = 0; q < 4; q++) {
-                    uint4 w;
-                    uint32_t* wp = &w.x;
-#pragma unroll
-                    for (int u = 0; u < 4; u++)
-                        wp[u] = some ? cvt_bf16x2(__uint_as_float(ov[q * 8 + 2 * u]) * inv,
-                                                  __uint_as_float(ov[q * 8 + 2 * u + 1]) * inv)
-                                     : 0u;
-                    stage16(st, lane, q, w);
-                }
-                __syncwarp();
-                bf16* o = reinterpret_cast<bf16*>(a.o);
-#pragma unroll 1
-                for (int e = 0; e < 4; e++) {
-                    const int sr = e * 8 + (lane >> 2), c = lane & 3;
-                    const int rr = quad * 32 + sr, q = rr / A.group, h = rr - q * A.group;
-                    if (q < nq)
-                        *reinterpret_cast<uint4*>(o + (int64_t)(row0 + q) * a.o_stride + (head0 + h) * HD +
-                                                  half * 32 + c * 8) =
-                            *reinterpret_cast<const uint4*>(st + sr * 64 + ((c ^ ((sr >> 1) & 3)) << 4));
-                }
-                if (half == 0 && qi < nq)
-                    a.lse[(int64_t)(head0 + hg) * a.total_q + row0 + qi] =
-                        some ? (m + log2f(l)) * LN2 : -INFINITY;
+                if (lane == 0) mbar_arrive(l_full + 8 * t);
             }
         }
     }
@@ -495,13 +545,27 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 int attention_packed_fwd_set_wait_limit(long long cycles) { return set_wait_limit(cycles); }
 
-int launch_attention_packed_forward_tc(const PackedAttn& a, cudaStream_t s) {
+// Items sorted by length are worth their own launch once there are more than
+// SMs to take them; beyond PACKED_PLAN_MAX the sort would cost more than the
+// imbalance, which evens out over so many.
+static bool planned(int slots, int Hkv) {
+    return (int64_t)slots * Hkv > gpt2_num_sms() && slots <= PACKED_PLAN_MAX;
+}
+
+size_t attention_packed_forward_tc_scratch(int n_seq, int total_q, int Hq, int Hkv) {
+    const int slots = packed_slots(total_q, n_seq, 2 * (128 / (Hq / Hkv)));
+    return slots <= PACKED_PLAN_MAX ? packed_plan_bytes(slots) : 0;
+}
+
+int launch_attention_packed_forward_tc(const PackedAttn& a, PackedPlan* plan, cudaStream_t s) {
     Args A;
     A.a = a;
     A.group = a.Hq / a.Hkv;
     A.qt = 128 / A.group;
-    A.items = (a.total_q / (2 * A.qt) + a.n_seq) * a.Hkv;
+    const int slots = packed_slots(a.total_q, a.n_seq, 2 * A.qt);
+    A.items = slots * a.Hkv;
     A.scale_log2 = LOG2E / sqrtf((float)HD);
+    A.plan = planned(slots, a.Hkv) ? plan : nullptr;
     CUtensorMap mq, mk, mv;
     // without keys nothing is loaded through the key and value maps
     const bool keys = a.total_k > 0;
@@ -511,6 +575,7 @@ int launch_attention_packed_forward_tc(const PackedAttn& a, cudaStream_t s) {
         return GPT2_ERR_CUDA;
     if (smem_attr((const void*)packed_fwd_tc_kernel, SMEM) != cudaSuccess) return GPT2_ERR_CUDA;
     const int grid = A.items < gpt2_num_sms() ? A.items : gpt2_num_sms();
+    if (A.plan) launch_packed_plan(a, plan, 2 * A.qt, s);
     packed_fwd_tc_kernel<<<grid, THREADS, SMEM, s>>>(mq, mk, mv, A);
-    return 1;
+    return A.plan ? 2 : 1;
 }

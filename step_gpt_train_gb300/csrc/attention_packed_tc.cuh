@@ -26,6 +26,35 @@ __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
     return d;
 }
 
+__device__ __forceinline__ float f2_total(uint64_t v) {
+    float lo, hi;
+    f2_unpack(v, lo, hi);
+    return lo + hi;
+}
+
+// Bounded wait by a whole warp for the phase with the given parity: one try
+// and one vote a turn. Roles off the critical path sleep NS nanoseconds between
+// turns, so that their turns do not take the other warps' issue slots.
+template <int NS = 0>
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+    if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+    const long long t0 = clock64();
+    const long long limit = *(volatile long long*)&wait_limit_cycles;
+#pragma unroll 1
+    for (uint32_t n = 1;; n++) {
+        if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+        if (NS) __nanosleep(NS);
+        if (n % 64 == 0) {
+            const bool late = clock64() - t0 > limit;
+            if (late) {
+                set_status(status, GPT2_FLAG_TIMEOUT);
+                *abort_flag = 1;
+            }
+            if (__any_sync(0xffffffffu, late || *abort_flag)) return false;
+        }
+    }
+}
+
 // The work items of a packed batch are tiles of `per` rows of each sequence,
 // numbered without a table: sequence s owns the slots floor(cu[s] / per) + s
 // up to the next sequence's, which are at least its ceil(len / per) tiles

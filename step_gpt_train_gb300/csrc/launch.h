@@ -122,9 +122,12 @@ struct PackedAttnGrad {
     int64_t dout_stride, dq_stride, dk_stride, dv_stride;
     float* D;  // [Hq, total_q]
 };
-size_t attention_packed_forward_scratch(int dtype, int n_seq, int max_q, int max_k, int Hq, int Hkv, int hd);
+size_t attention_packed_forward_scratch(int dtype, int n_seq, int total_q, int max_q, int max_k, int Hq, int Hkv,
+                                        int hd);
 // bf16 on the tensor cores.
-int launch_attention_packed_forward_tc(const PackedAttn& a, cudaStream_t s);
+struct PackedPlan;
+size_t attention_packed_forward_tc_scratch(int n_seq, int total_q, int Hq, int Hkv);
+int launch_attention_packed_forward_tc(const PackedAttn& a, PackedPlan* plan, cudaStream_t s);
 int attention_packed_fwd_set_wait_limit(long long cycles);
 int launch_attention_packed_forward(int dtype, const PackedAttn& a, void* scratch, cudaStream_t s);
 size_t attention_packed_backward_scratch(int dtype, int n_seq, int total_q, int total_k, int Hq, int Hkv, int hd);
