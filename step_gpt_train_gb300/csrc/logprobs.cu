@@ -1,124 +1,412 @@
 // Log-probabilities of given tokens, with entropy and the top alternatives,
-// and their gradient.
+// and their gradient. Both are bound by HBM: the logits are read once (and
+// the gradient written once); everything else stays in registers.
+//
+// With m the row's maximum, d_j = (z_j - m) log2(e) and e_j = 2^d_j,
+//   S = sum e_j, T = sum e_j d_j:  lse = m + ln S,  entropy = ln S - ln2 T / S,
+// in one pass: a thread keeps its own m, S, T and moves them to a new maximum
+// by S' = f S, T' = f (T + S (m - m') log2(e)), f = 2^((m - m') log2(e)).
 #include "common.cuh"
 #include "launch.h"
+#include "tc_common.cuh"
+
+#include <cooperative_groups.h>
 
 namespace {
 
-constexpr int LP_NT = 256;
+namespace cg = cooperative_groups;
+using namespace tc;
 
-// A logit's place in the order (larger logits larger; -0 as 0) above its
-// column's (lower columns larger): unique within a row.
+constexpr int NT = 256;       // threads of a block
+constexpr int BATCH = 4;      // 16-byte vectors a thread has in flight
+constexpr int MAX_SPLIT = 8;  // blocks (a cluster) that share a row
+constexpr int MAX_K = 64;
+constexpr int CAND = 512;     // candidates for the top k that fit in shared memory
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+
+template <typename T> constexpr int VEC = 16 / sizeof(T);  // values of a 16-byte vector
+
+__device__ __forceinline__ void unpack(const uint4& u, float (&f)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void unpack(const uint4& u, float (&f)[4]) {
+    f[0] = __uint_as_float(u.x);
+    f[1] = __uint_as_float(u.y);
+    f[2] = __uint_as_float(u.z);
+    f[3] = __uint_as_float(u.w);
+}
+__device__ __forceinline__ void pack(uint4& u, const float (&f)[8]) {
+    uint32_t* w = &u.x;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+__device__ __forceinline__ void pack(uint4& u, const float (&f)[4]) {
+    u = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+
+// Maxima that a NaN passes through.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// A logit's place in the order (larger logits larger, -0 as 0) above its
+// column's (lower columns larger): unique within a row, never 0.
 __device__ __forceinline__ uint64_t order_key(float z, int col) {
     const int b = __float_as_int(z + 0.f);
     const uint32_t u = (uint32_t)(b < 0 ? ~b : b ^ 0x80000000);
     return ((uint64_t)u << 32) | (uint32_t)~col;
 }
+__device__ __forceinline__ int key_col(uint64_t k) { return (int)~(uint32_t)k; }
+__device__ __forceinline__ float key_logit(uint64_t k) {
+    const uint32_t u = (uint32_t)(k >> 32);
+    return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
+}
 
+// Maximum, sum and weighted sum of some of a row's values.
+struct Stats {
+    float m, s, t;
+};
+// The reference that d is taken against: 0 before any finite value, so that
+// e = 2^-inf = 0 and nothing becomes inf - inf.
+__device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.f : m; }
+__device__ __forceinline__ void move_to(Stats& x, float m) {
+    if (x.m == m) return;
+    if (x.m == -INFINITY) {
+        x.m = m;  // s = t = 0
+        return;
+    }
+    const float d = (x.m - m) * LOG2E, f = ex2_approx(d);
+    x.t = f == 0.f ? 0.f : f * (x.t + x.s * d);
+    x.s *= f;
+    x.m = m;
+}
+__device__ __forceinline__ Stats join(Stats a, Stats b) {
+    const float m = max_nan(a.m, b.m);
+    move_to(a, m);
+    move_to(b, m);
+    a.s += b.s;
+    a.t += b.t;
+    return a;
+}
+
+// One vector's values (columns col .. col + VEC - 1, those at or past V left
+// out) into x; `bm` their maximum.
+template <typename T> __device__ __forceinline__ void add_vec(const float (&f)[VEC<T>], Stats& x) {
+    const float m = reference(x.m);
+    const uint64_t m2 = f2_pack(m, m), l2e = f2_pack(LOG2E, LOG2E);
+    uint64_t s2 = 0, t2 = 0;
+#pragma unroll
+    for (int j = 0; j < VEC<T>; j += 2) {
+        float d0, d1;
+        // the difference first: z log2(e) - m log2(e) is off by |m| 2^-24, and masks go down to -1e38
+        f2_unpack(f2_mul(f2_sub(f2_pack(f[j], f[j + 1]), m2), l2e), d0, d1);
+        const uint64_t e2 = f2_pack(ex2_approx(d0), ex2_approx(d1));
+        s2 = f2_add(s2, e2);
+        // below 2^-150 e is 0, and 0 * -inf must not count
+        t2 = f2_fma(e2, f2_pack(fmaxf(d0, -200.f), fmaxf(d1, -200.f)), t2);
+    }
+    float a, b;
+    f2_unpack(s2, a, b);
+    x.s += a + b;
+    f2_unpack(t2, a, b);
+    x.t += a + b;
+}
+
+// The split-th part of a row's vectors: [first, last).
+__device__ __forceinline__ void part(int nv, int split, int rank, int& first, int& last) {
+    const int per = (nv + split - 1) / split;
+    first = min(rank * per, nv);
+    last = min(first + per, nv);
+}
+
+// A row is read by `split` blocks (a cluster), 256 threads each, thread t
+// taking every 256th vector of the block's part. Top k: each thread knows its
+// largest logit; the k-th largest of those 256 bounds the block's k-th largest
+// from below, so the few threads above it look through their own vectors again
+// (from L2) and keep what reaches the bound: about k candidates, ranked by
+// counting. More than CAND (many equal logits) are found one by one. The
+// blocks' lists and sums meet in the first block's shared memory.
 template <typename T>
-__global__ void __launch_bounds__(LP_NT)
-    logprobs_kernel(float* logp, float* lse, float* entropy, float* top_logp, int32_t* top_ids, int k,
-                    const T* logits, const int32_t* targets, int N, int V, int Vp, int* status) {
-    __shared__ float sh[3][LP_NT];
-    __shared__ uint64_t best[LP_NT];
-    const int row = blockIdx.x, tid = threadIdx.x;
+__global__ void __launch_bounds__(NT)
+    logprobs_kernel(float* __restrict__ logp, float* __restrict__ lse, float* __restrict__ entropy,
+                    float* __restrict__ top_logp, int32_t* __restrict__ top_ids, int k, const T* __restrict__ logits,
+                    const int32_t* __restrict__ targets, int V, int Vp, int split, int* status) {
+    __shared__ Stats ws[NT / 32], cs[MAX_SPLIT];
+    __shared__ uint64_t keys[CAND], lists[MAX_SPLIT * MAX_K], bound;
+    __shared__ int count;
+    const int row = blockIdx.x / split, rank = blockIdx.x - row * split;
+    const int tid = threadIdx.x, lane = tid & 31;
     const T* z = logits + (int64_t)row * Vp;
-    float m = -INFINITY;
-    for (int j = tid; j < V; j += LP_NT) {
-        const float x = to_float(z[j]);
-        m = x > m || x != x ? x : m;
-    }
-    sh[0][tid] = m;
-    __syncthreads();
-    for (int w = LP_NT / 2; w > 0; w /= 2) {
-        if (tid < w) {
-            const float x = sh[0][tid], y = sh[0][tid + w];
-            sh[0][tid] = y > x || y != y ? y : x;
+    const uint4* zv = reinterpret_cast<const uint4*>(z);
+    const int nv = (V + VEC<T> - 1) / VEC<T>;
+    int v0, v1;
+    part(nv, split, rank, v0, v1);
+    // every block of the cluster is running before another writes to its shared memory
+    if (split > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    float zt = 0.f;  // the target's logit, on its way while the row is read
+    if (rank == 0 && tid == 0 && logp) {
+        int tgt = targets[row];
+        if (tgt < 0 || tgt >= V) {
+            set_status(status, GPT2_FLAG_TARGET_RANGE);
+            tgt = 0;
         }
-        __syncthreads();
+        zt = to_float(z[tgt]);
     }
-    m = sh[0][0];
-    float s = 0.f, t = 0.f;
-    for (int j = tid; j < V; j += LP_NT) {
-        const float d = to_float(z[j]) - m, e = expf(d);
-        s += e;
-        if (!(e == 0.f)) t += e * d;
-    }
-    sh[1][tid] = s;
-    sh[2][tid] = t;
-    __syncthreads();
-    for (int w = LP_NT / 2; w > 0; w /= 2) {
-        if (tid < w) {
-            sh[1][tid] += sh[1][tid + w];
-            sh[2][tid] += sh[2][tid + w];
+
+    Stats x = {-INFINITY, 0.f, 0.f};
+    for (int i = v0 + tid; i < v1; i += BATCH * NT) {
+        uint4 u[BATCH];
+#pragma unroll
+        for (int b = 0; b < BATCH; b++)
+            if (i + b * NT < v1) u[b] = __ldg(zv + i + b * NT);
+#pragma unroll
+        for (int b = 0; b < BATCH; b++) {
+            const int v = i + b * NT;
+            if (v >= v1) break;
+            float f[VEC<T>];
+            unpack(u[b], f);
+            if (v * VEC<T> + VEC<T> > V) {  // the vector that V cuts
+#pragma unroll
+                for (int j = 0; j < VEC<T>; j++)
+                    if (v * VEC<T> + j >= V) f[j] = -INFINITY;
+            }
+            float m = x.m;
+#pragma unroll
+            for (int j = 0; j < VEC<T>; j += 2) m = max_nan(m, f[j], f[j + 1]);
+            if (m != x.m) move_to(x, m);
+            add_vec<T>(f, x);
         }
-        __syncthreads();
     }
-    s = sh[1][0];
-    t = sh[2][0];
-    const bool none = m == -INFINITY;
-    const float L = isinf(m) ? m : m + logf(s);
+    const float mine = x.m;  // this thread's largest logit
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) {
+        const Stats y = {__shfl_xor_sync(0xffffffffu, x.m, o), __shfl_xor_sync(0xffffffffu, x.s, o),
+                         __shfl_xor_sync(0xffffffffu, x.t, o)};
+        x = (lane & o) ? join(y, x) : join(x, y);  // the same order in both lanes
+    }
+    if (lane == 0) ws[tid >> 5] = x;
+    if (split > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+
+    if (k) {
+        const bool any = v0 + tid < v1;
+        // the k-th largest thread maximum (keys unique by thread); 0 with fewer threads than k
+        const uint64_t key = any ? order_key(mine, tid) : 0;
+        keys[tid] = key;
+        if (tid == 0) bound = 0, count = 0;
+        __syncthreads();
+        int above = 0;
+        for (int j = 0; j < NT; j++) above += keys[j] > key;
+        if (any && above == k - 1) bound = key;
+        __syncthreads();
+        const uint64_t least = bound;
+        __syncthreads();  // keys[] is reused for the candidates
+        auto each = [&](auto&& f) {  // this thread's logits as keys
+            for (int v = v0 + tid; v < v1; v += NT) {
+                float g[VEC<T>];
+                unpack(__ldg(zv + v), g);
+#pragma unroll
+                for (int j = 0; j < VEC<T>; j++)
+                    if (v * VEC<T> + j < V) f(order_key(g[j], v * VEC<T> + j));
+            }
+        };
+        if (any && (key >> 32) >= (least >> 32))  // equal logits too: the order goes by columns
+            each([&](uint64_t q) {
+                if ((q >> 32) >= (least >> 32)) {
+                    const int at = atomicAdd(&count, 1);
+                    if (at < CAND) keys[at] = q;
+                }
+            });
+        __syncthreads();
+        uint64_t* list = keys;
+        if (split > 1) list = cg::this_cluster().map_shared_rank(lists, 0) + rank * MAX_K;
+        const int n = count;
+        if (n <= CAND) {
+            for (int c = tid; c < MAX_K; c += NT)
+                if (split > 1 && c >= n) list[c] = 0;  // a part with fewer than k columns
+            uint64_t q[2];
+            int r[2];
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int c = tid + h * NT;
+                q[h] = c < n ? keys[c] : 0;
+                r[h] = MAX_K;
+                if (c < n) {
+                    r[h] = 0;
+                    for (int j = 0; j < n; j++) r[h] += keys[j] > q[h];
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+                if (r[h] < k) list[r[h]] = q[h];
+        } else {
+            // one by one: the largest of the threads' largest, whose thread then looks for its next
+            uint64_t best = 0;
+            each([&](uint64_t q) { best = q > best ? q : best; });
+            uint64_t found[(MAX_K + NT - 1) / NT] = {0};
+            for (int r = 0; r < k; r++) {
+                __syncthreads();
+                keys[tid] = best;
+                __syncthreads();
+                uint64_t top = 0;
+                for (int j = lane; j < NT; j += 32) top = keys[j] > top ? keys[j] : top;
+#pragma unroll
+                for (int o = 16; o > 0; o /= 2) {
+                    const uint64_t y = __shfl_xor_sync(0xffffffffu, top, o);
+                    top = y > top ? y : top;
+                }
+                if (tid == r) found[0] = top;
+                if (best == top && top) {
+                    best = 0;
+                    each([&](uint64_t q) { best = q < top && q > best ? q : best; });
+                }
+            }
+            __syncthreads();
+            if (tid < MAX_K && (tid < k || split > 1)) list[tid] = tid < k ? found[0] : 0;
+        }
+    }
+    __syncthreads();
+    x = ws[0];
+#pragma unroll
+    for (int w = 1; w < NT / 32; w++) x = join(x, ws[w]);
+    if (split > 1) {
+        if (tid == 0) *cg::this_cluster().map_shared_rank(&cs[rank], 0) = x;
+        cg::this_cluster().sync();
+        if (rank) return;
+        x = cs[0];
+        for (int r = 1; r < split; r++) x = join(x, cs[r]);
+    }
+    const bool none = x.m == -INFINITY;
+    const float L = isinf(x.m) ? x.m : x.m + LN2 * log2f(x.s);
     if (tid == 0) {
         lse[row] = L;
-        if (entropy) entropy[row] = none ? 0.f : logf(s) - t / s;
-        if (logp) {
-            int tgt = targets[row];
-            if (tgt < 0 || tgt >= V) {
-                set_status(status, GPT2_FLAG_TARGET_RANGE);
-                tgt = 0;
-            }
-            logp[row] = none ? -INFINITY : to_float(z[tgt]) - L;
-        }
+        if (entropy) entropy[row] = none ? 0.f : LN2 * (log2f(x.s) - x.t / x.s);
+        if (logp) logp[row] = none ? -INFINITY : zt - L;
     }
-    uint64_t last = ~0ull;
-    for (int r = 0; r < k; r++) {
-        uint64_t b = 0;
-        for (int j = tid; j < V; j += LP_NT) {
-            const uint64_t x = order_key(to_float(z[j]), j);
-            if (x < last && x > b) b = x;
-        }
-        best[tid] = b;
-        __syncthreads();
-        for (int w = LP_NT / 2; w > 0; w /= 2) {
-            if (tid < w && best[tid + w] > best[tid]) best[tid] = best[tid + w];
-            __syncthreads();
-        }
-        last = best[0];
-        const int col = (int)~(uint32_t)last;
-        if (tid == 0) {
-            top_ids[(int64_t)row * k + r] = col;
-            top_logp[(int64_t)row * k + r] = none ? -INFINITY : to_float(z[col]) - L;
+    if (!k) return;
+    if (split > 1) {  // the k largest of the parts' lists
+        for (int c = tid; c < split * MAX_K; c += NT) {
+            const uint64_t q = lists[c];
+            if (!q || (c % MAX_K) >= k) continue;
+            int r = c % MAX_K;  // its own list is sorted
+            for (int s = 0; s < split; s++)
+                if (s != c / MAX_K)
+                    for (int j = 0; j < k && lists[s * MAX_K + j] > q; j++) r++;
+            if (r < k) keys[r] = q;
         }
         __syncthreads();
+    }
+    if (tid < k) {
+        const uint64_t q = keys[tid];
+        top_ids[(int64_t)row * k + tid] = key_col(q);
+        top_logp[(int64_t)row * k + tid] = none ? -INFINITY : key_logit(q) - L;
     }
 }
 
+// Row blockIdx.x, vectors part blockIdx.y of gridDim.y.
 template <typename T>
-__global__ void __launch_bounds__(LP_NT)
-    logprobs_bwd_kernel(T* dlogits, const T* logits, const int32_t* targets, const float* lse, const float* entropy,
-                        const float* dlogp, const float* dlse, const float* dentropy, int V, int Vp, int* status) {
+__global__ void __launch_bounds__(NT)
+    logprobs_bwd_kernel(T* dlogits, const T* logits, const int32_t* __restrict__ targets,
+                        const float* __restrict__ lse, const float* __restrict__ entropy,
+                        const float* __restrict__ dlogp, const float* __restrict__ dlse,
+                        const float* __restrict__ dentropy, int V, int Vp, int* status) {
     const int row = blockIdx.x;
-    const T* z = logits + (int64_t)row * Vp;
-    T* dz = dlogits + (int64_t)row * Vp;
+    const uint4* zv = reinterpret_cast<const uint4*>(logits + (int64_t)row * Vp);
+    uint4* dv = reinterpret_cast<uint4*>(dlogits + (int64_t)row * Vp);
+    int v0, v1;
+    part(Vp / VEC<T>, gridDim.y, blockIdx.y, v0, v1);
     const float L = lse[row], H = dentropy ? entropy[row] : 0.f;
-    const float g = dlogp ? dlogp[row] : 0.f, a = dlse ? dlse[row] : 0.f, b = dentropy ? dentropy[row] : 0.f;
+    const float g = dlogp ? dlogp[row] : 0.f, b = dentropy ? dentropy[row] : 0.f;
+    const float c = (dlse ? dlse[row] : 0.f) - g - b * H;  // dz = p (c - b log p) + g [target]
     int tgt = -1;
     if (dlogp) {
         tgt = targets[row];
         if (tgt < 0 || tgt >= V) {
-            if (threadIdx.x == 0) set_status(status, GPT2_FLAG_TARGET_RANGE);
+            if (threadIdx.x == 0 && blockIdx.y == 0) set_status(status, GPT2_FLAG_TARGET_RANGE);
             tgt = 0;
         }
     }
-    for (int j = threadIdx.x; j < Vp; j += LP_NT) {
-        float d = 0.f;
-        if (j < V && L != -INFINITY) {
-            const float lp = to_float(z[j]) - L, p = expf(lp);
-            if (!(p == 0.f)) d = p * (a - g - b * (lp + H));
-            if (j == tgt) d += g;
+    const bool none = L == -INFINITY;
+    const int tvec = tgt < 0 ? -1 : tgt / VEC<T>;
+    for (int i = v0 + (int)threadIdx.x; i < v1; i += BATCH * NT) {
+        uint4 u[BATCH];
+#pragma unroll
+        for (int e = 0; e < BATCH; e++)
+            if (i + e * NT < v1) u[e] = __ldcs(zv + i + e * NT);
+#pragma unroll
+        for (int e = 0; e < BATCH; e++) {
+            const int v = i + e * NT;
+            if (v >= v1) break;
+            float f[VEC<T>];
+            unpack(u[e], f);
+#pragma unroll
+            for (int j = 0; j < VEC<T>; j++) {
+                const float lp = f[j] - L, p = ex2_approx(lp * LOG2E);
+                f[j] = p * (c - b * fmaxf(lp, -1e4f));  // p is 0 long before the bound
+            }
+            if (v == tvec) {
+#pragma unroll
+                for (int j = 0; j < VEC<T>; j++)
+                    if (v * VEC<T> + j == tgt) f[j] += g;
+            }
+            if (none || v * VEC<T> + VEC<T> > V) {
+#pragma unroll
+                for (int j = 0; j < VEC<T>; j++)
+                    if (none || v * VEC<T> + j >= V) f[j] = 0.f;
+            }
+            uint4 w;
+            pack(w, f);
+            __stcs(dv + v, w);
         }
-        dz[j] = from_float<T>(d);
     }
+}
+
+template <typename T>
+int forward(float* logp, float* lse, float* entropy, float* top_logp, int32_t* top_ids, int k, const T* logits,
+            const int32_t* targets, int N, int V, int Vp, int* status, cudaStream_t s) {
+    // as many blocks to a row as leave each SM one, and each block a batch of vectors
+    int split = 1;
+    while (split < MAX_SPLIT && (int64_t)N * split * 2 <= gpt2_num_sms() && V / VEC<T> >= split * 2 * NT) split *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(N * split));
+    cfg.blockDim = dim3(NT);
+    cfg.stream = s;
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = split;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = split > 1 ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, logprobs_kernel<T>, logp, lse, entropy, top_logp, top_ids, k, logits, targets, V, Vp,
+                           split, status) != cudaSuccess)
+        return GPT2_ERR_CUDA;
+    return 1;
+}
+
+template <typename T>
+int backward(T* dlogits, const T* logits, const int32_t* targets, const float* lse, const float* entropy,
+             const float* dlogp, const float* dlse, const float* dentropy, int N, int V, int Vp, int* status,
+             cudaStream_t s) {
+    int split = 1;
+    while ((int64_t)N * split < 4 * gpt2_num_sms() && Vp / VEC<T> > split * BATCH * NT) split *= 2;
+    logprobs_bwd_kernel<T><<<dim3(N, split), NT, 0, s>>>(dlogits, logits, targets, lse, entropy, dlogp, dlse, dentropy,
+                                                         V, Vp, status);
+    return 1;
 }
 
 }  // namespace
@@ -127,22 +415,16 @@ int launch_token_logprobs(int dtype, float* logp, float* lse, float* entropy, fl
                           int k, const void* logits, const int32_t* targets, int N, int V, int Vp, int* status,
                           cudaStream_t s) {
     if (dtype == GPT2_MODE_BF16)
-        logprobs_kernel<bf16><<<N, LP_NT, 0, s>>>(logp, lse, entropy, top_logp, top_ids, k, (const bf16*)logits,
-                                                  targets, N, V, Vp, status);
-    else
-        logprobs_kernel<float><<<N, LP_NT, 0, s>>>(logp, lse, entropy, top_logp, top_ids, k, (const float*)logits,
-                                                   targets, N, V, Vp, status);
-    return 1;
+        return forward(logp, lse, entropy, top_logp, top_ids, k, (const bf16*)logits, targets, N, V, Vp, status, s);
+    return forward(logp, lse, entropy, top_logp, top_ids, k, (const float*)logits, targets, N, V, Vp, status, s);
 }
 
 int launch_token_logprobs_backward(int dtype, void* dlogits, const void* logits, const int32_t* targets,
                                    const float* lse, const float* entropy, const float* dlogp, const float* dlse,
                                    const float* dentropy, int N, int V, int Vp, int* status, cudaStream_t s) {
     if (dtype == GPT2_MODE_BF16)
-        logprobs_bwd_kernel<bf16><<<N, LP_NT, 0, s>>>((bf16*)dlogits, (const bf16*)logits, targets, lse, entropy,
-                                                      dlogp, dlse, dentropy, V, Vp, status);
-    else
-        logprobs_bwd_kernel<float><<<N, LP_NT, 0, s>>>((float*)dlogits, (const float*)logits, targets, lse, entropy,
-                                                       dlogp, dlse, dentropy, V, Vp, status);
-    return 1;
+        return backward((bf16*)dlogits, (const bf16*)logits, targets, lse, entropy, dlogp, dlse, dentropy, N, V, Vp,
+                        status, s);
+    return backward((float*)dlogits, (const float*)logits, targets, lse, entropy, dlogp, dlse, dentropy, N, V, Vp,
+                    status, s);
 }
