@@ -95,36 +95,56 @@ __device__ __forceinline__ void move_to(Stats& x, float m) {
     x.s *= f;
     x.m = m;
 }
-__device__ __forceinline__ Stats join(Stats a, Stats b) {
-    const float m = max_nan(a.m, b.m);
-    move_to(a, m);
-    move_to(b, m);
-    a.s += b.s;
-    a.t += b.t;
-    return a;
+// The same for all of LANES neighbouring lanes: the maximum first, then each
+// lane's sums moved to it once and added (x + y and y + x: the same bits in
+// every lane).
+template <int LANES> __device__ __forceinline__ Stats join(Stats x) {
+    float m = x.m;
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o /= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    move_to(x, m);
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o /= 2) {
+        x.s += __shfl_xor_sync(0xffffffffu, x.s, o);
+        x.t += __shfl_xor_sync(0xffffffffu, x.t, o);
+    }
+    return x;
 }
 
-// One vector's values (columns col .. col + VEC - 1, those at or past V left
-// out) into x; `bm` their maximum.
-template <typename T> __device__ __forceinline__ void add_vec(const float (&f)[VEC<T>], Stats& x) {
-    const float m = reference(x.m);
-    const uint64_t m2 = f2_pack(m, m), l2e = f2_pack(LOG2E, LOG2E);
-    uint64_t s2 = 0, t2 = 0;
+// N values into x, whose maximum is already at least theirs, 2^d taken
+//   fast: with d = z log2(e) - m log2(e) in one step. The rounding of m log2(e)
+//     shifts every d alike (lse by |m| 2^-24) while |m| is moderate, and e d is
+//     a NaN where z is -inf, which the caller sees in x.t;
+//   else: from the difference z - m, exact for the largest, and with d bounded
+//     (e is 0 below -150, and 0 * -inf must not count): for masks from -1e38 to
+//     -inf and far-off rows.
+template <bool FAST, int N> __device__ __forceinline__ void add_values(const float (&f)[N], Stats& x) {
+    const float m = reference(x.m), ml = -m * LOG2E;
+    const uint64_t m2 = FAST ? f2_pack(ml, ml) : f2_pack(m, m), l2e = f2_pack(LOG2E, LOG2E);
+    uint64_t s2[2] = {0, 0}, t2[2] = {0, 0};
 #pragma unroll
-    for (int j = 0; j < VEC<T>; j += 2) {
+    for (int j = 0; j < N; j += 2) {
+        const uint64_t z2 = f2_pack(f[j], f[j + 1]);
+        uint64_t d2 = FAST ? f2_fma(z2, l2e, m2) : f2_mul(f2_sub(z2, m2), l2e);
         float d0, d1;
-        // the difference first: z log2(e) - m log2(e) is off by |m| 2^-24, and masks go down to -1e38
-        f2_unpack(f2_mul(f2_sub(f2_pack(f[j], f[j + 1]), m2), l2e), d0, d1);
+        f2_unpack(d2, d0, d1);
         const uint64_t e2 = f2_pack(ex2_approx(d0), ex2_approx(d1));
-        s2 = f2_add(s2, e2);
-        // below 2^-150 e is 0, and 0 * -inf must not count
-        t2 = f2_fma(e2, f2_pack(fmaxf(d0, -200.f), fmaxf(d1, -200.f)), t2);
+        if (!FAST) d2 = f2_pack(fmaxf(d0, -200.f), fmaxf(d1, -200.f));
+        s2[(j >> 1) & 1] = f2_add(s2[(j >> 1) & 1], e2);
+        t2[(j >> 1) & 1] = f2_fma(e2, d2, t2[(j >> 1) & 1]);
     }
     float a, b;
-    f2_unpack(s2, a, b);
+    f2_unpack(f2_add(s2[0], s2[1]), a, b);
     x.s += a + b;
-    f2_unpack(t2, a, b);
+    f2_unpack(f2_add(t2[0], t2[1]), a, b);
     x.t += a + b;
+}
+template <int N> __device__ __forceinline__ void raise(const float (&f)[N], Stats& x) {
+    float m[2] = {x.m, -INFINITY};
+#pragma unroll
+    for (int j = 0; j < N; j += 2) m[(j >> 1) & 1] = max_nan(m[(j >> 1) & 1], f[j], f[j + 1]);
+    const float top = max_nan(m[0], m[1]);
+    if (!(top <= x.m)) move_to(x, top);
 }
 
 // The split-th part of a row's vectors: [first, last).
@@ -136,19 +156,22 @@ __device__ __forceinline__ void part(int nv, int split, int rank, int& first, in
 
 // A row is read by `split` blocks (a cluster), 256 threads each, thread t
 // taking every 256th vector of the block's part. Top k: each thread knows its
-// largest logit; the k-th largest of those 256 bounds the block's k-th largest
-// from below, so the few threads above it look through their own vectors again
-// (from L2) and keep what reaches the bound: about k candidates, ranked by
-// counting. More than CAND (many equal logits) are found one by one. The
-// blocks' lists and sums meet in the first block's shared memory.
+// largest logit, which gives a lower bound of the block's k-th largest; the few
+// threads that reach it have their vectors looked through again (from L2) for
+// what reaches the bound: some more than k candidates, ranked by counting. More
+// than CAND (many equal logits) are found one by one. The blocks' lists and
+// sums meet in the first block's shared memory.
 template <typename T>
 __global__ void __launch_bounds__(NT)
     logprobs_kernel(float* __restrict__ logp, float* __restrict__ lse, float* __restrict__ entropy,
                     float* __restrict__ top_logp, int32_t* __restrict__ top_ids, int k, const T* __restrict__ logits,
                     const int32_t* __restrict__ targets, int V, int Vp, int split, int* status) {
     __shared__ Stats ws[NT / 32], cs[MAX_SPLIT];
-    __shared__ uint64_t keys[CAND], lists[MAX_SPLIT * MAX_K], bound;
+    __shared__ uint64_t keys[CAND], lists[MAX_SPLIT * MAX_K];
+    __shared__ __align__(16) uint32_t maxima[NT];
+    __shared__ uint32_t bound;
     __shared__ int count;
+    __shared__ float whole;  // the row's lse
     const int row = blockIdx.x / split, rank = blockIdx.x - row * split;
     const int tid = threadIdx.x, lane = tid & 31;
     const T* z = logits + (int64_t)row * Vp;
@@ -169,7 +192,29 @@ __global__ void __launch_bounds__(NT)
     }
 
     Stats x = {-INFINITY, 0.f, 0.f};
-    for (int i = v0 + tid; i < v1; i += BATCH * NT) {
+    int i = v0 + tid;
+    for (const int whole = min(v1, V / VEC<T>); i + (BATCH - 1) * NT < whole; i += BATCH * NT) {
+        uint4 u[BATCH];
+#pragma unroll
+        for (int b = 0; b < BATCH; b++) u[b] = __ldg(zv + i + b * NT);
+        float f[BATCH * VEC<T>];
+#pragma unroll
+        for (int b = 0; b < BATCH; b++) {
+            float g[VEC<T>];
+            unpack(u[b], g);
+#pragma unroll
+            for (int j = 0; j < VEC<T>; j++) f[b * VEC<T> + j] = g[j];
+        }
+        raise(f, x);
+        const Stats was = x;
+        const bool near = fabsf(x.m) < 1e4f;
+        if (near) add_values<true>(f, x);
+        if (!near || x.t != x.t) {
+            x = was;
+            add_values<false>(f, x);
+        }
+    }
+    {  // the rest, BATCH vectors at most, with the one that V cuts
         uint4 u[BATCH];
 #pragma unroll
         for (int b = 0; b < BATCH; b++)
@@ -180,41 +225,65 @@ __global__ void __launch_bounds__(NT)
             if (v >= v1) break;
             float f[VEC<T>];
             unpack(u[b], f);
-            if (v * VEC<T> + VEC<T> > V) {  // the vector that V cuts
 #pragma unroll
-                for (int j = 0; j < VEC<T>; j++)
-                    if (v * VEC<T> + j >= V) f[j] = -INFINITY;
-            }
-            float m = x.m;
-#pragma unroll
-            for (int j = 0; j < VEC<T>; j += 2) m = max_nan(m, f[j], f[j + 1]);
-            if (m != x.m) move_to(x, m);
-            add_vec<T>(f, x);
+            for (int j = 0; j < VEC<T>; j++)
+                if (v * VEC<T> + j >= V) f[j] = -INFINITY;
+            raise(f, x);
+            add_values<false>(f, x);
         }
     }
     const float mine = x.m;  // this thread's largest logit
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2) {
-        const Stats y = {__shfl_xor_sync(0xffffffffu, x.m, o), __shfl_xor_sync(0xffffffffu, x.s, o),
-                         __shfl_xor_sync(0xffffffffu, x.t, o)};
-        x = (lane & o) ? join(y, x) : join(x, y);  // the same order in both lanes
-    }
+    x = join<32>(x);
     if (lane == 0) ws[tid >> 5] = x;
     if (split > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    static_assert(NT / 32 == 8 && MAX_SPLIT == 8, "eight lanes join the warps, and the blocks");
+    const Stats empty = {-INFINITY, 0.f, 0.f};
+    auto finish = [&](const Stats& r) {  // by the first warp
+        if (lane) return;
+        const float L = isinf(r.m) ? r.m : r.m + LN2 * log2f(r.s);
+        lse[row] = L;
+        if (entropy) entropy[row] = r.m == -INFINITY ? 0.f : LN2 * (log2f(r.s) - r.t / r.s);
+        if (logp) logp[row] = r.m == -INFINITY ? -INFINITY : zt - L;
+        whole = L;
+    };
+    auto meet = [&] {  // the warps' sums, by the first warp
+        if (tid >= 32) return;
+        x = join<8>(lane < 8 ? ws[lane] : empty);
+        if (split == 1) finish(x);
+        else if (lane == 0) *cg::this_cluster().map_shared_rank(&cs[rank], 0) = x;
+    };
+    if (!k) {
+        __syncthreads();
+        meet();
+    }
 
     if (k) {
+        // The k-th largest of the maxima of 64 groups of four threads (of the threads for k above 32) bounds the
+        // k-th largest logit from below. -inf and no data come out as the lowest.
         const bool any = v0 + tid < v1;
-        // the k-th largest thread maximum (keys unique by thread); 0 with fewer threads than k
-        const uint64_t key = any ? order_key(mine, tid) : 0;
-        keys[tid] = key;
-        if (tid == 0) bound = 0, count = 0;
+        const uint32_t key = any ? (uint32_t)(order_key(mine, 0) >> 32) : 0;
+        const int groups = k > 32 ? NT : NT / 4;
+        uint32_t most = key;
+        if (k <= 32) {
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        }
+        if (k > 32) maxima[tid] = most;
+        else if (lane % 4 == 0) maxima[tid / 4] = most;
+        if (tid == 0) bound = ~0u, count = 0;
         __syncthreads();
-        int above = 0;
-        for (int j = 0; j < NT; j++) above += keys[j] > key;
-        if (any && above == k - 1) bound = key;
+        meet();
+        if (NT - 1 - tid < groups) {  // (the last warps: the first is busy)
+            const uint32_t own = maxima[NT - 1 - tid];
+            int above = 0;
+            for (int j = 0; j < groups; j += 4) {
+                const uint4 o = *reinterpret_cast<const uint4*>(maxima + j);
+                above += (o.x > own) + (o.y > own) + (o.z > own) + (o.w > own);
+            }
+            if (above < k) atomicMin(&bound, own);
+        }
         __syncthreads();
-        const uint64_t least = bound;
-        __syncthreads();  // keys[] is reused for the candidates
+        const uint32_t least = bound;
         auto each = [&](auto&& f) {  // this thread's logits as keys
             for (int v = v0 + tid; v < v1; v += NT) {
                 float g[VEC<T>];
@@ -224,13 +293,38 @@ __global__ void __launch_bounds__(NT)
                     if (v * VEC<T> + j < V) f(order_key(g[j], v * VEC<T> + j));
             }
         };
-        if (any && (key >> 32) >= (least >> 32))  // equal logits too: the order goes by columns
-            each([&](uint64_t q) {
-                if ((q >> 32) >= (least >> 32)) {
-                    const int at = atomicAdd(&count, 1);
-                    if (at < CAND) keys[at] = q;
+        // the vectors of each thread whose maximum reaches the bound, by its whole warp, one to a lane, four
+        // threads' at a time
+        constexpr int HOT = 4;
+        for (uint32_t hot = __ballot_sync(0xffffffffu, any && key >= least); hot;) {
+            int v[HOT];
+#pragma unroll
+            for (int h = 0; h < HOT; h++) {
+                v[h] = hot ? v0 + (tid & ~31) + __ffs(hot) - 1 + lane * NT : v1;
+                hot &= hot - 1;
+            }
+            while (__any_sync(0xffffffffu, min(min(v[0], v[1]), min(v[2], v[3])) < v1)) {
+                uint4 u[HOT];
+#pragma unroll
+                for (int h = 0; h < HOT; h++)
+                    if (v[h] < v1) u[h] = __ldg(zv + v[h]);
+#pragma unroll
+                for (int h = 0; h < HOT; h++) {
+                    if (v[h] >= v1) continue;
+                    float g[VEC<T>];
+                    unpack(u[h], g);
+#pragma unroll
+                    for (int j = 0; j < VEC<T>; j++) {
+                        const uint64_t q = order_key(g[j], v[h] * VEC<T> + j);
+                        if ((uint32_t)(q >> 32) >= least && v[h] * VEC<T> + j < V) {
+                            const int at = atomicAdd(&count, 1);
+                            if (at < CAND) keys[at] = q;
+                        }
+                    }
+                    v[h] += 32 * NT;
                 }
-            });
+            }
+        }
         __syncthreads();
         uint64_t* list = keys;
         if (split > 1) list = cg::this_cluster().map_shared_rank(lists, 0) + rank * MAX_K;
@@ -280,23 +374,10 @@ __global__ void __launch_bounds__(NT)
             if (tid < MAX_K && (tid < k || split > 1)) list[tid] = tid < k ? found[0] : 0;
         }
     }
-    __syncthreads();
-    x = ws[0];
-#pragma unroll
-    for (int w = 1; w < NT / 32; w++) x = join(x, ws[w]);
     if (split > 1) {
-        if (tid == 0) *cg::this_cluster().map_shared_rank(&cs[rank], 0) = x;
         cg::this_cluster().sync();
         if (rank) return;
-        x = cs[0];
-        for (int r = 1; r < split; r++) x = join(x, cs[r]);
-    }
-    const bool none = x.m == -INFINITY;
-    const float L = isinf(x.m) ? x.m : x.m + LN2 * log2f(x.s);
-    if (tid == 0) {
-        lse[row] = L;
-        if (entropy) entropy[row] = none ? 0.f : LN2 * (log2f(x.s) - x.t / x.s);
-        if (logp) logp[row] = none ? -INFINITY : zt - L;
+        if (tid < 32) finish(join<8>(lane < split ? cs[lane] : empty));
     }
     if (!k) return;
     if (split > 1) {  // the k largest of the parts' lists
@@ -309,12 +390,13 @@ __global__ void __launch_bounds__(NT)
                     for (int j = 0; j < k && lists[s * MAX_K + j] > q; j++) r++;
             if (r < k) keys[r] = q;
         }
-        __syncthreads();
     }
+    __syncthreads();
     if (tid < k) {
+        const float L = whole;
         const uint64_t q = keys[tid];
         top_ids[(int64_t)row * k + tid] = key_col(q);
-        top_logp[(int64_t)row * k + tid] = none ? -INFINITY : key_logit(q) - L;
+        top_logp[(int64_t)row * k + tid] = L == -INFINITY ? -INFINITY : key_logit(q) - L;
     }
 }
 
