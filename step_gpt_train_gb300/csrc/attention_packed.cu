@@ -156,7 +156,14 @@ __global__ void __launch_bounds__(128) packed_dkdv_kernel(PackedAttn a, PackedAt
 // short item of each other at the end: dealt round robin in sequence order
 // they were busy two thirds of the time on 16 ragged prompts.
 constexpr int PLAN_SEQ = 2048;  // sequences whose offsets are searched in shared memory
-__global__ void __launch_bounds__(1024) packed_plan_kernel(PackedAttn a, PackedPlan* plan, int per, int slots) {
+struct PlanArgs {
+    PackedCut cut[2];
+    PackedPlan* plan[2];
+};
+__global__ void __launch_bounds__(1024) packed_plan_kernel(PackedAttn a, PlanArgs args) {
+    const PackedCut cut = args.cut[blockIdx.x];
+    PackedPlan* plan = args.plan[blockIdx.x];
+    const int slots = cut.slots(a), per = cut.per, total = cut.total(a);
     constexpr int BUCKETS = 1024;
     __shared__ int count[BUCKETS], warps[32], first[PLAN_SEQ], keys[PLAN_SEQ + 1], rows[PLAN_SEQ + 1];
     const int tid = threadIdx.x, lane = tid & 31;
@@ -165,28 +172,28 @@ __global__ void __launch_bounds__(1024) packed_plan_kernel(PackedAttn a, PackedP
         for (int s = tid; s <= a.n_seq; s += 1024) {
             rows[s] = a.cu_q[s];
             keys[s] = a.cu_k[s];
-            if (s < a.n_seq) first[s] = min(max(rows[s], 0), a.total_q) / per + s;
+            if (s < a.n_seq) first[s] = min(max((cut.keys ? keys : rows)[s], 0), total) / per + s;
         }
     count[tid] = 0;
     __syncthreads();
     PackedAttn c = a;
     if (near) c.cu_q = rows, c.cu_k = keys;
-    packed_check(c, tid, 1024);
+    if (blockIdx.x == 0) packed_check(c, tid, 1024);
     // the tile of a slot, its bucket, or -1
     auto look = [&](int slot, PackedTile& t) -> int {
         int lo = -1, hi = a.n_seq, f = 0;  // the last sequence whose first slot is at or before this one
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            const int x = near ? first[mid] : min(max(a.cu_q[mid], 0), a.total_q) / per + mid;
+            const int x = near ? first[mid] : min(max(cut.cu(a)[mid], 0), total) / per + mid;
             if (x <= slot) lo = mid, f = x;
             else hi = mid;
         }
         if (lo < 0) return -1;
         const PackedSeq p = packed_seq(c, lo);
         const int at = (slot - f) * per;
-        if (at < 0 || at >= p.lq) return -1;
-        t = packed_tile(p, at, per);
-        return BUCKETS - 1 - min(packed_blocks(t, t.nq), BUCKETS - 1);
+        if (at < 0 || at >= cut.rows(p)) return -1;
+        t = cut.tile(p, at);
+        return BUCKETS - 1 - min(cut.blocks(t, t.n), BUCKETS - 1);
     };
     PackedTile t0;
     const int b0 = tid < slots ? look(tid, t0) : -1;
@@ -246,8 +253,13 @@ template <typename T, int HD> int backward(const PackedAttn& a, const PackedAttn
 
 }  // namespace
 
-int launch_packed_plan(const PackedAttn& a, PackedPlan* plan, int per, cudaStream_t s) {
-    packed_plan_kernel<<<1, 1024, 0, s>>>(a, plan, per, packed_slots(a.total_q, a.n_seq, per));
+int launch_packed_plans(const PackedAttn& a, const PackedCut* cuts, PackedPlan* const* plans, int n, cudaStream_t s) {
+    PlanArgs args;
+    for (int i = 0; i < 2; i++) {
+        args.cut[i] = cuts[i < n ? i : 0];
+        args.plan[i] = plans[i < n ? i : 0];
+    }
+    packed_plan_kernel<<<n, 1024, 0, s>>>(a, args);
     return 1;
 }
 
@@ -268,6 +280,8 @@ int launch_attention_packed_forward(int dtype, const PackedAttn& a, void* scratc
 }
 
 size_t attention_packed_backward_scratch(int dtype, int n_seq, int total_q, int total_k, int Hq, int Hkv, int hd) {
+    if (dtype == GPT2_MODE_BF16 && Hq / Hkv <= 64)
+        return attention_packed_backward_tc_scratch(n_seq, total_q, total_k, Hq, Hkv);
     return (size_t)Hq * total_q * 4;
 }
 
@@ -275,7 +289,11 @@ int launch_attention_packed_backward(int dtype, const PackedAttn& a, const Packe
                                      cudaStream_t s) {
     PackedAttnGrad g = grad;
     g.D = (float*)scratch;
-    if (dtype == GPT2_MODE_BF16) return backward<bf16, 64>(a, g, s);
+    if (dtype == GPT2_MODE_BF16) {
+        // the tensor-core kernels lay a key head's whole group into 64 rows
+        if (a.Hq / a.Hkv <= 64) return launch_attention_packed_backward_tc(a, g, scratch, s);
+        return backward<bf16, 64>(a, g, s);
+    }
     switch (a.hd) {
         case 8: return backward<float, 8>(a, g, s);
         case 16: return backward<float, 16>(a, g, s);

@@ -46,12 +46,16 @@ __device__ __forceinline__ int packed_find_row(const int32_t* cu, int n_seq, int
     return lo;
 }
 
-// A work item of the query-tile kernels: `per` consecutive queries of one
-// sequence (less at its end).
+// A work item: up to `per` consecutive rows of one sequence, and the rows of
+// the other kind that meet them.
+//   queries: rows r0 .. r0 + n - 1, keys s0 .. s0 + len - 1 of the sequence;
+//     shift = the keys that the first query sees (may be negative);
+//   keys: rows r0 .. of keys, queries s0 ..; the first key is seen by the
+//     sequence's queries from shift on (may be negative).
 struct PackedTile {
-    int q0, nq;   // first row in the buffer, queries
-    int k0, lk;   // the sequence's keys
-    int vis;      // keys that the first query sees (may be negative)
+    int r0, n;
+    int s0, len;
+    int shift;
     int pad[3];
 };
 // The items of a call, the longest first, with a counter from which the CTAs
@@ -64,13 +68,28 @@ inline size_t packed_plan_bytes(int slots) { return 32 + (size_t)slots * sizeof(
 // Slots (at least as many as tiles) of `per` rows: see find_slot.
 inline int packed_slots(int total, int n_seq, int per) { return total / per + n_seq; }
 constexpr int PACKED_PLAN_MAX = 8192;  // slots that one block sorts in about the time of a launch
-int launch_packed_plan(const PackedAttn& a, PackedPlan* plan, int per, cudaStream_t s);
 
-__device__ __forceinline__ PackedTile packed_tile(const PackedSeq& p, int at, int per) {
-    PackedTile t = {p.q0 + at, min(per, p.lq - at), p.k0, p.lk, at + 1 + p.lk - p.lq, {0, 0, 0}};
-    return t;
-}
-// Key blocks of 128 that the first n queries of a tile see.
-__device__ __forceinline__ int packed_blocks(const PackedTile& t, int n) {
-    return n > 0 ? (max(0, t.vis + n - 1) + 127) / 128 : 0;
-}
+// How a kernel cuts its sequences: tiles of `per` queries (or keys), against
+// blocks of `block` keys (or queries).
+struct PackedCut {
+    bool keys;  // the tiles are of keys
+    int per, block;
+    __host__ __device__ int slots(const PackedAttn& a) const { return (keys ? a.total_k : a.total_q) / per + a.n_seq; }
+    __device__ __forceinline__ const int32_t* cu(const PackedAttn& a) const { return keys ? a.cu_k : a.cu_q; }
+    __device__ __forceinline__ int total(const PackedAttn& a) const { return keys ? a.total_k : a.total_q; }
+    __device__ __forceinline__ int rows(const PackedSeq& p) const { return keys ? p.lk : p.lq; }
+    __device__ __forceinline__ PackedTile tile(const PackedSeq& p, int at) const {
+        if (keys) return PackedTile{p.k0 + at, min(per, p.lk - at), p.q0, p.lq, at - (p.lk - p.lq), {0, 0, 0}};
+        return PackedTile{p.q0 + at, min(per, p.lq - at), p.k0, p.lk, at + 1 + p.lk - p.lq, {0, 0, 0}};
+    }
+    // Keys: the first of the queries that the blocks cover (a block starts at a multiple of its size).
+    __device__ __forceinline__ int first(const PackedTile& t) const { return keys ? max(0, t.shift) / block * block : 0; }
+    // Blocks that the tile's first n rows meet.
+    __device__ __forceinline__ int blocks(const PackedTile& t, int n) const {
+        if (n <= 0) return 0;
+        if (keys) return t.shift < t.len ? (t.len - first(t) + block - 1) / block : 0;
+        return (max(0, t.shift + n - 1) + block - 1) / block;
+    }
+};
+// Sorts the tiles of n (1 or 2) cuts into their plans in one launch.
+int launch_packed_plans(const PackedAttn& a, const PackedCut* cuts, PackedPlan* const* plans, int n, cudaStream_t s);

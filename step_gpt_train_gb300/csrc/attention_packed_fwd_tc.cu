@@ -64,6 +64,7 @@ struct Args {
     int group, qt;        // query heads per key head, queries per tile (128 / group)
     int items;
     float scale_log2;     // log2(e) / sqrt(hd)
+    PackedCut cut;        // pairs of tiles, key blocks of 128
     PackedPlan* plan;     // sorted items, or null: found from the offsets
 };
 
@@ -277,47 +278,20 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_drain(drain + 8 * t, 0, status);
     } else if (warp == 3) {
         // ------------------------------------------------------ work items, tails of V
-        const int per = 2 * A.qt;
-        const int slots = A.items / a.Hkv;
         int x = blockIdx.x, blocks = 0;
         if (blockIdx.x == 0 && !A.plan) packed_check(a, lane, 32);
-        auto next_tile = [&](PackedTile& p, int& kh) -> bool {
-            if (A.plan) {
-                int n = 0;
-                if (lane == 0) n = atomicAdd(&A.plan->next, 1);
-                n = __shfl_sync(0xffffffffu, n, 0);
-                if (n >= A.plan->count * a.Hkv) return false;
-                p = A.plan->tile[n / a.Hkv];
-                kh = n % a.Hkv;
-                return true;
-            }
-            for (; x < A.items; x += gridDim.x) {
-                int f;
-                const int slot = slots - 1 - x / a.Hkv;  // the later tiles of a sequence, which see more keys, first
-                const int s = find_slot(a.cu_q, a.n_seq, a.total_q, per, slot, f);
-                if (s < 0) continue;
-                const PackedSeq q = packed_seq(a, s);
-                const int at = (slot - f) * per;
-                if (at < 0 || at >= q.lq) continue;
-                p = packed_tile(q, at, per);
-                kh = x % a.Hkv;
-                x += gridDim.x;
-                return true;
-            }
-            return false;
-        };
         auto put = [&](int i, Item& it) -> bool {  // the next item, or the end, into ring slot i
             PackedTile p;
-            it.valid = next_tile(p, it.kh);
+            it.valid = next_tile(a, A.cut, A.plan, A.items, x, p, it.kh);
             if (it.valid) {
-                it.q0 = p.q0;
-                it.nq0 = min(A.qt, p.nq);
-                it.nq1 = p.nq - it.nq0;
-                it.k0 = p.k0;
-                it.lk = p.lk;
-                it.vis = p.vis;
-                it.n0 = packed_blocks(p, it.nq0);
-                it.n1 = it.nq1 > 0 ? packed_blocks(p, p.nq) : 0;
+                it.q0 = p.r0;
+                it.nq0 = min(A.qt, p.n);
+                it.nq1 = p.n - it.nq0;
+                it.k0 = p.s0;
+                it.lk = p.len;
+                it.vis = p.shift;
+                it.n0 = A.cut.blocks(p, it.nq0);
+                it.n1 = it.nq1 > 0 ? A.cut.blocks(p, p.n) : 0;
                 it.base = blocks;
                 blocks += max(it.n0, it.n1);
             }
@@ -545,13 +519,6 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 int attention_packed_fwd_set_wait_limit(long long cycles) { return set_wait_limit(cycles); }
 
-// Items sorted by length are worth their own launch once there are more than
-// SMs to take them; beyond PACKED_PLAN_MAX the sort would cost more than the
-// imbalance, which evens out over so many.
-static bool planned(int slots, int Hkv) {
-    return (int64_t)slots * Hkv > gpt2_num_sms() && slots <= PACKED_PLAN_MAX;
-}
-
 size_t attention_packed_forward_tc_scratch(int n_seq, int total_q, int Hq, int Hkv) {
     const int slots = packed_slots(total_q, n_seq, 2 * (128 / (Hq / Hkv)));
     return slots <= PACKED_PLAN_MAX ? packed_plan_bytes(slots) : 0;
@@ -562,10 +529,10 @@ int launch_attention_packed_forward_tc(const PackedAttn& a, PackedPlan* plan, cu
     A.a = a;
     A.group = a.Hq / a.Hkv;
     A.qt = 128 / A.group;
-    const int slots = packed_slots(a.total_q, a.n_seq, 2 * A.qt);
-    A.items = slots * a.Hkv;
+    A.cut = PackedCut{false, 2 * A.qt, 128};
+    A.items = A.cut.slots(a) * a.Hkv;
     A.scale_log2 = LOG2E / sqrtf((float)HD);
-    A.plan = planned(slots, a.Hkv) ? plan : nullptr;
+    A.plan = planned(A.cut.slots(a), a.Hkv) ? plan : nullptr;
     CUtensorMap mq, mk, mv;
     // without keys nothing is loaded through the key and value maps
     const bool keys = a.total_k > 0;
@@ -575,7 +542,7 @@ int launch_attention_packed_forward_tc(const PackedAttn& a, PackedPlan* plan, cu
         return GPT2_ERR_CUDA;
     if (smem_attr((const void*)packed_fwd_tc_kernel, SMEM) != cudaSuccess) return GPT2_ERR_CUDA;
     const int grid = A.items < gpt2_num_sms() ? A.items : gpt2_num_sms();
-    if (A.plan) launch_packed_plan(a, plan, 2 * A.qt, s);
+    if (A.plan) launch_packed_plans(a, &A.cut, &A.plan, 1, s);
     packed_fwd_tc_kernel<<<grid, THREADS, SMEM, s>>>(mq, mk, mv, A);
     return A.plan ? 2 : 1;
 }

@@ -32,6 +32,24 @@ __device__ __forceinline__ float f2_total(uint64_t v) {
     return lo + hi;
 }
 
+// Load 16 consecutive fp32 columns of this thread's TMEM lane (as tc_ld32_issue).
+__device__ __forceinline__ void tc_ld16_issue(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tc_ld16_wait(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15])
+                 :
+                 : "memory");
+}
+
 // Bounded wait by a whole warp for the phase with the given parity: one try
 // and one vote a turn. Roles off the critical path sleep NS nanoseconds between
 // turns, so that their turns do not take the other warps' issue slots.
@@ -84,6 +102,44 @@ __device__ __forceinline__ int find_slot(const int32_t* cu, int n_seq, int total
     }
     first = f_lo;
     return lo;
+}
+
+// The next work item of this CTA, by a whole warp: a tile and a key head, from
+// the sorted plan or (x counts on from blockIdx.x) from the offsets themselves.
+__device__ __forceinline__ bool next_tile(const PackedAttn& a, const PackedCut& cut, PackedPlan* plan, int items,
+                                          int& x, PackedTile& t, int& kh) {
+    if (plan) {
+        int n = 0;
+        if ((threadIdx.x & 31) == 0) n = atomicAdd(&plan->next, 1);
+        n = __shfl_sync(0xffffffffu, n, 0);
+        if (n >= plan->count * a.Hkv) return false;
+        t = plan->tile[n / a.Hkv];
+        kh = n % a.Hkv;
+        return true;
+    }
+    const int slots = items / a.Hkv;
+    while (x < items) {
+        const int i = x;
+        x += gridDim.x;
+        // the later queries of a sequence, which see more keys, first; the earlier keys, seen by more queries
+        const int slot = cut.keys ? i / a.Hkv : slots - 1 - i / a.Hkv;
+        int f;
+        const int s = find_slot(cut.cu(a), a.n_seq, cut.total(a), cut.per, slot, f);
+        if (s < 0) continue;
+        const PackedSeq q = packed_seq(a, s);
+        const int at = (slot - f) * cut.per;
+        if (at < 0 || at >= cut.rows(q)) continue;
+        t = cut.tile(q, at);
+        kh = i % a.Hkv;
+        return true;
+    }
+    return false;
+}
+// Items sorted by length are worth their own launch once there are more than
+// SMs to take them; beyond PACKED_PLAN_MAX the sort would cost more than the
+// imbalance, which evens out over so many.
+inline bool planned(int slots, int Hkv) {
+    return (int64_t)slots * Hkv > gpt2_num_sms() && slots <= PACKED_PLAN_MAX;
 }
 
 // Rows of [heads][64] bf16 at `stride` elements, viewed as (64, heads, rows)

@@ -128,7 +128,10 @@ size_t attention_packed_forward_scratch(int dtype, int n_seq, int total_q, int m
 struct PackedPlan;
 size_t attention_packed_forward_tc_scratch(int n_seq, int total_q, int Hq, int Hkv);
 int launch_attention_packed_forward_tc(const PackedAttn& a, PackedPlan* plan, cudaStream_t s);
+size_t attention_packed_backward_tc_scratch(int n_seq, int total_q, int total_k, int Hq, int Hkv);
+int launch_attention_packed_backward_tc(const PackedAttn& a, const PackedAttnGrad& g, void* scratch, cudaStream_t s);
 int attention_packed_fwd_set_wait_limit(long long cycles);
+int attention_packed_bwd_set_wait_limit(long long cycles);
 int launch_attention_packed_forward(int dtype, const PackedAttn& a, void* scratch, cudaStream_t s);
 size_t attention_packed_backward_scratch(int dtype, int n_seq, int total_q, int total_k, int Hq, int Hkv, int hd);
 int launch_attention_packed_backward(int dtype, const PackedAttn& a, const PackedAttnGrad& g, void* scratch,

@@ -405,7 +405,7 @@ int gpt2_op_adamw(float* master, void* param_bf16, const float* grad, float* m, 
 int gpt2_debug_set_wait_limit(int64_t cycles) {
     const long long c = cycles > 0 ? (long long)cycles : 0;
     if (gemm_tc_set_wait_limit(c) || attention_tc_set_wait_limit(c) || attention_packed_fwd_set_wait_limit(c) ||
-        classifier_set_wait_limit(c))
+        attention_packed_bwd_set_wait_limit(c) || classifier_set_wait_limit(c))
         return GPT2_ERR_CUDA;
     return GPT2_OK;
 }
