@@ -256,8 +256,8 @@ int gpt2_op_attention_backward(int dtype, void* dqkv, const void* dout, const vo
  *   - n_seq = 0 or total_q = 0 launches nothing.
  * Scratch: the list of work items, or partial results of keys split over
  * blocks (few queries). */
-size_t gpt2_op_attention_packed_forward_scratch(int dtype, int n_seq, int total_q, int max_q, int max_k, int Hq,
-                                                int Hkv, int hd);
+size_t gpt2_op_attention_packed_forward_scratch(int dtype, int n_seq, int total_q, int total_k, int max_q, int max_k,
+                                                int Hq, int Hkv, int hd);
 int gpt2_op_attention_packed_forward(int dtype, void* o, int64_t o_stride, float* lse, const void* q,
                                      int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                                      int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k, int n_seq,

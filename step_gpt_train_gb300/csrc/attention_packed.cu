@@ -263,20 +263,19 @@ int launch_packed_plans(const PackedAttn& a, const PackedCut* cuts, PackedPlan* 
     return 1;
 }
 
-size_t attention_packed_forward_scratch(int dtype, int n_seq, int total_q, int max_q, int max_k, int Hq, int Hkv,
-                                        int hd) {
+size_t attention_packed_forward_scratch(int dtype, int n_seq, int total_q, int total_k, int max_q, int max_k, int Hq,
+                                        int Hkv, int hd) {
     if (dtype != GPT2_MODE_BF16) return 0;
+    if (attention_packed_few(max_q, Hq, Hkv)) 
+        return attention_packed_few_scratch(n_seq, total_k, max_q, max_k, Hq, Hkv);
     return attention_packed_forward_tc_scratch(n_seq, total_q, Hq, Hkv);
 }
 
 int launch_attention_packed_forward(int dtype, const PackedAttn& a, void* scratch, cudaStream_t s) {
+    if (dtype == GPT2_MODE_BF16 && attention_packed_few(a.max_q, a.Hq, a.Hkv))
+        return launch_attention_packed_few(a, scratch, s);
     if (dtype == GPT2_MODE_BF16) return launch_attention_packed_forward_tc(a, (PackedPlan*)scratch, s);
-    switch (a.hd) {
-        case 8: return forward<float, 8>(a, s);
-        case 16: return forward<float, 16>(a, s);
-        case 32: return forward<float, 32>(a, s);
-        default: return forward<float, 64>(a, s);
-    }
+    return launch_attention_packed_forward_f32(a, s);
 }
 
 size_t attention_packed_backward_scratch(int dtype, int n_seq, int total_q, int total_k, int Hq, int Hkv, int hd) {
@@ -294,10 +293,5 @@ int launch_attention_packed_backward(int dtype, const PackedAttn& a, const Packe
         if (a.Hq / a.Hkv <= 64) return launch_attention_packed_backward_tc(a, g, scratch, s);
         return backward<bf16, 64>(a, g, s);
     }
-    switch (a.hd) {
-        case 8: return backward<float, 8>(a, g, s);
-        case 16: return backward<float, 16>(a, g, s);
-        case 32: return backward<float, 32>(a, g, s);
-        default: return backward<float, 64>(a, g, s);
-    }
+    return launch_attention_packed_backward_f32(a, g, s);
 }

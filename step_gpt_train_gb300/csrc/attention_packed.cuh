@@ -7,6 +7,24 @@
 
 #define GPT2_FLAG_OFFSETS 8
 
+// Launches a kernel that may start while the one before it in the stream still
+// runs (its launch and setup hidden behind that), and waits for it itself with
+// griddepcontrol.wait before it reads what that kernel wrote.
+template <typename... P, typename... V>
+inline cudaError_t launch_dependent(void (*kernel)(P...), int grid, int threads, int smem, cudaStream_t s, const V&... v) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, v...);
+}
+
 // One sequence's rows: queries q0 .. q0 + lq - 1, keys k0 .. k0 + lk - 1.
 // Clamped into the buffers whatever the offsets hold.
 struct PackedSeq {
@@ -43,6 +61,39 @@ __device__ __forceinline__ int packed_find_row(const int32_t* cu, int n_seq, int
         if (cu[mid] <= row) lo = mid;
         else hi = mid;
     }
+    return lo;
+}
+
+// The work items of a packed batch are tiles of `per` rows of each sequence,
+// numbered without a table: sequence s owns the slots floor(cu[s] / per) + s
+// up to the next sequence's, which are at least its ceil(len / per) tiles
+// (floor(a + len) - floor(a) + 1 >= ceil(len) in units of per) and at most one
+// more, so total / per + n_seq slots hold every tile. The last sequence whose
+// first slot is at or before `slot`, found by a whole warp (32 probes a
+// round), or -1; any offsets give an answer in range.
+// (mul: rows to an offset's unit, which `per` counts.)
+__device__ __forceinline__ int find_slot(const int32_t* cu, int n_seq, int total, int per, int slot, int& first,
+                                         int mul = 1) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = n_seq, f_lo = 0;
+    bool any = false;
+    while (true) {
+        const int step = (hi - lo + 31) / 32;
+        const int s = lo + lane * step;
+        const int f = s < hi ? min(max(cu[s], 0), total) * mul / per + s : 0;
+        const uint32_t hit = __ballot_sync(0xffffffffu, s < hi && f <= slot);
+        const int c = __popc(hit);
+        if (c) {
+            any = true;
+            f_lo = __shfl_sync(0xffffffffu, f, c - 1);
+            lo += (c - 1) * step;
+        } else if (!any) {
+            return -1;
+        }
+        if (step == 1) break;
+        hi = min(hi, lo + step);
+    }
+    first = f_lo;
     return lo;
 }
 

@@ -73,37 +73,6 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
     }
 }
 
-// The work items of a packed batch are tiles of `per` rows of each sequence,
-// numbered without a table: sequence s owns the slots floor(cu[s] / per) + s
-// up to the next sequence's, which are at least its ceil(len / per) tiles
-// (floor(a + len) - floor(a) + 1 >= ceil(len) in units of per) and at most one
-// more, so total / per + n_seq slots hold every tile. The last sequence whose
-// first slot is at or before `slot`, found by a whole warp (32 probes a
-// round), or -1; any offsets give an answer in range.
-__device__ __forceinline__ int find_slot(const int32_t* cu, int n_seq, int total, int per, int slot, int& first) {
-    const int lane = threadIdx.x & 31;
-    int lo = 0, hi = n_seq, f_lo = 0;
-    bool any = false;
-    while (true) {
-        const int step = (hi - lo + 31) / 32;
-        const int s = lo + lane * step;
-        const int f = s < hi ? min(max(cu[s], 0), total) / per + s : 0;
-        const uint32_t hit = __ballot_sync(0xffffffffu, s < hi && f <= slot);
-        const int c = __popc(hit);
-        if (c) {
-            any = true;
-            f_lo = __shfl_sync(0xffffffffu, f, c - 1);
-            lo += (c - 1) * step;
-        } else if (!any) {
-            return -1;
-        }
-        if (step == 1) break;
-        hi = min(hi, lo + step);
-    }
-    first = f_lo;
-    return lo;
-}
-
 // The next work item of this CTA, by a whole warp: a tile and a key head, from
 // the sorted plan or (x counts on from blockIdx.x) from the offsets themselves.
 __device__ __forceinline__ bool next_tile(const PackedAttn& a, const PackedCut& cut, PackedPlan* plan, int items,

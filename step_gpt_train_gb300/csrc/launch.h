@@ -122,12 +122,18 @@ struct PackedAttnGrad {
     int64_t dout_stride, dq_stride, dk_stride, dv_stride;
     float* D;  // [Hq, total_q]
 };
-size_t attention_packed_forward_scratch(int dtype, int n_seq, int total_q, int max_q, int max_k, int Hq, int Hkv,
-                                        int hd);
+size_t attention_packed_forward_scratch(int dtype, int n_seq, int total_q, int total_k, int max_q, int max_k, int Hq,
+                                        int Hkv, int hd);
+int launch_attention_packed_forward_f32(const PackedAttn& a, cudaStream_t s);
+int launch_attention_packed_backward_f32(const PackedAttn& a, const PackedAttnGrad& g, cudaStream_t s);
 // bf16 on the tensor cores.
 struct PackedPlan;
 size_t attention_packed_forward_tc_scratch(int n_seq, int total_q, int Hq, int Hkv);
 int launch_attention_packed_forward_tc(const PackedAttn& a, PackedPlan* plan, cudaStream_t s);
+// bf16 with at most 16 rows (queries x heads of a group) to a key head of a sequence.
+bool attention_packed_few(int max_q, int Hq, int Hkv);
+size_t attention_packed_few_scratch(int n_seq, int total_k, int max_q, int max_k, int Hq, int Hkv);
+int launch_attention_packed_few(const PackedAttn& a, void* scratch, cudaStream_t s);
 size_t attention_packed_backward_tc_scratch(int n_seq, int total_q, int total_k, int Hq, int Hkv);
 int launch_attention_packed_backward_tc(const PackedAttn& a, const PackedAttnGrad& g, void* scratch, cudaStream_t s);
 int attention_packed_fwd_set_wait_limit(long long cycles);

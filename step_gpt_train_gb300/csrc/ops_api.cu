@@ -268,10 +268,10 @@ static bool rows_ok(const void* p, int64_t stride, int heads, int hd, int dtype)
     return al16(p) && stride >= (int64_t)heads * hd && stride % per16 == 0 && stride < ((int64_t)1 << 31);
 }
 
-size_t gpt2_op_attention_packed_forward_scratch(int dtype, int n_seq, int total_q, int max_q, int max_k, int Hq,
-                                                int Hkv, int hd) {
-    if (!packed_ok(dtype, total_q, 0, n_seq, max_q, max_k, Hq, Hkv, hd)) return 0;
-    return attention_packed_forward_scratch(dtype, n_seq, total_q, max_q, max_k, Hq, Hkv, hd);
+size_t gpt2_op_attention_packed_forward_scratch(int dtype, int n_seq, int total_q, int total_k, int max_q, int max_k,
+                                                int Hq, int Hkv, int hd) {
+    if (!packed_ok(dtype, total_q, total_k, n_seq, max_q, max_k, Hq, Hkv, hd)) return 0;
+    return attention_packed_forward_scratch(dtype, n_seq, total_q, total_k, max_q, max_k, Hq, Hkv, hd);
 }
 
 int gpt2_op_attention_packed_forward(int dtype, void* o, int64_t o_stride, float* lse, const void* q,
@@ -285,7 +285,7 @@ int gpt2_op_attention_packed_forward(int dtype, void* o, int64_t o_stride, float
     if (!rows_ok(o, o_stride, Hq, hd, dtype) || !rows_ok(q, q_stride, Hq, hd, dtype) ||
         !rows_ok(k, k_stride, Hkv, hd, dtype) || !rows_ok(v, v_stride, Hkv, hd, dtype))
         return GPT2_ERR_ARG;
-    const size_t need = attention_packed_forward_scratch(dtype, n_seq, total_q, max_q, max_k, Hq, Hkv, hd);
+    const size_t need = attention_packed_forward_scratch(dtype, n_seq, total_q, total_k, max_q, max_k, Hq, Hkv, hd);
     if (need && (!scratch || scratch_bytes < need)) return GPT2_ERR_WORKSPACE;
     const PackedAttn a = {q,    k,     v,     q_stride, k_stride, v_stride, o,     o_stride, lse, cu_q,
                           cu_k, n_seq, total_q, total_k,  max_q,    max_k,    Hq,    Hkv,      hd,  d_status};

@@ -135,7 +135,7 @@ _SIGNATURES = {
     "gpt2_op_attention_backward_scratch": (c_size_t, [c_int, c_int, c_int]),
     "gpt2_op_attention_backward": (c_int, [c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int,
                                            c_int, c_int, c_void_p, c_size_t, c_void_p]),
-    "gpt2_op_attention_packed_forward_scratch": (c_size_t, [c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int]),
+    "gpt2_op_attention_packed_forward_scratch": (c_size_t, [c_int] * 9),
     "gpt2_op_attention_packed_forward": (c_int, [c_int, c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_void_p,
                                                  c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_int, c_int, c_int,
                                                  c_int, c_int, c_int, c_int, c_int, c_void_p, c_size_t, c_void_p,
@@ -611,7 +611,7 @@ def gpt2_op_attention_packed_forward(o, lse, q, k, v, cu_q, cu_k, max_q, max_k, 
     if cu_k.numel() != cu_q.numel():
         raise ValueError("cu_q and cu_k need the same number of sequences")
     n = cu_q.numel() - 1
-    nb = lib.gpt2_op_attention_packed_forward_scratch(dt, n, tq, max_q, max_k, hq, hkv, hd)
+    nb = lib.gpt2_op_attention_packed_forward_scratch(dt, n, tq, tk, max_q, max_k, hq, hkv, hd)
     sc = _scratch(nb) if nb else None
     check(lib.gpt2_op_attention_packed_forward(dt, _p(o), _rows(o, "o"), _p(lse), _p(q), _rows(q, "q"), _p(k),
                                                _rows(k, "k"), _p(v), _rows(v, "v"), _p(cu_q), _p(cu_k), n, tq, tk,

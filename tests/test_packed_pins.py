@@ -144,14 +144,14 @@ def test_attention_backward_refusals(lib, bad):
 def test_attention_workspace_and_nothing_to_do(lib):
     assert backward(lib, nb=lib.gpt2_op_attention_packed_backward_scratch(1, 3, 300, 300, 12, 12, 64) - 1) == WORKSPACE
     assert backward(lib, sc=None) == WORKSPACE
-    need = lib.gpt2_op_attention_packed_forward_scratch(1, 3, 300, 1, 1 << 17, 12, 12, 64)
-    if need:
-        assert forward(lib, mq=1, mk=1 << 17, nb=need - 1) == WORKSPACE
-        assert forward(lib, mq=1, mk=1 << 17, sc=None) == WORKSPACE
+    need = lib.gpt2_op_attention_packed_forward_scratch(1, 3, 3, 1 << 17, 1, 1 << 17, 12, 12, 64)
+    assert need > 0
+    assert forward(lib, tq=3, tk=1 << 17, mq=1, mk=1 << 17, nb=need - 1) == WORKSPACE
+    assert forward(lib, tq=3, tk=1 << 17, mq=1, mk=1 << 17, sc=None) == WORKSPACE
     for kw in (dict(n=0), dict(tq=0)):
         assert forward(lib, **kw) == OK
     assert backward(lib, n=0) == OK and backward(lib, tq=0, tk=0) == OK
-    assert lib.gpt2_op_attention_packed_forward_scratch(1, -1, 1, 1, 1, 12, 12, 64) == 0
+    assert lib.gpt2_op_attention_packed_forward_scratch(1, -1, 1, 1, 1, 1, 12, 12, 64) == 0
 
 
 def logprobs(lib, **kw):
