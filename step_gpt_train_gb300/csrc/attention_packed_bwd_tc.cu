@@ -28,7 +28,8 @@
 // behind the sequence's end set to zero (0 * NaN from a neighbour would reach
 // the accumulators), outputs of items that meet nothing; 4..7 accumulators out
 // (while the next item runs); 8..15, 16..23 elementwise. Every wait is bounded.
-// Before them a pass forms D = rowsum(dO * O) and lse log2(e) per row.
+// Before them a pass forms D = rowsum(dO * O) and lse log2(e) per row and sorts
+// the items.
 #include "attention_packed_tc.cuh"
 
 namespace {
@@ -70,21 +71,52 @@ struct Args {
     PackedPlan* plan;
 };
 
-// lse log2(e) and D of every (row, head): eight lanes per pair, 16 bytes each.
-__global__ void __launch_bounds__(256) packed_prep_kernel(PackedAttn a, PackedAttnGrad g, float2* ld) {
-    const int i = blockIdx.x * 32 + threadIdx.x / 8, e = threadIdx.x % 8;
-    const bool in = i < a.total_q * a.Hq;
-    const int row = in ? i / a.Hq : 0, h = in ? i - row * a.Hq : 0;
-    float x[8], y[8], d = 0.f;
-    load8((const bf16*)a.o + (int64_t)row * a.o_stride + h * HD + e * 8, x);
-    load8((const bf16*)g.dout + (int64_t)row * g.dout_stride + h * HD + e * 8, y);
+// Before the two kernels: blocks 0 and 1 sort their items (with plans), the
+// others form lse log2(e) and D of every (row, head), eight lanes to each, 16
+// bytes of O and dO a lane, four pairs in flight.
+constexpr int PREP = 512;  // pairs of a block of 1024 threads
+struct PrepArgs {
+    PackedAttn a;
+    PackedAttnGrad g;
+    float2* ld;
+    int plans;
+    PackedCut cut[2];
+    PackedPlan* plan[2];
+};
+__global__ void __launch_bounds__(1024) packed_prep_kernel(const __grid_constant__ PrepArgs A) {
+    const PackedAttn& a = A.a;
+    if ((int)blockIdx.x < A.plans) {
+        packed_plan_block(a, A.cut[blockIdx.x], A.plan[blockIdx.x], blockIdx.x == 0);
+        return;
+    }
+    const int first = (blockIdx.x - A.plans) * PREP + threadIdx.x / 8, e = threadIdx.x % 8;
+    uint4 x[4], y[4];
+    int row[4], h[4];
+    bool in[4];
 #pragma unroll
-    for (int j = 0; j < 8; j++) d += x[j] * y[j];
+    for (int k = 0; k < 4; k++) {
+        const int i = first + k * 128;
+        in[k] = i < a.total_q * a.Hq;
+        row[k] = in[k] ? i / a.Hq : 0;
+        h[k] = in[k] ? i - row[k] * a.Hq : 0;
+        x[k] = *reinterpret_cast<const uint4*>((const bf16*)a.o + (int64_t)row[k] * a.o_stride + h[k] * HD + e * 8);
+        y[k] = *reinterpret_cast<const uint4*>((const bf16*)A.g.dout + (int64_t)row[k] * A.g.dout_stride + h[k] * HD + e * 8);
+    }
 #pragma unroll
-    for (int o = 4; o > 0; o /= 2) d += __shfl_xor_sync(0xffffffffu, d, o);
-    if (in && e == 0) {
-        const float l = a.lse[(int64_t)h * a.total_q + row];
-        ld[(int64_t)h * a.total_q + row] = make_float2(l == -INFINITY ? 0.f : l * LOG2E, d);
+    for (int k = 0; k < 4; k++) {
+        const uint32_t u[4] = {x[k].x, x[k].y, x[k].z, x[k].w}, v[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
+        float d = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            d += __uint_as_float(u[j] << 16) * __uint_as_float(v[j] << 16) +
+                 __uint_as_float(u[j] & 0xFFFF0000u) * __uint_as_float(v[j] & 0xFFFF0000u);
+#pragma unroll
+        for (int o = 4; o > 0; o /= 2) d += __shfl_xor_sync(0xffffffffu, d, o);
+        if (in[k] && e == 0) {
+            const int64_t at = (int64_t)h[k] * a.total_q + row[k];
+            const float l = a.lse[at];
+            A.ld[at] = make_float2(l == -INFINITY ? 0.f : l * LOG2E, d);
+        }
     }
 }
 
@@ -624,10 +656,11 @@ int launch_attention_packed_backward_tc(const PackedAttn& a, const PackedAttnGra
     if (smem_attr((const void*)packed_bwd_tc_kernel<true>, SMEM) != cudaSuccess ||
         smem_attr((const void*)packed_bwd_tc_kernel<false>, SMEM) != cudaSuccess)
         return GPT2_ERR_CUDA;
+    PrepArgs P = {a, g, ld, plan[0] ? 2 : 0, {cut[0], cut[1]}, {plan[0], plan[1]}};
+    const int prep = P.plans + (int)(((int64_t)a.total_q * a.Hq + PREP - 1) / PREP);
     int launches = 0;
-    if (plan[0]) launches += launch_packed_plans(a, cut, plan, 2, s);
-    if (hq) {
-        packed_prep_kernel<<<(a.total_q * a.Hq + 31) / 32, 256, 0, s>>>(a, g, ld);
+    if (prep) {
+        packed_prep_kernel<<<prep, 1024, 0, s>>>(P);
         launches++;
     }
     const int sms = gpt2_num_sms();

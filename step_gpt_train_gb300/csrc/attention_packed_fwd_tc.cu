@@ -68,6 +68,11 @@ struct Args {
     PackedPlan* plan;     // sorted items, or null: found from the offsets
 };
 
+__global__ void __launch_bounds__(1024) packed_plan_kernel(PackedAttn a, PackedCut cut, PackedPlan* plan) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the forward's blocks may set themselves up
+    packed_plan_block(a, cut, plan, true);
+}
+
 __global__ void __launch_bounds__(THREADS, 1)
     packed_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Args A) {
@@ -280,6 +285,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // ------------------------------------------------------ work items, tails of V
         int x = blockIdx.x, blocks = 0;
         if (blockIdx.x == 0 && !A.plan) packed_check(a, lane, 32);
+        if (A.plan) asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is written
         auto put = [&](int i, Item& it) -> bool {  // the next item, or the end, into ring slot i
             PackedTile p;
             it.valid = next_tile(a, A.cut, A.plan, A.items, x, p, it.kh);
@@ -542,7 +548,12 @@ int launch_attention_packed_forward_tc(const PackedAttn& a, PackedPlan* plan, cu
         return GPT2_ERR_CUDA;
     if (smem_attr((const void*)packed_fwd_tc_kernel, SMEM) != cudaSuccess) return GPT2_ERR_CUDA;
     const int grid = A.items < gpt2_num_sms() ? A.items : gpt2_num_sms();
-    if (A.plan) launch_packed_plans(a, &A.cut, &A.plan, 1, s);
-    packed_fwd_tc_kernel<<<grid, THREADS, SMEM, s>>>(mq, mk, mv, A);
-    return A.plan ? 2 : 1;
+    if (!A.plan) {
+        packed_fwd_tc_kernel<<<grid, THREADS, SMEM, s>>>(mq, mk, mv, A);
+        return 1;
+    }
+    packed_plan_kernel<<<1, 1024, 0, s>>>(a, A.cut, plan);
+    if (launch_dependent(packed_fwd_tc_kernel, grid, THREADS, SMEM, s, mq, mk, mv, A) != cudaSuccess)
+        return GPT2_ERR_CUDA;
+    return 2;
 }
