@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto bar = [&](int n) { const uint32_t b = bars + 8u * nbar; nbar += n; return b; };
     const uint32_t it_full = bar(NIT), it_empty = bar(NIT), a_full = bar(2), a_empty = bar(2);
     const uint32_t b_full = bar(NB), b_empty = bar(NB), b_raw = bar(NB);
-    const uint32_t s_full = bar(2), s_free = bar(2), dp_full = bar(2), dp_free = bar(2), p_full = bar(2);
+    const uint32_t s_full = bar(2), dp_full = bar(2), p_full = bar(2);
     const uint32_t ds_full = bar(2), ds_free = bar(2), acc_full = bar(1), acc_empty = bar(1), drain = bar(1);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(gbase + OFF_BAR + 496);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + OFF_BAR + 500);
@@ -156,9 +156,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(a_full + 8 * i, 1);
             mbar_init(a_empty + 8 * i, 1);
             mbar_init(s_full + 8 * i, 1);
-            mbar_init(s_free + 8 * i, EW);
             mbar_init(dp_full + 8 * i, 1);
-            mbar_init(dp_free + 8 * i, EW);
             mbar_init(p_full + 8 * i, EW);
             mbar_init(ds_full + 8 * i, EW);
             mbar_init(ds_free + 8 * i, 1);
@@ -260,12 +258,14 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!take(c.i + 1, it)) return Cur{false, 0, 0, 0, 0};
             return Cur{true, c.i + 1, 0, it.nb, c.g + 1};
         };
-        auto issue_s = [&](const Cur& c) -> bool {
-            const int st = c.g % NB, p = c.g & 1;
+        // S and dP of step g + 2 go where those of step g were: free once the elementwise warps have handed in
+        // P (dQ: dS) and dS of step g, which the callers have waited for
+        auto loaded = [&](const Cur& c) -> bool {
             if (c.n == 0 && !wait(a_full + 8 * (c.i & 1), (c.i >> 1) & 1, abort_flag, status)) return false;
-            if (!wait(b_full + 8 * st, (c.g / NB) & 1, abort_flag, status)) return false;
-            if (!wait(s_free + 8 * p, ((c.g >> 1) & 1) ^ 1u, abort_flag, status)) return false;
-            tc_fence_after();
+            return wait(b_full + 8 * (c.g % NB), (c.g / NB) & 1, abort_flag, status);
+        };
+        auto issue_s = [&](const Cur& c) {
+            const int st = c.g % NB, p = c.g & 1;
             const uint64_t da = sw128_desc(sA(c.i & 1, 0), 16, 1024), db = sw128_desc(sB(st, 0), 16, 1024);
             if (leader) {
 #pragma unroll
@@ -274,12 +274,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tc_commit(s_full + 8 * p);
             }
             __syncwarp();
-            return true;
         };
-        auto issue_dp = [&](const Cur& c) -> bool {
+        auto issue_dp = [&](const Cur& c) {
             const int st = c.g % NB, p = c.g & 1;
-            if (!wait(dp_free + 8 * p, ((c.g >> 1) & 1) ^ 1u, abort_flag, status)) return false;
-            tc_fence_after();
             const uint64_t da = sw128_desc(sA(c.i & 1, 1), 16, 1024), db = sw128_desc(sB(st, 1), 16, 1024);
             if (leader) {
 #pragma unroll
@@ -289,15 +286,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (c.n == c.nb - 1) tc_commit(a_empty + 8 * (c.i & 1));  // the item's last read of A1, A2
             }
             __syncwarp();
-            return true;
         };
-        int done = 0;  // finished items
         // accumulate from P or dS (MN-major B: one 16-row k step = 2048 bytes = 128 units of the address field)
-        auto accumulate = [&](const Cur& c, uint32_t acc, uint32_t src, int which, uint32_t full) -> bool {
+        auto accumulate = [&](const Cur& c, uint32_t acc, uint32_t src, int which) {
             const int st = c.g % NB, p = c.g & 1;
-            if (c.n == 0 && (DQ || which) && !wait(acc_empty, (done & 1) ^ 1u, abort_flag, status)) return false;
-            if (!wait(full + 8 * p, (c.g >> 1) & 1, abort_flag, status)) return false;
-            tc_fence_after();
             const uint64_t db = sw128_desc(sB(st, which), 8192, 1024);
             if (leader) {
 #pragma unroll
@@ -306,23 +298,42 @@ __global__ void __launch_bounds__(THREADS, 1)
                               (c.n > 0 || k > 0) ? 1u : 0u);
             }
             __syncwarp();
-            return true;
         };
         Item it0;
         Cur c = {false, 0, 0, 0, 0};
         if (take(0, it0)) c = Cur{true, 0, 0, it0.nb, 0};
         Cur c1 = next(c);
         bool ok = true;
-        if (c.valid) ok = issue_s(c) && issue_dp(c);
-        if (ok && c1.valid) ok = issue_s(c1) && issue_dp(c1);
+        for (int k = 0; ok && k < 2; k++) {
+            const Cur& x = k ? c1 : c;
+            if (!x.valid || !(ok = loaded(x))) break;
+            tc_fence_after();
+            issue_s(x);
+            issue_dp(x);
+        }
+        int done = 0;  // finished items
         while (ok && c.valid) {
+            const uint32_t p = c.g & 1, ph = (c.g >> 1) & 1;
             const Cur c2 = next(c1);
-            if (c2.valid && !(ok = issue_s(c2))) break;
-            if (!DQ && !(ok = accumulate(c, T_ACC1, T_P, 1, p_full))) break;
-            if (c2.valid && !(ok = issue_dp(c2))) break;
-            if (!(ok = accumulate(c, T_ACC0, T_DS, 0, ds_full))) break;
+            // everything but this step's P and dS has long arrived. The products of the step after next come
+            // first: its elementwise warps wait for them
+            if (c2.valid && !(ok = loaded(c2))) break;
+            if (c.n == 0 && !(ok = wait(acc_empty, (done & 1) ^ 1u, abort_flag, status))) break;
+            if (!DQ) {
+                if (!(ok = wait(p_full + 8 * p, ph, abort_flag, status))) break;
+                tc_fence_after();
+                if (c2.valid) issue_s(c2);
+                accumulate(c, T_ACC1, T_P, 1);
+            }
+            if (!(ok = wait(ds_full + 8 * p, ph, abort_flag, status))) break;
+            tc_fence_after();
+            if (c2.valid) {
+                if (DQ) issue_s(c2);
+                issue_dp(c2);
+            }
+            accumulate(c, T_ACC0, T_DS, 0);
             if (leader) {
-                tc_commit(ds_free + 8 * (c.g & 1));
+                tc_commit(ds_free + 8 * p);
                 tc_commit(b_empty + 8 * (c.g % NB));
                 if (c.n == c.nb - 1) tc_commit(acc_full);
             }
@@ -518,9 +529,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tc_fence_after();
                 tc_ld32_issue(tS, v);
                 tc_ld_wait(v);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(s_free + 8 * odd);
                 const uint64_t* nl2 = reinterpret_cast<const uint64_t*>(slot);
                 const uint64_t nlr = f2_pack(-ld.x, -ld.x), dr = f2_pack(ld.y, ld.y);
                 float p[32];
@@ -558,11 +566,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                     uint32_t w[16];
                     tc_ld16_issue(tDP + 16 * hh, w);
                     tc_ld16_wait(w);
-                    if (hh) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(dp_free + 8 * odd);
-                    }
 #pragma unroll
                     for (int c = 0; c < 16; c += 2) {
                         const int e = 16 * hh + c;
