@@ -20,11 +20,10 @@
 // A step's chain (wait, load S, exponentials, store P, wait, load dP, store dS)
 // is all latency, so two steps are in flight: even and odd steps have their own
 // TMEM buffers (S, dP, P, dS: 192 columns each) and their own eight elementwise
-// warps (32 columns a thread). One MMA warp issues S and dP of step g + 2
-// between the accumulations of step g, always in step order, which fixes the
-// order of every sum.
+// warps (32 columns a thread). One warp issues all accumulations, in step order,
+// which fixes the order of every sum; another S and dP, two steps ahead.
 //
-// Warps: 0 TMA producer; 1 MMA; 2 work items (ring of four), rows of a block
+// Warps: 0 TMA producer; 1, 3 MMA; 2 work items (ring of four), rows of a block
 // behind the sequence's end set to zero (0 * NaN from a neighbour would reach
 // the accumulators), outputs of items that meet nothing; 4..7 accumulators out
 // (while the next item runs); 8..15, 16..23 elementwise. Every wait is bounded.
@@ -138,7 +137,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t it_full = bar(NIT), it_empty = bar(NIT), a_full = bar(2), a_empty = bar(2);
     const uint32_t b_full = bar(NB), b_empty = bar(NB), b_raw = bar(NB);
     const uint32_t s_full = bar(2), dp_full = bar(2), p_full = bar(2);
-    const uint32_t ds_full = bar(2), ds_free = bar(2), acc_full = bar(1), acc_empty = bar(1), drain = bar(1);
+    const uint32_t ds_full = bar(2), ds_free = bar(2), acc_full = bar(1), acc_empty = bar(1), drain = bar(2);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(gbase + OFF_BAR + 496);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + OFF_BAR + 500);
     Item* ring = reinterpret_cast<Item*>(gbase + OFF_IT);
@@ -150,7 +149,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < NIT; i++) {
             mbar_init(it_full + 8 * i, 1);
-            mbar_init(it_empty + 8 * i, 2 + 4 + 2 * EW);
+            mbar_init(it_empty + 8 * i, 3 + 4 + 2 * EW);
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(a_full + 8 * i, 1);
@@ -169,6 +168,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_init(acc_full, 1);
         mbar_init(acc_empty, 4);
         mbar_init(drain, 1);
+        mbar_init(drain + 8, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -241,109 +241,83 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         }
         __syncwarp();
-    } else if (warp == 1) {
-        // ------------------------------------------------------ MMA: the whole warp runs the schedule, one
-        // elected lane issues
+    } else if (warp == 1 || warp == 3) {
+        // ------------------------------------------------------ MMA: warp 1 S and dP, warp 3 the accumulations; the
+        // whole warp runs the schedule, one elected lane issues (an issue takes about 60 cycles, more than these
+        // products, and a wait that passes at once 90: one warp for both took 1500 a step)
         const bool leader = elect_one();
         constexpr uint32_t idesc_s = make_idesc(128, BLK, false, false);  // K-major x K-major
         constexpr uint32_t idesc_o = make_idesc(128, HD, false, true);    // K-major x MN-major
-        struct Cur {
-            bool valid;
-            int i, n, nb, g;  // item, block, blocks, step
-        };
-        auto next = [&](const Cur& c) -> Cur {
-            if (!c.valid) return c;
-            if (c.n + 1 < c.nb) return Cur{true, c.i, c.n + 1, c.nb, c.g + 1};
-            Item it;
-            if (!take(c.i + 1, it)) return Cur{false, 0, 0, 0, 0};
-            return Cur{true, c.i + 1, 0, it.nb, c.g + 1};
-        };
-        // S and dP of step g + 2 go where those of step g were: free once the elementwise warps have handed in
-        // P (dQ: dS) and dS of step g, which the callers have waited for
-        auto loaded = [&](const Cur& c) -> bool {
-            if (c.n == 0 && !wait(a_full + 8 * (c.i & 1), (c.i >> 1) & 1, abort_flag, status)) return false;
-            return wait(b_full + 8 * (c.g % NB), (c.g / NB) & 1, abort_flag, status);
-        };
-        auto issue_s = [&](const Cur& c) {
-            const int st = c.g % NB, p = c.g & 1;
-            const uint64_t da = sw128_desc(sA(c.i & 1, 0), 16, 1024), db = sw128_desc(sB(st, 0), 16, 1024);
-            if (leader) {
-#pragma unroll
-                for (int k = 0; k < HD / 16; k++)
-                    tc_mma(tmem + T_STEP * p + T_S, da + 2 * k, db + 2 * k, idesc_s, k > 0 ? 1u : 0u);
-                tc_commit(s_full + 8 * p);
-            }
-            __syncwarp();
-        };
-        auto issue_dp = [&](const Cur& c) {
-            const int st = c.g % NB, p = c.g & 1;
-            const uint64_t da = sw128_desc(sA(c.i & 1, 1), 16, 1024), db = sw128_desc(sB(st, 1), 16, 1024);
-            if (leader) {
-#pragma unroll
-                for (int k = 0; k < HD / 16; k++)
-                    tc_mma(tmem + T_STEP * p + T_DP, da + 2 * k, db + 2 * k, idesc_s, k > 0 ? 1u : 0u);
-                tc_commit(dp_full + 8 * p);
-                if (c.n == c.nb - 1) tc_commit(a_empty + 8 * (c.i & 1));  // the item's last read of A1, A2
-            }
-            __syncwarp();
-        };
-        // accumulate from P or dS (MN-major B: one 16-row k step = 2048 bytes = 128 units of the address field)
-        auto accumulate = [&](const Cur& c, uint32_t acc, uint32_t src, int which) {
-            const int st = c.g % NB, p = c.g & 1;
-            const uint64_t db = sw128_desc(sB(st, which), 8192, 1024);
-            if (leader) {
-#pragma unroll
-                for (int k = 0; k < BLK / 16; k++)
-                    tc_mma_ts(tmem + acc, tmem + T_STEP * p + src + 8 * k, db + 128 * k, idesc_o,
-                              (c.n > 0 || k > 0) ? 1u : 0u);
-            }
-            __syncwarp();
-        };
-        Item it0;
-        Cur c = {false, 0, 0, 0, 0};
-        if (take(0, it0)) c = Cur{true, 0, 0, it0.nb, 0};
-        Cur c1 = next(c);
+        Item it;
         bool ok = true;
-        for (int k = 0; ok && k < 2; k++) {
-            const Cur& x = k ? c1 : c;
-            if (!x.valid || !(ok = loaded(x))) break;
-            tc_fence_after();
-            issue_s(x);
-            issue_dp(x);
+        for (int i = 0; ok && take(i, it); i++) {
+            if (warp == 1) {
+                if (!(ok = wait(a_full + 8 * (i & 1), (i >> 1) & 1, abort_flag, status))) break;
+                const uint64_t da1 = sw128_desc(sA(i & 1, 0), 16, 1024), da2 = sw128_desc(sA(i & 1, 1), 16, 1024);
+#pragma unroll 1
+                for (int n = 0; n < it.nb; n++) {
+                    const int g = it.base + n, st = g % NB, p = g & 1;
+                    const uint32_t before = ((g >> 1) & 1) ^ 1;
+                    const uint64_t db1 = sw128_desc(sB(st, 0), 16, 1024), db2 = sw128_desc(sB(st, 1), 16, 1024);
+                    if (!(ok = wait(b_full + 8 * st, (g / NB) & 1, abort_flag, status))) break;
+                    // S and dP go where those of step g - 2 were: free once its P (dQ: dS) and dS have come
+                    if (!(ok = wait((DQ ? ds_full : p_full) + 8 * p, before, abort_flag, status))) break;
+                    tc_fence_after();
+                    if (leader) {
+#pragma unroll
+                        for (int k = 0; k < HD / 16; k++)
+                            tc_mma(tmem + T_STEP * p + T_S, da1 + 2 * k, db1 + 2 * k, idesc_s, k > 0 ? 1u : 0u);
+                        tc_commit(s_full + 8 * p);
+                    }
+                    __syncwarp();
+                    if (!DQ && !(ok = wait(ds_full + 8 * p, before, abort_flag, status))) break;
+                    tc_fence_after();
+                    if (leader) {
+#pragma unroll
+                        for (int k = 0; k < HD / 16; k++)
+                            tc_mma(tmem + T_STEP * p + T_DP, da2 + 2 * k, db2 + 2 * k, idesc_s, k > 0 ? 1u : 0u);
+                        tc_commit(dp_full + 8 * p);
+                        if (n == it.nb - 1) tc_commit(a_empty + 8 * (i & 1));  // the item's last read of A1, A2
+                    }
+                    __syncwarp();
+                }
+            } else {
+                if (!(ok = wait(acc_empty, (i & 1) ^ 1u, abort_flag, status))) break;
+#pragma unroll 1
+                for (int n = 0; n < it.nb; n++) {
+                    const int g = it.base + n, st = g % NB, p = g & 1;
+                    const uint32_t ph = (g >> 1) & 1;
+                    // MN-major B: one 16-row k step = 2048 bytes = 128 units of the address field
+                    const uint64_t db1 = sw128_desc(sB(st, 0), 8192, 1024), db2 = sw128_desc(sB(st, 1), 8192, 1024);
+                    if (!(ok = wait(b_full + 8 * st, (g / NB) & 1, abort_flag, status))) break;
+                    if (!DQ) {
+                        if (!(ok = wait(p_full + 8 * p, ph, abort_flag, status))) break;
+                        tc_fence_after();
+                        if (leader) {
+#pragma unroll
+                            for (int k = 0; k < BLK / 16; k++)
+                                tc_mma_ts(tmem + T_ACC1, tmem + T_STEP * p + T_P + 8 * k, db2 + 128 * k, idesc_o,
+                                          (n > 0 || k > 0) ? 1u : 0u);
+                        }
+                        __syncwarp();
+                    }
+                    if (!(ok = wait(ds_full + 8 * p, ph, abort_flag, status))) break;
+                    tc_fence_after();
+                    if (leader) {
+#pragma unroll
+                        for (int k = 0; k < BLK / 16; k++)
+                            tc_mma_ts(tmem + T_ACC0, tmem + T_STEP * p + T_DS + 8 * k, db1 + 128 * k, idesc_o,
+                                      (n > 0 || k > 0) ? 1u : 0u);
+                        tc_commit(ds_free + 8 * p);
+                        tc_commit(b_empty + 8 * st);
+                        if (n == it.nb - 1) tc_commit(acc_full);
+                    }
+                    __syncwarp();
+                }
+            }
         }
-        int done = 0;  // finished items
-        while (ok && c.valid) {
-            const uint32_t p = c.g & 1, ph = (c.g >> 1) & 1;
-            const Cur c2 = next(c1);
-            // everything but this step's P and dS has long arrived. The products of the step after next come
-            // first: its elementwise warps wait for them
-            if (c2.valid && !(ok = loaded(c2))) break;
-            if (c.n == 0 && !(ok = wait(acc_empty, (done & 1) ^ 1u, abort_flag, status))) break;
-            if (!DQ) {
-                if (!(ok = wait(p_full + 8 * p, ph, abort_flag, status))) break;
-                tc_fence_after();
-                if (c2.valid) issue_s(c2);
-                accumulate(c, T_ACC1, T_P, 1);
-            }
-            if (!(ok = wait(ds_full + 8 * p, ph, abort_flag, status))) break;
-            tc_fence_after();
-            if (c2.valid) {
-                if (DQ) issue_s(c2);
-                issue_dp(c2);
-            }
-            accumulate(c, T_ACC0, T_DS, 0);
-            if (leader) {
-                tc_commit(ds_free + 8 * p);
-                tc_commit(b_empty + 8 * (c.g % NB));
-                if (c.n == c.nb - 1) tc_commit(acc_full);
-            }
-            __syncwarp();
-            if (c.n == c.nb - 1) done++;
-            c = c1;
-            c1 = c2;
-        }
-        if (leader) tc_commit(drain);
-        mbar_drain(drain, 0, status);
+        if (leader) tc_commit(drain + 8 * (warp >> 1));
+        mbar_drain(drain + 8 * (warp >> 1), 0, status);
     } else if (warp == 2) {
         // ------------------------------------------------------ work items, tails of blocks
         int x = blockIdx.x, steps = 0;
@@ -386,8 +360,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
             return true;
         };
-        // The MMA warp looks two steps ahead, so an item's tails may wait for its load only after the two items
-        // behind it are in the ring.
+        // S and dP run two steps ahead of the accumulations, so an item's tail may wait for its load only after
+        // the two items behind it are in the ring.
         int uses[NB];
         for (int i = 0; i < NB; i++) uses[i] = 0;
         Item it[3];
