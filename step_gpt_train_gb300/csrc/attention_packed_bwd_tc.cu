@@ -23,7 +23,7 @@
 // warps (32 columns a thread). One warp issues all accumulations, in step order,
 // which fixes the order of every sum; another S and dP, two steps ahead.
 //
-// Warps: 0 TMA producer; 1, 3 MMA; 2 work items (ring of four), rows of a block
+// Warps: 0 TMA producer; 1, 3 MMA; 2 work items (ring of two), rows of a block
 // behind the sequence's end set to zero (0 * NaN from a neighbour would reach
 // the accumulators), outputs of items that meet nothing; 4..7 accumulators out
 // (while the next item runs); 8..15, 16..23 elementwise. Every wait is bounded.
@@ -38,7 +38,7 @@ using namespace packed_tc;
 constexpr int BLK = 64;             // rows or keys of a streamed block
 constexpr int BT = BLK * HD * 2;    // 8 KB
 constexpr int NB = 4;               // streamed stages
-constexpr int NIT = 4;              // work item ring
+constexpr int NIT = 2;              // work item ring: an item is drawn when the one before it begins, not earlier
 constexpr int EW = 8;               // elementwise warps of a step
 constexpr int THREADS = 32 * (8 + 2 * EW);
 // TMEM columns: step parity p at 192 p: S, dP (fp32), P, dS (bf16 pairs); accumulators
@@ -360,21 +360,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
             return true;
         };
-        // S and dP run two steps ahead of the accumulations, so an item's tail may wait for its load only after
-        // the two items behind it are in the ring.
         int uses[NB];
         for (int i = 0; i < NB; i++) uses[i] = 0;
-        Item it[3];
-        bool ok = put(0, it[0]);
-        for (int i = 1; i < 3; i++) {
-            it[i].valid = 0;
-            if (ok && it[i - 1].valid) ok = put(i, it[i]);
-        }
+        Item cur, nxt;
+        bool ok = put(0, cur);
 #pragma unroll 1
-        for (int i = 0; ok && it[0].valid; i++) {
-            const int n = it[0].nb - 1, left = real(it[0], n);
-            if (left < A.bq) {
-                const int st = (it[0].base + n) % NB;
+        for (int i = 0; ok && cur.valid; i++) {
+            ok = put(i + 1, nxt);
+            const int n = cur.nb - 1, left = real(cur, n);
+            if (ok && left < A.bq) {
+                const int st = (cur.base + n) % NB;
                 int u = 0;
 #pragma unroll
                 for (int e = 0; e < NB; e++)
@@ -390,10 +385,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_full + 8 * st);
             }
-            it[0] = it[1];
-            it[1] = it[2];
-            it[2].valid = 0;
-            if (it[1].valid) ok = put(i + 3, it[2]);
+            cur = nxt;
         }
     } else if (warp >= 4 && warp < 8) {
         // ------------------------------------------------------ accumulators out

@@ -22,7 +22,7 @@
 // leaves through a swizzled staging buffer.
 //
 // Warps: 0 TMA producer; 1, 2 MMA issue for tile 0, 1 (S of the next step
-// before PV of the current one); 3 finds the work items (a ring of four in
+// before PV of the current one); 3 finds the work items (a ring of two in
 // shared memory) and zeroes the rows of a V block behind the sequence's end
 // (0 * NaN from a neighbour would reach O); 4..7 output, so that the softmax
 // warps go on with the next item (short documents spent more on the way out
@@ -35,7 +35,7 @@ namespace {
 using namespace packed_tc;
 
 constexpr int NST = 4;              // K and V stages
-constexpr int NIT = 4;              // work item ring
+constexpr int NIT = 2;              // work item ring: an item is drawn when the one before it begins, not earlier
 constexpr int SOFT = 8;             // softmax warps, four to a tile
 constexpr int THREADS = 32 * (8 + SOFT);
 constexpr int REGS_SOFT = 184, REGS_REST = 72;  // 256 * 184 + 256 * 72 = the 65536 of the launch (128 a thread)
