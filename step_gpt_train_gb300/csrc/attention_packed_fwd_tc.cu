@@ -11,15 +11,19 @@
 //
 // Persistent, one CTA per SM. Per tile and key block:
 //   S = Q K^T          tcgen05.mma M=128 N=128 K=64 into TMEM;
-//   P = exp2(S log2(e)/sqrt(hd) - m) with a per-row reference m that moves only
-//                      when the maximum grows by more than 8 (log2 units), in
-//                      fp32; back to TMEM as bf16 pairs (its one rounding);
+//   P = exp2(S log2(e)/sqrt(hd) - m) in fp32, m the row's maximum in its first
+//                      block; back to TMEM as bf16 pairs (its one rounding);
 //   O += P V           tcgen05.mma with P from TMEM as the A operand.
 // One thread per row, 128 scores in its registers: two threads per row with 64
 // each (16 softmax warps) exchanged their maxima and spent 470 instructions a
-// warp and step where this form spends about as many for twice the scores. O
-// moves with m (rarely) in TMEM; at the end of an item it is normalised and
-// leaves through a swizzled staging buffer.
+// warp and step where this form spends about as many for twice the scores.
+//
+// P, the sum l and O are floating-point numbers, precise at any scale, so m
+// needs to be the maximum only to within fp32's range: later blocks are not
+// searched for a larger one (which took a seventh of a step), and O never
+// moves. A row whose l is not between 1 and 2^40 at the end (scores that grow
+// by 28 over the first block's, infinities, NaN) is computed once more by its
+// output warp, 32 keys at a time with a running maximum.
 //
 // Warps: 0 TMA producer; 1, 2 MMA issue for tile 0, 1 (S of the next step
 // before PV of the current one); 3 finds the work items (a ring of two in
@@ -39,7 +43,7 @@ constexpr int NIT = 2;              // work item ring: an item is drawn when the
 constexpr int SOFT = 8;             // softmax warps, four to a tile
 constexpr int THREADS = 32 * (8 + SOFT);
 constexpr int REGS_SOFT = 184, REGS_REST = 72;  // 256 * 184 + 256 * 72 = the 65536 of the launch (128 a thread)
-constexpr float RESCALE = 8.f;      // log2 of the largest P before the reference max moves
+constexpr float MOST = 0x1p40f;     // sum of a row's weights up to which its first block's maximum serves
 // TMEM columns: S of tile 0, 1 | P of tile 0, 1 (bf16 pairs) | O of tile 0, 1
 constexpr uint32_t C_S = 0, C_P = 256, C_O = 384;
 // shared memory: Q [2 buffers][2 tiles] | K [NST] | V [NST] | staging per output warp | m, l | items | barriers
@@ -67,6 +71,53 @@ struct Args {
     PackedCut cut;        // pairs of tiles, key blocks of 128
     PackedPlan* plan;     // sorted items, or null: found from the offsets
 };
+
+// One row by a warp, the keys 32 at a time: lane = key for the scores, lane =
+// two dims for the output. sq: 64 floats of shared memory of this warp.
+__device__ __noinline__ void row_again(const PackedAttn& a, float scale_log2, int row, int h, int k0, int kh, int keys,
+                                       float* sq, int lane) {
+    const bf16* q = (const bf16*)a.q + (int64_t)row * a.q_stride + h * HD;
+    __syncwarp();
+    sq[lane] = to_float(q[lane]);
+    sq[32 + lane] = to_float(q[32 + lane]);
+    __syncwarp();
+    float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
+#pragma unroll 1
+    for (int j = 0; j < keys; j += 32) {
+        float s = -INFINITY;
+        if (j + lane < keys) {
+            const bf16* k = (const bf16*)a.k + (int64_t)(k0 + j + lane) * a.k_stride + kh * HD;
+            s = 0.f;
+#pragma unroll 1
+            for (int d = 0; d < HD; d += 8) {
+                float x[8];
+                load8(k + d, x);
+#pragma unroll
+                for (int e = 0; e < 8; e++) s = fmaf(sq[d + e], x[e], s);
+            }
+            s *= scale_log2;
+        }
+        const float nm = fmaxf(m, warp_max(s)), f = m == nm ? 1.f : ex2_approx(m - nm);
+        const float p = s == -INFINITY ? 0.f : ex2_approx(s - nm);
+        m = nm;
+        l = l * f + p;
+        o0 *= f;
+        o1 *= f;
+#pragma unroll 1
+        for (int e = 0; e < 32 && j + e < keys; e++) {
+            const float w = __shfl_sync(0xffffffffu, p, e);
+            const uint32_t v = *reinterpret_cast<const uint32_t*>((const bf16*)a.v + (int64_t)(k0 + j + e) * a.v_stride +
+                                                                  kh * HD + 2 * lane);
+            o0 = fmaf(w, __uint_as_float(v << 16), o0);
+            o1 = fmaf(w, __uint_as_float(v & 0xFFFF0000u), o1);
+        }
+    }
+    l = warp_sum(l);
+    const float inv = 1.f / l;
+    *reinterpret_cast<uint32_t*>((bf16*)a.o + (int64_t)row * a.o_stride + h * HD + 2 * lane) = cvt_bf16x2(o0 * inv, o1 * inv);
+    if (lane == 0) a.lse[(int64_t)h * a.total_q + row] = (m + log2f(l)) * LN2;
+    __syncwarp();
+}
 
 __global__ void __launch_bounds__(1024) packed_plan_kernel(PackedAttn a, PackedCut cut, PackedPlan* plan) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the forward's blocks may set themselves up
@@ -353,13 +404,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int64_t off = mine ? (int64_t)row * a.o_stride + (it.kh * A.group + hg) * HD : -1;
                 uint8_t* my = st + lane * 128;
                 float L = -INFINITY;
+                uint32_t again = 0;  // rows to be computed once more
                 if (n) {
                     const int d = t ? done[1]++ : done[0]++;
                     if (!(ok = wait(l_full + 8 * t, d & 1, abort_flag, status))) break;
                     const float m = ml[t * 256 + r], l = ml[t * 256 + 128 + r];
+                    const int vis = it.vis + (t ? A.qt : 0) + qi;  // keys that the row sees
+                    again = __ballot_sync(0xffffffffu, mine && vis > 0 && !(l > 0.5f && l < MOST));
                     if (!(ok = wait(o_done + 8 * t, d & 1, abort_flag, status))) break;
                     tc_fence_after();
-                    const bool some = it.vis + (t ? A.qt : 0) + qi > 0;  // the query sees a key
+                    const bool some = vis > 0;
                     const float inv = 1.f / l;
 #pragma unroll
                     for (int hh = 0; hh < 2; hh++) {
@@ -402,6 +456,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 __syncwarp();  // the staged rows have been read
                 if (mine) a.lse[(int64_t)(it.kh * A.group + hg) * a.total_q + row] = L;
+#pragma unroll 1
+                for (; again; again &= again - 1) {
+                    const int src = __ffs(again) - 1, rr = quad * 32 + src, q = rr / A.group, h = it.kh * A.group + rr - q * A.group;
+                    row_again(a, A.scale_log2, it.q0 + (t ? A.qt : 0) + q, h, it.k0, it.kh, it.vis + (t ? A.qt : 0) + q,
+                              reinterpret_cast<float*>(st), lane);
+                }
             }
         }
     } else {
@@ -409,7 +469,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int t = (warp >> 2) & 1, quad = warp & 3;
         const int r = quad * 32 + lane;  // row of the tile = TMEM lane
         const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
-        const uint32_t tS = trow + C_S + 128 * t, tP = trow + C_P + 64 * t, tO = trow + C_O + 64 * t;
+        const uint32_t tS = trow + C_S + 128 * t, tP = trow + C_P + 64 * t;
         const int qi = r / A.group;      // this row's query in the tile
         float* ml = reinterpret_cast<float*>(gbase + OFF_ML) + t * 256;
         const uint64_t scale2 = f2_pack(A.scale_log2, A.scale_log2);
@@ -449,20 +509,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                                 if (c * 32 + e >= hi) v[c][e] = 0xff800000u;
                         }
                 }
-                // From here to the stores one straight block: branches in it cost more than the work they saved
-                // (chunks that no row sees left out: 113 -> 133 us on the ragged prompts)
-                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                if (j == 0) {
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 4; c++)
+                    for (int c = 0; c < 4; c++)
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
-                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * A.scale_log2;
-                const bool move = mx > m + RESCALE;
-                const float factor = move ? ex2_approx(m - mx) : 1.f;  // 0 from -inf
-                m = move ? mx : m;
-                l *= factor;
-                const float nm = m == -INFINITY ? 0.f : -m;  // no finite score yet: every weight is 0
+                        for (int e = 0; e < 32; e += 2)
+                            m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
+                    m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * A.scale_log2;
+                }
+                const float nm = m == -INFINITY ? 0.f : -m;
                 const uint64_t nm2 = f2_pack(nm, nm);
                 uint64_t l2[4] = {0, 0, 0, 0};
                 uint32_t pk[2][32];
@@ -476,23 +532,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                         l2[(e >> 1) & 3] = f2_add(l2[(e >> 1) & 3], f2_pack(p0, p1));
                         pk[c >> 1][(c & 1) * 16 + e / 2] = cvt_bf16x2(p0, p1);
                     }
-                // PV of the previous step has finished with P and O
+                // PV of the previous step has finished with P
                 if (!(ok = wait(p_free + 8 * t, (g & 1) ^ 1u, abort_flag, status))) break;
                 tc_fence_after();
                 tc_st32(tP, pk[0]);
                 tc_st32(tP + 32, pk[1]);
                 l += f2_total(f2_add(f2_add(l2[0], l2[1]), f2_add(l2[2], l2[3])));
-                if (j > 0 && __any_sync(0xffffffffu, move)) {
-#pragma unroll
-                    for (int c = 0; c < 2; c++) {
-                        uint32_t ov[32];
-                        tc_ld32_issue(tO + 32 * c, ov);
-                        tc_ld_wait(ov);
-#pragma unroll
-                        for (int e = 0; e < 32; e++) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * factor);
-                        tc_st32(tO + 32 * c, ov);
-                    }
-                }
                 tc_st_wait();
                 tc_fence_before();
                 __syncwarp();
