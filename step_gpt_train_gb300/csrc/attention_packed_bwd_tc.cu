@@ -70,36 +70,39 @@ struct Args {
     PackedPlan* plan;
 };
 
-// Before the two kernels: blocks 0 and 1 sort their items (with plans), the
-// others form lse log2(e) and D of every (row, head), eight lanes to each, 16
-// bytes of O and dO a lane, four pairs in flight.
-constexpr int PREP = 512;  // pairs of a block of 1024 threads
-struct PrepArgs {
+// The launches of a call overlap: the sort lets the pass that forms D start at
+// once; dQ sets itself up during that pass and waits for it (which has waited
+// for the sort); dK, dV starts on the SMs that dQ leaves, since it needs
+// nothing from it, and ends after it.
+__device__ __forceinline__ void depend_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void depend_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+struct PlanArgs {
     PackedAttn a;
-    PackedAttnGrad g;
-    float2* ld;
-    int plans;
     PackedCut cut[2];
     PackedPlan* plan[2];
 };
-__global__ void __launch_bounds__(1024) packed_prep_kernel(const __grid_constant__ PrepArgs A) {
-    const PackedAttn& a = A.a;
-    if ((int)blockIdx.x < A.plans) {
-        packed_plan_block(a, A.cut[blockIdx.x], A.plan[blockIdx.x], blockIdx.x == 0);
-        return;
-    }
-    const int first = (blockIdx.x - A.plans) * PREP + threadIdx.x / 8, e = threadIdx.x % 8;
+__global__ void __launch_bounds__(1024) packed_plans_kernel(const __grid_constant__ PlanArgs A) {
+    depend_launch();
+    packed_plan_block(A.a, A.cut[blockIdx.x], A.plan[blockIdx.x], blockIdx.x == 0);
+}
+
+// lse log2(e) and D of every (row, head): eight lanes to each, 16 bytes of O
+// and dO a lane, four pairs in flight.
+constexpr int PREP = 128;  // pairs of a block
+__global__ void __launch_bounds__(256) packed_prep_kernel(PackedAttn a, PackedAttnGrad g, float2* ld) {
+    depend_launch();
+    const int first = blockIdx.x * PREP + threadIdx.x / 8, e = threadIdx.x % 8;
     uint4 x[4], y[4];
-    int row[4], h[4];
-    bool in[4];
+    int64_t at[4];
 #pragma unroll
     for (int k = 0; k < 4; k++) {
-        const int i = first + k * 128;
-        in[k] = i < a.total_q * a.Hq;
-        row[k] = in[k] ? i / a.Hq : 0;
-        h[k] = in[k] ? i - row[k] * a.Hq : 0;
-        x[k] = *reinterpret_cast<const uint4*>((const bf16*)a.o + (int64_t)row[k] * a.o_stride + h[k] * HD + e * 8);
-        y[k] = *reinterpret_cast<const uint4*>((const bf16*)A.g.dout + (int64_t)row[k] * A.g.dout_stride + h[k] * HD + e * 8);
+        const int i = first + k * 32;
+        const bool in = i < a.total_q * a.Hq;
+        const int row = in ? i / a.Hq : 0, h = in ? i - row * a.Hq : 0;
+        at[k] = in ? (int64_t)h * a.total_q + row : -1;
+        x[k] = __ldcs(reinterpret_cast<const uint4*>((const bf16*)a.o + (int64_t)row * a.o_stride + h * HD + e * 8));
+        y[k] = *reinterpret_cast<const uint4*>((const bf16*)g.dout + (int64_t)row * g.dout_stride + h * HD + e * 8);
     }
 #pragma unroll
     for (int k = 0; k < 4; k++) {
@@ -111,12 +114,12 @@ __global__ void __launch_bounds__(1024) packed_prep_kernel(const __grid_constant
                  __uint_as_float(u[j] & 0xFFFF0000u) * __uint_as_float(v[j] & 0xFFFF0000u);
 #pragma unroll
         for (int o = 4; o > 0; o /= 2) d += __shfl_xor_sync(0xffffffffu, d, o);
-        if (in[k] && e == 0) {
-            const int64_t at = (int64_t)h[k] * a.total_q + row[k];
-            const float l = a.lse[at];
-            A.ld[at] = make_float2(l == -INFINITY ? 0.f : l * LOG2E, d);
+        if (at[k] >= 0 && e == 0) {
+            const float l = a.lse[at[k]];
+            ld[at[k]] = make_float2(l == -INFINITY ? 0.f : l * LOG2E, d);
         }
     }
+    depend_wait();  // the sort too is done when this pass is
 }
 
 template <bool DQ>
@@ -137,7 +140,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t it_full = bar(NIT), it_empty = bar(NIT), a_full = bar(2), a_empty = bar(2);
     const uint32_t b_full = bar(NB), b_empty = bar(NB), b_raw = bar(NB);
     const uint32_t s_full = bar(2), dp_full = bar(2), p_full = bar(2);
-    const uint32_t ds_full = bar(2), ds_free = bar(2), acc_full = bar(1), acc_empty = bar(1), drain = bar(2);
+    const uint32_t ds_full = bar(2), ds_free = bar(2), acc_full = bar(2), acc_empty = bar(2), drain = bar(2);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(gbase + OFF_BAR + 496);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + OFF_BAR + 500);
     Item* ring = reinterpret_cast<Item*>(gbase + OFF_IT);
@@ -165,8 +168,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(b_empty + 8 * i, 1);
             mbar_init(b_raw + 8 * i, 1);
         }
-        mbar_init(acc_full, 1);
-        mbar_init(acc_empty, 4);
+        for (int i = 0; i < 2; i++) {
+            mbar_init(acc_full + 8 * i, 1);
+            mbar_init(acc_empty + 8 * i, 4);
+        }
         mbar_init(drain, 1);
         mbar_init(drain + 8, 1);
         *abort_flag = 0;
@@ -282,7 +287,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                     __syncwarp();
                 }
             } else {
-                if (!(ok = wait(acc_empty, (i & 1) ^ 1u, abort_flag, status))) break;
+                // dQ has the accumulators of two items, dK and dV those of one
+                const int b = DQ ? i & 1 : 0;
+                const uint32_t acc0 = tmem + (b ? T_ACC1 : T_ACC0);
+                if (!(ok = wait(acc_empty + 8 * b, ((DQ ? i >> 1 : i) & 1) ^ 1u, abort_flag, status))) break;
 #pragma unroll 1
                 for (int n = 0; n < it.nb; n++) {
                     const int g = it.base + n, st = g % NB, p = g & 1;
@@ -306,11 +314,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (leader) {
 #pragma unroll
                         for (int k = 0; k < BLK / 16; k++)
-                            tc_mma_ts(tmem + T_ACC0, tmem + T_STEP * p + T_DS + 8 * k, db1 + 128 * k, idesc_o,
+                            tc_mma_ts(acc0, tmem + T_STEP * p + T_DS + 8 * k, db1 + 128 * k, idesc_o,
                                       (n > 0 || k > 0) ? 1u : 0u);
                         tc_commit(ds_free + 8 * p);
                         tc_commit(b_empty + 8 * st);
-                        if (n == it.nb - 1) tc_commit(acc_full);
+                        if (n == it.nb - 1) tc_commit(acc_full + 8 * b);
                     }
                     __syncwarp();
                 }
@@ -321,6 +329,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp == 2) {
         // ------------------------------------------------------ work items, tails of blocks
         int x = blockIdx.x, steps = 0;
+        if (DQ) {
+            depend_wait();    // the sort and D are there
+            depend_launch();  // dK, dV may start where this kernel has ended
+        }
         if (DQ && blockIdx.x == 0 && !A.plan) packed_check(a, lane, 32);
         auto put = [&](int i, Item& it) -> bool {  // the next item, or the end, into ring slot i
             PackedTile p;
@@ -398,7 +410,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         bool ok = true;
 #pragma unroll 1
         for (int i = 0; ok && take(i, it); i++) {
-            if (!(ok = wait(acc_full, i & 1, abort_flag, status))) break;
+            const int b = DQ ? i & 1 : 0;
+            if (!(ok = wait(acc_full + 8 * b, (DQ ? i >> 1 : i) & 1, abort_flag, status))) break;
             tc_fence_after();
             const bool mine = qi < it.n;  // (dQ: a tile's unused last rows lie behind its n queries)
 #pragma unroll 1
@@ -407,12 +420,12 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int hh = 0; hh < 2; hh++) {
                     uint32_t v[32];
-                    tc_ld32_issue(trow + (k ? T_ACC1 : T_ACC0) + 32 * hh, v);
+                    tc_ld32_issue(trow + (k || b ? T_ACC1 : T_ACC0) + 32 * hh, v);
                     tc_ld_wait(v);
                     if (k == 0 && hh == 1) {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(acc_empty);
+                        if (lane == 0) mbar_arrive(acc_empty + 8 * b);
                     }
 #pragma unroll
                     for (int c = 0; c < 4; c++) {
@@ -448,6 +461,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t tP = trow + T_P + 16 * half, tDS = trow + T_DS + 16 * half;
         const uint64_t scale2 = f2_pack(A.scale_log2, A.scale_log2);
         // dQ: this row's query in the tile and head in the group; dK/dV: those of column 32 half + lane
+        if (DQ) depend_wait();
         const int own = DQ ? r : 32 * half + lane;
         const int qi = own / A.group, hg = own - qi * A.group;
         float* slot = reinterpret_cast<float*>(gbase + OFF_SLOT) + ew * 64;  // -lse log2(e), D of the 32 columns
@@ -558,6 +572,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     }
 
+    if (!DQ) depend_wait();  // dQ is done when dK, dV are
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -625,11 +640,17 @@ int launch_attention_packed_backward_tc(const PackedAttn& a, const PackedAttnGra
     if (smem_attr((const void*)packed_bwd_tc_kernel<true>, SMEM) != cudaSuccess ||
         smem_attr((const void*)packed_bwd_tc_kernel<false>, SMEM) != cudaSuccess)
         return GPT2_ERR_CUDA;
-    PrepArgs P = {a, g, ld, plan[0] ? 2 : 0, {cut[0], cut[1]}, {plan[0], plan[1]}};
-    const int prep = P.plans + (int)(((int64_t)a.total_q * a.Hq + PREP - 1) / PREP);
     int launches = 0;
-    if (prep) {
-        packed_prep_kernel<<<prep, 1024, 0, s>>>(P);
+    if (plan[0]) {
+        const PlanArgs P = {a, {cut[0], cut[1]}, {plan[0], plan[1]}};
+        packed_plans_kernel<<<2, 1024, 0, s>>>(P);
+        launches++;
+    }
+    if (hq) {
+        const int blocks = (int)(((int64_t)a.total_q * a.Hq + PREP - 1) / PREP);
+        // (after anything but the sort, a launch like any other: what it reads has to be complete)
+        if (!plan[0]) packed_prep_kernel<<<blocks, 256, 0, s>>>(a, g, ld);
+        else if (launch_dependent(packed_prep_kernel, blocks, 256, 0, s, a, g, ld) != cudaSuccess) return GPT2_ERR_CUDA;
         launches++;
     }
     const int sms = gpt2_num_sms();
@@ -640,10 +661,13 @@ int launch_attention_packed_backward_tc(const PackedAttn& a, const PackedAttnGra
         const int grid = A.items < sms ? A.items : sms;
         if (i == 0) {
             A.bq = BLK;
-            packed_bwd_tc_kernel<true><<<grid, THREADS, SMEM, s>>>(q128, y128, k64, v64, A);
+            if (!launches) packed_bwd_tc_kernel<true><<<grid, THREADS, SMEM, s>>>(q128, y128, k64, v64, A);
+            else if (launch_dependent(packed_bwd_tc_kernel<true>, grid, THREADS, SMEM, s, q128, y128, k64, v64, A) != cudaSuccess)
+                return GPT2_ERR_CUDA;
         } else {
             A.bq = qb;
-            packed_bwd_tc_kernel<false><<<grid, THREADS, SMEM, s>>>(k128, v128, q64, y64, A);
+            if (launch_dependent(packed_bwd_tc_kernel<false>, grid, THREADS, SMEM, s, k128, v128, q64, y64, A) != cudaSuccess)
+                return GPT2_ERR_CUDA;
         }
         launches++;
     }
