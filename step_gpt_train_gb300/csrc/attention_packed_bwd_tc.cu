@@ -509,15 +509,19 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tc_fence_after();
                 tc_ld32_issue(tS, v);
                 tc_ld_wait(v);
-                const uint64_t* nl2 = reinterpret_cast<const uint64_t*>(slot);
+                const ulonglong2* nl4 = reinterpret_cast<const ulonglong2*>(slot);  // four columns a load
                 const uint64_t nlr = f2_pack(-ld.x, -ld.x), dr = f2_pack(ld.y, ld.y);
                 float p[32];
 #pragma unroll
-                for (int c = 0; c < 32; c += 2) {
-                    float x0, x1;
-                    f2_unpack(f2_fma(f2_pack(v[c], v[c + 1]), scale2, DQ ? nlr : nl2[c / 2]), x0, x1);
+                for (int c = 0; c < 32; c += 4) {
+                    const ulonglong2 nl = DQ ? make_ulonglong2(nlr, nlr) : nl4[c / 4];
+                    float x0, x1, x2, x3;
+                    f2_unpack(f2_fma(f2_pack(v[c], v[c + 1]), scale2, nl.x), x0, x1);
+                    f2_unpack(f2_fma(f2_pack(v[c + 2], v[c + 3]), scale2, nl.y), x2, x3);
                     p[c] = ex2_approx(x0);
                     p[c + 1] = ex2_approx(x1);
+                    p[c + 2] = ex2_approx(x2);
+                    p[c + 3] = ex2_approx(x3);
                 }
                 if (cut) {
 #pragma unroll
@@ -540,19 +544,21 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!(ok = wait(dp_full + 8 * odd, ph, abort_flag, status))) break;
                 tc_fence_after();
                 uint32_t dk[16];
-                const uint64_t* d2 = reinterpret_cast<const uint64_t*>(slot + 32);
+                const ulonglong2* d4 = reinterpret_cast<const ulonglong2*>(slot + 32);
 #pragma unroll
                 for (int hh = 0; hh < 2; hh++) {
                     uint32_t w[16];
                     tc_ld16_issue(tDP + 16 * hh, w);
                     tc_ld16_wait(w);
 #pragma unroll
-                    for (int c = 0; c < 16; c += 2) {
+                    for (int c = 0; c < 16; c += 4) {
                         const int e = 16 * hh + c;
-                        float d0, d1;
-                        f2_unpack(f2_mul(f2_pack(p[e], p[e + 1]), f2_sub(f2_pack(w[c], w[c + 1]), DQ ? dr : d2[e / 2])),
-                                  d0, d1);
+                        const ulonglong2 dd = DQ ? make_ulonglong2(dr, dr) : d4[e / 4];
+                        float d0, d1, d2, d3;
+                        f2_unpack(f2_mul(f2_pack(p[e], p[e + 1]), f2_sub(f2_pack(w[c], w[c + 1]), dd.x)), d0, d1);
+                        f2_unpack(f2_mul(f2_pack(p[e + 2], p[e + 3]), f2_sub(f2_pack(w[c + 2], w[c + 3]), dd.y)), d2, d3);
                         dk[e / 2] = cvt_bf16x2(d0, d1);
+                        dk[e / 2 + 1] = cvt_bf16x2(d2, d3);
                     }
                 }
                 if (cut) {  // not 0 * NaN either
