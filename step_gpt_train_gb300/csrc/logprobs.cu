@@ -17,7 +17,6 @@ namespace {
 namespace cg = cooperative_groups;
 using namespace tc;
 
-constexpr int NT = 256;       // threads of a block
 constexpr int BATCH = 4;      // 16-byte vectors a thread has in flight
 constexpr int MAX_SPLIT = 8;  // blocks (a cluster) that share a row
 constexpr int MAX_K = 64;
@@ -154,21 +153,21 @@ __device__ __forceinline__ void part(int nv, int split, int rank, int& first, in
     last = min(first + per, nv);
 }
 
-// A row is read by `split` blocks (a cluster), 256 threads each, thread t
-// taking every 256th vector of the block's part. Top k: each thread knows its
+// A row is read by `split` blocks (a cluster), thread t of NT taking every
+// NT-th vector of the block's part. Top k: each thread knows its
 // largest logit, which gives a lower bound of the block's k-th largest; the few
 // threads that reach it have their vectors looked through again (from L2) for
 // what reaches the bound: some more than k candidates, ranked by counting. More
 // than CAND (many equal logits) are found one by one. The blocks' lists and
 // sums meet in the first block's shared memory.
-template <typename T>
+template <typename T, int NT, bool TOP>
 __global__ void __launch_bounds__(NT)
     logprobs_kernel(float* __restrict__ logp, float* __restrict__ lse, float* __restrict__ entropy,
                     float* __restrict__ top_logp, int32_t* __restrict__ top_ids, int k, const T* __restrict__ logits,
                     const int32_t* __restrict__ targets, int V, int Vp, int split, int* status) {
     __shared__ Stats ws[NT / 32], cs[MAX_SPLIT];
-    __shared__ uint64_t keys[CAND], lists[MAX_SPLIT * MAX_K];
-    __shared__ __align__(16) uint32_t maxima[NT];
+    __shared__ uint64_t keys[TOP ? CAND : 1], lists[TOP ? MAX_SPLIT * MAX_K : 1];
+    __shared__ __align__(16) uint32_t maxima[TOP ? NT : 4];
     __shared__ uint32_t bound;
     __shared__ int count;
     __shared__ float whole;  // the row's lse
@@ -236,7 +235,7 @@ __global__ void __launch_bounds__(NT)
     x = join<32>(x);
     if (lane == 0) ws[tid >> 5] = x;
     if (split > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-    static_assert(NT / 32 == 8 && MAX_SPLIT == 8, "eight lanes join the warps, and the blocks");
+    static_assert(NT / 32 <= 8 && MAX_SPLIT == 8, "eight lanes join the warps, and the blocks");
     const Stats empty = {-INFINITY, 0.f, 0.f};
     auto finish = [&](const Stats& r) {  // by the first warp
         if (lane) return;
@@ -248,16 +247,17 @@ __global__ void __launch_bounds__(NT)
     };
     auto meet = [&] {  // the warps' sums, by the first warp
         if (tid >= 32) return;
-        x = join<8>(lane < 8 ? ws[lane] : empty);
+        x = join<8>(lane < NT / 32 ? ws[lane] : empty);
         if (split == 1) finish(x);
         else if (lane == 0) *cg::this_cluster().map_shared_rank(&cs[rank], 0) = x;
     };
-    if (!k) {
+    if constexpr (!TOP) {
         __syncthreads();
         meet();
     }
 
-    if (k) {
+    if constexpr (TOP) {
+        static_assert(NT >= 4 * MAX_K && CAND == 2 * NT, "the sizes below");
         // The k-th largest of the maxima of 64 groups of four threads (of the threads for k above 32) bounds the
         // k-th largest logit from below. -inf and no data come out as the lowest.
         const bool any = v0 + tid < v1;
@@ -379,30 +379,32 @@ __global__ void __launch_bounds__(NT)
         if (rank) return;
         if (tid < 32) finish(join<8>(lane < split ? cs[lane] : empty));
     }
-    if (!k) return;
-    if (split > 1) {  // the k largest of the parts' lists
-        for (int c = tid; c < split * MAX_K; c += NT) {
-            const uint64_t q = lists[c];
-            if (!q || (c % MAX_K) >= k) continue;
-            int r = c % MAX_K;  // its own list is sorted
-            for (int s = 0; s < split; s++)
-                if (s != c / MAX_K)
-                    for (int j = 0; j < k && lists[s * MAX_K + j] > q; j++) r++;
-            if (r < k) keys[r] = q;
+    if constexpr (TOP) {
+        if (split > 1) {  // the k largest of the parts' lists
+            for (int c = tid; c < split * MAX_K; c += NT) {
+                const uint64_t q = lists[c];
+                if (!q || (c % MAX_K) >= k) continue;
+                int r = c % MAX_K;  // its own list is sorted
+                for (int s = 0; s < split; s++)
+                    if (s != c / MAX_K)
+                        for (int j = 0; j < k && lists[s * MAX_K + j] > q; j++) r++;
+                if (r < k) keys[r] = q;
+            }
         }
-    }
-    __syncthreads();
-    if (tid < k) {
-        const float L = whole;
-        const uint64_t q = keys[tid];
-        top_ids[(int64_t)row * k + tid] = key_col(q);
-        top_logp[(int64_t)row * k + tid] = L == -INFINITY ? -INFINITY : key_logit(q) - L;
+        __syncthreads();
+        if (tid < k) {
+            const float L = whole;
+            const uint64_t q = keys[tid];
+            top_ids[(int64_t)row * k + tid] = key_col(q);
+            top_logp[(int64_t)row * k + tid] = L == -INFINITY ? -INFINITY : key_logit(q) - L;
+        }
     }
 }
 
 // Row blockIdx.x, vectors part blockIdx.y of gridDim.y.
+constexpr int BNT = 256;
 template <typename T>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(BNT)
     logprobs_bwd_kernel(T* dlogits, const T* logits, const int32_t* __restrict__ targets,
                         const float* __restrict__ lse, const float* __restrict__ entropy,
                         const float* __restrict__ dlogp, const float* __restrict__ dlse,
@@ -425,14 +427,14 @@ __global__ void __launch_bounds__(NT)
     }
     const bool none = L == -INFINITY;
     const int tvec = tgt < 0 ? -1 : tgt / VEC<T>;
-    for (int i = v0 + (int)threadIdx.x; i < v1; i += BATCH * NT) {
+    for (int i = v0 + (int)threadIdx.x; i < v1; i += BATCH * BNT) {
         uint4 u[BATCH];
 #pragma unroll
         for (int e = 0; e < BATCH; e++)
-            if (i + e * NT < v1) u[e] = __ldcs(zv + i + e * NT);
+            if (i + e * BNT < v1) u[e] = __ldcs(zv + i + e * BNT);
 #pragma unroll
         for (int e = 0; e < BATCH; e++) {
-            const int v = i + e * NT;
+            const int v = i + e * BNT;
             if (v >= v1) break;
             float f[VEC<T>];
             unpack(u[e], f);
@@ -458,12 +460,12 @@ __global__ void __launch_bounds__(NT)
     }
 }
 
-template <typename T>
+template <typename T, int NT, bool TOP>
 int forward(float* logp, float* lse, float* entropy, float* top_logp, int32_t* top_ids, int k, const T* logits,
             const int32_t* targets, int N, int V, int Vp, int* status, cudaStream_t s) {
-    // as many blocks to a row as leave each SM one, and each block a batch of vectors
+    // as many blocks to a row as leave each SM one, and each thread two vectors
     int split = 1;
-    while (split < MAX_SPLIT && (int64_t)N * split * 2 <= gpt2_num_sms() && V / VEC<T> >= split * 2 * NT) split *= 2;
+    while (split < MAX_SPLIT && (int64_t)N * split * 2 <= gpt2_num_sms() && V / VEC<T> >= split * 2 * 256) split *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(N * split));
     cfg.blockDim = dim3(NT);
@@ -474,10 +476,19 @@ int forward(float* logp, float* lse, float* entropy, float* top_logp, int32_t* t
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = split > 1 ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, logprobs_kernel<T>, logp, lse, entropy, top_logp, top_ids, k, logits, targets, V, Vp,
-                           split, status) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, logprobs_kernel<T, NT, TOP>, logp, lse, entropy, top_logp, top_ids, k, logits, targets,
+                           V, Vp, split, status) != cudaSuccess)
         return GPT2_ERR_CUDA;
     return 1;
+}
+// Threads of a block: twice as many rows on their way in blocks of 128 read
+// 32768 rows of 50257 at the speed of a copy (496 us; 535 with 256), but few
+// rows, and the search for alternatives, want the wider block (2043 rows with
+// 20: 60 us; 67 with 128).
+template <typename T, typename... A>
+int forward_of(int k, int N, A... args) {
+    if (k) return forward<T, 256, true>(args...);
+    return N > gpt2_num_sms() ? forward<T, 128, false>(args...) : forward<T, 256, false>(args...);
 }
 
 template <typename T>
@@ -485,8 +496,8 @@ int backward(T* dlogits, const T* logits, const int32_t* targets, const float* l
              const float* dlogp, const float* dlse, const float* dentropy, int N, int V, int Vp, int* status,
              cudaStream_t s) {
     int split = 1;
-    while ((int64_t)N * split < 4 * gpt2_num_sms() && Vp / VEC<T> > split * BATCH * NT) split *= 2;
-    logprobs_bwd_kernel<T><<<dim3(N, split), NT, 0, s>>>(dlogits, logits, targets, lse, entropy, dlogp, dlse, dentropy,
+    while ((int64_t)N * split < 4 * gpt2_num_sms() && Vp / VEC<T> > split * BATCH * BNT) split *= 2;
+    logprobs_bwd_kernel<T><<<dim3(N, split), BNT, 0, s>>>(dlogits, logits, targets, lse, entropy, dlogp, dlse, dentropy,
                                                          V, Vp, status);
     return 1;
 }
@@ -497,8 +508,10 @@ int launch_token_logprobs(int dtype, float* logp, float* lse, float* entropy, fl
                           int k, const void* logits, const int32_t* targets, int N, int V, int Vp, int* status,
                           cudaStream_t s) {
     if (dtype == GPT2_MODE_BF16)
-        return forward(logp, lse, entropy, top_logp, top_ids, k, (const bf16*)logits, targets, N, V, Vp, status, s);
-    return forward(logp, lse, entropy, top_logp, top_ids, k, (const float*)logits, targets, N, V, Vp, status, s);
+        return forward_of<bf16>(k, N, logp, lse, entropy, top_logp, top_ids, k, (const bf16*)logits, targets, N, V, Vp,
+                                status, s);
+    return forward_of<float>(k, N, logp, lse, entropy, top_logp, top_ids, k, (const float*)logits, targets, N, V, Vp,
+                             status, s);
 }
 
 int launch_token_logprobs_backward(int dtype, void* dlogits, const void* logits, const int32_t* targets,
