@@ -3,19 +3,23 @@
 //
 // Rows are a key head's queries x the heads of its group, in this order, so
 // shared heads share the K and V blocks (and their sums dK, dV lie inside the
-// products). A block of 128 threads takes 64 rows (forward, dQ) or 64 keys
+// products). A block of 256 threads takes 64 rows (forward, dQ) or 64 keys
 // (dK, dV) against blocks of 64 of the others, all in shared memory; thread
-// (ty, tx) of 16 x 8 holds rows ty + 16 r and columns tx + 8 c of the 64 x 64
+// (ty, tx) of 16 x 16 holds rows ty + 16 r and columns tx + 16 c of the 64 x 64
 // scores. Scores are dot products over 16-byte pieces of both rows, products
-// with P or dS walk 16-byte pieces of a P row: either way 12 shared 16-byte
-// loads feed 128 FMA a thread, and the row padding of four floats keeps the
-// eight rows or columns that a warp reads at once in different banks.
-// Gradients have one writer each: deterministic.
+// with P or dS walk 16-byte pieces of a P row: either way 8 shared 16-byte
+// loads feed 64 FMA a thread, and the row padding of four floats spreads the
+// rows that a warp reads at once over the banks. (128 threads with twice the
+// columns load a quarter less and took as long: 93 against 92 us on 16
+// documents of 3582 tokens, where the FMA of the tiles, the masked halves of
+// the diagonal ones included, take 33 and all instructions 51; the rest is the
+// blocks' unequal lengths.) Gradients have one writer each: deterministic.
 #include "attention_packed.cuh"
 
 namespace {
 
-constexpr int TL = 64, NT = 128;
+constexpr int TL = 64, NT = 256;
+constexpr int TX = 16, NC = TL / TX, NR = 4;  // threads of a row, their columns; rows of a thread
 constexpr int LP = TL + 4;  // floats of a P row
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
@@ -28,10 +32,11 @@ struct Args {
 
 template <int HD> struct Shape {
     static constexpr int LD = HD + 4;  // floats of an operand's row
-    static constexpr int DV = HD / 8;  // output columns of a thread
+    static constexpr int DV = HD / TX > 1 ? HD / TX : 1;  // output columns of a thread
     static constexpr int T = TL * LD;  // floats of a tile
-    // output column of element e
-    static __device__ __forceinline__ int col(int tx, int e) { return HD >= 32 ? e / 4 * 32 + tx * 4 + e % 4 : tx * DV + e; }
+    // output column of element e (HD 8: the upper half of the threads doubles the lower)
+    static __device__ __forceinline__ int col(int tx, int e) { return HD < TX ? tx % HD : tx * DV + e; }
+    static __device__ __forceinline__ bool writes(int tx) { return HD >= TX || tx < HD; }
 };
 
 // Rows [0, n) of a tile from src(row), the rest zero.
@@ -47,23 +52,23 @@ template <int HD, typename F> __device__ __forceinline__ void load_tile(float* d
 }
 
 // s[r][c] = A row (ty + 16 r) . B row (tx + 8 c)
-template <int HD> __device__ __forceinline__ void dots(float (&s)[4][8], const float* A, const float* B, int ty, int tx) {
+template <int HD> __device__ __forceinline__ void dots(float (&s)[NR][NC], const float* A, const float* B, int ty, int tx) {
     constexpr int LD = Shape<HD>::LD;
 #pragma unroll
     for (int r = 0; r < 4; r++)
 #pragma unroll
-        for (int c = 0; c < 8; c++) s[r][c] = 0.f;
+        for (int c = 0; c < NC; c++) s[r][c] = 0.f;
 #pragma unroll 2
     for (int d = 0; d < HD; d += 4) {
-        float4 x[4], y[8];
+        float4 x[NR], y[NC];
 #pragma unroll
         for (int r = 0; r < 4; r++) x[r] = *reinterpret_cast<const float4*>(A + (ty + 16 * r) * LD + d);
 #pragma unroll
-        for (int c = 0; c < 8; c++) y[c] = *reinterpret_cast<const float4*>(B + (tx + 8 * c) * LD + d);
+        for (int c = 0; c < NC; c++) y[c] = *reinterpret_cast<const float4*>(B + (tx + TX * c) * LD + d);
 #pragma unroll
         for (int r = 0; r < 4; r++)
 #pragma unroll
-            for (int c = 0; c < 8; c++)
+            for (int c = 0; c < NC; c++)
                 s[r][c] = fmaf(x[r].w, y[c].w, fmaf(x[r].z, y[c].z, fmaf(x[r].y, y[c].y, fmaf(x[r].x, y[c].x, s[r][c]))));
     }
 }
@@ -84,10 +89,10 @@ __device__ __forceinline__ void products(float (&o)[4][Shape<HD>::DV], const flo
         for (int k = 0; k < 4; k++) {
             const float* b = B + (j + k) * LD;
             float v[DV];
-            if constexpr (HD >= 32) {
-#pragma unroll
-                for (int e = 0; e < DV; e += 4)
-                    *reinterpret_cast<float4*>(v + e) = *reinterpret_cast<const float4*>(b + Shape<HD>::col(tx, e));
+            if constexpr (DV == 4) {
+                *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(b + Shape<HD>::col(tx, 0));
+            } else if constexpr (DV == 2) {
+                *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(b + Shape<HD>::col(tx, 0));
             } else {
 #pragma unroll
                 for (int e = 0; e < DV; e++) v[e] = b[Shape<HD>::col(tx, e)];
@@ -99,21 +104,21 @@ __device__ __forceinline__ void products(float (&o)[4][Shape<HD>::DV], const flo
         }
     }
 }
-__device__ __forceinline__ void put(float* P, const float (&s)[4][8], int ty, int tx) {
+__device__ __forceinline__ void put(float* P, const float (&s)[NR][NC], int ty, int tx) {
 #pragma unroll
     for (int r = 0; r < 4; r++)
 #pragma unroll
-        for (int c = 0; c < 8; c++) P[(ty + 16 * r) * LP + tx + 8 * c] = s[r][c];
+        for (int c = 0; c < NC; c++) P[(ty + 16 * r) * LP + tx + TX * c] = s[r][c];
 }
-// Over the eight threads of a row.
+// Over the threads of a row.
 __device__ __forceinline__ float row_max(float v) {
 #pragma unroll
-    for (int o = 4; o > 0; o /= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = TX / 2; o > 0; o /= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
 __device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
-    for (int o = 4; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = TX / 2; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
@@ -149,7 +154,7 @@ template <int HD> __global__ void __launch_bounds__(NT) packed_fwd_f32_kernel(co
     const PackedAttn& a = A.a;
     extern __shared__ __align__(16) float sm[];
     float *sq = sm, *sk = sm + S::T, *sv = sk + S::T, *sp = sv + S::T;
-    const int tid = threadIdx.x, tx = tid % 8, ty = tid / 8;
+    const int tid = threadIdx.x, tx = tid % TX, ty = tid / TX;
     if (blockIdx.x == 0) packed_check(a, tid, NT);
     PackedSeq p;
     int kh, at;
@@ -187,14 +192,14 @@ template <int HD> __global__ void __launch_bounds__(NT) packed_fwd_f32_kernel(co
         load_v(j);
         cp_async_wait<1>();  // K (and Q)
         __syncthreads();
-        float s[4][8];
+        float s[NR][NC];
         dots<HD>(s, sq, sk, ty, tx);
 #pragma unroll
         for (int r = 0; r < 4; r++) {
             float mx = m[r];
 #pragma unroll
-            for (int c = 0; c < 8; c++) {
-                s[r][c] = j + tx + 8 * c < vis[r] ? s[r][c] * A.scale_log2 : -INFINITY;
+            for (int c = 0; c < NC; c++) {
+                s[r][c] = j + tx + TX * c < vis[r] ? s[r][c] * A.scale_log2 : -INFINITY;
                 mx = fmaxf(mx, s[r][c]);
             }
             mx = row_max(mx);
@@ -202,7 +207,7 @@ template <int HD> __global__ void __launch_bounds__(NT) packed_fwd_f32_kernel(co
             m[r] = mx;
             float sum = 0.f;
 #pragma unroll
-            for (int c = 0; c < 8; c++) {
+            for (int c = 0; c < NC; c++) {
                 s[r][c] = ex2_approx(s[r][c] - ref);
                 sum += s[r][c];
             }
@@ -224,7 +229,8 @@ template <int HD> __global__ void __launch_bounds__(NT) packed_fwd_f32_kernel(co
         if (i < n) {
             float* out = const_cast<float*>(rows.at(a.o, a.o_stride, HD, at + i));
 #pragma unroll
-            for (int e = 0; e < S::DV; e++) out[S::col(tx, e)] = vis[r] > 0 ? o[r][e] * inv : 0.f;
+            for (int e = 0; e < S::DV; e++)
+                if (S::writes(tx)) out[S::col(tx, e)] = vis[r] > 0 ? o[r][e] * inv : 0.f;
             if (tx == 0) a.lse[rows.stat(a.total_q, at + i)] = vis[r] > 0 ? (m[r] + log2f(sum)) * LN2 : -INFINITY;
         }
     }
@@ -236,7 +242,7 @@ template <int HD> __global__ void __launch_bounds__(NT) packed_dq_f32_kernel(con
     const PackedAttn& a = A.a;
     extern __shared__ __align__(16) float sm[];
     float *sq = sm, *sy = sm + S::T, *sk = sy + S::T, *sv = sk + S::T, *sp = sv + S::T;
-    const int tid = threadIdx.x, tx = tid % 8, ty = tid / 8;
+    const int tid = threadIdx.x, tx = tid % TX, ty = tid / TX;
     if (blockIdx.x == 0) packed_check(a, tid, NT);
     PackedSeq p;
     int kh, at;
@@ -258,7 +264,8 @@ template <int HD> __global__ void __launch_bounds__(NT) packed_dq_f32_kernel(con
         if (i < n) {
             const float* o = rows.at(a.o, a.o_stride, HD, at + i);
 #pragma unroll
-            for (int e = 0; e < S::DV; e++) d += o[S::col(tx, e)] * sy[i * S::LD + S::col(tx, e)];
+            for (int e = 0; e < S::DV; e++)
+                if (S::writes(tx)) d += o[S::col(tx, e)] * sy[i * S::LD + S::col(tx, e)];
             if (vis[r] > 0) lse2[r] = a.lse[rows.stat(a.total_q, at + i)] * LOG2E;
         }
         D[r] = row_sum(d);
@@ -273,7 +280,7 @@ template <int HD> __global__ void __launch_bounds__(NT) packed_dq_f32_kernel(con
         load_tile<HD>(sv, nk, [&](int r) { return (const float*)a.v + (int64_t)(p.k0 + j + r) * a.v_stride + kh * HD; });
         cp_async_wait<1>();
         __syncthreads();
-        float s[4][8], dp[4][8];
+        float s[NR][NC], dp[NR][NC];
         dots<HD>(s, sq, sk, ty, tx);
         cp_async_wait<0>();
         __syncthreads();
@@ -281,8 +288,8 @@ template <int HD> __global__ void __launch_bounds__(NT) packed_dq_f32_kernel(con
 #pragma unroll
         for (int r = 0; r < 4; r++)
 #pragma unroll
-            for (int c = 0; c < 8; c++)
-                s[r][c] = j + tx + 8 * c < vis[r] ? ex2_approx(fmaf(s[r][c], A.scale_log2, -lse2[r])) * (dp[r][c] - D[r])
+            for (int c = 0; c < NC; c++)
+                s[r][c] = j + tx + TX * c < vis[r] ? ex2_approx(fmaf(s[r][c], A.scale_log2, -lse2[r])) * (dp[r][c] - D[r])
                                                   : 0.f;
         put(sp, s, ty, tx);
         __syncthreads();
@@ -295,7 +302,8 @@ template <int HD> __global__ void __launch_bounds__(NT) packed_dq_f32_kernel(con
         if (i >= n) continue;
         float* out = const_cast<float*>(rows.at(A.g.dq, A.g.dq_stride, HD, at + i));
 #pragma unroll
-        for (int e = 0; e < S::DV; e++) out[S::col(tx, e)] = dq[r][e] * A.scale;
+        for (int e = 0; e < S::DV; e++)
+            if (S::writes(tx)) out[S::col(tx, e)] = dq[r][e] * A.scale;
     }
 }
 
@@ -306,7 +314,7 @@ template <int HD> __global__ void __launch_bounds__(NT) packed_dkdv_f32_kernel(c
     extern __shared__ __align__(16) float sm[];
     float *sk = sm, *sv = sm + S::T, *sq = sv + S::T, *sy = sq + S::T, *sp = sy + S::T, *sd = sp + TL * LP;
     float* stat = sd + TL * LP;  // lse log2(e), D of the block's rows
-    const int tid = threadIdx.x, tx = tid % 8, ty = tid / 8;
+    const int tid = threadIdx.x, tx = tid % TX, ty = tid / TX;
     if (a.total_q == 0 && blockIdx.x == 0) packed_check(a, tid, NT);
     const int slot = blockIdx.x / a.Hkv, kh = blockIdx.x - slot * a.Hkv;
     int first;
@@ -340,12 +348,12 @@ template <int HD> __global__ void __launch_bounds__(NT) packed_dkdv_f32_kernel(c
         }
         cp_async_wait<0>();
         __syncthreads();
-        float s[4][8], dp[4][8];
+        float s[NR][NC], dp[NR][NC];
         dots<HD>(s, sk, sq, ty, tx);
         dots<HD>(dp, sv, sy, ty, tx);
 #pragma unroll
-        for (int c = 0; c < 8; c++) {
-            const int row = tx + 8 * c;
+        for (int c = 0; c < NC; c++) {
+            const int row = tx + TX * c;
             // keys below this are seen
             const int seen = row < n ? (i + row) / A.group + 1 + off - at : 0;
             const float L = stat[row], D = stat[TL + row];
@@ -373,6 +381,7 @@ template <int HD> __global__ void __launch_bounds__(NT) packed_dkdv_f32_kernel(c
         float* ov = (float*)A.g.dv + row * A.g.dv_stride + kh * HD;
 #pragma unroll
         for (int e = 0; e < S::DV; e++) {
+            if (!S::writes(tx)) continue;
             ok[S::col(tx, e)] = dk[r][e] * A.scale;
             ov[S::col(tx, e)] = dv[r][e];
         }
