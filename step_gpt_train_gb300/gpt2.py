@@ -419,21 +419,34 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+_torch = None  # imported with the first op: an import statement in every call costs more than a small kernel's launch
+
+
+def _tc():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _s(stream):
     if stream is None:
-        import torch
-        stream = torch.cuda.current_stream()
+        c = _tc()._C
+        try:  # current_stream().cuda_stream without the object made for it
+            return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+        except AttributeError:
+            stream = _torch.cuda.current_stream()
     return stream.cuda_stream
 
 
 def _dtype_of(t) -> int:
-    import torch
-    return MODE_BF16 if t.dtype == torch.bfloat16 else MODE_FP32
+    return MODE_BF16 if t.dtype == _tc().bfloat16 else MODE_FP32
 
 
 def _scratch(nbytes: int):
-    import torch
-    return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device="cuda")
+    t = _tc()
+    return t.empty(max(int(nbytes), 256), dtype=t.uint8, device="cuda")
 
 
 def gpt2_op_encoder_forward(x0, tokens, wte, wpe, V, status=None, stream=None):
@@ -595,9 +608,20 @@ def gpt2_op_attention_backward(dqkv, dout, qkv, o, lse, B, T, H, stream=None):
 
 def _rows(t, what):
     """Row stride of a [rows, heads, hd] tensor whose heads are contiguous in a row."""
-    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-        raise ValueError(f"{what}: a [rows, heads, hd] tensor with the heads of a row contiguous is needed")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    shape = t.shape
+    if len(shape) == 3:
+        rows, heads, hd = shape
+        s0, s1, s2 = t.stride()
+        if s2 == 1 and (s1 == hd or heads <= 1):
+            return s0 if rows > 1 else heads * hd
+    raise ValueError(f"{what}: a [rows, heads, hd] tensor with the heads of a row contiguous is needed")
+
+
+def _sequences(cu_q, cu_k):
+    n = cu_q.shape[0] - 1
+    if cu_k is not cu_q and cu_k.shape[0] - 1 != n:
+        raise ValueError("cu_q and cu_k need the same number of sequences")
+    return n
 
 
 def gpt2_op_attention_packed_forward(o, lse, q, k, v, cu_q, cu_k, max_q, max_k, status=None, stream=None):
@@ -607,15 +631,14 @@ def gpt2_op_attention_packed_forward(o, lse, q, k, v, cu_q, cu_k, max_q, max_k, 
     lib = load_library()
     dt = _dtype_of(q)
     tq, hq, hd = q.shape
-    tk, hkv = k.shape[0], k.shape[1]
-    if cu_k.numel() != cu_q.numel():
-        raise ValueError("cu_q and cu_k need the same number of sequences")
-    n = cu_q.numel() - 1
+    tk, hkv, _ = k.shape
+    n = _sequences(cu_q, cu_k)
     nb = lib.gpt2_op_attention_packed_forward_scratch(dt, n, tq, tk, max_q, max_k, hq, hkv, hd)
     sc = _scratch(nb) if nb else None
-    check(lib.gpt2_op_attention_packed_forward(dt, _p(o), _rows(o, "o"), _p(lse), _p(q), _rows(q, "q"), _p(k),
-                                               _rows(k, "k"), _p(v), _rows(v, "v"), _p(cu_q), _p(cu_k), n, tq, tk,
-                                               max_q, max_k, hq, hkv, hd, _p(sc), nb, _p(status), _s(stream)),
+    check(lib.gpt2_op_attention_packed_forward(dt, o.data_ptr(), _rows(o, "o"), lse.data_ptr(), q.data_ptr(),
+                                               _rows(q, "q"), k.data_ptr(), _rows(k, "k"), v.data_ptr(),
+                                               _rows(v, "v"), cu_q.data_ptr(), cu_k.data_ptr(), n, tq, tk, max_q,
+                                               max_k, hq, hkv, hd, _p(sc), nb, _p(status), _s(stream)),
           "gpt2_op_attention_packed_forward")
     return sc
 
@@ -626,17 +649,16 @@ def gpt2_op_attention_packed_backward(dq, dk, dv, dout, q, k, v, o, lse, cu_q, c
     lib = load_library()
     dt = _dtype_of(q)
     tq, hq, hd = q.shape
-    tk, hkv = k.shape[0], k.shape[1]
-    if cu_k.numel() != cu_q.numel():
-        raise ValueError("cu_q and cu_k need the same number of sequences")
-    n = cu_q.numel() - 1
+    tk, hkv, _ = k.shape
+    n = _sequences(cu_q, cu_k)
     nb = lib.gpt2_op_attention_packed_backward_scratch(dt, n, tq, tk, hq, hkv, hd)
     sc = _scratch(nb)
-    check(lib.gpt2_op_attention_packed_backward(dt, _p(dq), _rows(dq, "dq"), _p(dk), _rows(dk, "dk"), _p(dv),
-                                                _rows(dv, "dv"), _p(dout), _rows(dout, "dout"), _p(q), _rows(q, "q"),
-                                                _p(k), _rows(k, "k"), _p(v), _rows(v, "v"), _p(o), _rows(o, "o"),
-                                                _p(lse), _p(cu_q), _p(cu_k), n, tq, tk, max_q, max_k, hq, hkv, hd,
-                                                _p(sc), sc.numel(), _p(status), _s(stream)),
+    check(lib.gpt2_op_attention_packed_backward(dt, dq.data_ptr(), _rows(dq, "dq"), dk.data_ptr(), _rows(dk, "dk"),
+                                                dv.data_ptr(), _rows(dv, "dv"), dout.data_ptr(), _rows(dout, "dout"),
+                                                q.data_ptr(), _rows(q, "q"), k.data_ptr(), _rows(k, "k"),
+                                                v.data_ptr(), _rows(v, "v"), o.data_ptr(), _rows(o, "o"),
+                                                lse.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(), n, tq, tk, max_q,
+                                                max_k, hq, hkv, hd, sc.data_ptr(), nb, _p(status), _s(stream)),
           "gpt2_op_attention_packed_backward")
     return sc
 
