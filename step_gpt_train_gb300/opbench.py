@@ -302,6 +302,61 @@ def main(argv=None):
 
     ops["classifier"] = (classifier, N * (2.0 * Vp * 2 + 8), "byte")
 
+    # Packed documents: N tokens cut into lengths of T down to T / 8, in the fused qkv buffer of the model.
+    def documents():
+        lens, left = [], N
+        while left:
+            lens.append(min(left, T >> (len(lens) % 4)))
+            left -= lens[-1]
+        cu = torch.tensor([0] + lens, device=dev).cumsum(0).int()
+        return lens, cu
+
+    def packed(backward):
+        def setup():
+            lens, cu = documents()
+            heads = lambda x, i: x[:, i * C:(i + 1) * C].unflatten(1, (H, C // H))  # noqa: E731
+            qkv, do = rnd(N, 3 * C), rnd(N, H, C // H)
+            q, k, v = (heads(qkv, i) for i in range(3))
+            o, lse = torch.empty(N, H, C // H, device=dev, dtype=bf), torch.empty(H, N, device=dev)
+            dqkv = torch.empty_like(qkv)
+            fwd = lambda: g.gpt2_op_attention_packed_forward(o, lse, q, k, v, cu, cu, T, T)  # noqa: E731
+            if not backward:
+                return fwd
+            fwd()
+            return lambda: g.gpt2_op_attention_packed_backward(*(heads(dqkv, i) for i in range(3)), do, q, k, v, o, lse,
+                                                               cu, cu, T, T)
+        return setup
+
+    packed_flops = 2.0 * C * sum(x * (x + 1) for x in documents()[0])
+    ops["attention_packed_fwd"] = (packed(False), packed_flops, "flop")
+    ops["attention_packed_bwd"] = (packed(True), 2.5 * packed_flops, "flop")
+
+    def new_tokens():  # one token each for B sequences over caches of T keys
+        q, k, v = rnd(B, H, C // H), rnd(N, H, C // H), rnd(N, H, C // H)
+        o, lse = torch.empty_like(q), torch.empty(H, B, device=dev)
+        cq, ck = (torch.arange(B + 1, device=dev, dtype=torch.int32) * n for n in (1, T))
+        return lambda: g.gpt2_op_attention_packed_forward(o, lse, q, k, v, cq, ck, 1, T)
+
+    ops["attention_packed_new_tokens"] = (new_tokens, 4.0 * N * C, "byte")
+
+    def logprobs(top, backward):
+        def setup():
+            z, tgt = rnd(N, Vp, std=2.0), torch.randint(0, V, (N,), device=dev, dtype=torch.int32)
+            logp, lse, ent = (torch.empty(N, device=dev) for _ in range(3))
+            tl, ti = ((torch.empty(N, top, device=dev), torch.empty(N, top, device=dev, dtype=torch.int32)) if top
+                      else (None, None))
+            fwd = lambda: g.gpt2_op_token_logprobs(logp, lse, ent, z, tgt, V, top_logp=tl, top_ids=ti)  # noqa: E731
+            if not backward:
+                return fwd
+            fwd()
+            dz = torch.empty_like(z)
+            return lambda: g.gpt2_op_token_logprobs_backward(dz, z, tgt, lse, ent, V, dlogp=logp, dentropy=ent)
+        return setup
+
+    ops["token_logprobs"] = (logprobs(0, False), N * 2.0 * V, "byte")
+    ops["token_logprobs_top20"] = (logprobs(20, False), N * 2.0 * V, "byte")
+    ops["token_logprobs_bwd"] = (logprobs(0, True), N * 2.0 * (V + Vp), "byte")
+
     def adamw():
         n = 124_475_904
         th, gr, m, v = (torch.randn(n, device=dev) for _ in range(4))
