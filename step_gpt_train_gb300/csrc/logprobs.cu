@@ -63,10 +63,10 @@ __device__ __forceinline__ float max_nan(float a, float b, float c) {
     return d;
 }
 
-// A logit's place in the order (larger logits larger, -0 as 0) above its
-// column's (lower columns larger): unique within a row, never 0.
+// A logit's place in the order (larger logits larger, -0 as 0, NaN largest)
+// above its column's (lower columns larger): unique within a row, neither 0 nor ~0.
 __device__ __forceinline__ uint64_t order_key(float z, int col) {
-    const int b = __float_as_int(z + 0.f);
+    const int b = z != z ? 0x7FFFFFFE : __float_as_int(z + 0.f);
     const uint32_t u = (uint32_t)(b < 0 ? ~b : b ^ 0x80000000);
     return ((uint64_t)u << 32) | (uint32_t)~col;
 }
@@ -153,13 +153,84 @@ __device__ __forceinline__ void part(int nv, int split, int rank, int& first, in
     last = min(first + per, nv);
 }
 
+// Whole vectors into x.
+template <typename T, int N> __device__ __forceinline__ void add_batch(const uint4 (&u)[N], Stats& x) {
+    float f[N * VEC<T>];
+#pragma unroll
+    for (int b = 0; b < N; b++) {
+        float g[VEC<T>];
+        unpack(u[b], g);
+#pragma unroll
+        for (int j = 0; j < VEC<T>; j++) f[b * VEC<T> + j] = g[j];
+    }
+    raise(f, x);
+    const Stats was = x;
+    const bool near = fabsf(x.m) < 1e4f;
+    if (near) add_values<true>(f, x);
+    if (!near || x.t != x.t) {
+        x = was;
+        add_values<false>(f, x);
+    }
+}
+// Vector v, which V may cut.
+template <typename T> __device__ __forceinline__ void add_vector(const uint4& u, int v, int V, Stats& x) {
+    float f[VEC<T>];
+    unpack(u, f);
+#pragma unroll
+    for (int j = 0; j < VEC<T>; j++)
+        if (v * VEC<T> + j >= V) f[j] = -INFINITY;
+    raise(f, x);
+    add_values<false>(f, x);
+}
+
+// The first columns of vectors [v0, v1) whose logits are at the bound itself, by a warp: behind the n places of
+// out that are taken, up to k. Returns the places taken then.
+template <typename T>
+__device__ __forceinline__ int add_equal(const uint4* zv, int v0, int v1, int V, uint32_t bound, int n, int k,
+                                         uint64_t* out) {
+    const int lane = threadIdx.x & 31;
+    for (; n < k && v0 < v1; v0 += 32) {
+        const int v = v0 + lane;
+        uint64_t q[VEC<T>];
+        float g[VEC<T>];
+        unpack(v < v1 ? __ldg(zv + v) : make_uint4(0, 0, 0, 0), g);
+        int own = 0;
+#pragma unroll
+        for (int j = 0; j < VEC<T>; j++) {
+            q[j] = order_key(g[j], v * VEC<T> + j);
+            if ((uint32_t)(q[j] >> 32) != bound || v >= v1 || v * VEC<T> + j >= V) q[j] = 0;
+            own += q[j] != 0;
+        }
+        int to = own;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int y = __shfl_up_sync(0xffffffffu, to, o);
+            if (lane >= o) to += y;
+        }
+        const int all = __shfl_sync(0xffffffffu, to, 31);
+        to += n - own;
+#pragma unroll
+        for (int j = 0; j < VEC<T>; j++)
+            if (q[j]) {
+                if (to < k) out[to] = q[j];
+                to++;
+            }
+        n += all;
+    }
+    return min(n, k);
+}
+
 // A row is read by `split` blocks (a cluster), thread t of NT taking every
 // NT-th vector of the block's part. Top k: each thread knows its
 // largest logit, which gives a lower bound of the block's k-th largest; the few
 // threads that reach it have their vectors looked through again (from L2) for
 // what reaches the bound: some more than k candidates, ranked by counting. More
-// than CAND (many equal logits) are found one by one. The blocks' lists and
-// sums meet in the first block's shared memory.
+// than CAND are equal logits at the bound, as in a row with fewer than k tokens
+// left unmasked: those above it are found in the same way, then the first
+// columns at it (4096 rows with all but 5 masked: 95 us; taken one by one
+// 1670). Only where CAND are above it (a row that rises, its largest logits all
+// in a few threads) are they taken one by one. The blocks' lists and sums meet
+// in the first block's shared memory.
 template <typename T, int NT, bool TOP>
 __global__ void __launch_bounds__(NT)
     logprobs_kernel(float* __restrict__ logp, float* __restrict__ lse, float* __restrict__ entropy,
@@ -196,22 +267,7 @@ __global__ void __launch_bounds__(NT)
         uint4 u[BATCH];
 #pragma unroll
         for (int b = 0; b < BATCH; b++) u[b] = __ldg(zv + i + b * NT);
-        float f[BATCH * VEC<T>];
-#pragma unroll
-        for (int b = 0; b < BATCH; b++) {
-            float g[VEC<T>];
-            unpack(u[b], g);
-#pragma unroll
-            for (int j = 0; j < VEC<T>; j++) f[b * VEC<T> + j] = g[j];
-        }
-        raise(f, x);
-        const Stats was = x;
-        const bool near = fabsf(x.m) < 1e4f;
-        if (near) add_values<true>(f, x);
-        if (!near || x.t != x.t) {
-            x = was;
-            add_values<false>(f, x);
-        }
+        add_batch<T>(u, x);
     }
     {  // the rest, BATCH vectors at most, with the one that V cuts
         uint4 u[BATCH];
@@ -219,17 +275,8 @@ __global__ void __launch_bounds__(NT)
         for (int b = 0; b < BATCH; b++)
             if (i + b * NT < v1) u[b] = __ldg(zv + i + b * NT);
 #pragma unroll
-        for (int b = 0; b < BATCH; b++) {
-            const int v = i + b * NT;
-            if (v >= v1) break;
-            float f[VEC<T>];
-            unpack(u[b], f);
-#pragma unroll
-            for (int j = 0; j < VEC<T>; j++)
-                if (v * VEC<T> + j >= V) f[j] = -INFINITY;
-            raise(f, x);
-            add_values<false>(f, x);
-        }
+        for (int b = 0; b < BATCH; b++)
+            if (i + b * NT < v1) add_vector<T>(u[b], i + b * NT, V, x);
     }
     const float mine = x.m;  // this thread's largest logit
     x = join<32>(x);
@@ -293,45 +340,57 @@ __global__ void __launch_bounds__(NT)
                     if (v * VEC<T> + j < V) f(order_key(g[j], v * VEC<T> + j));
             }
         };
-        // the vectors of each thread whose maximum reaches the bound, by its whole warp, one to a lane, four
-        // threads' at a time
+        // The logits that reach the bound: the vectors of each thread whose maximum does, by its whole warp, one to a
+        // lane, four threads' at a time. Where many are at the bound (more than CAND, or half a warp's threads), those
+        // above it, and the first columns at it after them.
         constexpr int HOT = 4;
-        for (uint32_t hot = __ballot_sync(0xffffffffu, any && key >= least); hot;) {
-            int v[HOT];
-#pragma unroll
-            for (int h = 0; h < HOT; h++) {
-                v[h] = hot ? v0 + (tid & ~31) + __ffs(hot) - 1 + lane * NT : v1;
-                hot &= hot - 1;
+        bool equal = false;
+        for (uint32_t from = least;; from++) {
+            uint32_t hot = __ballot_sync(0xffffffffu, any && key >= from);
+            if (!equal && __popc(hot) > 16) {
+                hot = 0;
+                if (lane == 0) atomicAdd(&count, CAND + 1);
             }
-            while (__any_sync(0xffffffffu, min(min(v[0], v[1]), min(v[2], v[3])) < v1)) {
-                uint4 u[HOT];
-#pragma unroll
-                for (int h = 0; h < HOT; h++)
-                    if (v[h] < v1) u[h] = __ldg(zv + v[h]);
+            while (hot) {
+                int v[HOT];
 #pragma unroll
                 for (int h = 0; h < HOT; h++) {
-                    if (v[h] >= v1) continue;
-                    float g[VEC<T>];
-                    unpack(u[h], g);
+                    v[h] = hot ? v0 + (tid & ~31) + __ffs(hot) - 1 + lane * NT : v1;
+                    hot &= hot - 1;
+                }
+                while (__any_sync(0xffffffffu, min(min(v[0], v[1]), min(v[2], v[3])) < v1)) {
+                    uint4 u[HOT];
 #pragma unroll
-                    for (int j = 0; j < VEC<T>; j++) {
-                        const uint64_t q = order_key(g[j], v[h] * VEC<T> + j);
-                        if ((uint32_t)(q >> 32) >= least && v[h] * VEC<T> + j < V) {
-                            const int at = atomicAdd(&count, 1);
-                            if (at < CAND) keys[at] = q;
+                    for (int h = 0; h < HOT; h++)
+                        if (v[h] < v1) u[h] = __ldg(zv + v[h]);
+#pragma unroll
+                    for (int h = 0; h < HOT; h++) {
+                        if (v[h] >= v1) continue;
+                        float g[VEC<T>];
+                        unpack(u[h], g);
+#pragma unroll
+                        for (int j = 0; j < VEC<T>; j++) {
+                            const uint64_t q = order_key(g[j], v[h] * VEC<T> + j);
+                            if ((uint32_t)(q >> 32) >= from && v[h] * VEC<T> + j < V) {
+                                const int at = atomicAdd(&count, 1);
+                                if (at < CAND) keys[at] = q;
+                            }
                         }
+                        v[h] += 32 * NT;
                     }
-                    v[h] += 32 * NT;
                 }
             }
+            __syncthreads();
+            if (equal || count <= CAND) break;
+            equal = true;
+            __syncthreads();
+            if (tid == 0) count = 0;
+            __syncthreads();
         }
-        __syncthreads();
         uint64_t* list = keys;
         if (split > 1) list = cg::this_cluster().map_shared_rank(lists, 0) + rank * MAX_K;
         const int n = count;
         if (n <= CAND) {
-            for (int c = tid; c < MAX_K; c += NT)
-                if (split > 1 && c >= n) list[c] = 0;  // a part with fewer than k columns
             uint64_t q[2];
             int r[2];
 #pragma unroll
@@ -348,6 +407,11 @@ __global__ void __launch_bounds__(NT)
 #pragma unroll
             for (int h = 0; h < 2; h++)
                 if (r[h] < k) list[r[h]] = q[h];
+            if (tid < 32) {
+                int have = min(n, k);
+                if (equal) have = add_equal<T>(zv, v0, v1, V, least, have, k, list);
+                for (int c = have + lane; c < k; c += 32) list[c] = 0;  // a part with fewer than k columns
+            }
         } else {
             // one by one: the largest of the threads' largest, whose thread then looks for its next
             uint64_t best = 0;
@@ -398,6 +462,302 @@ __global__ void __launch_bounds__(NT)
             top_ids[(int64_t)row * k + tid] = key_col(q);
             top_logp[(int64_t)row * k + tid] = L == -INFINITY ? -INFINITY : key_logit(q) - L;
         }
+    }
+}
+
+// Many rows with alternatives: the search for them is a few microseconds of
+// waiting, so eight warps read row after row and two others search the rows
+// before: they are handed each reading thread's largest logit and the warps'
+// sums through shared memory. A block for a row that read and then searched
+// took 59 us for 2043 rows of 50257 with 20 alternatives and 734 for 32768,
+// this 51 and 700; three places for a thread's batches instead of two took 70
+// (the search's own loads wait behind them).
+constexpr int TNT = 256;   // threads that read
+constexpr int TB = 4;      // vectors of its batch
+constexpr int TOP_BLOCKS = 3;  // on an SM
+constexpr int RING = 2;    // batches that a reading thread has in shared memory or on their way
+constexpr int LOOK = 16;   // threads whose vectors the search has in shared memory at once, 32 of each
+constexpr int LIST = 256;  // candidates that fit
+constexpr int MANY = 128;  // of the reading threads reach the bound: equal logits (k threads, or 32 groups of 4, at most else)
+struct Search {            // a searching warp's own
+    uint4 part[LOOK][32];
+    uint64_t keys[LIST], out[MAX_K];
+    int hot[TNT], vectors[LIST], found, count;
+};
+struct TopShared {
+    uint4 ring[RING][TB][TNT];
+    Search search[2];
+    Stats ws[2][TNT / 32];
+    uint32_t maxima[2][TNT];  // a thread's largest logit (the lowest: -inf, or none)
+};
+// Hardware barriers of the reading threads and the search, a pair for each place: its row is read; its row is done with.
+__device__ __forceinline__ void full_sync(int b) {
+    if (b) asm volatile("bar.sync 2, %0;" ::"n"(TNT + 32) : "memory");
+    else asm volatile("bar.sync 1, %0;" ::"n"(TNT + 32) : "memory");
+}
+__device__ __forceinline__ void full_arrive(int b) {
+    if (b) asm volatile("bar.arrive 2, %0;" ::"n"(TNT + 32) : "memory");
+    else asm volatile("bar.arrive 1, %0;" ::"n"(TNT + 32) : "memory");
+}
+__device__ __forceinline__ void empty_sync(int b) {
+    if (b) asm volatile("bar.sync 4, %0;" ::"n"(TNT + 32) : "memory");
+    else asm volatile("bar.sync 3, %0;" ::"n"(TNT + 32) : "memory");
+}
+__device__ __forceinline__ void empty_arrive(int b) {
+    if (b) asm volatile("bar.arrive 4, %0;" ::"n"(TNT + 32) : "memory");
+    else asm volatile("bar.arrive 3, %0;" ::"n"(TNT + 32) : "memory");
+}
+
+template <typename T>
+__global__ void __launch_bounds__(TNT + 64, TOP_BLOCKS)
+    logprobs_top_kernel(float* __restrict__ logp, float* __restrict__ lse, float* __restrict__ entropy,
+                        float* __restrict__ top_logp, int32_t* __restrict__ top_ids, int k,
+                        const T* __restrict__ logits, const int32_t* __restrict__ targets, int N, int V, int Vp,
+                        int* status) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    TopShared& sh = *reinterpret_cast<TopShared*>(smem);
+    auto& maxima = sh.maxima;
+    auto& ws = sh.ws;
+    const int tid = threadIdx.x, lane = tid & 31, nv = (V + VEC<T> - 1) / VEC<T>;
+    if (tid < TNT) {
+        // a thread copies and reads its own vectors, across the ends of rows
+        int64_t next = blockIdx.x;  // the row and the first vector of the batch to be asked for next
+        int at = tid, slot = 0;
+        auto ask = [&](int to) {
+            if (next < N) {
+                const uint4* zv = reinterpret_cast<const uint4*>(logits + next * Vp);
+#pragma unroll
+                for (int e = 0; e < TB; e++)
+                    if (at + e * TNT < nv) cp_async16(&sh.ring[to][e][tid], zv + at + e * TNT);
+                at += TB * TNT;
+                if (at - tid >= nv) at = tid, next += gridDim.x;
+            }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int r = 0; r < RING - 1; r++) ask(r);
+        int it = 0;
+        for (int64_t row = blockIdx.x; row < N; row += gridDim.x, it++) {
+            const int b = it & 1;
+            Stats x = {-INFINITY, 0.f, 0.f};
+            for (int v = tid; v - tid < nv; v += TB * TNT) {
+                ask(slot == 0 ? RING - 1 : slot - 1);
+                cp_async_wait<RING - 1>();
+                if (v + (TB - 1) * TNT < V / VEC<T>) {
+                    uint4 u[TB];
+#pragma unroll
+                    for (int e = 0; e < TB; e++) u[e] = sh.ring[slot][e][tid];
+                    add_batch<T>(u, x);
+                } else {
+#pragma unroll 1
+                    for (int e = 0; e < TB; e++)
+                        if (v + e * TNT < nv) add_vector<T>(sh.ring[slot][e][tid], v + e * TNT, V, x);
+                }
+                slot = slot == RING - 1 ? 0 : slot + 1;
+            }
+            const uint32_t key = tid < nv ? (uint32_t)(order_key(x.m, 0) >> 32) : 0;
+            x = join<32>(x);
+            if (it >= 2) empty_sync(b);
+            maxima[b][tid] = key;
+            if (lane == 0) ws[b][tid >> 5] = x;
+            full_arrive(b);
+        }
+        cp_async_wait<0>();
+        return;
+    }
+    const int b = (tid - TNT) / 32;  // two warps search, every other row
+    Search& mine = sh.search[b];
+    for (int64_t row = blockIdx.x + (int64_t)b * gridDim.x; row < N; row += 2 * gridDim.x) {
+        const T* z = logits + row * Vp;
+        const uint4* zv = reinterpret_cast<const uint4*>(z);
+        float zt = 0.f;
+        if (logp && lane == 0) {
+            int tgt = targets[row];
+            if (tgt < 0 || tgt >= V) {
+                set_status(status, GPT2_FLAG_TARGET_RANGE);
+                tgt = 0;
+            }
+            zt = to_float(z[tgt]);
+        }
+        full_sync(b);
+        const Stats empty = {-INFINITY, 0.f, 0.f};
+        const Stats x = join<8>(lane < TNT / 32 ? ws[b][lane] : empty);
+        float L = isinf(x.m) ? x.m : x.m + LN2 * log2f(x.s);
+        L = __shfl_sync(0xffffffffu, L, 0);
+        if (lane == 0) {
+            lse[row] = L;
+            if (entropy) entropy[row] = x.m == -INFINITY ? 0.f : LN2 * (log2f(x.s) - x.t / x.s);
+            if (logp) logp[row] = x.m == -INFINITY ? -INFINITY : zt - L;
+        }
+        // The k-th largest of the maxima of 64 groups of four threads (of the threads for k above 32) bounds the
+        // k-th largest logit from below.
+        uint32_t least = ~0u;
+        if (k <= 32) {
+            static_assert(TNT == 256, "two groups of four threads to a lane");
+            uint32_t own[2];
+            int above[2] = {0, 0};
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int g = lane + 32 * h;
+                const uint4 o = *reinterpret_cast<const uint4*>(&maxima[b][4 * g]);
+                own[h] = max(max(o.x, o.y), max(o.z, o.w));
+            }
+#pragma unroll
+            for (int j = 0; j < 32; j++) {
+                const uint32_t o0 = __shfl_sync(0xffffffffu, own[0], j), o1 = __shfl_sync(0xffffffffu, own[1], j);
+                above[0] += (o0 > own[0]) + (o1 > own[0]);
+                above[1] += (o0 > own[1]) + (o1 > own[1]);
+            }
+            if (above[0] < k) least = own[0];
+            if (above[1] < k) least = min(least, own[1]);
+        } else {
+            uint32_t own[TNT / 32];
+            int above[TNT / 32];
+#pragma unroll
+            for (int h = 0; h < TNT / 32; h++) own[h] = maxima[b][lane + 32 * h], above[h] = 0;
+            for (int j = 0; j < TNT; j += 4) {
+                const uint4 o = *reinterpret_cast<const uint4*>(&maxima[b][j]);
+#pragma unroll
+                for (int h = 0; h < TNT / 32; h++)
+                    above[h] += (o.x > own[h]) + (o.y > own[h]) + (o.z > own[h]) + (o.w > own[h]);
+            }
+#pragma unroll
+            for (int h = 0; h < TNT / 32; h++)
+                if (above[h] < k) least = min(least, own[h]);
+        }
+        least = __reduce_min_sync(0xffffffffu, least);
+        uint32_t most[TNT / 32];
+#pragma unroll
+        for (int h = 0; h < TNT / 32; h++) most[h] = lane + 32 * h < nv ? maxima[b][lane + 32 * h] : 0;
+        __syncwarp();
+        if (row + 2 * gridDim.x < N) empty_arrive(b);  // their sums and maxima are read
+        // The reading threads whose maximum reaches a bound.
+        auto threads = [&](uint32_t bound) {
+            int n = 0;
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < TNT / 32; h++) {
+                const uint32_t vote = __ballot_sync(0xffffffffu, most[h] >= bound && lane + 32 * h < nv);
+                if (vote >> lane & 1) mine.hot[n + __popc(vote & ((1u << lane) - 1))] = lane + 32 * h;
+                n += __popc(vote);
+            }
+            if (lane == 0) mine.found = mine.count = 0;
+            __syncwarp();
+            return n;
+        };
+        // The first nh threads' logits that reach it, in any order: their number, or more than LIST.
+        auto collect = [&](int nh, uint32_t bound) {
+            // their vectors, copied at once, then looked at: those whose largest reaches the bound
+            for (int h0 = 0; h0 < nh; h0 += LOOK)
+                for (int at = 0; at * TNT < nv; at += 32) {
+                    const int hn = min(LOOK, nh - h0), v0 = (at + lane) * TNT;
+                    for (int h = 0; h < hn; h++) {
+                        const int v = v0 + mine.hot[h0 + h];
+                        if (v < nv) cp_async16(&mine.part[h][lane], zv + v);
+                    }
+                    cp_async_commit();
+                    cp_async_wait<0>();
+                    for (int h = 0; h < hn; h++) {
+                        const int v = v0 + mine.hot[h0 + h];
+                        if (v >= nv) continue;
+                        float g[VEC<T>], top = -INFINITY;
+                        unpack(mine.part[h][lane], g);
+                        if (v == nv - 1) {
+#pragma unroll
+                            for (int j = 0; j < VEC<T>; j++)
+                                if (v * VEC<T> + j >= V) g[j] = -INFINITY;
+                        }
+#pragma unroll
+                        for (int j = 0; j < VEC<T>; j += 2) top = max_nan(top, g[j], g[j + 1]);
+                        if ((uint32_t)(order_key(top, 0) >> 32) >= bound) {
+                            const int to = atomicAdd(&mine.found, 1);
+                            if (to < LIST) mine.vectors[to] = v;
+                        }
+                    }
+                }
+            __syncwarp();
+            // and of these the logits that reach it
+            const int nf = mine.found;
+            if (nf > LIST) return nf;
+            for (int c = lane; c < nf; c += 32) {
+                const int v = mine.vectors[c];
+                float g[VEC<T>];
+                unpack(__ldg(zv + v), g);
+#pragma unroll
+                for (int j = 0; j < VEC<T>; j++) {
+                    const uint64_t q = order_key(g[j], v * VEC<T> + j);
+                    if ((uint32_t)(q >> 32) >= bound && v * VEC<T> + j < V) {
+                        const int to = atomicAdd(&mine.count, 1);
+                        if (to < LIST) mine.keys[to] = q;
+                    }
+                }
+            }
+            __syncwarp();
+            return mine.count;
+        };
+        int nh = threads(least), n = nh <= MANY ? collect(nh, least) : LIST + 1;
+        const bool equal = n > LIST;  // many at the bound: those above it first, then the first columns at it
+        if (equal) {
+            nh = threads(least + 1);
+            n = collect(nh, least + 1);
+        }
+        if (n <= LIST) {
+            for (int c = lane; c < n; c += 32) {
+                const uint64_t q = mine.keys[c];
+                int r = 0;
+                for (int j = 0; j < n; j++) r += mine.keys[j] > q;
+                if (r < k) mine.out[r] = q;
+            }
+            if (equal) add_equal<T>(zv, 0, nv, V, least, n, k, mine.out);
+        } else {
+            // many in few threads: one by one, each the largest of the reading threads' largest, whose vectors are
+            // then looked through for the next
+            auto best_of = [&](int t, uint64_t below) {
+                uint64_t best = 0;
+                for (int v = t + lane * TNT; v < nv; v += 32 * TNT) {
+                    float g[VEC<T>];
+                    unpack(__ldg(zv + v), g);
+#pragma unroll
+                    for (int j = 0; j < VEC<T>; j++) {
+                        const uint64_t q = order_key(g[j], v * VEC<T> + j);
+                        if (v * VEC<T> + j < V && q < below && q > best) best = q;
+                    }
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o /= 2) {
+                    const uint64_t y = __shfl_xor_sync(0xffffffffu, best, o);
+                    best = y > best ? y : best;
+                }
+                return best;
+            };
+            static_assert(LIST >= TNT, "the largest of each reading thread");
+            __syncwarp();
+            for (int t = 0; t < TNT; t++) {
+                const uint64_t best = best_of(t, ~0ull);
+                if (lane == 0) mine.keys[t] = best;
+            }
+            for (int r = 0; r < k; r++) {
+                __syncwarp();
+                uint64_t top = 0;
+                for (int t = lane; t < TNT; t += 32) top = mine.keys[t] > top ? mine.keys[t] : top;
+#pragma unroll
+                for (int o = 16; o > 0; o /= 2) {
+                    const uint64_t y = __shfl_xor_sync(0xffffffffu, top, o);
+                    top = y > top ? y : top;
+                }
+                const int t = key_col(top) / VEC<T> % TNT;
+                const uint64_t next = best_of(t, top);
+                __syncwarp();
+                if (lane == 0) mine.out[r] = top, mine.keys[t] = next;
+            }
+        }
+        __syncwarp();
+        for (int r = lane; r < k; r += 32) {
+            const uint64_t q = mine.out[r];
+            top_ids[row * k + r] = key_col(q);
+            top_logp[row * k + r] = L == -INFINITY ? -INFINITY : key_logit(q) - L;
+        }
+        __syncwarp();
     }
 }
 
@@ -481,14 +841,23 @@ int forward(float* logp, float* lse, float* entropy, float* top_logp, int32_t* t
         return GPT2_ERR_CUDA;
     return 1;
 }
+template <typename T>
+int forward_top(float* logp, float* lse, float* entropy, float* top_logp, int32_t* top_ids, int k, const T* logits,
+                const int32_t* targets, int N, int V, int Vp, int* status, cudaStream_t s) {
+    const void* kernel = (const void*)logprobs_top_kernel<T>;
+    if (smem_attr(kernel, sizeof(TopShared)) != cudaSuccess) return GPT2_ERR_CUDA;
+    logprobs_top_kernel<T><<<min(N, TOP_BLOCKS * gpt2_num_sms()), TNT + 64, sizeof(TopShared), s>>>(
+        logp, lse, entropy, top_logp, top_ids, k, logits, targets, N, V, Vp, status);
+    return 1;
+}
 // Threads of a block: twice as many rows on their way in blocks of 128 read
 // 32768 rows of 50257 at the speed of a copy (496 us; 535 with 256), but few
-// rows, and the search for alternatives, want the wider block (2043 rows with
-// 20: 60 us; 67 with 128).
+// rows want the wider block.
 template <typename T, typename... A>
 int forward_of(int k, int N, A... args) {
-    if (k) return forward<T, 256, true>(args...);
-    return N > gpt2_num_sms() ? forward<T, 128, false>(args...) : forward<T, 256, false>(args...);
+    const bool many = N > gpt2_num_sms();
+    if (k) return many ? forward_top<T>(args...) : forward<T, 256, true>(args...);
+    return many ? forward<T, 128, false>(args...) : forward<T, 256, false>(args...);
 }
 
 template <typename T>

@@ -421,6 +421,42 @@ def test_logprobs_non_finite_rows(torch_cuda):
         assert torch.equal(a[[0, 3]], b[[0, 3]])
 
 
+@pytest.mark.parametrize("mode", [1, 0], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("V,k", [(40, 40), (1000, 20), (1000, 64), (50257, 5), (50257, 40)])
+def test_logprobs_alternatives_of_many_rows(torch_cuda, V, k, mode):
+    """More rows than SMs, ties, masks and NaN among them."""
+    Vp, N = -(-V // 8) * 8 + 8, 331
+    z = inputs(24, (N, Vp), 2.0, mode).astype(np.float64)
+    z[1::9] = 0.0
+    z[2::9] = np.round(z[2::9])
+    z[3::9] = -np.inf
+    z[12::9, V // 2] = 1.0           # (row 3 stays without any token)
+    z[4::9, ::2] = -np.inf
+    z[5::9] = np.linspace(-20, 20, Vp).astype(np.float32)
+    z[6::9] = -1e30
+    z[6::9, 17] = 1.0
+    z = data.round_to_bf16(z.astype(np.float32)).astype(np.float64) if mode == 1 else z.astype(np.float32).astype(np.float64)
+    z[:, V:] = np.nan                # padding columns are not looked at
+    check_logprobs(torch_cuda, z, np.random.default_rng(5).integers(0, V, N), V, k, mode)
+
+
+@pytest.mark.parametrize("N", [3, 400])
+def test_logprobs_rows_of_nan(torch_cuda, N):
+    """Rows of NaN, with more of them than the alternatives asked for: ids are the first such columns."""
+    torch = torch_cuda
+    V, k = 50257, 9
+    z = inputs(25, (N, 50304), 2.0, 1).astype(np.float64)
+    t = np.full(N, 4)
+    plain = run_logprobs(torch, z, t, V, k, 1)
+    z[1], z[N - 1, 300:] = np.nan, np.nan
+    z[1, ::2] *= -1                  # of either sign
+    got = run_logprobs(torch, z, t, V, k, 1)
+    ids = got[6].cpu().numpy()
+    assert (ids[1] == np.arange(k)).all() and (ids[N - 1] == 300 + np.arange(k)).all()
+    for a, b in zip(got[2:7], plain[2:7]):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[2:N - 1], b[2:N - 1])
+
+
 def test_logprobs_many_rows_stream_and_graph(torch_cuda):
     torch = torch_cuda
     from step_gpt_train_gb300.gpt2 import gpt2_op_token_logprobs, gpt2_op_token_logprobs_backward
