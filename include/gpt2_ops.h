@@ -270,7 +270,8 @@ int gpt2_op_attention_packed_forward(int dtype, void* o, int64_t o_stride, float
  * group. dq [total_q] rows, dk, dv [total_k] rows (dtype, their own strides,
  * overwritten; rows of no sequence are left as they were, a key that no query
  * sees gets 0). Deterministic (no atomics). dq, dk, dv must not overlap the
- * inputs. Sequences, strides and limits as in the forward. Scratch: D. */
+ * inputs. Sequences, strides and limits as in the forward. Scratch: D and, for
+ * bf16, lse beside it and the lists of work items. */
 size_t gpt2_op_attention_packed_backward_scratch(int dtype, int n_seq, int total_q, int total_k, int Hq, int Hkv,
                                                  int hd);
 int gpt2_op_attention_packed_backward(int dtype, void* dq, int64_t dq_stride, void* dk, int64_t dk_stride, void* dv,
@@ -353,8 +354,8 @@ int gpt2_op_classifier(int dtype, void* logits, float* losses, const int32_t* ta
  * row whose every logit is -inf has no distribution: lse = logp = top_logp =
  * -inf, entropy = 0. A row with a NaN gets NaN in all of them; one with +inf
  * (and no NaN) gets lse = inf, entropy = NaN, and log-probabilities of -inf
- * (NaN for its infinite columns). top_ids stay in [0,V), unspecified for a
- * row with a NaN. */
+ * (NaN for its infinite columns). top_ids stay in [0,V); a NaN counts as
+ * the largest. */
 int gpt2_op_token_logprobs(int dtype, float* logp, float* lse, float* entropy, float* top_logp, int32_t* top_ids,
                            int k, const void* logits, const int32_t* targets, int N, int V, int Vp, int* d_status,
                            void* stream);

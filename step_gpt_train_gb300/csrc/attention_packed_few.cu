@@ -410,7 +410,7 @@ int launch_attention_packed_few(const PackedAttn& a, void* scratch, cudaStream_t
     while (a.Hkv % warps) warps /= 2;
     if (smem_attr((const void*)packed_few_kernel, WARPS * NST * STAGE) != cudaSuccess) return GPT2_ERR_CUDA;
     packed_few_kernel<<<A.chunks * (a.Hkv / warps), warps * 32, warps * NST * STAGE, s>>>(A);
-    if (A.chunks == 1) return 1;
+    if (A.chunks == 1 || A.rows == 0) return 1;
     return launch_dependent(packed_few_join_kernel, a.n_seq * a.Hkv * A.rows, 128, 0, s, A) == cudaSuccess
                ? 2
                : GPT2_ERR_CUDA;

@@ -316,7 +316,7 @@ int gpt2_op_attention_packed_backward(int dtype, void* dq, int64_t dq_stride, vo
         !rows_ok(v, v_stride, Hkv, hd, dtype) || !rows_ok(o, o_stride, Hq, hd, dtype))
         return GPT2_ERR_ARG;
     const size_t need = attention_packed_backward_scratch(dtype, n_seq, total_q, total_k, Hq, Hkv, hd);
-    if (!scratch || scratch_bytes < need) return GPT2_ERR_WORKSPACE;
+    if (need && (!scratch || scratch_bytes < need)) return GPT2_ERR_WORKSPACE;
     const PackedAttn a = {q,    k,     v,     q_stride, k_stride, v_stride, const_cast<void*>(o),
                           o_stride, const_cast<float*>(lse), cu_q, cu_k, n_seq, total_q, total_k, max_q,
                           max_k,    Hq,    Hkv,   hd,       d_status};

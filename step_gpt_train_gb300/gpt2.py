@@ -618,10 +618,25 @@ def _rows(t, what):
 
 
 def _sequences(cu_q, cu_k):
-    n = cu_q.shape[0] - 1
-    if cu_k is not cu_q and cu_k.shape[0] - 1 != n:
-        raise ValueError("cu_q and cu_k need the same number of sequences")
+    n, i32 = cu_q.shape[0] - 1, _tc().int32
+    if cu_k.shape[0] - 1 != n or cu_q.dtype is not i32 or cu_k.dtype is not i32:
+        raise ValueError("cu_q and cu_k need the same number of sequences, as int32")
     return n
+
+
+def _alike(what, like, *tensors):
+    """Operands that have to have one shape and type."""
+    shape, dtype = like.shape, like.dtype
+    for t in tensors:
+        if t.shape != shape or t.dtype is not dtype:
+            raise ValueError(f"{what} need one shape and type")
+
+
+def _logits(t):
+    """Rows and padded columns of contiguous logits."""
+    if t.dim() != 2 or not t.is_contiguous():
+        raise ValueError("contiguous logits [N, Vp] are needed")
+    return t.shape
 
 
 def gpt2_op_attention_packed_forward(o, lse, q, k, v, cu_q, cu_k, max_q, max_k, status=None, stream=None):
@@ -633,6 +648,10 @@ def gpt2_op_attention_packed_forward(o, lse, q, k, v, cu_q, cu_k, max_q, max_k, 
     tq, hq, hd = q.shape
     tk, hkv, _ = k.shape
     n = _sequences(cu_q, cu_k)
+    _alike("q and o", q, o)
+    _alike("k and v", k, v)
+    if k.dtype is not q.dtype or k.shape[2] != hd or lse.shape != (hq, tq):
+        raise ValueError("k like q in type and head size, and lse [Hq, total_q], are needed")
     nb = lib.gpt2_op_attention_packed_forward_scratch(dt, n, tq, tk, max_q, max_k, hq, hkv, hd)
     sc = _scratch(nb) if nb else None
     check(lib.gpt2_op_attention_packed_forward(dt, o.data_ptr(), _rows(o, "o"), lse.data_ptr(), q.data_ptr(),
@@ -651,6 +670,10 @@ def gpt2_op_attention_packed_backward(dq, dk, dv, dout, q, k, v, o, lse, cu_q, c
     tq, hq, hd = q.shape
     tk, hkv, _ = k.shape
     n = _sequences(cu_q, cu_k)
+    _alike("q, o, dout and dq", q, o, dout, dq)
+    _alike("k, v, dk and dv", k, v, dk, dv)
+    if k.dtype is not q.dtype or k.shape[2] != hd or lse.shape != (hq, tq):
+        raise ValueError("k like q in type and head size, and lse [Hq, total_q], are needed")
     nb = lib.gpt2_op_attention_packed_backward_scratch(dt, n, tq, tk, hq, hkv, hd)
     sc = _scratch(nb)
     check(lib.gpt2_op_attention_packed_backward(dt, dq.data_ptr(), _rows(dq, "dq"), dk.data_ptr(), _rows(dk, "dk"),
@@ -667,7 +690,7 @@ def gpt2_op_token_logprobs(logp, lse, entropy, logits, targets, V, top_logp=None
                            stream=None):
     """logp, lse, entropy (float32 [N]) of the rows of logits [N, Vp] over their first V columns; top_logp and
     top_ids ([N, k], both or none): the k largest."""
-    N, Vp = logits.shape
+    N, Vp = _logits(logits)
     if (top_logp is None) != (top_ids is None) or (top_ids is not None and top_logp.shape != top_ids.shape):
         raise ValueError("top_logp and top_ids come together, in one shape")
     check(load_library().gpt2_op_token_logprobs(_dtype_of(logits), _p(logp), _p(lse), _p(entropy), _p(top_logp),
@@ -679,7 +702,9 @@ def gpt2_op_token_logprobs(logp, lse, entropy, logits, targets, V, top_logp=None
 def gpt2_op_token_logprobs_backward(dlogits, logits, targets, lse, entropy, V, dlogp=None, dlse=None, dentropy=None,
                                     status=None, stream=None):
     """dlogits [N, Vp] (may be logits) from the gradients of gpt2_op_token_logprobs' logp, lse and entropy."""
-    N, Vp = logits.shape
+    N, Vp = _logits(logits)
+    _alike("logits and dlogits", logits, dlogits)
+    _logits(dlogits)
     check(load_library().gpt2_op_token_logprobs_backward(_dtype_of(logits), _p(dlogits), _p(logits), _p(targets),
                                                          _p(lse), _p(entropy), _p(dlogp), _p(dlse), _p(dentropy), N,
                                                          V, Vp, _p(status), _s(stream)),

@@ -59,7 +59,7 @@ class Packed:
         self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
 
         def blocks(*xs):  # column blocks of one buffer, or buffers of their own
-            ts = [dev(x.astype(np.float32).reshape(len(x), -1), mode) for x in xs]
+            ts = [dev(x.astype(np.float32).reshape(len(x), x.shape[1] * x.shape[2]), mode) for x in xs]
             if not fused:
                 return [t.unflatten(1, (-1, hd)) for t in ts]
             buf = torch.cat([torch.full((len(xs[0]), 16), float("nan"), dtype=ts[0].dtype, device="cuda")] + ts, 1)
@@ -155,6 +155,56 @@ def test_attention_many_sequences(torch_cuda, mode):
     c.forward()
     c.backward()
     c.check()
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (6, 2), (3, 3), (16, 4), (12, 12)])
+def test_attention_few_queries_of_many_sequences(torch_cuda, Hq, Hkv):
+    """New tokens over caches of every length from none on, some sequences without a query between them."""
+    r = np.random.default_rng(7)
+    lk = [int(x) for x in np.exp(r.uniform(0, np.log(900), 90)).round()] + [5000, 0, 0, 40, 16, 0, 2600]
+    lq = [int(x) for x in r.integers(0, min(3, 16 // (Hq // Hkv)) + 1, len(lk))]
+    lq[90], lq[96] = 0, 1  # a long cache that nobody asks for
+    c = Packed(torch_cuda, 26, lq, lk, Hq, Hkv, 64, 1)
+    c.forward()
+    c.check(back=False)
+
+
+def test_attention_few_queries_neighbours_do_not_leak(torch_cuda):
+    """Caches of NaN and infinities between others, that end and begin inside a tile of keys."""
+    torch = torch_cuda
+    lk = [5, 9, 16, 200, 3, 1, 77, 31, 500]
+    c = Packed(torch, 27, [1] * len(lk), lk, 8, 4, 64, 1)
+    c.forward()
+    o, lse = c.o.clone(), c.lse.clone()
+    for s in range(0, len(lk), 2):
+        at = slice(int(c.cu_k[s]), int(c.cu_k[s + 1]))
+        c.tk[at], c.tv[at] = float("nan"), float("inf")
+    c.forward()
+    torch.cuda.synchronize()
+    for s in range(1, len(lk), 2):
+        row = int(c.cu_q[s])
+        assert torch.equal(o[row], c.o[row]) and torch.equal(lse[:, row], c.lse[:, row]), s
+
+
+@pytest.mark.parametrize("mode", [1, 0], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("lq,lk", [([40, 0, 7], [0, 0, 0]), ([1, 1], [0, 0]), ([0, 0], [70, 300]), ([0, 0, 0], [0, 0, 0])])
+def test_attention_batches_without_keys_or_queries(torch_cuda, mode, lq, lk):
+    """Nothing to see (outputs 0, lse -inf, gradients 0), or nobody that sees: dK and dV are 0."""
+    c = Packed(torch_cuda, 28, lq, lk, 4, 2, 64, mode, before=0, after=0)
+    c.forward()
+    c.backward()
+    c.check()
+
+
+def test_attention_no_queries_announced(torch_cuda):
+    """max_q = 0 with queries there: reported, and nothing is written."""
+    torch = torch_cuda
+    c = Packed(torch, 29, [1, 1], [3000, 700], 4, 4, 64, 1)
+    c.max_q = 0
+    before = c.o.clone(), c.lse.clone()
+    c.forward()
+    torch.cuda.synchronize()
+    assert c.status.item() == 8 and torch.equal(before[0], c.o) and torch.equal(before[1], c.lse)
 
 
 @pytest.mark.parametrize("Hq,Hkv,lo,hi", [(12, 12, 1, 520), (8, 4, 20, 100), (25, 25, 100, 700)])
@@ -487,6 +537,56 @@ def test_logprobs_many_rows_stream_and_graph(torch_cuda):
     torch.cuda.synchronize()
     for a, b in zip(first, (*out, dz)):
         assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------- offsets past 32 bits
+
+@pytest.mark.parametrize("lq,lk", [([700, 1, 1500], [700, 1, 1500]), ([2, 0, 1], [700, 1, 1500])])
+def test_attention_rows_far_apart(torch_cuda, lq, lk):
+    """Buffers of more than 2^31 elements (a row stride of 2^20): the same bits as from rows side by side."""
+    torch = torch_cuda
+    stride = 1 << 20
+    c = Packed(torch, 30, lq, lk, 4, 2, 64, 1, before=0, after=0)
+    c.forward()
+    c.backward()
+    near = [x.clone() for x in (c.o, c.lse, c.dq, c.dk, c.dv)]
+    wide = torch.empty(c.rows_k * stride, dtype=torch.bfloat16, device="cuda")
+    at = [0]
+
+    def far(t):  # its own columns of the wide rows
+        x = wide.as_strided((t.shape[0], t.shape[1], 64), (stride, 64, 1), at[0])
+        at[0] += t.shape[1] * 64
+        x.copy_(t)
+        return x
+    for name in ("tq", "tk", "tv", "tdout", "o", "dq", "dk", "dv"):
+        setattr(c, name, far(getattr(c, name)))
+    c.forward()
+    c.backward()
+    torch.cuda.synchronize()
+    for x, y in zip(near, (c.o, c.lse, c.dq, c.dk, c.dv)):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("k", [0, 6])
+def test_logprobs_more_logits_than_32_bits_count(torch_cuda, k):
+    torch = torch_cuda
+    from step_gpt_train_gb300.gpt2 import gpt2_op_token_logprobs, gpt2_op_token_logprobs_backward
+    N, n, V, Vp = 43000, 200, 50257, 50304
+
+    def run(z, dz):
+        rows = len(z)
+        t = torch.full((rows,), 50256, dtype=torch.int32, device="cuda")
+        out = [torch.zeros(rows, device="cuda") for _ in range(3)]
+        top = [torch.zeros(rows, k, device="cuda"), torch.zeros(rows, k, dtype=torch.int32, device="cuda")] if k else [None] * 2
+        gpt2_op_token_logprobs(*out, z, t, V, *top)
+        gpt2_op_token_logprobs_backward(dz, z, t, out[1], out[2], V, dlogp=out[0], dentropy=out[2])
+        return [x[-n:].clone() for x in (*out, *top, dz) if x is not None]
+    some = torch.randn(n, Vp, device="cuda").bfloat16()
+    z = torch.zeros(N, Vp, dtype=torch.bfloat16, device="cuda")
+    z[-n:] = some
+    few = run(some, torch.empty_like(some))
+    for x, y in zip(run(z, z), few):  # the gradient in place
+        assert torch.equal(x, y)
 
 
 # ---------------------------------------------------------------- together

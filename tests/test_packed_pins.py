@@ -182,6 +182,33 @@ def test_logprobs_more_refusals(lib):
     assert logprobs(lib, N=0) == OK and logprobs_backward(lib, N=0) == OK
 
 
+def test_wrapper_refuses_operands_that_differ(lib):
+    import torch
+    from step_gpt_train_gb300 import gpt2 as g
+    bf = torch.bfloat16
+    q, k, cu, lse = torch.zeros(4, 2, 64, dtype=bf), torch.zeros(9, 1, 64, dtype=bf), torch.tensor([0, 4]).int(), torch.zeros(2, 4)
+    long = torch.tensor([0, 4])
+    for o, ls, kk, v, cq, ck in ((q[:3], lse, k, k, cu, cu), (q.float(), lse, k, k, cu, cu), (q, lse[:1], k, k, cu, cu),
+                                 (q, lse, k, k[:8], cu, cu), (q, lse, k.float(), k.float(), cu, cu),
+                                 (q, lse, k, k, long, long), (q, lse, k, k, cu, torch.zeros(3).int())):
+        with pytest.raises(ValueError):
+            g.gpt2_op_attention_packed_forward(o, ls, q, kk, v, cq, ck, 4, 9)
+        with pytest.raises(ValueError):
+            g.gpt2_op_attention_packed_backward(q, k, k, q, q, kk, v, o, ls, cq, ck, 4, 9)
+    with pytest.raises(ValueError):
+        g.gpt2_op_attention_packed_backward(q[:2], k, k, q, q, k, k, q, lse, cu, cu, 4, 9)
+    z, t, s = torch.zeros(4, 64, dtype=bf), torch.zeros(4).int(), torch.zeros(4)
+    for bad in (z[:, :32], z[0], z.T):
+        with pytest.raises(ValueError):
+            g.gpt2_op_token_logprobs(s, s, s, bad, t, 30)
+        with pytest.raises(ValueError):
+            g.gpt2_op_token_logprobs_backward(z, bad, t, s, s, 30, dlogp=s)
+        with pytest.raises(ValueError):
+            g.gpt2_op_token_logprobs_backward(bad, z, t, s, s, 30, dlogp=s)
+    with pytest.raises(ValueError):
+        g.gpt2_op_token_logprobs(s, s, s, z, t, 30, top_logp=torch.zeros(4, 3))
+
+
 def test_wrapper_refuses_other_layouts():
     import torch
     from step_gpt_train_gb300 import gpt2 as g
