@@ -328,6 +328,37 @@ def test_attention_same_bits_again_on_a_stream_and_in_a_graph(torch_cuda, lq, lk
     c.check()
 
 
+def test_attention_graphs_that_share_their_workspaces(torch_cuda):
+    """Graphs of one memory pool, replayed in turn: each call writes its lists and parts before it reads them."""
+    torch = torch_cuda
+    cs = [Packed(torch, 31, [300, 41, 700], [300, 41, 700], 8, 2, 64, 1), Packed(torch, 32, [1] * 5, [900, 1, 40, 3000, 0], 8, 2, 64, 1),
+          Packed(torch, 33, [130, 64], [700, 64], 4, 4, 64, 1), Packed(torch, 34, [2, 1], [2000, 77], 12, 12, 64, 1)]
+    names = ("o", "lse", "dq", "dk", "dv")
+    first = []
+    for c in cs:
+        c.forward()
+        c.backward()
+        first.append([getattr(c, n).clone() for n in names])
+    torch.cuda.synchronize()
+    pool, graphs = torch.cuda.graph_pool_handle(), []
+    for c in cs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, pool=pool):
+            c.forward()
+            c.backward()
+        graphs.append(g)
+    for _ in range(2):
+        for c in cs:
+            for n in names:
+                getattr(c, n).fill_(c.FILL)
+        for g in graphs + graphs[::-1]:
+            g.replay()
+        torch.cuda.synchronize()
+        for c, f in zip(cs, first):
+            for n, x in zip(names, f):
+                assert torch.equal(x, getattr(c, n)), n
+
+
 def test_attention_equals_the_rectangular_one(torch_cuda):
     """Equal lengths and a key head per query head: the attention of the step, within both kernels' bounds."""
     torch = torch_cuda
