@@ -606,15 +606,37 @@ def gpt2_op_attention_backward(dqkv, dout, qkv, o, lse, B, T, H, stream=None):
     return sc
 
 
-def _rows(t, what):
-    """Row stride of a [rows, heads, hd] tensor whose heads are contiguous in a row."""
-    shape = t.shape
-    if len(shape) == 3:
-        rows, heads, hd = shape
+def _borrow(nbytes, stream):
+    """Scratch of one call, as an address: torch's caching allocator hands it out on the stream that will use it and
+    may hand it on there as soon as it is given back. (A tensor for it costs a small call 6 us on the host.)"""
+    c = _tc()._C
+    try:
+        return c._cuda_cudaCachingAllocator_raw_alloc(nbytes, stream or 0)
+    except AttributeError:
+        return _torch.cuda.caching_allocator_alloc(nbytes, stream=stream or 0)
+
+
+def _give_back(address):
+    try:
+        _torch._C._cuda_cudaCachingAllocator_raw_delete(address)
+    except AttributeError:
+        _torch.cuda.caching_allocator_delete(address)
+
+
+def _rows(what, like, *more):
+    """Row strides of [rows, heads, hd] tensors of one shape and type whose heads are contiguous in a row."""
+    shape, dtype, strides = like.shape, like.dtype, []
+    if len(shape) != 3:
+        raise ValueError(f"{what}: [rows, heads, hd] tensors are needed")
+    rows, heads, hd = shape
+    for t in (like, *more):
+        if t is not like and (t.shape != shape or t.dtype is not dtype):
+            raise ValueError(f"{what} need one shape and type")
         s0, s1, s2 = t.stride()
-        if s2 == 1 and (s1 == hd or heads <= 1):
-            return s0 if rows > 1 else heads * hd
-    raise ValueError(f"{what}: a [rows, heads, hd] tensor with the heads of a row contiguous is needed")
+        if s2 != 1 or (s1 != hd and heads > 1):
+            raise ValueError(f"{what}: the heads of a row have to be contiguous")
+        strides.append(s0 if rows > 1 else heads * hd)
+    return strides
 
 
 def _sequences(cu_q, cu_k):
@@ -622,14 +644,6 @@ def _sequences(cu_q, cu_k):
     if cu_k.shape[0] - 1 != n or cu_q.dtype is not i32 or cu_k.dtype is not i32:
         raise ValueError("cu_q and cu_k need the same number of sequences, as int32")
     return n
-
-
-def _alike(what, like, *tensors):
-    """Operands that have to have one shape and type."""
-    shape, dtype = like.shape, like.dtype
-    for t in tensors:
-        if t.shape != shape or t.dtype is not dtype:
-            raise ValueError(f"{what} need one shape and type")
 
 
 def _logits(t):
@@ -646,20 +660,22 @@ def gpt2_op_attention_packed_forward(o, lse, q, k, v, cu_q, cu_k, max_q, max_k, 
     lib = load_library()
     dt = _dtype_of(q)
     tq, hq, hd = q.shape
-    tk, hkv, _ = k.shape
+    tk, hkv, d = k.shape
     n = _sequences(cu_q, cu_k)
-    _alike("q and o", q, o)
-    _alike("k and v", k, v)
-    if k.dtype is not q.dtype or k.shape[2] != hd or lse.shape != (hq, tq):
+    sq, so = _rows("q and o", q, o)
+    sk, sv = _rows("k and v", k, v)
+    if k.dtype is not q.dtype or d != hd or lse.shape != (hq, tq):
         raise ValueError("k like q in type and head size, and lse [Hq, total_q], are needed")
     nb = lib.gpt2_op_attention_packed_forward_scratch(dt, n, tq, tk, max_q, max_k, hq, hkv, hd)
-    sc = _scratch(nb) if nb else None
-    check(lib.gpt2_op_attention_packed_forward(dt, o.data_ptr(), _rows(o, "o"), lse.data_ptr(), q.data_ptr(),
-                                               _rows(q, "q"), k.data_ptr(), _rows(k, "k"), v.data_ptr(),
-                                               _rows(v, "v"), cu_q.data_ptr(), cu_k.data_ptr(), n, tq, tk, max_q,
-                                               max_k, hq, hkv, hd, _p(sc), nb, _p(status), _s(stream)),
-          "gpt2_op_attention_packed_forward")
-    return sc
+    args = (dt, o.data_ptr(), so, lse.data_ptr(), q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv,
+            cu_q.data_ptr(), cu_k.data_ptr(), n, tq, tk, max_q, max_k, hq, hkv, hd)
+    st = _s(stream)
+    sc = _borrow(nb, st) if nb else None
+    try:
+        check(lib.gpt2_op_attention_packed_forward(*args, sc, nb, _p(status), st), "gpt2_op_attention_packed_forward")
+    finally:
+        if sc:
+            _give_back(sc)
 
 
 def gpt2_op_attention_packed_backward(dq, dk, dv, dout, q, k, v, o, lse, cu_q, cu_k, max_q, max_k, status=None,
@@ -668,22 +684,23 @@ def gpt2_op_attention_packed_backward(dq, dk, dv, dout, q, k, v, o, lse, cu_q, c
     lib = load_library()
     dt = _dtype_of(q)
     tq, hq, hd = q.shape
-    tk, hkv, _ = k.shape
+    tk, hkv, d = k.shape
     n = _sequences(cu_q, cu_k)
-    _alike("q, o, dout and dq", q, o, dout, dq)
-    _alike("k, v, dk and dv", k, v, dk, dv)
-    if k.dtype is not q.dtype or k.shape[2] != hd or lse.shape != (hq, tq):
+    sq, so, sdo, sdq = _rows("q, o, dout and dq", q, o, dout, dq)
+    sk, sv, sdk, sdv = _rows("k, v, dk and dv", k, v, dk, dv)
+    if k.dtype is not q.dtype or d != hd or lse.shape != (hq, tq):
         raise ValueError("k like q in type and head size, and lse [Hq, total_q], are needed")
     nb = lib.gpt2_op_attention_packed_backward_scratch(dt, n, tq, tk, hq, hkv, hd)
-    sc = _scratch(nb)
-    check(lib.gpt2_op_attention_packed_backward(dt, dq.data_ptr(), _rows(dq, "dq"), dk.data_ptr(), _rows(dk, "dk"),
-                                                dv.data_ptr(), _rows(dv, "dv"), dout.data_ptr(), _rows(dout, "dout"),
-                                                q.data_ptr(), _rows(q, "q"), k.data_ptr(), _rows(k, "k"),
-                                                v.data_ptr(), _rows(v, "v"), o.data_ptr(), _rows(o, "o"),
-                                                lse.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(), n, tq, tk, max_q,
-                                                max_k, hq, hkv, hd, sc.data_ptr(), nb, _p(status), _s(stream)),
-          "gpt2_op_attention_packed_backward")
-    return sc
+    args = (dt, dq.data_ptr(), sdq, dk.data_ptr(), sdk, dv.data_ptr(), sdv, dout.data_ptr(), sdo, q.data_ptr(), sq,
+            k.data_ptr(), sk, v.data_ptr(), sv, o.data_ptr(), so, lse.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(), n,
+            tq, tk, max_q, max_k, hq, hkv, hd)
+    st = _s(stream)
+    sc = _borrow(nb, st) if nb else None
+    try:
+        check(lib.gpt2_op_attention_packed_backward(*args, sc, nb, _p(status), st), "gpt2_op_attention_packed_backward")
+    finally:
+        if sc:
+            _give_back(sc)
 
 
 def gpt2_op_token_logprobs(logp, lse, entropy, logits, targets, V, top_logp=None, top_ids=None, status=None,
@@ -703,8 +720,8 @@ def gpt2_op_token_logprobs_backward(dlogits, logits, targets, lse, entropy, V, d
                                     status=None, stream=None):
     """dlogits [N, Vp] (may be logits) from the gradients of gpt2_op_token_logprobs' logp, lse and entropy."""
     N, Vp = _logits(logits)
-    _alike("logits and dlogits", logits, dlogits)
-    _logits(dlogits)
+    if _logits(dlogits) != logits.shape or dlogits.dtype is not logits.dtype:
+        raise ValueError("logits and dlogits need one shape and type")
     check(load_library().gpt2_op_token_logprobs_backward(_dtype_of(logits), _p(dlogits), _p(logits), _p(targets),
                                                          _p(lse), _p(entropy), _p(dlogp), _p(dlse), _p(dentropy), N,
                                                          V, Vp, _p(status), _s(stream)),

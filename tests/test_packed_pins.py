@@ -213,8 +213,11 @@ def test_wrapper_refuses_other_layouts():
     import torch
     from step_gpt_train_gb300 import gpt2 as g
     x = torch.zeros(4, 2, 8)
-    assert g._rows(x, "x") == 16
-    assert g._rows(torch.zeros(4, 48)[:, 16:32].unflatten(1, (2, 8)), "x") == 48
+    assert g._rows("x", x) == [16]
+    assert g._rows("x", x, torch.zeros(4, 48)[:, 16:32].unflatten(1, (2, 8))) == [16, 48]
+    assert g._rows("x", torch.zeros(1, 2, 8).expand(1, 2, 8)) == [16]
     for bad in (torch.zeros(4, 16), x.transpose(0, 1), x.transpose(1, 2), torch.zeros(4, 2, 16)[:, :, ::2]):
         with pytest.raises(ValueError):
-            g._rows(bad, "x")
+            g._rows("x", bad)
+        with pytest.raises(ValueError):
+            g._rows("x", x, bad)
