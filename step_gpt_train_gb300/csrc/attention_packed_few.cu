@@ -10,7 +10,9 @@
 // over 177402 keys of 4 heads (182 MB) took 47 us with a block for a part of
 // one sequence and one head, 39 so. A sequence inside one chunk is written at
 // once; of the others each chunk leaves its part (O, m, l) in scratch, and a
-// second kernel joins them (about 5 us of the 39).
+// second kernel joins them (about 5 us of the 39). Sequences of up to 128 keys
+// are not cut, which saves the second kernel (4 sequences of up to 74 keys: 8.3
+// us on the device with it).
 //
 // The block's warps copy whole rows of its heads to shared memory (cp.async),
 // NST - 1 tiles ahead and across the ends of sequences: 512 bytes of one row to
@@ -40,6 +42,7 @@ constexpr int STAGE = TILE * HD * 2 * 2;   // bytes of a tile for each warp
 constexpr int PART = HD + 2;               // floats of a row's partial result: O, m, l
 constexpr int FILL = 16 * 152;             // warps at work at once
 constexpr int MIN_KEYS = 32;               // of a chunk: what a block has on its way at once
+constexpr int WHOLE = 128;                 // longest sequence of a batch whose sequences are not cut
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 // The reference that scores are taken against may fall behind the maximum by
 // this (a factor of 256) before the sums are moved to a new one.
@@ -49,7 +52,7 @@ struct Args {
     PackedAttn a;
     int group;
     int rows;    // rows of scratch per (slot, key head)
-    int chunks;  // at most
+    int chunks;  // at most; 0: a block takes a whole sequence
     float scale_log2;
     float* scratch;  // [slot][key head][rows][PART]; the slot of chunk c's part of sequence s is c + s
 };
@@ -117,11 +120,22 @@ __global__ void __launch_bounds__(WARPS * 32) packed_few_kernel(const __grid_con
     const int blocks = a.Hkv / warps, chunk = blockIdx.x / blocks;
     const int lead = (blockIdx.x - chunk * blocks) * warps, kh = lead + warp;
     if (blockIdx.x == 0) packed_check(a, tid, blockDim.x);
+    const bool whole = A.chunks == 0;
+    bool final = whole;  // no chunk behind this one
+    int c0, c1;
     Search search;
-    search.probe(a.cu_k, 0, a.n_seq);
-    const Cut cut = cut_of(A);
-    if (chunk >= cut.chunks) return;
-    const int c0 = chunk * cut.keys, c1 = min(cut.total, c0 + cut.keys);
+    if (whole) {
+        const PackedSeq p = packed_seq(a, chunk);
+        c0 = p.k0;
+        c1 = p.k0 + p.lk;
+    } else {
+        search.probe(a.cu_k, 0, a.n_seq);
+        const Cut cut = cut_of(A);
+        if (chunk >= cut.chunks) return;
+        final = chunk == cut.chunks - 1;
+        c0 = chunk * cut.keys;
+        c1 = min(cut.total, c0 + cut.keys);
+    }
 
     // Copies: 16 bytes of every fourth row of the block's heads. Places: [tile][K, V][head][key][16 bytes], the last
     // index turned by the key so that eight lanes of a reading warp find eight different 16 bytes of a 128-byte line.
@@ -170,9 +184,10 @@ __global__ void __launch_bounds__(WARPS * 32) packed_few_kernel(const __grid_con
     const uint8_t* kt = smem + (warp * TILE + n) * 128 + (t ^ (n & 1) << 2) * 16;
     const uint8_t* vt = smem + half + (warp * TILE + 2 * t) * 128 + (n ^ t << 1) * 16;
 
-    for (int s = search.find(a.cu_k, a.n_seq, c0); s < a.n_seq; s++) {
+    const int end = whole ? chunk + 1 : a.n_seq;
+    for (int s = whole ? chunk : search.find(a.cu_k, a.n_seq, c0); s < end; s++) {
         const PackedSeq p = packed_seq(a, s);
-        if (p.k0 >= c1 && chunk < cut.chunks - 1) break;
+        if (p.k0 >= c1 && !final) break;
         const int lq = min(p.lq, A.rows / A.group), R = lq * A.group;
         const int a0 = max(p.k0, c0), a1 = min(p.k0 + p.lk, c1);  // the chunk's rows of the sequence
         if (lq == 0 || (a0 >= a1 && p.lk)) continue;
@@ -289,7 +304,7 @@ __global__ void __launch_bounds__(WARPS * 32) packed_few_kernel(const __grid_con
             if (at + TILE > a1) break;  // the next sequence begins in this tile
         }
         // thread: rows n, n + 8, dims 16t .. 16t + 15
-        const bool all = a1 - a0 == p.lk || A.chunks == 1;  // the whole sequence
+        const bool all = a1 - a0 == p.lk || A.chunks <= 1;  // the whole sequence
 #pragma unroll
         for (int h = 0; h < 2; h++) {
             const int r = n + 8 * h, j = r / A.group, head = kh * A.group + r - j * A.group;
@@ -384,6 +399,7 @@ __global__ void __launch_bounds__(128) packed_few_join_kernel(const __grid_const
 }
 
 int chunks_of(int n_seq, int total_k, int max_k, int Hkv) {
+    if (max_k <= WHOLE) return 0;
     const int64_t all = min((int64_t)total_k, (int64_t)n_seq * max_k);
     return (int)max((int64_t)1, min((int64_t)FILL / Hkv, (all + MIN_KEYS - 1) / MIN_KEYS));
 }
@@ -394,7 +410,7 @@ bool attention_packed_few(int max_q, int Hq, int Hkv) { return (int64_t)max_q * 
 
 size_t attention_packed_few_scratch(int n_seq, int total_k, int max_q, int max_k, int Hq, int Hkv) {
     const int chunks = chunks_of(n_seq, total_k, max_k, Hkv);
-    if (chunks == 1) return 0;
+    if (chunks <= 1) return 0;
     return (size_t)(chunks + n_seq) * Hkv * max_q * (Hq / Hkv) * PART * 4;
 }
 
@@ -409,8 +425,8 @@ int launch_attention_packed_few(const PackedAttn& a, void* scratch, cudaStream_t
     int warps = WARPS;
     while (a.Hkv % warps) warps /= 2;
     if (smem_attr((const void*)packed_few_kernel, WARPS * NST * STAGE) != cudaSuccess) return GPT2_ERR_CUDA;
-    packed_few_kernel<<<A.chunks * (a.Hkv / warps), warps * 32, warps * NST * STAGE, s>>>(A);
-    if (A.chunks == 1 || A.rows == 0) return 1;
+    packed_few_kernel<<<(A.chunks ? A.chunks : a.n_seq) * (a.Hkv / warps), warps * 32, warps * NST * STAGE, s>>>(A);
+    if (A.chunks <= 1 || A.rows == 0) return 1;
     return launch_dependent(packed_few_join_kernel, a.n_seq * a.Hkv * A.rows, 128, 0, s, A) == cudaSuccess
                ? 2
                : GPT2_ERR_CUDA;
