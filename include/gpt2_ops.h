@@ -270,8 +270,8 @@ int gpt2_op_attention_packed_forward(int dtype, void* o, int64_t o_stride, float
  * group. dq [total_q] rows, dk, dv [total_k] rows (dtype, their own strides,
  * overwritten; rows of no sequence are left as they were, a key that no query
  * sees gets 0). Deterministic (no atomics). dq, dk, dv must not overlap the
- * inputs. Sequences, strides and limits as in the forward. Scratch: D and, for
- * bf16, lse beside it and the lists of work items. */
+ * inputs. Sequences, strides and limits as in the forward. Scratch (bf16): lse
+ * and D, the lists of work items. */
 size_t gpt2_op_attention_packed_backward_scratch(int dtype, int n_seq, int total_q, int total_k, int Hq, int Hkv,
                                                  int hd);
 int gpt2_op_attention_packed_backward(int dtype, void* dq, int64_t dq_stride, void* dk, int64_t dk_stride, void* dv,

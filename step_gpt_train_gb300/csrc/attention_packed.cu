@@ -132,9 +132,9 @@ int launch_attention_packed_forward(int dtype, const PackedAttn& a, void* scratc
 }
 
 size_t attention_packed_backward_scratch(int dtype, int n_seq, int total_q, int total_k, int Hq, int Hkv, int hd) {
-    if (dtype == GPT2_MODE_BF16 && Hq / Hkv <= 64)
-        return attention_packed_backward_tc_scratch(n_seq, total_q, total_k, Hq, Hkv);
-    return (size_t)Hq * total_q * 4;
+    if (dtype != GPT2_MODE_BF16) return 0;
+    if (Hq / Hkv <= 64) return attention_packed_backward_tc_scratch(n_seq, total_q, total_k, Hq, Hkv);
+    return (size_t)Hq * total_q * 4;  // D
 }
 
 int launch_attention_packed_backward(int dtype, const PackedAttn& a, const PackedAttnGrad& grad, void* scratch,

@@ -27,6 +27,7 @@ struct Args {
     PackedAttn a;
     PackedAttnGrad g;
     int group;
+    int key_blocks;  // backward: the blocks of dK, dV, before those of dQ
     float scale, scale_log2;
 };
 
@@ -135,11 +136,11 @@ struct Rows {
     }
 };
 
-// The block's sequence, key head and first row of its tile; false for none.
-__device__ __forceinline__ bool row_tile(const Args& A, PackedSeq& p, int& kh, int& at) {
+// The sequence, key head and first row of the tile of a block of `blocks`; false for none.
+__device__ __forceinline__ bool row_tile(const Args& A, int block, int blocks, PackedSeq& p, int& kh, int& at) {
     const PackedAttn& a = A.a;
-    const int slots = gridDim.x / a.Hkv, i = blockIdx.x / a.Hkv;
-    kh = blockIdx.x - i * a.Hkv;
+    const int slots = blocks / a.Hkv, i = block / a.Hkv;
+    kh = block - i * a.Hkv;
     const int slot = slots - 1 - i;  // the later rows of a sequence, which see more keys, first
     int first;
     const int s = find_slot(a.cu_q, a.n_seq, a.total_q, TL, slot, first, A.group);
@@ -158,7 +159,7 @@ template <int HD> __global__ void __launch_bounds__(NT) packed_fwd_f32_kernel(co
     if (blockIdx.x == 0) packed_check(a, tid, NT);
     PackedSeq p;
     int kh, at;
-    if (!row_tile(A, p, kh, at)) return;
+    if (!row_tile(A, blockIdx.x, gridDim.x, p, kh, at)) return;
     const Rows rows = {p.q0, A.group, kh * A.group};
     const int n = min(TL, p.lq * A.group - at);
     load_tile<HD>(sq, n, [&](int r) { return rows.at(a.q, a.q_stride, HD, at + r); });
@@ -236,17 +237,15 @@ template <int HD> __global__ void __launch_bounds__(NT) packed_fwd_f32_kernel(co
     }
 }
 
-// dQ of 64 rows, and their D = rowsum(dO * O) for the other kernel.
-template <int HD> __global__ void __launch_bounds__(NT) packed_dq_f32_kernel(const __grid_constant__ Args A) {
+// dQ of 64 rows.
+template <int HD> __device__ __forceinline__ void dq_rows(const Args& A, float* sm, int block, int blocks) {
     using S = Shape<HD>;
     const PackedAttn& a = A.a;
-    extern __shared__ __align__(16) float sm[];
     float *sq = sm, *sy = sm + S::T, *sk = sy + S::T, *sv = sk + S::T, *sp = sv + S::T;
     const int tid = threadIdx.x, tx = tid % TX, ty = tid / TX;
-    if (blockIdx.x == 0) packed_check(a, tid, NT);
     PackedSeq p;
     int kh, at;
-    if (!row_tile(A, p, kh, at)) return;
+    if (!row_tile(A, block, blocks, p, kh, at)) return;
     const Rows rows = {p.q0, A.group, kh * A.group};
     const int n = min(TL, p.lq * A.group - at);
     load_tile<HD>(sq, n, [&](int r) { return rows.at(a.q, a.q_stride, HD, at + r); });
@@ -269,7 +268,6 @@ template <int HD> __global__ void __launch_bounds__(NT) packed_dq_f32_kernel(con
             if (vis[r] > 0) lse2[r] = a.lse[rows.stat(a.total_q, at + i)] * LOG2E;
         }
         D[r] = row_sum(d);
-        if (i < n && tx == 0) A.g.D[rows.stat(a.total_q, at + i)] = D[r];
 #pragma unroll
         for (int e = 0; e < S::DV; e++) dq[r][e] = 0.f;
     }
@@ -307,16 +305,15 @@ template <int HD> __global__ void __launch_bounds__(NT) packed_dq_f32_kernel(con
     }
 }
 
-// dK, dV of 64 keys of one key head.
-template <int HD> __global__ void __launch_bounds__(NT) packed_dkdv_f32_kernel(const __grid_constant__ Args A) {
+// dK, dV of 64 keys of one key head; D = rowsum(dO * O) of each block of rows
+// on the way, so that nothing waits for dQ.
+template <int HD> __device__ __forceinline__ void dkdv_keys(const Args& A, float* sm, int block) {
     using S = Shape<HD>;
     const PackedAttn& a = A.a;
-    extern __shared__ __align__(16) float sm[];
     float *sk = sm, *sv = sm + S::T, *sq = sv + S::T, *sy = sq + S::T, *sp = sy + S::T, *sd = sp + TL * LP;
     float* stat = sd + TL * LP;  // lse log2(e), D of the block's rows
     const int tid = threadIdx.x, tx = tid % TX, ty = tid / TX;
-    if (a.total_q == 0 && blockIdx.x == 0) packed_check(a, tid, NT);
-    const int slot = blockIdx.x / a.Hkv, kh = blockIdx.x - slot * a.Hkv;
+    const int slot = block / a.Hkv, kh = block - slot * a.Hkv;
     int first;
     const int s0 = find_slot(a.cu_k, a.n_seq, a.total_k, TL, slot, first);
     if (s0 < 0) return;
@@ -337,20 +334,32 @@ template <int HD> __global__ void __launch_bounds__(NT) packed_dkdv_f32_kernel(c
         const int n = min(TL, all - i);
         load_tile<HD>(sq, n, [&](int r) { return rows.at(a.q, a.q_stride, HD, i + r); });
         load_tile<HD>(sy, n, [&](int r) { return rows.at(A.g.dout, A.g.dout_stride, HD, i + r); });
-        for (int r = tid; r < 2 * TL; r += NT) {
-            const int row = r % TL;
-            float v = 0.f;
-            if (row < n) {
-                v = (r < TL ? a.lse : A.g.D)[rows.stat(a.total_q, i + row)];
-                if (r < TL) v = v == -INFINITY ? 0.f : v * LOG2E;
-            }
-            stat[r] = v;
+        if (tid < TL) {
+            const float v = tid < n ? a.lse[rows.stat(a.total_q, i + tid)] : 0.f;
+            stat[tid] = v == -INFINITY ? 0.f : v * LOG2E;
+        }
+        constexpr int Q = HD / 4;  // four threads to a row of O
+        const int drow = tid / 4, dcol = tid % 4 * Q;
+        float o[Q];
+#pragma unroll
+        for (int e = 0; e < Q; e++) o[e] = 0.f;
+        if (drow < n) {
+            const float* x = rows.at(a.o, a.o_stride, HD, i + drow) + dcol;
+#pragma unroll
+            for (int e = 0; e < Q; e += 2) *reinterpret_cast<float2*>(o + e) = *reinterpret_cast<const float2*>(x + e);
         }
         cp_async_wait<0>();
         __syncthreads();
+        float d = 0.f;
+#pragma unroll
+        for (int e = 0; e < Q; e++) d += o[e] * sy[drow * S::LD + dcol + e];
+        d += __shfl_xor_sync(0xffffffffu, d, 1);
+        d += __shfl_xor_sync(0xffffffffu, d, 2);
+        if (tid % 4 == 0) stat[TL + drow] = d;
         float s[NR][NC], dp[NR][NC];
         dots<HD>(s, sk, sq, ty, tx);
         dots<HD>(dp, sv, sy, ty, tx);
+        __syncthreads();  // D
 #pragma unroll
         for (int c = 0; c < NC; c++) {
             const int row = tx + TX * c;
@@ -388,6 +397,15 @@ template <int HD> __global__ void __launch_bounds__(NT) packed_dkdv_f32_kernel(c
     }
 }
 
+// Both gradients in one launch: on 9 chunks of up to 400 tokens, where the
+// longest sequence's blocks take as long as the rest, dQ beside dK, dV.
+template <int HD> __global__ void __launch_bounds__(NT) packed_bwd_f32_kernel(const __grid_constant__ Args A) {
+    extern __shared__ __align__(16) float sm[];
+    if (blockIdx.x == 0) packed_check(A.a, threadIdx.x, NT);
+    if ((int)blockIdx.x < A.key_blocks) dkdv_keys<HD>(A, sm, blockIdx.x);
+    else dq_rows<HD>(A, sm, blockIdx.x - A.key_blocks, gridDim.x - A.key_blocks);
+}
+
 Args args_of(const PackedAttn& a) {
     Args A = {};
     A.a = a;
@@ -408,16 +426,14 @@ template <int HD> int forward(const PackedAttn& a, cudaStream_t s) {
     return 1;
 }
 template <int HD> int backward(const PackedAttn& a, const PackedAttnGrad& g, cudaStream_t s) {
-    constexpr int SMEM_Q = (4 * Shape<HD>::T + TL * LP) * 4, SMEM_K = (4 * Shape<HD>::T + 2 * TL * LP + 2 * TL) * 4;
-    const auto dq = packed_dq_f32_kernel<HD>;
-    const auto dkdv = packed_dkdv_f32_kernel<HD>;
-    if (smem_attr((const void*)dq, SMEM_Q) != cudaSuccess || smem_attr((const void*)dkdv, SMEM_K) != cudaSuccess)
-        return GPT2_ERR_CUDA;
+    constexpr int SMEM = (4 * Shape<HD>::T + 2 * TL * LP + 2 * TL) * 4;  // (dQ uses less)
+    const auto kernel = packed_bwd_f32_kernel<HD>;
+    if (smem_attr((const void*)kernel, SMEM) != cudaSuccess) return GPT2_ERR_CUDA;
     Args A = args_of(a);
     A.g = g;
-    if (a.total_q) dq<<<row_blocks(a), NT, SMEM_Q, s>>>(A);
-    if (a.total_k) dkdv<<<packed_slots(a.total_k, a.n_seq, TL) * a.Hkv, NT, SMEM_K, s>>>(A);
-    return (a.total_q > 0) + (a.total_k > 0);
+    A.key_blocks = a.total_k ? packed_slots(a.total_k, a.n_seq, TL) * a.Hkv : 0;
+    kernel<<<A.key_blocks + (a.total_q ? row_blocks(a) : 0), NT, SMEM, s>>>(A);
+    return 1;
 }
 
 }  // namespace
