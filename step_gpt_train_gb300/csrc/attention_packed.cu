@@ -118,8 +118,8 @@ int backward_wide(const PackedAttn& a, const PackedAttnGrad& g, cudaStream_t s) 
 
 size_t attention_packed_forward_scratch(int dtype, int n_seq, int total_q, int total_k, int max_q, int max_k, int Hq,
                                         int Hkv, int hd) {
-    if (dtype != GPT2_MODE_BF16) return 0;
-    if (attention_packed_few(max_q, Hq, Hkv)) 
+    if (dtype != GPT2_MODE_BF16) return attention_packed_forward_f32_scratch(n_seq, total_q, Hq, Hkv);
+    if (attention_packed_few(max_q, Hq, Hkv))
         return attention_packed_few_scratch(n_seq, total_k, max_q, max_k, Hq, Hkv);
     return attention_packed_forward_tc_scratch(n_seq, total_q, Hq, Hkv);
 }
@@ -128,7 +128,7 @@ int launch_attention_packed_forward(int dtype, const PackedAttn& a, void* scratc
     if (dtype == GPT2_MODE_BF16 && attention_packed_few(a.max_q, a.Hq, a.Hkv))
         return launch_attention_packed_few(a, scratch, s);
     if (dtype == GPT2_MODE_BF16) return launch_attention_packed_forward_tc(a, (PackedPlan*)scratch, s);
-    return launch_attention_packed_forward_f32(a, s);
+    return launch_attention_packed_forward_f32(a, (PackedPlan*)scratch, s);
 }
 
 size_t attention_packed_backward_scratch(int dtype, int n_seq, int total_q, int total_k, int Hq, int Hkv, int hd) {

@@ -10,10 +10,11 @@
 // with P or dS walk 16-byte pieces of a P row: either way 8 shared 16-byte
 // loads feed 64 FMA a thread, and the row padding of four floats spreads the
 // rows that a warp reads at once over the banks. (128 threads with twice the
-// columns load a quarter less and took as long: 93 against 92 us on 16
-// documents of 3582 tokens, where the FMA of the tiles, the masked halves of
-// the diagonal ones included, take 33 and all instructions 51; the rest is the
-// blocks' unequal lengths.) Gradients have one writer each: deterministic.
+// columns load a quarter less and took as long.) The forward's tiles are sorted,
+// the longest first, where they come in several rounds: 16 documents of 3582
+// tokens and 12 heads take 78 us (unsorted 91), of which the FMA of the tiles,
+// the masked halves of the diagonal ones included, are 33 and all instructions
+// 51. Gradients have one writer each: deterministic.
 #include "attention_packed.cuh"
 
 namespace {
@@ -27,6 +28,7 @@ struct Args {
     PackedAttn a;
     PackedAttnGrad g;
     int group;
+    const PackedPlan* plan;  // forward: its tiles, or null
     int key_blocks;  // backward: the blocks of dK, dV, before those of dQ
     float scale, scale_log2;
 };
@@ -59,7 +61,7 @@ template <int HD> __device__ __forceinline__ void dots(float (&s)[NR][NC], const
     for (int r = 0; r < 4; r++)
 #pragma unroll
         for (int c = 0; c < NC; c++) s[r][c] = 0.f;
-#pragma unroll 2
+#pragma unroll 4
     for (int d = 0; d < HD; d += 4) {
         float4 x[NR], y[NC];
 #pragma unroll
@@ -78,7 +80,7 @@ template <int HD> __device__ __forceinline__ void dots(float (&s)[NR][NC], const
 template <int HD>
 __device__ __forceinline__ void products(float (&o)[4][Shape<HD>::DV], const float* P, const float* B, int ty, int tx) {
     constexpr int LD = Shape<HD>::LD, DV = Shape<HD>::DV;
-#pragma unroll 2
+#pragma unroll 4
     for (int j = 0; j < TL; j += 4) {
         float p[4][4];
 #pragma unroll
@@ -136,18 +138,37 @@ struct Rows {
     }
 };
 
-// The sequence, key head and first row of the tile of a block of `blocks`; false for none.
-__device__ __forceinline__ bool row_tile(const Args& A, int block, int blocks, PackedSeq& p, int& kh, int& at) {
+// Up to TL rows of a key head: rows at .. at + n - 1 from query q0 on, the keys of their sequence, and how many of
+// those query q0 sees.
+struct RowTile {
+    int kh, q0, at, n, k0, lk, sees;
+    __device__ __forceinline__ int keys(int i, int group) const { return max(0, min(lk, (at + i) / group + sees)); }
+};
+// The tile of a block of `blocks`; false for none.
+__device__ __forceinline__ bool row_tile(const Args& A, int block, int blocks, RowTile& t) {
     const PackedAttn& a = A.a;
     const int slots = blocks / a.Hkv, i = block / a.Hkv;
-    kh = block - i * a.Hkv;
+    t.kh = block - i * a.Hkv;
+    if (A.plan) {  // the longest tiles first
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (i >= A.plan->count) return false;
+        const PackedTile p = A.plan->tile[i];
+        t.q0 = p.r0, t.at = 0, t.n = p.n * A.group, t.k0 = p.s0, t.lk = p.len, t.sees = p.shift;
+        return true;
+    }
     const int slot = slots - 1 - i;  // the later rows of a sequence, which see more keys, first
     int first;
     const int s = find_slot(a.cu_q, a.n_seq, a.total_q, TL, slot, first, A.group);
     if (s < 0) return false;
-    p = packed_seq(a, s);
-    at = (slot - first) * TL;
-    return at < p.lq * A.group;
+    const PackedSeq p = packed_seq(a, s);
+    t.q0 = p.q0, t.at = (slot - first) * TL, t.n = min(TL, p.lq * A.group - t.at);
+    t.k0 = p.k0, t.lk = p.lk, t.sees = 1 + p.lk - p.lq;
+    return t.n > 0;
+}
+
+__global__ void __launch_bounds__(1024) packed_plan_f32_kernel(PackedAttn a, PackedCut cut, PackedPlan* plan) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    packed_plan_block(a, cut, plan, true);
 }
 
 template <int HD> __global__ void __launch_bounds__(NT) packed_fwd_f32_kernel(const __grid_constant__ Args A) {
@@ -156,20 +177,19 @@ template <int HD> __global__ void __launch_bounds__(NT) packed_fwd_f32_kernel(co
     extern __shared__ __align__(16) float sm[];
     float *sq = sm, *sk = sm + S::T, *sv = sk + S::T, *sp = sv + S::T;
     const int tid = threadIdx.x, tx = tid % TX, ty = tid / TX;
-    if (blockIdx.x == 0) packed_check(a, tid, NT);
-    PackedSeq p;
-    int kh, at;
-    if (!row_tile(A, blockIdx.x, gridDim.x, p, kh, at)) return;
+    if (blockIdx.x == 0 && !A.plan) packed_check(a, tid, NT);
+    RowTile p;
+    if (!row_tile(A, blockIdx.x, gridDim.x, p)) return;
+    const int kh = p.kh, at = p.at, n = p.n;
     const Rows rows = {p.q0, A.group, kh * A.group};
-    const int n = min(TL, p.lq * A.group - at);
     load_tile<HD>(sq, n, [&](int r) { return rows.at(a.q, a.q_stride, HD, at + r); });
     int vis[4];  // keys that the row sees
 #pragma unroll
     for (int r = 0; r < 4; r++) {
         const int i = ty + 16 * r;
-        vis[r] = i < n ? min(p.lk, (at + i) / A.group + 1 + p.lk - p.lq) : 0;
+        vis[r] = i < n ? p.keys(i, A.group) : 0;
     }
-    const int keys = max(0, min(p.lk, (at + n - 1) / A.group + 1 + p.lk - p.lq));  // that any row sees
+    const int keys = p.keys(n - 1, A.group);  // that any row sees
     float m[4], l[4], o[4][S::DV];
 #pragma unroll
     for (int r = 0; r < 4; r++) {
@@ -243,11 +263,10 @@ template <int HD> __device__ __forceinline__ void dq_rows(const Args& A, float* 
     const PackedAttn& a = A.a;
     float *sq = sm, *sy = sm + S::T, *sk = sy + S::T, *sv = sk + S::T, *sp = sv + S::T;
     const int tid = threadIdx.x, tx = tid % TX, ty = tid / TX;
-    PackedSeq p;
-    int kh, at;
-    if (!row_tile(A, block, blocks, p, kh, at)) return;
+    RowTile p;
+    if (!row_tile(A, block, blocks, p)) return;
+    const int kh = p.kh, at = p.at, n = p.n;
     const Rows rows = {p.q0, A.group, kh * A.group};
-    const int n = min(TL, p.lq * A.group - at);
     load_tile<HD>(sq, n, [&](int r) { return rows.at(a.q, a.q_stride, HD, at + r); });
     load_tile<HD>(sy, n, [&](int r) { return rows.at(A.g.dout, A.g.dout_stride, HD, at + r); });
     int vis[4];
@@ -257,7 +276,7 @@ template <int HD> __device__ __forceinline__ void dq_rows(const Args& A, float* 
 #pragma unroll
     for (int r = 0; r < 4; r++) {
         const int i = ty + 16 * r;
-        vis[r] = i < n ? min(p.lk, (at + i) / A.group + 1 + p.lk - p.lq) : 0;
+        vis[r] = i < n ? p.keys(i, A.group) : 0;
         float d = 0.f;
         lse2[r] = 0.f;
         if (i < n) {
@@ -271,7 +290,7 @@ template <int HD> __device__ __forceinline__ void dq_rows(const Args& A, float* 
 #pragma unroll
         for (int e = 0; e < S::DV; e++) dq[r][e] = 0.f;
     }
-    const int keys = max(0, min(p.lk, (at + n - 1) / A.group + 1 + p.lk - p.lq));
+    const int keys = p.keys(n - 1, A.group);
     for (int j = 0; j < keys; j += TL) {
         const int nk = min(TL, keys - j);
         load_tile<HD>(sk, nk, [&](int r) { return (const float*)a.k + (int64_t)(p.k0 + j + r) * a.k_stride + kh * HD; });
@@ -397,8 +416,9 @@ template <int HD> __device__ __forceinline__ void dkdv_keys(const Args& A, float
     }
 }
 
-// Both gradients in one launch: on 9 chunks of up to 400 tokens, where the
-// longest sequence's blocks take as long as the rest, dQ beside dK, dV.
+// Both gradients in one launch, dQ beside dK and dV: 9 chunks of up to 400
+// tokens (6 heads of 32 on 2), bound by the longest sequence's chain of tiles,
+// take 29 us, one after the other 47.
 template <int HD> __global__ void __launch_bounds__(NT) packed_bwd_f32_kernel(const __grid_constant__ Args A) {
     extern __shared__ __align__(16) float sm[];
     if (blockIdx.x == 0) packed_check(A.a, threadIdx.x, NT);
@@ -418,12 +438,28 @@ int row_blocks(const PackedAttn& a) {  // slots of the rows, times the key heads
     return (int)((int64_t)a.total_q * (a.Hq / a.Hkv) / TL + a.n_seq) * a.Hkv;
 }
 
-template <int HD> int forward(const PackedAttn& a, cudaStream_t s) {
+// The forward's sorted tiles of whole queries; with fewer blocks than are at work
+// at once the sort would only be a launch more.
+constexpr int SORT_BLOCKS = 2 * 152;
+PackedCut row_cut(int Hq, int Hkv) { return PackedCut{false, max(1, TL / (Hq / Hkv)), TL}; }
+size_t plan_bytes(int n_seq, int total_q, int Hq, int Hkv) {
+    const int slots = packed_slots(total_q, n_seq, row_cut(Hq, Hkv).per);
+    return Hq / Hkv <= TL && slots <= PACKED_PLAN_MAX && (int64_t)slots * Hkv > SORT_BLOCKS ? packed_plan_bytes(slots) : 0;
+}
+
+template <int HD> int forward(const PackedAttn& a, PackedPlan* plan, cudaStream_t s) {
     constexpr int SMEM = (3 * Shape<HD>::T + TL * LP) * 4;
     const auto kernel = packed_fwd_f32_kernel<HD>;
     if (smem_attr((const void*)kernel, SMEM) != cudaSuccess) return GPT2_ERR_CUDA;
-    kernel<<<row_blocks(a), NT, SMEM, s>>>(args_of(a));
-    return 1;
+    Args A = args_of(a);
+    if (!plan_bytes(a.n_seq, a.total_q, a.Hq, a.Hkv)) {
+        kernel<<<row_blocks(a), NT, SMEM, s>>>(A);
+        return 1;
+    }
+    const PackedCut cut = row_cut(a.Hq, a.Hkv);
+    A.plan = plan;
+    packed_plan_f32_kernel<<<1, 1024, 0, s>>>(a, cut, plan);
+    return launch_dependent(kernel, cut.slots(a) * a.Hkv, NT, SMEM, s, A) == cudaSuccess ? 2 : GPT2_ERR_CUDA;
 }
 template <int HD> int backward(const PackedAttn& a, const PackedAttnGrad& g, cudaStream_t s) {
     constexpr int SMEM = (4 * Shape<HD>::T + 2 * TL * LP + 2 * TL) * 4;  // (dQ uses less)
@@ -438,12 +474,16 @@ template <int HD> int backward(const PackedAttn& a, const PackedAttnGrad& g, cud
 
 }  // namespace
 
-int launch_attention_packed_forward_f32(const PackedAttn& a, cudaStream_t s) {
+size_t attention_packed_forward_f32_scratch(int n_seq, int total_q, int Hq, int Hkv) {
+    return plan_bytes(n_seq, total_q, Hq, Hkv);
+}
+
+int launch_attention_packed_forward_f32(const PackedAttn& a, PackedPlan* plan, cudaStream_t s) {
     switch (a.hd) {
-        case 8: return forward<8>(a, s);
-        case 16: return forward<16>(a, s);
-        case 32: return forward<32>(a, s);
-        default: return forward<64>(a, s);
+        case 8: return forward<8>(a, plan, s);
+        case 16: return forward<16>(a, plan, s);
+        case 32: return forward<32>(a, plan, s);
+        default: return forward<64>(a, plan, s);
     }
 }
 

@@ -124,10 +124,11 @@ struct PackedAttnGrad {
 };
 size_t attention_packed_forward_scratch(int dtype, int n_seq, int total_q, int total_k, int max_q, int max_k, int Hq,
                                         int Hkv, int hd);
-int launch_attention_packed_forward_f32(const PackedAttn& a, cudaStream_t s);
+struct PackedPlan;
+size_t attention_packed_forward_f32_scratch(int n_seq, int total_q, int Hq, int Hkv);
+int launch_attention_packed_forward_f32(const PackedAttn& a, PackedPlan* plan, cudaStream_t s);
 int launch_attention_packed_backward_f32(const PackedAttn& a, const PackedAttnGrad& g, cudaStream_t s);
 // bf16 on the tensor cores.
-struct PackedPlan;
 size_t attention_packed_forward_tc_scratch(int n_seq, int total_q, int Hq, int Hkv);
 int launch_attention_packed_forward_tc(const PackedAttn& a, PackedPlan* plan, cudaStream_t s);
 // bf16 with at most 16 rows (queries x heads of a group) to a key head of a sequence.
