@@ -305,17 +305,18 @@ __global__ void __launch_bounds__(NT)
 
     if constexpr (TOP) {
         static_assert(NT >= 4 * MAX_K && CAND == 2 * NT, "the sizes below");
-        // The k-th largest of the maxima of 64 groups of four threads (of the threads for k above 32) bounds the
-        // k-th largest logit from below. -inf and no data come out as the lowest.
+        // The k-th largest of the maxima of 64 groups of four threads (of the threads, where fewer than 2 k groups have
+        // data) bounds the k-th largest logit from below. -inf and no data come out as the lowest.
         const bool any = v0 + tid < v1;
         const uint32_t key = any ? (uint32_t)(order_key(mine, 0) >> 32) : 0;
-        const int groups = k > 32 ? NT : NT / 4;
+        const bool fours = min(NT, v1 - v0) >= 8 * k;
+        const int groups = fours ? NT / 4 : NT;
         uint32_t most = key;
-        if (k <= 32) {
+        if (fours) {
             most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
             most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
         }
-        if (k > 32) maxima[tid] = most;
+        if (!fours) maxima[tid] = most;
         else if (lane % 4 == 0) maxima[tid / 4] = most;
         if (tid == 0) bound = ~0u, count = 0;
         __syncthreads();
@@ -477,8 +478,8 @@ constexpr int TB = 4;      // vectors of its batch
 constexpr int TOP_BLOCKS = 3;  // on an SM
 constexpr int RING = 2;    // batches that a reading thread has in shared memory or on their way
 constexpr int LOOK = 16;   // threads whose vectors the search has in shared memory at once, 32 of each
-constexpr int LIST = 256;  // candidates that fit
-constexpr int MANY = 128;  // of the reading threads reach the bound: equal logits (k threads, or 32 groups of 4, at most else)
+constexpr int LIST = 512;  // candidates that fit (all logits of a row with fewer than MAX_K vectors)
+constexpr int MANY = 128;  // of the reading threads reach the bound: equal logits (k threads, or k groups of four, else)
 struct Search {            // a searching warp's own
     uint4 part[LOOK][32];
     uint64_t keys[LIST], out[MAX_K];
@@ -589,10 +590,9 @@ __global__ void __launch_bounds__(TNT + 64, TOP_BLOCKS)
             if (entropy) entropy[row] = x.m == -INFINITY ? 0.f : LN2 * (log2f(x.s) - x.t / x.s);
             if (logp) logp[row] = x.m == -INFINITY ? -INFINITY : zt - L;
         }
-        // The k-th largest of the maxima of 64 groups of four threads (of the threads for k above 32) bounds the
-        // k-th largest logit from below.
+        // The bound as above.
         uint32_t least = ~0u;
-        if (k <= 32) {
+        if (min(TNT, nv) >= 8 * k) {
             static_assert(TNT == 256, "two groups of four threads to a lane");
             uint32_t own[2];
             int above[2] = {0, 0};

@@ -447,7 +447,7 @@ def check_logprobs_backward(torch, z, t, V, mode, zt, tt, lse, ent, seed=5):
 
 
 @pytest.mark.parametrize("mode", [1, 0], ids=["bf16", "fp32"])
-@pytest.mark.parametrize("N,V,Vp,k", [(1, 1, 8, 1), (3, 7, 8, 7), (5, 64, 64, 64), (4, 300, 304, 5), (257, 512, 512, 3),
+@pytest.mark.parametrize("N,V,Vp,k", [(1, 1, 8, 1), (3, 7, 8, 7), (5, 64, 64, 64), (4, 300, 304, 5), (257, 512, 512, 3), (5, 503, 512, 32), (7, 477, 480, 64),
                                       (9, 4097, 4104, 33), (6, 50257, 50304, 20), (3, 50257, 50304, 0),
                                       (2, 130001, 130048, 64), (1, 300001, 300008, 8)])
 def test_logprobs(torch_cuda, N, V, Vp, k, mode):
@@ -503,7 +503,7 @@ def test_logprobs_non_finite_rows(torch_cuda):
 
 
 @pytest.mark.parametrize("mode", [1, 0], ids=["bf16", "fp32"])
-@pytest.mark.parametrize("V,k", [(40, 40), (1000, 20), (1000, 64), (50257, 5), (50257, 40)])
+@pytest.mark.parametrize("V,k", [(40, 40), (477, 32), (503, 64), (1000, 20), (1000, 64), (50257, 5), (50257, 40)])
 def test_logprobs_alternatives_of_many_rows(torch_cuda, V, k, mode):
     """More rows than SMs, ties, masks and NaN among them."""
     Vp, N = -(-V // 8) * 8 + 8, 331
