@@ -478,7 +478,7 @@ constexpr int TB = 4;      // vectors of its batch
 constexpr int TOP_BLOCKS = 3;  // on an SM
 constexpr int RING = 2;    // batches that a reading thread has in shared memory or on their way
 constexpr int LOOK = 16;   // threads whose vectors the search has in shared memory at once, 32 of each
-constexpr int LIST = 512;  // candidates that fit (all logits of a row with fewer than MAX_K vectors)
+constexpr int LIST = 256;  // candidates that fit (all logits of a row with fewer than 32 vectors)
 constexpr int MANY = 128;  // of the reading threads reach the bound: equal logits (k threads, or k groups of four, else)
 struct Search {            // a searching warp's own
     uint4 part[LOOK][32];
@@ -852,12 +852,16 @@ int forward_top(float* logp, float* lse, float* entropy, float* top_logp, int32_
 }
 // Threads of a block: twice as many rows on their way in blocks of 128 read
 // 32768 rows of 50257 at the speed of a copy (496 us; 535 with 256), but few
-// rows want the wider block.
+// rows want the wider block. With alternatives, rows are handed to searching
+// warps where a block for each (four to an SM) would come in more than one
+// round, and for k up to 32 (rows of 50257 with 20: 600 take 25 us handed over
+// and 18 a block each, 1000 31 either way, 2043 51 and 59; 8192 rows of 32768
+// with 20 142 and 158, with 64 331 and 264).
 template <typename T, typename... A>
 int forward_of(int k, int N, A... args) {
-    const bool many = N > gpt2_num_sms();
-    if (k) return many ? forward_top<T>(args...) : forward<T, 256, true>(args...);
-    return many ? forward<T, 128, false>(args...) : forward<T, 256, false>(args...);
+    const int sms = gpt2_num_sms();
+    if (k) return k <= 32 && N > 4 * sms ? forward_top<T>(args...) : forward<T, 256, true>(args...);
+    return N > sms ? forward<T, 128, false>(args...) : forward<T, 256, false>(args...);
 }
 
 template <typename T>
