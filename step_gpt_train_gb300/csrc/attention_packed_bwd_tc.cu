@@ -29,6 +29,10 @@
 // (while the next item runs); 8..15, 16..23 elementwise. Every wait is bounded.
 // Before them a pass forms D = rowsum(dO * O) and lse log2(e) per row and sorts
 // the items.
+//
+// Measured: 62 documents of 100 to 1024 tokens, 12 heads, 174 us in all (50
+// GFLOP: 285 TFLOP/s; HBM would take 44). Bound by the elementwise warps' chain;
+// the tensor cores are busy 22% of the time in either kernel.
 #include "attention_packed_tc.cuh"
 
 namespace {

@@ -32,6 +32,12 @@
 // warps go on with the next item (short documents spent more on the way out
 // than on their blocks); 8..15 softmax. Registers: 184 a thread for the
 // softmax warps, 72 for the others. Every wait is bounded.
+//
+// Measured: 62 documents of 100 to 1024 tokens, 12 heads, 71 us; 16 prompts of
+// up to 4096 tokens, 16 heads on 4, 97 us (75 GFLOP: 770 TFLOP/s). Bound by the
+// softmax warps' chain of about 2000 cycles a block (wait, 128 scores from TMEM,
+// exponentials, P back), two such warps to a scheduler; the exponential unit
+// alone would take 17 and 44 us, the tensor cores 10 and 38.
 #include "attention_packed_tc.cuh"
 
 namespace {
