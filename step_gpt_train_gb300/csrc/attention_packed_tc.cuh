@@ -51,9 +51,7 @@ __device__ __forceinline__ void tc_ld16_wait(uint32_t (&r)[16]) {
 }
 
 // Bounded wait by a whole warp for the phase with the given parity: one try
-// and one vote a turn. Roles off the critical path sleep NS nanoseconds between
-// turns, so that their turns do not take the other warps' issue slots.
-template <int NS = 0>
+// and one vote a turn.
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
     if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
     const long long t0 = clock64();
@@ -61,7 +59,6 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
 #pragma unroll 1
     for (uint32_t n = 1;; n++) {
         if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
-        if (NS) __nanosleep(NS);
         if (n % 64 == 0) {
             const bool late = clock64() - t0 > limit;
             if (late) {
