@@ -623,6 +623,16 @@ def _give_back(address):
         _torch.cuda.caching_allocator_delete(address)
 
 
+def _mode_of(what, t):
+    """The mode of a tensor's type; nothing but the two that the kernels read is taken."""
+    dtype = t.dtype
+    if dtype is _tc().bfloat16:
+        return MODE_BF16
+    if dtype is _torch.float32:
+        return MODE_FP32
+    raise ValueError(f"{what}: bfloat16 or float32 is needed, not {dtype}")
+
+
 def _rows(what, like, *more):
     """Row strides of [rows, heads, hd] tensors of one shape and type whose heads are contiguous in a row."""
     shape, dtype, strides = like.shape, like.dtype, []
@@ -639,11 +649,20 @@ def _rows(what, like, *more):
     return strides
 
 
+def _arrays(what, dtype, shape, *tensors):
+    """Contiguous tensors of one type and shape; None passes."""
+    for t in tensors:
+        if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()):
+            raise ValueError(f"{what}: contiguous {dtype} of shape {tuple(shape)} is needed")
+
+
 def _sequences(cu_q, cu_k):
-    n, i32 = cu_q.shape[0] - 1, _tc().int32
-    if cu_k.shape[0] - 1 != n or cu_q.dtype is not i32 or cu_k.dtype is not i32:
+    shape, i32 = cu_q.shape, _tc().int32
+    if len(shape) != 1 or shape[0] < 1 or cu_k.shape != shape or cu_q.dtype is not i32 or cu_k.dtype is not i32:
         raise ValueError("cu_q and cu_k need the same number of sequences, as int32")
-    return n
+    if not cu_q.is_contiguous() or not cu_k.is_contiguous():
+        raise ValueError("cu_q and cu_k have to be contiguous")
+    return shape[0] - 1
 
 
 def _logits(t):
@@ -658,14 +677,15 @@ def gpt2_op_attention_packed_forward(o, lse, q, k, v, cu_q, cu_k, max_q, max_k, 
     k and v [total_k, Hkv, hd] (each may be a column block of a wider buffer), cu_q and cu_k int32 [n_seq + 1]
     CUDA offsets, max_q and max_k the longest sequence's queries and keys."""
     lib = load_library()
-    dt = _dtype_of(q)
+    dt = _mode_of("q", q)
+    sq, so = _rows("q and o", q, o)
+    sk, sv = _rows("k and v", k, v)
     tq, hq, hd = q.shape
     tk, hkv, d = k.shape
     n = _sequences(cu_q, cu_k)
-    sq, so = _rows("q and o", q, o)
-    sk, sv = _rows("k and v", k, v)
-    if k.dtype is not q.dtype or d != hd or lse.shape != (hq, tq):
-        raise ValueError("k like q in type and head size, and lse [Hq, total_q], are needed")
+    if k.dtype is not q.dtype or d != hd:
+        raise ValueError("k like q in type and head size is needed")
+    _arrays("lse [Hq, total_q]", _torch.float32, (hq, tq), lse)
     nb = lib.gpt2_op_attention_packed_forward_scratch(dt, n, tq, tk, max_q, max_k, hq, hkv, hd)
     args = (dt, o.data_ptr(), so, lse.data_ptr(), q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv,
             cu_q.data_ptr(), cu_k.data_ptr(), n, tq, tk, max_q, max_k, hq, hkv, hd)
@@ -682,14 +702,15 @@ def gpt2_op_attention_packed_backward(dq, dk, dv, dout, q, k, v, o, lse, cu_q, c
                                       stream=None):
     """dq, dk, dv of gpt2_op_attention_packed_forward from dout and the forward's o and lse."""
     lib = load_library()
-    dt = _dtype_of(q)
+    dt = _mode_of("q", q)
+    sq, so, sdo, sdq = _rows("q, o, dout and dq", q, o, dout, dq)
+    sk, sv, sdk, sdv = _rows("k, v, dk and dv", k, v, dk, dv)
     tq, hq, hd = q.shape
     tk, hkv, d = k.shape
     n = _sequences(cu_q, cu_k)
-    sq, so, sdo, sdq = _rows("q, o, dout and dq", q, o, dout, dq)
-    sk, sv, sdk, sdv = _rows("k, v, dk and dv", k, v, dk, dv)
-    if k.dtype is not q.dtype or d != hd or lse.shape != (hq, tq):
-        raise ValueError("k like q in type and head size, and lse [Hq, total_q], are needed")
+    if k.dtype is not q.dtype or d != hd:
+        raise ValueError("k like q in type and head size is needed")
+    _arrays("lse [Hq, total_q]", _torch.float32, (hq, tq), lse)
     nb = lib.gpt2_op_attention_packed_backward_scratch(dt, n, tq, tk, hq, hkv, hd)
     args = (dt, dq.data_ptr(), sdq, dk.data_ptr(), sdk, dv.data_ptr(), sdv, dout.data_ptr(), sdo, q.data_ptr(), sq,
             k.data_ptr(), sk, v.data_ptr(), sv, o.data_ptr(), so, lse.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(), n,
@@ -705,26 +726,39 @@ def gpt2_op_attention_packed_backward(dq, dk, dv, dout, q, k, v, o, lse, cu_q, c
 
 def gpt2_op_token_logprobs(logp, lse, entropy, logits, targets, V, top_logp=None, top_ids=None, status=None,
                            stream=None):
-    """logp, lse, entropy (float32 [N]) of the rows of logits [N, Vp] over their first V columns; top_logp and
-    top_ids ([N, k], both or none): the k largest."""
+    """logp, lse, entropy (float32 [N]) of the rows of logits [N, Vp] over their first V columns (targets int32 [N]);
+    top_logp (float32) and top_ids (int32), both [N, k] or none: the k largest."""
+    dt = _mode_of("logits", logits)
     N, Vp = _logits(logits)
     if (top_logp is None) != (top_ids is None) or (top_ids is not None and top_logp.shape != top_ids.shape):
         raise ValueError("top_logp and top_ids come together, in one shape")
-    check(load_library().gpt2_op_token_logprobs(_dtype_of(logits), _p(logp), _p(lse), _p(entropy), _p(top_logp),
-                                                _p(top_ids), 0 if top_ids is None else top_ids.shape[1], _p(logits),
-                                                _p(targets), N, V, Vp, _p(status), _s(stream)),
+    k = 0
+    if top_ids is not None:
+        if top_ids.dim() != 2:
+            raise ValueError("top_logp and top_ids [N, k] are needed")
+        k = top_ids.shape[1]
+        _arrays("top_logp", _torch.float32, (N, k), top_logp)
+        _arrays("top_ids", _torch.int32, (N, k), top_ids)
+    _arrays("logp, lse and entropy", _torch.float32, (N,), logp, lse, entropy)
+    _arrays("targets", _torch.int32, (N,), targets)
+    check(load_library().gpt2_op_token_logprobs(dt, _p(logp), _p(lse), _p(entropy), _p(top_logp), _p(top_ids), k,
+                                                _p(logits), _p(targets), N, V, Vp, _p(status), _s(stream)),
           "gpt2_op_token_logprobs")
 
 
 def gpt2_op_token_logprobs_backward(dlogits, logits, targets, lse, entropy, V, dlogp=None, dlse=None, dentropy=None,
                                     status=None, stream=None):
-    """dlogits [N, Vp] (may be logits) from the gradients of gpt2_op_token_logprobs' logp, lse and entropy."""
+    """dlogits [N, Vp] (may be logits) from the gradients (float32 [N]) of gpt2_op_token_logprobs' logp, lse and
+    entropy."""
+    dt = _mode_of("logits", logits)
     N, Vp = _logits(logits)
     if _logits(dlogits) != logits.shape or dlogits.dtype is not logits.dtype:
         raise ValueError("logits and dlogits need one shape and type")
-    check(load_library().gpt2_op_token_logprobs_backward(_dtype_of(logits), _p(dlogits), _p(logits), _p(targets),
-                                                         _p(lse), _p(entropy), _p(dlogp), _p(dlse), _p(dentropy), N,
-                                                         V, Vp, _p(status), _s(stream)),
+    _arrays("lse, entropy and the gradients", _torch.float32, (N,), lse, entropy, dlogp, dlse, dentropy)
+    _arrays("targets", _torch.int32, (N,), targets)
+    check(load_library().gpt2_op_token_logprobs_backward(dt, _p(dlogits), _p(logits), _p(targets), _p(lse),
+                                                         _p(entropy), _p(dlogp), _p(dlse), _p(dentropy), N, V, Vp,
+                                                         _p(status), _s(stream)),
           "gpt2_op_token_logprobs_backward")
 
 
