@@ -672,6 +672,19 @@ def _logits(t):
     return t.shape
 
 
+def _here(what, status, *tensors):
+    """Every tensor on the current CUDA device: the kernels run there and take addresses."""
+    try:
+        device = _torch._C._cuda_getDevice()
+    except (AttributeError, RuntimeError):  # no CUDA: nothing is there
+        device = 0
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise RuntimeError(f"{what}: every tensor has to be on the current CUDA device")
+    if status is not None and (status.dtype is not _torch.int32 or status.get_device() != device):
+        raise RuntimeError(f"{what}: status has to be int32 on the current CUDA device")
+
+
 def gpt2_op_attention_packed_forward(o, lse, q, k, v, cu_q, cu_k, max_q, max_k, status=None, stream=None):
     """o [total_q, Hq, hd], lse [Hq, total_q] (float32): causal attention over packed sequences; q like o,
     k and v [total_k, Hkv, hd] (each may be a column block of a wider buffer), cu_q and cu_k int32 [n_seq + 1]
@@ -686,6 +699,7 @@ def gpt2_op_attention_packed_forward(o, lse, q, k, v, cu_q, cu_k, max_q, max_k, 
     if k.dtype is not q.dtype or d != hd:
         raise ValueError("k like q in type and head size is needed")
     _arrays("lse [Hq, total_q]", _torch.float32, (hq, tq), lse)
+    _here("gpt2_op_attention_packed_forward", status, o, lse, q, k, v, cu_q, cu_k)
     nb = lib.gpt2_op_attention_packed_forward_scratch(dt, n, tq, tk, max_q, max_k, hq, hkv, hd)
     args = (dt, o.data_ptr(), so, lse.data_ptr(), q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv,
             cu_q.data_ptr(), cu_k.data_ptr(), n, tq, tk, max_q, max_k, hq, hkv, hd)
@@ -711,6 +725,7 @@ def gpt2_op_attention_packed_backward(dq, dk, dv, dout, q, k, v, o, lse, cu_q, c
     if k.dtype is not q.dtype or d != hd:
         raise ValueError("k like q in type and head size is needed")
     _arrays("lse [Hq, total_q]", _torch.float32, (hq, tq), lse)
+    _here("gpt2_op_attention_packed_backward", status, dq, dk, dv, dout, q, k, v, o, lse, cu_q, cu_k)
     nb = lib.gpt2_op_attention_packed_backward_scratch(dt, n, tq, tk, hq, hkv, hd)
     args = (dt, dq.data_ptr(), sdq, dk.data_ptr(), sdk, dv.data_ptr(), sdv, dout.data_ptr(), sdo, q.data_ptr(), sq,
             k.data_ptr(), sk, v.data_ptr(), sv, o.data_ptr(), so, lse.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(), n,
@@ -741,6 +756,7 @@ def gpt2_op_token_logprobs(logp, lse, entropy, logits, targets, V, top_logp=None
         _arrays("top_ids", _torch.int32, (N, k), top_ids)
     _arrays("logp, lse and entropy", _torch.float32, (N,), logp, lse, entropy)
     _arrays("targets", _torch.int32, (N,), targets)
+    _here("gpt2_op_token_logprobs", status, logp, lse, entropy, logits, targets, top_logp, top_ids)
     check(load_library().gpt2_op_token_logprobs(dt, _p(logp), _p(lse), _p(entropy), _p(top_logp), _p(top_ids), k,
                                                 _p(logits), _p(targets), N, V, Vp, _p(status), _s(stream)),
           "gpt2_op_token_logprobs")
@@ -756,6 +772,7 @@ def gpt2_op_token_logprobs_backward(dlogits, logits, targets, lse, entropy, V, d
         raise ValueError("logits and dlogits need one shape and type")
     _arrays("lse, entropy and the gradients", _torch.float32, (N,), lse, entropy, dlogp, dlse, dentropy)
     _arrays("targets", _torch.int32, (N,), targets)
+    _here("gpt2_op_token_logprobs_backward", status, dlogits, logits, targets, lse, entropy, dlogp, dlse, dentropy)
     check(load_library().gpt2_op_token_logprobs_backward(dt, _p(dlogits), _p(logits), _p(targets), _p(lse),
                                                          _p(entropy), _p(dlogp), _p(dlse), _p(dentropy), N, V, Vp,
                                                          _p(status), _s(stream)),

@@ -1,6 +1,6 @@
 """What the wrappers of packed attention and token log-probabilities refuse before they hand addresses to a kernel:
-types that the kernels do not read, layouts that they do not follow, arrays that are too short (CPU; nothing is
-launched)."""
+types that the kernels do not read, layouts that they do not follow, arrays that are too short, tensors that are not
+on the device (CPU; nothing is launched)."""
 import pytest
 import torch
 
@@ -51,6 +51,16 @@ def test_attention_refuses(name):
         g.gpt2_op_attention_packed_forward(*forward, **kw)
     with pytest.raises(ValueError):
         g.gpt2_op_attention_packed_backward(*backward, **kw)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attention_refuses_tensors_that_are_not_on_the_device(dtype):
+    for kw in (dict(), dict(status=torch.zeros(1).int()), dict(status=torch.zeros(1).long())):
+        forward, backward, kw = attention(dtype, **kw)
+        with pytest.raises(RuntimeError, match="current CUDA device"):
+            g.gpt2_op_attention_packed_forward(*forward, **kw)
+        with pytest.raises(RuntimeError, match="current CUDA device"):
+            g.gpt2_op_attention_packed_backward(*backward, **kw)
 
 
 def logprobs(**kw):
@@ -105,4 +115,13 @@ def logprobs_backward(**kw):
 def test_logprobs_backward_refuses(bad):
     a, kw = logprobs_backward(**bad)
     with pytest.raises(ValueError):
+        g.gpt2_op_token_logprobs_backward(*a, **kw)
+
+
+def test_logprobs_refuses_tensors_that_are_not_on_the_device():
+    a, kw = logprobs()
+    with pytest.raises(RuntimeError, match="current CUDA device"):
+        g.gpt2_op_token_logprobs(*a, **kw)
+    a, kw = logprobs_backward()
+    with pytest.raises(RuntimeError, match="current CUDA device"):
         g.gpt2_op_token_logprobs_backward(*a, **kw)
