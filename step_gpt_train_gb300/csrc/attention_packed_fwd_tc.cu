@@ -22,8 +22,9 @@
 // needs to be the maximum only to within fp32's range: later blocks are not
 // searched for a larger one (which took a seventh of a step), and O never
 // moves. A row whose l is not between 1 and 2^40 at the end (scores that grow
-// by 28 over the first block's, infinities, NaN) is computed once more by its
-// output warp, 32 keys at a time with a running maximum.
+// by 28 over the first block's, infinities, NaN), or whose first block's scores
+// are all -inf, is computed once more by its output warp, 32 keys at a time
+// with a running maximum.
 //
 // Warps: 0 TMA producer; 1, 2 MMA issue for tile 0, 1 (S of the next step
 // before PV of the current one); 3 finds the work items (a ring of two in
@@ -416,7 +417,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (!(ok = wait(l_full + 8 * t, d & 1, abort_flag, status))) break;
                     const float m = ml[t * 256 + r], l = ml[t * 256 + 128 + r];
                     const int vis = it.vis + (t ? A.qt : 0) + qi;  // keys that the row sees
-                    again = __ballot_sync(0xffffffffu, mine && vis > 0 && !(l > 0.5f && l < MOST));
+                    // (m = -inf: no finite score in the first block, so l is against 0 and says nothing)
+                    again = __ballot_sync(0xffffffffu, mine && vis > 0 && !(m > -INFINITY && l > 0.5f && l < MOST));
                     if (!(ok = wait(o_done + 8 * t, d & 1, abort_flag, status))) break;
                     tc_fence_after();
                     const bool some = vis > 0;
