@@ -215,12 +215,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int buf = i & 1;
                 const uint32_t qph = (uint32_t)(i >> 1) & 1u;
                 ok = mbar_wait(q_empty + 8 * buf, qph ^ 1u, abort_flag, status);
-                if (ok) {
+                if (ok) q_issued[buf] = (int)qph;
+                if (ok && it.n0 == 0 && it.n1 == 0) {
+                    // nobody comes for its Q: none is loaded, whose bytes could still be on their way when the buffer
+                    // is filled for the item after the next
+                    mbar_arrive(q_full + 8 * buf);
+                    mbar_arrive(q_empty + 8 * buf);
+                    mbar_arrive(q_empty + 8 * buf);
+                } else if (ok) {
                     const uint32_t box = (uint32_t)(A.qt * A.group * HD * 2);
                     mbar_expect_tx(q_full + 8 * buf, it.nq1 > 0 ? 2 * box : box);
                     tma_load_3d(sQ(buf, 0), &tm_q, q_full + 8 * buf, 0, it.kh * A.group, it.q0);
                     if (it.nq1 > 0) tma_load_3d(sQ(buf, 1), &tm_q, q_full + 8 * buf, 0, it.kh * A.group, it.q0 + A.qt);
-                    q_issued[buf] = (int)qph;
                     // a tile without blocks does not come for its Q, nor for blocks it does not see
                     if (it.n0 == 0) mbar_arrive(q_empty + 8 * buf);
                     if (it.n1 == 0) mbar_arrive(q_empty + 8 * buf);

@@ -46,3 +46,16 @@ def test_attention_first_keys_score_minus_infinity(torch_cuda, lq, hidden, mode)
     within(host(c.dk)[rest], dk, bk, "dk")
     within(host(c.dv)[rest], dv, bv, "dv")
     assert not c.dk[first].any() and not c.dv[first].any()
+
+
+@pytest.mark.parametrize("mode", [1, 0], ids=["bf16", "fp32"])
+def test_attention_runs_of_items_without_keys(torch_cuda, mode):
+    """Many work items in a row that meet no key (longer than a processor's share of them), among some that do."""
+    r = np.random.default_rng(5)
+    lq = [int(x) for x in r.integers(1, 300, 900)]
+    lk = [0] * len(lq)
+    lk[100], lk[101], lk[500], lq[700], lk[700] = 200, 7, 40, 2000, 300
+    c = Packed(torch_cuda, 47, lq, lk, 4, 2, 64, mode)
+    c.forward()
+    c.backward()
+    c.check()
