@@ -72,8 +72,9 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
 
 // The next work item of this CTA, by a whole warp: a tile and a key head, from
 // the sorted plan or (x counts on from blockIdx.x) from the offsets themselves.
+// id (optional): the item's number, from which tile_of finds it again.
 __device__ __forceinline__ bool next_tile(const PackedAttn& a, const PackedCut& cut, PackedPlan* plan, int items,
-                                          int& x, PackedTile& t, int& kh) {
+                                          int& x, PackedTile& t, int& kh, int* id = nullptr) {
     if (plan) {
         int n = 0;
         if ((threadIdx.x & 31) == 0) n = atomicAdd(&plan->next, 1);
@@ -81,6 +82,7 @@ __device__ __forceinline__ bool next_tile(const PackedAttn& a, const PackedCut& 
         if (n >= plan->count * a.Hkv) return false;
         t = plan->tile[n / a.Hkv];
         kh = n % a.Hkv;
+        if (id) *id = n;
         return true;
     }
     const int slots = items / a.Hkv;
@@ -97,9 +99,20 @@ __device__ __forceinline__ bool next_tile(const PackedAttn& a, const PackedCut& 
         if (at < 0 || at >= cut.rows(q)) continue;
         t = cut.tile(q, at);
         kh = i % a.Hkv;
+        if (id) *id = i;
         return true;
     }
     return false;
+}
+// An item that next_tile gave out before.
+__device__ __forceinline__ void tile_of(const PackedAttn& a, const PackedCut& cut, const PackedPlan* plan, int items,
+                                        int id, PackedTile& t, int& kh) {
+    if (plan) {
+        t = plan->tile[id / a.Hkv];
+        kh = id % a.Hkv;
+    } else {
+        next_tile(a, cut, nullptr, items, id, t, kh);
+    }
 }
 // Items sorted by length are worth their own launch once there are more than
 // SMs to take them; beyond PACKED_PLAN_MAX the sort would cost more than the

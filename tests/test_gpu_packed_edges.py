@@ -59,3 +59,48 @@ def test_attention_runs_of_items_without_keys(torch_cuda, mode):
     c.forward()
     c.backward()
     c.check()
+
+
+def test_attention_scores_that_grow_stay_below_the_wait_limit(torch_cuda):
+    """Rows whose scores outgrow their first block's by far take no longer than a wait may: with the bound of every
+    wait at about a millisecond a prompt of 4096 tokens of such rows is done, and right."""
+    torch = torch_cuda
+    from step_gpt_train_gb300.gpt2 import check, load_library
+    c = Packed(torch, 42, [4096], [4096], 16, 4, 64, 1)
+    c.q[c.real_q] = 0
+    c.q[c.real_q, :, 0] = 8.0
+    n = int(c.real_k.sum())
+    c.k[c.real_k, :, 0] = data.round_to_bf16(np.linspace(-100, 100, n).astype(np.float32))[:, None]
+    c.tq.copy_(dev(c.q.astype(np.float32)))
+    c.tk.copy_(dev(c.k.astype(np.float32)))
+    lib = load_library()
+    try:
+        check(lib.gpt2_debug_set_wait_limit(2_000_000), "gpt2_debug_set_wait_limit")
+        c.forward()
+        torch.cuda.synchronize()
+    finally:
+        check(lib.gpt2_debug_set_wait_limit(0), "gpt2_debug_set_wait_limit")
+    c.check(back=False)
+
+
+@pytest.mark.parametrize("n,Hq,Hkv", [(3, 2, 2), (3, 10, 2), (60, 10, 2), (60, 12, 12)])
+def test_attention_some_sequences_grow(torch_cuda, n, Hq, Hkv):
+    """Every other sequence's scores rise or fall by 100 over its length, the rest stay as they are; the same bits twice."""
+    torch = torch_cuda
+    r = np.random.default_rng(n)
+    lk = [int(x) for x in r.integers(1, 700, n)]
+    lk[1] = 1500
+    lq = [int(r.integers(0, x + 2)) if i % 3 else x for i, x in enumerate(lk)]
+    c = Packed(torch, 48, lq, lk, Hq, Hkv, 64, 1)
+    for i in range(1, n, 2):
+        a, b = (slice(int(x[i]), int(x[i + 1])) for x in (c.cu_q, c.cu_k))
+        c.q[a, :, 0] = 8.0 if i % 4 == 1 else -8.0
+        c.k[b, :, 0] = data.round_to_bf16(np.linspace(-50, 50, lk[i]).astype(np.float32))[:, None]
+    c.tq.copy_(dev(c.q.astype(np.float32)))
+    c.tk.copy_(dev(c.k.astype(np.float32)))
+    c.forward()
+    o, lse = c.o.clone(), c.lse.clone()
+    c.forward()
+    c.backward()
+    c.check()
+    assert torch.equal(o.nan_to_num(), c.o.nan_to_num()) and torch.equal(lse, c.lse)
