@@ -163,7 +163,7 @@ __device__ __forceinline__ bool row_tile(const Args& A, int block, int blocks, R
     const PackedSeq p = packed_seq(a, s);
     t.q0 = p.q0, t.at = (slot - first) * TL, t.n = min(TL, p.lq * A.group - t.at);
     t.k0 = p.k0, t.lk = p.lk, t.sees = 1 + p.lk - p.lq;
-    return t.n > 0;
+    return t.at >= 0 && t.n > 0;  // (before 0: offsets that descend)
 }
 
 __global__ void __launch_bounds__(1024) packed_plan_f32_kernel(PackedAttn a, PackedCut cut, PackedPlan* plan) {
@@ -338,7 +338,7 @@ template <int HD> __device__ __forceinline__ void dkdv_keys(const Args& A, float
     if (s0 < 0) return;
     const PackedSeq p = packed_seq(a, s0);
     const int at = (slot - first) * TL;
-    if (at >= p.lk) return;
+    if (at < 0 || at >= p.lk) return;
     const Rows rows = {p.q0, A.group, kh * A.group};
     const int nk = min(TL, p.lk - at), off = p.lk - p.lq, all = p.lq * A.group;
     load_tile<HD>(sk, nk, [&](int r) { return (const float*)a.k + (int64_t)(p.k0 + at + r) * a.k_stride + kh * HD; });

@@ -83,6 +83,38 @@ def test_attention_scores_that_grow_stay_below_the_wait_limit(torch_cuda):
     c.check(back=False)
 
 
+@pytest.mark.parametrize("mode,hd", [(0, 64), (0, 16), (1, 64)])
+@pytest.mark.parametrize("group", [1, 4])
+def test_attention_offsets_in_any_order_touch_nothing_outside(torch_cuda, group, mode, hd):
+    """Offsets out of order or range set bit 8, and nothing around the outputs is written, whatever they are."""
+    torch = torch_cuda
+    r = np.random.default_rng(group)
+    arrays = [[398, 102, 43, 244, 9, 194], [393, 0, 0, 0, 0, 393], [0, 300, 20, 380, 10, 393], [393, 300, 200, 100, 50, 0]]
+    arrays += [r.integers(-5, 400, 6).tolist() for _ in range(12)]
+    around = 4096
+    c = Packed(torch, 49, [80, 80, 80, 80, 73], [80, 80, 80, 80, 73], group, 1, hd, mode, before=0, after=0)
+    c.max_q = c.max_k = 400
+    fine = lambda x: x[0] >= 0 and x[-1] <= 393 and x == sorted(x)  # noqa: E731
+    held = {}
+
+    def within_walls(t):  # a copy with `around` values of 7 on either side
+        wall = torch.full((t.numel() + 2 * around,), 7.0, dtype=t.dtype, device="cuda")
+        return wall, wall[around:-around].view(t.shape)
+    for name in ("o", "lse", "dq", "dk", "dv"):
+        held[name], x = within_walls(getattr(c, name))
+        setattr(c, name, x)
+    for cu in arrays:
+        for q, k in ((cu, [0, 80, 160, 240, 320, 393]), ([0, 80, 160, 240, 320, 393], cu), (cu, cu)):
+            c.dev_cu = [torch.tensor(x, dtype=torch.int32, device="cuda") for x in (q, k)]
+            for run in (c.forward, c.backward):
+                c.status.zero_()
+                run()
+                torch.cuda.synchronize()
+                assert c.status.item() == (0 if fine(q) and fine(k) else 8), (q, k)
+    for name, wall in held.items():
+        assert (wall[:around] == 7).all() and (wall[-around:] == 7).all(), name
+
+
 @pytest.mark.parametrize("n,Hq,Hkv", [(3, 2, 2), (3, 10, 2), (60, 10, 2), (60, 12, 12)])
 def test_attention_some_sequences_grow(torch_cuda, n, Hq, Hkv):
     """Every other sequence's scores rise or fall by 100 over its length, the rest stay as they are; the same bits twice."""
