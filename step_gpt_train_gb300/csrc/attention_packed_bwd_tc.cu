@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     hi = it.shift + qi - n * BLK - half * 32;
                 } else {
                     const int t = it.first + n * A.bq;
-                    lo = (it.shift + r - t) * A.group - half * 32;
+                    lo = max(0, it.shift + r - t) * A.group - half * 32;  // (far below 0 the product passes 31 bits)
                     hi = min(A.bq, it.len - t) * A.group - half * 32;
                 }
                 const bool cut = __any_sync(0xffffffffu, lo > 0 || hi < 32);

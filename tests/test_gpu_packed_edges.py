@@ -136,3 +136,28 @@ def test_attention_some_sequences_grow(torch_cuda, n, Hq, Hkv):
     c.backward()
     c.check()
     assert torch.equal(o.nan_to_num(), c.o.nan_to_num()) and torch.equal(lse, c.lse)
+
+
+def test_attention_backward_positions_times_heads_past_31_bits(torch_cuda):
+    """64 heads on one over 2^25 keys: key positions counted in (query, head) rows pass 2^31. Every key is seen by the
+    one query with the same weight, so every row of dV is the same, and dK is 0."""
+    torch = torch_cuda
+    from step_gpt_train_gb300.gpt2 import gpt2_op_attention_packed_backward
+    lk, H = (1 << 25) + 256, 64
+    z = lambda n, h: torch.zeros(n, h, 64, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    q, o, dq, dout = z(1, H), z(1, H), z(1, H), z(1, H)
+    dout.fill_(1.0)
+    k, dk, dv = z(lk, 1), z(lk, 1), z(lk, 1)
+    dk.fill_(7.0)
+    dv.fill_(7.0)
+    lse = torch.full((H, 1), float(np.log(lk)), device="cuda")
+    cu_q, cu_k = (torch.tensor([0, n], dtype=torch.int32, device="cuda") for n in (1, lk))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gpt2_op_attention_packed_backward(dq, dk, dv, dout, q, k, k, o, lse, cu_q, cu_k, 1, lk, status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    # P rounds to bf16, the sum of 64 equal terms and dV's own rounding add half a step each; lse is off by 2^-24 |lse|
+    want = H / lk
+    lo, hi = dv.min().item(), dv.max().item()
+    assert want * (1 - 2.5 * P.BF16) <= lo and hi <= want * (1 + 2.5 * P.BF16), (lo, hi, want)
+    assert not dk.any() and not dq.any()
