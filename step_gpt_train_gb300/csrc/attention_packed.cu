@@ -70,6 +70,7 @@ __global__ void __launch_bounds__(128) packed_dq_kernel(PackedAttn a, PackedAttn
 // One thread per (key head, key).
 __global__ void __launch_bounds__(128) packed_dkdv_kernel(PackedAttn a, PackedAttnGrad g, float scale) {
     const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    if (a.total_q == 0) packed_check(a, i, gridDim.x * blockDim.x);  // (else the other kernel looks)
     if (i >= a.total_k * a.Hkv) return;
     const int hk = i / a.total_k, row = i - hk * a.total_k;
     const int s = packed_find_row(a.cu_k, a.n_seq, row);

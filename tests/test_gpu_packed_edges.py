@@ -161,3 +161,13 @@ def test_attention_backward_positions_times_heads_past_31_bits(torch_cuda):
     lo, hi = dv.min().item(), dv.max().item()
     assert want * (1 - 2.5 * P.BF16) <= lo and hi <= want * (1 + 2.5 * P.BF16), (lo, hi, want)
     assert not dk.any() and not dq.any()
+
+
+def test_attention_backward_wide_groups_report_bad_offsets_without_queries(torch_cuda):
+    torch = torch_cuda
+    c = Packed(torch, 43, [0, 0, 0], [30, 20, 10], 128, 1, 64, 1, before=0, after=0)
+    c.dev_cu[1] = torch.tensor([0, 50, 30, 60], dtype=torch.int32, device="cuda")
+    c.max_k = 60
+    c.backward()
+    torch.cuda.synchronize()
+    assert c.status.item() == 8
