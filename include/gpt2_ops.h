@@ -348,7 +348,9 @@ int gpt2_op_classifier(int dtype, void* logits, float* losses, const int32_t* ta
  *   entropy[i] = -sum_j p_ij log p_ij with p = exp(z - lse) (0 log 0 = 0),
  *   top_ids[i, 0..k-1] = the columns of the k largest logits, largest first,
  *   equal logits by the lowest column, top_logp[i, r] their log-probability.
- * All outputs fp32 (top_ids int32); 0 <= k <= 64, k <= V, top_logp and top_ids
+ * Log-probabilities are (z - max) - ln S: accurate to a few 2^-24 and their own
+ * size however far the logits are from 0, never positive; no entropy is
+ * negative. All outputs fp32 (top_ids int32); 0 <= k <= 64, k <= V, top_logp and top_ids
  * [N, k] (unused for k = 0); entropy may be null; logp and targets may both be
  * null. A target outside [0,V) sets bit 4 of *d_status and is treated as 0. A
  * row whose every logit is -inf has no distribution: lse = logp = top_logp =

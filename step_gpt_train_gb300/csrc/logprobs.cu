@@ -1,10 +1,12 @@
 // Log-probabilities of given tokens, with entropy and the top alternatives,
 // and their gradient. Both are bound by HBM: the logits are read once (and
 // the gradient written once); everything else stays in registers. 32768 rows of
-// 50257 bf16 logits take 495 us (6.6 TB/s), the gradient of 8192 242 us (6.8).
+// 50257 bf16 logits take 498 us (6.6 TB/s), the gradient of 8192 242 us (6.8).
 //
 // With m the row's maximum, d_j = (z_j - m) log2(e) and e_j = 2^d_j,
 //   S = sum e_j, T = sum e_j d_j:  lse = m + ln S,  entropy = ln S - ln2 T / S,
+//   log p_j = (z_j - m) - ln S (not z_j - lse: lse carries a rounding of its own
+//   size, which far from 0 is more than a sure token's log-probability),
 // in one pass: a thread keeps its own m, S, T and moves them to a new maximum
 // by S' = f S, T' = f (T + S (m - m') log2(e)), f = 2^((m - m') log2(e)).
 #include "common.cuh"
@@ -114,8 +116,12 @@ template <int LANES> __device__ __forceinline__ Stats join(Stats x) {
 
 // N values into x, whose maximum is already at least theirs, 2^d taken
 //   fast: with d = z log2(e) - m log2(e) in one step. The rounding of m log2(e)
-//     shifts every d alike (lse by |m| 2^-24) while |m| is moderate, and e d is
-//     a NaN where z is -inf, which the caller sees in x.t;
+//     shifts every d alike, by delta (below 2^-11 while |m| is moderate), which
+//     is taken out of the sums: S 2^-delta, 2^-delta (T - delta S) (left in, the
+//     largest weight is not 1 and log-probabilities are off by |m| 2^-24; 495 us
+//     for the 32768 rows then, 498 so; m log2(e) rounded to a whole number, whose
+//     shift goes out once a row: 506). e d is a NaN where z is -inf, which the
+//     caller sees in x.t;
 //   else: from the difference z - m, exact for the largest, and with d bounded
 //     (e is 0 below -150, and 0 * -inf must not count): for masks from -1e38 to
 //     -inf and far-off rows.
@@ -136,9 +142,16 @@ template <bool FAST, int N> __device__ __forceinline__ void add_values(const flo
     }
     float a, b;
     f2_unpack(f2_add(s2[0], s2[1]), a, b);
-    x.s += a + b;
+    float s = a + b;
     f2_unpack(f2_add(t2[0], t2[1]), a, b);
-    x.t += a + b;
+    float t = a + b;
+    if (FAST) {
+        const float delta = fmaf(m, LOG2E, ml), y = -LN2 * delta, c = fmaf(y, fmaf(y, 0.5f, 1.f), 1.f);  // 2^-delta
+        t = c * fmaf(-delta, s, t);
+        s *= c;
+    }
+    x.s += s;
+    x.t += t;
 }
 template <int N> __device__ __forceinline__ void raise(const float (&f)[N], Stats& x) {
     float m[2] = {x.m, -INFINITY};
@@ -147,6 +160,19 @@ template <int N> __device__ __forceinline__ void raise(const float (&f)[N], Stat
     const float top = max_nan(m[0], m[1]);
     if (!(top <= x.m)) move_to(x, top);
 }
+
+// What a row's sums say.
+struct Row {
+    float m, ln_s;  // ln S: at least 0 but for rounding, as the largest logit's own weight is 1 (0 for m = +-inf)
+    __device__ __forceinline__ Row(float m, float ln_s) : m(m), ln_s(ln_s) {}
+    __device__ __forceinline__ explicit Row(const Stats& x)
+        : m(x.m), ln_s(isinf(x.m) ? 0.f : max_nan(LN2 * log2f(x.s), 0.f)) {}
+    __device__ __forceinline__ float lse() const { return m + ln_s; }
+    __device__ __forceinline__ float entropy(const Stats& x) const {
+        return m == -INFINITY ? 0.f : max_nan(ln_s - LN2 * (x.t / x.s), 0.f);
+    }
+    __device__ __forceinline__ float logp(float z) const { return m == -INFINITY ? -INFINITY : (z - m) - ln_s; }
+};
 
 // The split-th part of a row's vectors: [first, last).
 __device__ __forceinline__ void part(int nv, int split, int rank, int& first, int& last) {
@@ -243,7 +269,7 @@ __global__ void __launch_bounds__(NT)
     __shared__ __align__(16) uint32_t maxima[TOP ? NT : 4];
     __shared__ uint32_t bound;
     __shared__ int count;
-    __shared__ float whole;  // the row's lse
+    __shared__ float whole[2];  // the row's maximum and ln S
     const int row = blockIdx.x / split, rank = blockIdx.x - row * split;
     const int tid = threadIdx.x, lane = tid & 31;
     const T* z = logits + (int64_t)row * Vp;
@@ -288,11 +314,11 @@ __global__ void __launch_bounds__(NT)
     const Stats empty = {-INFINITY, 0.f, 0.f};
     auto finish = [&](const Stats& r) {  // by the first warp
         if (lane) return;
-        const float L = isinf(r.m) ? r.m : r.m + LN2 * log2f(r.s);
-        lse[row] = L;
-        if (entropy) entropy[row] = r.m == -INFINITY ? 0.f : LN2 * (log2f(r.s) - r.t / r.s);
-        if (logp) logp[row] = r.m == -INFINITY ? -INFINITY : zt - L;
-        whole = L;
+        const Row w(r);
+        lse[row] = w.lse();
+        if (entropy) entropy[row] = w.entropy(r);
+        if (logp) logp[row] = w.logp(zt);
+        whole[0] = w.m, whole[1] = w.ln_s;
     };
     auto meet = [&] {  // the warps' sums, by the first warp
         if (tid >= 32) return;
@@ -460,10 +486,9 @@ __global__ void __launch_bounds__(NT)
         }
         __syncthreads();
         if (tid < k) {
-            const float L = whole;
             const uint64_t q = keys[tid];
             top_ids[(int64_t)row * k + tid] = key_col(q);
-            top_logp[(int64_t)row * k + tid] = L == -INFINITY ? -INFINITY : key_logit(q) - L;
+            top_logp[(int64_t)row * k + tid] = Row(whole[0], whole[1]).logp(key_logit(q));
         }
     }
 }
@@ -585,13 +610,13 @@ __global__ void __launch_bounds__(TNT + 64, TOP_BLOCKS)
         full_sync(b);
         const Stats empty = {-INFINITY, 0.f, 0.f};
         const Stats x = join<8>(lane < TNT / 32 ? ws[b][lane] : empty);
-        float L = isinf(x.m) ? x.m : x.m + LN2 * log2f(x.s);
-        L = __shfl_sync(0xffffffffu, L, 0);
+        Row w(x);
         if (lane == 0) {
-            lse[row] = L;
-            if (entropy) entropy[row] = x.m == -INFINITY ? 0.f : LN2 * (log2f(x.s) - x.t / x.s);
-            if (logp) logp[row] = x.m == -INFINITY ? -INFINITY : zt - L;
+            lse[row] = w.lse();
+            if (entropy) entropy[row] = w.entropy(x);
+            if (logp) logp[row] = w.logp(zt);
         }
+        w = Row(__shfl_sync(0xffffffffu, w.m, 0), __shfl_sync(0xffffffffu, w.ln_s, 0));
         // The bound as above.
         uint32_t least = ~0u;
         if (min(TNT, nv) >= 8 * k) {
@@ -757,7 +782,7 @@ __global__ void __launch_bounds__(TNT + 64, TOP_BLOCKS)
         for (int r = lane; r < k; r += 32) {
             const uint64_t q = mine.out[r];
             top_ids[row * k + r] = key_col(q);
-            top_logp[row * k + r] = L == -INFINITY ? -INFINITY : key_logit(q) - L;
+            top_logp[row * k + r] = w.logp(key_logit(q));
         }
         __syncwarp();
     }

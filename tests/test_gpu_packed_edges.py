@@ -171,3 +171,41 @@ def test_attention_backward_wide_groups_report_bad_offsets_without_queries(torch
     c.backward()
     torch.cuda.synchronize()
     assert c.status.item() == 8
+
+
+def sure_rows(mode, N, V, Vp):
+    """Rows in which one token holds nearly everything, at offsets from 0 to beyond 10^4, of either sign."""
+    r = np.random.default_rng(N + V)
+    z = inputs(44, (N, Vp), 1.0, 0).astype(np.float64)
+    offsets = np.array([0.0, 10.0, -10.0, 100.0, -100.0, 1000.0, -1000.0, 4000.0, 9000.0, -30000.0])
+    top = r.integers(0, V, N)
+    z[np.arange(N), top] = 45.0 + r.random(N)
+    z += (offsets[np.arange(N) % 10] * (1 + r.random(N)))[:, None]
+    z = data.round_to_bf16(z.astype(np.float32)).astype(np.float64) if mode == 1 else z.astype(np.float32).astype(np.float64)
+    return z, top
+
+
+@pytest.mark.parametrize("mode", [1, 0], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("N,V,k", [(30, 500, 0), (30, 500, 5), (3, 50257, 5), (3, 50257, 0), (60, 50257, 40), (200, 50257, 0),
+                                   (700, 5003, 20), (700, 5003, 0)])
+def test_logprobs_of_sure_tokens(torch_cuda, N, V, k, mode):
+    """Log-probabilities keep their accuracy however far the logits are from 0: none is positive, no entropy negative."""
+    from tests.test_gpu_packed import run_logprobs
+    z, top = sure_rows(mode, N, V, -(-V // 8) * 8)
+    t = np.where(np.arange(N) % 3 == 2, (top + 1) % V, top)
+    _, _, logp, lse, ent, tl, ids, status = run_logprobs(torch_cuda, z, t, V, k, mode)
+    ref = P.token_logprobs(z, t, V, k)
+    m = z[:, :V].max(axis=1, keepdims=True)
+    others = np.exp(z[:, :V] - m).sum(axis=1) - 1  # the weight beside the largest's
+    # z - m rounds once (bf16 logits: not at all) and logp once; ln S is off by its largest term's exponential (2^-22)
+    # and four roundings near 1, and by the others' weight where it is lost beside 1
+    bound = lambda x: 2 * P.F32 * np.abs(x) + 8 * P.F32 + np.abs(others)  # noqa: E731
+    assert status.item() == 0
+    within(host(logp), ref[1], bound(ref[1]), "logp")
+    within(host(lse), ref[0], P.F32 * np.abs(ref[0]) + bound(0), "lse")
+    # entropy = ln S - T / S, T of the others' weight times their distance (at most 64, or 130 in steps of bf16)
+    within(host(ent), ref[2], bound(0) + 400 * np.abs(others), "entropy")
+    assert (host(logp) <= 0).all() and (host(ent) >= 0).all() and (host(tl) <= 0).all()
+    if k:
+        assert (ids.cpu().numpy() == ref[3]).all()
+        within(host(tl), ref[4], 2 * P.F32 * np.abs(ref[4]) + 8 * P.F32 + np.abs(others)[:, None], "top")
