@@ -115,6 +115,30 @@ def test_attention_offsets_in_any_order_touch_nothing_outside(torch_cuda, group,
         assert (wall[:around] == 7).all() and (wall[-around:] == 7).all(), name
 
 
+@pytest.mark.parametrize("group", [1, 4])
+def test_attention_new_tokens_with_offsets_in_any_order(torch_cuda, group):
+    """The same for the kernels of few queries, cut over the keys and (max_k of 128) not."""
+    torch = torch_cuda
+    r = np.random.default_rng(10 + group)
+    around = 4096
+    c = Packed(torch, 50, [2] * 6, [80, 80, 80, 80, 73, 4000], group, 1, 64, 1, before=0, after=0)
+    c.max_q = 4
+    wall = torch.full((c.o.numel() + 2 * around,), 7.0, dtype=torch.bfloat16, device="cuda")
+    wall_lse = torch.full((c.lse.numel() + 2 * around,), 7.0, device="cuda")
+    c.o, c.lse = wall[around:-around].view(c.o.shape), wall_lse[around:-around].view(c.lse.shape)
+    for c.max_k in (128, 4393):
+        for _ in range(20):
+            q, k = r.permutation(13)[:7].tolist(), r.integers(-5, 4400, 7).tolist()
+            assert q != sorted(q)
+            c.dev_cu = [torch.tensor(x, dtype=torch.int32, device="cuda") for x in (q, k)]
+            c.status.zero_()
+            c.forward()
+            torch.cuda.synchronize()
+            assert c.status.item() == 8, (q, k)
+    for w in (wall, wall_lse):
+        assert (w[:around] == 7).all() and (w[-around:] == 7).all()
+
+
 @pytest.mark.parametrize("n,Hq,Hkv", [(3, 2, 2), (3, 10, 2), (60, 10, 2), (60, 12, 12)])
 def test_attention_some_sequences_grow(torch_cuda, n, Hq, Hkv):
     """Every other sequence's scores rise or fall by 100 over its length, the rest stay as they are; the same bits twice."""
@@ -209,3 +233,69 @@ def test_logprobs_of_sure_tokens(torch_cuda, N, V, k, mode):
     if k:
         assert (ids.cpu().numpy() == ref[3]).all()
         within(host(tl), ref[4], 2 * P.F32 * np.abs(ref[4]) + 8 * P.F32 + np.abs(others)[:, None], "top")
+
+
+@pytest.mark.parametrize("mode", [1, 0], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("n,hi", [(2100, 40), (9000, 4)], ids=["offsets searched in memory", "unsorted"])
+def test_attention_thousands_of_sequences(torch_cuda, n, hi, mode):
+    """More sequences than the sort keeps in shared memory, and more work items than it takes."""
+    r = np.random.default_rng(n)
+    lk = [int(x) for x in r.integers(0, hi + 1, n)]
+    lq = [int(r.integers(0, x + 2)) for x in lk]
+    lk[n // 2] = lq[n // 2] = 700
+    c = Packed(torch_cuda, 45, lq, lk, 2, 1, 64, mode)
+    c.forward()
+    c.backward()
+    c.check()
+
+
+@pytest.mark.parametrize("n", [1500, 3000])
+def test_attention_new_tokens_of_thousands_of_sequences(torch_cuda, n):
+    r = np.random.default_rng(n)
+    lk = [int(x) for x in r.integers(0, 30, n)]
+    lk[7], lk[n - 5], lk[n // 3] = 3000, 2000, 0
+    c = Packed(torch_cuda, 46, [int(x) for x in r.integers(0, 2, n)], lk, 8, 2, 64, 1)
+    c.forward()
+    c.check(back=False)
+
+
+@pytest.mark.parametrize("lq,lk", [(200, 300000), (100000, 100000)])
+def test_attention_waits_that_run_out(torch_cuda, lq, lk):
+    """With the bound of the waits at nothing the long waits of a long sequence run out: the kernels report it, stop
+    and give back what they hold, so that the same call right after is as before."""
+    torch = torch_cuda
+    from step_gpt_train_gb300 import gpt2 as g
+    new = lambda n, seed: dev(inputs(seed, (n, 1, 64), 1.0, 1))  # noqa: E731
+    q, k, v, dout = new(lq, 51), new(lk, 52), new(lk, 53), new(lq, 54)
+    o, lse = torch.zeros_like(q), torch.zeros(1, lq, device="cuda")
+    dq, dk, dv = (torch.zeros_like(x) for x in (q, k, v))
+    cu_q, cu_k = (torch.tensor([0, n], dtype=torch.int32, device="cuda") for n in (lq, lk))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def forward():
+        g.gpt2_op_attention_packed_forward(o, lse, q, k, v, cu_q, cu_k, lq, lk, status=status)
+
+    def backward():
+        g.gpt2_op_attention_packed_backward(dq, dk, dv, dout, q, k, v, o, lse, cu_q, cu_k, lq, lk, status=status)
+    forward()
+    backward()
+    first = [x.clone() for x in (o, lse, dq, dk, dv)]
+    assert status.item() == 0
+    lib = g.load_library()
+    for run in (forward, backward):
+        for x, y in zip((o, lse), first):  # (the backward's inputs)
+            x.copy_(y)
+        try:
+            g.check(lib.gpt2_debug_set_wait_limit(1), "gpt2_debug_set_wait_limit")
+            run()
+            torch.cuda.synchronize()
+        finally:
+            g.check(lib.gpt2_debug_set_wait_limit(0), "gpt2_debug_set_wait_limit")
+        assert status.item() == 2
+        status.zero_()
+    forward()
+    backward()
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    for x, y in zip((o, lse, dq, dk, dv), first):
+        assert torch.equal(x, y)
