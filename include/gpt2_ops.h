@@ -244,7 +244,9 @@ int gpt2_op_attention_backward(int dtype, void* dqkv, const void* dout, const vo
  * cu_q[0], at or after cu_q[n_seq]) are left as they were, and no row's
  * result depends on rows of another sequence, whatever they hold. Within a
  * sequence, a NaN or infinity at a position may reach the results of earlier
- * positions of the same 128-row tile.
+ * positions of the same 128-row tile (in the backward also gradients of the
+ * tile's keys that its query does not see). o and lse must not overlap the
+ * inputs.
  *   - max_q, max_k: at least the longest sequence's queries and keys (they
  *     choose the kernel; a longer sequence sets bit 8 of *d_status).
  *   - Offsets that descend or leave [0, total] set bit 8 of *d_status; they
@@ -254,8 +256,10 @@ int gpt2_op_attention_backward(int dtype, void* dqkv, const void* dout, const vo
  *     multiples of 16 bytes and at least the row. total_q * Hq, total_k * Hkv
  *     and n_seq * Hq below 2^30 (else GPT2_ERR_ARG).
  *   - n_seq = 0 or total_q = 0 launches nothing.
- * Scratch: the list of work items, or partial results of keys split over
- * blocks (few queries). */
+ *   - Every wait of the bf16 kernels is bounded by 4e9 cycles (bit 2 of
+ *     *d_status): a sequence of more than 5e7 keys may run into it.
+ * Scratch: the list of work items and links of those that come again, or
+ * partial results of keys split over blocks (few queries). */
 size_t gpt2_op_attention_packed_forward_scratch(int dtype, int n_seq, int total_q, int total_k, int max_q, int max_k,
                                                 int Hq, int Hkv, int hd);
 int gpt2_op_attention_packed_forward(int dtype, void* o, int64_t o_stride, float* lse, const void* q,
@@ -368,7 +372,7 @@ int gpt2_op_token_logprobs(int dtype, float* logp, float* lse, float* entropy, f
  * for j < V (0 where p_ij = 0, and in a row that has no distribution), 0 for
  * V <= j < Vp. dlogits [N, Vp] (dtype, overwritten) may be logits itself.
  * entropy is needed with dentropy, targets with dlogp; targets out of range as
- * above. Nothing is summed across rows: deterministic. */
+ * above. p carries lse's own rounding (|lse| 2^-24, relative). Nothing is summed across rows: deterministic. */
 int gpt2_op_token_logprobs_backward(int dtype, void* dlogits, const void* logits, const int32_t* targets,
                                     const float* lse, const float* entropy, const float* dlogp, const float* dlse,
                                     const float* dentropy, int N, int V, int Vp, int* d_status, void* stream);

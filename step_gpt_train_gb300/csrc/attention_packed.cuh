@@ -7,6 +7,9 @@
 
 #define GPT2_FLAG_OFFSETS 8
 
+// SMs of a GB300, where scratch sizes depend on them (they are asked for without a device).
+constexpr int PACKED_SMS = 152;
+
 // Launches a kernel that may start while the one before it in the stream still
 // runs (its launch and setup hidden behind that), and waits for it itself with
 // griddepcontrol.wait before it reads what that kernel wrote.

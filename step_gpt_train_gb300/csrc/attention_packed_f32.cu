@@ -54,7 +54,7 @@ template <int HD, typename F> __device__ __forceinline__ void load_tile(float* d
     cp_async_commit();
 }
 
-// s[r][c] = A row (ty + 16 r) . B row (tx + 8 c)
+// s[r][c] = A row (ty + 16 r) . B row (tx + 16 c)
 template <int HD> __device__ __forceinline__ void dots(float (&s)[NR][NC], const float* A, const float* B, int ty, int tx) {
     constexpr int LD = Shape<HD>::LD;
 #pragma unroll
@@ -440,7 +440,7 @@ int row_blocks(const PackedAttn& a) {  // slots of the rows, times the key heads
 
 // The forward's sorted tiles of whole queries; with fewer blocks than are at work
 // at once the sort would only be a launch more.
-constexpr int SORT_BLOCKS = 2 * 152;
+constexpr int SORT_BLOCKS = 2 * PACKED_SMS;
 PackedCut row_cut(int Hq, int Hkv) { return PackedCut{false, max(1, TL / (Hq / Hkv)), TL}; }
 size_t plan_bytes(int n_seq, int total_q, int Hq, int Hkv) {
     const int slots = packed_slots(total_q, n_seq, row_cut(Hq, Hkv).per);

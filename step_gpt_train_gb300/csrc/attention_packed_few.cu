@@ -10,9 +10,12 @@
 // over 177402 keys of 4 heads (182 MB) took 47 us with a block for a part of
 // one sequence and one head, 39 so. A sequence inside one chunk is written at
 // once; of the others each chunk leaves its part (O, m, l) in scratch, and a
-// second kernel joins them (about 5 us of the 39). Sequences of up to 128 keys
-// are not cut, which saves the second kernel (4 sequences of up to 74 keys: 8.3
-// us on the device with it).
+// second kernel joins them (about 5 us of the 39). Where no sequence has more
+// than 128 keys none is cut, which saves the second kernel: of 64 keys 4
+// sequences take 6.3 us whole and 8.3 cut (1024 of 4 heads 14 and 35), of 128
+// keys 8.3 and 8.3 (27 and 49), of 192 keys 9.3 and 8.3, of 512 keys 16.6 and
+// 8.4. (Batches of hundreds of sequences would gain from whole ones beyond that:
+// 1024 of 512 keys and 4 heads 84 and 107.)
 //
 // The block's warps copy whole rows of its heads to shared memory (cp.async),
 // NST - 1 tiles ahead and across the ends of sequences: 512 bytes of one row to
@@ -20,7 +23,8 @@
 // each warp copying its own head's 128 bytes of four rows the loads alone took
 // 44 us, with 512 contiguous bytes 36 (12 heads of 128 bytes: 27 us to 21).
 // A block of fewer heads (their number is not a multiple of four) has fewer
-// warps, and more blocks fit.
+// warps, and more blocks fit: 64 new tokens over caches of up to 8192 keys read
+// 6.8 TB/s with 24 heads, 6.3 with 25 (a warp to a block, 128 bytes at a time).
 //
 // The contraction's order is free as long as both sides agree, so 16 bytes are
 // used as they come. Q K^T: thread (n = lane / 4, t = lane % 4) takes dims
@@ -40,7 +44,7 @@ constexpr int ROWS = 16;
 constexpr int NST = 3;                     // tiles that a warp has in shared memory or on their way
 constexpr int STAGE = TILE * HD * 2 * 2;   // bytes of a tile for each warp
 constexpr int PART = HD + 2;               // floats of a row's partial result: O, m, l
-constexpr int FILL = 16 * 152;             // warps at work at once
+constexpr int FILL = 16 * PACKED_SMS;      // warps at work at once
 constexpr int MIN_KEYS = 32;               // of a chunk: what a block has on its way at once
 constexpr int WHOLE = 128;                 // longest sequence of a batch whose sequences are not cut
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;

@@ -41,10 +41,13 @@
 // softmax warps, 72 for the others. Every wait is bounded.
 //
 // Measured: 62 documents of 100 to 1024 tokens, 12 heads, 71 us; 16 prompts of
-// up to 4096 tokens, 16 heads on 4, 95 us (75 GFLOP: 785 TFLOP/s). Bound by the
-// softmax warps' chain of about 2000 cycles a block (wait, 128 scores from TMEM,
-// exponentials, P back), two such warps to a scheduler; the exponential unit
-// alone would take 17 and 44 us, the tensor cores 10 and 38.
+// up to 4096 tokens, 16 heads on 4, 95 us (75 GFLOP: 785 TFLOP/s). Long
+// sequences are bound by the softmax warps' chain of about 2000 cycles a block
+// (wait, 128 scores from TMEM, exponentials, P back), two such warps to a
+// scheduler: 63 pairs of blocks a CTA on the prompts. The documents are ten items
+// a CTA and 32 pairs of blocks, half of their time; the rest is what an item
+// costs from its draw to its first scores and from its last P to O. The
+// exponential unit alone would take 17 and 44 us, the tensor cores 10 and 38.
 #include "attention_packed_tc.cuh"
 
 #include <type_traits>

@@ -850,8 +850,8 @@ __global__ void __launch_bounds__(BNT)
 template <typename T, int NT, bool TOP>
 int forward(float* logp, float* lse, float* entropy, float* top_logp, int32_t* top_ids, int k, const T* logits,
             const int32_t* targets, int N, int V, int Vp, int* status, cudaStream_t s) {
-    // as many blocks to a row as leave each SM one, and each thread two vectors (8 rows of 50257 in fp32: 6.2 us with
-    // eight, 8.3 with one; with 5 alternatives 9.5 with four, 11.3 with eight, with 40 16.5 and 32)
+    // as many blocks to a row as leave each SM one, and each thread a vector (8 rows of 50257 in fp32: 6.2 us with
+    // eight, 8.3 with one; with 5 alternatives 8.7 with four, 11.3 with eight, with 40 16.5 and 32)
     int split = 1;
     while (split < (TOP ? TOP_SPLIT : MAX_SPLIT) && (int64_t)N * split * 2 <= gpt2_num_sms() && V / VEC<T> >= split * 2 * 256) split *= 2;
     cudaLaunchConfig_t cfg = {};
