@@ -649,11 +649,30 @@ def _rows(what, like, *more):
     return strides
 
 
-def _arrays(what, dtype, shape, *tensors):
-    """Contiguous tensors of one type and shape; None passes."""
-    for t in tensors:
-        if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()):
-            raise ValueError(f"{what}: contiguous {dtype} of shape {tuple(shape)} is needed")
+_ONE = (1,)
+
+
+def _fit(device, n, f32, i32):
+    """Contiguous arrays of n float32, and of n int32, on a device (None passes)? One value's stride says nothing, so
+    False may be wrong: _refuse looks again."""
+    size, dtype = 4 * n, _torch.float32
+    for t in f32:
+        if t is not None and (t.nbytes != size or t.dtype is not dtype or t.stride() != _ONE
+                              or t.get_device() != device):
+            return False
+    return i32 is None or (i32.nbytes == size and i32.dtype is _torch.int32 and i32.stride() == _ONE
+                           and i32.get_device() == device)
+
+
+def _refuse(what, device, n, f32, i32):
+    """Raises for what does not fit: types and shapes before devices."""
+    for dtype, tensors in ((_torch.float32, f32), (_torch.int32, (i32,))):
+        for t in tensors:
+            if t is not None and (t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous()):
+                raise ValueError(f"{what}: contiguous {dtype} of shape {(n,)} is needed")
+    for t in (*f32, i32):
+        if t is not None and t.get_device() != device:
+            raise _elsewhere(what)
 
 
 def _sequences(cu_q, cu_k):
@@ -672,17 +691,30 @@ def _logits(t):
     return t.shape
 
 
-def _here(what, status, *tensors):
-    """Every tensor on the current CUDA device: the kernels run there and take addresses."""
+def _where(stream):
+    """The current device and the stream of a call."""
+    c = _torch._C
     try:
-        device = _torch._C._cuda_getDevice()
-    except (AttributeError, RuntimeError):  # no CUDA: nothing is there
-        device = 0
-    for t in tensors:
-        if t is not None and t.get_device() != device:
-            raise RuntimeError(f"{what}: every tensor has to be on the current CUDA device")
-    if status is not None and (status.dtype is not _torch.int32 or status.get_device() != device):
+        device = c._cuda_getDevice()
+        # current_stream().cuda_stream without the object made for it
+        return device, c._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    except AttributeError:
+        return _torch.cuda.current_device(), (stream or _torch.cuda.current_stream()).cuda_stream
+    except RuntimeError:  # no CUDA: nothing is there
+        return 0, None
+
+
+def _elsewhere(what):
+    return RuntimeError(f"{what}: every tensor has to be on the current CUDA device")
+
+
+def _status(what, status, device):
+    """The address of the status word; None passes."""
+    if status is None:
+        return None
+    if status.dtype is not _torch.int32 or status.get_device() != device:
         raise RuntimeError(f"{what}: status has to be int32 on the current CUDA device")
+    return status.data_ptr()
 
 
 def gpt2_op_attention_packed_forward(o, lse, q, k, v, cu_q, cu_k, max_q, max_k, status=None, stream=None):
@@ -698,15 +730,19 @@ def gpt2_op_attention_packed_forward(o, lse, q, k, v, cu_q, cu_k, max_q, max_k, 
     n = _sequences(cu_q, cu_k)
     if k.dtype is not q.dtype or d != hd:
         raise ValueError("k like q in type and head size is needed")
-    _arrays("lse [Hq, total_q]", _torch.float32, (hq, tq), lse)
-    _here("gpt2_op_attention_packed_forward", status, o, lse, q, k, v, cu_q, cu_k)
+    if lse.dtype is not _torch.float32 or lse.shape != (hq, tq) or not lse.is_contiguous():
+        raise ValueError("lse: contiguous float32 of shape [Hq, total_q] is needed")
+    device, st = _where(stream)
+    if not (device == q.get_device() == k.get_device() == v.get_device() == o.get_device() == lse.get_device()
+            == cu_q.get_device() == cu_k.get_device()):
+        raise _elsewhere("gpt2_op_attention_packed_forward")
     nb = lib.gpt2_op_attention_packed_forward_scratch(dt, n, tq, tk, max_q, max_k, hq, hkv, hd)
     args = (dt, o.data_ptr(), so, lse.data_ptr(), q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv,
             cu_q.data_ptr(), cu_k.data_ptr(), n, tq, tk, max_q, max_k, hq, hkv, hd)
-    st = _s(stream)
+    status = _status("gpt2_op_attention_packed_forward", status, device)
     sc = _borrow(nb, st) if nb else None
     try:
-        check(lib.gpt2_op_attention_packed_forward(*args, sc, nb, _p(status), st), "gpt2_op_attention_packed_forward")
+        check(lib.gpt2_op_attention_packed_forward(*args, sc, nb, status, st), "gpt2_op_attention_packed_forward")
     finally:
         if sc:
             _give_back(sc)
@@ -724,16 +760,21 @@ def gpt2_op_attention_packed_backward(dq, dk, dv, dout, q, k, v, o, lse, cu_q, c
     n = _sequences(cu_q, cu_k)
     if k.dtype is not q.dtype or d != hd:
         raise ValueError("k like q in type and head size is needed")
-    _arrays("lse [Hq, total_q]", _torch.float32, (hq, tq), lse)
-    _here("gpt2_op_attention_packed_backward", status, dq, dk, dv, dout, q, k, v, o, lse, cu_q, cu_k)
+    if lse.dtype is not _torch.float32 or lse.shape != (hq, tq) or not lse.is_contiguous():
+        raise ValueError("lse: contiguous float32 of shape [Hq, total_q] is needed")
+    device, st = _where(stream)
+    if not (device == q.get_device() == k.get_device() == v.get_device() == o.get_device() == lse.get_device()
+            == cu_q.get_device() == cu_k.get_device() == dout.get_device() == dq.get_device() == dk.get_device()
+            == dv.get_device()):
+        raise _elsewhere("gpt2_op_attention_packed_backward")
     nb = lib.gpt2_op_attention_packed_backward_scratch(dt, n, tq, tk, hq, hkv, hd)
     args = (dt, dq.data_ptr(), sdq, dk.data_ptr(), sdk, dv.data_ptr(), sdv, dout.data_ptr(), sdo, q.data_ptr(), sq,
             k.data_ptr(), sk, v.data_ptr(), sv, o.data_ptr(), so, lse.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(), n,
             tq, tk, max_q, max_k, hq, hkv, hd)
-    st = _s(stream)
+    status = _status("gpt2_op_attention_packed_backward", status, device)
     sc = _borrow(nb, st) if nb else None
     try:
-        check(lib.gpt2_op_attention_packed_backward(*args, sc, nb, _p(status), st), "gpt2_op_attention_packed_backward")
+        check(lib.gpt2_op_attention_packed_backward(*args, sc, nb, status, st), "gpt2_op_attention_packed_backward")
     finally:
         if sc:
             _give_back(sc)
@@ -745,21 +786,25 @@ def gpt2_op_token_logprobs(logp, lse, entropy, logits, targets, V, top_logp=None
     top_logp (float32) and top_ids (int32), both [N, k] or none: the k largest."""
     dt = _mode_of("logits", logits)
     N, Vp = _logits(logits)
-    if (top_logp is None) != (top_ids is None) or (top_ids is not None and top_logp.shape != top_ids.shape):
-        raise ValueError("top_logp and top_ids come together, in one shape")
-    k = 0
-    if top_ids is not None:
-        if top_ids.dim() != 2:
-            raise ValueError("top_logp and top_ids [N, k] are needed")
-        k = top_ids.shape[1]
-        _arrays("top_logp", _torch.float32, (N, k), top_logp)
-        _arrays("top_ids", _torch.int32, (N, k), top_ids)
-    _arrays("logp, lse and entropy", _torch.float32, (N,), logp, lse, entropy)
-    _arrays("targets", _torch.int32, (N,), targets)
-    _here("gpt2_op_token_logprobs", status, logp, lse, entropy, logits, targets, top_logp, top_ids)
-    check(load_library().gpt2_op_token_logprobs(dt, _p(logp), _p(lse), _p(entropy), _p(top_logp), _p(top_ids), k,
-                                                _p(logits), _p(targets), N, V, Vp, _p(status), _s(stream)),
-          "gpt2_op_token_logprobs")
+    device, st = _where(stream)
+    k, top, here = 0, (None, None), True
+    if top_logp is not None or top_ids is not None:
+        if top_logp is None or top_ids is None or top_ids.dim() != 2 or top_logp.shape != top_ids.shape:
+            raise ValueError("top_logp and top_ids come together, in one shape [N, k]")
+        n, k = top_ids.shape
+        if n != N or top_logp.dtype is not _torch.float32 or top_ids.dtype is not _torch.int32 \
+                or not top_logp.is_contiguous() or not top_ids.is_contiguous():
+            raise ValueError("contiguous top_logp (float32) and top_ids (int32) of shape [N, k] are needed")
+        here = device == top_logp.get_device() == top_ids.get_device()
+        top = top_logp.data_ptr(), top_ids.data_ptr()
+    arrays = (logp, lse, entropy)
+    if not _fit(device, N, arrays, targets):
+        _refuse("gpt2_op_token_logprobs", device, N, arrays, targets)
+    if not (here and logits.get_device() == device):
+        raise _elsewhere("gpt2_op_token_logprobs")
+    status = _status("gpt2_op_token_logprobs", status, device)
+    check(load_library().gpt2_op_token_logprobs(dt, _p(logp), _p(lse), _p(entropy), *top, k, logits.data_ptr(),
+                                                _p(targets), N, V, Vp, status, st), "gpt2_op_token_logprobs")
 
 
 def gpt2_op_token_logprobs_backward(dlogits, logits, targets, lse, entropy, V, dlogp=None, dlse=None, dentropy=None,
@@ -767,16 +812,19 @@ def gpt2_op_token_logprobs_backward(dlogits, logits, targets, lse, entropy, V, d
     """dlogits [N, Vp] (may be logits) from the gradients (float32 [N]) of gpt2_op_token_logprobs' logp, lse and
     entropy."""
     dt = _mode_of("logits", logits)
-    N, Vp = _logits(logits)
-    if _logits(dlogits) != logits.shape or dlogits.dtype is not logits.dtype:
+    N, Vp = shape = _logits(logits)
+    if _logits(dlogits) != shape or dlogits.dtype is not logits.dtype:
         raise ValueError("logits and dlogits need one shape and type")
-    _arrays("lse, entropy and the gradients", _torch.float32, (N,), lse, entropy, dlogp, dlse, dentropy)
-    _arrays("targets", _torch.int32, (N,), targets)
-    _here("gpt2_op_token_logprobs_backward", status, dlogits, logits, targets, lse, entropy, dlogp, dlse, dentropy)
-    check(load_library().gpt2_op_token_logprobs_backward(dt, _p(dlogits), _p(logits), _p(targets), _p(lse),
-                                                         _p(entropy), _p(dlogp), _p(dlse), _p(dentropy), N, V, Vp,
-                                                         _p(status), _s(stream)),
-          "gpt2_op_token_logprobs_backward")
+    device, st = _where(stream)
+    arrays = (lse, entropy, dlogp, dlse, dentropy)
+    if not _fit(device, N, arrays, targets):
+        _refuse("gpt2_op_token_logprobs_backward", device, N, arrays, targets)
+    if not device == logits.get_device() == dlogits.get_device():
+        raise _elsewhere("gpt2_op_token_logprobs_backward")
+    status = _status("gpt2_op_token_logprobs_backward", status, device)
+    check(load_library().gpt2_op_token_logprobs_backward(dt, dlogits.data_ptr(), logits.data_ptr(), _p(targets),
+                                                         _p(lse), _p(entropy), _p(dlogp), _p(dlse), _p(dentropy), N, V,
+                                                         Vp, status, st), "gpt2_op_token_logprobs_backward")
 
 
 def gpt2_op_gelu_forward(g, u, stream=None):
