@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(NT)
 // before: they are handed each reading thread's largest logit and the warps'
 // sums through shared memory. A block for a row that read and then searched
 // took 59 us for 2043 rows of 50257 with 20 alternatives and 734 for 32768,
-// this 51 and 700; three places for a thread's batches instead of two took 70
+// this 51 and 686; three places for a thread's batches instead of two took 70
 // (the search's own loads wait behind them).
 constexpr int TNT = 256;   // threads that read
 constexpr int TB = 4;      // vectors of its batch
@@ -851,7 +851,7 @@ template <typename T, int NT, bool TOP>
 int forward(float* logp, float* lse, float* entropy, float* top_logp, int32_t* top_ids, int k, const T* logits,
             const int32_t* targets, int N, int V, int Vp, int* status, cudaStream_t s) {
     // as many blocks to a row as leave each SM one, and each thread a vector (8 rows of 50257 in fp32: 6.2 us with
-    // eight, 8.3 with one; with 5 alternatives 8.7 with four, 11.3 with eight, with 40 16.5 and 32)
+    // eight, 8.3 with one; with 5 alternatives 8.5 with four, 11.3 with eight, with 40 16.5 and 32)
     int split = 1;
     while (split < (TOP ? TOP_SPLIT : MAX_SPLIT) && (int64_t)N * split * 2 <= gpt2_num_sms() && V / VEC<T> >= split * 2 * 256) split *= 2;
     cudaLaunchConfig_t cfg = {};
@@ -879,7 +879,7 @@ int forward_top(float* logp, float* lse, float* entropy, float* top_logp, int32_
     return 1;
 }
 // Threads of a block: twice as many rows on their way in blocks of 128 read
-// 32768 rows of 50257 at the speed of a copy (496 us; 535 with 256), but few
+// 32768 rows of 50257 at the speed of a copy (498 us; about 8% more with 256), but few
 // rows want the wider block. With alternatives, rows are handed to searching
 // warps where a block for each (four to an SM) would come in more than one
 // round, and for k up to 32 (rows of 50257 with 20: 600 take 25 us handed over
