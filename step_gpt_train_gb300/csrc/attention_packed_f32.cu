@@ -243,6 +243,7 @@ template <int HD> __global__ void __launch_bounds__(NT) packed_fwd_f32_kernel(co
         products<HD>(o, sp, sv, ty, tx);
         __syncthreads();  // done with V and P
     }
+    if (keys == 0) cp_async_wait<0>();  // Q, which nobody waited for
 #pragma unroll
     for (int r = 0; r < 4; r++) {
         const int i = ty + 16 * r;

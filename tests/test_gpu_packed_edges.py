@@ -162,6 +162,36 @@ def test_attention_some_sequences_grow(torch_cuda, n, Hq, Hkv):
     assert torch.equal(o.nan_to_num(), c.o.nan_to_num()) and torch.equal(lse, c.lse)
 
 
+def test_attention_growing_scores_in_graphs(torch_cuda):
+    """Graphs whose calls go through their items twice, replayed in turn with eager calls and on two streams at once."""
+    torch = torch_cuda
+    cs = []
+    for seed, n in ((55, 900), (56, 2000)):
+        c = Packed(torch, seed, [n, 50], [n, 700], 8, 2, 64, 1)
+        c.tq[c.cu_q[0]:c.cu_q[-1], :, 0] = 8.0
+        c.tk[c.cu_k[0]:c.cu_k[-1], :, 0] = torch.linspace(-90, 90, n + 700, device="cuda")[:, None].bfloat16()
+        c.forward()
+        cs.append((c, c.o.clone(), c.lse.clone(), torch.cuda.CUDAGraph(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for c, _, _, graph, _ in cs:
+        with torch.cuda.graph(graph):
+            c.forward()
+    for _ in range(3):
+        for c, *_ in cs:
+            c.o.fill_(c.FILL)
+            c.lse.fill_(c.FILL)
+        torch.cuda.synchronize()
+        for c, _, _, graph, stream in cs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for c, o, lse, _, _ in cs:
+            assert c.status.item() == 0 and torch.equal(c.o, o) and torch.equal(c.lse, lse)
+            c.forward()
+            torch.cuda.synchronize()
+            assert torch.equal(c.o, o) and torch.equal(c.lse, lse)
+
+
 def test_attention_backward_positions_times_heads_past_31_bits(torch_cuda):
     """64 heads on one over 2^25 keys: key positions counted in (query, head) rows pass 2^31. Every key is seen by the
     one query with the same weight, so every row of dV is the same, and dK is 0."""
