@@ -390,6 +390,166 @@ int gpt2_op_adamw(float* master, void* param_bf16, const float* grad, float* m, 
                   int64_t n, float lr, float beta1, float beta2, float eps, float weight_decay,
                   int t, void* stream);
 
+/* Norms of queries and keys for each head with the position rotation, in one
+ * pass (an addition of this library: positions for packed sequences, whose
+ * tokens the encoder's learned positions do not count). For N rows (tokens) of
+ * Hq query heads and Hk key heads of hd values, each head x becomes
+ *   n = x * rstd * gamma, rstd = 1 / sqrt(mean(x^2) + eps)   (norm != 0; else n = x)
+ *   y_a = amplitude (n_a cos t - n_b sin t), y_b = amplitude (n_a sin t + n_b cos t)
+ * for the pairs of its first rot values: (j, j + rot / 2) (interleaved = 0) or
+ * (2 j, 2 j + 1) (interleaved != 0), j < rot / 2; the other values keep n. The
+ * angle t is pos[row] * turns[j] * 2^-64 turns, modulo one turn: turns is a
+ * device array of rot / 2 fractions of a turn per position (gpt2_rotary_turns
+ * fills one on the host), and any int32 position keeps its angle to 2^-33 of a turn.
+ *   q, qo: rows of Hq * hd values, k, ko: rows of Hk * hd (dtype), head h at
+ *   columns h*hd .. of a row; *_stride: elements from one row to the next, so
+ *   they may be column blocks of one fused buffer. qo may be q and ko k (with
+ *   the same stride); otherwise outputs must not overlap inputs.
+ *   q_gamma, k_gamma: [hd] in dtype, or null (ones); unused without norm.
+ *   - hd 8, 16, 32, 64 or 128; rot a multiple of 8, 0 <= rot <= hd (turns may
+ *     be null for 0). Hq, Hk >= 0, not both 0 (pointers of none are unused).
+ *     Pointers 16-byte aligned, strides multiples of 16 bytes and at least the
+ *     row. eps > 0 with norm; amplitude finite. N = 0 launches nothing. */
+int gpt2_op_qk_norm_rotary_forward(int dtype, void* qo, int64_t qo_stride, void* ko, int64_t ko_stride, const void* q,
+                                   int64_t q_stride, const void* k, int64_t k_stride, const void* q_gamma,
+                                   const void* k_gamma, const int32_t* pos, const uint64_t* turns, int N, int Hq,
+                                   int Hk, int hd, int rot, int interleaved, int norm, float eps, float amplitude,
+                                   void* stream);
+
+/* Its backward: from dqo, dko (gradients of qo, ko) and the forward's q, k
+ * (read with norm only; they may be null without), with dn the gradient turned
+ * back, xhat = x rstd: dx = rstd (dn gamma - xhat mean(dn gamma xhat)) into dq,
+ * dk (dtype, overwritten; dq may be dqo and dk dko with the same stride),
+ * dq_gamma, dk_gamma [hd] fp32 = the sums of dn xhat over rows and heads
+ * (overwritten; either may be null, both are unused without norm).
+ * Deterministic (no atomics). N = 0 sets the gammas' gradients to 0. Scratch:
+ * partial sums of the gammas' gradients. Limits as in the forward. */
+size_t gpt2_op_qk_norm_rotary_backward_scratch(int N, int hd);
+int gpt2_op_qk_norm_rotary_backward(int dtype, void* dq, int64_t dq_stride, void* dk, int64_t dk_stride,
+                                    float* dq_gamma, float* dk_gamma, const void* dqo, int64_t dqo_stride,
+                                    const void* dko, int64_t dko_stride, const void* q, int64_t q_stride,
+                                    const void* k, int64_t k_stride, const void* q_gamma, const void* k_gamma,
+                                    const int32_t* pos, const uint64_t* turns, int N, int Hq, int Hk, int hd, int rot,
+                                    int interleaved, int norm, float eps, float amplitude, void* scratch,
+                                    size_t scratch_bytes, void* stream);
+
+/* Host: turns[j] = round(2^64 f_j / (2 pi)) for j < rot / 2 (host memory), with
+ * the frequencies f_j = base^(-2 j / rot) stretched for contexts longer than
+ * the model's own:
+ *   GPT2_ROTARY_PLAIN   as they are;
+ *   GPT2_ROTARY_LINEAR  divided by factor (positions interpolated);
+ *   GPT2_ROTARY_BASE    base * factor^(rot / (rot - 2)) in place of base: the
+ *                       fastest pair stays, the slowest is divided by factor;
+ *   GPT2_ROTARY_PARTS   divided by factor where a pair turns less than slow
+ *                       times over `context` positions, kept where it turns
+ *                       more than fast times, blended linearly in the number
+ *                       of turns between.
+ * rot even and >= 0, base > 1, factor >= 1, and for PARTS context >= 1, fast > slow >= 0
+ * (else GPT2_ERR_ARG). */
+#define GPT2_ROTARY_PLAIN 0
+#define GPT2_ROTARY_LINEAR 1
+#define GPT2_ROTARY_BASE 2
+#define GPT2_ROTARY_PARTS 3
+int gpt2_rotary_turns(uint64_t* turns, int rot, double base, int scaling, double factor, double context, double fast,
+                      double slow);
+
+/* Softmax cross entropy from hidden states and the head's weight, without
+ * keeping the logits (an addition of this library: gpt2_op_matmul with the
+ * head's weight followed by gpt2_op_classifier, without the N x V buffer
+ * between them). With z = x W^T over the first V rows of W:
+ *   lse[i] = log sum_j<V exp z_ij, losses[i] = lse[i] - z_i,targets[i] (fp32),
+ * formed as (max - z_target) + ln sum exp(z - max): never negative, and as
+ * exact far from 0 as near it. x [N, C], w [>= V, C] in dtype (the rows of w
+ * from V on are not used, whatever they hold); the logits are fp32 and are not
+ * rounded. A target outside [0,V) sets bit 4 of *d_status and is treated as 0.
+ * Rows of x are independent; a row with a logit that is not finite gets NaN.
+ * C % 8 == 0, C >= 8, V >= 1, x and w 16-byte aligned, N * C and V * C below
+ * 2^31 - 2048; N = 0 launches nothing. Scratch: row statistics of the
+ * vocabulary's tiles (fp32: also the logits of a piece of the vocabulary). */
+size_t gpt2_op_linear_classifier_forward_scratch(int dtype, int N, int C, int V);
+int gpt2_op_linear_classifier_forward(int dtype, float* losses, float* lse, const void* x, const void* w,
+                                      const int32_t* targets, int N, int C, int V, void* scratch,
+                                      size_t scratch_bytes, int* d_status, void* stream);
+
+/* Its gradient from the forward's lse: with p = exp(z - lse) formed again, in
+ * pieces of the vocabulary,
+ *   dz_ij = (dloss[i] + dlse[i]) p_ij - dloss[i] [j == targets[i]],
+ *   dx = dz W (dtype, overwritten), dw = dz^T x.
+ * dloss, dlse: [N] fp32, gradients of losses and lse, either may be null (0). A
+ * row whose dloss and dlse are 0 has dz = 0 whatever its logits are (a prompt's
+ * or padding's tokens; its x has to be finite: dw adds 0 x). dw [Vp, C], Vp >= V,
+ * Vp % 8 == 0: fp32 (dw_fp32 = 1; the only form in fp32) or bf16; rows from V
+ * on get 0. accumulate (fp32 dw only): dw += instead, rows from V on stay. In
+ * bf16 dz is rounded to bf16 for the products, as gpt2_op_classifier's dlogits
+ * are: half a step (2^-8) of each value; sums are fp32. p carries lse's own
+ * rounding (|lse| 2^-24, relative). Deterministic (no atomics). dx and dw must
+ * not overlap the inputs or each other. Limits as in the forward; N = 0 sets
+ * dw to 0 (or leaves it, with accumulate). Scratch: a piece of dz (about 256 MB,
+ * or 2048 columns where that is more), dx in fp32, partial products. */
+size_t gpt2_op_linear_classifier_backward_scratch(int dtype, int N, int C, int V, int dw_fp32, int accumulate);
+int gpt2_op_linear_classifier_backward(int dtype, void* dx, void* dw, int dw_fp32, int accumulate, const void* x,
+                                       const void* w, const int32_t* targets, const float* lse, const float* dloss,
+                                       const float* dlse, int N, int C, int V, int Vp, void* scratch,
+                                       size_t scratch_bytes, int* d_status, void* stream);
+
+/* AdamW over many tensors at once, with moments in 32 or in 8 bits (an
+ * addition of this library: gpt2_op_adamw for a list of tensors of any sizes).
+ * For each value of each tensor, with g = grad * grad_scale * clip, clip =
+ * min(1, max_grad_norm / (||grad|| grad_scale + 1e-6)) over all tensors if
+ * max_grad_norm > 0, else 1 (as gpt2_adamw_step_ex):
+ *   m = b1 m + (1-b1) g; v = b2 v + (1-b2) g^2;
+ *   theta -= lr (m/(1-b1^t) / (sqrt(v/(1-b2^t)) + eps) + weight_decay theta),
+ * and bf16(theta) to param_bf16 where that is not null. grad_norm, if not
+ * null, receives ||grad|| (before grad_scale; device float). Deterministic.
+ *
+ * The list is host memory and is read during the call only. grads are all in
+ * grad_dtype. n >= 0 values of any count (n = 0: nothing to do); addresses need
+ * the alignment of their type only (16 bytes are faster). Tensors must not
+ * overlap. At most 2^24 tensors of together fewer than 2^42 values.
+ *
+ * bits = 32: m and v are fp32 [n]; m_scale and v_scale are unused. bits = 8: m
+ * and v are n bytes each, m_scale and v_scale ceil(n / 128) bytes; zeros are
+ * moments of 0. The value of a code under its block's scale byte s (128
+ * consecutive values share one) is code * 2^(s - 127):
+ *   m   sign, 4 exponent bits (bias 7), 3 mantissa bits; the largest magnitude
+ *       of a block lies in [2^7, 2^8]; 0x7F and 0xFF are NaN;
+ *   v   5 exponent bits (bias 15), 3 mantissa bits, no sign; the largest lies
+ *       in [2^14, 2^15]; 0xFF is NaN.
+ * Both have subnormals. The new m and v are formed in fp32 and used for theta
+ * as they are; stored, they are rounded up or down to a neighbouring code so
+ * that they are right on average: up where (what is left over the lower code)
+ * / (the codes' distance) + u >= 1, with u = r / 2^16 and r 16 bits of
+ * splitmix64's finaliser mix: values 2p and 2p + 1 of tensor k (from 0 in the
+ * list) take bits 0-15 and 32-47 (m) and 16-31 and 48-63 (v) of
+ *   mix(mix(seed + t G) + (k 2^40 + p) G), G = 0x9E3779B97F4A7C15.
+ * A v above 0 is stored as its lowest code at least. What is not finite is
+ * stored as NaN and leaves its block's scale alone.
+ *
+ * beta1, beta2 in [0, 1), eps >= 0, t >= 1, max_grad_norm >= 0. Scratch: partial
+ * sums of the norm (needed with max_grad_norm > 0 or grad_norm). */
+typedef struct gpt2_adamw_tensor {
+    float* master;
+    void* param_bf16;
+    const void* grad;
+    void* m;
+    void* v;
+    uint8_t* m_scale;
+    uint8_t* v_scale;
+    int64_t n;
+    float weight_decay;
+} gpt2_adamw_tensor;
+size_t gpt2_op_adamw_many_scratch(const gpt2_adamw_tensor* tensors, int n_tensors);
+int gpt2_op_adamw_many(const gpt2_adamw_tensor* tensors, int n_tensors, int grad_dtype, int bits, float lr,
+                       float beta1, float beta2, float eps, float grad_scale, float max_grad_norm, float* grad_norm,
+                       int t, uint64_t seed, void* scratch, size_t scratch_bytes, void* stream);
+
+/* The values of 8-bit moments of the tensors, in dtype (bf16 holds every one
+ * of them exactly, down to its subnormals): m_values[i] and v_values[i] (host
+ * arrays of device pointers) receive tensors[i].n values each. Of the tensors,
+ * m, v, m_scale, v_scale and n are read. */
+int gpt2_op_adamw_many_states(const gpt2_adamw_tensor* tensors, void* const* m_values, void* const* v_values,
+                              int n_tensors, int dtype, void* stream);
+
 /* Failure-path testing of the bounded device waits (the design's failure
  * detection: a wait that runs out sets a status bit and the kernel returns;
  * nothing traps or hangs).

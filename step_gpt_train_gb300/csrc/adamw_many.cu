@@ -1,0 +1,415 @@
+// AdamW over many tensors in one launch, moments in 32 or in 8 bits
+// (gpt2_op_adamw_many), and 8-bit moments read back (gpt2_op_adamw_many_states).
+//
+// The tensors' addresses travel as kernel parameters, so a call leaves nothing
+// behind. A block serves CHUNK consecutive values of one tensor, found by a
+// binary search over the tensors' first blocks; a thread holds four neighbours
+// of each of its groups, a warp the 128 values that share an 8-bit moment's
+// scale.
+//
+// 8-bit moments: m as e4m3 codes and v as e5m3 codes (no sign bit, bias 15)
+// under a power of two for each 128 values, chosen so that the block's largest
+// value lies in [2^7, 2^8) and [2^14, 2^15): 17 and 31 binades below it can be
+// told apart. A power of two keeps codes that did not change exact from step to
+// step, and one byte holds it. Rounding goes up or down by 16 random bits, so
+// that the stored moment is right on average: with three mantissa bits,
+// rounding to nearest would never let v shrink at beta2 = 0.95 or above (a step
+// changes it by 5% at most, half a code is 6%). A v above 0 keeps at least the
+// lowest code, so that no m meets a v that was rounded away. The parameter's
+// own update uses m and v before they are rounded.
+//
+// HBM bounds it: per parameter 8 bytes of master, 2 of its bf16 copy, the
+// gradient, and 16 or 4 + 1/32 of moments.
+#include "common.cuh"
+#include "launch.h"
+
+#include <math.h>
+
+namespace {
+
+constexpr int THREADS = 256;
+constexpr int GROUPS = 4;                       // groups of four values a thread
+constexpr int CHUNK = THREADS * 4 * GROUPS;     // values a block
+constexpr int SCALE_BLOCK = 128;                // values that share a scale: a warp's group
+
+struct Entry {
+    float* master;
+    bf16* param;
+    const void* grad;
+    void *m, *v;
+    uint8_t *m_scale, *v_scale;
+    int64_t n;
+    float decay;
+    int first;   // first block of this tensor
+    int aligned; // every address allows four values at once
+    int pad;
+};
+
+// MOST tensors a launch: few fit the classic 4 KB of parameters, whose upload is cheaper.
+template <int MOST> struct Batch {
+    Entry e[MOST];
+    int n, base;  // base: the first tensor's number in the call
+};
+constexpr int FEW = 48, MANY = 380;
+static_assert(sizeof(Batch<FEW>) <= 4000 && sizeof(Batch<MANY>) <= 32000, "kernel parameters");
+
+struct Values {
+    float lr, b1, b2, eps, inv_bc1, inv_bc2, grad_scale, max_norm;
+    const float* norm;  // or null
+    uint64_t key;
+};
+
+template <int MOST> __device__ __forceinline__ int find(const Batch<MOST>& b, int block) {
+    int lo = 0, hi = b.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (b.e[mid].first <= block) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ uint64_t mix(uint64_t z) {  // the finaliser of splitmix64
+    z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ULL;
+    z = (z ^ (z >> 27)) * 0x94D049BB133111EBULL;
+    return z ^ (z >> 31);
+}
+
+// Four neighbours of n values from i on; what lies behind the end reads as 0 and is not written.
+__device__ __forceinline__ void get4(const float* p, int64_t i, int64_t n, bool whole, float (&f)[4]) {
+    if (whole) {
+        const float4 a = __ldcs(reinterpret_cast<const float4*>(p + i));
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++) f[j] = i + j < n ? p[i + j] : 0.f;
+    }
+}
+__device__ __forceinline__ void get4(const bf16* p, int64_t i, int64_t n, bool whole, float (&f)[4]) {
+    if (whole) {
+        const uint2 u = __ldcs(reinterpret_cast<const uint2*>(p + i));
+        f[0] = __uint_as_float(u.x << 16); f[1] = __uint_as_float(u.x & 0xFFFF0000u);
+        f[2] = __uint_as_float(u.y << 16); f[3] = __uint_as_float(u.y & 0xFFFF0000u);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++) f[j] = i + j < n ? __bfloat162float(p[i + j]) : 0.f;
+    }
+}
+__device__ __forceinline__ uint32_t get4(const uint8_t* p, int64_t i, int64_t n, bool whole) {
+    if (whole) return __ldcs(reinterpret_cast<const uint32_t*>(p + i));
+    uint32_t u = 0;
+#pragma unroll
+    for (int j = 0; j < 4; j++) u |= i + j < n ? (uint32_t)p[i + j] << (8 * j) : 0u;
+    return u;
+}
+__device__ __forceinline__ void put4(float* p, int64_t i, int64_t n, bool whole, const float (&f)[4]) {
+    if (whole) {
+        __stcs(reinterpret_cast<float4*>(p + i), make_float4(f[0], f[1], f[2], f[3]));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            if (i + j < n) p[i + j] = f[j];
+    }
+}
+__device__ __forceinline__ void put4(bf16* p, int64_t i, int64_t n, bool whole, const float (&f)[4]) {
+    if (whole) {
+        uint2 u;
+        __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
+        h[0] = __floats2bfloat162_rn(f[0], f[1]);
+        h[1] = __floats2bfloat162_rn(f[2], f[3]);
+        *reinterpret_cast<uint2*>(p + i) = u;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            if (i + j < n) p[i + j] = __float2bfloat16_rn(f[j]);
+    }
+}
+__device__ __forceinline__ void put4(uint8_t* p, int64_t i, int64_t n, bool whole, uint32_t u) {
+    if (whole) {
+        __stcs(reinterpret_cast<uint32_t*>(p + i), u);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            if (i + j < n) p[i + j] = (uint8_t)(u >> (8 * j));
+    }
+}
+
+// A code of three mantissa bits read as the top of an fp32 number: 2^(127 - bias) restores its exponent,
+// and codes below the lowest whole exponent come out right as fp32 subnormals.
+__device__ __forceinline__ float decode_m(uint32_t c, float scale) {
+    const uint32_t k = c & 0x7Fu;
+    float y = __uint_as_float(k << 20) * 0x1p120f;
+    if (k == 0x7Fu) y = __uint_as_float(0x7FC00000u);
+    return (c & 0x80u ? -y : y) * scale;
+}
+__device__ __forceinline__ float decode_v(uint32_t c, float scale) {
+    const float y = __uint_as_float(c << 20) * 0x1p112f;
+    return (c == 0xFFu ? __uint_as_float(0x7FC00000u) : y) * scale;
+}
+__device__ __forceinline__ float scale_of(uint8_t b) { return __uint_as_float((b < 1 ? 1u : b > 254 ? 254u : b) << 23); }
+
+// The code of y >= 0 (already divided by the scale) with exponent bias BIAS, rounded up with probability
+// (what is left of it) / (a code's step): r are 16 random bits. Not a number, or infinite: all ones.
+template <int BIAS> __device__ __forceinline__ uint32_t encode(float y, uint32_t r) {
+    constexpr float LOWEST = BIAS == 7 ? 0x1p-6f : 0x1p-14f, STEPS = BIAS == 7 ? 0x1p9f : 0x1p17f;
+    if (y >= LOWEST) return ((__float_as_uint(y) + (r << 4)) >> 20) - ((127u - BIAS) << 3);
+    return (uint32_t)(y * STEPS + (float)r * 0x1p-16f);
+}
+__device__ __forceinline__ uint32_t finite_bits(float x) {
+    const uint32_t u = __float_as_uint(x) & 0x7FFFFFFFu;
+    return u < 0x7F800000u ? u : 0u;
+}
+// The scale byte of a block whose largest magnitude has these bits.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t largest, int top) {
+    const int b = (int)(largest >> 23) - top;
+    return b < 1 ? 1u : (uint32_t)b;
+}
+
+template <int MOST, typename G, bool EIGHT>
+__global__ void __launch_bounds__(THREADS) adamw_many_kernel(const __grid_constant__ Batch<MOST> b, const Values h) {
+    const int k = find(b, blockIdx.x);
+    const Entry& e = b.e[k];
+    const int64_t n = e.n, base = (int64_t)((int)blockIdx.x - e.first) * CHUNK + threadIdx.x * 4;
+    float gs = h.grad_scale;
+    if (h.norm) gs *= fminf(1.f, h.max_norm / (*h.norm * h.grad_scale + 1e-6f));
+    const uint64_t tensor = (uint64_t)(b.base + k) << 40;
+#pragma unroll
+    for (int u = 0; u < GROUPS; u++) {
+        const int64_t i = base + u * (THREADS * 4);
+        if (i - (threadIdx.x & 31) * 4 >= n) break;  // the whole warp
+        const bool whole = e.aligned && i + 4 <= n;
+        float th[4], g[4], m[4], v[4];
+        get4(e.master, i, n, whole, th);
+        get4((const G*)e.grad, i, n, whole, g);
+        if (EIGHT) {
+            const int64_t at = i / SCALE_BLOCK;
+            const float ms = scale_of(e.m_scale[at]), vs = scale_of(e.v_scale[at]);
+            const uint32_t cm = get4((const uint8_t*)e.m, i, n, whole), cv = get4((const uint8_t*)e.v, i, n, whole);
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                m[j] = decode_m(cm >> (8 * j) & 0xFFu, ms);
+                v[j] = decode_v(cv >> (8 * j) & 0xFFu, vs);
+            }
+        } else {
+            get4((const float*)e.m, i, n, whole, m);
+            get4((const float*)e.v, i, n, whole, v);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const float gj = g[j] * gs;
+            m[j] = h.b1 * m[j] + (1.f - h.b1) * gj;
+            v[j] = h.b2 * v[j] + (1.f - h.b2) * gj * gj;
+            th[j] = th[j] - h.lr * (m[j] * h.inv_bc1 / (sqrtf(v[j] * h.inv_bc2) + h.eps) + e.decay * th[j]);
+        }
+        put4(e.master, i, n, whole, th);
+        if (e.param) put4(e.param, i, n, whole, th);
+        if (EIGHT) {
+            uint32_t am = 0, av = 0;
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                am = max(am, finite_bits(m[j]));
+                av = max(av, finite_bits(v[j]));
+            }
+            am = __reduce_max_sync(0xffffffffu, am);
+            av = __reduce_max_sync(0xffffffffu, av);
+            const uint32_t bm = scale_byte(am, 7), bv = scale_byte(av, 14);
+            const float im = __uint_as_float((254u - bm) << 23), iv = __uint_as_float((254u - bv) << 23);
+            uint32_t cm = 0, cv = 0;
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+                const uint64_t r = mix(h.key + (tensor + (uint64_t)(i + j) / 2) * 0x9E3779B97F4A7C15ULL);
+#pragma unroll
+                for (int o = 0; o < 2; o++) {
+                    const uint32_t w = (uint32_t)(r >> (32 * o));
+                    const float x = m[j + o], y = v[j + o];
+                    uint32_t c = isfinite(x) ? encode<7>(fabsf(x) * im, w & 0xFFFFu) : 0x7Fu;
+                    if (x < 0.f) c |= 0x80u;
+                    cm |= c << (8 * (j + o));
+                    c = isfinite(y) ? encode<15>(y * iv, w >> 16) : 0xFFu;
+                    if (c == 0 && y > 0.f) c = 1;
+                    cv |= c << (8 * (j + o));
+                }
+            }
+            put4((uint8_t*)e.m, i, n, whole, cm);
+            put4((uint8_t*)e.v, i, n, whole, cv);
+            if ((threadIdx.x & 31) == 0) {
+                e.m_scale[i / SCALE_BLOCK] = (uint8_t)bm;
+                e.v_scale[i / SCALE_BLOCK] = (uint8_t)bv;
+            }
+        } else {
+            put4((float*)e.m, i, n, whole, m);
+            put4((float*)e.v, i, n, whole, v);
+        }
+    }
+}
+
+// Sum of squares of a block's gradients, in a fixed order.
+template <int MOST, typename G>
+__global__ void __launch_bounds__(THREADS) sumsq_many_kernel(const __grid_constant__ Batch<MOST> b,
+                                                             float* __restrict__ partial) {
+    __shared__ float sh[THREADS / 32];
+    const Entry& e = b.e[find(b, blockIdx.x)];
+    const int64_t n = e.n, base = (int64_t)((int)blockIdx.x - e.first) * CHUNK + threadIdx.x * 4;
+    float acc = 0.f;
+#pragma unroll
+    for (int u = 0; u < GROUPS; u++) {
+        const int64_t i = base + u * (THREADS * 4);
+        float g[4];
+        get4((const G*)e.grad, i, n, e.aligned && i + 4 <= n, g);
+        acc += g[0] * g[0] + g[1] * g[1] + g[2] * g[2] + g[3] * g[3];
+    }
+    acc = warp_sum(acc);
+    if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = acc;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float t = 0.f;
+#pragma unroll
+        for (int w = 0; w < THREADS / 32; w++) t += sh[w];
+        partial[blockIdx.x] = t;
+    }
+}
+
+__global__ void __launch_bounds__(1024) norm_many_kernel(float* __restrict__ norm, float* __restrict__ out,
+                                                         const float* __restrict__ partial, int64_t n) {
+    __shared__ double sh[32];
+    double v = 0.0;
+    for (int64_t i = threadIdx.x; i < n; i += 1024) v += partial[i];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = v;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double t = 0.0;
+        for (int w = 0; w < 32; w++) t += sh[w];
+        *norm = (float)sqrt(t);
+        if (out) *out = *norm;
+    }
+}
+
+template <int MOST, typename T>
+__global__ void __launch_bounds__(THREADS) states_many_kernel(const __grid_constant__ Batch<MOST> b) {
+    const Entry& e = b.e[find(b, blockIdx.x)];
+    const int64_t n = e.n, base = (int64_t)((int)blockIdx.x - e.first) * CHUNK + threadIdx.x * 4;
+#pragma unroll
+    for (int u = 0; u < GROUPS; u++) {
+        const int64_t i = base + u * (THREADS * 4);
+        if (i >= n) break;
+        const bool whole = e.aligned && i + 4 <= n;
+        const int64_t at = i / SCALE_BLOCK;
+        const float ms = scale_of(e.m_scale[at]), vs = scale_of(e.v_scale[at]);
+        const uint32_t cm = get4((const uint8_t*)e.m, i, n, whole), cv = get4((const uint8_t*)e.v, i, n, whole);
+        float m[4], v[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            m[j] = decode_m(cm >> (8 * j) & 0xFFu, ms);
+            v[j] = decode_v(cv >> (8 * j) & 0xFFu, vs);
+        }
+        put4((T*)(void*)e.master, i, n, whole, m);  // the values' places travel in master and param
+        put4((T*)(void*)e.param, i, n, whole, v);
+    }
+}
+
+bool at16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+// The entries of tensors [i0, i1) and the blocks that they take.
+template <int MOST, typename Fill> int gather(Batch<MOST>& b, const gpt2_adamw_tensor* t, int i0, int i1, Fill fill) {
+    int64_t blocks = 0;
+    b.n = 0;
+    b.base = i0;
+    for (int i = i0; i < i1; i++) {
+        Entry& e = b.e[b.n++];
+        e = {t[i].master, (bf16*)t[i].param_bf16, t[i].grad, t[i].m, t[i].v, t[i].m_scale, t[i].v_scale, t[i].n,
+             t[i].weight_decay, (int)blocks, 0, 0};
+        fill(e, i);
+        e.aligned = at16(e.master) && at16(e.param) && at16(e.grad) && at16(e.m) && at16(e.v);
+        blocks += (e.n + CHUNK - 1) / CHUNK;
+    }
+    return (int)blocks;
+}
+
+int64_t blocks_of(const gpt2_adamw_tensor* t, int n) {
+    int64_t blocks = 0;
+    for (int i = 0; i < n; i++) blocks += (t[i].n + CHUNK - 1) / CHUNK;
+    return blocks;
+}
+
+// Calls go(batch, blocks) for the tensors in as few launches as they fit.
+template <typename Fill, typename Go> int in_batches(const gpt2_adamw_tensor* t, int n, Fill fill, Go go) {
+    int launches = 0;
+    for (int i = 0; i < n;) {
+        const int left = n - i;
+        if (left <= FEW) {
+            Batch<FEW> b;
+            const int blocks = gather(b, t, i, n, fill);
+            if (blocks) launches++, go(b, blocks);
+            i = n;
+        } else {
+            const int to = left < MANY ? n : i + MANY;
+            Batch<MANY> b;
+            const int blocks = gather(b, t, i, to, fill);
+            if (blocks) launches++, go(b, blocks);
+            i = to;
+        }
+    }
+    return launches;
+}
+
+template <int MOST, typename G>
+void start_adamw(const Batch<MOST>& b, int blocks, int bits, const Values& h, cudaStream_t s) {
+    if (bits == 8) adamw_many_kernel<MOST, G, true><<<blocks, THREADS, 0, s>>>(b, h);
+    else adamw_many_kernel<MOST, G, false><<<blocks, THREADS, 0, s>>>(b, h);
+}
+
+uint64_t host_mix(uint64_t z) {
+    z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ULL;
+    z = (z ^ (z >> 27)) * 0x94D049BB133111EBULL;
+    return z ^ (z >> 31);
+}
+
+}  // namespace
+
+// The norm, then a partial sum for each block.
+size_t adamw_many_scratch(const gpt2_adamw_tensor* t, int n) { return 256 + (size_t)blocks_of(t, n) * 4; }
+
+int launch_adamw_many(const gpt2_adamw_tensor* t, int n, int grad_dtype, int bits, float lr, float b1, float b2,
+                      float eps, float grad_scale, float max_norm, float* grad_norm, int step, uint64_t seed,
+                      void* scratch, cudaStream_t s) {
+    const double bc1 = 1.0 - pow((double)b1, (double)step), bc2 = 1.0 - pow((double)b2, (double)step);
+    Values h = {lr, b1, b2, eps, (float)(1.0 / bc1), (float)(1.0 / bc2), grad_scale, max_norm, nullptr,
+                host_mix(seed + (uint64_t)step * 0x9E3779B97F4A7C15ULL)};
+    int launches = 0;
+    auto as_is = [](Entry&, int) {};
+    if (max_norm > 0.f || grad_norm) {
+        float* norm = (float*)scratch;
+        float* partial = norm + 64;
+        int64_t at = 0;
+        launches += in_batches(t, n, as_is, [&](const auto& b, int blocks) {
+            constexpr int MOST = sizeof(b.e) / sizeof(Entry);
+            if (grad_dtype == GPT2_MODE_BF16) sumsq_many_kernel<MOST, bf16><<<blocks, THREADS, 0, s>>>(b, partial + at);
+            else sumsq_many_kernel<MOST, float><<<blocks, THREADS, 0, s>>>(b, partial + at);
+            at += blocks;
+        });
+        norm_many_kernel<<<1, 1024, 0, s>>>(norm, grad_norm, partial, at);
+        launches++;
+        if (max_norm > 0.f) h.norm = norm;
+    }
+    return launches + in_batches(t, n, as_is, [&](const auto& b, int blocks) {
+        constexpr int MOST = sizeof(b.e) / sizeof(Entry);
+        if (grad_dtype == GPT2_MODE_BF16) start_adamw<MOST, bf16>(b, blocks, bits, h, s);
+        else start_adamw<MOST, float>(b, blocks, bits, h, s);
+    });
+}
+
+int launch_adamw_many_states(const gpt2_adamw_tensor* t, void* const* m_values, void* const* v_values, int n,
+                             int dtype, cudaStream_t s) {
+    auto places = [&](Entry& e, int i) {
+        e.master = (float*)m_values[i];
+        e.param = (bf16*)v_values[i];
+        e.grad = nullptr;
+    };
+    return in_batches(t, n, places, [&](const auto& b, int blocks) {
+        constexpr int MOST = sizeof(b.e) / sizeof(Entry);
+        if (dtype == GPT2_MODE_BF16) states_many_kernel<MOST, bf16><<<blocks, THREADS, 0, s>>>(b);
+        else states_many_kernel<MOST, float><<<blocks, THREADS, 0, s>>>(b);
+    });
+}

@@ -68,6 +68,11 @@ template <int BN, int NB = 1> struct TileCfg {
 constexpr int EPI_NONE = 0;
 constexpr int EPI_GELU = 1;  // u = bf16(x); D = gelu'(u), D2 = gelu(u): the MLP's first linear and its GELU
 constexpr int EPI_MUL = 2;   // D = bf16(x) * aux: the input gradient through that GELU, aux = gelu'(u)
+// The linear classifier (x: logits of a piece of the vocabulary, which no one stores):
+constexpr int EPI_LSE = 3;   // nothing of x is stored: a row's maximum and sum of exponentials in each half tile
+constexpr int EPI_DZ = 4;    // D = bf16((dloss + dlse) exp(x - lse) - dloss [column = target])
+constexpr int EPI_ADD = 5;   // D (fp32) = or += x, added by the copy that stores it (one writer for each value)
+constexpr bool epi_stores(int epi) { return epi != EPI_LSE; }
 
 struct GemmArgs {
     const void* bias;    // bf16 [N] or null
@@ -89,6 +94,16 @@ struct GemmArgs {
     const float* b_scale;  // multiplied back (the product scales the accumulator)
     int a_fmt, b_fmt;      // FP8 operands: their formats (0 e4m3, 1 e5m2)
 };
+// With the linear classifier's part; the other kernels' arguments do not carry it.
+struct HeadGemmArgs : GemmArgs {
+    HeadEpi head;
+};
+template <int EPI> struct ArgsOf { typedef GemmArgs type; };
+template <> struct ArgsOf<EPI_LSE> { typedef HeadGemmArgs type; };
+template <> struct ArgsOf<EPI_DZ> { typedef HeadGemmArgs type; };
+template <> struct ArgsOf<EPI_ADD> { typedef HeadGemmArgs type; };
+__device__ __forceinline__ const HeadEpi* head_of(const HeadGemmArgs& g) { return &g.head; }
+__device__ __forceinline__ const HeadEpi* head_of(const GemmArgs&) { return nullptr; }
 
 // One unit of a CTA's work: k-blocks [kb0, kb1) of tile (mt, nt); z = partial slot.
 struct Work {
@@ -168,6 +183,70 @@ __device__ __forceinline__ uint8_t* stage_store_bf16(const float (&f)[32], Stage
     return stage;
 }
 
+// TMA store of a box that adds to what is there (fp32, in L2).
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
+                 ::"l"((uint64_t)map), "r"(x), "r"(y), "r"(z), "r"(src)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// What EPI_LSE and EPI_DZ keep of this lane's row. at: the target's column relative to
+// the tile's half (negative or past it where it lies elsewhere).
+struct RowHead {
+    float m, s;      // EPI_LSE: the running maximum and the sum of exp(z - maximum)
+    float a, d, lse; // EPI_DZ: dloss + dlse, dloss, lse in base 2
+    int at;
+};
+constexpr float LOG2E = 1.4426950408889634f;
+
+// EPI_LSE: 32 more logits of this lane's row, the first ncols of them inside the vocabulary. The
+// exponentials' reference is the maximum so far; the rounding of its product with log2 e, which all of them
+// share, is taken out of their sum again, so that the sum is as exact far from 0 as near it.
+template <bool WHOLE>
+__device__ __forceinline__ void lse_chunk(const uint32_t (&r)[32], RowHead& h, int ncols, int c0, float* target) {
+    float mx = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 32; j++) mx = fmaxf(mx, WHOLE || j < ncols ? __uint_as_float(r[j]) : -INFINITY);
+    const float m = fmaxf(h.m, mx);
+    const float ml = m * LOG2E, off = fmaf(m, LOG2E, -ml);
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+        const float e0 = ex2_approx(fmaf(__uint_as_float(r[j]), LOG2E, -ml));
+        const float e1 = ex2_approx(fmaf(__uint_as_float(r[j + 1]), LOG2E, -ml));
+        s0 += WHOLE || j < ncols ? e0 : 0.f;
+        s1 += WHOLE || j + 1 < ncols ? e1 : 0.f;
+    }
+    h.s = fmaf(h.s, ex2_approx((h.m - m) * LOG2E), (s0 + s1) * ex2_approx(-off));
+    h.m = m;
+    const int t = h.at - c0;
+    if (t >= 0 && t < 32) {  // once in a row's whole vocabulary
+        float z = 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; j++) z = j == t ? __uint_as_float(r[j]) : z;
+        *target = z;
+    }
+}
+
+// EPI_DZ: this lane's 32 logits become their gradients. A row that does not count (dloss = dlse = 0) gets
+// zeros whatever its logits are.
+template <bool WHOLE>
+__device__ __forceinline__ void dz_chunk(const uint32_t (&r)[32], const RowHead& h, int ncols, int c0,
+                                         float (&f)[32]) {
+    const bool counts = h.a != 0.f || h.d != 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; j++) {
+        const float p = h.a * ex2_approx(fmaf(__uint_as_float(r[j]), LOG2E, -h.lse));
+        f[j] = counts && (WHOLE || j < ncols) ? p : 0.f;
+    }
+    const int t = h.at - c0;
+    if (t >= 0 && t < 32) {
+#pragma unroll
+        for (int j = 0; j < 32; j++) f[j] -= j == t ? h.d : 0.f;
+    }
+}
+
 // One 32-column chunk of this warp's 32 rows: + bias, the epilogue op,
 // convert, stage, TMA store. fp32 output goes out as two 16-column halves.
 // ncols_valid = columns of the chunk inside the matrix (> 0). aux holds this
@@ -183,8 +262,20 @@ __device__ __forceinline__ void epi_chunk(const uint32_t (&r)[32], const float* 
                                           Stager<NB>& st, const CUtensorMap* mapD,
                                           const CUtensorMap* mapD2, const uint4 (&aux)[4], int x, int y, int z,
                                           int ncols_valid, int lane, float alpha = 1.f, float* csum_dst = nullptr,
-                                          int nrows = 32, __nv_bfloat162* am2 = nullptr) {
+                                          int nrows = 32, __nv_bfloat162* am2 = nullptr, RowHead* head = nullptr,
+                                          int c0 = 0, float* target = nullptr, bool add = false) {
+    if constexpr (EPI == EPI_LSE) {
+        if (ncols_valid >= 32) lse_chunk<true>(r, *head, 32, c0, target);
+        else lse_chunk<false>(r, *head, ncols_valid, c0, target);
+        return;
+    }
     float f[32];
+    if constexpr (EPI == EPI_DZ) {
+        if (ncols_valid >= 32) dz_chunk<true>(r, *head, 32, c0, f);
+        else dz_chunk<false>(r, *head, ncols_valid, c0, f);
+        stage_store_bf16(f, st, mapD, x, y, z, lane);
+        return;
+    }
     if (!F8 && bias_s) {
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {  // + bias, in pairs
@@ -246,9 +337,37 @@ __device__ __forceinline__ void epi_chunk(const uint32_t (&r)[32], const float* 
                                    __float_as_uint(f[hh * 16 + q * 4 + 2]), __float_as_uint(f[hh * 16 + q * 4 + 3])));
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) tma_store_3d(mapD, st.addr(), x + hh * 16, y, z);
+            if (lane == 0) {
+                if (EPI == EPI_ADD && add) tma_add_3d(mapD, st.addr(), x + hh * 16, y, z);
+                else tma_store_3d(mapD, st.addr(), x + hh * 16, y, z);
+            }
             st.advance();
         }
+    }
+}
+
+// EPI_LSE, EPI_DZ: a row's values for a tile half that begins at vocabulary column v0.
+template <int EPI> __device__ __forceinline__ void head_begin(const HeadEpi* e, int row, int M, int v0, RowHead& h) {
+    if constexpr (EPI == EPI_LSE || EPI == EPI_DZ) {
+        h.m = -INFINITY;
+        h.s = h.a = h.d = h.lse = 0.f;
+        h.at = -1;
+        if (row < M) {
+            int t = e->targets[row];
+            if (t < 0 || t >= e->vocab) t = 0;
+            h.at = t - (v0 + e->first);
+            if (EPI == EPI_DZ) {
+                h.d = e->dloss ? e->dloss[row] : 0.f;
+                h.a = h.d + (e->dlse ? e->dlse[row] : 0.f);
+                h.lse = e->lse[row] * LOG2E;
+            }
+        }
+    }
+}
+template <int EPI>
+__device__ __forceinline__ void head_end(const HeadEpi* e, int row, int M, int slot, bool any, const RowHead& h) {
+    if constexpr (EPI == EPI_LSE) {
+        if (row < M) e->stats[(int64_t)slot * M + row] = any ? make_float2(h.m, h.s) : make_float2(-INFINITY, 0.f);
     }
 }
 
@@ -268,10 +387,10 @@ template <int BN, bool A_MN, bool B_MN, int EPI, bool F8 = false>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmD2,
-                   const GemmArgs g) {
+                   const typename ArgsOf<EPI>::type g) {
     static_assert(!F8 || (!A_MN && !B_MN), "FP8 operands: K-major");
     constexpr int KE = F8 ? 128 : BK;  // values of a k-block (128 bytes of each row either way)
-    constexpr int NB = EPI != EPI_NONE ? 2 : 1;  // output staging buffers per epilogue warp
+    constexpr int NB = EPI == EPI_GELU || EPI == EPI_MUL ? 2 : 1;  // output staging buffers per epilogue warp
     using Cfg = TileCfg<BN, NB>;
     constexpr int S = Cfg::STAGES;
     extern __shared__ uint8_t smem_raw[];
@@ -436,6 +555,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint8_t* stage = out_stage + ew * NB * Cfg::OUT_STAGE_BYTES;
         Stager<NB> stg{stage, smem_addr(stage), 0};
         const bool use_bias = g.bias != nullptr && !g.partials;
+        const HeadEpi* he = head_of(g);
         const float alpha = F8 ? *g.a_scale * *g.b_scale : 1.f;
         // EPI_MUL column sums: each warp writes the sums of its 32 rows of a
         // tile, row 4 * mt + quad of g.colsum
@@ -491,11 +611,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const int z = split ? w.z : 0;
             const int ys = split ? quad * 32 : y;
             auto xcol = [&](int c) { return (split ? 0 : n0) + (cfirst + c) * 32; };
-            auto ncols = [&](int c) { return g.N - (n0 + (cfirst + c) * 32); };
+            auto ncols = [&](int c) { return (EPI == EPI_DZ ? he->vocab - he->first : g.N) - (n0 + (cfirst + c) * 32); };
             auto bias_at = [&](int c) -> const float* { return use_bias ? bias_s + c * 32 : nullptr; };
             float* csum_row = want_csum ? g.colsum + (int64_t)(w.mt * 4 + quad) * g.N + n0 + cfirst * 32 : nullptr;
             auto csum_at = [&](int c) -> float* { return want_csum ? csum_row + c * 32 : nullptr; };
             const int nrows = max(0, min(32, g.M - y));  // this warp's rows inside the matrix
+            RowHead head;
+            head_begin<EPI>(he, m0 + row_in_tile, g.M, n0 + cfirst * 32, head);
+            float* target = EPI == EPI_LSE ? he->target_logit + m0 + row_in_tile : nullptr;
             uint32_t ra[32], rb[32];
             if (nchunks > 0) {
                 tc_ld32_issue(tbase + (uint32_t)(cfirst * 32), ra);
@@ -507,7 +630,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 if (more) tc_ld32_issue(tbase + (uint32_t)((cfirst + c + 1) * 32), rb);
                 epi_chunk<EPI, F8>(ra, bias_at(c), fp32_out, stg, &tmD, &tmD2, aux[0], xcol(c), ys, z,
                                    ncols(c), lane, alpha, csum_at(c), nrows,
-                                   want_amax && m0 + row_in_tile < g.M ? &am2 : nullptr);
+                                   want_amax && m0 + row_in_tile < g.M ? &am2 : nullptr, &head, c * 32, target,
+                                   EPI == EPI_ADD && he->add);
                 if (EPI == EPI_MUL && c + 2 < CHUNKS) load_aux(c + 2, aux[0]);
                 __syncwarp();  // reconverge before the warp-collective TMEM ops
                 if (!more) break;
@@ -516,7 +640,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 if (more2) tc_ld32_issue(tbase + (uint32_t)((cfirst + c + 2) * 32), ra);
                 epi_chunk<EPI, F8>(rb, bias_at(c + 1), fp32_out, stg, &tmD, &tmD2, aux[1], xcol(c + 1),
                                    ys, z, ncols(c + 1), lane, alpha, csum_at(c + 1), nrows,
-                                   want_amax && m0 + row_in_tile < g.M ? &am2 : nullptr);
+                                   want_amax && m0 + row_in_tile < g.M ? &am2 : nullptr, &head, c * 32 + 32, target,
+                                   EPI == EPI_ADD && he->add);
                 if (EPI == EPI_MUL && c + 3 < CHUNKS) load_aux(c + 3, aux[1]);
                 __syncwarp();
                 if (more2) tc_ld_wait(ra);
@@ -524,6 +649,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(tempty_bar(acc));
+            head_end<EPI>(he, m0 + row_in_tile, g.M, 2 * w.nt + half, nchunks > 0, head);
             if (want_csum) {  // rows outside the matrix: zero sums for the columns inside it
                 for (int c = nchunks; c < CHUNKS; c++)
                     if (n0 + (cfirst + c) * 32 + lane < g.N) csum_row[c * 32 + lane] = 0.f;
@@ -680,7 +806,7 @@ template <bool A_MN, bool B_MN, int EPI, int PN>
 __global__ void __launch_bounds__(P_THREADS, 1)
     gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmD2,
-                     const GemmArgs g) {
+                     const typename ArgsOf<EPI>::type g) {
     static_assert(PN == 256 || PN == 192, "pair tile width");
     // 192-wide tiles with MN-major B: a CTA's 96 columns of B as three 32-column
     // atoms of the 64-byte swizzle (the 128-byte swizzle's atoms are 64 columns)
@@ -863,6 +989,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         uint8_t* stage = out_stage + ew * P_NBUF * 2048;
         Stager<P_NBUF> stg{stage, smem_addr(stage), 0};
         const bool use_bias = g.bias != nullptr && !g.partials;
+        const HeadEpi* he = head_of(g);
         const bool want_csum = EPI == EPI_MUL && g.colsum != nullptr;
         int acc = 0;
         uint32_t acc_phase = 0;
@@ -907,13 +1034,16 @@ __global__ void __launch_bounds__(P_THREADS, 1)
             const int z = split ? w.z : 0;
             const int ys = split ? (int)rank * 128 + quad * 32 : y;
             auto xcol = [&](int c) { return (split ? 0 : n0) + (cfirst + c) * 32; };
-            auto ncols = [&](int c) { return g.N - (n0 + (cfirst + c) * 32); };
+            auto ncols = [&](int c) { return (EPI == EPI_DZ ? he->vocab - he->first : g.N) - (n0 + (cfirst + c) * 32); };
             auto bias_at = [&](int c) -> const float* { return use_bias ? bias_s + c * 32 : nullptr; };
             // EPI_MUL column sums of this warp's 32 rows: row 4 * (128-row tile) + quad
             float* csum_row =
                 want_csum ? g.colsum + (int64_t)((2 * w.mt + (int)rank) * 4 + quad) * g.N + n0 + cfirst * 32 : nullptr;
             auto csum_at = [&](int c) -> float* { return want_csum ? csum_row + c * 32 : nullptr; };
             const int nrows = max(0, min(32, g.M - y));  // this warp's rows inside the matrix
+            RowHead head;
+            head_begin<EPI>(he, m0 + row_in_tile, g.M, n0 + cfirst * 32, head);
+            float* target = EPI == EPI_LSE ? he->target_logit + m0 + row_in_tile : nullptr;
             uint32_t ra[32], rb[32];
             if (nchunks > 0) {
                 tc_ld32_issue(tbase + (uint32_t)(cfirst * 32), ra);
@@ -923,7 +1053,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                 const bool more = c + 1 < nchunks;
                 if (more) tc_ld32_issue(tbase + (uint32_t)((cfirst + c + 1) * 32), rb);
                 epi_chunk<EPI>(ra, bias_at(c), fp32_out, stg, &tmD, &tmD2, aux[0], xcol(c), ys, z,
-                               ncols(c), lane, 1.f, csum_at(c), nrows);
+                               ncols(c), lane, 1.f, csum_at(c), nrows, nullptr, &head, c * 32, target,
+                                   EPI == EPI_ADD && he->add);
                 if (EPI == EPI_MUL && c + 2 < CHUNKS) load_aux(c + 2, aux[0]);
                 __syncwarp();
                 if (!more) break;
@@ -931,7 +1062,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                 const bool more2 = c + 2 < nchunks;
                 if (more2) tc_ld32_issue(tbase + (uint32_t)((cfirst + c + 2) * 32), ra);
                 epi_chunk<EPI>(rb, bias_at(c + 1), fp32_out, stg, &tmD, &tmD2, aux[1], xcol(c + 1), ys,
-                               z, ncols(c + 1), lane, 1.f, csum_at(c + 1), nrows);
+                               z, ncols(c + 1), lane, 1.f, csum_at(c + 1), nrows, nullptr, &head, c * 32 + 32,
+                               target, EPI == EPI_ADD && he->add);
                 if (EPI == EPI_MUL && c + 3 < CHUNKS) load_aux(c + 3, aux[1]);
                 __syncwarp();
                 if (more2) tc_ld_wait(ra);
@@ -942,6 +1074,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                 if (rank == 0) mbar_arrive(tempty_bar(acc));
                 else mbar_arrive_cta(tempty_bar(acc), 0);
             }
+            head_end<EPI>(he, m0 + row_in_tile, g.M, 2 * w.nt + half, nchunks > 0, head);
             if (want_csum && m0 + (int)rank * 128 < g.M) {
                 // rows outside the matrix in a 128-row tile that has rows inside it (the
                 // partials hold 4 rows per such tile): zero sums for the columns inside it
@@ -1119,14 +1252,17 @@ Plan make_plan(int M, int N, int K, int d_fp32) {
     return p;
 }
 
+template <int EPI> const typename ArgsOf<EPI>::type& args_of(const HeadGemmArgs& a) { return a; }
+
 template <int BN, bool A_MN, bool B_MN, int EPI, bool F8 = false>
 void launch_tc(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& md, const CUtensorMap& md2,
-               const GemmArgs& args, int grid, cudaStream_t s) {
-    using Cfg = TileCfg<BN, EPI != EPI_NONE ? 2 : 1>;
+               const HeadGemmArgs& args, int grid, cudaStream_t s) {
+    using Cfg = TileCfg<BN, EPI == EPI_GELU || EPI == EPI_MUL ? 2 : 1>;
     constexpr int smem = Cfg::SMEM_BYTES;
     static_assert(smem <= 232448, "shared memory per CTA");
     smem_attr((const void*)gemm_tc_kernel<BN, A_MN, B_MN, EPI, F8>, smem);
-    gemm_tc_kernel<BN, A_MN, B_MN, EPI, F8><<<grid, NUM_THREADS, smem, s>>>(ma, mb, md, md2, args);
+    gemm_tc_kernel<BN, A_MN, B_MN, EPI, F8><<<grid, NUM_THREADS, smem, s>>>(ma, mb, md, md2,
+                                                                                        args_of<EPI>(args));
 }
 
 // The operand layouts, and the fused epilogues only where the step uses them:
@@ -1134,13 +1270,20 @@ void launch_tc(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& 
 // gradient (B MN-major).
 template <int BN>
 bool launch_tc_layout(int epi, int a_mn, int b_mn, const CUtensorMap& ma, const CUtensorMap& mb,
-                      const CUtensorMap& md, const CUtensorMap& md2, const GemmArgs& args, int grid, cudaStream_t s) {
+                      const CUtensorMap& md, const CUtensorMap& md2, const HeadGemmArgs& args, int grid, cudaStream_t s) {
     if (epi == EPI_GELU) {
         if (a_mn || b_mn) return false;
         launch_tc<BN, false, false, EPI_GELU>(ma, mb, md, md2, args, grid, s);
     } else if (epi == EPI_MUL) {
         if (a_mn || !b_mn) return false;
         launch_tc<BN, false, true, EPI_MUL>(ma, mb, md, md2, args, grid, s);
+    } else if (epi == EPI_LSE || epi == EPI_DZ) {
+        if (a_mn || b_mn) return false;
+        if (epi == EPI_LSE) launch_tc<BN, false, false, EPI_LSE>(ma, mb, md, md2, args, grid, s);
+        else launch_tc<BN, false, false, EPI_DZ>(ma, mb, md, md2, args, grid, s);
+    } else if (epi == EPI_ADD) {
+        if (a_mn || !b_mn) return false;
+        launch_tc<BN, false, true, EPI_ADD>(ma, mb, md, md2, args, grid, s);
     } else if (!a_mn && !b_mn) {
         launch_tc<BN, false, false, EPI_NONE>(ma, mb, md, md2, args, grid, s);
     } else if (!a_mn && b_mn) {
@@ -1156,7 +1299,7 @@ bool launch_tc_layout(int epi, int a_mn, int b_mn, const CUtensorMap& ma, const 
 // FP8 operands (K-major): the plain, GELU-forward and GELU-backward epilogues.
 template <int BN>
 bool launch_tc_layout_f8(int epi, const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& md,
-                         const CUtensorMap& md2, const GemmArgs& args, int grid, cudaStream_t s) {
+                         const CUtensorMap& md2, const HeadGemmArgs& args, int grid, cudaStream_t s) {
     if (epi == EPI_GELU) launch_tc<BN, false, false, EPI_GELU, true>(ma, mb, md, md2, args, grid, s);
     else if (epi == EPI_MUL) launch_tc<BN, false, false, EPI_MUL, true>(ma, mb, md, md2, args, grid, s);
     else launch_tc<BN, false, false, EPI_NONE, true>(ma, mb, md, md2, args, grid, s);
@@ -1167,7 +1310,7 @@ bool launch_tc_layout_f8(int epi, const CUtensorMap& ma, const CUtensorMap& mb, 
 // launched in clusters of two.
 template <bool A_MN, bool B_MN, int EPI, int PN = 256>
 cudaError_t launch_pair(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& md, const CUtensorMap& md2,
-                        const GemmArgs& args, int pairs, cudaStream_t s) {
+                        const HeadGemmArgs& args, int pairs, cudaStream_t s) {
     constexpr int smem = PairCfg<PN>::SMEM_BYTES;
     static_assert(smem <= 232448, "shared memory per CTA");
     smem_attr((const void*)gemm_pair_kernel<A_MN, B_MN, EPI, PN>, smem);
@@ -1183,7 +1326,7 @@ cudaError_t launch_pair(const CUtensorMap& ma, const CUtensorMap& mb, const CUte
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gemm_pair_kernel<A_MN, B_MN, EPI, PN>, ma, mb, md, md2, args);
+    return cudaLaunchKernelEx(&cfg, gemm_pair_kernel<A_MN, B_MN, EPI, PN>, ma, mb, md, md2, args_of<EPI>(args));
 }
 
 // Clusters of two CTA-pair kernel CTAs that can be resident at once on the
@@ -1232,9 +1375,10 @@ bool g_pair_mn192 = true;  // 192-wide tiles also with MN-major B
 int g_pair_override = 0;  // > 0: the number of clusters to launch instead of the resident count
 // The pair tile width for this product, or 0 for the one-CTA kernel.
 int use_pair(int M, int N, int K, bool partials, int epi, int b_mn) {
-    if (!g_use_pair || (epi != EPI_NONE && !g_pair_epi) || partials || M < 512) return 0;
+    const bool plain = epi == EPI_NONE || epi == EPI_LSE || epi == EPI_DZ || epi == EPI_ADD;
+    if (!g_use_pair || (!plain && !g_pair_epi) || partials || M < 512) return 0;
     if (N >= 1024) return 256;
-    return epi == EPI_NONE && (!b_mn || g_pair_mn192) && N >= 384 && N % 192 == 0 && K >= 2048 && K <= 16384
+    return (epi == EPI_NONE || epi == EPI_ADD) && (!b_mn || g_pair_mn192) && N >= 384 && N % 192 == 0 && K >= 2048 && K <= 16384
                ? 192
                : 0;
 }
@@ -1272,7 +1416,10 @@ namespace {
 // D (and D2) = the epilogue op of A B^T (+ bias); see launch_matmul_tc.
 int matmul_tc(int epi, void* D, void* D2, const bf16* aux, int d_fp32, const void* A, int a_mn, const void* B,
               int b_mn, const void* bias, int M, int N, int K, void* scratch, int* status, cudaStream_t s,
-              int accumulate = 0, float* colsum = nullptr, const F8Args* f8 = nullptr, unsigned* amax = nullptr) {
+              int accumulate = 0, float* colsum = nullptr, const F8Args* f8 = nullptr, unsigned* amax = nullptr,
+              const HeadEpi* head = nullptr, int b_rows = 0) {
+    // (b_rows: the rows of B that are read, where they are fewer than N or, MN-major, K; the rest count as 0)
+    const uint64_t rows_of_b = b_rows ? b_rows : b_mn ? K : N;
     if (f8 && (a_mn || b_mn || K % 16 || N % 8)) return GPT2_ERR_ARG;
     Plan p = make_plan(M, N, f8 ? (K + 1) / 2 : K, epi == EPI_NONE ? d_fp32 : 0);
     // partial tiles for the reduce kernel: split-K, or an fp32 result added to D
@@ -1284,16 +1431,18 @@ int matmul_tc(int epi, void* D, void* D2, const bf16* aux, int d_fp32, const voi
         const int m_tiles = (M + PBM - 1) / PBM, n_tiles = (N + pn - 1) / pn;
         CUtensorMap ma, mb, md, md2;
         bool ok = a_mn ? make_map(&ma, A, (uint64_t)M, (uint64_t)K, 64) : make_map(&ma, A, (uint64_t)K, (uint64_t)M, 128);
-        ok = ok && (b_mn ? (pn == 192 ? make_map_sw64(&mb, B, (uint64_t)N, (uint64_t)K)
-                                      : make_map(&mb, B, (uint64_t)N, (uint64_t)K, 64))
-                         : make_map(&mb, B, (uint64_t)K, (uint64_t)N, (uint32_t)(pn / 2)));
-        ok = ok && make_out_map(&md, D, d_fp32 != 0, (uint64_t)N, (uint64_t)M, 1);
+        ok = ok && (b_mn ? (pn == 192 ? make_map_sw64(&mb, B, (uint64_t)N, rows_of_b)
+                                      : make_map(&mb, B, (uint64_t)N, rows_of_b, 64))
+                         : make_map(&mb, B, (uint64_t)K, rows_of_b, (uint32_t)(pn / 2)));
+        if (epi_stores(epi)) ok = ok && make_out_map(&md, D, d_fp32 != 0, (uint64_t)N, (uint64_t)M, 1);
+        else md = ma;
         if (epi == EPI_GELU) ok = ok && make_out_map(&md2, D2, false, (uint64_t)N, (uint64_t)M, 1);
         else md2 = md;
         if (!ok) return GPT2_ERR_CUDA;
-        GemmArgs g = {};
+        HeadGemmArgs g = {};
         g.a_scale = g.b_scale = nullptr;
         g.a_fmt = g.b_fmt = 0;
+        if (head) g.head = *head;
         g.bias = bias;
         g.aux = aux;
         g.colsum = colsum;
@@ -1314,7 +1463,10 @@ int matmul_tc(int epi, void* D, void* D2, const bf16* aux, int d_fp32, const voi
         const int resident = g_pair_override ? g_pair_override : pair_clusters();
         const int pairs = g.units < resident ? g.units : resident;
         cudaError_t e;
-        if (pn == 192) {
+        if (pn == 192 && epi == EPI_ADD) {
+            if (a_mn || !b_mn) return GPT2_ERR_ARG;
+            e = launch_pair<false, true, EPI_ADD, 192>(ma, mb, md, md2, g, pairs, s);
+        } else if (pn == 192) {
             if (epi != EPI_NONE) return GPT2_ERR_ARG;
             if (!b_mn)
                 e = a_mn ? launch_pair<true, false, EPI_NONE, 192>(ma, mb, md, md2, g, pairs, s)
@@ -1328,6 +1480,13 @@ int matmul_tc(int epi, void* D, void* D2, const bf16* aux, int d_fp32, const voi
         } else if (epi == EPI_MUL) {
             if (a_mn || !b_mn) return GPT2_ERR_ARG;
             e = launch_pair<false, true, EPI_MUL>(ma, mb, md, md2, g, pairs, s);
+        } else if (epi == EPI_LSE || epi == EPI_DZ) {
+            if (a_mn || b_mn) return GPT2_ERR_ARG;
+            e = epi == EPI_LSE ? launch_pair<false, false, EPI_LSE>(ma, mb, md, md2, g, pairs, s)
+                               : launch_pair<false, false, EPI_DZ>(ma, mb, md, md2, g, pairs, s);
+        } else if (epi == EPI_ADD) {
+            if (a_mn || !b_mn) return GPT2_ERR_ARG;
+            e = launch_pair<false, true, EPI_ADD>(ma, mb, md, md2, g, pairs, s);
         } else if (!a_mn && !b_mn) {
             e = launch_pair<false, false, EPI_NONE>(ma, mb, md, md2, g, pairs, s);
         } else if (!a_mn && b_mn) {
@@ -1345,18 +1504,20 @@ int matmul_tc(int epi, void* D, void* D2, const bf16* aux, int d_fp32, const voi
         ok = make_map_u8(&ma, A, (uint64_t)K, (uint64_t)M, BM) && make_map_u8(&mb, B, (uint64_t)K, (uint64_t)N, p.bn);
     } else {
         ok = a_mn ? make_map(&ma, A, (uint64_t)M, (uint64_t)K, 64) : make_map(&ma, A, (uint64_t)K, (uint64_t)M, BM);
-        ok = ok && (b_mn ? make_map(&mb, B, (uint64_t)N, (uint64_t)K, 64)
-                         : make_map(&mb, B, (uint64_t)K, (uint64_t)N, (uint32_t)p.bn));
+        ok = ok && (b_mn ? make_map(&mb, B, (uint64_t)N, rows_of_b, 64)
+                         : make_map(&mb, B, (uint64_t)K, rows_of_b, (uint32_t)p.bn));
     }
     CUtensorMap md, md2;
     if (partials) ok = ok && make_out_map(&md, scratch, true, (uint64_t)p.bn, BM, (uint64_t)p.units);
-    else ok = ok && make_out_map(&md, D, d_fp32 != 0, (uint64_t)N, (uint64_t)M, 1);
+    else if (epi_stores(epi)) ok = ok && make_out_map(&md, D, d_fp32 != 0, (uint64_t)N, (uint64_t)M, 1);
+    else md = ma;
     if (epi == EPI_GELU) ok = ok && make_out_map(&md2, D2, false, (uint64_t)N, (uint64_t)M, 1);
     else md2 = md;
     if (!ok) return GPT2_ERR_CUDA;
-    GemmArgs g = {};
+    HeadGemmArgs g = {};
     g.a_scale = g.b_scale = nullptr;
     g.a_fmt = g.b_fmt = 0;
+    if (head) g.head = *head;
     g.bias = partials ? nullptr : bias;
     g.aux = aux;
     g.colsum = epi == EPI_MUL ? colsum : nullptr;
@@ -1449,4 +1610,39 @@ int launch_matmul_gelu_backward(void* du, const void* dY, const void* W, const v
     if (M == 0 || N == 0) return 0;
     return matmul_tc(EPI_MUL, du, nullptr, (const bf16*)dgelu, 0, dY, 0, W, 1, nullptr, M, N, K, nullptr, status,
                      s, 0, du_colsum, nullptr, amax);
+}
+
+// ---------------------------------------------------------------- the linear classifier's products
+
+// The slots of HeadEpi::stats that launch_head_lse writes for these sizes: two for each column tile.
+int head_lse_slots(int M, int N, int K) {
+    const int pn = use_pair(M, N, K, false, EPI_LSE, 0);
+    return 2 * (pn ? (N + pn - 1) / pn : make_plan(M, N, K, 0).n_tiles);
+}
+
+int launch_head_lse(const void* x, const void* w, int M, int N, int K, const HeadEpi& e, int* status, cudaStream_t s) {
+    return matmul_tc(EPI_LSE, nullptr, nullptr, nullptr, 0, x, 0, w, 0, nullptr, M, N, K, nullptr, status, s, 0, nullptr,
+                     nullptr, nullptr, &e);
+}
+
+int launch_head_dz(void* dz, const void* x, const void* w, int M, int N, int K, int rows, const HeadEpi& e, int* status,
+                   cudaStream_t s) {
+    return matmul_tc(EPI_DZ, dz, nullptr, nullptr, 0, x, 0, w, 0, nullptr, M, N, K, nullptr, status, s, 0, nullptr,
+                     nullptr, nullptr, &e, rows);
+}
+
+// Whether an M x N product has tiles enough to be added whole, without a split of K.
+static bool head_dx_whole(int M, int N) {
+    return (int64_t)((M + BM - 1) / BM) * ((N + 255) / 256) * 2 >= gpt2_num_sms();
+}
+
+size_t head_dx_scratch(int M, int N, int K) { return head_dx_whole(M, N) ? 0 : matmul_tc_scratch(M, N, K, 1, 1); }
+
+int launch_head_dx(float* dx, const void* dz, const void* w, int M, int N, int K, int rows, bool add, void* scratch,
+                   int* status, cudaStream_t s) {
+    const bool whole = head_dx_whole(M, N);
+    HeadEpi e = {};
+    e.add = add;
+    return matmul_tc(whole ? EPI_ADD : EPI_NONE, dx, nullptr, nullptr, 1, dz, 0, w, 1, nullptr, M, N, K, scratch, status, s,
+                     add && !whole, nullptr, nullptr, nullptr, &e, rows);
 }

@@ -9,6 +9,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/gpt2_ops.h"
+
 int launch_encoder_forward(int dtype, void* x0, const int32_t* tokens, const void* wte, const void* wpe, int B,
                            int T, int C, int V, int* status, cudaStream_t s);
 size_t encoder_backward_scratch(int B, int T, int C);
@@ -151,6 +153,63 @@ int launch_token_logprobs(int dtype, float* logp, float* lse, float* entropy, fl
 int launch_token_logprobs_backward(int dtype, void* dlogits, const void* logits, const int32_t* targets,
                                    const float* lse, const float* entropy, const float* dlogp, const float* dlse,
                                    const float* dentropy, int N, int V, int Vp, int* status, cudaStream_t s);
+
+// Norms of queries and keys for each head with the position rotation (gpt2_op_qk_norm_rotary_*):
+// validated arguments. Forward: q, k -> qo, ko. Backward: dqo, dko (and q, k with norm) -> qo, ko, which
+// are dq and dk there.
+struct RotaryArgs {
+    const void *q, *k, *dqo, *dko;
+    void *qo, *ko;
+    int64_t q_stride, k_stride, dqo_stride, dko_stride, qo_stride, ko_stride;  // elements between rows
+    const void *q_gamma, *k_gamma;                                           // [hd] or null: ones
+    const int32_t* pos;                                                      // [N]
+    const uint64_t* turns;                                                   // [rot / 2]
+    float eps, amplitude;
+    int N, Hq, Hk, hd, rot, interleaved, norm;
+};
+size_t rotary_backward_scratch(int N, int hd);
+int launch_rotary(int dtype, const RotaryArgs& a, bool back, float* dq_gamma, float* dk_gamma, void* scratch,
+                  cudaStream_t s);
+
+// The linear classifier's part in the epilogue of a matmul (gemm_tc.cu): the columns of the product are the
+// vocabulary's from `first` on.
+struct HeadEpi {
+    const int32_t* targets;      // [M]; outside [0, vocab): 0
+    const float *lse, *dloss, *dlse;  // gradients: [M] (dloss, dlse or null: 0)
+    float2* stats;               // forward: [slots][M] maximum and sum of exp(z - maximum)
+    float* target_logit;         // forward: [M]
+    int vocab, first;
+    int add;                     // launch_head_dx's own
+};
+// Forward: the row statistics of the M x N logits x W^T in head_lse_slots() slots and the targets' logits.
+int head_lse_slots(int M, int N, int K);
+int launch_head_lse(const void* x, const void* w, int M, int N, int K, const HeadEpi& e, int* status, cudaStream_t s);
+// dz [M, N] (bf16) of a piece of the vocabulary; rows: those of w that are read (the columns from there on get 0).
+int launch_head_dz(void* dz, const void* x, const void* w, int M, int N, int K, int rows, const HeadEpi& e, int* status,
+                   cudaStream_t s);
+// dx [M, N] (fp32) = or += dz [M, K] W [K, N], of which `rows` rows are read.
+size_t head_dx_scratch(int M, int N, int K);
+int launch_head_dx(float* dx, const void* dz, const void* w, int M, int N, int K, int rows, bool add, void* scratch,
+                   int* status, cudaStream_t s);
+
+// Softmax cross entropy of x W^T without the logits (gpt2_op_linear_classifier_*): validated arguments.
+size_t linear_classifier_forward_scratch(int dtype, int N, int C, int V);
+int launch_linear_classifier_forward(int dtype, float* losses, float* lse, const void* x, const void* w,
+                                     const int32_t* targets, int N, int C, int V, void* scratch, int* status,
+                                     cudaStream_t s);
+size_t linear_classifier_backward_scratch(int dtype, int N, int C, int V, int dw_fp32, int accumulate);
+int launch_linear_classifier_backward(int dtype, void* dx, void* dw, int dw_fp32, int accumulate, const void* x,
+                                      const void* w, const int32_t* targets, const float* lse, const float* dloss,
+                                      const float* dlse, int N, int C, int V, int Vp, void* scratch, int* status,
+                                      cudaStream_t s);
+
+// AdamW over many tensors (gpt2_op_adamw_many): validated arguments.
+size_t adamw_many_scratch(const gpt2_adamw_tensor* t, int n);
+int launch_adamw_many(const gpt2_adamw_tensor* t, int n, int grad_dtype, int bits, float lr, float b1, float b2,
+                      float eps, float grad_scale, float max_norm, float* grad_norm, int step, uint64_t seed,
+                      void* scratch, cudaStream_t s);
+int launch_adamw_many_states(const gpt2_adamw_tensor* t, void* const* m_values, void* const* v_values, int n,
+                             int dtype, cudaStream_t s);
 
 // bf16 linear forward with the GELU fused into its epilogue: u = A W^T + bias
 // (A [M,K], W [N,K], both K-major) rounded to bf16, out = gelu(u), dgelu =

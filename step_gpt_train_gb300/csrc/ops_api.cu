@@ -2,6 +2,9 @@
 #include "common.cuh"
 #include "launch.h"
 
+#include <cmath>
+#include <initializer_list>
+
 namespace {
 
 inline bool dt_ok(int dtype) { return dtype == GPT2_MODE_FP32 || dtype == GPT2_MODE_BF16; }
@@ -400,6 +403,200 @@ int gpt2_op_adamw(float* master, void* param_bf16, const float* grad, float* m, 
         return GPT2_ERR_ARG;
     return finish(launch_adamw(master, param_bf16, grad, m, v, n, lr, beta1, beta2, eps, weight_decay, t,
                                st(stream)));
+}
+
+static bool rotary_ok(int dtype, int N, int Hq, int Hk, int hd, int rot, int norm, float eps, float amplitude) {
+    if (!dt_ok(dtype) || N < 0 || Hq < 0 || Hk < 0 || Hq + (int64_t)Hk < 1 || Hq + (int64_t)Hk > (1 << 20)) return false;
+    if (hd != 8 && hd != 16 && hd != 32 && hd != 64 && hd != 128) return false;
+    return rot >= 0 && rot <= hd && rot % 8 == 0 && (!norm || (eps > 0.f && std::isfinite(eps))) &&
+           std::isfinite(amplitude);
+}
+
+int gpt2_op_qk_norm_rotary_forward(int dtype, void* qo, int64_t qo_stride, void* ko, int64_t ko_stride, const void* q,
+                                   int64_t q_stride, const void* k, int64_t k_stride, const void* q_gamma,
+                                   const void* k_gamma, const int32_t* pos, const uint64_t* turns, int N, int Hq,
+                                   int Hk, int hd, int rot, int interleaved, int norm, float eps, float amplitude,
+                                   void* stream) {
+    if (!rotary_ok(dtype, N, Hq, Hk, hd, rot, norm, eps, amplitude)) return GPT2_ERR_ARG;
+    if (N == 0) return GPT2_OK;
+    if (rot && (!pos || !turns)) return GPT2_ERR_ARG;
+    if (Hq && (!qo || !q || !rows_ok(qo, qo_stride, Hq, hd, dtype) || !rows_ok(q, q_stride, Hq, hd, dtype)))
+        return GPT2_ERR_ARG;
+    if (Hk && (!ko || !k || !rows_ok(ko, ko_stride, Hk, hd, dtype) || !rows_ok(k, k_stride, Hk, hd, dtype)))
+        return GPT2_ERR_ARG;
+    if (!al16(q_gamma) || !al16(k_gamma)) return GPT2_ERR_ARG;
+    RotaryArgs a = {};
+    a.q = q, a.k = k, a.qo = qo, a.ko = ko;
+    a.q_stride = q_stride, a.k_stride = k_stride, a.qo_stride = qo_stride, a.ko_stride = ko_stride;
+    a.q_gamma = q_gamma, a.k_gamma = k_gamma, a.pos = pos, a.turns = turns;
+    a.eps = eps, a.amplitude = amplitude;
+    a.N = N, a.Hq = Hq, a.Hk = Hk, a.hd = hd, a.rot = rot, a.interleaved = interleaved != 0, a.norm = norm != 0;
+    return finish(launch_rotary(dtype, a, false, nullptr, nullptr, nullptr, st(stream)));
+}
+
+size_t gpt2_op_qk_norm_rotary_backward_scratch(int N, int hd) {
+    return N < 1 || hd < 1 || hd > 128 ? 0 : rotary_backward_scratch(N, hd);
+}
+
+int gpt2_op_qk_norm_rotary_backward(int dtype, void* dq, int64_t dq_stride, void* dk, int64_t dk_stride,
+                                    float* dq_gamma, float* dk_gamma, const void* dqo, int64_t dqo_stride,
+                                    const void* dko, int64_t dko_stride, const void* q, int64_t q_stride,
+                                    const void* k, int64_t k_stride, const void* q_gamma, const void* k_gamma,
+                                    const int32_t* pos, const uint64_t* turns, int N, int Hq, int Hk, int hd, int rot,
+                                    int interleaved, int norm, float eps, float amplitude, void* scratch,
+                                    size_t scratch_bytes, void* stream) {
+    if (!rotary_ok(dtype, N, Hq, Hk, hd, rot, norm, eps, amplitude)) return GPT2_ERR_ARG;
+    if (N == 0) {
+        for (float* g : {dq_gamma, dk_gamma})
+            if (norm && g && cudaMemsetAsync(g, 0, (size_t)hd * 4, st(stream)) != cudaSuccess) return GPT2_ERR_CUDA;
+        return GPT2_OK;
+    }
+    if (rot && (!pos || !turns)) return GPT2_ERR_ARG;
+    if (Hq && (!dq || !dqo || !rows_ok(dq, dq_stride, Hq, hd, dtype) || !rows_ok(dqo, dqo_stride, Hq, hd, dtype) ||
+               (norm && (!q || !rows_ok(q, q_stride, Hq, hd, dtype)))))
+        return GPT2_ERR_ARG;
+    if (Hk && (!dk || !dko || !rows_ok(dk, dk_stride, Hk, hd, dtype) || !rows_ok(dko, dko_stride, Hk, hd, dtype) ||
+               (norm && (!k || !rows_ok(k, k_stride, Hk, hd, dtype)))))
+        return GPT2_ERR_ARG;
+    if (!al16(q_gamma) || !al16(k_gamma)) return GPT2_ERR_ARG;
+    if (norm && (dq_gamma || dk_gamma) && (!scratch || scratch_bytes < rotary_backward_scratch(N, hd)))
+        return GPT2_ERR_WORKSPACE;
+    RotaryArgs a = {};
+    a.q = q, a.k = k, a.dqo = dqo, a.dko = dko, a.qo = dq, a.ko = dk;
+    a.q_stride = q_stride, a.k_stride = k_stride, a.dqo_stride = dqo_stride, a.dko_stride = dko_stride;
+    a.qo_stride = dq_stride, a.ko_stride = dk_stride;
+    a.q_gamma = q_gamma, a.k_gamma = k_gamma, a.pos = pos, a.turns = turns;
+    a.eps = eps, a.amplitude = amplitude;
+    a.N = N, a.Hq = Hq, a.Hk = Hk, a.hd = hd, a.rot = rot, a.interleaved = interleaved != 0, a.norm = norm != 0;
+    return finish(launch_rotary(dtype, a, true, dq_gamma, dk_gamma, scratch, st(stream)));
+}
+
+int gpt2_rotary_turns(uint64_t* turns, int rot, double base, int scaling, double factor, double context, double fast,
+                      double slow) {
+    if (rot < 0 || rot % 2 || (rot && !turns) || scaling < GPT2_ROTARY_PLAIN || scaling > GPT2_ROTARY_PARTS)
+        return GPT2_ERR_ARG;
+    if (!(base > 1.0) || !std::isfinite(base) || !(factor >= 1.0) || !std::isfinite(factor)) return GPT2_ERR_ARG;
+    if (scaling == GPT2_ROTARY_PARTS &&
+        (!(context >= 1.0) || !std::isfinite(context) || !(slow >= 0.0) || !(fast > slow) || !std::isfinite(fast)))
+        return GPT2_ERR_ARG;
+    if (scaling == GPT2_ROTARY_BASE && rot > 2) base *= std::pow(factor, rot / (rot - 2.0));
+    for (int j = 0; j < rot / 2; j++) {
+        double f = std::pow(base, -2.0 * j / rot) / (2.0 * 3.14159265358979323846);
+        if (scaling == GPT2_ROTARY_LINEAR) f /= factor;
+        if (scaling == GPT2_ROTARY_PARTS) {
+            const double turned = (f * context - slow) / (fast - slow), keep = std::fmin(1.0, std::fmax(0.0, turned));
+            f *= keep + (1.0 - keep) / factor;
+        }
+        turns[j] = (uint64_t)std::nearbyint(std::ldexp(f, 64));
+    }
+    return GPT2_OK;
+}
+
+static bool linear_classifier_ok(int dtype, int N, int C, int V) {
+    const int64_t most = ((int64_t)1 << 31) - 2048;
+    return dt_ok(dtype) && N >= 0 && C >= 8 && C % 8 == 0 && V >= 1 && (int64_t)N * C < most && (int64_t)V * C < most &&
+           V < (1 << 30);
+}
+
+size_t gpt2_op_linear_classifier_forward_scratch(int dtype, int N, int C, int V) {
+    return N < 1 || !linear_classifier_ok(dtype, N, C, V) ? 0 : linear_classifier_forward_scratch(dtype, N, C, V);
+}
+
+int gpt2_op_linear_classifier_forward(int dtype, float* losses, float* lse, const void* x, const void* w,
+                                      const int32_t* targets, int N, int C, int V, void* scratch,
+                                      size_t scratch_bytes, int* d_status, void* stream) {
+    if (!linear_classifier_ok(dtype, N, C, V)) return GPT2_ERR_ARG;
+    if (N == 0) return GPT2_OK;
+    if (!losses || !lse || !x || !w || !targets || !al16(x) || !al16(w)) return GPT2_ERR_ARG;
+    if (!scratch || scratch_bytes < linear_classifier_forward_scratch(dtype, N, C, V)) return GPT2_ERR_WORKSPACE;
+    return finish(launch_linear_classifier_forward(dtype, losses, lse, x, w, targets, N, C, V, scratch, d_status,
+                                                   st(stream)));
+}
+
+size_t gpt2_op_linear_classifier_backward_scratch(int dtype, int N, int C, int V, int dw_fp32, int accumulate) {
+    return N < 1 || !linear_classifier_ok(dtype, N, C, V)
+               ? 0
+               : linear_classifier_backward_scratch(dtype, N, C, V, dw_fp32 != 0, accumulate != 0);
+}
+
+int gpt2_op_linear_classifier_backward(int dtype, void* dx, void* dw, int dw_fp32, int accumulate, const void* x,
+                                       const void* w, const int32_t* targets, const float* lse, const float* dloss,
+                                       const float* dlse, int N, int C, int V, int Vp, void* scratch,
+                                       size_t scratch_bytes, int* d_status, void* stream) {
+    dw_fp32 = dw_fp32 != 0;
+    accumulate = accumulate != 0;
+    if (!linear_classifier_ok(dtype, N, C, V) || Vp < V || Vp % 8 || (int64_t)Vp * C >= ((int64_t)1 << 31) - 2048)
+        return GPT2_ERR_ARG;
+    if (!dw || !al16(dw) || (dtype == GPT2_MODE_FP32 && !dw_fp32) || (accumulate && !dw_fp32)) return GPT2_ERR_ARG;
+    if (N == 0) {
+        if (!accumulate && cudaMemsetAsync(dw, 0, (size_t)Vp * C * (dw_fp32 ? 4 : 2), st(stream)) != cudaSuccess)
+            return GPT2_ERR_CUDA;
+        return GPT2_OK;
+    }
+    if (!dx || !x || !w || !targets || !lse || !al16(dx) || !al16(x) || !al16(w)) return GPT2_ERR_ARG;
+    if (!scratch || scratch_bytes < linear_classifier_backward_scratch(dtype, N, C, V, dw_fp32, accumulate))
+        return GPT2_ERR_WORKSPACE;
+    return finish(launch_linear_classifier_backward(dtype, dx, dw, dw_fp32, accumulate, x, w, targets, lse, dloss, dlse,
+                                                    N, C, V, Vp, scratch, d_status, st(stream)));
+}
+
+// Whether the list can be walked at all; the addresses of what a call reads are checked there.
+static bool tensors_ok(const gpt2_adamw_tensor* t, int n) {
+    if (n < 0 || n > (1 << 24) || (n && !t)) return false;
+    const int64_t most = (int64_t)1 << 42;
+    int64_t total = 0;
+    for (int i = 0; i < n; i++) {
+        if (t[i].n < 0 || t[i].n >= most) return false;
+        total += t[i].n + 4096;  // whole blocks, whose numbers have 31 bits
+        if (total >= most) return false;
+    }
+    return true;
+}
+static bool al(const void* p, unsigned bytes) { return p && ((uintptr_t)p & (bytes - 1)) == 0; }
+
+size_t gpt2_op_adamw_many_scratch(const gpt2_adamw_tensor* tensors, int n_tensors) {
+    return tensors_ok(tensors, n_tensors) ? adamw_many_scratch(tensors, n_tensors) : 0;
+}
+
+int gpt2_op_adamw_many(const gpt2_adamw_tensor* tensors, int n_tensors, int grad_dtype, int bits, float lr,
+                       float beta1, float beta2, float eps, float grad_scale, float max_grad_norm, float* grad_norm,
+                       int t, uint64_t seed, void* scratch, size_t scratch_bytes, void* stream) {
+    if (!tensors_ok(tensors, n_tensors) || !dt_ok(grad_dtype) || (bits != 8 && bits != 32) || t < 1) return GPT2_ERR_ARG;
+    if (!(beta1 >= 0.f && beta1 < 1.f) || !(beta2 >= 0.f && beta2 < 1.f) || !(eps >= 0.f) || !(max_grad_norm >= 0.f))
+        return GPT2_ERR_ARG;
+    const unsigned gb = grad_dtype == GPT2_MODE_BF16 ? 2 : 4;
+    int64_t total = 0;
+    for (int i = 0; i < n_tensors; i++) {
+        const gpt2_adamw_tensor& x = tensors[i];
+        if (x.n == 0) continue;
+        total += x.n;
+        if (!al(x.master, 4) || !al(x.grad, gb) || (x.param_bf16 && !al(x.param_bf16, 2))) return GPT2_ERR_ARG;
+        if (bits == 32 ? !al(x.m, 4) || !al(x.v, 4) : !x.m || !x.v || !x.m_scale || !x.v_scale) return GPT2_ERR_ARG;
+    }
+    if (total == 0) {
+        if (grad_norm && cudaMemsetAsync(grad_norm, 0, 4, st(stream)) != cudaSuccess) return GPT2_ERR_CUDA;
+        return GPT2_OK;
+    }
+    if ((max_grad_norm > 0.f || grad_norm) && (!scratch || scratch_bytes < adamw_many_scratch(tensors, n_tensors)))
+        return GPT2_ERR_WORKSPACE;
+    return finish(launch_adamw_many(tensors, n_tensors, grad_dtype, bits, lr, beta1, beta2, eps, grad_scale,
+                                    max_grad_norm, grad_norm, t, seed, scratch, st(stream)));
+}
+
+int gpt2_op_adamw_many_states(const gpt2_adamw_tensor* tensors, void* const* m_values, void* const* v_values,
+                              int n_tensors, int dtype, void* stream) {
+    if (!tensors_ok(tensors, n_tensors) || !dt_ok(dtype) || (n_tensors && (!m_values || !v_values))) return GPT2_ERR_ARG;
+    const unsigned eb = dtype == GPT2_MODE_BF16 ? 2 : 4;
+    int64_t total = 0;
+    for (int i = 0; i < n_tensors; i++) {
+        const gpt2_adamw_tensor& x = tensors[i];
+        if (x.n == 0) continue;
+        if (!x.m || !x.v || !x.m_scale || !x.v_scale || !al(m_values[i], eb) || !al(v_values[i], eb))
+            return GPT2_ERR_ARG;
+        total += x.n;
+    }
+    if (total == 0) return GPT2_OK;
+    return finish(launch_adamw_many_states(tensors, m_values, v_values, n_tensors, dtype, st(stream)));
 }
 
 int gpt2_debug_set_wait_limit(int64_t cycles) {

@@ -25,6 +25,7 @@ STATUS_NAMES = {
 }
 
 TENSOR_PARAM, TENSOR_MASTER, TENSOR_GRAD, TENSOR_ADAM_M, TENSOR_ADAM_V = range(5)
+ROTARY_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "parts": 3}  # gpt2_rotary_turns
 FP8_E4M3, FP8_E5M2 = 0, 1  # the FP8 formats of gpt2_op_quantize_fp8 / gpt2_op_matmul_fp8
 
 FAMILIES = ["encoder_forward", "layernorm_forward", "matmul", "attention_forward", "residual_forward",
@@ -54,6 +55,11 @@ class gpt2_adamw_config(ctypes.Structure):
     _fields_ = [("lr", c_float), ("beta1", c_float), ("beta2", c_float), ("eps", c_float),
                 ("weight_decay", c_float), ("t", c_int32), ("grad_scale", c_float), ("max_grad_norm", c_float),
                 ("decay_mask", c_int32)]
+
+
+class gpt2_adamw_tensor(ctypes.Structure):
+    _fields_ = [("master", c_void_p), ("param_bf16", c_void_p), ("grad", c_void_p), ("m", c_void_p), ("v", c_void_p),
+                ("m_scale", c_void_p), ("v_scale", c_void_p), ("n", c_int64), ("weight_decay", c_float)]
 
 
 _lib = None
@@ -150,6 +156,24 @@ _SIGNATURES = {
                                        c_void_p, c_int, c_int, c_int, c_void_p, c_void_p]),
     "gpt2_op_token_logprobs_backward": (c_int, [c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                                 c_void_p, c_void_p, c_int, c_int, c_int, c_void_p, c_void_p]),
+    "gpt2_op_qk_norm_rotary_forward": (c_int, [c_int] + [c_void_p, c_int64] * 4 + [c_void_p] * 4 + [c_int] * 7
+                                       + [c_float, c_float, c_void_p]),
+    "gpt2_op_qk_norm_rotary_backward_scratch": (c_size_t, [c_int, c_int]),
+    "gpt2_op_qk_norm_rotary_backward": (c_int, [c_int] + [c_void_p, c_int64] * 2 + [c_void_p] * 2
+                                        + [c_void_p, c_int64] * 4 + [c_void_p] * 4 + [c_int] * 7
+                                        + [c_float, c_float, c_void_p, c_size_t, c_void_p]),
+    "gpt2_rotary_turns": (c_int, [c_void_p, c_int, c_double, c_int, c_double, c_double, c_double, c_double]),
+    "gpt2_op_linear_classifier_forward_scratch": (c_size_t, [c_int] * 4),
+    "gpt2_op_linear_classifier_forward": (c_int, [c_int] + [c_void_p] * 5 + [c_int] * 3
+                                          + [c_void_p, c_size_t, c_void_p, c_void_p]),
+    "gpt2_op_linear_classifier_backward_scratch": (c_size_t, [c_int] * 6),
+    "gpt2_op_linear_classifier_backward": (c_int, [c_int, c_void_p, c_void_p, c_int, c_int] + [c_void_p] * 6
+                                           + [c_int] * 4 + [c_void_p, c_size_t, c_void_p, c_void_p]),
+    "gpt2_op_adamw_many_scratch": (c_size_t, [POINTER(gpt2_adamw_tensor), c_int]),
+    "gpt2_op_adamw_many": (c_int, [POINTER(gpt2_adamw_tensor), c_int, c_int, c_int] + [c_float] * 6
+                           + [c_void_p, c_int, c_uint64, c_void_p, c_size_t, c_void_p]),
+    "gpt2_op_adamw_many_states": (c_int, [POINTER(gpt2_adamw_tensor), POINTER(c_void_p), POINTER(c_void_p), c_int,
+                                          c_int, c_void_p]),
     "gpt2_op_gelu_forward": (c_int, [c_int, c_void_p, c_void_p, c_int64, c_void_p]),
     "gpt2_op_gelu_backward": (c_int, [c_int, c_void_p, c_void_p, c_void_p, c_int64, c_void_p]),
     "gpt2_op_residual_forward": (c_int, [c_int, c_void_p, c_void_p, c_void_p, c_int64, c_void_p]),
@@ -825,6 +849,256 @@ def gpt2_op_token_logprobs_backward(dlogits, logits, targets, lse, entropy, V, d
     check(load_library().gpt2_op_token_logprobs_backward(dt, dlogits.data_ptr(), logits.data_ptr(), _p(targets),
                                                          _p(lse), _p(entropy), _p(dlogp), _p(dlse), _p(dentropy), N, V,
                                                          Vp, status, st), "gpt2_op_token_logprobs_backward")
+
+
+def gpt2_rotary_turns(rot, base=10000.0, scaling="plain", factor=1.0, context=1024, fast=32.0, slow=1.0):
+    """The turns of each pair of a rotation of `rot` values from one position to the next, in units of 2^-64 (int64 CPU
+    tensor [rot / 2]): frequencies base^(-2 j / rot), stretched by `factor` as `scaling` says ("plain", "linear",
+    "base", "parts"; see gpt2_ops.h)."""
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError(f"scaling: one of {', '.join(ROTARY_SCALINGS)} is needed")
+    turns = _tc().empty(max(int(rot), 0) // 2, dtype=_torch.int64)
+    check(load_library().gpt2_rotary_turns(turns.data_ptr(), int(rot), float(base), ROTARY_SCALINGS[scaling],
+                                           float(factor), float(context), float(fast), float(slow)),
+          "gpt2_rotary_turns")
+    return turns
+
+
+def _here(what, device, *tensors):
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise _elsewhere(what)
+
+
+def _rotary(what, q, k, pos, turns, gammas):
+    """Checks what a rotation reads beside its rows; rows, heads of q and of k, head size, rotated values."""
+    n, hq, hd = q.shape
+    m, hk, d = k.shape
+    if m != n or d != hd or k.dtype is not q.dtype:
+        raise ValueError(f"{what}: k like q in rows, type and head size is needed")
+    if pos.dtype is not _torch.int32 or pos.shape != (n,) or not pos.is_contiguous():
+        raise ValueError(f"{what}: pos: contiguous int32 of shape [rows] is needed")
+    if turns.dtype is not _torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
+        raise ValueError(f"{what}: turns: contiguous int64 of shape [rot / 2] is needed")
+    for t in gammas:
+        if t is not None and (t.dtype is not q.dtype or t.shape != (hd,) or not t.is_contiguous()):
+            raise ValueError(f"{what}: gammas: contiguous {q.dtype} of shape [hd] is needed")
+    return n, hq, hk, hd, 2 * turns.shape[0]
+
+
+def gpt2_op_qk_norm_rotary_forward(qo, ko, q, k, pos, turns, q_gamma=None, k_gamma=None, eps=None, interleaved=False,
+                                   amplitude=1.0, stream=None):
+    """qo, ko = the heads of q [rows, Hq, hd] and k [rows, Hk, hd] (each may be a column block of a wider buffer;
+    outputs may be the inputs), normed (eps not None) and rotated by pos (int32 [rows]) times turns (int64
+    [rot / 2], from gpt2_rotary_turns)."""
+    what = "gpt2_op_qk_norm_rotary_forward"
+    lib = load_library()
+    dt = _mode_of("q", q)
+    sq, sqo = _rows("q and qo", q, qo)
+    sk, sko = _rows("k and ko", k, ko)
+    sizes = _rotary(what, q, k, pos, turns, (q_gamma, k_gamma))
+    device, st = _where(stream)
+    _here(what, device, q, k, qo, ko, pos, turns, q_gamma, k_gamma)
+    check(lib.gpt2_op_qk_norm_rotary_forward(dt, qo.data_ptr(), sqo, ko.data_ptr(), sko, q.data_ptr(), sq, k.data_ptr(),
+                                             sk, _p(q_gamma), _p(k_gamma), pos.data_ptr(), turns.data_ptr(), *sizes,
+                                             bool(interleaved), eps is not None, eps or 0.0, amplitude, st), what)
+
+
+def gpt2_op_qk_norm_rotary_backward(dq, dk, dqo, dko, q, k, pos, turns, q_gamma=None, k_gamma=None, dq_gamma=None,
+                                    dk_gamma=None, eps=None, interleaved=False, amplitude=1.0, stream=None):
+    """dq, dk (may be dqo, dko) and, with a norm, dq_gamma, dk_gamma (float32 [hd]) of gpt2_op_qk_norm_rotary_forward
+    from dqo, dko and the forward's q and k."""
+    what = "gpt2_op_qk_norm_rotary_backward"
+    lib = load_library()
+    dt = _mode_of("q", q)
+    sq, sdqo, sdq = _rows("q, dqo and dq", q, dqo, dq)
+    sk, sdko, sdk = _rows("k, dko and dk", k, dko, dk)
+    n, hq, hk, hd, rot = _rotary(what, q, k, pos, turns, (q_gamma, k_gamma))
+    weights = dq_gamma is not None or dk_gamma is not None
+    if weights and eps is None:
+        raise ValueError("dq_gamma and dk_gamma come with a norm")
+    for t in (dq_gamma, dk_gamma):
+        if t is not None and (t.dtype is not _torch.float32 or t.shape != (hd,) or not t.is_contiguous()):
+            raise ValueError("dq_gamma and dk_gamma: contiguous float32 of shape [hd] is needed")
+    device, st = _where(stream)
+    _here(what, device, q, k, dq, dk, dqo, dko, pos, turns, q_gamma, k_gamma, dq_gamma, dk_gamma)
+    nb = lib.gpt2_op_qk_norm_rotary_backward_scratch(n, hd) if weights else 0
+    args = (dt, dq.data_ptr(), sdq, dk.data_ptr(), sdk, _p(dq_gamma), _p(dk_gamma), dqo.data_ptr(), sdqo,
+            dko.data_ptr(), sdko, q.data_ptr(), sq, k.data_ptr(), sk, _p(q_gamma), _p(k_gamma), pos.data_ptr(),
+            turns.data_ptr(), n, hq, hk, hd, rot, bool(interleaved), eps is not None, eps or 0.0, amplitude)
+    sc = _borrow(nb, st) if nb else None
+    try:
+        check(lib.gpt2_op_qk_norm_rotary_backward(*args, sc, nb, st), what)
+    finally:
+        if sc:
+            _give_back(sc)
+
+
+def _hidden(x, w, V):
+    """Rows, width and padded vocabulary of the linear classifier's operands."""
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1] or w.dtype is not x.dtype \
+            or not x.is_contiguous() or not w.is_contiguous():
+        raise ValueError("contiguous x [N, C] and w [Vp, C] of one type are needed")
+    if not 1 <= V <= w.shape[0]:
+        raise ValueError("V: from 1 to the rows of w")
+    return *x.shape, w.shape[0]
+
+
+def gpt2_op_linear_classifier_forward(losses, lse, x, w, targets, V, status=None, stream=None):
+    """losses, lse (float32 [N]) of the softmax cross entropy of x w[:V]^T (x [N, C], w [Vp, C]) at targets (int32
+    [N]); the logits are not kept."""
+    what = "gpt2_op_linear_classifier_forward"
+    lib = load_library()
+    dt = _mode_of("x", x)
+    N, C, _ = _hidden(x, w, V)
+    device, st = _where(stream)
+    if not _fit(device, N, (losses, lse), targets):
+        _refuse(what, device, N, (losses, lse), targets)
+    if not device == x.get_device() == w.get_device():
+        raise _elsewhere(what)
+    status = _status(what, status, device)
+    args = (dt, losses.data_ptr(), lse.data_ptr(), x.data_ptr(), w.data_ptr(), targets.data_ptr(), N, C, V)
+    nb = lib.gpt2_op_linear_classifier_forward_scratch(dt, N, C, V)
+    sc = _borrow(nb, st) if nb else None
+    try:
+        check(lib.gpt2_op_linear_classifier_forward(*args, sc, nb, status, st), what)
+    finally:
+        if sc:
+            _give_back(sc)
+
+
+def gpt2_op_linear_classifier_backward(dx, dw, x, w, targets, lse, V, dloss=None, dlse=None, accumulate=False,
+                                       status=None, stream=None):
+    """dx [N, C] and dw [Vp, C] (float32 or like w; += with accumulate) of gpt2_op_linear_classifier_forward from dloss
+    and dlse (float32 [N], None: 0), the gradients of its losses and lse."""
+    what = "gpt2_op_linear_classifier_backward"
+    lib = load_library()
+    dt = _mode_of("x", x)
+    N, C, Vp = _hidden(x, w, V)
+    if dx.shape != x.shape or dx.dtype is not x.dtype or not dx.is_contiguous():
+        raise ValueError("dx: like x")
+    if dw.shape != w.shape or dw.dtype not in (_torch.float32, w.dtype) or not dw.is_contiguous():
+        raise ValueError("dw: contiguous, like w or float32 of its shape")
+    dw32 = int(dw.dtype is _torch.float32)
+    if accumulate and not dw32:
+        raise ValueError("accumulate: dw in float32 is needed")
+    device, st = _where(stream)
+    arrays = (lse, dloss, dlse)
+    if not _fit(device, N, arrays, targets):
+        _refuse(what, device, N, arrays, targets)
+    if not device == x.get_device() == w.get_device() == dx.get_device() == dw.get_device():
+        raise _elsewhere(what)
+    status = _status(what, status, device)
+    args = (dt, dx.data_ptr(), dw.data_ptr(), dw32, bool(accumulate), x.data_ptr(), w.data_ptr(), targets.data_ptr(),
+            lse.data_ptr(), _p(dloss), _p(dlse), N, C, V, Vp)
+    nb = lib.gpt2_op_linear_classifier_backward_scratch(dt, N, C, V, dw32, bool(accumulate))
+    sc = _borrow(nb, st) if nb else None
+    try:
+        check(lib.gpt2_op_linear_classifier_backward(*args, sc, nb, status, st), what)
+    finally:
+        if sc:
+            _give_back(sc)
+
+
+class AdamWTensors:
+    """The tensors of gpt2_op_adamw_many calls, checked once; holds them while it lives. From gpt2_adamw_tensors."""
+    __slots__ = ("array", "count", "grads", "bits", "device", "scratch", "values", "mode", "held")
+
+
+def gpt2_adamw_tensors(masters, grads, ms, vs, params=None, m_scales=None, v_scales=None, weight_decay=0.0,
+                       m_values=None, v_values=None):
+    """A list of tensors for gpt2_op_adamw_many. For each: master (float32), grad (float32 or bfloat16, all alike), m
+    and v (float32, or uint8 codes with m_scales and v_scales, uint8 [ceil(n / 128)]), params (bfloat16 or None)
+    and weight_decay (a number, or one for each). m_values, v_values: where gpt2_op_adamw_many_states writes the
+    values of 8-bit moments (float32 or bfloat16, all alike). All contiguous, on one device."""
+    torch = _tc()
+    n = len(masters)
+    decay = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else [float(x) for x in weight_decay]
+    columns = {"params": params, "grads": grads, "ms": ms, "vs": vs, "m_scales": m_scales, "v_scales": v_scales,
+               "m_values": m_values, "v_values": v_values}
+    columns = {k: [None] * n if c is None else list(c) for k, c in columns.items()}
+    if len(decay) != n or any(len(c) != n for c in columns.values()):
+        raise ValueError("gpt2_adamw_tensors: every list needs one entry a tensor")
+    h = AdamWTensors()
+    h.count, h.bits, h.grads, h.values, h.device, h.mode = n, 32, MODE_FP32, None, None, MODE_FP32
+    if n:
+        h.grads = _mode_of("grads", grads[0])
+        if ms[0].dtype is torch.uint8:
+            h.bits = 8
+        elif ms[0].dtype is not torch.float32:
+            raise ValueError("moments: float32 or uint8 is needed")
+        h.device = masters[0].get_device()
+        if (m_values is None) != (v_values is None) or (m_values is not None and h.bits != 8):
+            raise ValueError("m_values and v_values come together, with moments in 8 bits")
+        if m_values is not None:
+            h.mode = _mode_of("m_values", columns["m_values"][0])
+    moment = torch.uint8 if h.bits == 8 else torch.float32
+    kinds = {"params": torch.bfloat16, "grads": torch.bfloat16 if h.grads == MODE_BF16 else torch.float32, "ms": moment,
+             "vs": moment, "m_scales": torch.uint8, "v_scales": torch.uint8,
+             "m_values": torch.bfloat16 if h.mode == MODE_BF16 else torch.float32}
+    kinds["v_values"] = kinds["m_values"]
+    h.array = (gpt2_adamw_tensor * max(n, 1))()
+    values = (c_void_p * max(n, 1))(), (c_void_p * max(n, 1))()
+    for i, master in enumerate(masters):
+        size = master.numel()
+        of = {"masters": (master, torch.float32, size)}
+        of |= {k: (c[i], kinds[k], -(-size // 128) if k.endswith("scales") else size) for k, c in columns.items()}
+        for k, (t, dtype, count) in of.items():
+            if t is None:
+                if k in ("grads", "ms", "vs") or (h.bits == 8 and k.endswith("scales")):
+                    raise ValueError(f"{k}: tensor {i} is needed")
+                if k.endswith("values") and m_values is not None:
+                    raise ValueError(f"{k}: tensor {i} is needed")
+            elif t.dtype is not dtype or t.numel() != count or not t.is_contiguous():
+                raise ValueError(f"{k}: contiguous {dtype} of {count} values is needed for tensor {i}")
+            elif t.get_device() != h.device:
+                raise RuntimeError("gpt2_adamw_tensors: every tensor has to be on one device")
+        a = h.array[i]
+        a.master, a.param_bf16, a.grad, a.m, a.v, a.m_scale, a.v_scale = (
+            _p(of[k][0]) for k in ("masters", "params", "grads", "ms", "vs", "m_scales", "v_scales"))
+        a.n, a.weight_decay = size, decay[i]
+        if m_values is not None:
+            values[0][i], values[1][i] = _p(of["m_values"][0]), _p(of["v_values"][0])
+    if m_values is not None:
+        h.values = values
+    h.scratch = load_library().gpt2_op_adamw_many_scratch(h.array, n)
+    h.held = (list(masters), columns)
+    return h
+
+
+def gpt2_op_adamw_many(tensors, lr, beta1, beta2, eps, t, grad_scale=1.0, max_grad_norm=0.0, grad_norm=None, seed=0,
+                       stream=None):
+    """One AdamW step t on the tensors of a gpt2_adamw_tensors list; grad_norm (float32 [1]) receives the norm of the
+    gradients over all of them, which max_grad_norm > 0 clips. seed: of the rounding of 8-bit moments."""
+    what = "gpt2_op_adamw_many"
+    lib = load_library()
+    device, st = (_tc(), _where(stream))[1]
+    if tensors.count and tensors.device != device:
+        raise _elsewhere(what)
+    if grad_norm is not None:
+        if grad_norm.dtype is not _torch.float32 or grad_norm.numel() != 1:
+            raise ValueError("grad_norm: one float32 is needed")
+        if grad_norm.get_device() != device:
+            raise _elsewhere(what)
+    nb = tensors.scratch if max_grad_norm > 0 or grad_norm is not None else 0
+    sc = _borrow(nb, st) if nb else None
+    try:
+        check(lib.gpt2_op_adamw_many(tensors.array, tensors.count, tensors.grads, tensors.bits, lr, beta1, beta2, eps,
+                                     grad_scale, max_grad_norm, _p(grad_norm), t, seed, sc, nb, st), what)
+    finally:
+        if sc:
+            _give_back(sc)
+
+
+def gpt2_op_adamw_many_states(tensors, stream=None):
+    """The values of the tensors' 8-bit moments, into the list's m_values and v_values."""
+    what = "gpt2_op_adamw_many_states"
+    if tensors.bits != 8 or tensors.values is None:
+        raise ValueError(f"{what}: a list of tensors with 8-bit moments, m_values and v_values is needed")
+    device, st = (_tc(), _where(stream))[1]
+    if tensors.device != device:
+        raise _elsewhere(what)
+    check(load_library().gpt2_op_adamw_many_states(tensors.array, *tensors.values, tensors.count, tensors.mode, st), what)
 
 
 def gpt2_op_gelu_forward(g, u, stream=None):
