@@ -513,8 +513,8 @@ int gpt2_op_linear_classifier_backward(int dtype, void* dx, void* dw, int dw_fp3
  * consecutive values share one) is code * 2^(s - 127):
  *   m   sign, 4 exponent bits (bias 7), 3 mantissa bits; the largest magnitude
  *       of a block lies in [2^7, 2^8]; 0x7F and 0xFF are NaN;
- *   v   5 exponent bits (bias 15), 3 mantissa bits, no sign; the largest lies
- *       in [2^14, 2^15]; 0xFF is NaN.
+ *   v   5 exponent bits (bias 15), 3 mantissa bits, no sign (the top of an
+ *       fp16 number); the largest lies in [2^14, 2^15]; NaN is written as 0xFF.
  * Both have subnormals. The new m and v are formed in fp32 and used for theta
  * as they are; stored, they are rounded up or down to a neighbouring code so
  * that they are right on average: up where (what is left over the lower code)

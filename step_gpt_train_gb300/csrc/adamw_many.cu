@@ -23,12 +23,13 @@
 #include "common.cuh"
 #include "launch.h"
 
+#include <cuda_fp16.h>
 #include <math.h>
 
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int GROUPS = 4;                       // groups of four values a thread
+constexpr int GROUPS = 2;                       // groups of four values a thread
 constexpr int CHUNK = THREADS * 4 * GROUPS;     // values a block
 constexpr int SCALE_BLOCK = 128;                // values that share a scale: a warp's group
 
@@ -75,6 +76,14 @@ __device__ __forceinline__ uint64_t mix(uint64_t z) {  // the finaliser of split
     return z ^ (z >> 31);
 }
 
+__device__ __forceinline__ void load4(const bf16* p, float (&f)[4]) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    f[0] = __uint_as_float(u.x << 16); f[1] = __uint_as_float(u.x & 0xFFFF0000u);
+    f[2] = __uint_as_float(u.y << 16); f[3] = __uint_as_float(u.y & 0xFFFF0000u);
+}
+
+constexpr uint64_t GOLDEN = 0x9E3779B97F4A7C15ULL;
+
 // Four neighbours of n values from i on; what lies behind the end reads as 0 and is not written.
 __device__ __forceinline__ void get4(const float* p, int64_t i, int64_t n, bool whole, float (&f)[4]) {
     if (whole) {
@@ -94,6 +103,19 @@ __device__ __forceinline__ void get4(const bf16* p, int64_t i, int64_t n, bool w
 #pragma unroll
         for (int j = 0; j < 4; j++) f[j] = i + j < n ? __bfloat162float(p[i + j]) : 0.f;
     }
+}
+// The same without the hint that the values are read once.
+__device__ __forceinline__ void keep4(const float* p, int64_t i, int64_t n, bool whole, float (&f)[4]) {
+    if (whole) {
+        const float4 a = *reinterpret_cast<const float4*>(p + i);
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    } else {
+        get4(p, i, n, false, f);
+    }
+}
+__device__ __forceinline__ void keep4(const bf16* p, int64_t i, int64_t n, bool whole, float (&f)[4]) {
+    if (whole) load4(p + i, f);
+    else get4(p, i, n, false, f);
 }
 __device__ __forceinline__ uint32_t get4(const uint8_t* p, int64_t i, int64_t n, bool whole) {
     if (whole) return __ldcs(reinterpret_cast<const uint32_t*>(p + i));
@@ -134,132 +156,186 @@ __device__ __forceinline__ void put4(uint8_t* p, int64_t i, int64_t n, bool whol
     }
 }
 
-// A code of three mantissa bits read as the top of an fp32 number: 2^(127 - bias) restores its exponent,
-// and codes below the lowest whole exponent come out right as fp32 subnormals.
-__device__ __forceinline__ float decode_m(uint32_t c, float scale) {
-    const uint32_t k = c & 0x7Fu;
-    float y = __uint_as_float(k << 20) * 0x1p120f;
-    if (k == 0x7Fu) y = __uint_as_float(0x7FC00000u);
-    return (c & 0x80u ? -y : y) * scale;
+// Four codes (a word) as fp32, without their scale. m: two e4m3 codes a conversion. v: a code is the top byte of an
+// fp16 number without its sign bit.
+__device__ __forceinline__ void decode_m(uint32_t w, float (&f)[4]) {
+#pragma unroll
+    for (int p = 0; p < 2; p++) {
+        uint32_t h;
+        asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}\n" : "=r"(h) : "r"(w >> (16 * p)));
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        f[2 * p] = x.x;
+        f[2 * p + 1] = x.y;
+    }
 }
-__device__ __forceinline__ float decode_v(uint32_t c, float scale) {
-    const float y = __uint_as_float(c << 20) * 0x1p112f;
-    return (c == 0xFFu ? __uint_as_float(0x7FC00000u) : y) * scale;
+__device__ __forceinline__ void decode_v(uint32_t w, float (&f)[4]) {
+#pragma unroll
+    for (int p = 0; p < 2; p++) {
+        const uint32_t h = __byte_perm(w, 0, p ? 0x4342 : 0x4140) << 7;
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        f[2 * p] = x.x;
+        f[2 * p + 1] = x.y;
+    }
 }
 __device__ __forceinline__ float scale_of(uint8_t b) { return __uint_as_float((b < 1 ? 1u : b > 254 ? 254u : b) << 23); }
 
-// The code of y >= 0 (already divided by the scale) with exponent bias BIAS, rounded up with probability
-// (what is left of it) / (a code's step): r are 16 random bits. Not a number, or infinite: all ones.
-template <int BIAS> __device__ __forceinline__ uint32_t encode(float y, uint32_t r) {
-    constexpr float LOWEST = BIAS == 7 ? 0x1p-6f : 0x1p-14f, STEPS = BIAS == 7 ? 0x1p9f : 0x1p17f;
-    if (y >= LOWEST) return ((__float_as_uint(y) + (r << 4)) >> 20) - ((127u - BIAS) << 3);
-    return (uint32_t)(y * STEPS + (float)r * 0x1p-16f);
-}
-__device__ __forceinline__ uint32_t finite_bits(float x) {
-    const uint32_t u = __float_as_uint(x) & 0x7FFFFFFFu;
-    return u < 0x7F800000u ? u : 0u;
-}
+// The code of y >= 0, given y under its scale, times 2^(bias - 127): then the top bits of the fp32 number are the
+// code, an fp32 subnormal holding what is below the code's lowest whole exponent. Adding 16 random bits right below
+// the code's last one carries into it with the probability (what is left over the lower code) / (the codes' distance).
+__device__ __forceinline__ uint32_t encode(float y, uint32_t r_shifted) { return (__float_as_uint(y) + r_shifted) >> 20; }
+
 // The scale byte of a block whose largest magnitude has these bits.
 __device__ __forceinline__ uint32_t scale_byte(uint32_t largest, int top) {
     const int b = (int)(largest >> 23) - top;
     return b < 1 ? 1u : (uint32_t)b;
 }
+constexpr uint32_t INF_BITS = 0x7F800000u;
 
-template <int MOST, typename G, bool EIGHT>
-__global__ void __launch_bounds__(THREADS) adamw_many_kernel(const __grid_constant__ Batch<MOST> b, const Values h) {
-    const int k = find(b, blockIdx.x);
-    const Entry& e = b.e[k];
-    const int64_t n = e.n, base = (int64_t)((int)blockIdx.x - e.first) * CHUNK + threadIdx.x * 4;
+// The square root and the quotient of 8-bit moments' updates are the hardware's (2^-22 of a step, where a stored
+// moment is off by up to 2^-4): the IEEE forms cost a third of the kernel.
+template <bool EIGHT> __device__ __forceinline__ float step_of(float m, float v, float eps) {
+    if (!EIGHT) return m / (sqrtf(v) + eps);
+    float root;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v));
+    return __fdividef(m, root + eps);
+}
+
+// A block's chunk of a tensor: all loads of the thread's groups first, then one group after another (what is stored
+// may be what a later group loads, as far as the compiler knows: it moves no load over a store). WHOLE: the chunk lies
+// inside the tensor and every address allows four values at once.
+template <typename G, bool EIGHT, bool WHOLE>
+__device__ __forceinline__ void adamw_chunk(const Entry& e, const Values& h, int64_t base, uint64_t draw) {
+    const int64_t n = e.n;
     float gs = h.grad_scale;
     if (h.norm) gs *= fminf(1.f, h.max_norm / (*h.norm * h.grad_scale + 1e-6f));
-    const uint64_t tensor = (uint64_t)(b.base + k) << 40;
+    float th[GROUPS][4], g[GROUPS][4], m[GROUPS][4], v[GROUPS][4];
+    uint32_t cm[GROUPS], cv[GROUPS];
+    uint8_t bm[GROUPS], bv[GROUPS];
+    auto whole = [&](int u) { return WHOLE || (e.aligned && base + u * (THREADS * 4) + 4 <= n); };
 #pragma unroll
     for (int u = 0; u < GROUPS; u++) {
         const int64_t i = base + u * (THREADS * 4);
-        if (i - (threadIdx.x & 31) * 4 >= n) break;  // the whole warp
-        const bool whole = e.aligned && i + 4 <= n;
-        float th[4], g[4], m[4], v[4];
-        get4(e.master, i, n, whole, th);
-        get4((const G*)e.grad, i, n, whole, g);
+        get4(e.master, i, n, whole(u), th[u]);
+        get4((const G*)e.grad, i, n, whole(u), g[u]);
         if (EIGHT) {
-            const int64_t at = i / SCALE_BLOCK;
-            const float ms = scale_of(e.m_scale[at]), vs = scale_of(e.v_scale[at]);
-            const uint32_t cm = get4((const uint8_t*)e.m, i, n, whole), cv = get4((const uint8_t*)e.v, i, n, whole);
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                m[j] = decode_m(cm >> (8 * j) & 0xFFu, ms);
-                v[j] = decode_v(cv >> (8 * j) & 0xFFu, vs);
-            }
+            const bool in = WHOLE || i < n;
+            bm[u] = in ? e.m_scale[i / SCALE_BLOCK] : 0;
+            bv[u] = in ? e.v_scale[i / SCALE_BLOCK] : 0;
+            cm[u] = get4((const uint8_t*)e.m, i, n, whole(u));
+            cv[u] = get4((const uint8_t*)e.v, i, n, whole(u));
         } else {
-            get4((const float*)e.m, i, n, whole, m);
-            get4((const float*)e.v, i, n, whole, v);
+            get4((const float*)e.m, i, n, whole(u), m[u]);
+            get4((const float*)e.v, i, n, whole(u), v[u]);
+        }
+    }
+    const float b1c = 1.f - h.b1, b2c = 1.f - h.b2;
+#pragma unroll
+    for (int u = 0; u < GROUPS; u++) {
+        const int64_t i = base + u * (THREADS * 4);
+        if (!WHOLE && i - (threadIdx.x & 31) * 4 >= n) break;  // the whole warp
+        if (EIGHT) {
+            const float ms = scale_of(bm[u]), vs = scale_of(bv[u]);
+            decode_m(cm[u], m[u]);
+            decode_v(cv[u], v[u]);
+#pragma unroll
+            for (int j = 0; j < 4; j++) m[u][j] *= ms, v[u][j] *= vs;
         }
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-            const float gj = g[j] * gs;
-            m[j] = h.b1 * m[j] + (1.f - h.b1) * gj;
-            v[j] = h.b2 * v[j] + (1.f - h.b2) * gj * gj;
-            th[j] = th[j] - h.lr * (m[j] * h.inv_bc1 / (sqrtf(v[j] * h.inv_bc2) + h.eps) + e.decay * th[j]);
+            const float gj = g[u][j] * gs;
+            m[u][j] = h.b1 * m[u][j] + b1c * gj;
+            v[u][j] = h.b2 * v[u][j] + b2c * gj * gj;
+            th[u][j] -= h.lr * (step_of<EIGHT>(m[u][j] * h.inv_bc1, v[u][j] * h.inv_bc2, h.eps) + e.decay * th[u][j]);
         }
-        put4(e.master, i, n, whole, th);
-        if (e.param) put4(e.param, i, n, whole, th);
+        put4(e.master, i, n, whole(u), th[u]);
+        if (e.param) put4(e.param, i, n, whole(u), th[u]);
         if (EIGHT) {
             uint32_t am = 0, av = 0;
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                am = max(am, finite_bits(m[j]));
-                av = max(av, finite_bits(v[j]));
+                am = max(am, __float_as_uint(m[u][j]) & 0x7FFFFFFFu);
+                av = max(av, __float_as_uint(v[u][j]) & 0x7FFFFFFFu);
             }
-            am = __reduce_max_sync(0xffffffffu, am);
-            av = __reduce_max_sync(0xffffffffu, av);
-            const uint32_t bm = scale_byte(am, 7), bv = scale_byte(av, 14);
-            const float im = __uint_as_float((254u - bm) << 23), iv = __uint_as_float((254u - bv) << 23);
-            uint32_t cm = 0, cv = 0;
+            const bool odd = __any_sync(0xffffffffu, max(am, av) >= INF_BITS);
+            if (odd) {  // what is not finite leaves the scale alone
+                am = av = 0;
 #pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-                const uint64_t r = mix(h.key + (tensor + (uint64_t)(i + j) / 2) * 0x9E3779B97F4A7C15ULL);
-#pragma unroll
-                for (int o = 0; o < 2; o++) {
-                    const uint32_t w = (uint32_t)(r >> (32 * o));
-                    const float x = m[j + o], y = v[j + o];
-                    uint32_t c = isfinite(x) ? encode<7>(fabsf(x) * im, w & 0xFFFFu) : 0x7Fu;
-                    if (x < 0.f) c |= 0x80u;
-                    cm |= c << (8 * (j + o));
-                    c = isfinite(y) ? encode<15>(y * iv, w >> 16) : 0xFFu;
-                    if (c == 0 && y > 0.f) c = 1;
-                    cv |= c << (8 * (j + o));
+                for (int j = 0; j < 4; j++) {
+                    const uint32_t x = __float_as_uint(m[u][j]) & 0x7FFFFFFFu, y = __float_as_uint(v[u][j]) & 0x7FFFFFFFu;
+                    am = max(am, x < INF_BITS ? x : 0u);
+                    av = max(av, y < INF_BITS ? y : 0u);
                 }
             }
-            put4((uint8_t*)e.m, i, n, whole, cm);
-            put4((uint8_t*)e.v, i, n, whole, cv);
+            am = scale_byte(__reduce_max_sync(0xffffffffu, am), 7);
+            av = scale_byte(__reduce_max_sync(0xffffffffu, av), 14);
+            const float im = __uint_as_float((254u - am) << 23), iv = __uint_as_float((254u - av) << 23);
+            uint32_t wm = 0, wv = 0;
+#pragma unroll
+            for (int p = 0; p < 2; p++) {
+                const uint64_t r = mix(draw + p * GOLDEN);
+#pragma unroll
+                for (int o = 0; o < 2; o++) {
+                    const int j = 2 * p + o;
+                    const uint32_t w = (uint32_t)(r >> (32 * o));
+                    uint32_t x = encode(fabsf(m[u][j]) * im * 0x1p-120f, w << 4 & 0xFFFF0u);
+                    uint32_t y = encode(v[u][j] * iv * 0x1p-112f, w >> 12 & 0xFFFF0u);
+                    y = max(y, v[u][j] > 0.f ? 1u : 0u);
+                    if (odd) {
+                        if (!isfinite(m[u][j])) x = 0x7Fu;
+                        if (!isfinite(v[u][j])) y = 0xFFu;
+                    }
+                    wm |= (x | (__float_as_uint(m[u][j]) >> 24 & 0x80u)) << (8 * j);
+                    wv |= y << (8 * j);
+                }
+            }
+            draw += (uint64_t)(THREADS * 2) * GOLDEN;
+            put4((uint8_t*)e.m, i, n, whole(u), wm);
+            put4((uint8_t*)e.v, i, n, whole(u), wv);
             if ((threadIdx.x & 31) == 0) {
-                e.m_scale[i / SCALE_BLOCK] = (uint8_t)bm;
-                e.v_scale[i / SCALE_BLOCK] = (uint8_t)bv;
+                e.m_scale[i / SCALE_BLOCK] = (uint8_t)am;
+                e.v_scale[i / SCALE_BLOCK] = (uint8_t)av;
             }
         } else {
-            put4((float*)e.m, i, n, whole, m);
-            put4((float*)e.v, i, n, whole, v);
+            put4((float*)e.m, i, n, whole(u), m[u]);
+            put4((float*)e.v, i, n, whole(u), v[u]);
         }
     }
 }
 
-// Sum of squares of a block's gradients, in a fixed order.
+template <int MOST, typename G, bool EIGHT>
+__global__ void __launch_bounds__(THREADS) adamw_many_kernel(const __grid_constant__ Batch<MOST> b, const Values h) {
+    // from the end: the norm's pass has just read the last gradients, which L2 still holds
+    const int block = gridDim.x - 1 - blockIdx.x;
+    const int k = find(b, block);
+    const Entry& e = b.e[k];
+    const int64_t first = (int64_t)(block - e.first) * CHUNK, base = first + threadIdx.x * 4;
+    const uint64_t draw = h.key + (((uint64_t)(b.base + k) << 40) + (uint64_t)base / 2) * GOLDEN;
+    if (e.aligned && first + CHUNK <= e.n) adamw_chunk<G, EIGHT, true>(e, h, base, draw);
+    else adamw_chunk<G, EIGHT, false>(e, h, base, draw);
+}
+
+// Sums of squares of the gradients: a block takes every gridDim.x-th chunk and adds in a fixed order.
 template <int MOST, typename G>
-__global__ void __launch_bounds__(THREADS) sumsq_many_kernel(const __grid_constant__ Batch<MOST> b,
+__global__ void __launch_bounds__(THREADS) sumsq_many_kernel(const __grid_constant__ Batch<MOST> b, int chunks,
                                                              float* __restrict__ partial) {
     __shared__ float sh[THREADS / 32];
-    const Entry& e = b.e[find(b, blockIdx.x)];
-    const int64_t n = e.n, base = (int64_t)((int)blockIdx.x - e.first) * CHUNK + threadIdx.x * 4;
-    float acc = 0.f;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const Entry& e = b.e[find(b, c)];
+        const int64_t n = e.n, base = (int64_t)(c - e.first) * CHUNK + threadIdx.x * 4;
+        float g[GROUPS][4];
 #pragma unroll
-    for (int u = 0; u < GROUPS; u++) {
-        const int64_t i = base + u * (THREADS * 4);
-        float g[4];
-        get4((const G*)e.grad, i, n, e.aligned && i + 4 <= n, g);
-        acc += g[0] * g[0] + g[1] * g[1] + g[2] * g[2] + g[3] * g[3];
+        for (int u = 0; u < GROUPS; u++) {
+            const int64_t i = base + u * (THREADS * 4);
+            keep4((const G*)e.grad, i, n, e.aligned && i + 4 <= n, g[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < GROUPS; u++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) acc[j] = fmaf(g[u][j], g[u][j], acc[j]);
     }
-    acc = warp_sum(acc);
-    if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = acc;
+    const float s = warp_sum((acc[0] + acc[1]) + (acc[2] + acc[3]));
+    if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = s;
     __syncthreads();
     if (threadIdx.x == 0) {
         float t = 0.f;
@@ -270,10 +346,10 @@ __global__ void __launch_bounds__(THREADS) sumsq_many_kernel(const __grid_consta
 }
 
 __global__ void __launch_bounds__(1024) norm_many_kernel(float* __restrict__ norm, float* __restrict__ out,
-                                                         const float* __restrict__ partial, int64_t n) {
+                                                         const float* __restrict__ partial, int n) {
     __shared__ double sh[32];
     double v = 0.0;
-    for (int64_t i = threadIdx.x; i < n; i += 1024) v += partial[i];
+    for (int i = threadIdx.x; i < n; i += 1024) v += partial[i];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = v;
@@ -297,13 +373,11 @@ __global__ void __launch_bounds__(THREADS) states_many_kernel(const __grid_const
         const bool whole = e.aligned && i + 4 <= n;
         const int64_t at = i / SCALE_BLOCK;
         const float ms = scale_of(e.m_scale[at]), vs = scale_of(e.v_scale[at]);
-        const uint32_t cm = get4((const uint8_t*)e.m, i, n, whole), cv = get4((const uint8_t*)e.v, i, n, whole);
         float m[4], v[4];
+        decode_m(get4((const uint8_t*)e.m, i, n, whole), m);
+        decode_v(get4((const uint8_t*)e.v, i, n, whole), v);
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            m[j] = decode_m(cm >> (8 * j) & 0xFFu, ms);
-            v[j] = decode_v(cv >> (8 * j) & 0xFFu, vs);
-        }
+        for (int j = 0; j < 4; j++) m[j] *= ms, v[j] *= vs;
         put4((T*)(void*)e.master, i, n, whole, m);  // the values' places travel in master and param
         put4((T*)(void*)e.param, i, n, whole, v);
     }
@@ -360,6 +434,8 @@ void start_adamw(const Batch<MOST>& b, int blocks, int bits, const Values& h, cu
     else adamw_many_kernel<MOST, G, false><<<blocks, THREADS, 0, s>>>(b, h);
 }
 
+int sumsq_blocks() { return gpt2_num_sms() * 8; }
+
 uint64_t host_mix(uint64_t z) {
     z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ULL;
     z = (z ^ (z >> 27)) * 0x94D049BB133111EBULL;
@@ -369,7 +445,10 @@ uint64_t host_mix(uint64_t z) {
 }  // namespace
 
 // The norm, then a partial sum for each block.
-size_t adamw_many_scratch(const gpt2_adamw_tensor* t, int n) { return 256 + (size_t)blocks_of(t, n) * 4; }
+size_t adamw_many_scratch(const gpt2_adamw_tensor* t, int n) {
+    const int64_t blocks = blocks_of(t, n), most = (int64_t)sumsq_blocks() * (n / MANY + 1);
+    return 256 + (size_t)(blocks < most ? blocks : most) * 4;
+}
 
 int launch_adamw_many(const gpt2_adamw_tensor* t, int n, int grad_dtype, int bits, float lr, float b1, float b2,
                       float eps, float grad_scale, float max_norm, float* grad_norm, int step, uint64_t seed,
@@ -382,12 +461,15 @@ int launch_adamw_many(const gpt2_adamw_tensor* t, int n, int grad_dtype, int bit
     if (max_norm > 0.f || grad_norm) {
         float* norm = (float*)scratch;
         float* partial = norm + 64;
-        int64_t at = 0;
+        int at = 0;
         launches += in_batches(t, n, as_is, [&](const auto& b, int blocks) {
             constexpr int MOST = sizeof(b.e) / sizeof(Entry);
-            if (grad_dtype == GPT2_MODE_BF16) sumsq_many_kernel<MOST, bf16><<<blocks, THREADS, 0, s>>>(b, partial + at);
-            else sumsq_many_kernel<MOST, float><<<blocks, THREADS, 0, s>>>(b, partial + at);
-            at += blocks;
+            const int grid = blocks < sumsq_blocks() ? blocks : sumsq_blocks();
+            if (grad_dtype == GPT2_MODE_BF16)
+                sumsq_many_kernel<MOST, bf16><<<grid, THREADS, 0, s>>>(b, blocks, partial + at);
+            else
+                sumsq_many_kernel<MOST, float><<<grid, THREADS, 0, s>>>(b, blocks, partial + at);
+            at += grid;
         });
         norm_many_kernel<<<1, 1024, 0, s>>>(norm, grad_norm, partial, at);
         launches++;

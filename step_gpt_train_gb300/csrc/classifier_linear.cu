@@ -41,13 +41,16 @@ Pieces pieces(int dtype, int N, int V) {
 int round8(int v) { return (v + 7) / 8 * 8; }
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
-// Joins the parts of a row, slot after slot in eight strands, then the strands: lse and loss.
-__global__ void __launch_bounds__(256) join_kernel(float* __restrict__ losses, float* __restrict__ lse,
-                                                   const float2* __restrict__ stats,
-                                                   const float* __restrict__ target_logit,
-                                                   const int32_t* __restrict__ targets, int N, int V, int slots,
-                                                   int* status) {
-    __shared__ float2 sm[8][32];
+// Joins the parts of 32 rows: strand after strand of slots (a warp's lanes read neighbouring rows of one slot),
+// then the strands. Loads run ahead in batches: a part's exponentials wait for it, the next parts do not.
+// 8 strands where there are rows enough to fill the device with them, 32 for fewer rows.
+template <int STRANDS, int AHEAD>
+__global__ void __launch_bounds__(STRANDS * 32) join_kernel(float* __restrict__ losses, float* __restrict__ lse,
+                                                           const float2* __restrict__ stats,
+                                                           const float* __restrict__ target_logit,
+                                                           const int32_t* __restrict__ targets, int N, int V, int slots,
+                                                           int* status) {
+    __shared__ float2 sm[STRANDS][32];
     const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
     const int64_t row = (int64_t)blockIdx.x * 32 + tx;
     float m = -INFINITY, s = 0.f;
@@ -57,12 +60,25 @@ __global__ void __launch_bounds__(256) join_kernel(float* __restrict__ losses, f
         s = s * ex2_approx((m - mm) * LOG2E) + p.y * ex2_approx((p.x - mm) * LOG2E);
         m = mm;
     };
-    if (row < N)
-        for (int i = ty; i < slots; i += 8) join(stats[(int64_t)i * N + row]);
+    for (int i = ty; i < slots; i += STRANDS * AHEAD) {
+        float2 p[AHEAD];
+#pragma unroll
+        for (int u = 0; u < AHEAD; u++) {
+            const int slot = i + u * STRANDS;
+            p[u] = slot < slots && row < N ? __ldcs(&stats[(int64_t)slot * N + row]) : make_float2(0.f, 0.f);
+        }
+#pragma unroll
+        for (int u = 0; u < AHEAD; u++) join(p[u]);
+    }
     sm[ty][tx] = make_float2(m, s);
-    __syncthreads();
+    for (int w = STRANDS / 2; w > 0; w /= 2) {  // halves of the strands, in a fixed order
+        __syncthreads();
+        if (ty < w) {
+            join(sm[ty + w][tx]);
+            sm[ty][tx] = make_float2(m, s);
+        }
+    }
     if (ty || row >= N) return;
-    for (int i = 1; i < 8; i++) join(sm[i][tx]);
     const int t = targets[row];
     if (t < 0 || t >= V) set_status(status, GPT2_FLAG_TARGET_RANGE);
     // (max - z) + ln S rather than lse - z: a sure token's loss keeps its digits wherever the logits lie, and
@@ -165,7 +181,10 @@ int launch_linear_classifier_forward(int dtype, float* losses, float* lse, const
             launches += n + 1;
         }
     }
-    join_kernel<<<(N + 31) / 32, 256, 0, s>>>(losses, lse, stats, target_logit, targets, N, V, slots, status);
+    const int blocks = (N + 31) / 32;
+    if (blocks >= 4 * gpt2_num_sms())
+        join_kernel<8, 8><<<blocks, 256, 0, s>>>(losses, lse, stats, target_logit, targets, N, V, slots, status);
+    else join_kernel<32, 4><<<blocks, 1024, 0, s>>>(losses, lse, stats, target_logit, targets, N, V, slots, status);
     return launches + 1;
 }
 

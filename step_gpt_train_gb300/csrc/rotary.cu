@@ -10,100 +10,95 @@
 // (2^-33 of a turn, where a 32-bit product of position and frequency is off by
 // 0.006 rad at 10^5); the signed top half, as half turns, goes to sincospif.
 //
-// A head is held by hd / E neighbouring lanes of a warp, E values (8 or 16
-// bytes) each; a warp takes a row and walks its heads, so a lane forms the
-// angles of its pairs once a row. The two values of a pair are in one lane
-// (interleaved) or in two lanes rot / 2 values apart, which exchange them by a
-// shuffle. Every value is read before the lanes of its head write, so the
-// output may be the input.
+// A head is held by hd / E neighbouring lanes of a warp, E values (16 bytes, or
+// 8 where the halves of a pair would not lie in whole lanes) each. A warp takes
+// a row: its lanes form the angles of the row's pairs once, share them through
+// shared memory, and walk the heads, a few of them loaded at a time. The two
+// values of a pair are in one lane (interleaved) or in two lanes rot / 2 values
+// apart, which exchange them by shuffles. Every value is read before the lanes
+// of its head write, so the output may be the input.
 //
-// The pass reads and writes each value once: HBM bounds it.
+// The pass reads and writes each value once: HBM bounds it where the
+// instructions of a value (an unpacking, a square, three products, an exchange,
+// a packing; on pairs of values where they lie so) leave it room.
 #include "common.cuh"
 #include "launch.h"
+#include "tc_common.cuh"
 
 namespace {
 
-constexpr int THREADS = 256;
-constexpr int WARPS = THREADS / 32;
+using tc::f2_add;
+using tc::f2_fma;
+using tc::f2_mul;
+using tc::f2_pack;
+using tc::f2_unpack;
 
-// E values of T at p (aligned to their size) as fp32.
-__device__ __forceinline__ void load_e(const float* p, float (&f)[4]) {
-    const float4 a = *reinterpret_cast<const float4*>(p);
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+constexpr int WARPS = 8;  // a block's
+constexpr int MOST_PAIRS = 64;
+constexpr int BACK_A_SM = 3;  // blocks of the backward on an SM
+
+// E values of T as loaded, and as fp32.
+template <typename T, int E> struct Raw;
+template <> struct Raw<bf16, 8> { uint32_t w[4]; };
+template <> struct Raw<bf16, 4> { uint32_t w[2]; };
+template <> struct Raw<float, 4> { uint32_t w[4]; };
+
+__device__ __forceinline__ void load_raw(Raw<bf16, 8>& r, const bf16* p) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    r.w[0] = u.x, r.w[1] = u.y, r.w[2] = u.z, r.w[3] = u.w;
 }
-__device__ __forceinline__ void load_e(const bf16* p, float (&f)[4]) {
+__device__ __forceinline__ void load_raw(Raw<bf16, 4>& r, const bf16* p) {
     const uint2 u = *reinterpret_cast<const uint2*>(p);
-    f[0] = __uint_as_float(u.x << 16); f[1] = __uint_as_float(u.x & 0xFFFF0000u);
-    f[2] = __uint_as_float(u.y << 16); f[3] = __uint_as_float(u.y & 0xFFFF0000u);
+    r.w[0] = u.x, r.w[1] = u.y;
 }
-template <typename T> __device__ __forceinline__ void load_e(const T* p, float (&f)[8]) { load8(p, f); }
+__device__ __forceinline__ void load_raw(Raw<float, 4>& r, const float* p) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    r.w[0] = u.x, r.w[1] = u.y, r.w[2] = u.z, r.w[3] = u.w;
+}
+template <int E> __device__ __forceinline__ void unpack(const Raw<bf16, E>& r, float (&f)[E]) {
+#pragma unroll
+    for (int i = 0; i < E / 2; i++) {
+        f[2 * i] = __uint_as_float(r.w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(r.w[i] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void unpack(const Raw<float, 4>& r, float (&f)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) f[i] = __uint_as_float(r.w[i]);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void store_e(bf16* p, const float (&f)[8]) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+}
+__device__ __forceinline__ void store_e(bf16* p, const float (&f)[4]) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
+}
 __device__ __forceinline__ void store_e(float* p, const float (&f)[4]) {
     *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
 }
-__device__ __forceinline__ void store_e(bf16* p, const float (&f)[4]) {
-    uint2 u;
-    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
-    h[0] = __floats2bfloat162_rn(f[0], f[1]);
-    h[1] = __floats2bfloat162_rn(f[2], f[3]);
-    *reinterpret_cast<uint2*>(p) = u;
+
+// x *= y, and the sum of x y, on pairs of values.
+template <int E> __device__ __forceinline__ void times(float (&x)[E], const float (&y)[E]) {
+#pragma unroll
+    for (int i = 0; i < E; i += 2)
+        f2_unpack(f2_mul(f2_pack(x[i], x[i + 1]), f2_pack(y[i], y[i + 1])), x[i], x[i + 1]);
 }
-template <typename T> __device__ __forceinline__ void store_e(T* p, const float (&f)[8]) { store8(p, f); }
-
-// cos and sin, times the amplitude, of the pairs that this lane's values
-// belong to: one for each value in the half layout, one for each two in the
-// interleaved one. sin has its sign for this lane's value folded in: the
-// rotated value is c * own + s * other.
-template <int E, bool PAIRS> struct Angles {
-    static constexpr int N = PAIRS ? E / 2 : E;
-    float c[N], s[N];
-
-    __device__ __forceinline__ void of(int pos, const uint64_t* turns, int at, int rot, float amplitude) {
-        const int half = rot / 2;
+template <int E> __device__ __forceinline__ void times(float (&x)[E], float y) {
+    const uint64_t yy = f2_pack(y, y);
 #pragma unroll
-        for (int i = 0; i < N; i++) {
-            int j = PAIRS ? at / 2 + i : at + i;
-            if (!PAIRS && j >= half) j -= half;
-            c[i] = 1.f;
-            s[i] = 0.f;
-            if (at < rot) {
-                const uint64_t t = (uint64_t)(int64_t)pos * turns[j];
-                float sn, cs;
-                sincospif((float)(int32_t)(t >> 32) * 0x1p-31f, &sn, &cs);
-                c[i] = cs * amplitude;
-                s[i] = sn * amplitude;
-            }
-        }
-    }
-};
-
-// The rotation (dir = 1) or its transpose (dir = -1) of one lane's values. at: the first
-// value's place in the head; lanes of one head exchange values by shuffles, so all of a warp call it.
-template <int E, bool PAIRS>
-__device__ __forceinline__ void rotate(float (&x)[E], const Angles<E, PAIRS>& a, int at, int rot, float dir) {
-    if (PAIRS) {
-        if (at < rot) {
-#pragma unroll
-            for (int i = 0; i < E / 2; i++) {
-                const float u = x[2 * i], v = x[2 * i + 1], s = dir * a.s[i];
-                x[2 * i] = u * a.c[i] - v * s;
-                x[2 * i + 1] = u * s + v * a.c[i];
-            }
-        }
-    } else {
-        const int half = rot / 2;
-        const bool first = at < half;
-        const int lane = threadIdx.x & 31;
-        // the lane that holds the other values of these pairs
-        const int other = at >= rot ? lane : first ? lane + half / E : lane - half / E;
-        const float sign = first ? -dir : dir;
-#pragma unroll
-        for (int i = 0; i < E; i++) {
-            const float v = __shfl_sync(0xffffffffu, x[i], other);
-            if (at < rot) x[i] = x[i] * a.c[i] + sign * a.s[i] * v;
-        }
-    }
+    for (int i = 0; i < E; i += 2) f2_unpack(f2_mul(f2_pack(x[i], x[i + 1]), yy), x[i], x[i + 1]);
 }
-
+template <int E> __device__ __forceinline__ float dot(const float (&x)[E], const float (&y)[E]) {
+    uint64_t s = f2_mul(f2_pack(x[0], x[1]), f2_pack(y[0], y[1]));
+#pragma unroll
+    for (int i = 2; i < E; i += 2) s = f2_fma(f2_pack(x[i], x[i + 1]), f2_pack(y[i], y[i + 1]), s);
+    float a, b;
+    f2_unpack(s, a, b);
+    return a + b;
+}
 // Sum over the lanes of a head (L a power of two).
 template <int L> __device__ __forceinline__ float head_sum(float v) {
 #pragma unroll
@@ -111,42 +106,123 @@ template <int L> __device__ __forceinline__ float head_sum(float v) {
     return v;
 }
 
-template <typename T, int E, int L, bool PAIRS, bool NORM>
-__global__ void __launch_bounds__(THREADS) rotary_forward_kernel(const RotaryArgs a) {
-    constexpr int HD = E * L, GROUPS = 32 / L;
-    const int lane = threadIdx.x & 31, at = lane % L * E, group = lane / L;
-    float gq[E], gk[E];
-#pragma unroll
-    for (int i = 0; i < E; i++) gq[i] = gk[i] = 1.f;
-    if (NORM && a.q_gamma) load_e((const T*)a.q_gamma + at, gq);
-    if (NORM && a.k_gamma) load_e((const T*)a.k_gamma + at, gk);
-    const int heads = a.Hq + a.Hk;
-    for (int64_t row = (int64_t)blockIdx.x * WARPS + threadIdx.x / 32; row < a.N; row += (int64_t)gridDim.x * WARPS) {
-        Angles<E, PAIRS> ang;
-        ang.of(a.pos[row], a.turns, at, a.rot, a.amplitude);
-        const T* q = (const T*)a.q + row * a.q_stride + at;
-        const T* k = (const T*)a.k + row * a.k_stride + at;
-        T* qo = (T*)a.qo + row * a.qo_stride + at;
-        T* ko = (T*)a.ko + row * a.ko_stride + at;
-#pragma unroll 4
-        for (int h0 = 0; h0 < heads; h0 += GROUPS) {
-            const int h = h0 + group;
-            const bool key = h >= a.Hq;
-            float x[E];
-#pragma unroll
-            for (int i = 0; i < E; i++) x[i] = 0.f;
-            if (h < heads) load_e(key ? k + (h - a.Hq) * HD : q + h * HD, x);
-            if (NORM) {
-                float ss = 0.f;
-#pragma unroll
-                for (int i = 0; i < E; i++) ss += x[i] * x[i];
-                const float r = 1.f / sqrtf(head_sum<L>(ss) * (1.f / HD) + a.eps);
-#pragma unroll
-                for (int i = 0; i < E; i++) x[i] *= r * (key ? gk[i] : gq[i]);
-            }
-            rotate<E, PAIRS>(x, ang, at, a.rot, 1.f);
-            if (h < heads) store_e(key ? ko + (h - a.Hq) * HD : qo + h * HD, x);
+// cos and sin, times the amplitude, of the pairs that this lane's values belong
+// to: one for each value in the half layout (sin with the sign that turns the
+// other value into this one's share: y = c x + s x_other), one for each two in
+// the interleaved one. Values behind rot get 1 and 0. share: a warp's cos and sin.
+template <int E, bool PAIRS> struct Angles {
+    static constexpr int N = PAIRS ? E / 2 : E;
+    float c[N], s[N];
+
+    __device__ __forceinline__ void of(int pos, const uint64_t* turns, int at, int rot, float amplitude,
+                                       float (&share)[2][MOST_PAIRS]) {
+        const int half = rot / 2, lane = threadIdx.x & 31;
+        __syncwarp();  // the row before has read its angles
+        for (int j = lane; j < half; j += 32) {
+            const uint64_t t = (uint64_t)(int64_t)pos * turns[j];
+            float sn, cs;
+            sincospif((float)(int32_t)(t >> 32) * 0x1p-31f, &sn, &cs);
+            share[0][j] = cs * amplitude;
+            share[1][j] = sn * amplitude;
         }
+        __syncwarp();
+        const bool first = PAIRS || at < half;
+        const int j0 = PAIRS ? at / 2 : first ? at : at - half;
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            c[i] = at < rot ? share[0][j0 + i] : 1.f;
+            s[i] = at < rot ? (!PAIRS && first ? -share[1][j0 + i] : share[1][j0 + i]) : 0.f;
+        }
+    }
+};
+
+// The rotation of one lane's values, or its transpose (BACK). other: the lane that holds the other values of
+// its pairs (half layout). Lanes of a head exchange values, so all of a warp call it.
+template <int E, bool PAIRS, bool BACK>
+__device__ __forceinline__ void rotate(float (&x)[E], const Angles<E, PAIRS>& a, int other) {
+    if (PAIRS) {
+#pragma unroll
+        for (int i = 0; i < E / 2; i++) {
+            const float u = x[2 * i], v = x[2 * i + 1], s = BACK ? -a.s[i] : a.s[i];
+            x[2 * i] = u * a.c[i] - v * s;
+            x[2 * i + 1] = u * s + v * a.c[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+            const float v = __shfl_sync(0xffffffffu, x[i], other), w = __shfl_sync(0xffffffffu, x[i + 1], other);
+            const uint64_t s = BACK ? f2_pack(-a.s[i], -a.s[i + 1]) : f2_pack(a.s[i], a.s[i + 1]);
+            const uint64_t y = f2_mul(f2_pack(v, w), s);
+            f2_unpack(f2_fma(f2_pack(x[i], x[i + 1]), f2_pack(a.c[i], a.c[i + 1]), y), x[i], x[i + 1]);
+        }
+    }
+}
+
+// This lane's place in its head (at), its head among the warp's (group), and its partner for the half layout.
+template <int E, int L> struct Place {
+    int lane, at, group, other;
+    __device__ __forceinline__ explicit Place(int rot) {
+        lane = threadIdx.x & 31;
+        at = lane % L * E;
+        group = lane / L;
+        other = at >= rot ? lane : at < rot / 2 ? lane + rot / 2 / E : lane - rot / 2 / E;
+    }
+};
+
+template <typename T, int E> __device__ __forceinline__ void load_gamma(float (&f)[E], const void* gamma, int at) {
+#pragma unroll
+    for (int i = 0; i < E; i++) f[i] = 1.f;
+    if (!gamma) return;
+    Raw<T, E> r;
+    load_raw(r, (const T*)gamma + at);
+    unpack(r, f);
+}
+
+template <typename T, int E, int L, bool PAIRS, bool NORM>
+__global__ void __launch_bounds__(WARPS * 32) rotary_forward_kernel(const RotaryArgs a) {
+    constexpr int HD = E * L, GROUPS = 32 / L, U = 3;
+    __shared__ float share[WARPS][2][MOST_PAIRS];
+    const Place<E, L> me(a.rot);
+    int64_t row = (int64_t)blockIdx.x * WARPS + threadIdx.x / 32;
+    int next = a.rot && row < a.N ? a.pos[row] : 0;
+    for (; row < a.N; row += (int64_t)gridDim.x * WARPS) {
+        const int pos = next;
+        if (a.rot && row + (int64_t)gridDim.x * WARPS < a.N) next = a.pos[row + (int64_t)gridDim.x * WARPS];
+        Raw<T, E> raw[U];
+        auto load = [&](int H, const T* x, int h0) {
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                const int h = h0 + u * GROUPS + me.group;
+                raw[u] = {};
+                if (h < H) load_raw(raw[u], x + h * HD);
+            }
+        };
+        const T* q = (const T*)a.q + row * a.q_stride + me.at;
+        load(a.Hq, q, 0);  // under way while the angles are formed
+        Angles<E, PAIRS> ang;
+        ang.of(pos, a.turns, me.at, a.rot, a.amplitude, share[threadIdx.x / 32]);
+        auto heads = [&](int H, const T* x, T* y, const void* weight, bool loaded) {
+            float gamma[E];  // (from the cache for each row: it would hold registers over the other heads)
+            if (NORM) load_gamma<T>(gamma, weight, me.at);
+            for (int h0 = 0; h0 < H; h0 += GROUPS * U) {
+                if (h0 || !loaded) load(H, x, h0);
+#pragma unroll
+                for (int u = 0; u < U; u++) {
+                    const int h = h0 + u * GROUPS + me.group;
+                    if (h0 + u * GROUPS >= H) break;
+                    float f[E];
+                    unpack(raw[u], f);
+                    if (NORM) {
+                        times(f, rsqrtf(head_sum<L>(dot(f, f)) * (1.f / HD) + a.eps));
+                        times(f, gamma);
+                    }
+                    rotate<E, PAIRS, false>(f, ang, me.other);
+                    if (h < H) store_e(y + h * HD, f);
+                }
+            }
+        };
+        heads(a.Hq, q, (T*)a.qo + row * a.qo_stride + me.at, a.q_gamma, true);
+        heads(a.Hk, (const T*)a.k + row * a.k_stride + me.at, (T*)a.ko + row * a.ko_stride + me.at, a.k_gamma, false);
     }
 }
 
@@ -156,121 +232,144 @@ __global__ void __launch_bounds__(THREADS) rotary_forward_kernel(const RotaryArg
 // registers over all its rows; block sums go to partial [block][2][HD], which
 // a column sum adds in a fixed order.
 template <typename T, int E, int L, bool PAIRS, bool NORM>
-__global__ void __launch_bounds__(THREADS) rotary_backward_kernel(const RotaryArgs a, float* __restrict__ partial) {
-    constexpr int HD = E * L, GROUPS = 32 / L;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, at = lane % L * E, group = lane / L;
-    float gq[E], gk[E], aq[E], ak[E];
+__global__ void __launch_bounds__(WARPS * 32, BACK_A_SM) rotary_backward_kernel(const RotaryArgs a, float* __restrict__ partial) {
+    constexpr int HD = E * L, GROUPS = 32 / L, U = 2;
+    __shared__ float share[WARPS][2][MOST_PAIRS];
+    const Place<E, L> me(a.rot);
+    const int warp = threadIdx.x / 32;
+    float aq[E], ak[E];
 #pragma unroll
-    for (int i = 0; i < E; i++) {
-        gq[i] = gk[i] = 1.f;
-        aq[i] = ak[i] = 0.f;
-    }
-    if (NORM && a.q_gamma) load_e((const T*)a.q_gamma + at, gq);
-    if (NORM && a.k_gamma) load_e((const T*)a.k_gamma + at, gk);
-    for (int64_t row = (int64_t)blockIdx.x * WARPS + warp; row < a.N; row += (int64_t)gridDim.x * WARPS) {
-        Angles<E, PAIRS> ang;
-        ang.of(a.pos[row], a.turns, at, a.rot, a.amplitude);
-        auto heads = [&](int H, const T* dy, const T* x, T* dx, const float (&gamma)[E], float (&acc)[E]) {
-#pragma unroll 2
-            for (int h0 = 0; h0 < H; h0 += GROUPS) {
-                const int h = h0 + group;
-                float d[E], v[E];
+    for (int i = 0; i < E; i++) aq[i] = ak[i] = 0.f;
+    int64_t row = (int64_t)blockIdx.x * WARPS + warp;
+    int next = a.rot && row < a.N ? a.pos[row] : 0;
+    for (; row < a.N; row += (int64_t)gridDim.x * WARPS) {
+        const int pos = next;
+        if (a.rot && row + (int64_t)gridDim.x * WARPS < a.N) next = a.pos[row + (int64_t)gridDim.x * WARPS];
+        Raw<T, E> rd[U], rx[U];
+        auto load = [&](int H, const T* dy, const T* x, int h0) {
 #pragma unroll
-                for (int i = 0; i < E; i++) d[i] = v[i] = 0.f;
+            for (int u = 0; u < U; u++) {
+                const int h = h0 + u * GROUPS + me.group;
+                rd[u] = rx[u] = {};
                 if (h < H) {
-                    load_e(dy + h * HD, d);
-                    if (NORM) load_e(x + h * HD, v);
+                    load_raw(rd[u], dy + h * HD);
+                    if (NORM) load_raw(rx[u], x + h * HD);
                 }
-                rotate<E, PAIRS>(d, ang, at, a.rot, -1.f);
-                if (NORM) {
-                    float ss = 0.f, in = 0.f;
-#pragma unroll
-                    for (int i = 0; i < E; i++) ss += v[i] * v[i];
-                    const float r = 1.f / sqrtf(head_sum<L>(ss) * (1.f / HD) + a.eps);
-#pragma unroll
-                    for (int i = 0; i < E; i++) {
-                        v[i] *= r;
-                        acc[i] += d[i] * v[i];
-                        d[i] *= gamma[i];
-                        in += d[i] * v[i];
-                    }
-                    in = head_sum<L>(in) * (1.f / HD);
-#pragma unroll
-                    for (int i = 0; i < E; i++) d[i] = r * (d[i] - v[i] * in);
-                }
-                if (h < H) store_e(dx + h * HD, d);
             }
         };
-        heads(a.Hq, (const T*)a.dqo + row * a.dqo_stride + at, (const T*)a.q + row * a.q_stride + at,
-              (T*)a.qo + row * a.qo_stride + at, gq, aq);
-        heads(a.Hk, (const T*)a.dko + row * a.dko_stride + at, (const T*)a.k + row * a.k_stride + at,
-              (T*)a.ko + row * a.ko_stride + at, gk, ak);
+        const T *dqo = (const T*)a.dqo + row * a.dqo_stride + me.at, *q = (const T*)a.q + row * a.q_stride + me.at;
+        load(a.Hq, dqo, q, 0);  // under way while the angles are formed
+        Angles<E, PAIRS> ang;
+        ang.of(pos, a.turns, me.at, a.rot, a.amplitude, share[warp]);
+        auto heads = [&](int H, const T* dy, const T* x, T* dx, const void* weight, float (&acc)[E], bool loaded) {
+            float gamma[E];
+            if (NORM) load_gamma<T>(gamma, weight, me.at);
+            for (int h0 = 0; h0 < H; h0 += GROUPS * U) {
+                if (h0 || !loaded) load(H, dy, x, h0);
+#pragma unroll
+                for (int u = 0; u < U; u++) {
+                    const int h = h0 + u * GROUPS + me.group;
+                    if (h0 + u * GROUPS >= H) break;
+                    float d[E];
+                    unpack(rd[u], d);
+                    rotate<E, PAIRS, true>(d, ang, me.other);
+                    if (NORM) {
+                        float v[E];
+                        unpack(rx[u], v);
+                        const float r = rsqrtf(head_sum<L>(dot(v, v)) * (1.f / HD) + a.eps);
+                        times(v, r);
+#pragma unroll
+                        for (int i = 0; i < E; i += 2)
+                            f2_unpack(f2_fma(f2_pack(d[i], d[i + 1]), f2_pack(v[i], v[i + 1]), f2_pack(acc[i], acc[i + 1])),
+                                      acc[i], acc[i + 1]);
+                        times(d, gamma);
+                        const float in = head_sum<L>(dot(d, v)) * (-1.f / HD);
+                        const uint64_t in2 = f2_pack(in, in), r2 = f2_pack(r, r);
+#pragma unroll
+                        for (int i = 0; i < E; i += 2)
+                            f2_unpack(f2_mul(f2_fma(f2_pack(v[i], v[i + 1]), in2, f2_pack(d[i], d[i + 1])), r2), d[i],
+                                      d[i + 1]);
+                    }
+                    if (h < H) store_e(dx + h * HD, d);
+                }
+            }
+        };
+        heads(a.Hq, dqo, q, (T*)a.qo + row * a.qo_stride + me.at, a.q_gamma, aq, true);
+        heads(a.Hk, (const T*)a.dko + row * a.dko_stride + me.at, (const T*)a.k + row * a.k_stride + me.at,
+              (T*)a.ko + row * a.ko_stride + me.at, a.k_gamma, ak, false);
     }
     if constexpr (NORM) {
-    if (!partial) return;
-    __shared__ float sm[WARPS][2][HD];
+        if (!partial) return;
+        __shared__ float sm[WARPS][2][HD];
 #pragma unroll
-    for (int i = 0; i < E; i++) {
+        for (int i = 0; i < E; i++) {
 #pragma unroll
-        for (int o = L; o < 32; o <<= 1) {
-            aq[i] += __shfl_xor_sync(0xffffffffu, aq[i], o);
-            ak[i] += __shfl_xor_sync(0xffffffffu, ak[i], o);
+            for (int o = L; o < 32; o <<= 1) {
+                aq[i] += __shfl_xor_sync(0xffffffffu, aq[i], o);
+                ak[i] += __shfl_xor_sync(0xffffffffu, ak[i], o);
+            }
+            if (me.group == 0) {
+                sm[warp][0][me.at + i] = aq[i];
+                sm[warp][1][me.at + i] = ak[i];
+            }
         }
-        if (group == 0) {
-            sm[warp][0][at + i] = aq[i];
-            sm[warp][1][at + i] = ak[i];
-        }
-    }
-    __syncthreads();
-    for (int c = threadIdx.x; c < 2 * HD; c += THREADS) {
-        float t = 0.f;
+        __syncthreads();
+        for (int c = threadIdx.x; c < 2 * HD; c += WARPS * 32) {
+            float t = 0.f;
 #pragma unroll
-        for (int w = 0; w < WARPS; w++) t += sm[w][c / HD][c % HD];
-        partial[(int64_t)blockIdx.x * 2 * HD + c] = t;
-    }
+            for (int w = 0; w < WARPS; w++) t += sm[w][c / HD][c % HD];
+            partial[(int64_t)blockIdx.x * 2 * HD + c] = t;
+        }
     }
 }
 
-int rotary_blocks(int N) {
-    const int64_t rows = ((int64_t)N + WARPS - 1) / WARPS, most = (int64_t)gpt2_num_sms() * 8;
+// Blocks for N rows of one warp each, as many as stay resident.
+int blocks_for(int N, int warps, int a_sm) {
+    const int64_t rows = ((int64_t)N + warps - 1) / warps, most = (int64_t)gpt2_num_sms() * a_sm;
     return (int)(rows < most ? rows : most);
 }
+int forward_blocks(int N) { return blocks_for(N, WARPS, 8); }
+int backward_blocks(int N) { return blocks_for(N, WARPS, BACK_A_SM); }
 
 template <typename T, int E, int L, bool PAIRS, bool NORM>
-int start(const RotaryArgs& a, bool back, float* partial, cudaStream_t s) {
-    const int blocks = rotary_blocks(a.N);
-    if (back) rotary_backward_kernel<T, E, L, PAIRS, NORM><<<blocks, THREADS, 0, s>>>(a, partial);
-    else rotary_forward_kernel<T, E, L, PAIRS, NORM><<<blocks, THREADS, 0, s>>>(a);
-    return blocks;
+void start(const RotaryArgs& a, bool back, float* partial, cudaStream_t s) {
+    if (back)
+        rotary_backward_kernel<T, E, L, PAIRS, NORM><<<backward_blocks(a.N), WARPS * 32, 0, s>>>(a, partial);
+    else rotary_forward_kernel<T, E, L, PAIRS, NORM><<<forward_blocks(a.N), WARPS * 32, 0, s>>>(a);
 }
 
-template <typename T, int E, int L>
-int start(const RotaryArgs& a, bool back, float* partial, cudaStream_t s) {
-    if (a.interleaved)
-        return a.norm ? start<T, E, L, true, true>(a, back, partial, s) : start<T, E, L, true, false>(a, back, partial, s);
-    return a.norm ? start<T, E, L, false, true>(a, back, partial, s) : start<T, E, L, false, false>(a, back, partial, s);
+template <typename T, int E, int L> void start(const RotaryArgs& a, bool back, float* partial, cudaStream_t s) {
+    if (a.interleaved) {
+        if (a.norm) start<T, E, L, true, true>(a, back, partial, s);
+        else start<T, E, L, true, false>(a, back, partial, s);
+    } else {
+        if (a.norm) start<T, E, L, false, true>(a, back, partial, s);
+        else start<T, E, L, false, false>(a, back, partial, s);
+    }
 }
 
-template <typename T>
-int start(const RotaryArgs& a, bool back, float* partial, cudaStream_t s) {
-    switch (a.hd) {
-        case 8: return start<T, 4, 2>(a, back, partial, s);
-        case 16: return start<T, 4, 4>(a, back, partial, s);
-        case 32: return start<T, 4, 8>(a, back, partial, s);
-        case 64: return start<T, 4, 16>(a, back, partial, s);
-        default: return start<T, 4, 32>(a, back, partial, s);
+// E values a lane: rot (and in the half layout rot / 2) has to be a multiple of them.
+template <typename T, int E> void start(const RotaryArgs& a, bool back, float* partial, cudaStream_t s) {
+    switch (a.hd / E) {
+        case 2: return start<T, E, 2>(a, back, partial, s);
+        case 4: return start<T, E, 4>(a, back, partial, s);
+        case 8: return start<T, E, 8>(a, back, partial, s);
+        case 16: return start<T, E, 16>(a, back, partial, s);
+        case 32: if constexpr (E == 4) return start<T, E, 32>(a, back, partial, s);
     }
 }
 
 }  // namespace
 
-size_t rotary_backward_scratch(int N, int hd) { return (size_t)rotary_blocks(N) * 2 * hd * 4; }
+size_t rotary_backward_scratch(int N, int hd) { return (size_t)backward_blocks(N) * 2 * hd * 4; }
 
 int launch_rotary(int dtype, const RotaryArgs& a, bool back, float* dq_gamma, float* dk_gamma, void* scratch,
                   cudaStream_t s) {
     float* partial = back && a.norm && (dq_gamma || dk_gamma) ? (float*)scratch : nullptr;
-    const int blocks = dtype == GPT2_MODE_BF16 ? start<bf16>(a, back, partial, s) : start<float>(a, back, partial, s);
+    if (dtype != GPT2_MODE_BF16) start<float, 4>(a, back, partial, s);
+    else if (a.hd >= 16 && a.rot % (a.interleaved ? 8 : 16) == 0) start<bf16, 8>(a, back, partial, s);
+    else start<bf16, 4>(a, back, partial, s);
     if (!partial) return 1;
-    ColsumJob job = {partial, {dq_gamma, dk_gamma, nullptr}, blocks, 2 * a.hd, a.hd, 0};
+    ColsumJob job = {partial, {dq_gamma, dk_gamma, nullptr}, backward_blocks(a.N), 2 * a.hd, a.hd, 0};
     return 1 + launch_colsum_jobs(&job, 1, s);
 }
