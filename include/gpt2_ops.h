@@ -465,7 +465,7 @@ int gpt2_rotary_turns(uint64_t* turns, int rot, double base, int scaling, double
  * Rows of x are independent; a row with a logit that is not finite gets NaN.
  * C % 8 == 0, C >= 8, V >= 1, x and w 16-byte aligned, N * C and V * C below
  * 2^31 - 2048; N = 0 launches nothing. Scratch: row statistics of the
- * vocabulary's tiles (fp32: also the logits of a piece of the vocabulary). */
+ * vocabulary's tiles. */
 size_t gpt2_op_linear_classifier_forward_scratch(int dtype, int N, int C, int V);
 int gpt2_op_linear_classifier_forward(int dtype, float* losses, float* lse, const void* x, const void* w,
                                       const int32_t* targets, int N, int C, int V, void* scratch,

@@ -15,7 +15,7 @@
 // copies that store them (one writer for each value in a launch, so the order
 // is fixed).
 //
-// fp32: the same with the fp32 matmul and the logits of a piece in scratch.
+// fp32: the same with products of fp32 FMA (classifier_linear_f32.cu).
 #include "common.cuh"
 #include "launch.h"
 
@@ -88,44 +88,6 @@ __global__ void __launch_bounds__(STRANDS * 32) join_kernel(float* __restrict__ 
     losses[row] = loss < 0.f ? 0.f : loss;
 }
 
-// fp32: a row's maximum and sum over a piece of the logits, and its target's logit. One warp a row.
-__global__ void __launch_bounds__(256) piece_stats_kernel(float2* __restrict__ stats, float* __restrict__ target_logit,
-                                                          const float* __restrict__ z,
-                                                          const int32_t* __restrict__ targets, int N, int cols,
-                                                          int first, int V) {
-    const int lane = threadIdx.x % 32;
-    const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
-    if (row >= N) return;
-    const float* p = z + row * cols;
-    float m = -INFINITY;
-    for (int i = lane; i < cols; i += 32) m = fmaxf(m, p[i]);
-    m = warp_max(m);
-    float s = 0.f;
-    for (int i = lane; i < cols; i += 32) s += expf(p[i] - m);
-    s = warp_sum(s);
-    if (lane) return;
-    stats[row] = make_float2(m, s);
-    int t = targets[row];
-    if (t < 0 || t >= V) t = 0;
-    if (t >= first && t < first + cols) target_logit[row] = p[t - first];
-}
-
-// fp32: a piece of the logits becomes its gradient.
-__global__ void __launch_bounds__(256) piece_dz_kernel(float* __restrict__ z, const int32_t* __restrict__ targets,
-                                                       const float* __restrict__ lse, const float* __restrict__ dloss,
-                                                       const float* __restrict__ dlse, int N, int cols, int first,
-                                                       int V) {
-    const int64_t row = blockIdx.y;
-    int t = targets[row];
-    if (t < 0 || t >= V) t = 0;
-    const float d = dloss ? dloss[row] : 0.f, a = d + (dlse ? dlse[row] : 0.f), l = lse[row];
-    for (int j = blockIdx.x * 256 + threadIdx.x; j < cols; j += gridDim.x * 256) {
-        float* p = z + row * cols + j;
-        const float e = a != 0.f || d != 0.f ? a * expf(*p - l) : 0.f;
-        *p = e - (first + j == t ? d : 0.f);
-    }
-}
-
 __global__ void __launch_bounds__(256) round_kernel(bf16* __restrict__ out, const float* __restrict__ in, int64_t n) {
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
     if (i >= n) return;
@@ -143,74 +105,65 @@ __global__ void __launch_bounds__(256) check_targets_kernel(const int32_t* __res
 
 }  // namespace
 
-// stats, target logits, fp32: a piece of the logits.
+// Statistics, target logits.
 size_t linear_classifier_forward_scratch(int dtype, int N, int C, int V) {
-    const bool bf = dtype == GPT2_MODE_BF16;
-    const Pieces p = pieces(dtype, N, V);
-    const int slots = bf ? head_lse_slots(N, V, C) : p.n;
-    return round256((size_t)slots * N * 8) + round256((size_t)N * 4) + (bf ? 0 : (size_t)N * p.width * 4);
+    const int slots = dtype == GPT2_MODE_BF16 ? head_lse_slots(N, V, C) : head_f32_slots(V);
+    return round256((size_t)slots * N * 8) + (size_t)N * 4;
 }
 
 int launch_linear_classifier_forward(int dtype, float* losses, float* lse, const void* x, const void* w,
                                      const int32_t* targets, int N, int C, int V, void* scratch, int* status,
                                      cudaStream_t s) {
     const bool bf = dtype == GPT2_MODE_BF16;
-    const Pieces p = pieces(dtype, N, V);
-    const int slots = bf ? head_lse_slots(N, V, C) : p.n;
-    float2* stats = (float2*)scratch;
-    float* target_logit = (float*)((char*)scratch + round256((size_t)slots * N * 8));
-    int launches = 0;
-    if (bf) {
-        HeadEpi e = {};
-        e.targets = targets;
-        e.stats = stats;
-        e.target_logit = target_logit;
-        e.vocab = V;
-        const int n = launch_head_lse(x, w, N, V, C, e, status, s);
-        if (n < 0) return n;
-        launches += n;
-    } else {
-        float* z = (float*)((char*)target_logit + round256((size_t)N * 4));
-        for (int i = 0; i < p.n; i++) {
-            const int v0 = i * p.width, cols = V - v0 < p.width ? V - v0 : p.width;
-            const int n = launch_matmul(dtype, z, 1, x, 0, (const float*)w + (int64_t)v0 * C, 0, nullptr, N, cols, C,
-                                        nullptr, status, s);
-            if (n < 0) return n;
-            piece_stats_kernel<<<(N + 7) / 8, 256, 0, s>>>(stats + (int64_t)i * N, target_logit, z, targets, N, cols,
-                                                           v0, V);
-            launches += n + 1;
-        }
-    }
+    const int slots = bf ? head_lse_slots(N, V, C) : head_f32_slots(V);
+    HeadEpi e = {};
+    e.targets = targets;
+    e.stats = (float2*)scratch;
+    e.target_logit = (float*)((char*)scratch + round256((size_t)slots * N * 8));
+    e.vocab = V;
+    const int n = bf ? launch_head_lse(x, w, N, V, C, e, status, s)
+                     : launch_head_f32_lse((const float*)x, (const float*)w, N, V, C, e, s);
+    if (n < 0) return n;
     const int blocks = (N + 31) / 32;
     if (blocks >= 4 * gpt2_num_sms())
-        join_kernel<8, 8><<<blocks, 256, 0, s>>>(losses, lse, stats, target_logit, targets, N, V, slots, status);
-    else join_kernel<32, 4><<<blocks, 1024, 0, s>>>(losses, lse, stats, target_logit, targets, N, V, slots, status);
-    return launches + 1;
+        join_kernel<8, 8><<<blocks, 256, 0, s>>>(losses, lse, e.stats, e.target_logit, targets, N, V, slots, status);
+    else
+        join_kernel<32, 4><<<blocks, 1024, 0, s>>>(losses, lse, e.stats, e.target_logit, targets, N, V, slots, status);
+    return n + 1;
 }
 
 namespace {
 
-// The matmuls' own scratch (split products), over the pieces.
-size_t products_scratch(int N, int C, int V, int dw_fp32, int accumulate, const Pieces& p) {
+// The products' own scratch (parts of split products), over the pieces.
+size_t products_scratch(int dtype, int N, int C, int V, int dw_fp32, int accumulate, const Pieces& p) {
+    const bool bf = dtype == GPT2_MODE_BF16;
     size_t most = 0;
     for (int v0 : {0, (p.n - 1) * p.width}) {
-        const int cols = round8(V - v0 < p.width ? V - v0 : p.width);
-        const size_t a = head_dx_scratch(N, C, cols);
-        const size_t b = matmul_scratch(GPT2_MODE_BF16, cols, C, N, dw_fp32, accumulate);
+        const int cols = V - v0 < p.width ? V - v0 : p.width, pitch = bf ? round8(cols) : cols;
+        const size_t a = bf ? head_dx_scratch(N, C, pitch) : head_f32_scratch(N, C, cols);
+        const size_t b = bf ? matmul_scratch(dtype, pitch, C, N, dw_fp32, accumulate) : head_f32_scratch(cols, C, N);
         most = a > most ? a : most;
         most = b > most ? b : most;
     }
     return most;
 }
 
+// A piece of dz; bf16: dx in fp32; the products' own.
+struct BackwardScratch {
+    size_t dz, dx, own;
+    BackwardScratch(int dtype, int N, int C, const Pieces& p) {
+        const bool bf = dtype == GPT2_MODE_BF16;
+        dz = 0;
+        dx = round256((size_t)N * p.width * (bf ? 2 : 4));
+        own = dx + (bf ? round256((size_t)N * C * 4) : 0);
+    }
+};
+
 }  // namespace
 
-// A piece of dz; bf16: dx in fp32, the products' own.
 size_t linear_classifier_backward_scratch(int dtype, int N, int C, int V, int dw_fp32, int accumulate) {
     const Pieces p = pieces(dtype, N, V);
-    if (dtype != GPT2_MODE_BF16) return (size_t)N * p.width * 4;
-    return round256((size_t)N * p.width * 2) + round256((size_t)N * C * 4) +
-           products_scratch(N, C, V, dw_fp32, accumulate, p);
+    return BackwardScratch(dtype, N, C, p).own + products_scratch(dtype, N, C, V, dw_fp32, accumulate, p);
 }
 
 int launch_linear_classifier_backward(int dtype, void* dx, void* dw, int dw_fp32, int accumulate, const void* x,
@@ -219,6 +172,10 @@ int launch_linear_classifier_backward(int dtype, void* dx, void* dw, int dw_fp32
                                       cudaStream_t s) {
     const bool bf = dtype == GPT2_MODE_BF16;
     const Pieces p = pieces(dtype, N, V);
+    const BackwardScratch at(dtype, N, C, p);
+    void* dz = (char*)scratch + at.dz;
+    float* sum = (float*)((char*)scratch + at.dx);
+    void* own = (char*)scratch + at.own;
     int launches = 0;
     const int64_t es = dw_fp32 ? 4 : 2, done = bf ? round8(V) : V;
     if (!accumulate && done < Vp &&
@@ -228,40 +185,28 @@ int launch_linear_classifier_backward(int dtype, void* dx, void* dw, int dw_fp32
         check_targets_kernel<<<(N + 255) / 256, 256, 0, s>>>(targets, N, V, status);
         launches++;
     }
-    float* sum = (float*)((char*)scratch + round256((size_t)N * p.width * 2));
-    void* own = (char*)sum + round256((size_t)N * C * 4);
+    HeadEpi e = {};
+    e.targets = targets;
+    e.lse = lse;
+    e.dloss = dloss;
+    e.dlse = dlse;
+    e.vocab = V;
     for (int i = 0; i < p.n; i++) {
         const int v0 = i * p.width, cols = V - v0 < p.width ? V - v0 : p.width;
-        int n[3] = {0, 0, 0};
+        e.first = v0;
+        int n[3];
         if (bf) {
             const bf16* wp = (const bf16*)w + (int64_t)v0 * C;
             const int pitch = round8(cols);
-            HeadEpi e = {};
-            e.targets = targets;
-            e.lse = lse;
-            e.dloss = dloss;
-            e.dlse = dlse;
-            e.vocab = V;
-            e.first = v0;
-            n[0] = launch_head_dz(scratch, x, wp, N, pitch, C, cols, e, status, s);
-            n[1] = launch_head_dx(sum, scratch, wp, N, C, pitch, cols, i > 0, own, status, s);
-            n[2] = launch_matmul(dtype, (char*)dw + (int64_t)v0 * C * es, dw_fp32, scratch, 1, x, 1, nullptr, pitch, C, N,
-                                 own, status, s, accumulate);
+            n[0] = launch_head_dz(dz, x, wp, N, pitch, C, cols, e, status, s);
+            n[1] = launch_head_dx(sum, dz, wp, N, C, pitch, cols, i > 0, own, status, s);
+            n[2] = launch_matmul(dtype, (char*)dw + (int64_t)v0 * C * es, dw_fp32, dz, 1, x, 1, nullptr, pitch, C, N, own,
+                                 status, s, accumulate);
         } else {
-            float* z = (float*)scratch;
-            const float* wp = (const float*)w + (int64_t)v0 * C;
-            n[0] = launch_matmul(dtype, z, 1, x, 0, wp, 0, nullptr, N, cols, C, nullptr, status, s);
-            const int wide = (cols + 255) / 256;
-            for (int r0 = 0; r0 < N; r0 += 65535) {
-                const int rows = N - r0 < 65535 ? N - r0 : 65535;
-                piece_dz_kernel<<<dim3(wide < 64 ? wide : 64, rows), 256, 0, s>>>(
-                    z + (int64_t)r0 * cols, targets + r0, lse + r0, dloss ? dloss + r0 : nullptr,
-                    dlse ? dlse + r0 : nullptr, rows, cols, v0, V);
-                launches++;
-            }
-            n[1] = launch_matmul(dtype, dx, 1, z, 0, wp, 1, nullptr, N, C, cols, nullptr, status, s, i > 0);
-            n[2] = launch_matmul(dtype, (float*)dw + (int64_t)v0 * C, 1, z, 1, x, 1, nullptr, cols, C, N, nullptr, status,
-                                 s, accumulate);
+            const float *xf = (const float*)x, *wp = (const float*)w + (int64_t)v0 * C;
+            n[0] = launch_head_f32_dz((float*)dz, xf, wp, N, cols, C, e, s);
+            n[1] = launch_head_f32_dx((float*)dx, (const float*)dz, wp, N, C, cols, i > 0, own, s);
+            n[2] = launch_head_f32_dw((float*)dw + (int64_t)v0 * C, (const float*)dz, xf, cols, C, N, accumulate, own, s);
         }
         for (int k = 0; k < 3; k++) {
             if (n[k] < 0) return n[k];

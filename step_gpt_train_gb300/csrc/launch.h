@@ -192,6 +192,17 @@ size_t head_dx_scratch(int M, int N, int K);
 int launch_head_dx(float* dx, const void* dz, const void* w, int M, int N, int K, int rows, bool add, void* scratch,
                    int* status, cudaStream_t s);
 
+// The same in fp32 (classifier_linear_f32.cu): statistics in head_f32_slots(V) slots, dz [M, N], dx [M, N] = or +=
+// dz [M, K] W [K, N], dw [M, N] = or += dz^T x with dz [K, M], x [K, N]; scratch for the two: head_f32_scratch(M, N, K).
+int head_f32_slots(int V);
+int launch_head_f32_lse(const float* x, const float* w, int M, int N, int K, const HeadEpi& e, cudaStream_t s);
+int launch_head_f32_dz(float* dz, const float* x, const float* w, int M, int N, int K, const HeadEpi& e, cudaStream_t s);
+size_t head_f32_scratch(int M, int N, int K);
+int launch_head_f32_dx(float* dx, const float* dz, const float* w, int M, int N, int K, bool add, void* scratch,
+                       cudaStream_t s);
+int launch_head_f32_dw(float* dw, const float* dz, const float* x, int M, int N, int K, bool add, void* scratch,
+                       cudaStream_t s);
+
 // Softmax cross entropy of x W^T without the logits (gpt2_op_linear_classifier_*): validated arguments.
 size_t linear_classifier_forward_scratch(int dtype, int N, int C, int V);
 int launch_linear_classifier_forward(int dtype, float* losses, float* lse, const void* x, const void* w,

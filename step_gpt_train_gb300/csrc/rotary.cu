@@ -27,34 +27,25 @@
 
 namespace {
 
-using tc::f2_add;
 using tc::f2_fma;
 using tc::f2_mul;
 using tc::f2_pack;
 using tc::f2_unpack;
 
-constexpr int WARPS = 8;  // a block's
+// A block's warps, the blocks on an SM and the steps whose copies are in flight. At 32768 rows of 24 heads of 64
+// (bf16, with norms): three blocks of the forward 37.3 us, two 41.0, four 41.0 (64 registers: spills); two blocks of
+// the backward 54.4, one 69.7, three 63.3 (80 registers). From two steps ahead to eight: within 1 us.
+constexpr int WARPS = 8;
+constexpr int FORWARD_A_SM = 3, BACKWARD_A_SM = 2;
+constexpr int AHEAD = 4;
 constexpr int MOST_PAIRS = 64;
-constexpr int BACK_A_SM = 3;  // blocks of the backward on an SM
 
 // E values of T as loaded, and as fp32.
 template <typename T, int E> struct Raw;
-template <> struct Raw<bf16, 8> { uint32_t w[4]; };
-template <> struct Raw<bf16, 4> { uint32_t w[2]; };
-template <> struct Raw<float, 4> { uint32_t w[4]; };
+template <> struct __align__(16) Raw<bf16, 8> { uint32_t w[4]; };
+template <> struct __align__(8) Raw<bf16, 4> { uint32_t w[2]; };
+template <> struct __align__(16) Raw<float, 4> { uint32_t w[4]; };
 
-__device__ __forceinline__ void load_raw(Raw<bf16, 8>& r, const bf16* p) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    r.w[0] = u.x, r.w[1] = u.y, r.w[2] = u.z, r.w[3] = u.w;
-}
-__device__ __forceinline__ void load_raw(Raw<bf16, 4>& r, const bf16* p) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    r.w[0] = u.x, r.w[1] = u.y;
-}
-__device__ __forceinline__ void load_raw(Raw<float, 4>& r, const float* p) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    r.w[0] = u.x, r.w[1] = u.y, r.w[2] = u.z, r.w[3] = u.w;
-}
 template <int E> __device__ __forceinline__ void unpack(const Raw<bf16, E>& r, float (&f)[E]) {
 #pragma unroll
     for (int i = 0; i < E / 2; i++) {
@@ -106,33 +97,54 @@ template <int L> __device__ __forceinline__ float head_sum(float v) {
     return v;
 }
 
-// cos and sin, times the amplitude, of the pairs that this lane's values belong
-// to: one for each value in the half layout (sin with the sign that turns the
-// other value into this one's share: y = c x + s x_other), one for each two in
-// the interleaved one. Values behind rot get 1 and 0. share: a warp's cos and sin.
+// A warp's cos, sin and -sin of a row's pairs, times the amplitude, and behind them 1 and 0 for values that are not
+// rotated.
+struct Shared {
+    __align__(16) float cos[MOST_PAIRS + 8], sin[2][MOST_PAIRS + 8];
+};
+
+template <int N> __device__ __forceinline__ void load_shared(float (&f)[N], const float* p) {
+    if (N == 2) {
+        const float2 v = *reinterpret_cast<const float2*>(p);
+        f[0] = v.x, f[1] = v.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(p + i);
+            f[i] = v.x, f[i + 1] = v.y, f[i + 2] = v.z, f[i + 3] = v.w;
+        }
+    }
+}
+
+// Those of the pairs that this lane's values belong to: one for each value in the half layout (sin with the sign that
+// turns the other value into this one's share: y = c x + s x_other), one for each two in the interleaved one.
 template <int E, bool PAIRS> struct Angles {
     static constexpr int N = PAIRS ? E / 2 : E;
     float c[N], s[N];
 
-    __device__ __forceinline__ void of(int pos, const uint64_t* turns, int at, int rot, float amplitude,
-                                       float (&share)[2][MOST_PAIRS]) {
+    static __device__ __forceinline__ void begin(Shared& w) {
+        const int lane = threadIdx.x & 31;
+        if (lane < 8) {
+            w.cos[MOST_PAIRS + lane] = 1.f;
+            w.sin[0][MOST_PAIRS + lane] = w.sin[1][MOST_PAIRS + lane] = 0.f;
+        }
+    }
+    __device__ __forceinline__ void of(int pos, const uint64_t* turns, int at, int rot, float amplitude, Shared& w) {
         const int half = rot / 2, lane = threadIdx.x & 31;
         __syncwarp();  // the row before has read its angles
         for (int j = lane; j < half; j += 32) {
             const uint64_t t = (uint64_t)(int64_t)pos * turns[j];
             float sn, cs;
             sincospif((float)(int32_t)(t >> 32) * 0x1p-31f, &sn, &cs);
-            share[0][j] = cs * amplitude;
-            share[1][j] = sn * amplitude;
+            w.cos[j] = cs * amplitude;
+            w.sin[0][j] = sn * amplitude;
+            w.sin[1][j] = -sn * amplitude;
         }
         __syncwarp();
-        const bool first = PAIRS || at < half;
-        const int j0 = PAIRS ? at / 2 : first ? at : at - half;
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-            c[i] = at < rot ? share[0][j0 + i] : 1.f;
-            s[i] = at < rot ? (!PAIRS && first ? -share[1][j0 + i] : share[1][j0 + i]) : 0.f;
-        }
+        const bool first = !PAIRS && at < half;
+        const int j0 = at >= rot ? MOST_PAIRS : PAIRS ? at / 2 : first ? at : at - half;
+        load_shared(c, w.cos + j0);
+        load_shared(s, w.sin[first] + j0);
     }
 };
 
@@ -169,60 +181,105 @@ template <int E, int L> struct Place {
     }
 };
 
-template <typename T, int E> __device__ __forceinline__ void load_gamma(float (&f)[E], const void* gamma, int at) {
-#pragma unroll
-    for (int i = 0; i < E; i++) f[i] = 1.f;
-    if (!gamma) return;
-    Raw<T, E> r;
-    load_raw(r, (const T*)gamma + at);
-    unpack(r, f);
+// The norms' weights in fp32 (ones where there are none), for a block.
+template <typename T, int HD>
+__device__ __forceinline__ void load_weights(float (&w)[2][HD], const void* q_gamma, const void* k_gamma) {
+    for (int i = threadIdx.x; i < 2 * HD; i += WARPS * 32) {
+        const T* g = (const T*)(i < HD ? q_gamma : k_gamma);
+        w[i / HD][i % HD] = g ? to_float(g[i % HD]) : 1.f;
+    }
 }
 
+// What a warp walks: its rows, and in each the query heads and then the key heads, a step of GROUPS heads at a time.
+// Sources of one kind (values, or gradients) by their rows' places.
+template <typename T> struct Source {
+    const T *q, *k;
+    int64_t q_step, k_step;
+    __device__ __forceinline__ Source(const void* q0, int64_t q_stride, const void* k0, int64_t k_stride, int64_t row, int at)
+        : q((const T*)q0 + row * q_stride + at), k((const T*)k0 + row * k_stride + at),
+          q_step(q_stride * (int64_t)(gridDim.x * WARPS)), k_step(k_stride * (int64_t)(gridDim.x * WARPS)) {}
+    __device__ __forceinline__ void next() { q += q_step, k += k_step; }
+};
+
+// A lane's vectors of the next DEPTH steps, on their way to its own slots of shared memory: the copies hold no
+// registers, so they run as far ahead as HBM needs them to. A lane reads what it copied itself, so it waits for its
+// own copies only. One slot more than copies in flight: the slot that a copy goes to was read a step ago.
+template <typename T, int E, int DEPTH, int SOURCES> struct Ring {
+    static constexpr int BYTES = E * sizeof(T);
+    static constexpr int SLOTS = DEPTH + 1;
+    char* mine;  // [SLOTS][SOURCES], 32 lanes' vectors apart
+    int at;
+
+    __device__ __forceinline__ void copy(int slot, int source, const T* from) {
+        const uint32_t s = (uint32_t)__cvta_generic_to_shared(mine + (slot * SOURCES + source) * 32 * BYTES);
+        if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(from) : "memory");
+        else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(s), "l"(from) : "memory");
+    }
+    __device__ __forceinline__ Raw<T, E> read(int source) const {
+        return *reinterpret_cast<const Raw<T, E>*>(mine + (at * SOURCES + source) * 32 * BYTES);
+    }
+    __device__ __forceinline__ int ahead() const { return at + DEPTH >= SLOTS ? at + DEPTH - SLOTS : at + DEPTH; }
+    __device__ __forceinline__ void next() { at = at + 1 == SLOTS ? 0 : at + 1; }
+};
+
 template <typename T, int E, int L, bool PAIRS, bool NORM>
-__global__ void __launch_bounds__(WARPS * 32) rotary_forward_kernel(const RotaryArgs a) {
-    constexpr int HD = E * L, GROUPS = 32 / L, U = 3;
-    __shared__ float share[WARPS][2][MOST_PAIRS];
+__global__ void __launch_bounds__(WARPS * 32, FORWARD_A_SM) rotary_forward_kernel(const RotaryArgs a) {
+    constexpr int HD = E * L, GROUPS = 32 / L;
+    using R = Ring<T, E, AHEAD, 1>;
+    __shared__ Shared share[WARPS];
+    __shared__ __align__(16) float weights[2][HD];
+    __shared__ __align__(16) char slots[WARPS][R::SLOTS * 32 * R::BYTES];
     const Place<E, L> me(a.rot);
-    int64_t row = (int64_t)blockIdx.x * WARPS + threadIdx.x / 32;
+    const int warp = threadIdx.x / 32, q_steps = (a.Hq + GROUPS - 1) / GROUPS, steps = q_steps + (a.Hk + GROUPS - 1) / GROUPS;
+    R ring = {slots[warp] + me.lane * R::BYTES, 0};
+    const int64_t stride = (int64_t)gridDim.x * WARPS;
+    int64_t row = (int64_t)blockIdx.x * WARPS + warp, ahead = row;
+    int step = 0;
+    Source<T> from(a.q, a.q_stride, a.k, a.k_stride, row, me.at);
+    auto fetch = [&](int slot) {
+        if (ahead < a.N) {
+            const bool key = step >= q_steps;
+            const int h = (key ? step - q_steps : step) * GROUPS + me.group;
+            if (h < (key ? a.Hk : a.Hq)) ring.copy(slot, 0, (key ? from.k : from.q) + h * HD);
+            if (++step == steps) {
+                step = 0;
+                ahead += stride;
+                from.next();
+            }
+        }
+        cp_async_commit();
+    };
+    if (NORM) load_weights<T>(weights, a.q_gamma, a.k_gamma);
+    Angles<E, PAIRS>::begin(share[warp]);
+    __syncthreads();
+#pragma unroll
+    for (int d = 0; d < AHEAD; d++) fetch(d);
     int next = a.rot && row < a.N ? a.pos[row] : 0;
-    for (; row < a.N; row += (int64_t)gridDim.x * WARPS) {
+    for (; row < a.N; row += stride) {
         const int pos = next;
-        if (a.rot && row + (int64_t)gridDim.x * WARPS < a.N) next = a.pos[row + (int64_t)gridDim.x * WARPS];
-        Raw<T, E> raw[U];
-        auto load = [&](int H, const T* x, int h0) {
-#pragma unroll
-            for (int u = 0; u < U; u++) {
-                const int h = h0 + u * GROUPS + me.group;
-                raw[u] = {};
-                if (h < H) load_raw(raw[u], x + h * HD);
-            }
-        };
-        const T* q = (const T*)a.q + row * a.q_stride + me.at;
-        load(a.Hq, q, 0);  // under way while the angles are formed
+        if (a.rot && row + stride < a.N) next = a.pos[row + stride];
         Angles<E, PAIRS> ang;
-        ang.of(pos, a.turns, me.at, a.rot, a.amplitude, share[threadIdx.x / 32]);
-        auto heads = [&](int H, const T* x, T* y, const void* weight, bool loaded) {
-            float gamma[E];  // (from the cache for each row: it would hold registers over the other heads)
-            if (NORM) load_gamma<T>(gamma, weight, me.at);
-            for (int h0 = 0; h0 < H; h0 += GROUPS * U) {
-                if (h0 || !loaded) load(H, x, h0);
-#pragma unroll
-                for (int u = 0; u < U; u++) {
-                    const int h = h0 + u * GROUPS + me.group;
-                    if (h0 + u * GROUPS >= H) break;
-                    float f[E];
-                    unpack(raw[u], f);
-                    if (NORM) {
-                        times(f, rsqrtf(head_sum<L>(dot(f, f)) * (1.f / HD) + a.eps));
-                        times(f, gamma);
-                    }
-                    rotate<E, PAIRS, false>(f, ang, me.other);
-                    if (h < H) store_e(y + h * HD, f);
+        ang.of(pos, a.turns, me.at, a.rot, a.amplitude, share[warp]);
+        auto heads = [&](int H, T* y, const float* weight) {
+            float gamma[E];
+            if (NORM) load_shared(gamma, weight + me.at);
+            for (int h0 = 0; h0 < H; h0 += GROUPS) {
+                const int h = h0 + me.group;
+                cp_async_wait<AHEAD - 1>();
+                float f[E];
+                unpack(ring.read(0), f);
+                fetch(ring.ahead());
+                ring.next();
+                if (NORM) {
+                    times(f, rsqrtf(head_sum<L>(dot(f, f)) * (1.f / HD) + a.eps));
+                    times(f, gamma);
                 }
+                rotate<E, PAIRS, false>(f, ang, me.other);
+                if (h < H) store_e(y + h * HD, f);
             }
         };
-        heads(a.Hq, q, (T*)a.qo + row * a.qo_stride + me.at, a.q_gamma, true);
-        heads(a.Hk, (const T*)a.k + row * a.k_stride + me.at, (T*)a.ko + row * a.ko_stride + me.at, a.k_gamma, false);
+        heads(a.Hq, (T*)a.qo + row * a.qo_stride + me.at, weights[0]);
+        heads(a.Hk, (T*)a.ko + row * a.ko_stride + me.at, weights[1]);
     }
 }
 
@@ -232,71 +289,84 @@ __global__ void __launch_bounds__(WARPS * 32) rotary_forward_kernel(const Rotary
 // registers over all its rows; block sums go to partial [block][2][HD], which
 // a column sum adds in a fixed order.
 template <typename T, int E, int L, bool PAIRS, bool NORM>
-__global__ void __launch_bounds__(WARPS * 32, BACK_A_SM) rotary_backward_kernel(const RotaryArgs a, float* __restrict__ partial) {
-    constexpr int HD = E * L, GROUPS = 32 / L, U = 2;
-    __shared__ float share[WARPS][2][MOST_PAIRS];
+__global__ void __launch_bounds__(WARPS * 32, BACKWARD_A_SM) rotary_backward_kernel(const RotaryArgs a,
+                                                                               float* __restrict__ partial) {
+    constexpr int HD = E * L, GROUPS = 32 / L, SOURCES = NORM ? 2 : 1;
+    using R = Ring<T, E, AHEAD, SOURCES>;
+    __shared__ Shared share[WARPS];
+    __shared__ __align__(16) float weights[2][HD];
+    __shared__ __align__(16) char slots[WARPS][R::SLOTS * SOURCES * 32 * R::BYTES];
     const Place<E, L> me(a.rot);
-    const int warp = threadIdx.x / 32;
+    const int warp = threadIdx.x / 32, q_steps = (a.Hq + GROUPS - 1) / GROUPS, steps = q_steps + (a.Hk + GROUPS - 1) / GROUPS;
     float aq[E], ak[E];
 #pragma unroll
     for (int i = 0; i < E; i++) aq[i] = ak[i] = 0.f;
-    int64_t row = (int64_t)blockIdx.x * WARPS + warp;
-    int next = a.rot && row < a.N ? a.pos[row] : 0;
-    for (; row < a.N; row += (int64_t)gridDim.x * WARPS) {
-        const int pos = next;
-        if (a.rot && row + (int64_t)gridDim.x * WARPS < a.N) next = a.pos[row + (int64_t)gridDim.x * WARPS];
-        Raw<T, E> rd[U], rx[U];
-        auto load = [&](int H, const T* dy, const T* x, int h0) {
-#pragma unroll
-            for (int u = 0; u < U; u++) {
-                const int h = h0 + u * GROUPS + me.group;
-                rd[u] = rx[u] = {};
-                if (h < H) {
-                    load_raw(rd[u], dy + h * HD);
-                    if (NORM) load_raw(rx[u], x + h * HD);
-                }
+    R ring = {slots[warp] + me.lane * R::BYTES, 0};
+    const int64_t stride = (int64_t)gridDim.x * WARPS;
+    int64_t row = (int64_t)blockIdx.x * WARPS + warp, ahead = row;
+    int step = 0;
+    Source<T> dy(a.dqo, a.dqo_stride, a.dko, a.dko_stride, row, me.at), x(a.q, a.q_stride, a.k, a.k_stride, row, me.at);
+    auto fetch = [&](int slot) {
+        if (ahead < a.N) {
+            const bool key = step >= q_steps;
+            const int h = (key ? step - q_steps : step) * GROUPS + me.group;
+            if (h < (key ? a.Hk : a.Hq)) {
+                ring.copy(slot, 0, (key ? dy.k : dy.q) + h * HD);
+                if (NORM) ring.copy(slot, SOURCES - 1, (key ? x.k : x.q) + h * HD);
             }
-        };
-        const T *dqo = (const T*)a.dqo + row * a.dqo_stride + me.at, *q = (const T*)a.q + row * a.q_stride + me.at;
-        load(a.Hq, dqo, q, 0);  // under way while the angles are formed
+            if (++step == steps) {
+                step = 0;
+                ahead += stride;
+                dy.next();
+                x.next();
+            }
+        }
+        cp_async_commit();
+    };
+    if (NORM) load_weights<T>(weights, a.q_gamma, a.k_gamma);
+    Angles<E, PAIRS>::begin(share[warp]);
+    __syncthreads();
+#pragma unroll
+    for (int d = 0; d < AHEAD; d++) fetch(d);
+    int next = a.rot && row < a.N ? a.pos[row] : 0;
+    for (; row < a.N; row += stride) {
+        const int pos = next;
+        if (a.rot && row + stride < a.N) next = a.pos[row + stride];
         Angles<E, PAIRS> ang;
         ang.of(pos, a.turns, me.at, a.rot, a.amplitude, share[warp]);
-        auto heads = [&](int H, const T* dy, const T* x, T* dx, const void* weight, float (&acc)[E], bool loaded) {
+        auto heads = [&](int H, T* dx, const float* weight, float (&acc)[E]) {
             float gamma[E];
-            if (NORM) load_gamma<T>(gamma, weight, me.at);
-            for (int h0 = 0; h0 < H; h0 += GROUPS * U) {
-                if (h0 || !loaded) load(H, dy, x, h0);
-#pragma unroll
-                for (int u = 0; u < U; u++) {
-                    const int h = h0 + u * GROUPS + me.group;
-                    if (h0 + u * GROUPS >= H) break;
-                    float d[E];
-                    unpack(rd[u], d);
-                    rotate<E, PAIRS, true>(d, ang, me.other);
-                    if (NORM) {
-                        float v[E];
-                        unpack(rx[u], v);
-                        const float r = rsqrtf(head_sum<L>(dot(v, v)) * (1.f / HD) + a.eps);
-                        times(v, r);
+            if (NORM) load_shared(gamma, weight + me.at);
+            for (int h0 = 0; h0 < H; h0 += GROUPS) {
+                const int h = h0 + me.group;
+                cp_async_wait<AHEAD - 1>();
+                float d[E], v[E];
+                unpack(ring.read(0), d);
+                if (NORM) unpack(ring.read(SOURCES - 1), v);
+                fetch(ring.ahead());
+                ring.next();
+                rotate<E, PAIRS, true>(d, ang, me.other);
+                if (NORM) {
+                    const float r = rsqrtf(head_sum<L>(dot(v, v)) * (1.f / HD) + a.eps);
+                    times(v, r);
+                    if (h < H) {
 #pragma unroll
                         for (int i = 0; i < E; i += 2)
                             f2_unpack(f2_fma(f2_pack(d[i], d[i + 1]), f2_pack(v[i], v[i + 1]), f2_pack(acc[i], acc[i + 1])),
                                       acc[i], acc[i + 1]);
-                        times(d, gamma);
-                        const float in = head_sum<L>(dot(d, v)) * (-1.f / HD);
-                        const uint64_t in2 = f2_pack(in, in), r2 = f2_pack(r, r);
-#pragma unroll
-                        for (int i = 0; i < E; i += 2)
-                            f2_unpack(f2_mul(f2_fma(f2_pack(v[i], v[i + 1]), in2, f2_pack(d[i], d[i + 1])), r2), d[i],
-                                      d[i + 1]);
                     }
-                    if (h < H) store_e(dx + h * HD, d);
+                    times(d, gamma);
+                    const float in = head_sum<L>(dot(d, v)) * (-1.f / HD);
+                    const uint64_t in2 = f2_pack(in, in), r2 = f2_pack(r, r);
+#pragma unroll
+                    for (int i = 0; i < E; i += 2)
+                        f2_unpack(f2_mul(f2_fma(f2_pack(v[i], v[i + 1]), in2, f2_pack(d[i], d[i + 1])), r2), d[i], d[i + 1]);
                 }
+                if (h < H) store_e(dx + h * HD, d);
             }
         };
-        heads(a.Hq, dqo, q, (T*)a.qo + row * a.qo_stride + me.at, a.q_gamma, aq, true);
-        heads(a.Hk, (const T*)a.dko + row * a.dko_stride + me.at, (const T*)a.k + row * a.k_stride + me.at,
-              (T*)a.ko + row * a.ko_stride + me.at, a.k_gamma, ak, false);
+        heads(a.Hq, (T*)a.qo + row * a.qo_stride + me.at, weights[0], aq);
+        heads(a.Hk, (T*)a.ko + row * a.ko_stride + me.at, weights[1], ak);
     }
     if constexpr (NORM) {
         if (!partial) return;
@@ -328,8 +398,8 @@ int blocks_for(int N, int warps, int a_sm) {
     const int64_t rows = ((int64_t)N + warps - 1) / warps, most = (int64_t)gpt2_num_sms() * a_sm;
     return (int)(rows < most ? rows : most);
 }
-int forward_blocks(int N) { return blocks_for(N, WARPS, 8); }
-int backward_blocks(int N) { return blocks_for(N, WARPS, BACK_A_SM); }
+int forward_blocks(int N) { return blocks_for(N, WARPS, FORWARD_A_SM); }
+int backward_blocks(int N) { return blocks_for(N, WARPS, BACKWARD_A_SM); }
 
 template <typename T, int E, int L, bool PAIRS, bool NORM>
 void start(const RotaryArgs& a, bool back, float* partial, cudaStream_t s) {
