@@ -30,7 +30,8 @@ namespace {
 
 constexpr int THREADS = 256;
 constexpr int GROUPS = 2;                       // groups of four values a thread
-constexpr int CHUNK = THREADS * 4 * GROUPS;     // values a block
+constexpr int CHUNK = THREADS * 4 * GROUPS;     // values a block of the update
+constexpr int WIDE = 8192;                      // and of the passes that only read or only decode
 constexpr int SCALE_BLOCK = 128;                // values that share a scale: a warp's group
 
 struct Entry {
@@ -41,9 +42,8 @@ struct Entry {
     uint8_t *m_scale, *v_scale;
     int64_t n;
     float decay;
-    int first;   // first block of this tensor
-    int aligned; // every address allows four values at once
-    int pad;
+    int first, first_wide;  // first block of this tensor, in chunks and in wide ones
+    int aligned;            // every address allows four values at once
 };
 
 // MOST tensors a launch: few fit the classic 4 KB of parameters, whose upload is cheaper.
@@ -60,11 +60,11 @@ struct Values {
     uint64_t key;
 };
 
-template <int MOST> __device__ __forceinline__ int find(const Batch<MOST>& b, int block) {
+template <int Entry::*FIRST, int MOST> __device__ __forceinline__ int find(const Batch<MOST>& b, int block) {
     int lo = 0, hi = b.n - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (b.e[mid].first <= block) lo = mid;
+        if (b.e[mid].*FIRST <= block) lo = mid;
         else hi = mid - 1;
     }
     return lo;
@@ -76,6 +76,11 @@ __device__ __forceinline__ uint64_t mix(uint64_t z) {  // the finaliser of split
     return z ^ (z >> 31);
 }
 
+// (Without the hint that the values are read once.)
+__device__ __forceinline__ void load4(const float* p, float (&f)[4]) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+}
 __device__ __forceinline__ void load4(const bf16* p, float (&f)[4]) {
     const uint2 u = *reinterpret_cast<const uint2*>(p);
     f[0] = __uint_as_float(u.x << 16); f[1] = __uint_as_float(u.x & 0xFFFF0000u);
@@ -103,19 +108,6 @@ __device__ __forceinline__ void get4(const bf16* p, int64_t i, int64_t n, bool w
 #pragma unroll
         for (int j = 0; j < 4; j++) f[j] = i + j < n ? __bfloat162float(p[i + j]) : 0.f;
     }
-}
-// The same without the hint that the values are read once.
-__device__ __forceinline__ void keep4(const float* p, int64_t i, int64_t n, bool whole, float (&f)[4]) {
-    if (whole) {
-        const float4 a = *reinterpret_cast<const float4*>(p + i);
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    } else {
-        get4(p, i, n, false, f);
-    }
-}
-__device__ __forceinline__ void keep4(const bf16* p, int64_t i, int64_t n, bool whole, float (&f)[4]) {
-    if (whole) load4(p + i, f);
-    else get4(p, i, n, false, f);
 }
 __device__ __forceinline__ uint32_t get4(const uint8_t* p, int64_t i, int64_t n, bool whole) {
     if (whole) return __ldcs(reinterpret_cast<const uint32_t*>(p + i));
@@ -179,18 +171,21 @@ __device__ __forceinline__ void decode_v(uint32_t w, float (&f)[4]) {
 }
 __device__ __forceinline__ float scale_of(uint8_t b) { return __uint_as_float((b < 1 ? 1u : b > 254 ? 254u : b) << 23); }
 
-// The code of y >= 0, given y under its scale, times 2^(bias - 127): then the top bits of the fp32 number are the
-// code, an fp32 subnormal holding what is below the code's lowest whole exponent. Adding 16 random bits right below
-// the code's last one carries into it with the probability (what is left over the lower code) / (the codes' distance).
-__device__ __forceinline__ uint32_t encode(float y, uint32_t r_shifted) { return (__float_as_uint(y) + r_shifted) >> 20; }
+// The code of y >= 0 in the top byte, given y under its scale, times 2^(bias - 127): bits 20 to 27 of the fp32 number
+// are the code, an fp32 subnormal holding what is below the code's lowest whole exponent. Adding 16 random bits right
+// below the code's last one carries into it with the probability (what is left over the lower code) / (the codes'
+// distance). One product (bits x 16 + random bits x 256) shifts both to the top: the integer pipe has half the rate of
+// the FMA pipe, and it bounds the kernel. random: the 16 bits in the middle two bytes.
+__device__ __forceinline__ uint32_t encode(float y, uint32_t random) { return __float_as_uint(y) * 16u + random; }
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+}
 
 // The scale byte of a block whose largest magnitude has these bits.
 __device__ __forceinline__ uint32_t scale_byte(uint32_t largest, int top) {
     const int b = (int)(largest >> 23) - top;
     return b < 1 ? 1u : (uint32_t)b;
 }
-constexpr uint32_t INF_BITS = 0x7F800000u;
-
 // The square root and the quotient of 8-bit moments' updates are the hardware's (2^-22 of a step, where a stored
 // moment is off by up to 2^-4): the IEEE forms cost a third of the kernel.
 template <bool EIGHT> __device__ __forceinline__ float step_of(float m, float v, float eps) {
@@ -250,26 +245,26 @@ __device__ __forceinline__ void adamw_chunk(const Entry& e, const Values& h, int
         put4(e.master, i, n, whole(u), th[u]);
         if (e.param) put4(e.param, i, n, whole(u), th[u]);
         if (EIGHT) {
-            uint32_t am = 0, av = 0;
+            float fm = 0.f, fv = 0.f, check = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                am = max(am, __float_as_uint(m[u][j]) & 0x7FFFFFFFu);
-                av = max(av, __float_as_uint(v[u][j]) & 0x7FFFFFFFu);
+                fm = fmaxf(fm, fabsf(m[u][j]));
+                fv = fmaxf(fv, fabsf(v[u][j]));
+                check = fmaf(m[u][j], 0.f, fmaf(v[u][j], 0.f, check));  // 0, or NaN where one is not finite
             }
-            const bool odd = __any_sync(0xffffffffu, max(am, av) >= INF_BITS);
+            const bool odd = __any_sync(0xffffffffu, check != 0.f);
             if (odd) {  // what is not finite leaves the scale alone
-                am = av = 0;
+                fm = fv = 0.f;
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
-                    const uint32_t x = __float_as_uint(m[u][j]) & 0x7FFFFFFFu, y = __float_as_uint(v[u][j]) & 0x7FFFFFFFu;
-                    am = max(am, x < INF_BITS ? x : 0u);
-                    av = max(av, y < INF_BITS ? y : 0u);
+                    if (isfinite(m[u][j])) fm = fmaxf(fm, fabsf(m[u][j]));
+                    if (isfinite(v[u][j])) fv = fmaxf(fv, fabsf(v[u][j]));
                 }
             }
-            am = scale_byte(__reduce_max_sync(0xffffffffu, am), 7);
-            av = scale_byte(__reduce_max_sync(0xffffffffu, av), 14);
+            const uint32_t am = scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(fm)), 7);
+            const uint32_t av = scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(fv)), 14);
             const float im = __uint_as_float((254u - am) << 23), iv = __uint_as_float((254u - av) << 23);
-            uint32_t wm = 0, wv = 0;
+            uint32_t x[4], y[4];
 #pragma unroll
             for (int p = 0; p < 2; p++) {
                 const uint64_t r = mix(draw + p * GOLDEN);
@@ -277,17 +272,20 @@ __device__ __forceinline__ void adamw_chunk(const Entry& e, const Values& h, int
                 for (int o = 0; o < 2; o++) {
                     const int j = 2 * p + o;
                     const uint32_t w = (uint32_t)(r >> (32 * o));
-                    uint32_t x = encode(fabsf(m[u][j]) * im * 0x1p-120f, w << 4 & 0xFFFF0u);
-                    uint32_t y = encode(v[u][j] * iv * 0x1p-112f, w >> 12 & 0xFFFF0u);
-                    y = max(y, v[u][j] > 0.f ? 1u : 0u);
+                    x[j] = encode(fabsf(m[u][j]) * im * 0x1p-120f, __byte_perm(w, 0, 0x4104));
+                    // (0x1p-129f, a subnormal, is the lowest code)
+                    const float least = fminf(v[u][j] * 0x1p120f, 0x1p-129f);
+                    y[j] = encode(fmaxf(v[u][j] * iv * 0x1p-112f, least), __byte_perm(w, 0, 0x4324));
                     if (odd) {
-                        if (!isfinite(m[u][j])) x = 0x7Fu;
-                        if (!isfinite(v[u][j])) y = 0xFFu;
+                        if (!isfinite(m[u][j])) x[j] = 0x7F000000u;
+                        if (!isfinite(v[u][j])) y[j] = 0xFF000000u;
                     }
-                    wm |= (x | (__float_as_uint(m[u][j]) >> 24 & 0x80u)) << (8 * j);
-                    wv |= y << (8 * j);
                 }
             }
+            const uint32_t sign = top_bytes(__float_as_uint(m[u][0]), __float_as_uint(m[u][1]), __float_as_uint(m[u][2]),
+                                            __float_as_uint(m[u][3]));
+            const uint32_t wm = top_bytes(x[0], x[1], x[2], x[3]) | (sign & 0x80808080u);
+            const uint32_t wv = top_bytes(y[0], y[1], y[2], y[3]);
             draw += (uint64_t)(THREADS * 2) * GOLDEN;
             put4((uint8_t*)e.m, i, n, whole(u), wm);
             put4((uint8_t*)e.v, i, n, whole(u), wv);
@@ -306,7 +304,7 @@ template <int MOST, typename G, bool EIGHT>
 __global__ void __launch_bounds__(THREADS) adamw_many_kernel(const __grid_constant__ Batch<MOST> b, const Values h) {
     // from the end: the norm's pass has just read the last gradients, which L2 still holds
     const int block = gridDim.x - 1 - blockIdx.x;
-    const int k = find(b, block);
+    const int k = find<&Entry::first>(b, block);
     const Entry& e = b.e[k];
     const int64_t first = (int64_t)(block - e.first) * CHUNK, base = first + threadIdx.x * 4;
     const uint64_t draw = h.key + (((uint64_t)(b.base + k) << 40) + (uint64_t)base / 2) * GOLDEN;
@@ -321,18 +319,29 @@ __global__ void __launch_bounds__(THREADS) sumsq_many_kernel(const __grid_consta
     __shared__ float sh[THREADS / 32];
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
-        const Entry& e = b.e[find(b, c)];
-        const int64_t n = e.n, base = (int64_t)(c - e.first) * CHUNK + threadIdx.x * 4;
-        float g[GROUPS][4];
+        const Entry& e = b.e[find<&Entry::first_wide>(b, c)];
+        const int64_t n = e.n, first = (int64_t)(c - e.first_wide) * WIDE, base = first + threadIdx.x * 4;
+        constexpr int LOADS = WIDE / (THREADS * 4);
+        auto add = [&](const float (&g)[4]) {
 #pragma unroll
-        for (int u = 0; u < GROUPS; u++) {
-            const int64_t i = base + u * (THREADS * 4);
-            keep4((const G*)e.grad, i, n, e.aligned && i + 4 <= n, g[u]);
+            for (int j = 0; j < 4; j++) acc[j] = fmaf(g[j], g[j], acc[j]);
+        };
+        if (e.aligned && first + WIDE <= n) {
+            float g[LOADS][4];
+#pragma unroll
+            for (int u = 0; u < LOADS; u++) load4((const G*)e.grad + base + u * (THREADS * 4), g[u]);
+#pragma unroll
+            for (int u = 0; u < LOADS; u++) add(g[u]);
+        } else {
+#pragma unroll 4
+            for (int u = 0; u < LOADS; u++) {
+                const int64_t i = base + u * (THREADS * 4);
+                if (i >= n) break;
+                float g[4];
+                get4((const G*)e.grad, i, n, e.aligned && i + 4 <= n, g);
+                add(g);
+            }
         }
-#pragma unroll
-        for (int u = 0; u < GROUPS; u++)
-#pragma unroll
-            for (int j = 0; j < 4; j++) acc[j] = fmaf(g[u][j], g[u][j], acc[j]);
     }
     const float s = warp_sum((acc[0] + acc[1]) + (acc[2] + acc[3]));
     if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = s;
@@ -362,66 +371,88 @@ __global__ void __launch_bounds__(1024) norm_many_kernel(float* __restrict__ nor
     }
 }
 
+// Eight codes a thread and load, all loads of a chunk first. The values' places travel in master and param.
 template <int MOST, typename T>
 __global__ void __launch_bounds__(THREADS) states_many_kernel(const __grid_constant__ Batch<MOST> b) {
-    const Entry& e = b.e[find(b, blockIdx.x)];
-    const int64_t n = e.n, base = (int64_t)((int)blockIdx.x - e.first) * CHUNK + threadIdx.x * 4;
+    const Entry& e = b.e[find<&Entry::first_wide>(b, blockIdx.x)];
+    const int64_t n = e.n, first = (int64_t)((int)blockIdx.x - e.first_wide) * WIDE;
+    const uint8_t *m = (const uint8_t*)e.m, *v = (const uint8_t*)e.v;
+    T *mo = (T*)(void*)e.master, *vo = (T*)(void*)e.param;
+    if (!e.aligned || first + WIDE > n) {
+        for (int64_t i = first + threadIdx.x * 4; i < min(n, first + WIDE); i += THREADS * 4) {
+            const bool whole = e.aligned && i + 4 <= n;
+            const float ms = scale_of(e.m_scale[i / SCALE_BLOCK]), vs = scale_of(e.v_scale[i / SCALE_BLOCK]);
+            float x[4], y[4];
+            decode_m(get4(m, i, n, whole), x);
+            decode_v(get4(v, i, n, whole), y);
 #pragma unroll
-    for (int u = 0; u < GROUPS; u++) {
-        const int64_t i = base + u * (THREADS * 4);
-        if (i >= n) break;
-        const bool whole = e.aligned && i + 4 <= n;
-        const int64_t at = i / SCALE_BLOCK;
-        const float ms = scale_of(e.m_scale[at]), vs = scale_of(e.v_scale[at]);
-        float m[4], v[4];
-        decode_m(get4((const uint8_t*)e.m, i, n, whole), m);
-        decode_v(get4((const uint8_t*)e.v, i, n, whole), v);
+            for (int j = 0; j < 4; j++) x[j] *= ms, y[j] *= vs;
+            put4(mo, i, n, whole, x);
+            put4(vo, i, n, whole, y);
+        }
+        return;
+    }
+    constexpr int LOADS = WIDE / (THREADS * 8);
+    uint2 cm[LOADS], cv[LOADS];
+    float sm[LOADS], sv[LOADS];
 #pragma unroll
-        for (int j = 0; j < 4; j++) m[j] *= ms, v[j] *= vs;
-        put4((T*)(void*)e.master, i, n, whole, m);  // the values' places travel in master and param
-        put4((T*)(void*)e.param, i, n, whole, v);
+    for (int u = 0; u < LOADS; u++) {
+        const int64_t i = first + (u * THREADS + threadIdx.x) * 8;
+        cm[u] = __ldcs(reinterpret_cast<const uint2*>(m + i));
+        cv[u] = __ldcs(reinterpret_cast<const uint2*>(v + i));
+        sm[u] = scale_of(e.m_scale[i / SCALE_BLOCK]);
+        sv[u] = scale_of(e.v_scale[i / SCALE_BLOCK]);
+    }
+#pragma unroll
+    for (int u = 0; u < LOADS; u++) {
+        const int64_t i = first + (u * THREADS + threadIdx.x) * 8;
+        float f[8];
+        auto decoded = [&](auto decode, uint2 c, float s, T* to) {
+            decode(c.x, reinterpret_cast<float(&)[4]>(f[0]));
+            decode(c.y, reinterpret_cast<float(&)[4]>(f[4]));
+#pragma unroll
+            for (int j = 0; j < 8; j++) f[j] *= s;
+            store8(to + i, f);
+        };
+        decoded([](uint32_t w, float (&x)[4]) { decode_m(w, x); }, cm[u], sm[u], mo);
+        decoded([](uint32_t w, float (&x)[4]) { decode_v(w, x); }, cv[u], sv[u], vo);
     }
 }
 
 bool at16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
-// The entries of tensors [i0, i1) and the blocks that they take.
-template <int MOST, typename Fill> int gather(Batch<MOST>& b, const gpt2_adamw_tensor* t, int i0, int i1, Fill fill) {
-    int64_t blocks = 0;
+// The entries of tensors [i0, i1) and the blocks that they take, in chunks and in wide ones.
+template <int MOST, typename Fill>
+void gather(Batch<MOST>& b, const gpt2_adamw_tensor* t, int i0, int i1, Fill fill, int& blocks, int& wide) {
+    blocks = wide = 0;
     b.n = 0;
     b.base = i0;
     for (int i = i0; i < i1; i++) {
         Entry& e = b.e[b.n++];
         e = {t[i].master, (bf16*)t[i].param_bf16, t[i].grad, t[i].m, t[i].v, t[i].m_scale, t[i].v_scale, t[i].n,
-             t[i].weight_decay, (int)blocks, 0, 0};
+             t[i].weight_decay, blocks, wide, 0};
         fill(e, i);
         e.aligned = at16(e.master) && at16(e.param) && at16(e.grad) && at16(e.m) && at16(e.v);
-        blocks += (e.n + CHUNK - 1) / CHUNK;
+        blocks += (int)((e.n + CHUNK - 1) / CHUNK);
+        wide += (int)((e.n + WIDE - 1) / WIDE);
     }
-    return (int)blocks;
 }
 
-int64_t blocks_of(const gpt2_adamw_tensor* t, int n) {
-    int64_t blocks = 0;
-    for (int i = 0; i < n; i++) blocks += (t[i].n + CHUNK - 1) / CHUNK;
-    return blocks;
-}
-
-// Calls go(batch, blocks) for the tensors in as few launches as they fit.
+// Calls go(batch, blocks, wide blocks) for the tensors in as few launches as they fit.
 template <typename Fill, typename Go> int in_batches(const gpt2_adamw_tensor* t, int n, Fill fill, Go go) {
-    int launches = 0;
+    int launches = 0, blocks, wide;
     for (int i = 0; i < n;) {
         const int left = n - i;
         if (left <= FEW) {
             Batch<FEW> b;
-            const int blocks = gather(b, t, i, n, fill);
-            if (blocks) launches++, go(b, blocks);
+            gather(b, t, i, n, fill, blocks, wide);
+            if (blocks) launches++, go(b, blocks, wide);
             i = n;
         } else {
             const int to = left < MANY ? n : i + MANY;
             Batch<MANY> b;
-            const int blocks = gather(b, t, i, to, fill);
-            if (blocks) launches++, go(b, blocks);
+            gather(b, t, i, to, fill, blocks, wide);
+            if (blocks) launches++, go(b, blocks, wide);
             i = to;
         }
     }
@@ -446,8 +477,10 @@ uint64_t host_mix(uint64_t z) {
 
 // The norm, then a partial sum for each block.
 size_t adamw_many_scratch(const gpt2_adamw_tensor* t, int n) {
-    const int64_t blocks = blocks_of(t, n), most = (int64_t)sumsq_blocks() * (n / MANY + 1);
-    return 256 + (size_t)(blocks < most ? blocks : most) * 4;
+    int64_t wide = 0;
+    for (int i = 0; i < n; i++) wide += (t[i].n + WIDE - 1) / WIDE;
+    const int64_t most = (int64_t)sumsq_blocks() * (n / MANY + 1);
+    return 256 + (size_t)(wide < most ? wide : most) * 4;
 }
 
 int launch_adamw_many(const gpt2_adamw_tensor* t, int n, int grad_dtype, int bits, float lr, float b1, float b2,
@@ -462,20 +495,20 @@ int launch_adamw_many(const gpt2_adamw_tensor* t, int n, int grad_dtype, int bit
         float* norm = (float*)scratch;
         float* partial = norm + 64;
         int at = 0;
-        launches += in_batches(t, n, as_is, [&](const auto& b, int blocks) {
+        launches += in_batches(t, n, as_is, [&](const auto& b, int, int wide) {
             constexpr int MOST = sizeof(b.e) / sizeof(Entry);
-            const int grid = blocks < sumsq_blocks() ? blocks : sumsq_blocks();
+            const int grid = wide < sumsq_blocks() ? wide : sumsq_blocks();
             if (grad_dtype == GPT2_MODE_BF16)
-                sumsq_many_kernel<MOST, bf16><<<grid, THREADS, 0, s>>>(b, blocks, partial + at);
+                sumsq_many_kernel<MOST, bf16><<<grid, THREADS, 0, s>>>(b, wide, partial + at);
             else
-                sumsq_many_kernel<MOST, float><<<grid, THREADS, 0, s>>>(b, blocks, partial + at);
+                sumsq_many_kernel<MOST, float><<<grid, THREADS, 0, s>>>(b, wide, partial + at);
             at += grid;
         });
         norm_many_kernel<<<1, 1024, 0, s>>>(norm, grad_norm, partial, at);
         launches++;
         if (max_norm > 0.f) h.norm = norm;
     }
-    return launches + in_batches(t, n, as_is, [&](const auto& b, int blocks) {
+    return launches + in_batches(t, n, as_is, [&](const auto& b, int blocks, int) {
         constexpr int MOST = sizeof(b.e) / sizeof(Entry);
         if (grad_dtype == GPT2_MODE_BF16) start_adamw<MOST, bf16>(b, blocks, bits, h, s);
         else start_adamw<MOST, float>(b, blocks, bits, h, s);
@@ -489,9 +522,9 @@ int launch_adamw_many_states(const gpt2_adamw_tensor* t, void* const* m_values, 
         e.param = (bf16*)v_values[i];
         e.grad = nullptr;
     };
-    return in_batches(t, n, places, [&](const auto& b, int blocks) {
+    return in_batches(t, n, places, [&](const auto& b, int, int wide) {
         constexpr int MOST = sizeof(b.e) / sizeof(Entry);
-        if (dtype == GPT2_MODE_BF16) states_many_kernel<MOST, bf16><<<blocks, THREADS, 0, s>>>(b);
-        else states_many_kernel<MOST, float><<<blocks, THREADS, 0, s>>>(b);
+        if (dtype == GPT2_MODE_BF16) states_many_kernel<MOST, bf16><<<wide, THREADS, 0, s>>>(b);
+        else states_many_kernel<MOST, float><<<wide, THREADS, 0, s>>>(b);
     });
 }
