@@ -29,30 +29,52 @@ constexpr int64_t PIECE_BYTES = 256ll << 20;
 struct Pieces {
     int width, n;
 };
-// Pieces of equal width, in steps of a tile, that hold PIECE_BYTES for all rows (but no fewer than 2048 columns).
-Pieces pieces(int dtype, int N, int V) {
+
+// The time of the products of one piece of `cols` columns, in arbitrary units: dz and dw go in rounds of CTA pairs over
+// 256 x 256 and 256 x 192 tiles, and a round that is not full costs as much as a full one. (dx has N x C tiles, whatever
+// the piece.)
+int64_t rounds_cost(int N, int C, int cols, int pairs) {
+    const int64_t ct = (cols + 255) / 256, mt = (N + 255) / 256, kt = (C + 191) / 192;
+    return (mt * ct + pairs - 1) / pairs * C * 256 + (ct * kt + pairs - 1) / pairs * N * 192;
+}
+
+// Pieces of one width, a whole number of tiles, that hold PIECE_BYTES for all rows (but no fewer than 2048 columns);
+// of the widths from half of that on, the one whose rounds cost least. The gradients of 8192 x 768 x 50257: 14592
+// columns, which fill three rounds of dw and 24 of dz, 1412 us; 12800 (four equal pieces) 1448; 16896 1419; 9728 1430;
+// 4864 1515; 25344 1434; all at once 1477.
+Pieces pieces(int dtype, int N, int C, int V) {
     const int64_t es = dtype == GPT2_MODE_BF16 ? 2 : 4;
-    int64_t most = PIECE_BYTES / ((int64_t)N * es);
+    int64_t most = PIECE_BYTES / ((int64_t)N * es) / 256 * 256;
     if (most < 2048) most = 2048;
-    const int n = (int)((V + most - 1) / most);
-    const int width = ((V + n - 1) / n + 255) / 256 * 256;
-    return {width, (V + width - 1) / width};
+    if (V <= most) return {(V + 255) / 256 * 256, 1};
+    const int pairs = gpt2_num_sms() / 2;
+    int best = (int)most;
+    int64_t least = INT64_MAX;
+    for (int w = (int)most; w >= most / 2 && w >= 2048; w -= 256) {
+        const int n = V / w, rest = V - n * w;
+        const int64_t cost = n * rounds_cost(N, C, w, pairs) + (rest ? rounds_cost(N, C, rest, pairs) : 0);
+        if (cost < least) {
+            least = cost;
+            best = w;
+        }
+    }
+    return {best, (V + best - 1) / best};
 }
 int round8(int v) { return (v + 7) / 8 * 8; }
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
-// Joins the parts of 32 rows: strand after strand of slots (a warp's lanes read neighbouring rows of one slot),
-// then the strands. Loads run ahead in batches: a part's exponentials wait for it, the next parts do not.
-// 8 strands where there are rows enough to fill the device with them, 32 for fewer rows.
-template <int STRANDS, int AHEAD>
-__global__ void __launch_bounds__(STRANDS * 32) join_kernel(float* __restrict__ losses, float* __restrict__ lse,
-                                                           const float2* __restrict__ stats,
-                                                           const float* __restrict__ target_logit,
-                                                           const int32_t* __restrict__ targets, int N, int V, int slots,
-                                                           int* status) {
-    __shared__ float2 sm[STRANDS][32];
-    const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
-    const int64_t row = (int64_t)blockIdx.x * 32 + tx;
+// Joins the parts of ROWS rows: strand after strand of slots (neighbouring lanes read neighbouring rows of one slot),
+// then the strands. Loads run ahead in batches: a part's exponentials wait for it, the next parts do not. Many rows go
+// in blocks of 32 with 8 strands; fewer in blocks of 8 with 64, so that all parts are on their way at once.
+template <int ROWS, int STRANDS, int BATCH>
+__global__ void __launch_bounds__(STRANDS * ROWS) join_kernel(float* __restrict__ losses, float* __restrict__ lse,
+                                                             const float2* __restrict__ stats,
+                                                             const float* __restrict__ target_logit,
+                                                             const int32_t* __restrict__ targets, int N, int V,
+                                                             int slots, int* status) {
+    __shared__ float2 sm[STRANDS][ROWS];
+    const int tx = threadIdx.x % ROWS, ty = threadIdx.x / ROWS;
+    const int64_t row = (int64_t)blockIdx.x * ROWS + tx;
     float m = -INFINITY, s = 0.f;
     auto join = [&](float2 p) {
         if (p.y == 0.f) return;  // a part without columns
@@ -60,15 +82,15 @@ __global__ void __launch_bounds__(STRANDS * 32) join_kernel(float* __restrict__ 
         s = s * ex2_approx((m - mm) * LOG2E) + p.y * ex2_approx((p.x - mm) * LOG2E);
         m = mm;
     };
-    for (int i = ty; i < slots; i += STRANDS * AHEAD) {
-        float2 p[AHEAD];
+    for (int i = ty; i < slots; i += STRANDS * BATCH) {
+        float2 p[BATCH];
 #pragma unroll
-        for (int u = 0; u < AHEAD; u++) {
+        for (int u = 0; u < BATCH; u++) {
             const int slot = i + u * STRANDS;
             p[u] = slot < slots && row < N ? __ldcs(&stats[(int64_t)slot * N + row]) : make_float2(0.f, 0.f);
         }
 #pragma unroll
-        for (int u = 0; u < AHEAD; u++) join(p[u]);
+        for (int u = 0; u < BATCH; u++) join(p[u]);
     }
     sm[ty][tx] = make_float2(m, s);
     for (int w = STRANDS / 2; w > 0; w /= 2) {  // halves of the strands, in a fixed order
@@ -92,7 +114,7 @@ __global__ void __launch_bounds__(256) round_kernel(bf16* __restrict__ out, cons
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
     if (i >= n) return;
     float f[8];
-    load8(in + i, f);
+    load8_stream(in + i, f);
     store8(out + i, f);
 }
 
@@ -124,11 +146,12 @@ int launch_linear_classifier_forward(int dtype, float* losses, float* lse, const
     const int n = bf ? launch_head_lse(x, w, N, V, C, e, status, s)
                      : launch_head_f32_lse((const float*)x, (const float*)w, N, V, C, e, s);
     if (n < 0) return n;
-    const int blocks = (N + 31) / 32;
-    if (blocks >= 4 * gpt2_num_sms())
-        join_kernel<8, 8><<<blocks, 256, 0, s>>>(losses, lse, e.stats, e.target_logit, targets, N, V, slots, status);
+    if (N >= 32 * gpt2_num_sms())
+        join_kernel<32, 8, 8><<<(N + 31) / 32, 256, 0, s>>>(losses, lse, e.stats, e.target_logit, targets, N, V, slots,
+                                                            status);
     else
-        join_kernel<32, 4><<<blocks, 1024, 0, s>>>(losses, lse, e.stats, e.target_logit, targets, N, V, slots, status);
+        join_kernel<8, 64, 8><<<(N + 7) / 8, 512, 0, s>>>(losses, lse, e.stats, e.target_logit, targets, N, V, slots,
+                                                          status);
     return n + 1;
 }
 
@@ -162,7 +185,7 @@ struct BackwardScratch {
 }  // namespace
 
 size_t linear_classifier_backward_scratch(int dtype, int N, int C, int V, int dw_fp32, int accumulate) {
-    const Pieces p = pieces(dtype, N, V);
+    const Pieces p = pieces(dtype, N, C, V);
     return BackwardScratch(dtype, N, C, p).own + products_scratch(dtype, N, C, V, dw_fp32, accumulate, p);
 }
 
@@ -171,7 +194,7 @@ int launch_linear_classifier_backward(int dtype, void* dx, void* dw, int dw_fp32
                                       const float* dlse, int N, int C, int V, int Vp, void* scratch, int* status,
                                       cudaStream_t s) {
     const bool bf = dtype == GPT2_MODE_BF16;
-    const Pieces p = pieces(dtype, N, V);
+    const Pieces p = pieces(dtype, N, C, V);
     const BackwardScratch at(dtype, N, C, p);
     void* dz = (char*)scratch + at.dz;
     float* sum = (float*)((char*)scratch + at.dx);

@@ -39,6 +39,12 @@ struct Product {
 
 // A slice of an operand: T rows by KS k's from (row0, k0), zero outside. MN: the operand is [k][rows], else [rows][k].
 // Each thread holds two vectors of four between the load and the store.
+//
+// Where a row keeps its k's in shared memory: its four vectors in an order that changes every 8 rows. A warp that stores
+// [k][rows] data writes one value to each of 16 rows 4 apart, 80 words from one to the next: in one order they would meet
+// two banks, in this one eight.
+__device__ __forceinline__ constexpr int place(int row, int k) { return (((k >> 2) ^ (row >> 3)) & 3) * 4 + (k & 3); }
+
 template <bool MN> struct Slice {
     float f[2][4];
 
@@ -80,9 +86,9 @@ template <bool MN> struct Slice {
             const int i = threadIdx.x + u * THREADS;
             if (MN) {
 #pragma unroll
-                for (int j = 0; j < 4; j++) s[i % 16 * 4 + j][i / 16] = f[u][j];
+                for (int j = 0; j < 4; j++) s[i % 16 * 4 + j][place(i % 16 * 4, i / 16)] = f[u][j];
             } else {
-                *reinterpret_cast<float4*>(&s[i / 4][i % 4 * 4]) = make_float4(f[u][0], f[u][1], f[u][2], f[u][3]);
+                *reinterpret_cast<float4*>(&s[i / 4][place(i / 4, i % 4 * 4)]) = make_float4(f[u][0], f[u][1], f[u][2], f[u][3]);
             }
         }
     }
@@ -117,13 +123,17 @@ __global__ void __launch_bounds__(THREADS, 3) head_f32_kernel(const Product g) {
         for (int kk = 0; kk < KS; kk += 4) {
             ulonglong2 x[TM], y[TN];
 #pragma unroll
-            for (int i = 0; i < TM; i++) x[i] = *reinterpret_cast<const ulonglong2*>(&As[buf][ty + 8 * i][kk]);
+            for (int i = 0; i < TM; i++) x[i] = *reinterpret_cast<const ulonglong2*>(&As[buf][ty + 8 * i][place(8 * i, kk)]);
 #pragma unroll
-            for (int j = 0; j < TN; j++) y[j] = *reinterpret_cast<const ulonglong2*>(&Bs[buf][tx + 16 * j][kk]);
+            for (int j = 0; j < TN; j++) y[j] = *reinterpret_cast<const ulonglong2*>(&Bs[buf][tx + 16 * j][place(tx + 16 * j, kk)]);
 #pragma unroll
             for (int i = 0; i < TM; i++)
 #pragma unroll
-                for (int j = 0; j < TN; j++) acc[i][j] = f2_fma(x[i].y, y[j].y, f2_fma(x[i].x, y[j].x, acc[i][j]));
+                for (int j = 0; j < TN; j++) acc[i][j] = f2_fma(x[i].x, y[j].x, acc[i][j]);
+#pragma unroll
+            for (int i = 0; i < TM; i++)
+#pragma unroll
+                for (int j = 0; j < TN; j++) acc[i][j] = f2_fma(x[i].y, y[j].y, acc[i][j]);
         }
     }
     float* d = g.D + (EPI == STORE ? (int64_t)blockIdx.y * g.M * g.N : 0);
