@@ -462,9 +462,10 @@ int gpt2_rotary_turns(uint64_t* turns, int rot, double base, int scaling, double
  * exact far from 0 as near it. x [N, C], w [>= V, C] in dtype (the rows of w
  * from V on are not used, whatever they hold); the logits are fp32 and are not
  * rounded. A target outside [0,V) sets bit 4 of *d_status and is treated as 0.
- * Rows of x are independent; a row with a logit that is not finite gets NaN.
- * C % 8 == 0, C >= 8, V >= 1, x and w 16-byte aligned, N * C and V * C below
- * 2^31 - 2048; N = 0 launches nothing. Scratch: row statistics of the
+ * Rows of x are independent. A logit of -inf counts as nothing (a row of nothing
+ * else gets lse = -inf and a loss of +inf); a row with a NaN or +inf gets NaN.
+ * C % 8 == 0, C >= 8, V >= 1, x and w 16-byte aligned; N * C, V * C and the
+ * 64 x 64 tiles of N x V below 2^31 - 2048; N = 0 launches nothing. Scratch: row statistics of the
  * vocabulary's tiles. */
 size_t gpt2_op_linear_classifier_forward_scratch(int dtype, int N, int C, int V);
 int gpt2_op_linear_classifier_forward(int dtype, float* losses, float* lse, const void* x, const void* w,
@@ -476,8 +477,9 @@ int gpt2_op_linear_classifier_forward(int dtype, float* losses, float* lse, cons
  *   dz_ij = (dloss[i] + dlse[i]) p_ij - dloss[i] [j == targets[i]],
  *   dx = dz W (dtype, overwritten), dw = dz^T x.
  * dloss, dlse: [N] fp32, gradients of losses and lse, either may be null (0). A
- * row whose dloss and dlse are 0 has dz = 0 whatever its logits are (a prompt's
- * or padding's tokens; its x has to be finite: dw adds 0 x). dw [Vp, C], Vp >= V,
+ * row whose dloss and dlse are 0, or whose lse is -inf, has dz = 0 whatever its
+ * logits are (a prompt's or padding's tokens; x and the first V rows of w have
+ * to be finite all the same: the products add 0 times them). dw [Vp, C], Vp >= V,
  * Vp % 8 == 0: fp32 (dw_fp32 = 1; the only form in fp32) or bf16; rows from V
  * on get 0. accumulate (fp32 dw only): dw += instead, rows from V on stay. In
  * bf16 dz is rounded to bf16 for the products, as gpt2_op_classifier's dlogits

@@ -158,10 +158,10 @@ def mix(z):
     return z ^ ((z >> 31) & ((1 << 33) - 1))
 
 
-def draws(n, tensor, t, seed, device="cpu"):
-    """u of the first and of the second moment's rounding for the n values of a tensor."""
+def draws(n, tensor, t, seed, device="cpu", start=0):
+    """u of the first and of the second moment's rounding for n values of a tensor, from the start-th (even) on."""
     key = mix((seed + t * GOLDEN) & ((1 << 64) - 1))
-    pair = torch.arange((n + 1) // 2, dtype=torch.int64, device=device)
+    pair = torch.arange((n + 1) // 2, dtype=torch.int64, device=device) + start // 2
     r = mix(((tensor << 40) + pair) * _wrap(GOLDEN) + _wrap(key))
     part = lambda i: ((r >> i) & 0xFFFF).double() / 65536  # noqa: E731
     return torch.stack((part(0), part(32)), 1).flatten()[:n], torch.stack((part(16), part(48)), 1).flatten()[:n]

@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(STRANDS * ROWS) join_kernel(float* __restrict_
     __shared__ float2 sm[STRANDS][ROWS];
     const int tx = threadIdx.x % ROWS, ty = threadIdx.x / ROWS;
     const int64_t row = (int64_t)blockIdx.x * ROWS + tx;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the statistics are still being formed
     float m = -INFINITY, s = 0.f;
     auto join = [&](float2 p) {
         if (p.y == 0.f) return;  // a part without columns
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(STRANDS * ROWS) join_kernel(float* __restrict_
     if (t < 0 || t >= V) set_status(status, GPT2_FLAG_TARGET_RANGE);
     // (max - z) + ln S rather than lse - z: a sure token's loss keeps its digits wherever the logits lie, and
     // none is negative
-    const float ls = logf(s), loss = (m - target_logit[row]) + ls;
+    const float ls = logf(s), loss = s == 0.f ? INFINITY : (m - target_logit[row]) + ls;  // (0: every logit is -inf)
     lse[row] = m + ls;
     losses[row] = loss < 0.f ? 0.f : loss;
 }
@@ -146,12 +147,27 @@ int launch_linear_classifier_forward(int dtype, float* losses, float* lse, const
     const int n = bf ? launch_head_lse(x, w, N, V, C, e, status, s)
                      : launch_head_f32_lse((const float*)x, (const float*)w, N, V, C, e, s);
     if (n < 0) return n;
-    if (N >= 32 * gpt2_num_sms())
-        join_kernel<32, 8, 8><<<(N + 31) / 32, 256, 0, s>>>(losses, lse, e.stats, e.target_logit, targets, N, V, slots,
-                                                            status);
-    else
-        join_kernel<8, 64, 8><<<(N + 7) / 8, 512, 0, s>>>(losses, lse, e.stats, e.target_logit, targets, N, V, slots,
-                                                          status);
+    // only its launch overlaps the statistics' kernel: it waits for that one's end (61 rows: 26.3 -> 24.7 us)
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = s;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    const float2* stats = e.stats;
+    const float* target_logit = e.target_logit;
+    cudaError_t r;
+    if (N >= 32 * gpt2_num_sms()) {
+        cfg.gridDim = (N + 31) / 32;
+        cfg.blockDim = 256;
+        r = cudaLaunchKernelEx(&cfg, join_kernel<32, 8, 8>, losses, lse, stats, target_logit, targets, N, V, slots, status);
+    } else {
+        cfg.gridDim = (N + 7) / 8;
+        cfg.blockDim = 512;
+        r = cudaLaunchKernelEx(&cfg, join_kernel<8, 64, 8>, losses, lse, stats, target_logit, targets, N, V, slots, status);
+    }
+    if (r != cudaSuccess) return GPT2_ERR_CUDA;
     return n + 1;
 }
 

@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(THREADS, 3) head_f32_kernel(const Product g) {
 #pragma unroll
             for (int j = 0; j < TN; j++) {
                 const int n = n0 + tx + 16 * j;
-                if (n < g.N) s += expf(z[j] - m);
+                if (n < g.N) s += expf(z[j] - (m > -INFINITY ? m : 0.f));  // (nothing but -inf: 0; a NaN stays)
                 if (n == t && row < g.M) g.head.target_logit[row] = z[j];
             }
 #pragma unroll
@@ -184,13 +184,12 @@ __global__ void __launch_bounds__(THREADS, 3) head_f32_kernel(const Product g) {
         } else if (row < g.M) {
             const float dl = g.head.dloss ? g.head.dloss[row] : 0.f;
             const float w = dl + (g.head.dlse ? g.head.dlse[row] : 0.f), l = g.head.lse[row];
+            const bool counts = (w != 0.f || dl != 0.f) && l != -INFINITY;
 #pragma unroll
             for (int j = 0; j < TN; j++) {
                 const int n = n0 + tx + 16 * j;
                 // a row that does not count gets zeros whatever its logits are
-                if (n < g.N)
-                    d[(int64_t)row * g.N + n] =
-                        (w != 0.f || dl != 0.f ? w * expf(z[j] - l) : 0.f) - (n == t ? dl : 0.f);
+                if (n < g.N) d[(int64_t)row * g.N + n] = counts ? w * expf(z[j] - l) - (n == t ? dl : 0.f) : 0.f;
             }
         }
     }

@@ -209,7 +209,8 @@ __device__ __forceinline__ void lse_chunk(const uint32_t (&r)[32], RowHead& h, i
 #pragma unroll
     for (int j = 0; j < 32; j++) mx = fmaxf(mx, WHOLE || j < ncols ? __uint_as_float(r[j]) : -INFINITY);
     const float m = fmaxf(h.m, mx);
-    const float ml = m * LOG2E, off = fmaf(m, LOG2E, -ml);
+    const float ref = m > -INFINITY ? m : 0.f;  // nothing but -inf so far: sums of 0
+    const float ml = ref * LOG2E, off = fmaf(ref, LOG2E, -ml);
     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
     for (int j = 0; j < 32; j += 2) {
@@ -218,7 +219,7 @@ __device__ __forceinline__ void lse_chunk(const uint32_t (&r)[32], RowHead& h, i
         s0 += WHOLE || j < ncols ? e0 : 0.f;
         s1 += WHOLE || j + 1 < ncols ? e1 : 0.f;
     }
-    h.s = fmaf(h.s, ex2_approx((h.m - m) * LOG2E), (s0 + s1) * ex2_approx(-off));
+    h.s = fmaf(h.s, ex2_approx((h.m - ref) * LOG2E), (s0 + s1) * ex2_approx(-off));
     h.m = m;
     const int t = h.at - c0;
     if (t >= 0 && t < 32) {  // once in a row's whole vocabulary
@@ -229,19 +230,19 @@ __device__ __forceinline__ void lse_chunk(const uint32_t (&r)[32], RowHead& h, i
     }
 }
 
-// EPI_DZ: this lane's 32 logits become their gradients. A row that does not count (dloss = dlse = 0) gets
-// zeros whatever its logits are.
+// EPI_DZ: this lane's 32 logits become their gradients. A row that does not count (dloss = dlse = 0, or every logit
+// -inf) gets zeros whatever its logits are.
 template <bool WHOLE>
 __device__ __forceinline__ void dz_chunk(const uint32_t (&r)[32], const RowHead& h, int ncols, int c0,
                                          float (&f)[32]) {
-    const bool counts = h.a != 0.f || h.d != 0.f;
+    const bool counts = (h.a != 0.f || h.d != 0.f) && h.lse != -INFINITY;
 #pragma unroll
     for (int j = 0; j < 32; j++) {
         const float p = h.a * ex2_approx(fmaf(__uint_as_float(r[j]), LOG2E, -h.lse));
         f[j] = counts && (WHOLE || j < ncols) ? p : 0.f;
     }
     const int t = h.at - c0;
-    if (t >= 0 && t < 32) {
+    if (counts && t >= 0 && t < 32) {
 #pragma unroll
         for (int j = 0; j < 32; j++) f[j] -= j == t ? h.d : 0.f;
     }
@@ -441,6 +442,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    // the kernel that joins the statistics may come up meanwhile (it waits for this one before it reads them)
+    if constexpr (EPI == EPI_LSE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
 
     if (warp == 0) {
@@ -865,6 +868,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    // the kernel that joins the statistics may come up meanwhile (it waits for this one before it reads them)
+    if constexpr (EPI == EPI_LSE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp == 0) {
         if (lane == 0) {

@@ -494,8 +494,9 @@ int gpt2_rotary_turns(uint64_t* turns, int rot, double base, int scaling, double
 
 static bool linear_classifier_ok(int dtype, int N, int C, int V) {
     const int64_t most = ((int64_t)1 << 31) - 2048;
-    return dt_ok(dtype) && N >= 0 && C >= 8 && C % 8 == 0 && V >= 1 && (int64_t)N * C < most && (int64_t)V * C < most &&
-           V < (1 << 30);
+    if (!dt_ok(dtype) || N < 0 || C < 8 || C % 8 || V < 1) return false;
+    // rows and tiles are counted in 31 bits
+    return (int64_t)N * C < most && (int64_t)V * C < most && ((int64_t)N + 63) / 64 * (((int64_t)V + 63) / 64) < most;
 }
 
 size_t gpt2_op_linear_classifier_forward_scratch(int dtype, int N, int C, int V) {

@@ -169,11 +169,10 @@ _SIGNATURES = {
     "gpt2_op_linear_classifier_backward_scratch": (c_size_t, [c_int] * 6),
     "gpt2_op_linear_classifier_backward": (c_int, [c_int, c_void_p, c_void_p, c_int, c_int] + [c_void_p] * 6
                                            + [c_int] * 4 + [c_void_p, c_size_t, c_void_p, c_void_p]),
-    "gpt2_op_adamw_many_scratch": (c_size_t, [POINTER(gpt2_adamw_tensor), c_int]),
-    "gpt2_op_adamw_many": (c_int, [POINTER(gpt2_adamw_tensor), c_int, c_int, c_int] + [c_float] * 6
+    "gpt2_op_adamw_many_scratch": (c_size_t, [c_void_p, c_int]),
+    "gpt2_op_adamw_many": (c_int, [c_void_p, c_int, c_int, c_int] + [c_float] * 6
                            + [c_void_p, c_int, c_uint64, c_void_p, c_size_t, c_void_p]),
-    "gpt2_op_adamw_many_states": (c_int, [POINTER(gpt2_adamw_tensor), POINTER(c_void_p), POINTER(c_void_p), c_int,
-                                          c_int, c_void_p]),
+    "gpt2_op_adamw_many_states": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int, c_void_p]),
     "gpt2_op_gelu_forward": (c_int, [c_int, c_void_p, c_void_p, c_int64, c_void_p]),
     "gpt2_op_gelu_backward": (c_int, [c_int, c_void_p, c_void_p, c_void_p, c_int64, c_void_p]),
     "gpt2_op_residual_forward": (c_int, [c_int, c_void_p, c_void_p, c_void_p, c_int64, c_void_p]),
@@ -664,7 +663,7 @@ def _rows(what, like, *more):
         raise ValueError(f"{what}: [rows, heads, hd] tensors are needed")
     rows, heads, hd = shape
     for t in (like, *more):
-        if t is not like and (t.shape != shape or t.dtype is not dtype):
+        if t is not like and (t.dtype is not dtype or t.shape != shape):
             raise ValueError(f"{what} need one shape and type")
         s0, s1, s2 = t.stride()
         if s2 != 1 or (s1 != hd and heads > 1):
@@ -864,26 +863,33 @@ def gpt2_rotary_turns(rot, base=10000.0, scaling="plain", factor=1.0, context=10
     return turns
 
 
-def _here(what, device, *tensors):
+def _here(what, device, tensors):
     for t in tensors:
         if t is not None and t.get_device() != device:
             raise _elsewhere(what)
 
 
-def _rotary(what, q, k, pos, turns, gammas):
+def _dense(t, dtype):
+    """Contiguous, of one dimension? (One value's stride says nothing, so the quick look may miss.)"""
+    return t.dtype is dtype and (t.stride() == _ONE or (t.dim() == 1 and t.is_contiguous()))
+
+
+def _rotary(what, q, k, pos, turns, q_gamma, k_gamma):
     """Checks what a rotation reads beside its rows; rows, heads of q and of k, head size, rotated values."""
     n, hq, hd = q.shape
     m, hk, d = k.shape
-    if m != n or d != hd or k.dtype is not q.dtype:
+    dtype = q.dtype
+    if m != n or d != hd or k.dtype is not dtype:
         raise ValueError(f"{what}: k like q in rows, type and head size is needed")
-    if pos.dtype is not _torch.int32 or pos.shape != (n,) or not pos.is_contiguous():
+    if not _dense(pos, _torch.int32) or pos.nbytes != 4 * n:
         raise ValueError(f"{what}: pos: contiguous int32 of shape [rows] is needed")
-    if turns.dtype is not _torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
+    if not _dense(turns, _torch.int64):
         raise ValueError(f"{what}: turns: contiguous int64 of shape [rot / 2] is needed")
-    for t in gammas:
-        if t is not None and (t.dtype is not q.dtype or t.shape != (hd,) or not t.is_contiguous()):
-            raise ValueError(f"{what}: gammas: contiguous {q.dtype} of shape [hd] is needed")
-    return n, hq, hk, hd, 2 * turns.shape[0]
+    if not (q_gamma is k_gamma is None):
+        for t in (q_gamma, k_gamma):
+            if t is not None and (not _dense(t, dtype) or t.numel() != hd):
+                raise ValueError(f"{what}: gammas: contiguous {dtype} of shape [hd] is needed")
+    return n, hq, hk, hd, turns.nbytes // 4
 
 
 def gpt2_op_qk_norm_rotary_forward(qo, ko, q, k, pos, turns, q_gamma=None, k_gamma=None, eps=None, interleaved=False,
@@ -896,9 +902,13 @@ def gpt2_op_qk_norm_rotary_forward(qo, ko, q, k, pos, turns, q_gamma=None, k_gam
     dt = _mode_of("q", q)
     sq, sqo = _rows("q and qo", q, qo)
     sk, sko = _rows("k and ko", k, ko)
-    sizes = _rotary(what, q, k, pos, turns, (q_gamma, k_gamma))
+    sizes = _rotary(what, q, k, pos, turns, q_gamma, k_gamma)
     device, st = _where(stream)
-    _here(what, device, q, k, qo, ko, pos, turns, q_gamma, k_gamma)
+    if not (device == q.get_device() == k.get_device() == qo.get_device() == ko.get_device() == pos.get_device()
+            == turns.get_device()):
+        raise _elsewhere(what)
+    if not (q_gamma is k_gamma is None):
+        _here(what, device, (q_gamma, k_gamma))
     check(lib.gpt2_op_qk_norm_rotary_forward(dt, qo.data_ptr(), sqo, ko.data_ptr(), sko, q.data_ptr(), sq, k.data_ptr(),
                                              sk, _p(q_gamma), _p(k_gamma), pos.data_ptr(), turns.data_ptr(), *sizes,
                                              bool(interleaved), eps is not None, eps or 0.0, amplitude, st), what)
@@ -913,15 +923,15 @@ def gpt2_op_qk_norm_rotary_backward(dq, dk, dqo, dko, q, k, pos, turns, q_gamma=
     dt = _mode_of("q", q)
     sq, sdqo, sdq = _rows("q, dqo and dq", q, dqo, dq)
     sk, sdko, sdk = _rows("k, dko and dk", k, dko, dk)
-    n, hq, hk, hd, rot = _rotary(what, q, k, pos, turns, (q_gamma, k_gamma))
+    n, hq, hk, hd, rot = _rotary(what, q, k, pos, turns, q_gamma, k_gamma)
     weights = dq_gamma is not None or dk_gamma is not None
     if weights and eps is None:
         raise ValueError("dq_gamma and dk_gamma come with a norm")
     for t in (dq_gamma, dk_gamma):
-        if t is not None and (t.dtype is not _torch.float32 or t.shape != (hd,) or not t.is_contiguous()):
+        if t is not None and (not _dense(t, _torch.float32) or t.nbytes != 4 * hd):
             raise ValueError("dq_gamma and dk_gamma: contiguous float32 of shape [hd] is needed")
     device, st = _where(stream)
-    _here(what, device, q, k, dq, dk, dqo, dko, pos, turns, q_gamma, k_gamma, dq_gamma, dk_gamma)
+    _here(what, device, (q, k, dq, dk, dqo, dko, pos, turns, q_gamma, k_gamma, dq_gamma, dk_gamma))
     nb = lib.gpt2_op_qk_norm_rotary_backward_scratch(n, hd) if weights else 0
     args = (dt, dq.data_ptr(), sdq, dk.data_ptr(), sdk, _p(dq_gamma), _p(dk_gamma), dqo.data_ptr(), sdqo,
             dko.data_ptr(), sdko, q.data_ptr(), sq, k.data_ptr(), sk, _p(q_gamma), _p(k_gamma), pos.data_ptr(),
@@ -1002,7 +1012,7 @@ def gpt2_op_linear_classifier_backward(dx, dw, x, w, targets, lse, V, dloss=None
 
 class AdamWTensors:
     """The tensors of gpt2_op_adamw_many calls, checked once; holds them while it lives. From gpt2_adamw_tensors."""
-    __slots__ = ("array", "count", "grads", "bits", "device", "scratch", "values", "mode", "held")
+    __slots__ = ("array", "address", "count", "grads", "bits", "device", "scratch", "values", "mode", "held")
 
 
 def gpt2_adamw_tensors(masters, grads, ms, vs, params=None, m_scales=None, v_scales=None, weight_decay=0.0,
@@ -1060,9 +1070,10 @@ def gpt2_adamw_tensors(masters, grads, ms, vs, params=None, m_scales=None, v_sca
         if m_values is not None:
             values[0][i], values[1][i] = _p(of["m_values"][0]), _p(of["v_values"][0])
     if m_values is not None:
-        h.values = values
-    h.scratch = load_library().gpt2_op_adamw_many_scratch(h.array, n)
-    h.held = (list(masters), columns)
+        h.values = tuple(ctypes.addressof(v) for v in values)
+    h.address = ctypes.addressof(h.array)
+    h.scratch = load_library().gpt2_op_adamw_many_scratch(h.address, n)
+    h.held = (list(masters), columns, values)
     return h
 
 
@@ -1083,7 +1094,7 @@ def gpt2_op_adamw_many(tensors, lr, beta1, beta2, eps, t, grad_scale=1.0, max_gr
     nb = tensors.scratch if max_grad_norm > 0 or grad_norm is not None else 0
     sc = _borrow(nb, st) if nb else None
     try:
-        check(lib.gpt2_op_adamw_many(tensors.array, tensors.count, tensors.grads, tensors.bits, lr, beta1, beta2, eps,
+        check(lib.gpt2_op_adamw_many(tensors.address, tensors.count, tensors.grads, tensors.bits, lr, beta1, beta2, eps,
                                      grad_scale, max_grad_norm, _p(grad_norm), t, seed, sc, nb, st), what)
     finally:
         if sc:
@@ -1098,7 +1109,7 @@ def gpt2_op_adamw_many_states(tensors, stream=None):
     device, st = (_tc(), _where(stream))[1]
     if tensors.device != device:
         raise _elsewhere(what)
-    check(load_library().gpt2_op_adamw_many_states(tensors.array, *tensors.values, tensors.count, tensors.mode, st), what)
+    check(load_library().gpt2_op_adamw_many_states(tensors.address, *tensors.values, tensors.count, tensors.mode, st), what)
 
 
 def gpt2_op_gelu_forward(g, u, stream=None):

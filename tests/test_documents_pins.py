@@ -209,7 +209,7 @@ def test_rotary_refuses(bad):
 
 @pytest.mark.parametrize("bad", [dict(dtype=7), dict(N=-1), dict(C=12), dict(C=0), dict(V=0), dict(losses=None),
                                  dict(lse=None), dict(x=None), dict(w=None), dict(targets=None), dict(x=P + 8),
-                                 dict(w=P + 4), dict(N=1 << 28), dict(V=1 << 28), dict(N=(1 << 31) - 1, C=8)], ids=str)
+                                 dict(w=P + 4), dict(N=1 << 28), dict(V=1 << 28), dict(N=(1 << 31) - 1, C=8), dict(N=1 << 27, V=1 << 27, C=8)], ids=str)
 def test_classifier_refuses(bad):
     lib = g.load_library(build=True)
     c = dict(dtype=1, losses=P, lse=P, x=P, w=P, targets=P, N=4, C=64, V=50)

@@ -170,6 +170,26 @@ def test_rotary_repeats_and_follows_graphs_and_streams():
     assert all(torch.equal(a, b) for a, b in zip(out, later)) and not torch.equal(out[0], first[0])
 
 
+def test_rotary_of_rows_more_than_31_bits_apart():
+    stride = (1 << 30) + 8
+    buf = torch.zeros(2 * stride + 256, device="cuda", dtype=BF)
+    q, k = buf.as_strided((3, 2, 64), (stride, 64, 1)), buf[128:].as_strided((3, 1, 64), (stride, 64, 1))
+    a, b = rnd(3, 2, 64, dtype=BF), rnd(3, 1, 64, dtype=BF)
+    q.copy_(a)
+    k.copy_(b)
+    pos, turns = torch.tensor([3, 70, 900], device="cuda").int(), g.gpt2_rotary_turns(64).cuda()
+    g.gpt2_op_qk_norm_rotary_forward(q, k, q, k, pos, turns, eps=1e-5)
+    for x, y in ((a, q), (b, k)):
+        near(y, *R.rotary(x.double(), pos, turns, None, 1e-5), "far rows")
+    da, db = rnd(3, 2, 64, dtype=BF), rnd(3, 1, 64, dtype=BF)
+    q.copy_(da)
+    k.copy_(db)
+    g.gpt2_op_qk_norm_rotary_backward(q, k, q, k, a, b, pos, turns, eps=1e-5)
+    for dy, x, y in ((da, a, q), (db, b, k)):
+        dx, _, bound, _ = R.rotary_backward(dy.double(), x.double(), pos, turns, None, 1e-5)
+        near(y, dx, bound, "far rows")
+
+
 # ---------------------------------------------------------------- cross entropy of hidden states
 
 def hidden(N, C, V, Vp=None, dtype=BF, std=2.5):
@@ -217,6 +237,12 @@ def test_classifier(dtype, dw_dtype, N, C, V):
 def test_classifier_in_pieces(dtype):
     # 70000 rows: pieces of 2048 columns, the last of them ragged
     classifier_case(70000, 16, 4357, dtype, F32, Vp=4400)
+
+
+@pytest.mark.parametrize("C", [768, 1024, 640])
+def test_classifier_adds_dx_from_piece_to_piece(C):
+    # two pieces; dx in 192-wide tiles of CTA pairs, in 256-wide ones, in tiles of one CTA
+    classifier_case(8192, C, 17001, BF, BF, dlse=False)
 
 
 def test_classifier_of_the_models_vocabulary():
@@ -374,6 +400,83 @@ def test_classifier_reports_a_wait_that_runs_out():
     assert torch.equal(right[0], again[0]) and torch.equal(right[1], again[1])
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_classifier_with_logits_of_minus_infinity(dtype):
+    N, C, V = 20, 64, 300
+    x, w, t = hidden(N, C, V, 304, dtype)
+    x = x.abs() + 1
+    w[40:200] = -math.inf  # whole chunks of the vocabulary
+    t.copy_(torch.arange(N))
+    t[7] = 60
+    losses, lse = forward(x, w, t, V)
+    keep = torch.cat((w[:40], w[200:V]))
+    want = R.classifier(x.double(), keep.double(), t, len(keep))
+    ok = torch.arange(N, device="cuda") != 7
+    near(losses[ok], want[0][ok], want[2][ok], "losses")
+    near(lse, want[1], want[3], "lse")
+    assert losses[7] == math.inf
+    w[:V] = -math.inf
+    losses, lse = forward(x, w, t, V)
+    assert (losses == math.inf).all() and (lse == -math.inf).all()
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    g.gpt2_op_linear_classifier_backward(dx, dw, x, w, t, lse, V, dloss=torch.ones(N, device="cuda"))
+    assert not dw.any()
+    for bad in (math.nan, math.inf):
+        x, w, t = hidden(N, C, V, 304, dtype)
+        x[3, 5] = bad
+        losses, lse = forward(x, w, t, V)
+        assert torch.isnan(losses[3]) and torch.isnan(lse[3])
+        assert torch.isfinite(losses[:3]).all() and torch.isfinite(losses[4:]).all()
+
+
+def test_classifier_of_more_values_than_31_bits():
+    # dz has 2^31 values and more, the statistics 4 GB; rows from both ends and the middle are looked at
+    N, C, V = (1 << 27) + 5, 8, 15
+    x = torch.randint(-8, 9, (N, C), device="cuda", dtype=torch.int8).to(BF)
+    _, w, _ = hidden(1, C, V, 16)
+    t = torch.randint(0, V, (N,), device="cuda", dtype=torch.int32)
+    losses, lse = forward(x, w, t, V)
+    d = torch.zeros(N, device="cuda")
+    at = torch.tensor([0, 1, 127, 128, N // 2, (1 << 26) + 3, N - 130, N - 2, N - 1], device="cuda")
+    d[at] = 1.0
+    dx, dw = torch.full_like(x, math.nan), torch.empty(16, C, device="cuda")
+    g.gpt2_op_linear_classifier_backward(dx, dw, x, w, t, lse, V, dloss=d)
+    want = R.classifier(x[at].double(), w.double(), t[at], V)
+    near(losses[at], want[0], want[2], "losses")
+    near(lse[at], want[1], want[3], "lse")
+    rx, rw, bx, bw = R.classifier_backward(x[at].double(), w.double(), t[at], V, d[at].double(), None, BF)
+    near(dx[at], rx, bx, "dx")
+    near(dw[:V], rw, bw, "dw")  # (the other rows add zeros)
+    dx[at] = 0
+    assert not dx.any()
+
+
+def test_classifier_graphs_that_share_a_pool():
+    V, pool, graphs = 777, torch.cuda.graph_pool_handle(), []
+    for N, C in ((300, 64), (700, 128)):
+        x, w, t = hidden(N, C, V, 784)
+        out = [torch.empty(N, device="cuda"), torch.empty(N, device="cuda"), torch.empty_like(x), torch.empty_like(w)]
+        d = rnd(N)
+
+        def run(x=x, w=w, t=t, out=out, d=d):
+            g.gpt2_op_linear_classifier_forward(out[0], out[1], x, w, t, V)
+            g.gpt2_op_linear_classifier_backward(out[2], out[3], x, w, t, out[1], V, dloss=d)
+        run()
+        first = [o.clone() for o in out]
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, pool=pool):
+            run()
+        graphs.append((graph, out, first, run))  # (run holds the operands that the graph reads)
+    for _ in range(3):
+        for graph, out, *_ in graphs:
+            for o in out:
+                o.zero_()
+            graph.replay()
+        for _, out, first, _ in graphs:
+            assert all(torch.equal(a, b) for a, b in zip(out, first))
+
+
 # ---------------------------------------------------------------- AdamW over many tensors
 
 HP = dict(lr=1e-2, beta1=0.9, beta2=0.95, eps=1e-8)
@@ -412,8 +515,8 @@ def held(s):
     return {k: [x.clone() for x in v] for k, v in s.items() if k != "weight_decay"}
 
 
-def compare(before, s, t, factor, seed=0):
-    """Every tensor of s after step t against the oracle's step from `before`."""
+def compare(before, s, t, factor, seed=0, start=0):
+    """Every tensor of s (from its start-th value on) after step t against the oracle's step from `before`."""
     eight = "m_scales" in s
     for i, master in enumerate(s["masters"]):
         n = master.numel()
@@ -439,7 +542,7 @@ def compare(before, s, t, factor, seed=0):
             near(s["vs"][i], v, ev, f"v {i}")
             continue
         for x, ex, code, scale, kind, u in zip((m, v), (em, ev), ("ms", "vs"), ("m_scales", "v_scales"), "mv",
-                                               R.draws(n, i, t, seed, "cuda")):
+                                               R.draws(n, i, t, seed, "cuda", start)):
             sc = s[scale][i].long()
             lo, hi = R.scales(x.abs() - ex, kind), R.scales(x.abs() + ex, kind)
             assert ((lo <= sc) & (sc <= hi)).all(), f"scale of {kind} {i}"
@@ -538,6 +641,28 @@ def test_adamw_many_keeps_a_nan_to_itself():
                 at = slice(b * 128, (b + 1) * 128)
                 assert torch.equal(clean["ms"][0][at], s["ms"][0][at]) and torch.equal(clean["vs"][0][at], s["vs"][0][at])
             assert torch.equal(clean["masters"][0][same], s["masters"][0][same])
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_adamw_many_of_more_values_than_31_bits(bits):
+    n, tail = (1 << 31) + 4096 + 77, 3 * 128 + 77
+    moment, kw = (torch.uint8 if bits == 8 else F32), dict(device="cuda")
+    s = {"masters": [torch.zeros(n, **kw)], "grads": [torch.zeros(n, dtype=BF, **kw)], "weight_decay": [0.1],
+         "ms": [torch.zeros(n, dtype=moment, **kw)], "vs": [torch.zeros(n, dtype=moment, **kw)], "params": [None]}
+    if bits == 8:
+        s |= {k: [torch.zeros(-(-n // 128), dtype=torch.uint8, **kw)] for k in ("m_scales", "v_scales")}
+    s["masters"][0][-tail:] = rnd(tail)
+    s["grads"][0][-tail:] = rnd(tail)
+    h = g.gpt2_adamw_tensors(**s)
+    ends = lambda s: {k: [x if x is None else x[-(4 if k.endswith("scales") else tail):].clone() for x in v]  # noqa: E731
+                      if k != "weight_decay" else v for k, v in s.items()}
+    before = ends(s)
+    norm = torch.empty(1, **kw)
+    g.gpt2_op_adamw_many(h, **HP, t=3, max_grad_norm=2.0, grad_norm=norm, seed=4)
+    want = before["grads"][0].double().norm().item()
+    assert abs(norm.item() - want) <= 600 * R.U * want
+    compare(before, ends(s), 3, 2.0 / (want + 1e-6), 4, start=n - tail)
+    assert not s["masters"][0][:-tail].any() and not s["ms"][0][:-tail].any()
 
 
 def test_eight_bit_moments_follow_the_gradients_size():
