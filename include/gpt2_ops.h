@@ -482,8 +482,8 @@ int gpt2_op_linear_classifier_forward(int dtype, float* losses, float* lse, cons
  * to be finite all the same: the products add 0 times them). dw [Vp, C], Vp >= V,
  * Vp % 8 == 0: fp32 (dw_fp32 = 1; the only form in fp32) or bf16; rows from V
  * on get 0. accumulate (fp32 dw only): dw += instead, rows from V on stay. In
- * bf16 dz is rounded to bf16 for the products, as gpt2_op_classifier's dlogits
- * are: half a step (2^-8) of each value; sums are fp32. p carries lse's own
+ * bf16 dz is rounded to bf16 for the products, in units of the largest |dloss|
+ * and |dloss + dlse|: half a step (2^-8) of each value; sums are fp32. p carries lse's own
  * rounding (|lse| 2^-24, relative). Deterministic (no atomics). dx and dw must
  * not overlap the inputs or each other. Limits as in the forward; N = 0 sets
  * dw to 0 (or leaves it, with accumulate). Scratch: a piece of dz (about 256 MB,

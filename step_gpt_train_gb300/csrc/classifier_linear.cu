@@ -13,7 +13,10 @@
 // dW are whole, and what is added to from piece to piece is dx, N x C values,
 // where pieces of rows would add to V x C. Its values are added in fp32 by the
 // copies that store them (one writer for each value in a launch, so the order
-// is fixed).
+// is fixed). dz is rounded to bf16 for the products, in units of the largest
+// |dloss| and |dloss + dlse|, by which the products' sums are scaled in fp32:
+// a mean's 1 / n, the same in every row, would otherwise lose up to half a step
+// (2^-8) of the whole gradient, in one direction.
 //
 // fp32: the same with products of fp32 FMA (classifier_linear_f32.cu).
 #include "common.cuh"
@@ -111,20 +114,45 @@ __global__ void __launch_bounds__(STRANDS * ROWS) join_kernel(float* __restrict_
     losses[row] = loss < 0.f ? 0.f : loss;
 }
 
-__global__ void __launch_bounds__(256) round_kernel(bf16* __restrict__ out, const float* __restrict__ in, int64_t n) {
+// out = in times *scale.
+__global__ void __launch_bounds__(256) round_kernel(bf16* __restrict__ out, const float* __restrict__ in, int64_t n,
+                                                    const float* __restrict__ scale) {
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
     if (i >= n) return;
+    const float s = *scale;
     float f[8];
     load8_stream(in + i, f);
+#pragma unroll
+    for (int j = 0; j < 8; j++) f[j] *= s;
     store8(out + i, f);
 }
 
-// Targets out of range, in the backward.
-__global__ void __launch_bounds__(256) check_targets_kernel(const int32_t* __restrict__ targets, int N, int V,
-                                                            int* status) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i < N && (targets[i] < 0 || targets[i] >= V)) set_status(status, GPT2_FLAG_TARGET_RANGE);
+// Targets out of range; and the largest finite |dloss| and |dloss + dlse| into *scale (0 where no row counts): by one
+// block as it is, by several as float bits (the caller zeroes them), whose largest is the same in any order.
+__global__ void __launch_bounds__(1024) rows_kernel(float* __restrict__ scale, const int32_t* __restrict__ targets,
+                                                    const float* __restrict__ dloss, const float* __restrict__ dlse,
+                                                    int N, int V, int* status) {
+    __shared__ float sm[32];
+    float m = 0.f;
+    bool bad = false;
+    for (int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x; i < N; i += (int64_t)gridDim.x * 1024) {
+        const float d = dloss ? dloss[i] : 0.f, a = d + (dlse ? dlse[i] : 0.f);
+        if (isfinite(d)) m = fmaxf(m, fabsf(d));
+        if (isfinite(a)) m = fmaxf(m, fabsf(a));
+        bad |= targets[i] < 0 || targets[i] >= V;
+    }
+    if (bad) set_status(status, GPT2_FLAG_TARGET_RANGE);
+    if (!scale) return;
+    m = warp_max(m);
+    if (threadIdx.x % 32 == 0) sm[threadIdx.x / 32] = m;
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
+    m = warp_max(sm[threadIdx.x]);
+    if (threadIdx.x) return;
+    if (gridDim.x == 1) *scale = m;
+    else atomicMax(reinterpret_cast<unsigned*>(scale), __float_as_uint(m));
 }
+constexpr int ROWS_A_BLOCK = 32768;
 
 }  // namespace
 
@@ -187,13 +215,13 @@ size_t products_scratch(int dtype, int N, int C, int V, int dw_fp32, int accumul
     return most;
 }
 
-// A piece of dz; bf16: dx in fp32; the products' own.
+// bf16: the scale; a piece of dz; bf16: dx in fp32; the products' own.
 struct BackwardScratch {
     size_t dz, dx, own;
     BackwardScratch(int dtype, int N, int C, const Pieces& p) {
         const bool bf = dtype == GPT2_MODE_BF16;
-        dz = 0;
-        dx = round256((size_t)N * p.width * (bf ? 2 : 4));
+        dz = bf ? 256 : 0;
+        dx = dz + round256((size_t)N * p.width * (bf ? 2 : 4));
         own = dx + (bf ? round256((size_t)N * C * 4) : 0);
     }
 };
@@ -220,8 +248,11 @@ int launch_linear_classifier_backward(int dtype, void* dx, void* dw, int dw_fp32
     if (!accumulate && done < Vp &&
         cudaMemsetAsync((char*)dw + done * C * es, 0, (size_t)(Vp - done) * C * es, s) != cudaSuccess)
         return GPT2_ERR_CUDA;
-    if (status) {
-        check_targets_kernel<<<(N + 255) / 256, 256, 0, s>>>(targets, N, V, status);
+    float* scale = bf ? (float*)scratch : nullptr;
+    if (bf || status) {
+        const int blocks = N <= ROWS_A_BLOCK ? 1 : N / ROWS_A_BLOCK < 152 ? N / ROWS_A_BLOCK : 152;
+        if (bf && blocks > 1 && cudaMemsetAsync(scale, 0, 4, s) != cudaSuccess) return GPT2_ERR_CUDA;
+        rows_kernel<<<blocks, 1024, 0, s>>>(scale, targets, dloss, dlse, N, V, status);
         launches++;
     }
     HeadEpi e = {};
@@ -230,6 +261,7 @@ int launch_linear_classifier_backward(int dtype, void* dx, void* dw, int dw_fp32
     e.dloss = dloss;
     e.dlse = dlse;
     e.vocab = V;
+    e.scale = scale;
     for (int i = 0; i < p.n; i++) {
         const int v0 = i * p.width, cols = V - v0 < p.width ? V - v0 : p.width;
         e.first = v0;
@@ -239,8 +271,8 @@ int launch_linear_classifier_backward(int dtype, void* dx, void* dw, int dw_fp32
             const int pitch = round8(cols);
             n[0] = launch_head_dz(dz, x, wp, N, pitch, C, cols, e, status, s);
             n[1] = launch_head_dx(sum, dz, wp, N, C, pitch, cols, i > 0, own, status, s);
-            n[2] = launch_matmul(dtype, (char*)dw + (int64_t)v0 * C * es, dw_fp32, dz, 1, x, 1, nullptr, pitch, C, N, own,
-                                 status, s, accumulate);
+            n[2] = launch_head_dw((char*)dw + (int64_t)v0 * C * es, dw_fp32, dz, x, pitch, C, N, scale, accumulate, own,
+                                  status, s);
         } else {
             const float *xf = (const float*)x, *wp = (const float*)w + (int64_t)v0 * C;
             n[0] = launch_head_f32_dz((float*)dz, xf, wp, N, cols, C, e, s);
@@ -254,7 +286,7 @@ int launch_linear_classifier_backward(int dtype, void* dx, void* dw, int dw_fp32
     }
     if (bf) {
         const int64_t values = (int64_t)N * C;
-        round_kernel<<<(unsigned)((values / 8 + 255) / 256), 256, 0, s>>>((bf16*)dx, sum, values);
+        round_kernel<<<(unsigned)((values / 8 + 255) / 256), 256, 0, s>>>((bf16*)dx, sum, values, scale);
         launches++;
     }
     return launches;

@@ -70,8 +70,9 @@ constexpr int EPI_GELU = 1;  // u = bf16(x); D = gelu'(u), D2 = gelu(u): the MLP
 constexpr int EPI_MUL = 2;   // D = bf16(x) * aux: the input gradient through that GELU, aux = gelu'(u)
 // The linear classifier (x: logits of a piece of the vocabulary, which no one stores):
 constexpr int EPI_LSE = 3;   // nothing of x is stored: a row's maximum and sum of exponentials in each half tile
-constexpr int EPI_DZ = 4;    // D = bf16((dloss + dlse) exp(x - lse) - dloss [column = target])
+constexpr int EPI_DZ = 4;    // D = bf16(((dloss + dlse) exp(x - lse) - dloss [column = target]) / scale)
 constexpr int EPI_ADD = 5;   // D (fp32) = or += x, added by the copy that stores it (one writer for each value)
+constexpr int EPI_SCALE = 6; // D = x times a device scalar (split products: the reduce kernel scales their sum)
 constexpr bool epi_stores(int epi) { return epi != EPI_LSE; }
 
 struct GemmArgs {
@@ -102,6 +103,7 @@ template <int EPI> struct ArgsOf { typedef GemmArgs type; };
 template <> struct ArgsOf<EPI_LSE> { typedef HeadGemmArgs type; };
 template <> struct ArgsOf<EPI_DZ> { typedef HeadGemmArgs type; };
 template <> struct ArgsOf<EPI_ADD> { typedef HeadGemmArgs type; };
+template <> struct ArgsOf<EPI_SCALE> { typedef HeadGemmArgs type; };
 __device__ __forceinline__ const HeadEpi* head_of(const HeadGemmArgs& g) { return &g.head; }
 __device__ __forceinline__ const HeadEpi* head_of(const GemmArgs&) { return nullptr; }
 
@@ -195,7 +197,7 @@ __device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, uint32_t src,
 // the tile's half (negative or past it where it lies elsewhere).
 struct RowHead {
     float m, s;      // EPI_LSE: the running maximum and the sum of exp(z - maximum)
-    float a, d, lse; // EPI_DZ: dloss + dlse, dloss, lse in base 2
+    float a, d, lse; // EPI_DZ: dloss + dlse and dloss in units of the scale, lse in base 2
     int at;
 };
 constexpr float LOG2E = 1.4426950408889634f;
@@ -286,7 +288,8 @@ __device__ __forceinline__ void epi_chunk(const uint32_t (&r)[32], const float* 
     } else {
 #pragma unroll
         for (int j = 0; j < 32; j++)
-            f[j] = (F8 ? __uint_as_float(r[j]) * alpha : __uint_as_float(r[j])) + (bias_s ? bias_s[j] : 0.f);
+            f[j] = (F8 || EPI == EPI_SCALE ? __uint_as_float(r[j]) * alpha : __uint_as_float(r[j])) +
+                   (bias_s ? bias_s[j] : 0.f);
     }
     if (EPI == EPI_MUL) {
         // the linear output rounded to bf16 (as a separate pass would read it),
@@ -358,8 +361,10 @@ template <int EPI> __device__ __forceinline__ void head_begin(const HeadEpi* e, 
             if (t < 0 || t >= e->vocab) t = 0;
             h.at = t - (v0 + e->first);
             if (EPI == EPI_DZ) {
-                h.d = e->dloss ? e->dloss[row] : 0.f;
-                h.a = h.d + (e->dlse ? e->dlse[row] : 0.f);
+                const float d = e->dloss ? e->dloss[row] : 0.f, a = d + (e->dlse ? e->dlse[row] : 0.f);
+                const float scale = *e->scale;  // 0: no row counts
+                h.d = d != 0.f ? d / scale : 0.f;
+                h.a = a != 0.f ? a / scale : 0.f;
                 h.lse = e->lse[row] * LOG2E;
             }
         }
@@ -559,7 +564,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         Stager<NB> stg{stage, smem_addr(stage), 0};
         const bool use_bias = g.bias != nullptr && !g.partials;
         const HeadEpi* he = head_of(g);
-        const float alpha = F8 ? *g.a_scale * *g.b_scale : 1.f;
+        float alpha = F8 ? *g.a_scale * *g.b_scale : 1.f;
+        if constexpr (EPI == EPI_SCALE) alpha = g.partials ? 1.f : *he->scale;
         // EPI_MUL column sums: each warp writes the sums of its 32 rows of a
         // tile, row 4 * mt + quad of g.colsum
         const bool want_csum = EPI == EPI_MUL && g.colsum != nullptr;
@@ -995,6 +1001,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         Stager<P_NBUF> stg{stage, smem_addr(stage), 0};
         const bool use_bias = g.bias != nullptr && !g.partials;
         const HeadEpi* he = head_of(g);
+        float alpha = 1.f;
+        if constexpr (EPI == EPI_SCALE) alpha = g.partials ? 1.f : *he->scale;
         const bool want_csum = EPI == EPI_MUL && g.colsum != nullptr;
         int acc = 0;
         uint32_t acc_phase = 0;
@@ -1058,7 +1066,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                 const bool more = c + 1 < nchunks;
                 if (more) tc_ld32_issue(tbase + (uint32_t)((cfirst + c + 1) * 32), rb);
                 epi_chunk<EPI>(ra, bias_at(c), fp32_out, stg, &tmD, &tmD2, aux[0], xcol(c), ys, z,
-                               ncols(c), lane, 1.f, csum_at(c), nrows, nullptr, &head, c * 32, target,
+                               ncols(c), lane, alpha, csum_at(c), nrows, nullptr, &head, c * 32, target,
                                    EPI == EPI_ADD && he->add);
                 if (EPI == EPI_MUL && c + 2 < CHUNKS) load_aux(c + 2, aux[0]);
                 __syncwarp();
@@ -1067,7 +1075,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                 const bool more2 = c + 2 < nchunks;
                 if (more2) tc_ld32_issue(tbase + (uint32_t)((cfirst + c + 2) * 32), ra);
                 epi_chunk<EPI>(rb, bias_at(c + 1), fp32_out, stg, &tmD, &tmD2, aux[1], xcol(c + 1), ys,
-                               z, ncols(c + 1), lane, 1.f, csum_at(c + 1), nrows, nullptr, &head, c * 32 + 32,
+                               z, ncols(c + 1), lane, alpha, csum_at(c + 1), nrows, nullptr, &head, c * 32 + 32,
                                target, EPI == EPI_ADD && he->add);
                 if (EPI == EPI_MUL && c + 3 < CHUNKS) load_aux(c + 3, aux[1]);
                 __syncwarp();
@@ -1111,9 +1119,12 @@ __global__ void __launch_bounds__(P_THREADS, 1)
 // Split-K reduce: D[m][n] (fp32) = bias[n] (if any) + the partial tiles of
 // the tile of (m, n), added in split order; with accumulate, added to D's
 // current value. 8 consecutive columns per thread (N and BN are multiples of 8).
+// SCALED: the partial tiles' sum times *scale.
+template <bool SCALED>
 __global__ void __launch_bounds__(256) split_reduce_kernel(float* __restrict__ D, const float* __restrict__ partial,
                                                            const bf16* __restrict__ bias, int M, int N, int BN,
-                                                           int n_tiles, int splits, int accumulate) {
+                                                           int n_tiles, int splits, int accumulate,
+                                                           const float* __restrict__ scale) {
     // 32-bit element index (the launcher keeps M * N < 2^31)
     const int i = (blockIdx.x * blockDim.x + threadIdx.x) * 8;
     if (i >= M * N) return;
@@ -1122,8 +1133,8 @@ __global__ void __launch_bounds__(256) split_reduce_kernel(float* __restrict__ D
     const int64_t tile_elems = (int64_t)BM * BN;
     const float* p = partial + tile * splits * tile_elems + (int64_t)(m % BM) * BN + n % BN;
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (bias) load8(bias + n, acc);
-    if (accumulate) {
+    if (!SCALED && bias) load8(bias + n, acc);
+    if (!SCALED && accumulate) {
         float d[8];
         load8(D + i, d);
 #pragma unroll
@@ -1134,6 +1145,13 @@ __global__ void __launch_bounds__(256) split_reduce_kernel(float* __restrict__ D
         load8(p + sp * tile_elems, v);
 #pragma unroll
         for (int j = 0; j < 8; j++) acc[j] += v[j];
+    }
+    if (SCALED) {
+        float d[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (accumulate) load8(D + i, d);
+        const float s = *scale;
+#pragma unroll
+        for (int j = 0; j < 8; j++) acc[j] = fmaf(acc[j], s, d[j]);
     }
     store8(D + i, acc);
 }
@@ -1289,6 +1307,9 @@ bool launch_tc_layout(int epi, int a_mn, int b_mn, const CUtensorMap& ma, const 
     } else if (epi == EPI_ADD) {
         if (a_mn || !b_mn) return false;
         launch_tc<BN, false, true, EPI_ADD>(ma, mb, md, md2, args, grid, s);
+    } else if (epi == EPI_SCALE) {
+        if (!a_mn || !b_mn) return false;
+        launch_tc<BN, true, true, EPI_SCALE>(ma, mb, md, md2, args, grid, s);
     } else if (!a_mn && !b_mn) {
         launch_tc<BN, false, false, EPI_NONE>(ma, mb, md, md2, args, grid, s);
     } else if (!a_mn && b_mn) {
@@ -1380,10 +1401,11 @@ bool g_pair_mn192 = true;  // 192-wide tiles also with MN-major B
 int g_pair_override = 0;  // > 0: the number of clusters to launch instead of the resident count
 // The pair tile width for this product, or 0 for the one-CTA kernel.
 int use_pair(int M, int N, int K, bool partials, int epi, int b_mn) {
-    const bool plain = epi == EPI_NONE || epi == EPI_LSE || epi == EPI_DZ || epi == EPI_ADD;
+    const bool plain = epi == EPI_NONE || epi == EPI_LSE || epi == EPI_DZ || epi == EPI_ADD ||
+                       epi == EPI_SCALE;
     if (!g_use_pair || (!plain && !g_pair_epi) || partials || M < 512) return 0;
     if (N >= 1024) return 256;
-    return (epi == EPI_NONE || epi == EPI_ADD) && (!b_mn || g_pair_mn192) && N >= 384 && N % 192 == 0 && K >= 2048 && K <= 16384
+    return (epi == EPI_NONE || epi == EPI_ADD || epi == EPI_SCALE) && (!b_mn || g_pair_mn192) && N >= 384 && N % 192 == 0 && K >= 2048 && K <= 16384
                ? 192
                : 0;
 }
@@ -1426,9 +1448,9 @@ int matmul_tc(int epi, void* D, void* D2, const bf16* aux, int d_fp32, const voi
     // (b_rows: the rows of B that are read, where they are fewer than N or, MN-major, K; the rest count as 0)
     const uint64_t rows_of_b = b_rows ? b_rows : b_mn ? K : N;
     if (f8 && (a_mn || b_mn || K % 16 || N % 8)) return GPT2_ERR_ARG;
-    Plan p = make_plan(M, N, f8 ? (K + 1) / 2 : K, epi == EPI_NONE ? d_fp32 : 0);
+    Plan p = make_plan(M, N, f8 ? (K + 1) / 2 : K, epi == EPI_NONE || epi == EPI_SCALE ? d_fp32 : 0);
     // partial tiles for the reduce kernel: split-K, or an fp32 result added to D
-    const bool partials = p.splits > 1 || (accumulate && d_fp32 && epi == EPI_NONE);
+    const bool partials = p.splits > 1 || (accumulate && d_fp32 && (epi == EPI_NONE || epi == EPI_SCALE));
     if (partials && (int64_t)M * N + 2048 >= ((int64_t)1 << 31)) return GPT2_ERR_ARG;  // the reduce uses 32-bit indices
     const int pn = f8 || amax ? 0 : use_pair(M, N, K, partials, epi, b_mn);
     if (pn) {
@@ -1471,6 +1493,9 @@ int matmul_tc(int epi, void* D, void* D2, const bf16* aux, int d_fp32, const voi
         if (pn == 192 && epi == EPI_ADD) {
             if (a_mn || !b_mn) return GPT2_ERR_ARG;
             e = launch_pair<false, true, EPI_ADD, 192>(ma, mb, md, md2, g, pairs, s);
+        } else if (pn == 192 && epi == EPI_SCALE) {
+            if (!a_mn || !b_mn) return GPT2_ERR_ARG;
+            e = launch_pair<true, true, EPI_SCALE, 192>(ma, mb, md, md2, g, pairs, s);
         } else if (pn == 192) {
             if (epi != EPI_NONE) return GPT2_ERR_ARG;
             if (!b_mn)
@@ -1492,6 +1517,9 @@ int matmul_tc(int epi, void* D, void* D2, const bf16* aux, int d_fp32, const voi
         } else if (epi == EPI_ADD) {
             if (a_mn || !b_mn) return GPT2_ERR_ARG;
             e = launch_pair<false, true, EPI_ADD>(ma, mb, md, md2, g, pairs, s);
+        } else if (epi == EPI_SCALE) {
+            if (!a_mn || !b_mn) return GPT2_ERR_ARG;
+            e = launch_pair<true, true, EPI_SCALE>(ma, mb, md, md2, g, pairs, s);
         } else if (!a_mn && !b_mn) {
             e = launch_pair<false, false, EPI_NONE>(ma, mb, md, md2, g, pairs, s);
         } else if (!a_mn && b_mn) {
@@ -1558,8 +1586,13 @@ int matmul_tc(int epi, void* D, void* D2, const bf16* aux, int d_fp32, const voi
     if (partials) {
         const int64_t MN = (int64_t)M * N;
         const int blocks = (int)((MN / 8 + 255) / 256);
-        split_reduce_kernel<<<blocks, 256, 0, s>>>((float*)D, (const float*)scratch, (const bf16*)bias, M, N, p.bn,
-                                                   p.n_tiles, p.splits, accumulate && d_fp32 ? 1 : 0);
+        const int add = accumulate && d_fp32 ? 1 : 0;
+        if (epi == EPI_SCALE)
+            split_reduce_kernel<true><<<blocks, 256, 0, s>>>((float*)D, (const float*)scratch, nullptr, M, N, p.bn,
+                                                             p.n_tiles, p.splits, add, head->scale);
+        else
+            split_reduce_kernel<false><<<blocks, 256, 0, s>>>((float*)D, (const float*)scratch, (const bf16*)bias, M, N,
+                                                              p.bn, p.n_tiles, p.splits, add, nullptr);
         return 2;
     }
     return 1;
@@ -1650,4 +1683,12 @@ int launch_head_dx(float* dx, const void* dz, const void* w, int M, int N, int K
     e.add = add;
     return matmul_tc(whole ? EPI_ADD : EPI_NONE, dx, nullptr, nullptr, 1, dz, 0, w, 1, nullptr, M, N, K, scratch, status, s,
                      add && !whole, nullptr, nullptr, nullptr, &e, rows);
+}
+
+int launch_head_dw(void* dw, int dw_fp32, const void* dz, const void* x, int M, int N, int K, const float* scale,
+                   bool add, void* scratch, int* status, cudaStream_t s) {
+    HeadEpi e = {};
+    e.scale = scale;
+    return matmul_tc(EPI_SCALE, dw, nullptr, nullptr, dw_fp32, dz, 1, x, 1, nullptr, M, N, K, scratch, status, s, add,
+                     nullptr, nullptr, nullptr, &e);
 }

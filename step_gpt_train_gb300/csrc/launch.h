@@ -176,6 +176,7 @@ int launch_rotary(int dtype, const RotaryArgs& a, bool back, float* dq_gamma, fl
 struct HeadEpi {
     const int32_t* targets;      // [M]; outside [0, vocab): 0
     const float *lse, *dloss, *dlse;  // gradients: [M] (dloss, dlse or null: 0)
+    const float* scale;          // gradients: what dz is given in units of, a device scalar
     float2* stats;               // forward: [slots][M] maximum and sum of exp(z - maximum)
     float* target_logit;         // forward: [M]
     int vocab, first;
@@ -191,6 +192,9 @@ int launch_head_dz(void* dz, const void* x, const void* w, int M, int N, int K, 
 size_t head_dx_scratch(int M, int N, int K);
 int launch_head_dx(float* dx, const void* dz, const void* w, int M, int N, int K, int rows, bool add, void* scratch,
                    int* status, cudaStream_t s);
+// dw [M, N] = or (fp32) += *scale dz^T x, dz [K, M], x [K, N]; scratch: matmul_scratch(bf16, M, N, K, dw_fp32, add).
+int launch_head_dw(void* dw, int dw_fp32, const void* dz, const void* x, int M, int N, int K, const float* scale,
+                   bool add, void* scratch, int* status, cudaStream_t s);
 
 // The same in fp32 (classifier_linear_f32.cu): statistics in head_f32_slots(V) slots, dz [M, N], dx [M, N] = or +=
 // dz [M, K] W [K, N], dw [M, N] = or += dz^T x with dz [K, M], x [K, N]; scratch for the two: head_f32_scratch(M, N, K).
