@@ -488,7 +488,7 @@ int gpt2_op_linear_classifier_forward(int dtype, float* losses, float* lse, cons
  * not overlap the inputs or each other. Limits as in the forward; N = 0 sets
  * dw to 0 (or leaves it, with accumulate). Scratch: a piece of dz (about 256 MB,
  * or 2048 columns where that is more), dx in fp32, partial products. */
-size_t gpt2_op_linear_classifier_backward_scratch(int dtype, int N, int C, int V, int dw_fp32, int accumulate);
+size_t gpt2_op_linear_classifier_backward_scratch(int dtype, int N, int C, int V, int Vp, int accumulate);
 int gpt2_op_linear_classifier_backward(int dtype, void* dx, void* dw, int dw_fp32, int accumulate, const void* x,
                                        const void* w, const int32_t* targets, const float* lse, const float* dloss,
                                        const float* dlse, int N, int C, int V, int Vp, void* scratch,

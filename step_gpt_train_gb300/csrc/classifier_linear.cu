@@ -127,19 +127,15 @@ __global__ void __launch_bounds__(256) round_kernel(bf16* __restrict__ out, cons
     store8(out + i, f);
 }
 
-// Targets out of range; and the largest finite |dloss| and |dloss + dlse| into *scale (0 where no row counts): by one
-// block as it is, by several as float bits (the caller zeroes them), whose largest is the same in any order.
-__global__ void __launch_bounds__(1024) rows_kernel(float* __restrict__ scale, const int32_t* __restrict__ targets,
-                                                    const float* __restrict__ dloss, const float* __restrict__ dlse,
-                                                    int N, int V, int* status) {
+// Targets out of range; and the scale (the largest head_magnitude: 0 where no row counts): by one block as it is, by
+// several as float bits (the caller zeroes them), whose largest is the same in any order.
+__global__ void __launch_bounds__(1024) rows_kernel(float* __restrict__ scale, const HeadEpi e, int N, int* status) {
     __shared__ float sm[32];
     float m = 0.f;
     bool bad = false;
     for (int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x; i < N; i += (int64_t)gridDim.x * 1024) {
-        const float d = dloss ? dloss[i] : 0.f, a = d + (dlse ? dlse[i] : 0.f);
-        if (isfinite(d)) m = fmaxf(m, fabsf(d));
-        if (isfinite(a)) m = fmaxf(m, fabsf(a));
-        bad |= targets[i] < 0 || targets[i] >= V;
+        m = fmaxf(m, head_magnitude(e, i));
+        bad |= e.targets[i] < 0 || e.targets[i] >= e.vocab;
     }
     if (bad) set_status(status, GPT2_FLAG_TARGET_RANGE);
     if (!scale) return;
@@ -152,7 +148,7 @@ __global__ void __launch_bounds__(1024) rows_kernel(float* __restrict__ scale, c
     if (gridDim.x == 1) *scale = m;
     else atomicMax(reinterpret_cast<unsigned*>(scale), __float_as_uint(m));
 }
-constexpr int ROWS_A_BLOCK = 32768;
+constexpr int ROWS_A_BLOCK = 32768, FIND_ROWS = 2048;
 
 }  // namespace
 
@@ -201,36 +197,47 @@ int launch_linear_classifier_forward(int dtype, float* losses, float* lse, const
 
 namespace {
 
+// The columns of dz that a piece's products work on: a multiple of 8; the last piece's go on to dw's last row where its
+// buffer has room, so that the rows from V on get their 0 with the others.
+int pitch_of(int v0, int V, int Vp, const Pieces& p) {
+    const int cols = V - v0 < p.width ? V - v0 : p.width;
+    return v0 + p.width >= V && Vp - v0 <= p.width ? Vp - v0 : round8(cols);
+}
+
 // The products' own scratch (parts of split products), over the pieces.
-size_t products_scratch(int dtype, int N, int C, int V, int dw_fp32, int accumulate, const Pieces& p) {
+size_t products_scratch(int dtype, int N, int C, int V, int Vp, int accumulate, const Pieces& p) {
     const bool bf = dtype == GPT2_MODE_BF16;
     size_t most = 0;
-    for (int v0 : {0, (p.n - 1) * p.width}) {
-        const int cols = V - v0 < p.width ? V - v0 : p.width, pitch = bf ? round8(cols) : cols;
-        const size_t a = bf ? head_dx_scratch(N, C, pitch) : head_f32_scratch(N, C, cols);
-        const size_t b = bf ? matmul_scratch(dtype, pitch, C, N, dw_fp32, accumulate) : head_f32_scratch(cols, C, N);
-        most = a > most ? a : most;
-        most = b > most ? b : most;
+    auto need = [&](size_t n) { most = n > most ? n : most; };
+    for (int i = 0; i < p.n; i += p.n > 1 ? p.n - 1 : 1) {
+        const int pitch = pitch_of(i * p.width, V, Vp, p);
+        if (bf) {
+            need(p.n == 1 ? head_scaled_scratch(N, C, pitch, false) : head_dx_scratch(N, C, pitch));
+            need(head_scaled_scratch(pitch, C, N, accumulate));
+        } else {
+            need(head_f32_scratch(N, C, pitch));
+            need(head_f32_scratch(pitch, C, N));
+        }
     }
     return most;
 }
 
-// bf16: the scale; a piece of dz; bf16: dx in fp32; the products' own.
+// bf16: the scale; a piece of dz; bf16 in pieces: dx in fp32; the products' own.
 struct BackwardScratch {
     size_t dz, dx, own;
     BackwardScratch(int dtype, int N, int C, const Pieces& p) {
         const bool bf = dtype == GPT2_MODE_BF16;
         dz = bf ? 256 : 0;
         dx = dz + round256((size_t)N * p.width * (bf ? 2 : 4));
-        own = dx + (bf ? round256((size_t)N * C * 4) : 0);
+        own = dx + (bf && p.n > 1 ? round256((size_t)N * C * 4) : 0);
     }
 };
 
 }  // namespace
 
-size_t linear_classifier_backward_scratch(int dtype, int N, int C, int V, int dw_fp32, int accumulate) {
+size_t linear_classifier_backward_scratch(int dtype, int N, int C, int V, int Vp, int accumulate) {
     const Pieces p = pieces(dtype, N, C, V);
-    return BackwardScratch(dtype, N, C, p).own + products_scratch(dtype, N, C, V, dw_fp32, accumulate, p);
+    return BackwardScratch(dtype, N, C, p).own + products_scratch(dtype, N, C, V, Vp, accumulate, p);
 }
 
 int launch_linear_classifier_backward(int dtype, void* dx, void* dw, int dw_fp32, int accumulate, const void* x,
@@ -244,47 +251,51 @@ int launch_linear_classifier_backward(int dtype, void* dx, void* dw, int dw_fp32
     float* sum = (float*)((char*)scratch + at.dx);
     void* own = (char*)scratch + at.own;
     int launches = 0;
-    const int64_t es = dw_fp32 ? 4 : 2, done = bf ? round8(V) : V;
+    const int64_t es = dw_fp32 ? 4 : 2;
+    const int last = (p.n - 1) * p.width, done = last + pitch_of(last, V, Vp, p);
     if (!accumulate && done < Vp &&
-        cudaMemsetAsync((char*)dw + done * C * es, 0, (size_t)(Vp - done) * C * es, s) != cudaSuccess)
+        cudaMemsetAsync((char*)dw + (int64_t)done * C * es, 0, (size_t)(Vp - done) * C * es, s) != cudaSuccess)
         return GPT2_ERR_CUDA;
-    float* scale = bf ? (float*)scratch : nullptr;
-    if (bf || status) {
-        const int blocks = N <= ROWS_A_BLOCK ? 1 : N / ROWS_A_BLOCK < 152 ? N / ROWS_A_BLOCK : 152;
-        if (bf && blocks > 1 && cudaMemsetAsync(scale, 0, 4, s) != cudaSuccess) return GPT2_ERR_CUDA;
-        rows_kernel<<<blocks, 1024, 0, s>>>(scale, targets, dloss, dlse, N, V, status);
-        launches++;
-    }
     HeadEpi e = {};
     e.targets = targets;
     e.lse = lse;
     e.dloss = dloss;
     e.dlse = dlse;
     e.vocab = V;
-    e.scale = scale;
+    float* scale = e.scale = bf ? (float*)scratch : nullptr;
+    // the scale and the targets' check: by the first product's epilogue for few rows (a launch less), else on their own
+    const bool find = bf && N <= FIND_ROWS;
+    if (!find && (bf || status)) {
+        const int blocks = N <= ROWS_A_BLOCK ? 1 : N / ROWS_A_BLOCK < 152 ? N / ROWS_A_BLOCK : 152;
+        if (bf && blocks > 1 && cudaMemsetAsync(scale, 0, 4, s) != cudaSuccess) return GPT2_ERR_CUDA;
+        rows_kernel<<<blocks, 1024, 0, s>>>(scale, e, N, status);
+        launches++;
+    }
     for (int i = 0; i < p.n; i++) {
         const int v0 = i * p.width, cols = V - v0 < p.width ? V - v0 : p.width;
         e.first = v0;
+        e.find = find && i == 0;
+        const int pitch = pitch_of(v0, V, Vp, p);
         int n[3];
         if (bf) {
             const bf16* wp = (const bf16*)w + (int64_t)v0 * C;
-            const int pitch = round8(cols);
             n[0] = launch_head_dz(dz, x, wp, N, pitch, C, cols, e, status, s);
-            n[1] = launch_head_dx(sum, dz, wp, N, C, pitch, cols, i > 0, own, status, s);
+            n[1] = p.n == 1 ? launch_head_dx_scaled(dx, dz, wp, N, C, pitch, cols, scale, own, status, s)
+                            : launch_head_dx(sum, dz, wp, N, C, pitch, cols, i > 0, own, status, s);
             n[2] = launch_head_dw((char*)dw + (int64_t)v0 * C * es, dw_fp32, dz, x, pitch, C, N, scale, accumulate, own,
                                   status, s);
         } else {
             const float *xf = (const float*)x, *wp = (const float*)w + (int64_t)v0 * C;
-            n[0] = launch_head_f32_dz((float*)dz, xf, wp, N, cols, C, e, s);
-            n[1] = launch_head_f32_dx((float*)dx, (const float*)dz, wp, N, C, cols, i > 0, own, s);
-            n[2] = launch_head_f32_dw((float*)dw + (int64_t)v0 * C, (const float*)dz, xf, cols, C, N, accumulate, own, s);
+            n[0] = launch_head_f32_dz((float*)dz, xf, wp, N, pitch, C, cols, e, s);
+            n[1] = launch_head_f32_dx((float*)dx, (const float*)dz, wp, N, C, pitch, cols, i > 0, own, s);
+            n[2] = launch_head_f32_dw((float*)dw + (int64_t)v0 * C, (const float*)dz, xf, pitch, C, N, accumulate, own, s);
         }
         for (int k = 0; k < 3; k++) {
             if (n[k] < 0) return n[k];
             launches += n[k];
         }
     }
-    if (bf) {
+    if (bf && p.n > 1) {
         const int64_t values = (int64_t)N * C;
         round_kernel<<<(unsigned)((values / 8 + 255) / 256), 256, 0, s>>>((bf16*)dx, sum, values, scale);
         launches++;

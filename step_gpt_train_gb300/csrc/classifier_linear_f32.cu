@@ -7,12 +7,13 @@
 // apart and its columns 16 apart, so that a warp's 16-byte reads meet different
 // banks. Two neighbouring k's of a row are one register pair, and the paired
 // FMA keeps a sum over the even and one over the odd k's: half the instructions
-// of single FMAs, no operand to duplicate, and sums of half the length. The
-// next slice's loads are under way while this one is multiplied. Products with
-// few tiles (dx: N x C outputs, K = V) are cut along k; a second kernel adds
-// the parts in order.
+// of single FMAs, no operand to duplicate, and sums of half the length. Slices
+// are under way two or three ahead: [rows][k] operands by asynchronous copies,
+// [k][rows] ones through registers, which turn them. Products with few tiles
+// (dx: N x C outputs, K = V) are cut along k; a second kernel adds the parts in
+// order.
 //
-// FMA bounds it: 1021 x 128 x 5003, see classifier_linear.cu for the times.
+// 1021 x 128 x 5003 (1.3 GFLOP a product, 17 us at 75 TFLOP/s): TIMES
 #include "common.cuh"
 #include "launch.h"
 #include "tc_common.cuh"
@@ -28,75 +29,60 @@ constexpr int TM = 8, TN = 4;
 
 constexpr int STORE = 0, LSE = 1, DZ = 2;
 
+// Rows, columns and k's are multiples of 4 where vectors run along them (x, w and dz are so laid out).
 struct Product {
     const float *A, *B;
     float* D;          // STORE: [M][N], or the parts [split][M][N]; DZ: [M][N]
     int M, N, K;
+    int b_rows;        // the rows of B that are read (n's, or k's where B is [k][n]); the rest count as 0
     int per_split;     // k's of a part, a multiple of KS
     int accumulate;    // STORE without parts: D +=
     HeadEpi head;
 };
 
-// A slice of an operand: T rows by KS k's from (row0, k0), zero outside. MN: the operand is [k][rows], else [rows][k].
-// Each thread holds two vectors of four between the load and the store.
-//
 // Where a row keeps its k's in shared memory: its four vectors in an order that changes every 8 rows. A warp that stores
 // [k][rows] data writes one value to each of 16 rows 4 apart, 80 words from one to the next: in one order they would meet
 // two banks, in this one eight.
 __device__ __forceinline__ constexpr int place(int row, int k) { return (((k >> 2) ^ (row >> 3)) & 3) * 4 + (k & 3); }
 
-template <bool MN> struct Slice {
+// A slice of an operand: T rows by KS k's from (row0, k0), two vectors of four a thread; zeros outside `rows` and k1.
+// [rows][k]: copied as it is.
+__device__ __forceinline__ void copy_slice(float (*s)[PITCH], const float* p, int rows, int K, int row0, int k0, int k1) {
+#pragma unroll
+    for (int u = 0; u < 2; u++) {
+        const int i = threadIdx.x + u * THREADS, r = row0 + i / 4, k = k0 + i % 4 * 4;
+        const bool in = r < rows && k < k1;
+        const float* from = in ? p + (int64_t)r * K + k : p;
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(&s[i / 4][place(i / 4, i % 4 * 4)]);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(in ? 16 : 0) : "memory");
+    }
+}
+// [k][rows]: through registers, turned when stored.
+struct Turned {
     float f[2][4];
-
-    __device__ __forceinline__ void load(const float* p, int rows, int K, int row0, int k0, int k1) {
+    __device__ __forceinline__ void load(const float* p, int rows, int row0, int k0, int k1) {
 #pragma unroll
         for (int u = 0; u < 2; u++) {
-            const int i = threadIdx.x + u * THREADS;  // 256 vectors
-            const int r = row0 + (MN ? i % 16 * 4 : i / 4), k = k0 + (MN ? i / 16 : i % 4 * 4);
-#pragma unroll
-            for (int j = 0; j < 4; j++) f[u][j] = 0.f;
-            if (MN) {
-                if (k >= k1) continue;
-                const float* q = p + (int64_t)k * rows + r;
-                if (r + 4 <= rows && rows % 4 == 0) {
-                    const float4 v = *reinterpret_cast<const float4*>(q);
-                    f[u][0] = v.x, f[u][1] = v.y, f[u][2] = v.z, f[u][3] = v.w;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        if (r + j < rows) f[u][j] = q[j];
-                }
-            } else {
-                if (r >= rows) continue;
-                const float* q = p + (int64_t)r * K + k;
-                if (k + 4 <= k1 && K % 4 == 0) {
-                    const float4 v = *reinterpret_cast<const float4*>(q);
-                    f[u][0] = v.x, f[u][1] = v.y, f[u][2] = v.z, f[u][3] = v.w;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        if (k + j < k1) f[u][j] = q[j];
-                }
-            }
+            const int i = threadIdx.x + u * THREADS, r = row0 + i % 16 * 4, k = k0 + i / 16;
+            const float4 v = r < rows && k < k1 ? *reinterpret_cast<const float4*>(p + (int64_t)k * rows + r)
+                                                : make_float4(0.f, 0.f, 0.f, 0.f);
+            f[u][0] = v.x, f[u][1] = v.y, f[u][2] = v.z, f[u][3] = v.w;
         }
     }
     __device__ __forceinline__ void store(float (*s)[PITCH]) const {
 #pragma unroll
         for (int u = 0; u < 2; u++) {
             const int i = threadIdx.x + u * THREADS;
-            if (MN) {
 #pragma unroll
-                for (int j = 0; j < 4; j++) s[i % 16 * 4 + j][place(i % 16 * 4, i / 16)] = f[u][j];
-            } else {
-                *reinterpret_cast<float4*>(&s[i / 4][place(i / 4, i % 4 * 4)]) = make_float4(f[u][0], f[u][1], f[u][2], f[u][3]);
-            }
+            for (int j = 0; j < 4; j++) s[i % 16 * 4 + j][place(i % 16 * 4, i / 16)] = f[u][j];
         }
     }
 };
 
 template <bool A_MN, bool B_MN, int EPI>
 __global__ void __launch_bounds__(THREADS, 3) head_f32_kernel(const Product g) {
-    __shared__ __align__(16) float As[2][T][PITCH], Bs[2][T][PITCH];
+    constexpr int STAGES = A_MN || B_MN ? 3 : 4, AHEAD = STAGES - 1;
+    __shared__ __align__(16) float As[STAGES][T][PITCH], Bs[STAGES][T][PITCH];
     const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
     const int n_tiles = (g.N + T - 1) / T;
     const int m0 = blockIdx.x / n_tiles * T, n0 = blockIdx.x % n_tiles * T;
@@ -106,26 +92,43 @@ __global__ void __launch_bounds__(THREADS, 3) head_f32_kernel(const Product g) {
     for (int i = 0; i < TM; i++)
 #pragma unroll
         for (int j = 0; j < TN; j++) acc[i][j] = 0;
-    Slice<A_MN> a;
-    Slice<B_MN> b;
-    a.load(g.A, g.M, g.K, m0, k0, k1);
-    b.load(g.B, g.N, g.K, n0, k0, k1);
-    int buf = 0;
-    for (int k = k0; k < k1; k += KS, buf ^= 1) {
-        a.store(As[buf]);
-        b.store(Bs[buf]);
-        __syncthreads();  // (the buffer written next was read before the slice's own barrier: two buffers are enough)
-        if (k + KS < k1) {
-            a.load(g.A, g.M, g.K, m0, k + KS, k1);
-            b.load(g.B, g.N, g.K, n0, k + KS, k1);
-        }
+    // A slice goes to its stage AHEAD slices early if it is copied; a turned one is loaded two slices early and stored
+    // one early (a stage was last read two slices before that, and there is a barrier between).
+    auto copy = [&](int k, int stage) {
+        if (!A_MN) copy_slice(As[stage], g.A, g.M, g.K, m0, k, k1);
+        if (!B_MN) copy_slice(Bs[stage], g.B, g.b_rows, g.K, n0, k, k1);
+        cp_async_commit();
+    };
+    Turned a, b;
+    auto load = [&](int k) {
+        if (A_MN) a.load(g.A, g.M, m0, k, k1);
+        if (B_MN) b.load(g.B, g.N, n0, k, min(k1, g.b_rows));
+    };
+    auto store = [&](int stage) {
+        if (A_MN) a.store(As[stage]);
+        if (B_MN) b.store(Bs[stage]);
+    };
+#pragma unroll
+    for (int u = 0; u < AHEAD; u++) copy(k0 + u * KS, u);
+    load(k0);
+    store(0);
+    load(k0 + KS);
+    int stage = 0;
+    auto after = [&](int n) { return stage + n >= STAGES ? stage + n - STAGES : stage + n; };
+    for (int k = k0; k < k1; k += KS) {
+        cp_async_wait<AHEAD - 1>();
+        __syncthreads();
+        copy(k + AHEAD * KS, after(AHEAD));
+        store(after(1));
+        load(k + 2 * KS);
 #pragma unroll
         for (int kk = 0; kk < KS; kk += 4) {
             ulonglong2 x[TM], y[TN];
 #pragma unroll
-            for (int i = 0; i < TM; i++) x[i] = *reinterpret_cast<const ulonglong2*>(&As[buf][ty + 8 * i][place(8 * i, kk)]);
+            for (int i = 0; i < TM; i++) x[i] = *reinterpret_cast<const ulonglong2*>(&As[stage][ty + 8 * i][place(8 * i, kk)]);
 #pragma unroll
-            for (int j = 0; j < TN; j++) y[j] = *reinterpret_cast<const ulonglong2*>(&Bs[buf][tx + 16 * j][place(tx + 16 * j, kk)]);
+            for (int j = 0; j < TN; j++)
+                y[j] = *reinterpret_cast<const ulonglong2*>(&Bs[stage][tx + 16 * j][place(tx + 16 * j, kk)]);
 #pragma unroll
             for (int i = 0; i < TM; i++)
 #pragma unroll
@@ -135,6 +138,7 @@ __global__ void __launch_bounds__(THREADS, 3) head_f32_kernel(const Product g) {
 #pragma unroll
                 for (int j = 0; j < TN; j++) acc[i][j] = f2_fma(x[i].y, y[j].y, acc[i][j]);
         }
+        stage = after(1);
     }
     float* d = g.D + (EPI == STORE ? (int64_t)blockIdx.y * g.M * g.N : 0);
 #pragma unroll
@@ -189,7 +193,7 @@ __global__ void __launch_bounds__(THREADS, 3) head_f32_kernel(const Product g) {
             for (int j = 0; j < TN; j++) {
                 const int n = n0 + tx + 16 * j;
                 // a row that does not count gets zeros whatever its logits are
-                if (n < g.N) d[(int64_t)row * g.N + n] = counts ? w * expf(z[j] - l) - (n == t ? dl : 0.f) : 0.f;
+                if (n < g.N) d[(int64_t)row * g.N + n] = counts && n < g.b_rows ? w * expf(z[j] - l) - (n == t ? dl : 0.f) : 0.f;
             }
         }
     }
@@ -216,11 +220,11 @@ int splits(int M, int N, int K) {
 }
 
 template <bool A_MN, bool B_MN>
-int start_store(float* D, const float* A, const float* B, int M, int N, int K, bool accumulate, float* scratch,
-                cudaStream_t s) {
+int start_store(float* D, const float* A, const float* B, int M, int N, int K, int b_rows, bool accumulate,
+                float* scratch, cudaStream_t s) {
     const int sp = splits(M, N, K);
     Product g = {};
-    g.A = A, g.B = B, g.M = M, g.N = N, g.K = K;
+    g.A = A, g.B = B, g.M = M, g.N = N, g.K = K, g.b_rows = b_rows;
     g.per_split = ((K + sp - 1) / sp + KS - 1) / KS * KS;
     const int parts = (K + g.per_split - 1) / g.per_split;
     g.D = parts > 1 ? scratch : D;
@@ -232,10 +236,12 @@ int start_store(float* D, const float* A, const float* B, int M, int N, int K, b
     return 2;
 }
 
-template <int EPI> int start_head(float* D, const float* x, const float* w, int M, int N, int K, const HeadEpi& e,
-                                  cudaStream_t s) {
+template <int EPI>
+int start_head(float* D, const float* x, const float* w, int M, int N, int K, int b_rows, const HeadEpi& e,
+               cudaStream_t s) {
     Product g = {};
-    g.A = x, g.B = w, g.D = D, g.M = M, g.N = N, g.K = K, g.per_split = (K + KS - 1) / KS * KS, g.head = e;
+    g.A = x, g.B = w, g.D = D, g.M = M, g.N = N, g.K = K, g.b_rows = b_rows, g.per_split = (K + KS - 1) / KS * KS;
+    g.head = e;
     head_f32_kernel<false, false, EPI><<<(unsigned)tiles(M, N), THREADS, 0, s>>>(g);
     return 1;
 }
@@ -245,20 +251,21 @@ template <int EPI> int start_head(float* D, const float* x, const float* w, int 
 int head_f32_slots(int V) { return (V + T - 1) / T; }
 
 int launch_head_f32_lse(const float* x, const float* w, int M, int N, int K, const HeadEpi& e, cudaStream_t s) {
-    return start_head<LSE>(nullptr, x, w, M, N, K, e, s);
+    return start_head<LSE>(nullptr, x, w, M, N, K, N, e, s);
 }
-int launch_head_f32_dz(float* dz, const float* x, const float* w, int M, int N, int K, const HeadEpi& e, cudaStream_t s) {
-    return start_head<DZ>(dz, x, w, M, N, K, e, s);
+int launch_head_f32_dz(float* dz, const float* x, const float* w, int M, int N, int K, int rows, const HeadEpi& e,
+                       cudaStream_t s) {
+    return start_head<DZ>(dz, x, w, M, N, K, rows, e, s);
 }
 size_t head_f32_scratch(int M, int N, int K) {
     const int sp = splits(M, N, K);
     return sp > 1 ? (size_t)sp * M * N * 4 : 0;
 }
-int launch_head_f32_dx(float* dx, const float* dz, const float* w, int M, int N, int K, bool add, void* scratch,
+int launch_head_f32_dx(float* dx, const float* dz, const float* w, int M, int N, int K, int rows, bool add, void* scratch,
                        cudaStream_t s) {
-    return start_store<false, true>(dx, dz, w, M, N, K, add, (float*)scratch, s);
+    return start_store<false, true>(dx, dz, w, M, N, K, rows, add, (float*)scratch, s);
 }
 int launch_head_f32_dw(float* dw, const float* dz, const float* x, int M, int N, int K, bool add, void* scratch,
                        cudaStream_t s) {
-    return start_store<true, true>(dw, dz, x, M, N, K, add, (float*)scratch, s);
+    return start_store<true, true>(dw, dz, x, M, N, K, K, add, (float*)scratch, s);
 }

@@ -39,6 +39,8 @@
 
 #include <cuda.h>
 
+#include <type_traits>
+
 namespace {
 
 using namespace tc;
@@ -72,7 +74,7 @@ constexpr int EPI_MUL = 2;   // D = bf16(x) * aux: the input gradient through th
 constexpr int EPI_LSE = 3;   // nothing of x is stored: a row's maximum and sum of exponentials in each half tile
 constexpr int EPI_DZ = 4;    // D = bf16(((dloss + dlse) exp(x - lse) - dloss [column = target]) / scale)
 constexpr int EPI_ADD = 5;   // D (fp32) = or += x, added by the copy that stores it (one writer for each value)
-constexpr int EPI_SCALE = 6; // D = x times a device scalar (split products: the reduce kernel scales their sum)
+constexpr int EPI_SCALE = 6; // D = x times a device scalar (split products, in either type: a reduce kernel scales)
 constexpr bool epi_stores(int epi) { return epi != EPI_LSE; }
 
 struct GemmArgs {
@@ -350,19 +352,38 @@ __device__ __forceinline__ void epi_chunk(const uint32_t (&r)[32], const float* 
     }
 }
 
+// EPI_DZ: the scale, which a kernel of its own has written, or (few rows) which every warp finds for itself, the first
+// one writing it for the products that come after.
+template <int EPI> __device__ __forceinline__ float head_scale(const HeadEpi* e, int M, bool first) {
+    if constexpr (EPI == EPI_DZ) {
+        if (!e->find) return *e->scale;
+        float m = 0.f;
+#pragma unroll 4
+        for (int i = threadIdx.x & 31; i < M; i += 32) m = fmaxf(m, head_magnitude(*e, i));
+        m = warp_max(m);
+        if (first && (threadIdx.x & 31) == 0) *e->scale = m;
+        return m;
+    }
+    return 1.f;
+}
+
 // EPI_LSE, EPI_DZ: a row's values for a tile half that begins at vocabulary column v0.
-template <int EPI> __device__ __forceinline__ void head_begin(const HeadEpi* e, int row, int M, int v0, RowHead& h) {
+template <int EPI>
+__device__ __forceinline__ void head_begin(const HeadEpi* e, int row, int M, int v0, float scale, int* status,
+                                           RowHead& h) {
     if constexpr (EPI == EPI_LSE || EPI == EPI_DZ) {
         h.m = -INFINITY;
         h.s = h.a = h.d = h.lse = 0.f;
         h.at = -1;
         if (row < M) {
             int t = e->targets[row];
-            if (t < 0 || t >= e->vocab) t = 0;
+            if (t < 0 || t >= e->vocab) {
+                if (EPI == EPI_DZ && e->find) set_status(status, GPT2_FLAG_TARGET_RANGE);
+                t = 0;
+            }
             h.at = t - (v0 + e->first);
             if (EPI == EPI_DZ) {
                 const float d = e->dloss ? e->dloss[row] : 0.f, a = d + (e->dlse ? e->dlse[row] : 0.f);
-                const float scale = *e->scale;  // 0: no row counts
                 h.d = d != 0.f ? d / scale : 0.f;
                 h.a = a != 0.f ? a / scale : 0.f;
                 h.lse = e->lse[row] * LOG2E;
@@ -566,6 +587,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const HeadEpi* he = head_of(g);
         float alpha = F8 ? *g.a_scale * *g.b_scale : 1.f;
         if constexpr (EPI == EPI_SCALE) alpha = g.partials ? 1.f : *he->scale;
+        const float scale = head_scale<EPI>(he, g.M, blockIdx.x == 0 && ew == 0);
         // EPI_MUL column sums: each warp writes the sums of its 32 rows of a
         // tile, row 4 * mt + quad of g.colsum
         const bool want_csum = EPI == EPI_MUL && g.colsum != nullptr;
@@ -626,7 +648,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             auto csum_at = [&](int c) -> float* { return want_csum ? csum_row + c * 32 : nullptr; };
             const int nrows = max(0, min(32, g.M - y));  // this warp's rows inside the matrix
             RowHead head;
-            head_begin<EPI>(he, m0 + row_in_tile, g.M, n0 + cfirst * 32, head);
+            head_begin<EPI>(he, m0 + row_in_tile, g.M, n0 + cfirst * 32, scale, g.status, head);
             float* target = EPI == EPI_LSE ? he->target_logit + m0 + row_in_tile : nullptr;
             uint32_t ra[32], rb[32];
             if (nchunks > 0) {
@@ -1003,6 +1025,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         const HeadEpi* he = head_of(g);
         float alpha = 1.f;
         if constexpr (EPI == EPI_SCALE) alpha = g.partials ? 1.f : *he->scale;
+        const float scale = head_scale<EPI>(he, g.M, blockIdx.x == 0 && ew == 0);
         const bool want_csum = EPI == EPI_MUL && g.colsum != nullptr;
         int acc = 0;
         uint32_t acc_phase = 0;
@@ -1055,7 +1078,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
             auto csum_at = [&](int c) -> float* { return want_csum ? csum_row + c * 32 : nullptr; };
             const int nrows = max(0, min(32, g.M - y));  // this warp's rows inside the matrix
             RowHead head;
-            head_begin<EPI>(he, m0 + row_in_tile, g.M, n0 + cfirst * 32, head);
+            head_begin<EPI>(he, m0 + row_in_tile, g.M, n0 + cfirst * 32, scale, g.status, head);
             float* target = EPI == EPI_LSE ? he->target_logit + m0 + row_in_tile : nullptr;
             uint32_t ra[32], rb[32];
             if (nchunks > 0) {
@@ -1119,12 +1142,9 @@ __global__ void __launch_bounds__(P_THREADS, 1)
 // Split-K reduce: D[m][n] (fp32) = bias[n] (if any) + the partial tiles of
 // the tile of (m, n), added in split order; with accumulate, added to D's
 // current value. 8 consecutive columns per thread (N and BN are multiples of 8).
-// SCALED: the partial tiles' sum times *scale.
-template <bool SCALED>
 __global__ void __launch_bounds__(256) split_reduce_kernel(float* __restrict__ D, const float* __restrict__ partial,
                                                            const bf16* __restrict__ bias, int M, int N, int BN,
-                                                           int n_tiles, int splits, int accumulate,
-                                                           const float* __restrict__ scale) {
+                                                           int n_tiles, int splits, int accumulate) {
     // 32-bit element index (the launcher keeps M * N < 2^31)
     const int i = (blockIdx.x * blockDim.x + threadIdx.x) * 8;
     if (i >= M * N) return;
@@ -1133,8 +1153,8 @@ __global__ void __launch_bounds__(256) split_reduce_kernel(float* __restrict__ D
     const int64_t tile_elems = (int64_t)BM * BN;
     const float* p = partial + tile * splits * tile_elems + (int64_t)(m % BM) * BN + n % BN;
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (!SCALED && bias) load8(bias + n, acc);
-    if (!SCALED && accumulate) {
+    if (bias) load8(bias + n, acc);
+    if (accumulate) {
         float d[8];
         load8(D + i, d);
 #pragma unroll
@@ -1146,13 +1166,51 @@ __global__ void __launch_bounds__(256) split_reduce_kernel(float* __restrict__ D
 #pragma unroll
         for (int j = 0; j < 8; j++) acc[j] += v[j];
     }
-    if (SCALED) {
-        float d[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (accumulate) load8(D + i, d);
-        const float s = *scale;
+    store8(D + i, acc);
+}
+
+// The same for EPI_SCALE: D = (D +) *scale times the sum of the partial tiles, D in bf16 or fp32 (accumulate: fp32 only).
+// With eight strands of threads each takes every eighth split, so that the partials of few outputs and many splits are
+// all on their way at once, and are added in a fixed order (61 x 768 outputs of 50 splits: 4.2 us, with one strand 11.2;
+// 1500 x 768 of 2 splits: 9.2, with one strand 3.6).
+template <typename T, int STRANDS>
+__global__ void __launch_bounds__(256) scaled_reduce_kernel(T* __restrict__ D, const float* __restrict__ partial, int M,
+                                                            int N, int BN, int n_tiles, int splits, int accumulate,
+                                                            const float* __restrict__ scale) {
+    constexpr int WIDE = 256 / STRANDS;
+    __shared__ float sm[STRANDS][WIDE][9];  // (9: the lanes of a warp in different banks)
+    const int tx = threadIdx.x % WIDE, ty = threadIdx.x / WIDE;
+    const int i = (blockIdx.x * WIDE + tx) * 8;
+    const bool in = i < M * N;
+    const int m = in ? i / N : 0, n = in ? i - m * N : 0;
+    const int64_t tile = (int64_t)(m / BM) * n_tiles + n / BN;
+    const int64_t tile_elems = (int64_t)BM * BN;
+    const float* p = partial + tile * splits * tile_elems + (int64_t)(m % BM) * BN + n % BN;
+    float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (in) {
+#pragma unroll 4
+        for (int sp = ty; sp < splits; sp += STRANDS) {
+            float v[8];
+            load8(p + sp * tile_elems, v);
 #pragma unroll
-        for (int j = 0; j < 8; j++) acc[j] = fmaf(acc[j], s, d[j]);
+            for (int j = 0; j < 8; j++) acc[j] += v[j];
+        }
     }
+    if (STRANDS > 1) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) sm[ty][tx][j] = acc[j];
+        __syncthreads();
+    }
+    if (ty || !in) return;
+#pragma unroll
+    for (int k = 1; k < STRANDS; k++)
+#pragma unroll
+        for (int j = 0; j < 8; j++) acc[j] += sm[k][tx][j];
+    float d[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (accumulate) load8(D + i, d);
+    const float s = *scale;
+#pragma unroll
+    for (int j = 0; j < 8; j++) acc[j] = fmaf(acc[j], s, d[j]);
     store8(D + i, acc);
 }
 
@@ -1253,6 +1311,8 @@ Plan make_plan(int M, int N, int K, int d_fp32) {
         const int bn_split = N <= 128 ? 128 : 256;
         const long long ts = (long long)p.m_tiles * ((N + bn_split - 1) / bn_split);
         for (int sp = 2; sp <= 64 && sp * 4 <= p.num_kb; sp++) {
+            // (full waves and the partials alone: more splits cannot win any more)
+            if ((double)ts * p.num_kb / sms * (bn_split / 256.0) + (double)sp * M * N * 8 / KB_HBM_BYTES >= best) break;
             const int kbs = (p.num_kb + sp - 1) / sp;
             const double cost = waves(ts * sp) * kbs * (bn_split / 256.0) + (double)sp * M * N * 8 / KB_HBM_BYTES;
             if (cost < best) {
@@ -1308,8 +1368,9 @@ bool launch_tc_layout(int epi, int a_mn, int b_mn, const CUtensorMap& ma, const 
         if (a_mn || !b_mn) return false;
         launch_tc<BN, false, true, EPI_ADD>(ma, mb, md, md2, args, grid, s);
     } else if (epi == EPI_SCALE) {
-        if (!a_mn || !b_mn) return false;
-        launch_tc<BN, true, true, EPI_SCALE>(ma, mb, md, md2, args, grid, s);
+        if (!b_mn) return false;
+        if (a_mn) launch_tc<BN, true, true, EPI_SCALE>(ma, mb, md, md2, args, grid, s);
+        else launch_tc<BN, false, true, EPI_SCALE>(ma, mb, md, md2, args, grid, s);
     } else if (!a_mn && !b_mn) {
         launch_tc<BN, false, false, EPI_NONE>(ma, mb, md, md2, args, grid, s);
     } else if (!a_mn && b_mn) {
@@ -1448,7 +1509,7 @@ int matmul_tc(int epi, void* D, void* D2, const bf16* aux, int d_fp32, const voi
     // (b_rows: the rows of B that are read, where they are fewer than N or, MN-major, K; the rest count as 0)
     const uint64_t rows_of_b = b_rows ? b_rows : b_mn ? K : N;
     if (f8 && (a_mn || b_mn || K % 16 || N % 8)) return GPT2_ERR_ARG;
-    Plan p = make_plan(M, N, f8 ? (K + 1) / 2 : K, epi == EPI_NONE || epi == EPI_SCALE ? d_fp32 : 0);
+    Plan p = make_plan(M, N, f8 ? (K + 1) / 2 : K, epi == EPI_SCALE ? 1 : epi == EPI_NONE ? d_fp32 : 0);
     // partial tiles for the reduce kernel: split-K, or an fp32 result added to D
     const bool partials = p.splits > 1 || (accumulate && d_fp32 && (epi == EPI_NONE || epi == EPI_SCALE));
     if (partials && (int64_t)M * N + 2048 >= ((int64_t)1 << 31)) return GPT2_ERR_ARG;  // the reduce uses 32-bit indices
@@ -1494,8 +1555,9 @@ int matmul_tc(int epi, void* D, void* D2, const bf16* aux, int d_fp32, const voi
             if (a_mn || !b_mn) return GPT2_ERR_ARG;
             e = launch_pair<false, true, EPI_ADD, 192>(ma, mb, md, md2, g, pairs, s);
         } else if (pn == 192 && epi == EPI_SCALE) {
-            if (!a_mn || !b_mn) return GPT2_ERR_ARG;
-            e = launch_pair<true, true, EPI_SCALE, 192>(ma, mb, md, md2, g, pairs, s);
+            if (!b_mn) return GPT2_ERR_ARG;
+            e = a_mn ? launch_pair<true, true, EPI_SCALE, 192>(ma, mb, md, md2, g, pairs, s)
+                     : launch_pair<false, true, EPI_SCALE, 192>(ma, mb, md, md2, g, pairs, s);
         } else if (pn == 192) {
             if (epi != EPI_NONE) return GPT2_ERR_ARG;
             if (!b_mn)
@@ -1518,8 +1580,9 @@ int matmul_tc(int epi, void* D, void* D2, const bf16* aux, int d_fp32, const voi
             if (a_mn || !b_mn) return GPT2_ERR_ARG;
             e = launch_pair<false, true, EPI_ADD>(ma, mb, md, md2, g, pairs, s);
         } else if (epi == EPI_SCALE) {
-            if (!a_mn || !b_mn) return GPT2_ERR_ARG;
-            e = launch_pair<true, true, EPI_SCALE>(ma, mb, md, md2, g, pairs, s);
+            if (!b_mn) return GPT2_ERR_ARG;
+            e = a_mn ? launch_pair<true, true, EPI_SCALE>(ma, mb, md, md2, g, pairs, s)
+                     : launch_pair<false, true, EPI_SCALE>(ma, mb, md, md2, g, pairs, s);
         } else if (!a_mn && !b_mn) {
             e = launch_pair<false, false, EPI_NONE>(ma, mb, md, md2, g, pairs, s);
         } else if (!a_mn && b_mn) {
@@ -1587,12 +1650,21 @@ int matmul_tc(int epi, void* D, void* D2, const bf16* aux, int d_fp32, const voi
         const int64_t MN = (int64_t)M * N;
         const int blocks = (int)((MN / 8 + 255) / 256);
         const int add = accumulate && d_fp32 ? 1 : 0;
-        if (epi == EPI_SCALE)
-            split_reduce_kernel<true><<<blocks, 256, 0, s>>>((float*)D, (const float*)scratch, nullptr, M, N, p.bn,
-                                                             p.n_tiles, p.splits, add, head->scale);
+        const float* parts = (const float*)scratch;
+        const bool strands = p.splits >= 8;
+        const int wide = (int)((MN / 8 + 31) / 32);
+        auto scaled = [&](auto* d) {
+            using T = std::remove_pointer_t<decltype(d)>;
+            if (strands)
+                scaled_reduce_kernel<T, 8><<<wide, 256, 0, s>>>(d, parts, M, N, p.bn, p.n_tiles, p.splits, add, head->scale);
+            else
+                scaled_reduce_kernel<T, 1><<<blocks, 256, 0, s>>>(d, parts, M, N, p.bn, p.n_tiles, p.splits, add, head->scale);
+        };
+        if (epi == EPI_SCALE && d_fp32) scaled((float*)D);
+        else if (epi == EPI_SCALE) scaled((bf16*)D);
         else
-            split_reduce_kernel<false><<<blocks, 256, 0, s>>>((float*)D, (const float*)scratch, (const bf16*)bias, M, N,
-                                                              p.bn, p.n_tiles, p.splits, add, nullptr);
+            split_reduce_kernel<<<blocks, 256, 0, s>>>((float*)D, parts, (const bf16*)bias, M, N, p.bn, p.n_tiles,
+                                                       p.splits, add);
         return 2;
     }
     return 1;
@@ -1685,7 +1757,17 @@ int launch_head_dx(float* dx, const void* dz, const void* w, int M, int N, int K
                      add && !whole, nullptr, nullptr, nullptr, &e, rows);
 }
 
-int launch_head_dw(void* dw, int dw_fp32, const void* dz, const void* x, int M, int N, int K, const float* scale,
+size_t head_scaled_scratch(int M, int N, int K, bool add) { return matmul_tc_scratch(M, N, K, 1, add); }
+
+int launch_head_dx_scaled(void* dx, const void* dz, const void* w, int M, int N, int K, int rows, float* scale,
+                          void* scratch, int* status, cudaStream_t s) {
+    HeadEpi e = {};
+    e.scale = scale;
+    return matmul_tc(EPI_SCALE, dx, nullptr, nullptr, 0, dz, 0, w, 1, nullptr, M, N, K, scratch, status, s, 0, nullptr,
+                     nullptr, nullptr, &e, rows);
+}
+
+int launch_head_dw(void* dw, int dw_fp32, const void* dz, const void* x, int M, int N, int K, float* scale,
                    bool add, void* scratch, int* status, cudaStream_t s) {
     HeadEpi e = {};
     e.scale = scale;

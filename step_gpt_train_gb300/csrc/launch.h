@@ -176,12 +176,18 @@ int launch_rotary(int dtype, const RotaryArgs& a, bool back, float* dq_gamma, fl
 struct HeadEpi {
     const int32_t* targets;      // [M]; outside [0, vocab): 0
     const float *lse, *dloss, *dlse;  // gradients: [M] (dloss, dlse or null: 0)
-    const float* scale;          // gradients: what dz is given in units of, a device scalar
+    float* scale;                // gradients: what dz is given in units of, a device scalar
+    int find;                    // the largest head_magnitude, which launch_head_dz finds and writes
     float2* stats;               // forward: [slots][M] maximum and sum of exp(z - maximum)
     float* target_logit;         // forward: [M]
     int vocab, first;
     int add;                     // launch_head_dx's own
 };
+// What row i asks of the scale: the largest finite |dloss| and |dloss + dlse|.
+__device__ __forceinline__ float head_magnitude(const HeadEpi& e, int64_t i) {
+    const float d = e.dloss ? e.dloss[i] : 0.f, a = d + (e.dlse ? e.dlse[i] : 0.f);
+    return fmaxf(isfinite(d) ? fabsf(d) : 0.f, isfinite(a) ? fabsf(a) : 0.f);
+}
 // Forward: the row statistics of the M x N logits x W^T in head_lse_slots() slots and the targets' logits.
 int head_lse_slots(int M, int N, int K);
 int launch_head_lse(const void* x, const void* w, int M, int N, int K, const HeadEpi& e, int* status, cudaStream_t s);
@@ -192,17 +198,23 @@ int launch_head_dz(void* dz, const void* x, const void* w, int M, int N, int K, 
 size_t head_dx_scratch(int M, int N, int K);
 int launch_head_dx(float* dx, const void* dz, const void* w, int M, int N, int K, int rows, bool add, void* scratch,
                    int* status, cudaStream_t s);
-// dw [M, N] = or (fp32) += *scale dz^T x, dz [K, M], x [K, N]; scratch: matmul_scratch(bf16, M, N, K, dw_fp32, add).
-int launch_head_dw(void* dw, int dw_fp32, const void* dz, const void* x, int M, int N, int K, const float* scale,
+// dx [M, N] (bf16) = *scale dz [M, K] W [K, N]: the whole vocabulary at once.
+// dw [M, N] (bf16 or fp32) = or (fp32) += *scale dz^T x, dz [K, M], x [K, N].
+size_t head_scaled_scratch(int M, int N, int K, bool add);
+int launch_head_dx_scaled(void* dx, const void* dz, const void* w, int M, int N, int K, int rows, float* scale,
+                          void* scratch, int* status, cudaStream_t s);
+int launch_head_dw(void* dw, int dw_fp32, const void* dz, const void* x, int M, int N, int K, float* scale,
                    bool add, void* scratch, int* status, cudaStream_t s);
 
 // The same in fp32 (classifier_linear_f32.cu): statistics in head_f32_slots(V) slots, dz [M, N], dx [M, N] = or +=
 // dz [M, K] W [K, N], dw [M, N] = or += dz^T x with dz [K, M], x [K, N]; scratch for the two: head_f32_scratch(M, N, K).
+// rows: as above; N of dz, K of dx and M of dw are multiples of 4.
 int head_f32_slots(int V);
 int launch_head_f32_lse(const float* x, const float* w, int M, int N, int K, const HeadEpi& e, cudaStream_t s);
-int launch_head_f32_dz(float* dz, const float* x, const float* w, int M, int N, int K, const HeadEpi& e, cudaStream_t s);
+int launch_head_f32_dz(float* dz, const float* x, const float* w, int M, int N, int K, int rows, const HeadEpi& e,
+                       cudaStream_t s);
 size_t head_f32_scratch(int M, int N, int K);
-int launch_head_f32_dx(float* dx, const float* dz, const float* w, int M, int N, int K, bool add, void* scratch,
+int launch_head_f32_dx(float* dx, const float* dz, const float* w, int M, int N, int K, int rows, bool add, void* scratch,
                        cudaStream_t s);
 int launch_head_f32_dw(float* dw, const float* dz, const float* x, int M, int N, int K, bool add, void* scratch,
                        cudaStream_t s);
@@ -212,7 +224,7 @@ size_t linear_classifier_forward_scratch(int dtype, int N, int C, int V);
 int launch_linear_classifier_forward(int dtype, float* losses, float* lse, const void* x, const void* w,
                                      const int32_t* targets, int N, int C, int V, void* scratch, int* status,
                                      cudaStream_t s);
-size_t linear_classifier_backward_scratch(int dtype, int N, int C, int V, int dw_fp32, int accumulate);
+size_t linear_classifier_backward_scratch(int dtype, int N, int C, int V, int Vp, int accumulate);
 int launch_linear_classifier_backward(int dtype, void* dx, void* dw, int dw_fp32, int accumulate, const void* x,
                                       const void* w, const int32_t* targets, const float* lse, const float* dloss,
                                       const float* dlse, int N, int C, int V, int Vp, void* scratch, int* status,

@@ -514,10 +514,11 @@ int gpt2_op_linear_classifier_forward(int dtype, float* losses, float* lse, cons
                                                    st(stream)));
 }
 
-size_t gpt2_op_linear_classifier_backward_scratch(int dtype, int N, int C, int V, int dw_fp32, int accumulate) {
-    return N < 1 || !linear_classifier_ok(dtype, N, C, V)
+size_t gpt2_op_linear_classifier_backward_scratch(int dtype, int N, int C, int V, int Vp, int accumulate) {
+    return N < 1 || !linear_classifier_ok(dtype, N, C, V) || Vp < V || Vp % 8 ||
+                   (int64_t)Vp * C >= ((int64_t)1 << 31) - 2048
                ? 0
-               : linear_classifier_backward_scratch(dtype, N, C, V, dw_fp32 != 0, accumulate != 0);
+               : linear_classifier_backward_scratch(dtype, N, C, V, Vp, accumulate != 0);
 }
 
 int gpt2_op_linear_classifier_backward(int dtype, void* dx, void* dw, int dw_fp32, int accumulate, const void* x,
@@ -535,7 +536,7 @@ int gpt2_op_linear_classifier_backward(int dtype, void* dx, void* dw, int dw_fp3
         return GPT2_OK;
     }
     if (!dx || !x || !w || !targets || !lse || !al16(dx) || !al16(x) || !al16(w)) return GPT2_ERR_ARG;
-    if (!scratch || scratch_bytes < linear_classifier_backward_scratch(dtype, N, C, V, dw_fp32, accumulate))
+    if (!scratch || scratch_bytes < linear_classifier_backward_scratch(dtype, N, C, V, Vp, accumulate))
         return GPT2_ERR_WORKSPACE;
     return finish(launch_linear_classifier_backward(dtype, dx, dw, dw_fp32, accumulate, x, w, targets, lse, dloss, dlse,
                                                     N, C, V, Vp, scratch, d_status, st(stream)));

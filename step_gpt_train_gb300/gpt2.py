@@ -1001,7 +1001,7 @@ def gpt2_op_linear_classifier_backward(dx, dw, x, w, targets, lse, V, dloss=None
     status = _status(what, status, device)
     args = (dt, dx.data_ptr(), dw.data_ptr(), dw32, bool(accumulate), x.data_ptr(), w.data_ptr(), targets.data_ptr(),
             lse.data_ptr(), _p(dloss), _p(dlse), N, C, V, Vp)
-    nb = lib.gpt2_op_linear_classifier_backward_scratch(dt, N, C, V, dw32, bool(accumulate))
+    nb = lib.gpt2_op_linear_classifier_backward_scratch(dt, N, C, V, Vp, bool(accumulate))
     sc = _borrow(nb, st) if nb else None
     try:
         check(lib.gpt2_op_linear_classifier_backward(*args, sc, nb, status, st), what)
