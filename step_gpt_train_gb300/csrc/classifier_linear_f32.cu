@@ -13,7 +13,10 @@
 // (dx: N x C outputs, K = V) are cut along k; a second kernel adds the parts in
 // order.
 //
-// 1021 x 128 x 5003 (1.3 GFLOP a product, 17 us at 75 TFLOP/s): TIMES
+// 1021 x 128 x 5003 (1.3 GFLOP a product, 17 us at 75 TFLOP/s): dz 44 us, dx 34
+// and dw 47, and 3 each to add their parts. What bounds it: three blocks of 160
+// registers an SM are three warps to a scheduler, whose FMAs wait for one
+// another (41% of the issue slots used); a third of what is issued is not FMA.
 #include "common.cuh"
 #include "launch.h"
 #include "tc_common.cuh"
@@ -45,37 +48,65 @@ struct Product {
 // two banks, in this one eight.
 __device__ __forceinline__ constexpr int place(int row, int k) { return (((k >> 2) ^ (row >> 3)) & 3) * 4 + (k & 3); }
 
-// A slice of an operand: T rows by KS k's from (row0, k0), two vectors of four a thread; zeros outside `rows` and k1.
-// [rows][k]: copied as it is.
-__device__ __forceinline__ void copy_slice(float (*s)[PITCH], const float* p, int rows, int K, int row0, int k0, int k1) {
+// A thread's two vectors of four of each slice (T rows by KS k's) of an operand, walked along k; zeros outside `rows`
+// and k1. [rows][k]: copied as they are.
+struct Copied {
+    const float* from[2];
+    uint32_t to[2];
+    int k, k1;
+    bool in[2];
+    __device__ __forceinline__ Copied(const float* p, int rows, int K, int row0, int k0, int k1_, float (*s)[PITCH])
+        : k(k0 + threadIdx.x % 4 * 4), k1(k1_) {
 #pragma unroll
-    for (int u = 0; u < 2; u++) {
-        const int i = threadIdx.x + u * THREADS, r = row0 + i / 4, k = k0 + i % 4 * 4;
-        const bool in = r < rows && k < k1;
-        const float* from = in ? p + (int64_t)r * K + k : p;
-        const uint32_t to = (uint32_t)__cvta_generic_to_shared(&s[i / 4][place(i / 4, i % 4 * 4)]);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(in ? 16 : 0) : "memory");
+        for (int u = 0; u < 2; u++) {
+            const int r = threadIdx.x / 4 + u * (THREADS / 4);
+            in[u] = row0 + r < rows;
+            from[u] = p + (in[u] ? (int64_t)(row0 + r) * K + k : 0);
+            to[u] = (uint32_t)__cvta_generic_to_shared(&s[r][place(r, threadIdx.x % 4 * 4)]);
+        }
     }
-}
+    __device__ __forceinline__ void next(int stage) {
+#pragma unroll
+        for (int u = 0; u < 2; u++) {
+            const bool now = in[u] && k < k1;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to[u] + stage * (T * PITCH * 4)),
+                         "l"(now ? from[u] : from[u] - (in[u] ? k : 0)), "r"(now ? 16 : 0)
+                         : "memory");
+            if (in[u]) from[u] += KS;
+        }
+        k += KS;
+    }
+};
 // [k][rows]: through registers, turned when stored.
 struct Turned {
     float f[2][4];
-    __device__ __forceinline__ void load(const float* p, int rows, int row0, int k0, int k1) {
+    const float* from[2];
+    int64_t step;
+    int k, k1;
+    bool in;
+    __device__ __forceinline__ Turned(const float* p, int rows, int row0, int k0, int k1_) : k(k0 + threadIdx.x / 16), k1(k1_) {
+        const int r = row0 + threadIdx.x % 16 * 4;
+        in = r < rows;
+        step = (int64_t)KS * rows;
+#pragma unroll
+        for (int u = 0; u < 2; u++) from[u] = p + (int64_t)(k + u * (THREADS / 16)) * rows + r;
+    }
+    __device__ __forceinline__ void next() {
 #pragma unroll
         for (int u = 0; u < 2; u++) {
-            const int i = threadIdx.x + u * THREADS, r = row0 + i % 16 * 4, k = k0 + i / 16;
-            const float4 v = r < rows && k < k1 ? *reinterpret_cast<const float4*>(p + (int64_t)k * rows + r)
-                                                : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 v = in && k + u * (THREADS / 16) < k1 ? *reinterpret_cast<const float4*>(from[u])
+                                                              : make_float4(0.f, 0.f, 0.f, 0.f);
             f[u][0] = v.x, f[u][1] = v.y, f[u][2] = v.z, f[u][3] = v.w;
+            from[u] += step;
         }
+        k += KS;
     }
     __device__ __forceinline__ void store(float (*s)[PITCH]) const {
 #pragma unroll
-        for (int u = 0; u < 2; u++) {
-            const int i = threadIdx.x + u * THREADS;
+        for (int u = 0; u < 2; u++)
 #pragma unroll
-            for (int j = 0; j < 4; j++) s[i % 16 * 4 + j][place(i % 16 * 4, i / 16)] = f[u][j];
-        }
+            for (int j = 0; j < 4; j++)
+                s[threadIdx.x % 16 * 4 + j][place(threadIdx.x % 16 * 4, threadIdx.x / 16 + u * (THREADS / 16))] = f[u][j];
     }
 };
 
@@ -94,41 +125,48 @@ __global__ void __launch_bounds__(THREADS, 3) head_f32_kernel(const Product g) {
         for (int j = 0; j < TN; j++) acc[i][j] = 0;
     // A slice goes to its stage AHEAD slices early if it is copied; a turned one is loaded two slices early and stored
     // one early (a stage was last read two slices before that, and there is a barrier between).
-    auto copy = [&](int k, int stage) {
-        if (!A_MN) copy_slice(As[stage], g.A, g.M, g.K, m0, k, k1);
-        if (!B_MN) copy_slice(Bs[stage], g.B, g.b_rows, g.K, n0, k, k1);
+    Copied ca(g.A, A_MN ? 0 : g.M, g.K, m0, k0, k1, As[0]), cb(g.B, B_MN ? 0 : g.b_rows, g.K, n0, k0, k1, Bs[0]);
+    Turned ta(g.A, A_MN ? g.M : 0, m0, k0, k1), tb(g.B, B_MN ? g.N : 0, n0, k0, min(k1, g.b_rows));
+    auto copy = [&](int stage) {
+        if (!A_MN) ca.next(stage);
+        if (!B_MN) cb.next(stage);
         cp_async_commit();
     };
-    Turned a, b;
-    auto load = [&](int k) {
-        if (A_MN) a.load(g.A, g.M, m0, k, k1);
-        if (B_MN) b.load(g.B, g.N, n0, k, min(k1, g.b_rows));
+    auto load = [&]() {
+        if (A_MN) ta.next();
+        if (B_MN) tb.next();
     };
     auto store = [&](int stage) {
-        if (A_MN) a.store(As[stage]);
-        if (B_MN) b.store(Bs[stage]);
+        if (A_MN) ta.store(As[stage]);
+        if (B_MN) tb.store(Bs[stage]);
     };
 #pragma unroll
-    for (int u = 0; u < AHEAD; u++) copy(k0 + u * KS, u);
-    load(k0);
+    for (int u = 0; u < AHEAD; u++) copy(u);
+    load();
     store(0);
-    load(k0 + KS);
+    load();
     int stage = 0;
     auto after = [&](int n) { return stage + n >= STAGES ? stage + n - STAGES : stage + n; };
+    // place(8 i, kk) is a constant; place(tx + 16 j, kk) exchanges neighbouring vectors for tx >= 8: from two bases,
+    // one for even and one for odd vectors, its places are constants too
+    const int turn = (tx >> 3) * 4;
     for (int k = k0; k < k1; k += KS) {
         cp_async_wait<AHEAD - 1>();
         __syncthreads();
-        copy(k + AHEAD * KS, after(AHEAD));
+        copy(after(AHEAD));
         store(after(1));
-        load(k + 2 * KS);
+        load();
+        const float *pa = &As[stage][ty][0], *pe = &Bs[stage][tx][0] + turn, *po = &Bs[stage][tx][0] - turn;
 #pragma unroll
-        for (int kk = 0; kk < KS; kk += 4) {
+        for (int q = 0; q < KS / 4; q++) {
             ulonglong2 x[TM], y[TN];
 #pragma unroll
-            for (int i = 0; i < TM; i++) x[i] = *reinterpret_cast<const ulonglong2*>(&As[stage][ty + 8 * i][place(8 * i, kk)]);
+            for (int i = 0; i < TM; i++) x[i] = *reinterpret_cast<const ulonglong2*>(pa + 8 * i * PITCH + place(8 * i, 4 * q));
 #pragma unroll
-            for (int j = 0; j < TN; j++)
-                y[j] = *reinterpret_cast<const ulonglong2*>(&Bs[stage][tx + 16 * j][place(tx + 16 * j, kk)]);
+            for (int j = 0; j < TN; j++) {
+                const int c = place(16 * j, 4 * q);  // of tx < 8
+                y[j] = *reinterpret_cast<const ulonglong2*>((c & 4 ? po : pe) + 16 * j * PITCH + c);
+            }
 #pragma unroll
             for (int i = 0; i < TM; i++)
 #pragma unroll
