@@ -486,8 +486,9 @@ int gpt2_op_linear_classifier_forward(int dtype, float* losses, float* lse, cons
  * and |dloss + dlse|: half a step (2^-8) of each value; sums are fp32. p carries lse's own
  * rounding (|lse| 2^-24, relative). Deterministic (no atomics). dx and dw must
  * not overlap the inputs or each other. Limits as in the forward; N = 0 sets
- * dw to 0 (or leaves it, with accumulate). Scratch: a piece of dz (about 256 MB,
- * or 2048 columns where that is more), dx in fp32, partial products. */
+ * dw to 0 (or leaves it, with accumulate). Scratch: a piece of dz (up to 1 GB,
+ * or 2048 columns where that is more), dx in fp32 where there are several
+ * pieces, partial products. */
 size_t gpt2_op_linear_classifier_backward_scratch(int dtype, int N, int C, int V, int Vp, int accumulate);
 int gpt2_op_linear_classifier_backward(int dtype, void* dx, void* dw, int dw_fp32, int accumulate, const void* x,
                                        const void* w, const int32_t* targets, const float* lse, const float* dloss,
@@ -584,6 +585,12 @@ int gpt2_debug_stall_matmul(int on);
  * the number of clusters the pair kernel launches (on != 0) or 0. A switch
  * for measurements and tests, not needed in normal use. */
 int gpt2_debug_matmul_pair(int on);
+
+/* gpt2_debug_linear_classifier_piece: the bytes that a piece of dz may take in
+ * gpt2_op_linear_classifier_backward (and its scratch call), instead of 1 GB;
+ * bytes <= 0 restores that. Process-wide, for measurements and tests: not
+ * between a scratch call and the call that uses the scratch. Returns GPT2_OK. */
+int gpt2_debug_linear_classifier_piece(int64_t bytes);
 
 #ifdef __cplusplus
 }

@@ -26,8 +26,11 @@ namespace {
 
 constexpr float LOG2E = 1.4426950408889634f;
 
-// What one piece of dz may take; see pieces().
-constexpr int64_t PIECE_BYTES = 256ll << 20;
+// What one piece of dz may take. The gradients of 8192 x 768 x 50257 in pieces of 14592 columns (239 MB) 1337 us, 19456
+// 1315, 29184 1295, all at once (824 MB) 1275; of 32768 rows 4096 (268 MB) 5573, 4864 5351, 8192 5363, 12800 (839 MB)
+// 5077, 25344 5016, all at once (3.3 GB) 4924: each piece costs its launches, their tails and a pass over dx.
+constexpr int64_t PIECE_BYTES = 1ll << 30;
+int64_t g_piece_bytes = PIECE_BYTES;  // (linear_classifier_piece() sets it for measurements and tests)
 
 struct Pieces {
     int width, n;
@@ -41,13 +44,12 @@ int64_t rounds_cost(int N, int C, int cols, int pairs) {
     return (mt * ct + pairs - 1) / pairs * C * 256 + (ct * kt + pairs - 1) / pairs * N * 192;
 }
 
-// Pieces of one width, a whole number of tiles, that hold PIECE_BYTES for all rows (but no fewer than 2048 columns);
-// of the widths from half of that on, the one whose rounds cost least. The gradients of 8192 x 768 x 50257: 14592
-// columns, which fill three rounds of dw and 24 of dz, 1412 us; 12800 (four equal pieces) 1448; 16896 1419; 9728 1430;
-// 4864 1515; 25344 1434; all at once 1477.
+// Pieces of one width, a whole number of tiles, that hold g_piece_bytes for all rows (but no fewer than 2048 columns);
+// of the widths from half of that on, the one whose rounds cost least (8192 x 768 x 50257: 14592 columns, which fill
+// three rounds of dw and 24 of dz, 1337 us; 12800, four equal pieces, 1353).
 Pieces pieces(int dtype, int N, int C, int V) {
     const int64_t es = dtype == GPT2_MODE_BF16 ? 2 : 4;
-    int64_t most = PIECE_BYTES / ((int64_t)N * es) / 256 * 256;
+    int64_t most = g_piece_bytes / ((int64_t)N * es) / 256 * 256;
     if (most < 2048) most = 2048;
     if (V <= most) return {(V + 255) / 256 * 256, 1};
     const int pairs = gpt2_num_sms() / 2;
@@ -151,6 +153,8 @@ __global__ void __launch_bounds__(1024) rows_kernel(float* __restrict__ scale, c
 constexpr int ROWS_A_BLOCK = 32768, FIND_ROWS = 2048;
 
 }  // namespace
+
+void linear_classifier_piece(int64_t bytes) { g_piece_bytes = bytes > 0 ? bytes : PIECE_BYTES; }
 
 // Statistics, target logits.
 size_t linear_classifier_forward_scratch(int dtype, int N, int C, int V) {

@@ -230,6 +230,9 @@ int launch_linear_classifier_backward(int dtype, void* dx, void* dw, int dw_fp32
                                       const float* dlse, int N, int C, int V, int Vp, void* scratch, int* status,
                                       cudaStream_t s);
 
+// The bytes that a piece of dz may take (<= 0: the default).
+void linear_classifier_piece(int64_t bytes);
+
 // AdamW over many tensors (gpt2_op_adamw_many): validated arguments.
 size_t adamw_many_scratch(const gpt2_adamw_tensor* t, int n);
 int launch_adamw_many(const gpt2_adamw_tensor* t, int n, int grad_dtype, int bits, float lr, float b1, float b2,

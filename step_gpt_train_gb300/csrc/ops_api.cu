@@ -611,6 +611,11 @@ int gpt2_debug_set_wait_limit(int64_t cycles) {
 
 int gpt2_debug_stall_matmul(int on) { return gemm_tc_stall_for_test(on) ? GPT2_ERR_CUDA : GPT2_OK; }
 
+int gpt2_debug_linear_classifier_piece(int64_t bytes) {
+    linear_classifier_piece(bytes);
+    return GPT2_OK;
+}
+
 int gpt2_debug_matmul_pair(int on) { return gemm_tc_use_pair(on); }
 
 }  // extern "C"

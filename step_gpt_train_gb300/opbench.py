@@ -366,6 +366,56 @@ def main(argv=None):
 
     ops["adamw"] = (adamw, 124_475_904 * 30.0, "byte")
 
+    # Head norms with rotary positions in the fused qkv buffer, the loss without logits, AdamW over the model's tensors.
+    def rotary(backward):
+        def setup():
+            x, (q, k) = rnd(N, 3 * C), (torch.empty(N, H, C // H, device=dev, dtype=bf) for _ in range(2))
+            heads = lambda x, i: x[:, i * C:(i + 1) * C].unflatten(1, (H, C // H))  # noqa: E731
+            pos = torch.arange(N, device=dev, dtype=torch.int32) % T
+            turns, gam = g.gpt2_rotary_turns(C // H).to(dev), torch.ones(C // H, device=dev, dtype=bf)
+            kw = dict(q_gamma=gam, k_gamma=gam, eps=1e-6)
+            if not backward:
+                return lambda: g.gpt2_op_qk_norm_rotary_forward(q, k, heads(x, 0), heads(x, 1), pos, turns, **kw)
+            dx, dg = torch.empty_like(x), [torch.empty(C // H, device=dev) for _ in range(2)]
+            return lambda: g.gpt2_op_qk_norm_rotary_backward(heads(dx, 0), heads(dx, 1), q, k, heads(x, 0), heads(x, 1), pos,
+                                                             turns, dq_gamma=dg[0], dk_gamma=dg[1], **kw)
+        return setup
+
+    ops["qk_norm_rotary_fwd"] = (rotary(False), N * (2.0 * C * 2 * 2 + 4), "byte")
+    ops["qk_norm_rotary_bwd"] = (rotary(True), N * (3.0 * C * 2 * 2 + 4), "byte")
+
+    def linear_classifier(backward):
+        def setup():
+            x, w = rnd(N, C), rnd(Vp, C, std=0.05)
+            tgt = torch.randint(0, V, (N,), device=dev, dtype=torch.int32)
+            losses, lse = torch.empty(N, device=dev), torch.empty(N, device=dev)
+            fwd = lambda: g.gpt2_op_linear_classifier_forward(losses, lse, x, w, tgt, V)  # noqa: E731
+            if not backward:
+                return fwd
+            fwd()
+            d, dx, dw = torch.full((N,), 1.0 / N, device=dev), torch.empty_like(x), torch.empty(Vp, C, device=dev)
+            return lambda: g.gpt2_op_linear_classifier_backward(dx, dw, x, w, tgt, lse, V, dloss=d)
+        return setup
+
+    ops["linear_classifier_fwd"] = (linear_classifier(False), 2.0 * N * C * V, "flop")
+    ops["linear_classifier_bwd"] = (linear_classifier(True), 6.0 * N * C * V, "flop")
+
+    def adamw_many(bits):
+        def setup():
+            one = [C, C, 3 * C * C, 3 * C, C * C, C, C, C, 4 * C * C, 4 * C, 4 * C * C, C]
+            sizes = [Vp * C, T * C] + 12 * one + [C, C]
+            f = lambda: [torch.randn(n, device=dev) for n in sizes]  # noqa: E731
+            m = torch.uint8 if bits == 8 else torch.float32
+            z = lambda per=1: [torch.zeros(-(-n // per), device=dev, dtype=m) for n in sizes]  # noqa: E731
+            kw = {"m_scales": z(128), "v_scales": z(128)} if bits == 8 else {}
+            h = g.gpt2_adamw_tensors(f(), f(), z(), z(), params=[torch.empty(n, device=dev, dtype=bf) for n in sizes], **kw)
+            return lambda: g.gpt2_op_adamw_many(h, 1e-9, 0.9, 0.95, 1e-8, 1)
+        return setup
+
+    values = Vp * C + T * C + 12 * (12 * C * C + 13 * C) + 2 * C
+    ops["adamw_many"] = (adamw_many(32), values * 30.0, "byte")
+    ops["adamw_many_8bit"] = (adamw_many(8), values * (18.0 + 4 / 128), "byte")
+
     def enc_fwd():
         tok = torch.randint(0, V, (B, T), device=dev, dtype=torch.int32)
         wte, wpe = rnd(Vp, C), rnd(T, C)

@@ -233,16 +233,48 @@ def test_classifier(dtype, dw_dtype, N, C, V):
     classifier_case(N, C, V, dtype, dw_dtype)
 
 
+@pytest.fixture
+def pieces_of_256_mb():
+    lib = g.load_library()
+    g.check(lib.gpt2_debug_linear_classifier_piece(256 << 20))
+    yield
+    g.check(lib.gpt2_debug_linear_classifier_piece(0))
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
-def test_classifier_in_pieces(dtype):
+def test_classifier_in_pieces(dtype, pieces_of_256_mb):
     # 70000 rows: pieces of 2048 columns, the last of them ragged
     classifier_case(70000, 16, 4357, dtype, F32, Vp=4400)
 
 
 @pytest.mark.parametrize("C", [768, 1024, 640])
-def test_classifier_adds_dx_from_piece_to_piece(C):
+def test_classifier_adds_dx_from_piece_to_piece(C, pieces_of_256_mb):
     # two pieces; dx in 192-wide tiles of CTA pairs, in 256-wide ones, in tiles of one CTA
     classifier_case(8192, C, 17001, BF, BF, dlse=False)
+
+
+@pytest.mark.parametrize("C", [768, 1024])
+def test_classifier_of_many_rows_at_once(C):
+    # one piece: dx and dw straight from 192-wide and 256-wide tiles of CTA pairs
+    classifier_case(8192, C, 9001, BF, BF, Vp=9216, dlse=False)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("N", [300, 2048, 2049, 40000, 70001])
+def test_classifier_of_means_over_any_number(N, dtype):
+    # 1 / N in every row, which bf16 does not hold: the gradients are off by their values' own roundings only
+    C, V = 64, 100
+    x, w, t = hidden(N, C, V, 104, dtype)
+    _, lse = forward(x, w, t, V)
+    d = torch.full((N,), 1.0 / N, device="cuda")
+    dx, dw = torch.empty_like(x), torch.empty(104, C, device="cuda")
+    g.gpt2_op_linear_classifier_backward(dx, dw, x, w, t, lse, V, dloss=d)
+    rx, rw, _, _ = R.classifier_backward(x.double(), w.double(), t, V, d.double(), None, dtype)
+    # the sum of dw over the vocabulary's rows along the gradient itself: a common factor would show
+    along = ((dw[:V].double() * rw).sum() / (rw * rw).sum()).item()
+    # roundings of 100 N values of dz, none off by more than 2^-8 and of either sign: 2^-8 / sqrt(3) / sqrt(N) at most
+    # of each row's largest, five times that, and fp32 sums
+    assert abs(along - 1) < 5 * (2.0 ** -8 if dtype is BF else 2.0 ** -20) / math.sqrt(3 * N) + 2e-6
 
 
 def test_classifier_of_the_models_vocabulary():
