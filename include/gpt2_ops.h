@@ -518,8 +518,9 @@ int gpt2_op_linear_classifier_backward(int dtype, void* dx, void* dw, int dw_fp3
  *       of a block lies in [2^7, 2^8]; 0x7F and 0xFF are NaN;
  *   v   5 exponent bits (bias 15), 3 mantissa bits, no sign (the top of an
  *       fp16 number); the largest lies in [2^14, 2^15]; NaN is written as 0xFF.
- * Both have subnormals. The new m and v are formed in fp32 and used for theta
- * as they are; stored, they are rounded up or down to a neighbouring code so
+ * Both have subnormals. The new m and v are formed in fp32, with each product
+ * and sum rounded on its own (b1 m + (1-b1) g, b2 v + (1-b2) (g g)), and used
+ * for theta as they are; stored, they are rounded up or down to a neighbouring code so
  * that they are right on average: up where (what is left over the lower code)
  * / (the codes' distance) + u >= 1, with u = r / 2^16 and r 16 bits of
  * splitmix64's finaliser mix: values 2p and 2p + 1 of tensor k (from 0 in the

@@ -202,7 +202,7 @@ template <typename G, bool EIGHT, bool WHOLE>
 __device__ __forceinline__ void adamw_chunk(const Entry& e, const Values& h, int64_t base, uint64_t draw) {
     const int64_t n = e.n;
     float gs = h.grad_scale;
-    if (h.norm) gs *= fminf(1.f, h.max_norm / (*h.norm * h.grad_scale + 1e-6f));
+    if (h.norm) gs *= fminf(1.f, h.max_norm / __fadd_rn(__fmul_rn(*h.norm, h.grad_scale), 1e-6f));
     float th[GROUPS][4], g[GROUPS][4], m[GROUPS][4], v[GROUPS][4];
     uint32_t cm[GROUPS], cv[GROUPS];
     uint8_t bm[GROUPS], bv[GROUPS];
@@ -238,8 +238,13 @@ __device__ __forceinline__ void adamw_chunk(const Entry& e, const Values& h, int
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             const float gj = g[u][j] * gs;
-            m[u][j] = h.b1 * m[u][j] + b1c * gj;
-            v[u][j] = h.b2 * v[u][j] + b2c * gj * gj;
+            if (EIGHT) {  // (each product and sum rounded on its own: the codes that follow are everyone's)
+                m[u][j] = __fadd_rn(__fmul_rn(h.b1, m[u][j]), __fmul_rn(b1c, gj));
+                v[u][j] = __fadd_rn(__fmul_rn(h.b2, v[u][j]), __fmul_rn(b2c, __fmul_rn(gj, gj)));
+            } else {
+                m[u][j] = h.b1 * m[u][j] + b1c * gj;
+                v[u][j] = h.b2 * v[u][j] + b2c * gj * gj;
+            }
             th[u][j] -= h.lr * (step_of<EIGHT>(m[u][j] * h.inv_bc1, v[u][j] * h.inv_bc2, h.eps) + e.decay * th[u][j]);
         }
         put4(e.master, i, n, whole(u), th[u]);
@@ -312,26 +317,36 @@ __global__ void __launch_bounds__(THREADS) adamw_many_kernel(const __grid_consta
     else adamw_chunk<G, EIGHT, false>(e, h, base, draw);
 }
 
+// A sum of squares in two fp32 numbers: four squares at a time, and what a rounding of `sum` drops goes to `rest`. The
+// norm scales every gradient, and a last bit of it can move codes of 8-bit moments: so it is summed to about its last
+// bit, the four squares' roundings being of either sign and far below the whole. (124M values: 81 us; each square exact
+// and on its own 100, in plain fp32 sums 80; in 64 bits the pass would take twice the time of its reads.)
+struct Squares {
+    float sum = 0.f, rest = 0.f;
+    __device__ __forceinline__ void add(const float (&g)[4]) {
+        const float p = fmaf(g[3], g[3], fmaf(g[2], g[2], fmaf(g[1], g[1], g[0] * g[0])));
+        const float t = __fadd_rn(sum, p), z = __fsub_rn(t, sum);
+        rest = __fadd_rn(rest, __fadd_rn(__fsub_rn(sum, __fsub_rn(t, z)), __fsub_rn(p, z)));
+        sum = t;
+    }
+};
+
 // Sums of squares of the gradients: a block takes every gridDim.x-th chunk and adds in a fixed order.
 template <int MOST, typename G>
 __global__ void __launch_bounds__(THREADS) sumsq_many_kernel(const __grid_constant__ Batch<MOST> b, int chunks,
-                                                             float* __restrict__ partial) {
-    __shared__ float sh[THREADS / 32];
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                                                             double* __restrict__ partial) {
+    __shared__ double sh[THREADS / 32];
+    Squares acc[2];
     for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
         const Entry& e = b.e[find<&Entry::first_wide>(b, c)];
         const int64_t n = e.n, first = (int64_t)(c - e.first_wide) * WIDE, base = first + threadIdx.x * 4;
         constexpr int LOADS = WIDE / (THREADS * 4);
-        auto add = [&](const float (&g)[4]) {
-#pragma unroll
-            for (int j = 0; j < 4; j++) acc[j] = fmaf(g[j], g[j], acc[j]);
-        };
         if (e.aligned && first + WIDE <= n) {
             float g[LOADS][4];
 #pragma unroll
             for (int u = 0; u < LOADS; u++) load4((const G*)e.grad + base + u * (THREADS * 4), g[u]);
 #pragma unroll
-            for (int u = 0; u < LOADS; u++) add(g[u]);
+            for (int u = 0; u < LOADS; u++) acc[u % 2].add(g[u]);
         } else {
 #pragma unroll 4
             for (int u = 0; u < LOADS; u++) {
@@ -339,15 +354,19 @@ __global__ void __launch_bounds__(THREADS) sumsq_many_kernel(const __grid_consta
                 if (i >= n) break;
                 float g[4];
                 get4((const G*)e.grad, i, n, e.aligned && i + 4 <= n, g);
-                add(g);
+                acc[u % 2].add(g);
             }
         }
     }
-    const float s = warp_sum((acc[0] + acc[1]) + (acc[2] + acc[3]));
+    double s = 0.0;
+#pragma unroll
+    for (int j = 0; j < 2; j++) s += (double)acc[j].sum + (double)acc[j].rest;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = s;
     __syncthreads();
     if (threadIdx.x == 0) {
-        float t = 0.f;
+        double t = 0.0;
 #pragma unroll
         for (int w = 0; w < THREADS / 32; w++) t += sh[w];
         partial[blockIdx.x] = t;
@@ -355,7 +374,7 @@ __global__ void __launch_bounds__(THREADS) sumsq_many_kernel(const __grid_consta
 }
 
 __global__ void __launch_bounds__(1024) norm_many_kernel(float* __restrict__ norm, float* __restrict__ out,
-                                                         const float* __restrict__ partial, int n) {
+                                                         const double* __restrict__ partial, int n) {
     __shared__ double sh[32];
     double v = 0.0;
     for (int i = threadIdx.x; i < n; i += 1024) v += partial[i];
@@ -480,7 +499,7 @@ size_t adamw_many_scratch(const gpt2_adamw_tensor* t, int n) {
     int64_t wide = 0;
     for (int i = 0; i < n; i++) wide += (t[i].n + WIDE - 1) / WIDE;
     const int64_t most = (int64_t)sumsq_blocks() * (n / MANY + 1);
-    return 256 + (size_t)(wide < most ? wide : most) * 4;
+    return 256 + (size_t)(wide < most ? wide : most) * 8;
 }
 
 int launch_adamw_many(const gpt2_adamw_tensor* t, int n, int grad_dtype, int bits, float lr, float b1, float b2,
@@ -493,7 +512,7 @@ int launch_adamw_many(const gpt2_adamw_tensor* t, int n, int grad_dtype, int bit
     auto as_is = [](Entry&, int) {};
     if (max_norm > 0.f || grad_norm) {
         float* norm = (float*)scratch;
-        float* partial = norm + 64;
+        double* partial = (double*)(norm + 64);
         int at = 0;
         launches += in_batches(t, n, as_is, [&](const auto& b, int, int wide) {
             constexpr int MOST = sizeof(b.e) / sizeof(Entry);

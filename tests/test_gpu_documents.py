@@ -697,6 +697,32 @@ def test_adamw_many_of_more_values_than_31_bits(bits):
     assert not s["masters"][0][:-tail].any() and not s["ms"][0][:-tail].any()
 
 
+@pytest.mark.parametrize("grads", [F32, BF])
+def test_eight_bit_codes_are_those_of_plain_fp32_steps(grads):
+    # each product and sum rounded on its own, the norm to its last bit: elementary fp32 operations give the same codes
+    s = tensors([200001, 3000], 8, grads)
+    h = g.gpt2_adamw_tensors(**s)
+    f = lambda x: torch.tensor(x, dtype=F32, device="cuda")  # noqa: E731
+    for t in (1, 2, 3):
+        before = held(s)
+        g.gpt2_op_adamw_many(h, **HP, t=t, grad_scale=0.25, max_grad_norm=0.5, seed=21)
+        norm = sum(x.double().square().sum() for x in before["grads"]).sqrt().float()
+        scale = f(0.25) * (f(0.5) / (norm * f(0.25) + f(1e-6))).clamp_max(1.0)
+        for i in range(2):
+            gr = before["grads"][i].float() * scale
+            b1, b2 = f(HP["beta1"]), f(HP["beta2"])
+            m0, v0 = (R.values(before[a][i], before[b][i], k).float() for a, b, k in (("ms", "m_scales", "m"),
+                                                                                     ("vs", "v_scales", "v")))
+            m, v = b1 * m0 + (1 - b1) * gr, b2 * v0 + (1 - b2) * (gr * gr)
+            for x, u, code, sc, kind in zip((m, v), R.draws(gr.numel(), i, t, 21, "cuda"), ("ms", "vs"),
+                                            ("m_scales", "v_scales"), "mv"):
+                assert torch.equal(s[sc][i].long(), R.scales(x.double(), kind))
+                got, want = R.values(s[code][i], s[sc][i], kind), R.stored(x.double(), s[sc][i].long(), u, kind)
+                unit = torch.exp2(s[sc][i].double() - 127)[torch.arange(len(x), device="cuda") // 128]
+                lowest = unit * 2.0 ** (-6 if kind == "m" else -14)  # (below it the code's own arithmetic rounds)
+                assert ((got == want) | (x.double().abs() < lowest)).all() and (got != want).sum() < 5
+
+
 def test_eight_bit_moments_follow_the_gradients_size():
     # gradients of one size for long, then of a tenth of it: v comes down too, which nearest rounding would not let it
     n = 4096
