@@ -31,6 +31,10 @@
 // that run at the same time read the same k-blocks of A and B in lockstep and
 // share them through L2. A split unit stores an fp32 partial tile; a reduce
 // kernel adds the S partials of each tile in split order (deterministic).
+// The linear classifier (classifier_linear.cu) runs the same kernels with
+// epilogues of its own: EPI_LSE reduces the logits of a half tile to row
+// statistics, EPI_DZ turns them into their gradient, EPI_ADD adds its tile to
+// D by the storing copy, EPI_SCALE multiplies by a device scalar.
 // Every mbarrier wait is bounded: on timeout the kernel sets a status bit,
 // stops, waits (bounded) for its own copies and MMAs, frees TMEM and returns.
 #include "common.cuh"
