@@ -666,6 +666,9 @@ def _rows(what, like, *more):
     for t in (like, *more):
         if t is not like and (t.dtype is not dtype or t.shape != shape):
             raise ValueError(f"{what} need one shape and type")
+        if t.is_contiguous():
+            strides.append(heads * hd)
+            continue
         s0, s1, s2 = t.stride()
         if s2 != 1 or (s1 != hd and heads > 1):
             raise ValueError(f"{what}: the heads of a row have to be contiguous")

@@ -773,6 +773,49 @@ def test_adamw_many_repeats_and_follows_graphs_and_streams(bits):
 
 # ---------------------------------------------------------------- together
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_calls_on_two_streams_at_once(dtype):
+    """Two programs of the same calls, several deep on a stream each, write what they write alone."""
+    def program(rows, C, V):
+        x, w, t = hidden(rows, C, V, dtype=dtype)
+        s = rotary_state(dtype, rows, 4, 2, 64, 64, True, False)
+        a = tensors([5000, 77, 40000], 8 if dtype is BF else 32)
+        start, h = held(a), g.gpt2_adamw_tensors(**a)
+        d, kw = rnd(rows), dict(q_gamma=s["q_gamma"], k_gamma=s["k_gamma"], eps=s["eps"])
+        out = [torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda"), torch.empty_like(x), torch.empty_like(w),
+               torch.empty_like(s["q"]), torch.empty_like(s["k"]), torch.empty(64, device="cuda"),
+               torch.empty(64, device="cuda")]
+        written = out + [y for k in ("masters", "params", "ms", "vs", "m_scales", "v_scales") for y in a.get(k, [])]
+
+        def run():
+            for k, ys in start.items():
+                for y, was in zip(a[k], ys):
+                    y.copy_(was)
+            g.gpt2_op_linear_classifier_forward(out[0], out[1], x, w, t, V)
+            g.gpt2_op_linear_classifier_backward(out[2], out[3], x, w, t, out[1], V, dloss=d)
+            g.gpt2_op_qk_norm_rotary_backward(out[4], out[5], s["q"], s["k"], s["q"], s["k"], s["pos"], s["turns"],
+                                              dq_gamma=out[6], dk_gamma=out[7], **kw)
+            g.gpt2_op_adamw_many(h, **HP, t=4, max_grad_norm=0.3, seed=8)
+        return run, written
+    programs = [program(300, 64, 3001), program(700, 128, 1777)]
+    alone = []
+    for run, written in programs:
+        run()
+        alone.append([y.clone() for y in written])
+    for _, written in programs:
+        for y in written:
+            y.zero_()
+    streams = [torch.cuda.Stream() for _ in programs]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for (run, _), stream in zip(programs, streams):
+            with torch.cuda.stream(stream):
+                run()
+    torch.cuda.synchronize()
+    for (_, written), want in zip(programs, alone):
+        assert all(torch.equal(y, z) for y, z in zip(written, want))
+
+
 def test_a_step_on_packed_documents():
     """Positions, attention over documents, the loss and the update, as a program runs them: the gradients against
     autograd in 64 bits, the update against the oracle."""
