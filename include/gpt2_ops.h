@@ -498,8 +498,9 @@ int gpt2_op_linear_classifier_backward(int dtype, void* dx, void* dw, int dw_fp3
 /* AdamW over many tensors at once, with moments in 32 or in 8 bits (an
  * addition of this library: gpt2_op_adamw for a list of tensors of any sizes).
  * For each value of each tensor, with g = grad * grad_scale * clip, clip =
- * min(1, max_grad_norm / (||grad|| grad_scale + 1e-6)) over all tensors if
- * max_grad_norm > 0, else 1 (as gpt2_adamw_step_ex):
+ * min(1, max_grad_norm / (||grad|| |grad_scale| + 1e-6)) over all tensors if
+ * max_grad_norm > 0, else 1 (as gpt2_adamw_step_ex). Squares are formed in
+ * fp32: from about 1e19 on ||grad|| is infinite, and clip 0; a NaN clips nothing.
  *   m = b1 m + (1-b1) g; v = b2 v + (1-b2) g^2;
  *   theta -= lr (m/(1-b1^t) / (sqrt(v/(1-b2^t)) + eps) + weight_decay theta),
  * and bf16(theta) to param_bf16 where that is not null. grad_norm, if not

@@ -202,7 +202,7 @@ template <typename G, bool EIGHT, bool WHOLE>
 __device__ __forceinline__ void adamw_chunk(const Entry& e, const Values& h, int64_t base, uint64_t draw) {
     const int64_t n = e.n;
     float gs = h.grad_scale;
-    if (h.norm) gs *= fminf(1.f, h.max_norm / __fadd_rn(__fmul_rn(*h.norm, h.grad_scale), 1e-6f));
+    if (h.norm) gs *= fminf(1.f, h.max_norm / __fadd_rn(__fmul_rn(*h.norm, fabsf(h.grad_scale)), 1e-6f));
     float th[GROUPS][4], g[GROUPS][4], m[GROUPS][4], v[GROUPS][4];
     uint32_t cm[GROUPS], cv[GROUPS];
     uint8_t bm[GROUPS], bv[GROUPS];
@@ -360,7 +360,8 @@ __global__ void __launch_bounds__(THREADS) sumsq_many_kernel(const __grid_consta
     }
     double s = 0.0;
 #pragma unroll
-    for (int j = 0; j < 2; j++) s += (double)acc[j].sum + (double)acc[j].rest;
+    for (int j = 0; j < 2; j++)  // (a sum past fp32's range is infinite and what it dropped is NaN)
+        s += (double)acc[j].sum + (isinf(acc[j].sum) ? 0.0 : (double)acc[j].rest);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = s;

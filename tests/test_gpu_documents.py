@@ -771,6 +771,42 @@ def test_adamw_many_repeats_and_follows_graphs_and_streams(bits):
     assert all(torch.equal(a, b) for a, b in zip(written, first))
 
 
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("grads", [F32, BF])
+@pytest.mark.parametrize("far", [math.inf, -math.inf, 1e30])
+def test_adamw_many_clips_by_an_infinite_norm(far, grads, bits):
+    """Gradients whose squares' sum is no fp32 number clip all finite ones to 0."""
+    s = tensors([20000, 700], bits, grads)
+    s["grads"][0][9000] = far
+    clean = held(s) | {"weight_decay": s["weight_decay"]}
+    norm = torch.zeros(1, device="cuda")
+    g.gpt2_op_adamw_many(g.gpt2_adamw_tensors(**s), **HP, t=2, seed=1, max_grad_norm=1.0, grad_norm=norm)
+    assert norm.item() == math.inf
+    for x in clean["grads"]:
+        x.zero_()
+    g.gpt2_op_adamw_many(g.gpt2_adamw_tensors(**clean), **HP, t=2, seed=1)
+    for k in ("masters", "params", "ms", "vs"):
+        for i, (a, b) in enumerate(zip(s[k], clean[k])):
+            same = torch.ones(a.numel(), dtype=torch.bool, device="cuda")
+            if math.isinf(far) and i == 0:  # inf * 0 is NaN, where it is; the block's scale is that of the other values
+                same[9000 // 128 * 128:(9000 // 128 + 1) * 128] = bits == 32 or k in ("masters", "params")
+                same[9000] = False
+            assert torch.equal(a[same], b[same]), (k, i)
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_adamw_many_clips_a_negative_scale(bits):
+    """grad_scale < 0 turns the gradients round, clipped or not."""
+    s = tensors([5000, 700], bits)
+    turned = held(s) | {"weight_decay": s["weight_decay"]}
+    for x in turned["grads"]:
+        x.neg_()
+    g.gpt2_op_adamw_many(g.gpt2_adamw_tensors(**s), **HP, t=2, seed=1, max_grad_norm=0.5, grad_scale=-0.25)
+    g.gpt2_op_adamw_many(g.gpt2_adamw_tensors(**turned), **HP, t=2, seed=1, max_grad_norm=0.5, grad_scale=0.25)
+    for k in ("masters", "params", "ms", "vs"):
+        assert all(torch.equal(a, b) for a, b in zip(s[k], turned[k])), k
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("dtype", [BF, F32])
