@@ -1015,7 +1015,8 @@ def gpt2_op_linear_classifier_backward(dx, dw, x, w, targets, lse, V, dloss=None
 
 
 class AdamWTensors:
-    """The tensors of gpt2_op_adamw_many calls, checked once; holds them while it lives. From gpt2_adamw_tensors."""
+    """The tensors of gpt2_op_adamw_many calls, checked once; holds their memory while it lives. From
+    gpt2_adamw_tensors."""
     __slots__ = ("array", "address", "count", "grads", "bits", "device", "scratch", "values", "mode", "held")
 
 
@@ -1024,7 +1025,10 @@ def gpt2_adamw_tensors(masters, grads, ms, vs, params=None, m_scales=None, v_sca
     """A list of tensors for gpt2_op_adamw_many. For each: master (float32), grad (float32 or bfloat16, all alike), m
     and v (float32, or uint8 codes with m_scales and v_scales, uint8 [ceil(n / 128)]), params (bfloat16 or None)
     and weight_decay (a number, or one for each). m_values, v_values: where gpt2_op_adamw_many_states writes the
-    values of 8-bit moments (float32 or bfloat16, all alike). All contiguous, on one device."""
+    values of 8-bit moments (float32 or bfloat16, all alike). All contiguous, on one device.
+
+    The list is one of memory: it keeps what the tensors stand on at this call, and a tensor that is given other memory
+    later (`.data`, `set_`) is not followed. The memory must not be resized while the list lives."""
     torch = _tc()
     n = len(masters)
     decay = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else [float(x) for x in weight_decay]
@@ -1053,6 +1057,7 @@ def gpt2_adamw_tensors(masters, grads, ms, vs, params=None, m_scales=None, v_sca
     kinds["v_values"] = kinds["m_values"]
     h.array = (gpt2_adamw_tensor * max(n, 1))()
     values = (c_void_p * max(n, 1))(), (c_void_p * max(n, 1))()
+    memory = []
     for i, master in enumerate(masters):
         size = master.numel()
         of = {"masters": (master, torch.float32, size)}
@@ -1067,6 +1072,8 @@ def gpt2_adamw_tensors(masters, grads, ms, vs, params=None, m_scales=None, v_sca
                 raise ValueError(f"{k}: contiguous {dtype} of {count} values is needed for tensor {i}")
             elif t.get_device() != h.device:
                 raise RuntimeError("gpt2_adamw_tensors: every tensor has to be on one device")
+            else:
+                memory.append(t.untyped_storage())
         a = h.array[i]
         a.master, a.param_bf16, a.grad, a.m, a.v, a.m_scale, a.v_scale = (
             _p(of[k][0]) for k in ("masters", "params", "grads", "ms", "vs", "m_scales", "v_scales"))
@@ -1077,7 +1084,7 @@ def gpt2_adamw_tensors(masters, grads, ms, vs, params=None, m_scales=None, v_sca
         h.values = tuple(ctypes.addressof(v) for v in values)
     h.address = ctypes.addressof(h.array)
     h.scratch = load_library().gpt2_op_adamw_many_scratch(h.address, n)
-    h.held = (list(masters), columns, values)
+    h.held = (memory, values)
     return h
 
 

@@ -1,0 +1,55 @@
+"""Head norms with rotary positions, the cross entropy of hidden states and AdamW over many tensors: what the host
+side holds, hands on and refuses (CPU; nothing is launched)."""
+import gc
+import weakref
+
+import numpy as np
+import pytest
+import torch
+
+from step_gpt_train_gb300 import gpt2 as g
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    return g.load_library(build=True)
+
+
+def tensors(bits=32, sizes=(5, 300)):
+    """Columns of a list of tensors, each on memory of its own."""
+    z = lambda dtype, per=1: [torch.zeros(-(-n // per), dtype=dtype) for n in sizes]  # noqa: E731
+    moment = F32 if bits == 32 else torch.uint8
+    c = dict(masters=z(F32), grads=z(F32), ms=z(moment), vs=z(moment), params=z(BF))
+    if bits == 8:
+        c |= dict(m_scales=z(torch.uint8, 128), v_scales=z(torch.uint8, 128), m_values=z(F32), v_values=z(F32))
+    return c
+
+
+# ---------------------------------------------------------------- the list of AdamW over many tensors
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_list_keeps_the_memory_it_was_given(bits):
+    """Tensors that get other memory (`.data`, as Module.to sets it) leave the old one to the list: a step would write
+    to it."""
+    c, alive = tensors(bits), []
+    for xs in c.values():
+        for i, x in enumerate(xs):
+            if x.dtype is BF:
+                continue  # (numpy has no such type)
+            a = np.zeros(x.numel(), dtype=x.numpy().dtype)
+            alive.append(weakref.ref(a))
+            xs[i] = torch.from_numpy(a)
+    del a
+    h = g.gpt2_adamw_tensors(**c)
+    address = h.array[1].master
+    assert address == c["masters"][1].data_ptr()
+    for xs in c.values():
+        for x in xs:
+            x.data = torch.zeros_like(x)
+    gc.collect()
+    assert c["masters"][1].data_ptr() != address and all(r() is not None for r in alive)
+    del h
+    gc.collect()
+    assert all(r() is None for r in alive)
