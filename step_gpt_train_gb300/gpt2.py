@@ -1017,7 +1017,8 @@ def gpt2_op_linear_classifier_backward(dx, dw, x, w, targets, lse, V, dloss=None
 class AdamWTensors:
     """The tensors of gpt2_op_adamw_many calls, checked once; holds their memory while it lives. From
     gpt2_adamw_tensors."""
-    __slots__ = ("array", "address", "count", "grads", "bits", "device", "scratch", "values", "mode", "held")
+    __slots__ = ("array", "address", "count", "grads", "bits", "device", "scratch", "values", "mode", "held", "leaves",
+                 "sizes")
 
 
 def gpt2_adamw_tensors(masters, grads, ms, vs, params=None, m_scales=None, v_scales=None, weight_decay=0.0,
@@ -1028,7 +1029,9 @@ def gpt2_adamw_tensors(masters, grads, ms, vs, params=None, m_scales=None, v_sca
     values of 8-bit moments (float32 or bfloat16, all alike). All contiguous, on one device.
 
     The list is one of memory: it keeps what the tensors stand on at this call, and a tensor that is given other memory
-    later (`.data`, `set_`) is not followed. The memory must not be resized while the list lives."""
+    later (`.data`, `set_`) is not followed. The memory must not be resized while the list lives. Gradients that are new
+    tensors in each step go to gpt2_op_adamw_many; where a gradient here is the .grad of its master or of its parameter,
+    a step without them refuses once it no longer is."""
     torch = _tc()
     n = len(masters)
     decay = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else [float(x) for x in weight_decay]
@@ -1057,7 +1060,7 @@ def gpt2_adamw_tensors(masters, grads, ms, vs, params=None, m_scales=None, v_sca
     kinds["v_values"] = kinds["m_values"]
     h.array = (gpt2_adamw_tensor * max(n, 1))()
     values = (c_void_p * max(n, 1))(), (c_void_p * max(n, 1))()
-    memory = []
+    memory, h.leaves, h.sizes = [], [], []
     for i, master in enumerate(masters):
         size = master.numel()
         of = {"masters": (master, torch.float32, size)}
@@ -1074,6 +1077,9 @@ def gpt2_adamw_tensors(masters, grads, ms, vs, params=None, m_scales=None, v_sca
                 raise RuntimeError("gpt2_adamw_tensors: every tensor has to be on one device")
             else:
                 memory.append(t.untyped_storage())
+        h.sizes.append(size)
+        h.leaves += [(i, t, columns["grads"][i]) for t in (master, columns["params"][i])
+                     if t is not None and t.is_leaf and t.grad is columns["grads"][i]]
         a = h.array[i]
         a.master, a.param_bf16, a.grad, a.m, a.v, a.m_scale, a.v_scale = (
             _p(of[k][0]) for k in ("masters", "params", "grads", "ms", "vs", "m_scales", "v_scales"))
@@ -1084,17 +1090,37 @@ def gpt2_adamw_tensors(masters, grads, ms, vs, params=None, m_scales=None, v_sca
         h.values = tuple(ctypes.addressof(v) for v in values)
     h.address = ctypes.addressof(h.array)
     h.scratch = load_library().gpt2_op_adamw_many_scratch(h.address, n)
-    h.held = (memory, values)
+    h.held = [memory, values, None]  # (and the gradients of later steps)
     return h
 
 
+def _check_grads(tensors, grads):
+    """Whether these tensors can take the place of the list's gradients."""
+    dtype = _torch.bfloat16 if tensors.grads == MODE_BF16 else _torch.float32
+    if len(grads) != tensors.count:
+        raise ValueError(f"grads: {tensors.count} tensors are needed")
+    for t, size in zip(grads, tensors.sizes):
+        if t is None or t.dtype is not dtype or t.numel() != size or not t.is_contiguous():
+            raise ValueError(f"grads: contiguous {dtype} of the list's sizes is needed")
+        if t.get_device() != tensors.device:
+            raise _elsewhere("gpt2_op_adamw_many")
+
+
 def gpt2_op_adamw_many(tensors, lr, beta1, beta2, eps, t, grad_scale=1.0, max_grad_norm=0.0, grad_norm=None, seed=0,
-                       stream=None):
+                       stream=None, grads=None):
     """One AdamW step t on the tensors of a gpt2_adamw_tensors list; grad_norm (float32 [1]) receives the norm of the
-    gradients over all of them, which max_grad_norm > 0 clips. seed: of the rounding of 8-bit moments."""
+    gradients over all of them, which max_grad_norm > 0 clips. seed: of the rounding of 8-bit moments. grads: gradients
+    that take the place of the list's, from this step on (of the same sizes and type)."""
     what = "gpt2_op_adamw_many"
     lib = load_library()
     device, st = (_tc(), _where(stream))[1]
+    if grads is not None:
+        grads = list(grads)
+        _check_grads(tensors, grads)
+    else:
+        for _, leaf, grad in tensors.leaves:
+            if grad is not None and leaf.grad is not grad:
+                raise RuntimeError(f"{what}: a tensor's .grad is no longer the list's gradient: give this step's grads")
     if tensors.count and tensors.device != device:
         raise _elsewhere(what)
     if grad_norm is not None:
@@ -1102,6 +1128,11 @@ def gpt2_op_adamw_many(tensors, lr, beta1, beta2, eps, t, grad_scale=1.0, max_gr
             raise ValueError("grad_norm: one float32 is needed")
         if grad_norm.get_device() != device:
             raise _elsewhere(what)
+    if grads is not None:
+        for a, x in zip(tensors.array, grads):
+            a.grad = x.data_ptr()
+        tensors.leaves = [(i, leaf, grads[i] if leaf.grad is grads[i] else None) for i, leaf, _ in tensors.leaves]
+        tensors.held[2] = [x.untyped_storage() for x in grads]
     nb = tensors.scratch if max_grad_norm > 0 or grad_norm is not None else 0
     sc = _borrow(nb, st) if nb else None
     try:

@@ -53,3 +53,54 @@ def test_a_list_keeps_the_memory_it_was_given(bits):
     del h
     gc.collect()
     assert all(r() is None for r in alive)
+
+
+def leaves(sizes=(5, 300)):
+    """Parameters whose gradients stand in their .grad."""
+    c = tensors(32, sizes)
+    c["masters"] = [torch.nn.Parameter(x) for x in c["masters"]]
+    for p, x in zip(c["masters"], c["grads"]):
+        p.grad = x
+    return c
+
+
+STEP = dict(lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8, t=1)
+
+
+def test_a_step_refuses_gradients_that_are_no_longer_the_parameters():
+    c = leaves()
+    h = g.gpt2_adamw_tensors(**c)
+    with pytest.raises(RuntimeError, match="current CUDA device"):  # all is well but the device
+        g.gpt2_op_adamw_many(h, **STEP)
+    c["masters"][1].grad = None  # as zero_grad leaves it
+    with pytest.raises(RuntimeError, match="give this step's grads"):
+        g.gpt2_op_adamw_many(h, **STEP)
+    c["masters"][1].grad = torch.zeros(300)  # as the next backward pass does
+    with pytest.raises(RuntimeError, match="give this step's grads"):
+        g.gpt2_op_adamw_many(h, **STEP)
+    c["masters"][1].grad = c["grads"][1]
+    with pytest.raises(RuntimeError, match="current CUDA device"):
+        g.gpt2_op_adamw_many(h, **STEP)
+    # bf16 parameters, their gradients beside fp32 masters
+    c = tensors(32)
+    c["params"] = [torch.nn.Parameter(x) for x in c["params"]]
+    c["grads"] = [x.to(BF) for x in c["grads"]]
+    for p, x in zip(c["params"], c["grads"]):
+        p.grad = x
+    h = g.gpt2_adamw_tensors(**c)
+    c["params"][0].grad = torch.zeros(5, dtype=BF)
+    with pytest.raises(RuntimeError, match="give this step's grads"):
+        g.gpt2_op_adamw_many(h, **STEP)
+
+
+@pytest.mark.parametrize("bad", [[torch.zeros(5)], [torch.zeros(5), torch.zeros(299)], [torch.zeros(5), None],
+                                 [torch.zeros(5), torch.zeros(300, dtype=BF)], [torch.zeros(5), torch.zeros(600)[::2]]],
+                         ids=["one", "short", "missing", "bf16", "strided"])
+def test_a_step_refuses_new_gradients_that_do_not_fit(bad):
+    h = g.gpt2_adamw_tensors(**tensors())
+    before = [h.array[i].grad for i in range(2)]
+    with pytest.raises(ValueError, match="grads"):
+        g.gpt2_op_adamw_many(h, **STEP, grads=bad)
+    with pytest.raises(RuntimeError, match="current CUDA device"):
+        g.gpt2_op_adamw_many(h, **STEP, grads=[torch.zeros(5), torch.zeros(300)])
+    assert [h.array[i].grad for i in range(2)] == before  # what is refused leaves the list as it was

@@ -1,0 +1,74 @@
+"""Head norms with rotary positions, the cross entropy of hidden states and AdamW over many tensors on the GPU where
+they are easily wrong, against the definitions in 64 bits."""
+import math
+
+import pytest
+import torch
+
+from oracle import documents_ref as R
+from step_gpt_train_gb300 import gpt2 as g
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(autouse=True)
+def seed():
+    torch.manual_seed(12)
+    torch.cuda.set_device(0)
+
+
+def rnd(*shape, dtype=F32, std=1.0):
+    return (torch.randn(*shape, device="cuda") * std).to(dtype)
+
+
+# ---------------------------------------------------------------- AdamW over many tensors
+
+@pytest.mark.parametrize("grads", [F32, BF])
+def test_adamw_many_takes_each_steps_gradients(grads):
+    """Gradients that are new tensors in every step, given to one list, do what a new list for each step does."""
+    sizes, hp = [5000, 77, 0, 40000], dict(lr=1e-2, beta1=0.9, beta2=0.95, eps=1e-8, max_grad_norm=0.5)
+    one = {"masters": [rnd(n) for n in sizes], "params": [rnd(n).to(BF) for n in sizes],
+           "ms": [torch.zeros(n, device="cuda") for n in sizes], "vs": [torch.zeros(n, device="cuda") for n in sizes]}
+    two = {k: [x.clone() for x in v] for k, v in one.items()}
+    h = g.gpt2_adamw_tensors(**one, grads=[torch.full((n,), math.nan, device="cuda").to(grads) for n in sizes])
+    for t in (1, 2, 3):
+        new = [rnd(n, dtype=grads) for n in sizes]
+        g.gpt2_op_adamw_many(h, **hp, t=t, grads=new)
+        g.gpt2_op_adamw_many(g.gpt2_adamw_tensors(**two, grads=new), **hp, t=t)
+        for k in one:
+            assert all(torch.equal(a, b) for a, b in zip(one[k], two[k])), (k, t)
+    # the last ones stay the list's
+    g.gpt2_op_adamw_many(h, **hp, t=4)
+    g.gpt2_op_adamw_many(g.gpt2_adamw_tensors(**two, grads=new), **hp, t=4)
+    assert all(torch.equal(a, b) for k in one for a, b in zip(one[k], two[k]))
+
+
+def test_adamw_many_follows_a_backward_pass():
+    """A loop that drops its gradients before each backward pass, as torch's zero_grad does."""
+    p = torch.nn.Parameter(rnd(300))
+    x = rnd(300)
+    m, v = torch.zeros(300, device="cuda"), torch.zeros(300, device="cuda")
+    hp = dict(lr=1e-2, beta1=0.9, beta2=0.95, eps=1e-8)
+    (p * x).sum().backward()
+    h = g.gpt2_adamw_tensors([p], [p.grad], [m], [v])
+    want, wm, wv = p.detach().double(), m.double(), v.double()
+    for t in (1, 2, 3):
+        p.grad = None
+        (p * p * x).sum().backward()
+        want, wm, wv = R.adamw(want, p.grad.double(), wm, wv, wd=0.0, t=t, factor=1.0, lr=hp["lr"], b1=hp["beta1"],
+                               b2=hp["beta2"], eps=hp["eps"])
+        with pytest.raises(RuntimeError, match="give this step's grads"):
+            g.gpt2_op_adamw_many(h, **hp, t=t)
+        g.gpt2_op_adamw_many(h, **hp, t=t, grads=[p.grad])
+        # a step is at most lr (1 - b1) / sqrt(1 - b2) of 1, in about 60 operations of U each
+        assert ((p.detach().double() - want).abs() <= 64 * R.U * t * (want.abs() + hp["lr"])).all()
+        want = p.detach().double()
+        wm, wv = m.double(), v.double()
+        g.gpt2_op_adamw_many(h, **{**hp, "lr": 0.0}, t=t)  # the gradients given stand in .grad: no refusal
+        m.copy_(wm), v.copy_(wv)
+    # gradients that are not the .grad are taken as they are, and stay the list's
+    p.grad = None
+    x = x.clone()
+    g.gpt2_op_adamw_many(h, **hp, t=4, grads=[x])
+    g.gpt2_op_adamw_many(h, **hp, t=5)
