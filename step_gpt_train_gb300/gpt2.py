@@ -1026,7 +1026,8 @@ def gpt2_adamw_tensors(masters, grads, ms, vs, params=None, m_scales=None, v_sca
     """A list of tensors for gpt2_op_adamw_many. For each: master (float32), grad (float32 or bfloat16, all alike), m
     and v (float32, or uint8 codes with m_scales and v_scales, uint8 [ceil(n / 128)]), params (bfloat16 or None)
     and weight_decay (a number, or one for each). m_values, v_values: where gpt2_op_adamw_many_states writes the
-    values of 8-bit moments (float32 or bfloat16, all alike). All contiguous, on one device.
+    values of 8-bit moments (float32 or bfloat16, all alike). All contiguous, on one device; none but gradients may
+    overlap.
 
     The list is one of memory: it keeps what the tensors stand on at this call, and a tensor that is given other memory
     later (`.data`, `set_`) is not followed. The memory must not be resized while the list lives. Gradients that are new
@@ -1035,8 +1036,8 @@ def gpt2_adamw_tensors(masters, grads, ms, vs, params=None, m_scales=None, v_sca
     torch = _tc()
     n = len(masters)
     decay = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else [float(x) for x in weight_decay]
-    columns = {"params": params, "grads": grads, "ms": ms, "vs": vs, "m_scales": m_scales, "v_scales": v_scales,
-               "m_values": m_values, "v_values": v_values}
+    columns = {"masters": masters, "params": params, "grads": grads, "ms": ms, "vs": vs, "m_scales": m_scales,
+               "v_scales": v_scales, "m_values": m_values, "v_values": v_values}
     columns = {k: [None] * n if c is None else list(c) for k, c in columns.items()}
     if len(decay) != n or any(len(c) != n for c in columns.values()):
         raise ValueError("gpt2_adamw_tensors: every list needs one entry a tensor")
@@ -1054,38 +1055,43 @@ def gpt2_adamw_tensors(masters, grads, ms, vs, params=None, m_scales=None, v_sca
         if m_values is not None:
             h.mode = _mode_of("m_values", columns["m_values"][0])
     moment = torch.uint8 if h.bits == 8 else torch.float32
-    kinds = {"params": torch.bfloat16, "grads": torch.bfloat16 if h.grads == MODE_BF16 else torch.float32, "ms": moment,
+    kinds = {"masters": torch.float32, "params": torch.bfloat16, "grads": torch.bfloat16 if h.grads == MODE_BF16 else torch.float32, "ms": moment,
              "vs": moment, "m_scales": torch.uint8, "v_scales": torch.uint8,
              "m_values": torch.bfloat16 if h.mode == MODE_BF16 else torch.float32}
     kinds["v_values"] = kinds["m_values"]
-    h.array = (gpt2_adamw_tensor * max(n, 1))()
-    values = (c_void_p * max(n, 1))(), (c_void_p * max(n, 1))()
-    memory, h.leaves, h.sizes = [], [], []
-    for i, master in enumerate(masters):
-        size = master.numel()
-        of = {"masters": (master, torch.float32, size)}
-        of |= {k: (c[i], kinds[k], -(-size // 128) if k.endswith("scales") else size) for k, c in columns.items()}
-        for k, (t, dtype, count) in of.items():
+    needed = ["masters", "grads", "ms", "vs"] + ["m_scales", "v_scales"] * (h.bits == 8)
+    needed += ["m_values", "v_values"] * (m_values is not None)
+    h.sizes = [x.numel() for x in masters]
+    blocks = [-(-x // 128) for x in h.sizes]
+    memory, spans, at = [], [], {}
+    for k, column in columns.items():
+        dtype, put, written = kinds[k], [], k != "grads"
+        at[k], wide = put, dtype.itemsize
+        for i, (t, count) in enumerate(zip(column, blocks if k.endswith("scales") else h.sizes)):
             if t is None:
-                if k in ("grads", "ms", "vs") or (h.bits == 8 and k.endswith("scales")):
+                if k in needed:
                     raise ValueError(f"{k}: tensor {i} is needed")
-                if k.endswith("values") and m_values is not None:
-                    raise ValueError(f"{k}: tensor {i} is needed")
-            elif t.dtype is not dtype or t.numel() != count or not t.is_contiguous():
+                put.append(None)
+                continue
+            if t.dtype is not dtype or t.numel() != count or not t.is_contiguous():
                 raise ValueError(f"{k}: contiguous {dtype} of {count} values is needed for tensor {i}")
-            elif t.get_device() != h.device:
+            if t.get_device() != h.device:
                 raise RuntimeError("gpt2_adamw_tensors: every tensor has to be on one device")
-            else:
-                memory.append(t.untyped_storage())
-        h.sizes.append(size)
-        h.leaves += [(i, t, columns["grads"][i]) for t in (master, columns["params"][i])
-                     if t is not None and t.is_leaf and t.grad is columns["grads"][i]]
-        a = h.array[i]
-        a.master, a.param_bf16, a.grad, a.m, a.v, a.m_scale, a.v_scale = (
-            _p(of[k][0]) for k in ("masters", "params", "grads", "ms", "vs", "m_scales", "v_scales"))
-        a.n, a.weight_decay = size, decay[i]
-        if m_values is not None:
-            values[0][i], values[1][i] = _p(of["m_values"][0]), _p(of["v_values"][0])
+            address = t.data_ptr()
+            put.append(address)
+            memory.append(t.untyped_storage())
+            if written and count:
+                spans.append((address, address + count * wide))
+    spans.sort()
+    if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):  # (two blocks would update the same values)
+        raise ValueError("gpt2_adamw_tensors: tensors that are written must not overlap; list shared ones once")
+    h.leaves = [(i, t, grad) for i, (grad, *ts) in enumerate(zip(columns["grads"], masters, columns["params"]))
+                for t in ts if t is not None and t.is_leaf and t.grad is grad]
+    h.array = (gpt2_adamw_tensor * max(n, 1))()
+    for i, fields in enumerate(zip(at["masters"], at["params"], at["grads"], at["ms"], at["vs"], at["m_scales"],
+                                   at["v_scales"], h.sizes, decay)):
+        h.array[i] = fields
+    values = [(c_void_p * max(n, 1))(*at[k]) for k in ("m_values", "v_values")]
     if m_values is not None:
         h.values = tuple(ctypes.addressof(v) for v in values)
     h.address = ctypes.addressof(h.array)

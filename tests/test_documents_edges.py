@@ -104,3 +104,28 @@ def test_a_step_refuses_new_gradients_that_do_not_fit(bad):
     with pytest.raises(RuntimeError, match="current CUDA device"):
         g.gpt2_op_adamw_many(h, **STEP, grads=[torch.zeros(5), torch.zeros(300)])
     assert [h.array[i].grad for i in range(2)] == before  # what is refused leaves the list as it was
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_list_refuses_tensors_that_overlap(bits):
+    c = tensors(bits, (300, 5, 300))
+    g.gpt2_adamw_tensors(**c)
+    for k in c:
+        twice = dict(c)
+        twice[k] = [c[k][0], c[k][1], c[k][0]]
+        if k == "grads":  # which are only read
+            g.gpt2_adamw_tensors(**twice)
+            continue
+        with pytest.raises(ValueError, match="overlap"):
+            g.gpt2_adamw_tensors(**twice)
+    # in part; across columns; one behind the other is no overlap, nor are tensors without values
+    flat = torch.zeros(605)
+    for parts in ([flat[:300], flat[300:305], flat[304:604]], [flat[:300], c["ms"][0][:5].float(), flat[299:599]]):
+        with pytest.raises(ValueError, match="overlap"):
+            g.gpt2_adamw_tensors(**{**c, "masters": parts})
+    g.gpt2_adamw_tensors(**{**c, "masters": [flat[:300], flat[300:305], flat[305:]]})
+    if bits == 32:
+        with pytest.raises(ValueError, match="overlap"):
+            g.gpt2_adamw_tensors(**{**c, "vs": c["ms"]})
+    none = [torch.zeros(0)] * 2
+    g.gpt2_adamw_tensors(none, none, none, none)
