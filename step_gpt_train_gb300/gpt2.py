@@ -1152,10 +1152,10 @@ def gpt2_op_adamw_many(tensors, lr, beta1, beta2, eps, t, grad_scale=1.0, max_gr
 def gpt2_op_adamw_many_states(tensors, stream=None):
     """The values of the tensors' 8-bit moments, into the list's m_values and v_values."""
     what = "gpt2_op_adamw_many_states"
-    if tensors.bits != 8 or tensors.values is None:
+    if tensors.values is None:  # (they come with moments in 8 bits only, or in a list of nothing)
         raise ValueError(f"{what}: a list of tensors with 8-bit moments, m_values and v_values is needed")
     device, st = (_tc(), _where(stream))[1]
-    if tensors.device != device:
+    if tensors.count and tensors.device != device:
         raise _elsewhere(what)
     check(load_library().gpt2_op_adamw_many_states(tensors.address, *tensors.values, tensors.count, tensors.mode, st), what)
 

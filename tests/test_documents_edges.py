@@ -129,3 +129,11 @@ def test_a_list_refuses_tensors_that_overlap(bits):
             g.gpt2_adamw_tensors(**{**c, "vs": c["ms"]})
     none = [torch.zeros(0)] * 2
     g.gpt2_adamw_tensors(none, none, none, none)
+
+
+def test_moments_of_an_empty_list_are_read_back():
+    h = g.gpt2_adamw_tensors([], [], [], [], m_scales=[], v_scales=[], m_values=[], v_values=[])
+    g.gpt2_op_adamw_many(h, **STEP)
+    g.gpt2_op_adamw_many_states(h)
+    with pytest.raises(ValueError):  # there is no place for values
+        g.gpt2_op_adamw_many_states(g.gpt2_adamw_tensors([], [], [], []))
