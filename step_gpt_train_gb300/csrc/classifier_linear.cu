@@ -226,13 +226,13 @@ size_t products_scratch(int dtype, int N, int C, int V, int Vp, int accumulate, 
     return most;
 }
 
-// bf16: the scale; a piece of dz; bf16 in pieces: dx in fp32; the products' own.
+// bf16: the scale; a piece of dz (the first is as wide as any); bf16 in pieces: dx in fp32; the products' own.
 struct BackwardScratch {
     size_t dz, dx, own;
-    BackwardScratch(int dtype, int N, int C, const Pieces& p) {
+    BackwardScratch(int dtype, int N, int C, int V, int Vp, const Pieces& p) {
         const bool bf = dtype == GPT2_MODE_BF16;
         dz = bf ? 256 : 0;
-        dx = dz + round256((size_t)N * p.width * (bf ? 2 : 4));
+        dx = dz + round256((size_t)N * pitch_of(0, V, Vp, p) * (bf ? 2 : 4));
         own = dx + (bf && p.n > 1 ? round256((size_t)N * C * 4) : 0);
     }
 };
@@ -241,7 +241,7 @@ struct BackwardScratch {
 
 size_t linear_classifier_backward_scratch(int dtype, int N, int C, int V, int Vp, int accumulate) {
     const Pieces p = pieces(dtype, N, C, V);
-    return BackwardScratch(dtype, N, C, p).own + products_scratch(dtype, N, C, V, Vp, accumulate, p);
+    return BackwardScratch(dtype, N, C, V, Vp, p).own + products_scratch(dtype, N, C, V, Vp, accumulate, p);
 }
 
 int launch_linear_classifier_backward(int dtype, void* dx, void* dw, int dw_fp32, int accumulate, const void* x,
@@ -250,7 +250,7 @@ int launch_linear_classifier_backward(int dtype, void* dx, void* dw, int dw_fp32
                                       cudaStream_t s) {
     const bool bf = dtype == GPT2_MODE_BF16;
     const Pieces p = pieces(dtype, N, C, V);
-    const BackwardScratch at(dtype, N, C, p);
+    const BackwardScratch at(dtype, N, C, V, Vp, p);
     void* dz = (char*)scratch + at.dz;
     float* sum = (float*)((char*)scratch + at.dx);
     void* own = (char*)scratch + at.own;

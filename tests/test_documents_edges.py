@@ -137,3 +137,16 @@ def test_moments_of_an_empty_list_are_read_back():
     g.gpt2_op_adamw_many_states(h)
     with pytest.raises(ValueError):  # there is no place for values
         g.gpt2_op_adamw_many_states(g.gpt2_adamw_tensors([], [], [], []))
+
+
+# ---------------------------------------------------------------- scratch of the loss's gradient
+
+@pytest.mark.parametrize("mode,size", [(1, 2), (0, 4)])
+@pytest.mark.parametrize("N,C,V,Vp", [((1 << 27) + 5, 8, 15, 16), (1 << 20, 64, 100, 104), (1000, 64, 300, 304),
+                                      (4096, 768, 50257, 50304)])
+def test_scratch_of_a_small_vocabulary_is_no_wider_than_it(lib, mode, size, N, C, V, Vp):
+    """One piece of dz: its columns are dw's rows, not the next 256."""
+    got = lib.gpt2_op_linear_classifier_backward_scratch(mode, N, C, V, Vp, 0)
+    # besides dz: the scale, and the parts of products split at most 64 times along k (fp32: as many as fill the device)
+    parts = 64 * 4 * max(128 * 256, -(-Vp // 128) * 128 * -(-C // 128) * 128)
+    assert N * Vp * size <= got <= N * Vp * size + 1024 + parts
