@@ -170,6 +170,9 @@ struct RotaryArgs {
 size_t rotary_backward_scratch(int N, int hd);
 int launch_rotary(int dtype, const RotaryArgs& a, bool back, float* dq_gamma, float* dk_gamma, void* scratch,
                   cudaStream_t s);
+// gpt2_rotary_turns: validated arguments (rotary_turns.cu; host only).
+void rotary_turns(uint64_t* turns, int rot, double base, int scaling, double factor, double context, double fast,
+                  double slow);
 
 // The linear classifier's part in the epilogue of a matmul (gemm_tc.cu): the columns of the product are the
 // vocabulary's from `first` on.

@@ -479,16 +479,7 @@ int gpt2_rotary_turns(uint64_t* turns, int rot, double base, int scaling, double
     if (scaling == GPT2_ROTARY_PARTS &&
         (!(context >= 1.0) || !std::isfinite(context) || !(slow >= 0.0) || !(fast > slow) || !std::isfinite(fast)))
         return GPT2_ERR_ARG;
-    if (scaling == GPT2_ROTARY_BASE && rot > 2) base *= std::pow(factor, rot / (rot - 2.0));
-    for (int j = 0; j < rot / 2; j++) {
-        double f = std::pow(base, -2.0 * j / rot) / (2.0 * 3.14159265358979323846);
-        if (scaling == GPT2_ROTARY_LINEAR) f /= factor;
-        if (scaling == GPT2_ROTARY_PARTS) {
-            const double turned = (f * context - slow) / (fast - slow), keep = std::fmin(1.0, std::fmax(0.0, turned));
-            f *= keep + (1.0 - keep) / factor;
-        }
-        turns[j] = (uint64_t)std::nearbyint(std::ldexp(f, 64));
-    }
+    rotary_turns(turns, rot, base, scaling, factor, context, fast, slow);
     return GPT2_OK;
 }
 

@@ -1,5 +1,6 @@
 """Head norms with rotary positions, the cross entropy of hidden states and AdamW over many tensors: what the host
 side holds, hands on and refuses (CPU; nothing is launched)."""
+import decimal
 import gc
 import weakref
 
@@ -150,3 +151,39 @@ def test_scratch_of_a_small_vocabulary_is_no_wider_than_it(lib, mode, size, N, C
     # besides dz: the scale, and the parts of products split at most 64 times along k (fp32: as many as fill the device)
     parts = 64 * 4 * max(128 * 256, -(-Vp // 128) * 128 * -(-C // 128) * 128)
     assert N * Vp * size <= got <= N * Vp * size + 1024 + parts
+
+# ---------------------------------------------------------------- turns
+
+def decimal_turns(rot, base, scaling, factor, context, fast, slow):
+    """2^64 times the fractions of a turn, to 60 digits."""
+    D = decimal.Decimal
+    with decimal.localcontext() as c:
+        c.prec = 60
+        # pi: Machin's formula
+        atan = lambda n: sum((-1) ** k / (D(n) ** (2 * k + 1) * (2 * k + 1)) for k in range(60))  # noqa: E731
+        pi = 4 * (4 * atan(5) - atan(239))
+        base, factor, context, fast, slow = (D(x) for x in (base, factor, context, fast, slow))
+        log = base.ln()
+        if scaling == "base" and rot > 2:
+            log += factor.ln() * rot / (rot - 2)
+        out = []
+        for j in range(rot // 2):
+            f = (log * (-2 * j) / rot).exp() / (2 * pi)
+            if scaling == "linear":
+                f /= factor
+            if scaling == "parts":
+                keep = min(D(1), max(D(0), (f * context - slow) / (fast - slow)))
+                f *= keep + (1 - keep) / factor
+            out.append(f * 2 ** 64)
+        return out
+
+
+@pytest.mark.parametrize("scaling", ["plain", "linear", "base", "parts"])
+@pytest.mark.parametrize("rot,base,factor", [(2, 1e4, 8.0), (8, 1e4, 1.0), (64, 1e4, 8.0), (128, 5e5, 32.0), (128, 1e6, 3.7),
+                                             (64, 1.0000001, 1.5), (64, 1.7e308, 1e300)])
+def test_turns_are_whole_to_their_last_bit(scaling, rot, base, factor):
+    """turns[j] is the nearest whole number of 2^-64 turns: a position of 31 bits keeps its angle to 2^-34 of a turn."""
+    kw = dict(base=base, scaling=scaling, factor=factor, context=8192.0, fast=32.0, slow=1.0)
+    got, want = g.gpt2_rotary_turns(rot, **kw).tolist(), decimal_turns(rot, **kw)
+    # half a unit of the rounding, and 2^-20 of one for the arithmetic before it (two numbers of 53 bits each)
+    assert all(abs(a - b) <= 0.5 + 2.0 ** -20 for a, b in zip(got, want)), max(abs(a - b) for a, b in zip(got, want))
