@@ -400,7 +400,9 @@ int gpt2_op_adamw(float* master, void* param_bf16, const float* grad, float* m, 
  * (2 j, 2 j + 1) (interleaved != 0), j < rot / 2; the other values keep n. The
  * angle t is pos[row] * turns[j] * 2^-64 turns, modulo one turn: turns is a
  * device array of rot / 2 fractions of a turn per position (gpt2_rotary_turns
- * fills one on the host), and any int32 position keeps its angle to 2^-33 of a turn.
+ * fills one on the host, good to 2^-34 of a turn at any int32 position); cos and
+ * sin are formed in fp32 from the exact product's distance to its nearest quarter
+ * turn, which is rounded to 2^-28 of a turn.
  *   q, qo: rows of Hq * hd values, k, ko: rows of Hk * hd (dtype), head h at
  *   columns h*hd .. of a row; *_stride: elements from one row to the next, so
  *   they may be column blocks of one fused buffer. qo may be q and ko k (with

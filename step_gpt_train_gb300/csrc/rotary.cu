@@ -6,9 +6,11 @@
 //
 // for the pairs (a, b) of the first rot values of a head. The angle t of pair
 // j at position p is p * turns[j] in units of 2^-64 turns, modulo one turn: a
-// 64-bit product that wraps, so its error does not grow with the position
-// (2^-33 of a turn, where a 32-bit product of position and frequency is off by
-// 0.006 rad at 10^5); the signed top half, as half turns, goes to sincospif.
+// 64-bit product that wraps, whose error is the table's alone (2^-34 of a turn
+// at position 2^31, where a 32-bit product of position and frequency is off by
+// 0.006 rad at 10^5). The nearest quarter turn is taken off in whole numbers; what
+// is left, an eighth of a turn at most, is rounded to fp32 (2^-28 of a turn) for
+// sincospif, and the quarters exchange cos and sin and turn their signs.
 //
 // A head is held by hd / E neighbouring lanes of a warp, E values (16 bytes, or
 // 8 where the halves of a pair would not lie in whole lanes) each. A warp takes
@@ -134,8 +136,19 @@ template <int E, bool PAIRS> struct Angles {
         __syncwarp();  // the row before has read its angles
         for (int j = lane; j < half; j += 32) {
             const uint64_t t = (uint64_t)(int64_t)pos * turns[j];
+            const uint32_t quarter = (uint32_t)((t + (1ull << 61)) >> 62);
             float sn, cs;
-            sincospif((float)(int32_t)(t >> 32) * 0x1p-31f, &sn, &cs);
+            // (32 bits, to 2^-34 of a turn, are converted in less time than 64)
+            sincospif((float)(int32_t)((t - ((uint64_t)quarter << 62)) >> 30) * 0x1p-33f, &sn, &cs);
+            if (quarter & 1) {
+                const float c = cs;
+                cs = -sn;
+                sn = c;
+            }
+            if (quarter & 2) {
+                cs = -cs;
+                sn = -sn;
+            }
             w.cos[j] = cs * amplitude;
             w.sin[0][j] = sn * amplitude;
             w.sin[1][j] = -sn * amplitude;

@@ -72,3 +72,34 @@ def test_adamw_many_follows_a_backward_pass():
     x = x.clone()
     g.gpt2_op_adamw_many(h, **hp, t=4, grads=[x])
     g.gpt2_op_adamw_many(h, **hp, t=5)
+
+
+# ---------------------------------------------------------------- rotation
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("rot", [8, 64])
+def test_angles_keep_their_bits_at_any_position(interleaved, rot):
+    """Rotations of (1, 0) and (0, 1): cos and sin themselves, of all int32 positions."""
+    n = 5000
+    pos = torch.randint(-(1 << 31), 1 << 31, (n,), device="cuda").int()
+    pos[:8] = torch.tensor([0, 1, -1, 2, 131071, 1 << 24, (1 << 31) - 1, -(1 << 31)]).int()
+    turns = g.gpt2_rotary_turns(rot).cuda()
+    a, b = (i.cuda() for i in R._pairs(rot, interleaved))
+    q, k = torch.zeros(n, 1, 64, device="cuda"), torch.zeros(n, 1, 64, device="cuda")
+    q[..., a] = 1
+    k[..., b] = 1
+    g.gpt2_op_qk_norm_rotary_forward(q, k, q, k, pos, turns, interleaved=interleaved)
+    cos, sin = R._cos_sin(pos, turns)
+    # the angle is taken off its nearest quarter turn before it becomes an fp32 number: at most an eighth of a turn is
+    # left, a quarter of half a turn, whose rounding is 2^-27 of half a turn; then one unit of the last place (2^-23 at
+    # most) of cos and sin
+    for got, want, slope in ((q[..., a], cos, sin), (q[..., b], sin, cos), (k[..., a], -sin, cos), (k[..., b], cos, sin)):
+        far = (got.double() - want).abs() - (math.pi * 2.0 ** -27 * slope.abs() + 2.0 ** -23 * want.abs() + 2.0 ** -50)
+        assert (far <= 0).all(), far.max().item()
+    assert not q[..., rot:].any() and not k[..., rot:].any()
+    # back again: the transposed rotation
+    ones, none = torch.zeros_like(q), torch.zeros_like(q)
+    ones[..., a] = 1
+    g.gpt2_op_qk_norm_rotary_backward(ones, none, ones, none, q, k, pos, turns, interleaved=interleaved)
+    for got, want, slope in ((ones[..., a], cos, sin), (ones[..., b], -sin, cos)):
+        assert ((got.double() - want).abs() <= math.pi * 2.0 ** -27 * slope.abs() + 2.0 ** -23 * want.abs() + 2.0 ** -50).all()
