@@ -203,7 +203,7 @@ __device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, uint32_t src,
 // the tile's half (negative or past it where it lies elsewhere).
 struct RowHead {
     float m, s;      // EPI_LSE: the running maximum and the sum of exp(z - maximum)
-    float a, d, lse; // EPI_DZ: dloss + dlse and dloss in units of the scale, lse in base 2
+    float a, d, lse; // EPI_DZ: dloss + dlse and dloss in units of the scale, lse in base 2 (its rounding is in a)
     int at;
 };
 constexpr float LOG2E = 1.4426950408889634f;
@@ -388,9 +388,12 @@ __device__ __forceinline__ void head_begin(const HeadEpi* e, int row, int M, int
             h.at = t - (v0 + e->first);
             if (EPI == EPI_DZ) {
                 const float d = e->dloss ? e->dloss[row] : 0.f, a = d + (e->dlse ? e->dlse[row] : 0.f);
+                const float lse = e->lse[row];
+                h.lse = lse * LOG2E;
+                // the rounding of this product, which every p of the row shares, is taken out of their factor again
+                const float off = isfinite(h.lse) ? fmaf(lse, LOG2E, -h.lse) : 0.f;
                 h.d = d != 0.f ? d / scale : 0.f;
-                h.a = a != 0.f ? a / scale : 0.f;
-                h.lse = e->lse[row] * LOG2E;
+                h.a = a != 0.f ? a / scale * ex2_approx(-off) : 0.f;
             }
         }
     }

@@ -103,3 +103,25 @@ def test_angles_keep_their_bits_at_any_position(interleaved, rot):
     g.gpt2_op_qk_norm_rotary_backward(ones, none, ones, none, q, k, pos, turns, interleaved=interleaved)
     for got, want, slope in ((ones[..., a], cos, sin), (ones[..., b], -sin, cos)):
         assert ((got.double() - want).abs() <= math.pi * 2.0 ** -27 * slope.abs() + 2.0 ** -23 * want.abs() + 2.0 ** -50).all()
+
+# ---------------------------------------------------------------- cross entropy of hidden states
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_probabilities_of_far_logits_are_off_by_lses_own_rounding_only(dtype):
+    """Rows whose logits lie at 1.3e5 to 2.6e5, exact in fp32, with an lse that is exact too: p is exp(z - lse)."""
+    n, C, V = 128, 16, 8
+    x = torch.zeros(n, C, device="cuda", dtype=dtype)
+    w = torch.zeros(V, C, device="cuda", dtype=dtype)
+    x[:, 0] = 256 + 2 * torch.arange(n, device="cuda").to(dtype)  # eight bits: a bf16 number
+    x[:, 1] = 1
+    w[:, 0] = 512
+    w[:, 1] = -0.25 * torch.arange(V, device="cuda").to(dtype)
+    w[:, 8:] = torch.eye(V, device="cuda").to(dtype)  # dx's last columns are dz's
+    lse = 512 * x[:, 0].float()
+    t = torch.zeros(n, device="cuda", dtype=torch.int32)
+    dx, dw = torch.empty_like(x), torch.empty(V, C, device="cuda")
+    g.gpt2_op_linear_classifier_backward(dx, dw, x, w, t, lse, V, dlse=torch.ones(n, device="cuda"))
+    p = torch.exp(w[:, 1].double()).expand(n, V)
+    # dz is rounded to its type and dx keeps it; before that: z - lse is exact in fp32 and at most 1.75, log2 e and its
+    # product are off by 2^-23 of it, the exponentials by 2^-22 each, two products by 2^-24 each
+    assert ((dx[:, 8:].double() - p).abs() <= p * (R.HALF[dtype] + 2.0 ** -20)).all()
