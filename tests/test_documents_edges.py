@@ -2,6 +2,9 @@
 side holds, hands on and refuses (CPU; nothing is launched)."""
 import decimal
 import gc
+import os
+import subprocess
+import sys
 import weakref
 
 import numpy as np
@@ -151,6 +154,22 @@ def test_scratch_of_a_small_vocabulary_is_no_wider_than_it(lib, mode, size, N, C
     # besides dz: the scale, and the parts of products split at most 64 times along k (fp32: as many as fill the device)
     parts = 64 * 4 * max(128 * 256, -(-Vp // 128) * 128 * -(-C // 128) * 128)
     assert N * Vp * size <= got <= N * Vp * size + 1024 + parts
+
+@pytest.mark.parametrize("mode,size", [(1, 2), (0, 4)])
+@pytest.mark.parametrize("N,C,V,Vp", [(32768, 768, 50257, 50304), (70000, 1024, 50257, 50264), (32768, 128, 20001, 20008)])
+def test_scratch_of_several_pieces(mode, size, N, C, V, Vp):
+    """Equal pieces, as few as 1 GB each asks for, on a host without a GPU too (in a process of its own: the call
+    divided by the number of SM pairs there, which is 0)."""
+    ask = ("from step_gpt_train_gb300 import gpt2 as g; "
+           f"print(g.load_library().gpt2_op_linear_classifier_backward_scratch({mode}, {N}, {C}, {V}, {Vp}, 0))")
+    r = subprocess.run([sys.executable, "-c", ask], capture_output=True, text=True, env={**os.environ, "CUDA_VISIBLE_DEVICES": ""},
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr
+    pieces = -(-V // ((1 << 30) // (N * size) // 256 * 256))  # (of whole tiles of 256)
+    wide = -(-V // pieces)  # (a piece's columns: that, rounded up to whole tiles)
+    rest = N * C * 4 * (mode == 1) + 64 * 4 * (wide + 256) * (C + 128) + 1024  # dx in fp32; parts of products
+    assert N * wide * size <= int(r.stdout) <= N * (wide + 255) * size + rest
+
 
 # ---------------------------------------------------------------- turns
 
