@@ -77,7 +77,8 @@ void rotary_turns(uint64_t* turns, int rot, double base, int scaling, double fac
         if (scaling == GPT2_ROTARY_LINEAR) f = f / Two{factor, 0.0};
         if (scaling == GPT2_ROTARY_PARTS) {
             const Two turned = (f * Two{context, 0.0} + Two{-slow, 0.0}) / sum_of(fast, -slow), one = {1.0, 0.0};
-            const Two keep = turned.h >= 1.0 ? one : turned.h <= 0.0 ? Two{0.0, 0.0} : turned;
+            // (a quotient past a double's range is no number here, and above 1)
+            const Two keep = !(turned.h < 1.0) ? one : turned.h <= 0.0 ? Two{0.0, 0.0} : turned;
             if (keep.h < 1.0) f = f * (keep + (one + -keep) / Two{factor, 0.0});
         }
         const double h = std::ldexp(f.h, 64), whole = std::floor(h), rest = (h - whole) + std::ldexp(f.l, 64);

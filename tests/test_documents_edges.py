@@ -206,3 +206,11 @@ def test_turns_are_whole_to_their_last_bit(scaling, rot, base, factor):
     got, want = g.gpt2_rotary_turns(rot, **kw).tolist(), decimal_turns(rot, **kw)
     # half a unit of the rounding, and 2^-20 of one for the arithmetic before it (two numbers of 53 bits each)
     assert all(abs(a - b) <= 0.5 + 2.0 ** -20 for a, b in zip(got, want)), max(abs(a - b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("context,fast,slow", [(1e308, 32.0, 1.0), (1e308, 1.0, 1.0 - 2.0 ** -53), (1.0, 5e-324, 0.0),
+                                               (1.0, 1e308, 0.0), (1e308, 1.5e307, 1e307), (1e6, 2.0 ** -1000, 0.0)])
+def test_turns_of_any_borders(context, fast, slow):
+    kw = dict(base=1e4, scaling="parts", factor=8.0, context=context, fast=fast, slow=slow)
+    got, want = g.gpt2_rotary_turns(64, **kw).tolist(), decimal_turns(64, **kw)
+    assert all(abs(a - b) <= 0.5 + 2.0 ** -20 for a, b in zip(got, want))
