@@ -411,7 +411,9 @@ int gpt2_op_adamw(float* master, void* param_bf16, const float* grad, float* m, 
  *   - hd 8, 16, 32, 64 or 128; rot a multiple of 8, 0 <= rot <= hd (turns may
  *     be null for 0). Hq, Hk >= 0, not both 0 (pointers of none are unused).
  *     Pointers 16-byte aligned, strides multiples of 16 bytes and at least the
- *     row. eps > 0 with norm; amplitude finite. N = 0 launches nothing. */
+ *     row. eps > 0 with norm; amplitude finite. N = 0 launches nothing.
+ *   - Squares are formed in fp32: a head with values from about 1e19 on has an
+ *     infinite mean and comes out as 0. */
 int gpt2_op_qk_norm_rotary_forward(int dtype, void* qo, int64_t qo_stride, void* ko, int64_t ko_stride, const void* q,
                                    int64_t q_stride, const void* k, int64_t k_stride, const void* q_gamma,
                                    const void* k_gamma, const int32_t* pos, const uint64_t* turns, int N, int Hq,
@@ -480,17 +482,20 @@ int gpt2_op_linear_classifier_forward(int dtype, float* losses, float* lse, cons
  *   dx = dz W (dtype, overwritten), dw = dz^T x.
  * dloss, dlse: [N] fp32, gradients of losses and lse, either may be null (0). A
  * row whose dloss and dlse are 0, or whose lse is -inf, has dz = 0 whatever its
- * logits are (a prompt's or padding's tokens; x and the first V rows of w have
- * to be finite all the same: the products add 0 times them). dw [Vp, C], Vp >= V,
- * Vp % 8 == 0: fp32 (dw_fp32 = 1; the only form in fp32) or bf16; rows from V
- * on get 0. accumulate (fp32 dw only): dw += instead, rows from V on stay. In
- * bf16 dz is rounded to bf16 for the products, in units of the largest |dloss|
- * and |dloss + dlse|: half a step (2^-8) of each value; sums are fp32. p carries lse's own
- * rounding (|lse| 2^-24, relative). Deterministic (no atomics). dx and dw must
+ * logits are (a prompt's or padding's tokens; it costs what any row costs, and x
+ * and the first V rows of w have to be finite all the same: the products add 0
+ * times them). dw [Vp, C], Vp >= V, Vp % 8 == 0: fp32 (dw_fp32 = 1; the only
+ * form in fp32) or bf16; rows from V on get 0. accumulate (fp32 dw only): dw +=
+ * instead, rows from V on stay. In bf16 dz is rounded to bf16 for the products, in units of the largest |dloss|
+ * and |dloss + dlse|: half a step (2^-8) of each value (what is below 2^-126 of
+ * that unit loses bits, and is 0 below 2^-134); sums are fp32. p carries lse's own
+ * rounding (|lse| 2^-24, relative). Deterministic: sums are taken in a fixed
+ * order (the one atomic is the largest |dloss|, the same in any). dx and dw must
  * not overlap the inputs or each other. Limits as in the forward; N = 0 sets
  * dw to 0 (or leaves it, with accumulate). Scratch: a piece of dz (up to 1 GB,
- * or 2048 columns where that is more), dx in fp32 where there are several
- * pieces, partial products. */
+ * or 2048 columns where that is more: all columns where they fit, 824 MB for
+ * 8192 rows of 50257 in bf16), dx in fp32 where there are several pieces,
+ * partial products (with accumulate, a piece of dw in fp32). */
 size_t gpt2_op_linear_classifier_backward_scratch(int dtype, int N, int C, int V, int Vp, int accumulate);
 int gpt2_op_linear_classifier_backward(int dtype, void* dx, void* dw, int dw_fp32, int accumulate, const void* x,
                                        const void* w, const int32_t* targets, const float* lse, const float* dloss,
@@ -531,6 +536,11 @@ int gpt2_op_linear_classifier_backward(int dtype, void* dx, void* dw, int dw_fp3
  *   mix(mix(seed + t G) + (k 2^40 + p) G), G = 0x9E3779B97F4A7C15.
  * A v above 0 is stored as its lowest code at least. What is not finite is
  * stored as NaN and leaves its block's scale alone.
+ *
+ * Tensors are numbered within their list: two lists of one step want two seeds.
+ * A captured call keeps its numbers (lr, t and so its bias corrections, seed,
+ * grad_scale) and its addresses: a replay is that step t again, on the values
+ * that the tensors hold then.
  *
  * beta1, beta2 in [0, 1), eps >= 0, t >= 1, max_grad_norm >= 0. Scratch: partial
  * sums of the norm (needed with max_grad_norm > 0 or grad_norm). */

@@ -15,8 +15,11 @@
 //
 // 1021 x 128 x 5003 (1.3 GFLOP a product, 17 us at 75 TFLOP/s): dz 44 us, dx 34
 // and dw 47, and 3 each to add their parts. What bounds it: three blocks of 160
-// registers an SM are three warps to a scheduler, whose FMAs wait for one
-// another (41% of the issue slots used); a third of what is issued is not FMA.
+// registers an SM are at most three warps to a scheduler, and 27% (dw, 316 blocks
+// for 456 places) to 41% (dz) of the issue slots are used. Between two of a warp's
+// instructions lie 1.0 to 1.4 cycles of fixed latencies, 0.5 to 0.9 of waiting for
+// the FMA pipe and 0.4 to 0.5 for operands from shared memory; a third of what is
+// issued is not FMA.
 #include "common.cuh"
 #include "launch.h"
 #include "tc_common.cuh"

@@ -36,7 +36,8 @@ using tc::f2_unpack;
 
 // A block's warps, the blocks on an SM and the steps whose copies are in flight. At 32768 rows of 24 heads of 64
 // (bf16, with norms): three blocks of the forward 37.3 us, two 41.0, four 41.0 (64 registers: spills); two blocks of
-// the backward 54.4, one 69.7, three 63.3 (80 registers). From two steps ahead to eight: within 1 us.
+// the backward 54.4, one 69.7, three 63.3 (80 registers). From two steps ahead to eight: within 1 us. (Measured before
+// the angles left their quarter turns in whole numbers: in one loop of both, 36.95 -> 37.05 and 57.15 -> 57.7.)
 constexpr int WARPS = 8;
 constexpr int FORWARD_A_SM = 3, BACKWARD_A_SM = 2;
 constexpr int AHEAD = 4;

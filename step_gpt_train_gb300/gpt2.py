@@ -1115,8 +1115,9 @@ def _check_grads(tensors, grads):
 def gpt2_op_adamw_many(tensors, lr, beta1, beta2, eps, t, grad_scale=1.0, max_grad_norm=0.0, grad_norm=None, seed=0,
                        stream=None, grads=None):
     """One AdamW step t on the tensors of a gpt2_adamw_tensors list; grad_norm (float32 [1]) receives the norm of the
-    gradients over all of them, which max_grad_norm > 0 clips. seed: of the rounding of 8-bit moments. grads: gradients
-    that take the place of the list's, from this step on (of the same sizes and type)."""
+    gradients over all of them, which max_grad_norm > 0 clips. seed: of the rounding of 8-bit moments (another for each
+    list of one step). grads: gradients that take the place of the list's, from this step on (of the same sizes and
+    type). A captured call replays this step: its numbers (lr, t, seed ..) and its addresses."""
     what = "gpt2_op_adamw_many"
     lib = load_library()
     device, st = (_tc(), _where(stream))[1]
