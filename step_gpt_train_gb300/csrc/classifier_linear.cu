@@ -36,8 +36,8 @@ struct Pieces {
     int width, n;
 };
 
-// As many pieces as g_piece_bytes for all rows asks for (but of no fewer than 2048 columns), of one width, a whole number
-// of tiles. (Widths chosen by a model of the products' rounds of tiles instead, over 13 shapes of 12000 to 65536 rows,
+// As few pieces as hold at most g_piece_bytes for all rows (or 2048 columns, where that is more), of one width, a whole
+// number of tiles. (Widths chosen by a model of the products' rounds of tiles instead, over 13 shapes of 12000 to 65536 rows,
 // 256 to 1600 values: between 3.4% faster and 4% slower, the same on average; 32768 x 768 x 50257 5219 us, equal pieces
 // 5080.)
 Pieces pieces(int dtype, int N, int V) {
