@@ -1031,8 +1031,8 @@ def gpt2_adamw_tensors(masters, grads, ms, vs, params=None, m_scales=None, v_sca
 
     The list is one of memory: it keeps what the tensors stand on at this call, and a tensor that is given other memory
     later (`.data`, `set_`) is not followed. The memory must not be resized while the list lives. Gradients that are new
-    tensors in each step go to gpt2_op_adamw_many; where a gradient here is the .grad of its master or of its parameter,
-    a step without them refuses once it no longer is."""
+    tensors in each step go to gpt2_op_adamw_many, and the list keeps those instead; where a gradient here is the .grad
+    of its master or of its parameter, a step without them refuses once it no longer is."""
     torch = _tc()
     n = len(masters)
     decay = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else [float(x) for x in weight_decay]
@@ -1055,18 +1055,18 @@ def gpt2_adamw_tensors(masters, grads, ms, vs, params=None, m_scales=None, v_sca
         if m_values is not None:
             h.mode = _mode_of("m_values", columns["m_values"][0])
     moment = torch.uint8 if h.bits == 8 else torch.float32
-    kinds = {"masters": torch.float32, "params": torch.bfloat16, "grads": torch.bfloat16 if h.grads == MODE_BF16 else torch.float32, "ms": moment,
-             "vs": moment, "m_scales": torch.uint8, "v_scales": torch.uint8,
+    kinds = {"masters": torch.float32, "params": torch.bfloat16, "ms": moment, "vs": moment, "m_scales": torch.uint8,
+             "v_scales": torch.uint8, "grads": torch.bfloat16 if h.grads == MODE_BF16 else torch.float32,
              "m_values": torch.bfloat16 if h.mode == MODE_BF16 else torch.float32}
     kinds["v_values"] = kinds["m_values"]
     needed = ["masters", "grads", "ms", "vs"] + ["m_scales", "v_scales"] * (h.bits == 8)
     needed += ["m_values", "v_values"] * (m_values is not None)
     h.sizes = [x.numel() for x in masters]
     blocks = [-(-x // 128) for x in h.sizes]
-    memory, spans, at = [], [], {}
+    memory, of_grads, spans, at = [], [], [], {}
     for k, column in columns.items():
         dtype, put, written = kinds[k], [], k != "grads"
-        at[k], wide = put, dtype.itemsize
+        at[k], wide, hold = put, dtype.itemsize, memory if written else of_grads
         for i, (t, count) in enumerate(zip(column, blocks if k.endswith("scales") else h.sizes)):
             if t is None:
                 if k in needed:
@@ -1079,7 +1079,7 @@ def gpt2_adamw_tensors(masters, grads, ms, vs, params=None, m_scales=None, v_sca
                 raise RuntimeError("gpt2_adamw_tensors: every tensor has to be on one device")
             address = t.data_ptr()
             put.append(address)
-            memory.append(t.untyped_storage())
+            hold.append(t.untyped_storage())
             if written and count:
                 spans.append((address, address + count * wide))
     spans.sort()
@@ -1096,7 +1096,7 @@ def gpt2_adamw_tensors(masters, grads, ms, vs, params=None, m_scales=None, v_sca
         h.values = tuple(ctypes.addressof(v) for v in values)
     h.address = ctypes.addressof(h.array)
     h.scratch = load_library().gpt2_op_adamw_many_scratch(h.address, n)
-    h.held = [memory, values, None]  # (and the gradients of later steps)
+    h.held = [memory, values, of_grads]
     return h
 
 

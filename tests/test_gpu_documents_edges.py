@@ -74,6 +74,18 @@ def test_adamw_many_follows_a_backward_pass():
     g.gpt2_op_adamw_many(h, **hp, t=5)
 
 
+def test_adamw_many_lets_go_of_gradients_that_were_replaced():
+    n, hp = 1 << 22, dict(lr=1e-2, beta1=0.9, beta2=0.95, eps=1e-8)
+    p, m, v = (torch.nn.Parameter(rnd(n)), *(torch.zeros(n, device="cuda") for _ in range(2)))
+    p.grad = rnd(n)
+    h = g.gpt2_adamw_tensors([p], [p.grad], [m], [v])
+    held = torch.cuda.memory_allocated()
+    for t in (1, 2, 3):
+        p.grad = rnd(n)
+        g.gpt2_op_adamw_many(h, **hp, t=t, grads=[p.grad])
+        assert torch.cuda.memory_allocated() == held
+
+
 # ---------------------------------------------------------------- rotation
 
 @pytest.mark.parametrize("interleaved", [False, True])
